@@ -8,8 +8,12 @@
  *   X  <- a_k X + (b_k A + c_k A A) X,  A = X X^T,  k = 1..ns_steps
  *         (on the smaller side: matrices with rows > cols are transposed)
  *   W' = (1 - lr*wd) W - lr * s_rule(rows, cols) * X
- * It also runs the AdamW step for the other parameters (muon_adamw_step) and
- * the Muon-Cayley step on the Stiefel manifold (muon_cayley_step).
+ * It also runs the AdamW step for the other parameters (muon_adamw_step),
+ * the Muon-Cayley step on the Stiefel manifold (muon_cayley_step), and the
+ * operators that make the gradients in a preference or policy step: norms
+ * around a block (muon_block_norm), token log-probabilities over a vocabulary
+ * head (muon_token_logp) and two losses on them (muon_preference_loss,
+ * muon_policy_loss).
  * Sources, cited by page title and section:
  *   [Muon优化器] linsight.cn/f25d614e.html -- the industrial Muon class
  *     (momentum, Nesterov, decay and apply), zeropower_via_newtonschulz
@@ -221,6 +225,206 @@ size_t muon_cayley_workspace_bytes(const muon_cayley_matrix* mats, int32_t n, co
 muon_status muon_cayley_step(const muon_cayley_matrix* mats, int32_t n, const muon_cayley_hparams* hp,
                              void* workspace, size_t workspace_bytes, void* stream);
 
+/* ===========================================================================
+ * Training operators: what runs between a model's last block and the
+ * optimizer step, and makes the gradients that muon_step and muon_adamw_step
+ * consume.  The conventions at the top of this header hold, with these
+ * additions:
+ *  - matrices are row-major with a row pitch `ld_*` in elements (>= cols) and
+ *    unit column stride; vectors are contiguous;
+ *  - every output element is written by every call (nothing accumulates into
+ *    what a buffer held before), and results are the same bits on every run;
+ *  - sums, softmax statistics and norms are held in fp32; an output is rounded
+ *    once (RNE) to its dtype;
+ *  - the calls allocate nothing and copy nothing from the host, so they can be
+ *    captured in a HIP graph.
+ * =========================================================================== */
+
+/* --- Norms around a block, with its gate and residual scale -----------------
+ *   a  = x * rstd0 * post_weight,    rstd0 = 1 / sqrt(mean(x^2) + eps)
+ *        (post_weight NULL: a = x)
+ *   r' = residual_scale * residual + gate * a         (gate NULL: 1)
+ *   n  = r' * rstd1 * pre_weight,    rstd1 = 1 / sqrt(mean(r'^2) + eps)
+ * x is the block's output, residual the stream it joins, n the next block's
+ * input.  n is formed from the fp32 value of r', not from the stored one. */
+#define MUON_GATE_NONE    0
+#define MUON_GATE_CHANNEL 1   /* gate[cols], weight_dtype */
+#define MUON_GATE_FULL    2   /* gate[rows][cols], dtype, pitch ld_gate */
+
+#define MUON_MAX_NORM_COLS 32768
+#define MUON_MAX_TOKENS    ((int64_t)1 << 30)
+
+typedef struct {
+    const void* x;            /* rows x cols */
+    const void* residual;     /* rows x cols */
+    const void* post_weight;  /* cols, or NULL: x is not normalized */
+    const void* gate;         /* by gate_kind; NULL for MUON_GATE_NONE */
+    const void* pre_weight;   /* cols; NULL exactly if out_norm is */
+    void*  out_residual;      /* rows x cols; may be `residual` itself (same pitch) */
+    void*  out_norm;          /* rows x cols, or NULL */
+    float* rstd;              /* 2 x rows (rstd0, rstd1) for the backward pass, or NULL; an absent norm writes 1 */
+    int64_t rows, cols;       /* rows >= 0, 1 <= cols <= MUON_MAX_NORM_COLS */
+    int64_t ld_x, ld_residual, ld_gate, ld_out_residual, ld_out_norm;
+    float   residual_scale;   /* finite */
+    float   eps;              /* finite, >= 0 */
+    int32_t dtype;            /* muon_dtype of the matrices */
+    int32_t weight_dtype;     /* muon_dtype of post_weight, pre_weight and a channel gate */
+    int32_t gate_kind;
+} muon_block_norm_args;
+
+muon_status muon_block_norm(const muon_block_norm_args* args, void* stream);
+
+/* Its gradients.  grad_norm (of n) and grad_out_residual (of r') may each be
+ * NULL (no gradient there), not both; out_residual and rstd are the forward
+ * pass's.  Weight gradients are sums over the rows, in weight_dtype, each NULL
+ * exactly if its weight is. */
+typedef struct {
+    const void* x;
+    const void* out_residual;
+    const float* rstd;               /* 2 x rows */
+    const void* grad_norm;           /* rows x cols or NULL */
+    const void* grad_out_residual;   /* rows x cols or NULL */
+    const void* post_weight;
+    const void* gate;
+    const void* pre_weight;          /* NULL only if grad_norm is */
+    void* grad_x;                    /* rows x cols */
+    void* grad_residual;             /* rows x cols; may be grad_out_residual itself (same pitch) */
+    void* grad_post_weight;          /* cols */
+    void* grad_gate;                 /* cols or rows x cols */
+    void* grad_pre_weight;           /* cols */
+    int64_t rows, cols;
+    int64_t ld_x, ld_out_residual, ld_grad_norm, ld_grad_out_residual, ld_gate, ld_grad_x, ld_grad_residual,
+        ld_grad_gate;
+    float   residual_scale;
+    int32_t dtype, weight_dtype, gate_kind;
+} muon_block_norm_backward_args;
+
+size_t muon_block_norm_backward_workspace_bytes(const muon_block_norm_backward_args* args);
+muon_status muon_block_norm_backward(const muon_block_norm_backward_args* args, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+/* --- Log-probabilities of target tokens under a vocabulary head -------------
+ *   z_ij = scale * sum_k hidden[i][k] head[j][k]
+ *   lse_i = log sum_j exp(z_ij),   logp_i = z_i,target_i - lse_i
+ * The tokens x vocab logits are not formed as an output.  A negative target
+ * marks a token that is not scored: logp = lse = 0, its gradients are zero and
+ * its hidden row is not used, whatever it holds.  A target >= vocab gives
+ * logp = NaN. */
+#define MUON_MAX_VOCAB (1 << 24)
+
+typedef struct {
+    const void*    hidden;    /* tokens x cols */
+    const void*    head;      /* vocab x cols */
+    const int64_t* targets;   /* tokens */
+    float* logp;              /* tokens */
+    float* lse;               /* tokens */
+    void*  saved;             /* muon_token_logp_saved_bytes() bytes, 256-byte aligned, or NULL: keeps what lets
+                                 the backward pass skip forming the logits again */
+    int64_t tokens, cols, vocab;   /* tokens >= 0, cols >= 1, vocab >= 1 */
+    int64_t ld_hidden, ld_head;
+    float   scale;            /* finite */
+    int32_t dtype;            /* muon_dtype of hidden and head */
+} muon_token_logp_args;
+
+size_t muon_token_logp_saved_bytes(const muon_token_logp_args* args);
+size_t muon_token_logp_workspace_bytes(const muon_token_logp_args* args);
+muon_status muon_token_logp(const muon_token_logp_args* args, void* workspace, size_t workspace_bytes, void* stream);
+
+/* With c_i = scale * grad_logp_i and p_ij = exp(z_ij - lse_i):
+ *   dz_ij = c_i ([j = target_i] - p_ij),  grad_hidden = dz head,  grad_head = dz^T hidden
+ * grad_hidden or grad_head may be NULL (not wanted), not both.  `saved` is what
+ * muon_token_logp kept for the same inputs, or NULL.  dz is rounded to the
+ * operands' precision (bf16, or as much of fp32 as three bf16 parts hold)
+ * before the two products. */
+typedef struct {
+    const void*    hidden;
+    const void*    head;
+    const int64_t* targets;
+    const float*   lse;
+    const float*   grad_logp;
+    const void*    saved;
+    void* grad_hidden;        /* tokens x cols or NULL, dtype */
+    void* grad_head;          /* vocab x cols or NULL, dtype */
+    int64_t tokens, cols, vocab;
+    int64_t ld_hidden, ld_head, ld_grad_hidden, ld_grad_head;
+    float   scale;
+    int32_t dtype;
+} muon_token_logp_backward_args;
+
+size_t muon_token_logp_backward_workspace_bytes(const muon_token_logp_backward_args* args);
+muon_status muon_token_logp_backward(const muon_token_logp_backward_args* args, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+/* --- Losses over per-token log-probabilities --------------------------------
+ * Tokens of `sequences` sequences lie one after the other: sequence s is
+ * tokens offsets[s] .. offsets[s + 1) - 1, with offsets in device memory,
+ * 0 <= offsets[0] and non-decreasing up to at most `tokens` (values outside are
+ * taken as the nearest bound; empty sequences are fine).  Tokens of no
+ * sequence, and tokens with mask 0, count for nothing and get gradient 0,
+ * whatever their log-probabilities hold.  The gradient of the loss with respect
+ * to logp, times grad_scale, comes with the same call. */
+
+/* Preference loss over pairs (sequence 2p preferred to sequence 2p + 1), over the
+ * pairs' mean:
+ *   r_s = sum_t mask_t (logp_t - ref_logp_t)   [/ number of counted tokens]
+ *   u = r_2p - r_2p+1,  h = beta u - margin
+ *   SIGMOID  -(1 - e) log sigma(h) - e log sigma(-h)     e = label_smoothing
+ *   HINGE    max(0, 1 - h)
+ *   SQUARED  (u - 1 / (2 beta))^2                        beta != 0, margin unused */
+typedef enum { MUON_PREFERENCE_SIGMOID = 0, MUON_PREFERENCE_HINGE = 1, MUON_PREFERENCE_SQUARED = 2 } muon_preference_kind;
+
+typedef struct {
+    const void*    logp;       /* tokens, dtype */
+    const void*    ref_logp;   /* tokens, dtype, or NULL (0) */
+    const uint8_t* mask;       /* tokens, or NULL (all count) */
+    const int64_t* offsets;    /* sequences + 1 */
+    float* loss;               /* 1 (0 for no pairs) */
+    float* rewards;            /* sequences: beta * r_s, or NULL */
+    void*  grad_logp;          /* tokens, dtype, or NULL */
+    int64_t tokens, sequences; /* sequences even */
+    float   beta, margin, label_smoothing, grad_scale;   /* finite; 0 <= label_smoothing <= 1 */
+    int32_t kind;              /* muon_preference_kind */
+    int32_t average;           /* nonzero: r_s is a mean over the counted tokens (0 if there are none) */
+    int32_t dtype;
+} muon_preference_args;
+
+size_t muon_preference_loss_workspace_bytes(const muon_preference_args* args);
+muon_status muon_preference_loss(const muon_preference_args* args, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+/* Clipped policy loss with a KL term.  Per counted token, with
+ * rho = exp(logp - old_logp), lo = 1 - clip_low, hi = 1 + clip_high:
+ *   gain = min(rho A, clamp(rho, lo, hi) A);  for A < 0 and dual_clip > 0, at least dual_clip A
+ *   KL   K1: logp - ref   K2: (logp - ref)^2 / 2   K3: exp(ref - logp) - (ref - logp) - 1
+ *   l    = -gain + kl_coef KL
+ * A token whose gain is held at a bound gets no gradient from it.
+ * REDUCE_TOKEN:    mean of l over all counted tokens
+ * REDUCE_SEQUENCE: mean over the sequences of each one's mean over its counted
+ *                  tokens (a sequence without any adds 0) */
+typedef enum { MUON_KL_NONE = 0, MUON_KL_K1 = 1, MUON_KL_K2 = 2, MUON_KL_K3 = 3 } muon_kl_kind;
+typedef enum { MUON_REDUCE_TOKEN = 0, MUON_REDUCE_SEQUENCE = 1 } muon_loss_reduction;
+
+typedef struct {
+    const void*    logp;        /* tokens, dtype */
+    const void*    old_logp;    /* tokens, dtype */
+    const void*    ref_logp;    /* tokens, dtype; NULL exactly if kl is MUON_KL_NONE */
+    const float*   advantages;  /* tokens, or sequences (advantage_per_sequence) */
+    const uint8_t* mask;        /* tokens, or NULL */
+    const int64_t* offsets;     /* sequences + 1 */
+    float* loss;                /* 1 */
+    float* stats;               /* 4: mean KL, share of tokens held at a bound, mean rho (over the counted
+                                   tokens), number of counted tokens; or NULL */
+    void*  grad_logp;           /* tokens, dtype, or NULL */
+    int64_t tokens, sequences;
+    float   clip_low, clip_high;   /* >= 0, finite */
+    float   dual_clip;             /* 0 (off), or >= 1, finite */
+    float   kl_coef, grad_scale;   /* finite */
+    int32_t kl, reduction, advantage_per_sequence, dtype;
+} muon_policy_args;
+
+size_t muon_policy_loss_workspace_bytes(const muon_policy_args* args);
+muon_status muon_policy_loss(const muon_policy_args* args, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* muon_status_string(int32_t status);
 /* Detail of the calling thread's last failure ("" if none). */
@@ -232,9 +436,11 @@ const char* muon_last_error_message(void);
  * the summed duration in milliseconds and the number of launches, then
  * resets the counters.  Classes: 0 momentum+norm, 1 norm finalize, 2 Gram,
  * 3 polynomial, 4 update, 5 apply, 6 AdamW, 7 Muon-Cayley (all its kernels),
- * 8 the last update of muon_step, which also applies decay and the step to W.
+ * 8 the last update of muon_step, which also applies decay and the step to W,
+ * 9 block norm (both directions), 10 token log-probabilities (both directions),
+ * 11 preference loss, 12 policy loss.
  * Host-side bookkeeping only. */
-#define MUON_KCLASS_COUNT 9
+#define MUON_KCLASS_COUNT 13
 typedef struct {
     double  ms[MUON_KCLASS_COUNT];
     int64_t launches[MUON_KCLASS_COUNT];

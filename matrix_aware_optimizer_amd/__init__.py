@@ -9,7 +9,13 @@ The names mirror the C entry points:
 ``muon_step``, ``muon_step_noalloc``, ``muon_ns``, ``muon_workspace_bytes``,
 ``muon_ns_workspace_bytes``, ``muon_adamw_step``,
 ``muon_adamw_workspace_bytes``, ``muon_cayley_step``,
-``muon_cayley_workspace_bytes``, ``muon_status_string``,
+``muon_cayley_workspace_bytes``, ``muon_block_norm``,
+``muon_block_norm_backward``, ``muon_block_norm_backward_workspace_bytes``,
+``muon_token_logp``, ``muon_token_logp_backward``,
+``muon_token_logp_saved_bytes``, ``muon_token_logp_workspace_bytes``,
+``muon_token_logp_backward_workspace_bytes``, ``muon_preference_loss``,
+``muon_preference_loss_workspace_bytes``, ``muon_policy_loss``,
+``muon_policy_loss_workspace_bytes``, ``muon_status_string``,
 ``muon_last_error_message``, ``muon_profile_enable``, ``muon_profile_read``,
 ``muon_version``.
 """
@@ -33,9 +39,13 @@ MUON_BF16 = 1
 
 SCALE_RULES = {"naive": 0, "kellerjordan": 1, "mup": 2, "moonlight": 3}
 MUON_FLAG_NESTEROV = 1
-MUON_KCLASS_COUNT = 9
+GATE_NONE, GATE_CHANNEL, GATE_FULL = 0, 1, 2
+PREFERENCE_KINDS = {"sigmoid": 0, "hinge": 1, "squared": 2}
+KL_KINDS = {"none": 0, "k1": 1, "k2": 2, "k3": 3}
+LOSS_REDUCTIONS = {"token": 0, "sequence": 1}
+MUON_KCLASS_COUNT = 13
 KERNEL_CLASSES = ("momentum_norm", "norm_finalize", "gram", "poly", "update", "apply", "adamw", "cayley",
-                  "update_apply")
+                  "update_apply", "block_norm", "token_logp", "preference_loss", "policy_loss")
 
 
 class MuonMatrix(ctypes.Structure):
@@ -79,6 +89,47 @@ class MuonCayleyHparams(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_float), ("beta", ctypes.c_float)]
 
 
+def _fields(spec):
+    kinds = {"p": ctypes.c_void_p, "q": ctypes.c_int64, "f": ctypes.c_float, "i": ctypes.c_int32}
+    return [(name, kinds[kind]) for kind, names in spec for name in names.split()]
+
+
+class MuonBlockNormArgs(ctypes.Structure):
+    _fields_ = _fields([("p", "x residual post_weight gate pre_weight out_residual out_norm rstd"),
+                        ("q", "rows cols ld_x ld_residual ld_gate ld_out_residual ld_out_norm"),
+                        ("f", "residual_scale eps"), ("i", "dtype weight_dtype gate_kind")])
+
+
+class MuonBlockNormBackwardArgs(ctypes.Structure):
+    _fields_ = _fields([("p", "x out_residual rstd grad_norm grad_out_residual post_weight gate pre_weight grad_x "
+                              "grad_residual grad_post_weight grad_gate grad_pre_weight"),
+                        ("q", "rows cols ld_x ld_out_residual ld_grad_norm ld_grad_out_residual ld_gate ld_grad_x "
+                              "ld_grad_residual ld_grad_gate"),
+                        ("f", "residual_scale"), ("i", "dtype weight_dtype gate_kind")])
+
+
+class MuonTokenLogpArgs(ctypes.Structure):
+    _fields_ = _fields([("p", "hidden head targets logp lse saved"), ("q", "tokens cols vocab ld_hidden ld_head"),
+                        ("f", "scale"), ("i", "dtype")])
+
+
+class MuonTokenLogpBackwardArgs(ctypes.Structure):
+    _fields_ = _fields([("p", "hidden head targets lse grad_logp saved grad_hidden grad_head"),
+                        ("q", "tokens cols vocab ld_hidden ld_head ld_grad_hidden ld_grad_head"),
+                        ("f", "scale"), ("i", "dtype")])
+
+
+class MuonPreferenceArgs(ctypes.Structure):
+    _fields_ = _fields([("p", "logp ref_logp mask offsets loss rewards grad_logp"), ("q", "tokens sequences"),
+                        ("f", "beta margin label_smoothing grad_scale"), ("i", "kind average dtype")])
+
+
+class MuonPolicyArgs(ctypes.Structure):
+    _fields_ = _fields([("p", "logp old_logp ref_logp advantages mask offsets loss stats grad_logp"),
+                        ("q", "tokens sequences"), ("f", "clip_low clip_high dual_clip kl_coef grad_scale"),
+                        ("i", "kl reduction advantage_per_sequence dtype")])
+
+
 class MuonProfile(ctypes.Structure):
     _fields_ = [("ms", ctypes.c_double * MUON_KCLASS_COUNT), ("launches", ctypes.c_int64 * MUON_KCLASS_COUNT)]
 
@@ -103,6 +154,23 @@ SIGNATURES = {
                                                       ctypes.POINTER(MuonCayleyHparams)]),
     "muon_cayley_step": (ctypes.c_int32, [ctypes.POINTER(MuonCayleyMatrix), ctypes.c_int32,
                                           ctypes.POINTER(MuonCayleyHparams), ctypes.c_void_p, ctypes.c_size_t,
+                                          ctypes.c_void_p]),
+    "muon_block_norm": (ctypes.c_int32, [ctypes.POINTER(MuonBlockNormArgs), ctypes.c_void_p]),
+    "muon_block_norm_backward_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(MuonBlockNormBackwardArgs)]),
+    "muon_block_norm_backward": (ctypes.c_int32, [ctypes.POINTER(MuonBlockNormBackwardArgs), ctypes.c_void_p,
+                                                  ctypes.c_size_t, ctypes.c_void_p]),
+    "muon_token_logp_saved_bytes": (ctypes.c_size_t, [ctypes.POINTER(MuonTokenLogpArgs)]),
+    "muon_token_logp_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(MuonTokenLogpArgs)]),
+    "muon_token_logp": (ctypes.c_int32, [ctypes.POINTER(MuonTokenLogpArgs), ctypes.c_void_p, ctypes.c_size_t,
+                                         ctypes.c_void_p]),
+    "muon_token_logp_backward_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(MuonTokenLogpBackwardArgs)]),
+    "muon_token_logp_backward": (ctypes.c_int32, [ctypes.POINTER(MuonTokenLogpBackwardArgs), ctypes.c_void_p,
+                                                  ctypes.c_size_t, ctypes.c_void_p]),
+    "muon_preference_loss_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(MuonPreferenceArgs)]),
+    "muon_preference_loss": (ctypes.c_int32, [ctypes.POINTER(MuonPreferenceArgs), ctypes.c_void_p, ctypes.c_size_t,
+                                              ctypes.c_void_p]),
+    "muon_policy_loss_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(MuonPolicyArgs)]),
+    "muon_policy_loss": (ctypes.c_int32, [ctypes.POINTER(MuonPolicyArgs), ctypes.c_void_p, ctypes.c_size_t,
                                           ctypes.c_void_p]),
     "muon_status_string": (ctypes.c_char_p, [ctypes.c_int32]),
     "muon_last_error_message": (ctypes.c_char_p, []),
@@ -164,11 +232,12 @@ def _check(status: int):
 
 def _dtype_code(t) -> int:
     import torch
-    if t.dtype == torch.bfloat16:
+    dtype = t if isinstance(t, torch.dtype) else t.dtype
+    if dtype == torch.bfloat16:
         return MUON_BF16
-    if t.dtype == torch.float32:
+    if dtype == torch.float32:
         return MUON_F32
-    raise ValueError(f"unsupported dtype {t.dtype}; use bfloat16 or float32")
+    raise ValueError(f"unsupported dtype {dtype}; use bfloat16 or float32")
 
 
 def _check_matrix(t, what):
@@ -448,6 +517,349 @@ def muon_cayley_step(weights, grads, moms, *, lr, beta=0.9, workspace=None, stre
     _check(lib.muon_cayley_step(arr, n, ctypes.byref(hp), ctypes.c_void_p(workspace.data_ptr()),
                                 workspace.numel() * workspace.element_size(), _stream_handle(stream)))
     return workspace
+
+
+# --------------------------------------------------------------------------
+# Training operators (norms around a block, token log-probabilities, losses)
+# --------------------------------------------------------------------------
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _same_device(first, *others):
+    """Every tensor on `first`'s device, which has to be the current GPU."""
+    import torch
+    dev = first.device
+    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+        raise ValueError(f"tensors must be on the current GPU, got {dev}")
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors must share one device, got {dev} and {t.device}")
+
+
+def _check_rows(t, what, shape, dtype):
+    """A matrix with unit column stride; returns its row pitch in elements."""
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    pitch, step = t.stride()
+    if shape[1] > 1 and step != 1:
+        raise ValueError(f"{what} must have unit column stride")
+    if shape[0] <= 1:
+        return shape[1]
+    if pitch < shape[1]:
+        raise ValueError(f"{what} has overlapping rows")
+    return pitch
+
+
+def _check_vector(t, what, n, dtypes):
+    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous vector of {n}, got {tuple(t.shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{what} must be one of {dtypes}, got {t.dtype}")
+
+
+def _call(fn, size_fn, args, workspace, device, stream):
+    """Runs one operator with the caller's workspace or one of its own; returns the workspace."""
+    if workspace is None:
+        need = size_fn(ctypes.byref(args))
+        if need == 0:
+            raise MuonError(MUON_ERR_INVALID_ARG, muon_last_error_message())
+        workspace = _workspace_for(int(need), None, device, stream)
+    elif stream is not None:
+        workspace = _workspace_for(0, workspace, device, stream)
+    _check(fn(ctypes.byref(args), ctypes.c_void_p(workspace.data_ptr()),
+              workspace.numel() * workspace.element_size(), _stream_handle(stream)))
+    return workspace
+
+
+def _size(size_fn, args) -> int:
+    need = size_fn(ctypes.byref(args))
+    if need == 0:
+        raise MuonError(MUON_ERR_INVALID_ARG, muon_last_error_message())
+    return int(need)
+
+
+def _norm_weights(x, post_weight, gate, pre_weight):
+    """(weight dtype, gate kind, gate pitch) of the norm's weights, checked against x."""
+    if x.dim() != 2:
+        raise ValueError(f"x must be 2-D, got shape {tuple(x.shape)}")
+    cols = x.shape[1]
+    kind, ld_gate, wdt = GATE_NONE, cols, None
+    if gate is not None:
+        kind = GATE_CHANNEL if gate.dim() == 1 else GATE_FULL
+        if kind == GATE_FULL:
+            ld_gate = _check_rows(gate, "gate", x.shape, x.dtype)
+    for w, what in ((post_weight, "post_weight"), (gate if kind == GATE_CHANNEL else None, "gate"),
+                    (pre_weight, "pre_weight")):
+        if w is None:
+            continue
+        wdt = w.dtype if wdt is None else wdt
+        _check_vector(w, what, cols, (wdt,))
+    return (_dtype_code(x) if wdt is None else _dtype_code(wdt)), kind, ld_gate
+
+
+def muon_block_norm(x, residual, out_residual, out_norm=None, *, post_weight=None, gate=None, pre_weight=None,
+                    rstd=None, residual_scale=1.0, eps=1e-6, stream=None):
+    """Post-norm of a block's output, its gated and scaled residual add, and the next block's pre-norm.
+
+    ``out_residual = residual_scale * residual + gate * (x / rms(x) * post_weight)`` and
+    ``out_norm = out_residual / rms(out_residual) * pre_weight``, ``rms(v) = sqrt(mean(v^2) + eps)`` per row.
+    Without ``post_weight`` x is taken as it is; ``gate`` is a vector over the columns, a matrix like x, or None;
+    ``out_norm`` and ``pre_weight`` go together.  ``out_residual`` may be ``residual`` itself.  ``rstd`` (float32,
+    2 x rows) keeps the two inverse rms for :func:`muon_block_norm_backward`.
+    """
+    import torch
+    wdt, kind, ld_gate = _norm_weights(x, post_weight, gate, pre_weight)
+    rows, cols = x.shape
+    if rstd is not None and (rstd.dtype != torch.float32 or rstd.shape != (2, rows) or not rstd.is_contiguous()):
+        raise ValueError(f"rstd must be contiguous float32 of shape (2, {rows})")
+    args = MuonBlockNormArgs(
+        x.data_ptr(), residual.data_ptr(), _ptr(post_weight), _ptr(gate), _ptr(pre_weight), out_residual.data_ptr(),
+        _ptr(out_norm), _ptr(rstd), rows, cols, _check_rows(x, "x", x.shape, x.dtype),
+        _check_rows(residual, "residual", x.shape, x.dtype), ld_gate,
+        _check_rows(out_residual, "out_residual", x.shape, x.dtype),
+        cols if out_norm is None else _check_rows(out_norm, "out_norm", x.shape, x.dtype),
+        residual_scale, eps, _dtype_code(x), wdt, kind)
+    _same_device(x, residual, post_weight, gate, pre_weight, out_residual, out_norm, rstd)
+    _check(load().muon_block_norm(ctypes.byref(args), _stream_handle(stream)))
+
+
+def muon_block_norm_backward_workspace_bytes(x, *, post_weight=None, gate=None, pre_weight=None) -> int:
+    """Workspace of :func:`muon_block_norm_backward` for these shapes (gradients shaped like what they are of)."""
+    wdt, kind, ld_gate = _norm_weights(x, post_weight, gate, pre_weight)
+    rows, cols = x.shape
+    # sizes only: distinct stand-in addresses, never dereferenced
+    at = iter(range(1 << 44, 1 << 62, 1 << 44))
+
+    def some(t=x):
+        return None if t is None else next(at)
+    args = MuonBlockNormBackwardArgs(
+        some(), some(), some(), some() if pre_weight is not None else None, some(), some(post_weight), some(gate),
+        some(pre_weight), some(), some(), some(post_weight), some(gate), some(pre_weight), rows, cols,
+        cols, cols, cols, cols, cols, cols, cols, cols, 1.0, _dtype_code(x), wdt, kind)
+    return _size(load().muon_block_norm_backward_workspace_bytes, args)
+
+
+def muon_block_norm_backward(x, out_residual, rstd, grad_norm, grad_x, grad_residual, *, grad_out_residual=None,
+                             post_weight=None, gate=None, pre_weight=None, grad_post_weight=None, grad_gate=None,
+                             grad_pre_weight=None, residual_scale=1.0, workspace=None, stream=None):
+    """Gradients of :func:`muon_block_norm`.
+
+    ``grad_norm`` and ``grad_out_residual`` are the gradients of its two outputs (either may be None);
+    ``out_residual`` and ``rstd`` are what it wrote.  ``grad_residual`` may be ``grad_out_residual`` itself.
+    Weight gradients are summed over the rows.
+    """
+    import torch
+    wdt, kind, ld_gate = _norm_weights(x, post_weight, gate, pre_weight)
+    rows, cols = x.shape
+    if rstd.dtype != torch.float32 or rstd.shape != (2, rows) or not rstd.is_contiguous():
+        raise ValueError(f"rstd must be contiguous float32 of shape (2, {rows})")
+    for w, g, what in ((post_weight, grad_post_weight, "post_weight"), (pre_weight, grad_pre_weight, "pre_weight"),
+                       (gate, grad_gate, "gate")):
+        if (w is None) != (g is None):
+            raise ValueError(f"{what} and its gradient go together")
+        if g is not None and g.dim() == 1:
+            _check_vector(g, f"gradient of {what}", cols, (w.dtype,))
+            if w.dim() != 1:
+                raise ValueError(f"gradient of {what} must have its shape")
+
+    def pitch(t, what):
+        return cols if t is None else _check_rows(t, what, x.shape, x.dtype)
+    args = MuonBlockNormBackwardArgs(
+        x.data_ptr(), out_residual.data_ptr(), rstd.data_ptr(), _ptr(grad_norm), _ptr(grad_out_residual),
+        _ptr(post_weight), _ptr(gate), _ptr(pre_weight), grad_x.data_ptr(), grad_residual.data_ptr(),
+        _ptr(grad_post_weight), _ptr(grad_gate), _ptr(grad_pre_weight), rows, cols, pitch(x, "x"),
+        pitch(out_residual, "out_residual"), pitch(grad_norm, "grad_norm"),
+        pitch(grad_out_residual, "grad_out_residual"), ld_gate, pitch(grad_x, "grad_x"),
+        pitch(grad_residual, "grad_residual"), pitch(grad_gate, "grad_gate") if kind == GATE_FULL else cols,
+        residual_scale, _dtype_code(x), wdt, kind)
+    _same_device(x, out_residual, rstd, grad_norm, grad_out_residual, post_weight, gate, pre_weight, grad_x,
+                 grad_residual, grad_post_weight, grad_gate, grad_pre_weight, workspace)
+    lib = load()
+    return _call(lib.muon_block_norm_backward, lib.muon_block_norm_backward_workspace_bytes, args, workspace, x.device,
+                 stream)
+
+
+def _logp_shape(hidden, head):
+    if hidden.dim() != 2 or head.dim() != 2 or hidden.shape[1] != head.shape[1] or hidden.dtype != head.dtype:
+        raise ValueError(f"hidden {tuple(hidden.shape)} {hidden.dtype} and head {tuple(head.shape)} {head.dtype} "
+                         "must be matrices of one dtype and width")
+    return hidden.shape[0], hidden.shape[1], head.shape[0]
+
+
+def _logp_sizes(hidden, head):
+    tokens, cols, vocab = _logp_shape(hidden, head)
+    # sizes only: stand-in addresses, never dereferenced
+    at = [k << 44 for k in range(1, 9)]
+    return tokens, cols, vocab, at
+
+
+def muon_token_logp_saved_bytes(hidden, head) -> int:
+    """Bytes of the ``saved`` buffer that :func:`muon_token_logp` can keep for the backward pass."""
+    tokens, cols, vocab, at = _logp_sizes(hidden, head)
+    args = MuonTokenLogpArgs(*at[:5], None, tokens, cols, vocab, cols, cols, 1.0, _dtype_code(hidden))
+    return _size(load().muon_token_logp_saved_bytes, args)
+
+
+def muon_token_logp_workspace_bytes(hidden, head) -> int:
+    tokens, cols, vocab, at = _logp_sizes(hidden, head)
+    args = MuonTokenLogpArgs(*at[:5], None, tokens, cols, vocab, _check_rows(hidden, "hidden", hidden.shape, hidden.dtype),
+                             _check_rows(head, "head", head.shape, head.dtype), 1.0, _dtype_code(hidden))
+    args.hidden, args.head = hidden.data_ptr() % 256 + at[0], head.data_ptr() % 256 + at[1]
+    return _size(load().muon_token_logp_workspace_bytes, args)
+
+
+def muon_token_logp(hidden, head, targets, logp, lse, *, scale=1.0, saved=None, workspace=None, stream=None):
+    """``logp[i] = z[i, targets[i]] - lse[i]`` with ``z = scale * hidden @ head.T`` and ``lse`` its log-sum-exp.
+
+    The tokens x vocab logits never exist as an output.  ``targets`` is int64; a negative one marks a token that is
+    not scored (logp = lse = 0).  ``logp`` and ``lse`` are float32.  ``saved`` (uint8, at least
+    :func:`muon_token_logp_saved_bytes`) keeps what spares the backward pass the logits' product.
+    """
+    import torch
+    tokens, cols, vocab = _logp_shape(hidden, head)
+    _check_vector(targets, "targets", tokens, (torch.int64,))
+    _check_vector(logp, "logp", tokens, (torch.float32,))
+    _check_vector(lse, "lse", tokens, (torch.float32,))
+    args = MuonTokenLogpArgs(hidden.data_ptr(), head.data_ptr(), targets.data_ptr(), logp.data_ptr(), lse.data_ptr(),
+                             _ptr(saved), tokens, cols, vocab, _check_rows(hidden, "hidden", hidden.shape, hidden.dtype),
+                             _check_rows(head, "head", head.shape, head.dtype), scale, _dtype_code(hidden))
+    _same_device(head, hidden, targets, logp, lse, saved, workspace)
+    lib = load()
+    _check_saved(lib, args, saved)
+    return _call(lib.muon_token_logp, lib.muon_token_logp_workspace_bytes, args, workspace, head.device, stream)
+
+
+def _check_saved(lib, args, saved):
+    if saved is not None:
+        need = lib.muon_token_logp_saved_bytes(ctypes.byref(args))
+        if saved.numel() * saved.element_size() < need:
+            raise MuonError(MUON_ERR_WORKSPACE, f"saved has {saved.numel() * saved.element_size()} bytes, {need} needed")
+
+
+def muon_token_logp_backward_workspace_bytes(hidden, head, *, use_saved=False) -> int:
+    tokens, cols, vocab, at = _logp_sizes(hidden, head)
+    args = MuonTokenLogpBackwardArgs(*at[:5], at[5] if use_saved else None, at[6], at[7], tokens, cols, vocab,
+                                     _check_rows(hidden, "hidden", hidden.shape, hidden.dtype),
+                                     _check_rows(head, "head", head.shape, head.dtype), cols, cols, 1.0,
+                                     _dtype_code(hidden))
+    args.hidden, args.head = hidden.data_ptr() % 256 + at[0], head.data_ptr() % 256 + at[1]
+    return _size(load().muon_token_logp_backward_workspace_bytes, args)
+
+
+def muon_token_logp_backward(hidden, head, targets, lse, grad_logp, grad_hidden=None, grad_head=None, *, scale=1.0,
+                             saved=None, workspace=None, stream=None):
+    """Gradients of :func:`muon_token_logp` for the gradient ``grad_logp`` (float32) of its ``logp``.
+
+    ``grad_hidden`` and ``grad_head`` have their operands' dtype and shape; one of them may be None.  ``saved`` is the
+    buffer that the forward call filled for the same inputs, or None: then the logits are formed again.
+    """
+    import torch
+    tokens, cols, vocab = _logp_shape(hidden, head)
+    _check_vector(targets, "targets", tokens, (torch.int64,))
+    _check_vector(lse, "lse", tokens, (torch.float32,))
+    _check_vector(grad_logp, "grad_logp", tokens, (torch.float32,))
+    args = MuonTokenLogpBackwardArgs(
+        hidden.data_ptr(), head.data_ptr(), targets.data_ptr(), lse.data_ptr(), grad_logp.data_ptr(), _ptr(saved),
+        _ptr(grad_hidden), _ptr(grad_head), tokens, cols, vocab,
+        _check_rows(hidden, "hidden", hidden.shape, hidden.dtype), _check_rows(head, "head", head.shape, head.dtype),
+        cols if grad_hidden is None else _check_rows(grad_hidden, "grad_hidden", hidden.shape, hidden.dtype),
+        cols if grad_head is None else _check_rows(grad_head, "grad_head", head.shape, head.dtype),
+        scale, _dtype_code(hidden))
+    _same_device(head, hidden, targets, lse, grad_logp, saved, grad_hidden, grad_head, workspace)
+    lib = load()
+    _check_saved(lib, MuonTokenLogpArgs(None, None, None, None, None, None, tokens, cols, vocab, cols, cols, scale,
+                                        args.dtype), saved)
+    return _call(lib.muon_token_logp_backward, lib.muon_token_logp_backward_workspace_bytes, args, workspace,
+                 head.device, stream)
+
+
+def _loss_inputs(logp, offsets, mask, loss, grad_logp, *same):
+    """Checks shared by the losses; returns (tokens, sequences)."""
+    import torch
+    n, dt = logp.shape[0] if logp.dim() == 1 else -1, logp.dtype
+    _check_vector(logp, "logp", n, (torch.float32, torch.bfloat16))
+    for t, what in same + ((grad_logp, "grad_logp"),):
+        if t is not None:
+            _check_vector(t, what, n, (dt,))
+    if mask is not None:
+        _check_vector(mask, "mask", n, (torch.uint8, torch.bool))
+    if offsets.dim() != 1 or offsets.numel() < 1 or offsets.dtype != torch.int64 or not offsets.is_contiguous():
+        raise ValueError("offsets must be a contiguous int64 vector of sequences + 1")
+    if loss is not None and (loss.numel() != 1 or loss.dtype != torch.float32):
+        raise ValueError("loss must be one float32")
+    return n, offsets.shape[0] - 1
+
+
+def _choice(table, value, what):
+    if value not in table:
+        raise ValueError(f"unknown {what} {value!r}; one of {sorted(table)}")
+    return table[value]
+
+
+def muon_preference_loss_workspace_bytes(logp, offsets) -> int:
+    n, sequences = _loss_inputs(logp, offsets, None, None, None)
+    at = [k << 44 for k in range(1, 5)]
+    args = MuonPreferenceArgs(at[0], None, None, at[1], at[2], None, at[3], n, sequences, 1.0, 0.0, 0.0, 1.0, 0, 0,
+                              _dtype_code(logp))
+    return _size(load().muon_preference_loss_workspace_bytes, args)
+
+
+def muon_preference_loss(logp, offsets, loss, grad_logp=None, *, ref_logp=None, mask=None, beta=0.1, kind="sigmoid",
+                         label_smoothing=0.0, margin=0.0, average=False, rewards=None, grad_scale=1.0, workspace=None,
+                         stream=None):
+    """Mean preference loss over pairs of sequences, and its gradient with respect to ``logp``.
+
+    Sequence s is ``logp[offsets[s]:offsets[s + 1]]`` (offsets: int64 on the GPU); sequence 2p is preferred to
+    2p + 1.  Tokens with ``mask`` 0 count for nothing.  ``kind`` is "sigmoid", "hinge" or "squared"; ``average``
+    divides each sequence's log ratio by its counted tokens.  ``rewards`` (float32, one per sequence) receives
+    ``beta`` times the log ratios.  ``grad_logp`` is scaled by ``grad_scale``.
+    """
+    import torch
+    n, sequences = _loss_inputs(logp, offsets, mask, loss, grad_logp, (ref_logp, "ref_logp"))
+    if rewards is not None:
+        _check_vector(rewards, "rewards", sequences, (torch.float32,))
+    args = MuonPreferenceArgs(logp.data_ptr(), _ptr(ref_logp), _ptr(mask), offsets.data_ptr(), loss.data_ptr(),
+                              _ptr(rewards), _ptr(grad_logp), n, sequences, beta, margin, label_smoothing, grad_scale,
+                              _choice(PREFERENCE_KINDS, kind, "kind"), 1 if average else 0, _dtype_code(logp))
+    _same_device(offsets, logp, ref_logp, mask, loss, rewards, grad_logp, workspace)
+    lib = load()
+    return _call(lib.muon_preference_loss, lib.muon_preference_loss_workspace_bytes, args, workspace, offsets.device,
+                 stream)
+
+
+def muon_policy_loss_workspace_bytes(logp, offsets) -> int:
+    n, sequences = _loss_inputs(logp, offsets, None, None, None)
+    at = [k << 44 for k in range(1, 7)]
+    args = MuonPolicyArgs(at[0], at[1], None, at[2], None, at[3], at[4], None, at[5], n, sequences, 0.2, 0.2, 0.0, 0.0,
+                          1.0, 0, 0, 0, _dtype_code(logp))
+    return _size(load().muon_policy_loss_workspace_bytes, args)
+
+
+def muon_policy_loss(logp, old_logp, advantages, offsets, loss, grad_logp=None, *, ref_logp=None, mask=None,
+                     clip_low=0.2, clip_high=0.2, dual_clip=0.0, kl_coef=0.0, kl="none", reduction="token",
+                     per_sequence=False, stats=None, grad_scale=1.0, workspace=None, stream=None):
+    """Clipped policy loss with a KL term, and its gradient with respect to ``logp``.
+
+    ``advantages`` (float32) is one per token, or one per sequence with ``per_sequence``.  ``kl`` is "none", "k1",
+    "k2" or "k3" (then with ``ref_logp``), ``reduction`` "token" or "sequence".  ``stats`` (float32, 4) receives the
+    mean KL, the share of tokens held at a bound, the mean ratio and the number of counted tokens.  Sequences,
+    ``mask`` and ``grad_scale`` are as in :func:`muon_preference_loss`.
+    """
+    import torch
+    n, sequences = _loss_inputs(logp, offsets, mask, loss, grad_logp, (old_logp, "old_logp"), (ref_logp, "ref_logp"))
+    _check_vector(advantages, "advantages", sequences if per_sequence else n, (torch.float32,))
+    if stats is not None:
+        _check_vector(stats, "stats", 4, (torch.float32,))
+    args = MuonPolicyArgs(logp.data_ptr(), old_logp.data_ptr(), _ptr(ref_logp), advantages.data_ptr(), _ptr(mask),
+                          offsets.data_ptr(), loss.data_ptr(), _ptr(stats), _ptr(grad_logp), n, sequences, clip_low,
+                          clip_high, dual_clip, kl_coef, grad_scale, _choice(KL_KINDS, kl, "kl"),
+                          _choice(LOSS_REDUCTIONS, reduction, "reduction"), 1 if per_sequence else 0,
+                          _dtype_code(logp))
+    _same_device(offsets, logp, old_logp, ref_logp, advantages, mask, loss, stats, grad_logp, workspace)
+    lib = load()
+    return _call(lib.muon_policy_loss, lib.muon_policy_loss_workspace_bytes, args, workspace, offsets.device, stream)
 
 
 def muon_profile_enable(on: bool = True):

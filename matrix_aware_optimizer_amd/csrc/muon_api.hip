@@ -15,6 +15,7 @@
 #include <type_traits>
 #include <vector>
 
+#include "api_common.h"
 #include "muon.h"
 #include "muon_internal.h"
 
@@ -23,6 +24,11 @@ using namespace muon;
 namespace {
 
 thread_local std::string g_last_error;
+std::mutex g_mu;
+
+}  // namespace
+
+namespace muon {
 
 muon_status fail(muon_status st, const char* fmt, ...) {
     char buf[512];
@@ -38,8 +44,12 @@ muon_status hip_fail(hipError_t e, const char* what) {
     return fail(MUON_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
 
-constexpr size_t ALIGN = 256;
-inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+void clear_error() { g_last_error.clear(); }
+
+}  // namespace muon
+
+namespace {
+
 inline int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
 // ---------------------------------------------------------------------------
@@ -292,9 +302,9 @@ void rebase(Plan& pl, char* base) {
 // Device checks, pinned staging, profiling
 // ---------------------------------------------------------------------------
 
-std::mutex g_mu;
+}  // namespace
 
-muon_status check_device(int* dev_out, int* cu_count) {
+muon_status muon::check_device(int* dev_out, int* cu_count) {
     int dev = 0;
     hipError_t e = hipGetDevice(&dev);
     if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
@@ -317,6 +327,8 @@ muon_status check_device(int* dev_out, int* cu_count) {
     *cu_count = cus[dev];
     return MUON_OK;
 }
+
+namespace {
 
 struct PinnedSlot {
     void* host = nullptr;
@@ -383,25 +395,32 @@ hipEvent_t prof_event() {
     return e;
 }
 
-template <typename F>
-muon_status timed_launch(int cls, hipStream_t s, const char* what, F launch) {
-    hipEvent_t a = nullptr, b = nullptr;
-    bool prof;
+}  // namespace
+
+namespace muon {
+
+ProfMark prof_begin(hipStream_t s) {
+    ProfMark mark;
     {
         std::lock_guard<std::mutex> lk(g_mu);
-        prof = g_prof.on;
-        if (prof) { a = prof_event(); b = prof_event(); }
+        if (!g_prof.on) return mark;
+        mark.a = prof_event();
+        mark.b = prof_event();
     }
-    if (prof && a) (void)hipEventRecord(a, s);
-    hipError_t e = launch();
-    if (e != hipSuccess) return hip_fail(e, what);
-    if (prof && b) {
-        (void)hipEventRecord(b, s);
-        std::lock_guard<std::mutex> lk(g_mu);
-        g_prof.recs.push_back({cls, a, b});
-    }
-    return MUON_OK;
+    if (mark.a) (void)hipEventRecord(mark.a, s);
+    return mark;
 }
+
+void prof_end(int cls, const ProfMark& mark, hipStream_t s) {
+    if (!mark.b) return;
+    (void)hipEventRecord(mark.b, s);
+    std::lock_guard<std::mutex> lk(g_mu);
+    g_prof.recs.push_back({cls, mark.a, mark.b});
+}
+
+}  // namespace muon
+
+namespace {
 
 // ---------------------------------------------------------------------------
 // Workspace of muon_step_noalloc: a file-scope device array, one copy per GPU,

@@ -1,0 +1,67 @@
+// Internal types of the training operators (block_norm.hip, token_logp.hip,
+// losses.hip) and their host side (train_api.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "muon.h"
+#include "muon_internal.h"
+
+namespace muon {
+
+// One element, as fp32, of a buffer of float or bf16 (uint16_t) values.
+template <typename T> __device__ __forceinline__ float ld_el(const void* p, size_t i);
+template <> __device__ __forceinline__ float ld_el<float>(const void* p, size_t i) {
+    return G(static_cast<const float*>(p))[i];
+}
+template <> __device__ __forceinline__ float ld_el<uint16_t>(const void* p, size_t i) {
+    return bf16_to_f32(G(static_cast<const uint16_t*>(p))[i]);
+}
+template <typename T> __device__ __forceinline__ void st_el(void* p, size_t i, float v);
+template <> __device__ __forceinline__ void st_el<float>(void* p, size_t i, float v) { G(static_cast<float*>(p))[i] = v; }
+template <> __device__ __forceinline__ void st_el<uint16_t>(void* p, size_t i, float v) {
+    G(static_cast<uint16_t*>(p))[i] = f32_to_bf16(v);
+}
+// The same with the dtype as a (uniform) value.
+__device__ __forceinline__ float ld_dt(const void* p, size_t i, int dt) {
+    return dt == DT_BF16 ? ld_el<uint16_t>(p, i) : ld_el<float>(p, i);
+}
+__device__ __forceinline__ void st_dt(void* p, size_t i, float v, int dt) {
+    if (dt == DT_BF16) st_el<uint16_t>(p, i, v);
+    else st_el<float>(p, i, v);
+}
+
+// Sum over a workgroup of NT threads, given to every thread; `red` holds NT / 64 floats.
+// The order of the additions is fixed.  Safe to call again at once with the same `red`.
+template <int NT> __device__ __forceinline__ float block_sum(float v, float* red) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+    if constexpr (NT > 64) {
+        lds_barrier();
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+        lds_barrier();
+        v = red[0];
+#pragma unroll
+        for (int w = 1; w < NT / 64; ++w) v += red[w];
+    }
+    return v;
+}
+
+hipError_t launch_block_norm(const muon_block_norm_args& a, int cu_count, hipStream_t s);
+size_t block_norm_backward_bytes(const muon_block_norm_backward_args& a);
+hipError_t launch_block_norm_backward(const muon_block_norm_backward_args& a, void* workspace, hipStream_t s);
+
+size_t token_logp_saved_bytes(const muon_token_logp_args& a);
+size_t token_logp_bytes(const muon_token_logp_args& a);
+hipError_t launch_token_logp(const muon_token_logp_args& a, void* workspace, int cu_count, hipStream_t s);
+size_t token_logp_backward_bytes(const muon_token_logp_backward_args& a);
+hipError_t launch_token_logp_backward(const muon_token_logp_backward_args& a, void* workspace, int cu_count,
+                                      hipStream_t s);
+
+size_t preference_bytes(const muon_preference_args& a);
+hipError_t launch_preference(const muon_preference_args& a, void* workspace, hipStream_t s);
+size_t policy_bytes(const muon_policy_args& a);
+hipError_t launch_policy(const muon_policy_args& a, void* workspace, hipStream_t s);
+
+}  // namespace muon

@@ -1,0 +1,273 @@
+"""GPU parity of the token log-probabilities against the fp64 oracle (through the public entry points).
+
+Bounds, with u = 2^-24 and S_ij = |scale| sum_k |h_ik w_jk|.  A logit is a sum of d products in
+fp32: within E_ij = (d / 16 + 32) u S_ij (bf16 operands: exact products; fp32 operands may be
+multiplied in parts that keep 2^-22 of each product).  lse and logp move by at most
+max_j E_ij each, plus the rounding of the sums, (v / 64 + 64) u.
+dz is rounded to the operands' precision before its products: e = 2^-8 relative for bf16, and twice
+that on p, since a kept exp(z - m) may have been rounded as well; 2^-21 for fp32.  So dz_ij is off by
+at most |c_i| (|[j = y] - p| e + p_ij (2 e + 2 max_j E_ij + (v / 64 + 64) u)), and a gradient by the
+products of that with the operand's magnitudes, its own sum's rounding and its own rounding.
+"""
+import numpy as np
+import pytest
+
+from oracle import train_oracle as to
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+ROUND = {"f32": 2 * U, "bf16": 2.0 ** -8}
+PARTS = {"f32": 2.0 ** -21, "bf16": 2.0 ** -8}
+
+
+def _dt(name):
+    import torch
+    return {"f32": torch.float32, "bf16": torch.bfloat16}[name]
+
+
+def _np(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _inputs(seed, t, d, v, dtype, ignored=0.25, lift=10.0):
+    import torch
+    rng = np.random.default_rng(seed)
+    w = torch.from_numpy((rng.standard_normal((v, d)) / np.sqrt(d)).astype(np.float32)).to(_dt(dtype))
+    y = rng.integers(0, v, t)
+    h = rng.standard_normal((t, d)) + lift * rng.random((t, 1)) * w.double().numpy()[y]
+    h = torch.from_numpy(h.astype(np.float32)).to(_dt(dtype))
+    y[rng.random(t) < ignored] = -100
+    c = (rng.standard_normal(t) / max(1, t)).astype(np.float32)
+    return h.cuda(), w.cuda(), torch.from_numpy(y).cuda(), torch.from_numpy(c).cuda()
+
+
+def _bounds(h, w, y, scale, dtype):
+    h, w = _np(h), _np(w)
+    h = np.where((np.asarray(y.cpu()) >= 0)[:, None], h, 0.0)
+    d, v = h.shape[1], w.shape[0]
+    S = abs(scale) * (np.abs(h) @ np.abs(w).T)
+    E = ((d / 16 + 32) * U + (2.0 ** -22 if dtype == "f32" else 0.0)) * S.max(1)
+    return h, w, E, (v / 64 + 64) * U
+
+
+def _forward(mao, h, w, y, scale=1.0, saved=None, **kw):
+    import torch
+    logp = torch.full((h.shape[0],), float("nan"), device="cuda")
+    lse = torch.full((h.shape[0],), float("nan"), device="cuda")
+    mao.muon_token_logp(h, w, y, logp, lse, scale=scale, saved=saved, **kw)
+    return logp, lse
+
+
+def _check_forward(h, w, y, scale, dtype, logp, lse):
+    hv, wv, E, sums = _bounds(h, w, y, scale, dtype)
+    rl, rs, _ = to.token_logp(hv, wv, np.asarray(y.cpu()), scale=np.float32(scale))
+    gl, gs = _np(logp), _np(lse)
+    assert np.all(np.abs(gl - rl) <= 2 * E + sums + 8 * U * np.abs(rl)), float(np.max(np.abs(gl - rl) / (2 * E + sums)))
+    assert np.all(np.abs(gs - rs) <= 2 * E + sums + 8 * U * np.abs(rs))
+    dead = np.asarray(y.cpu()) < 0
+    assert not gl[dead].any() and not gs[dead].any()
+
+
+def _backward(mao, h, w, y, lse, c, scale=1.0, saved=None, want=("h", "w")):
+    import torch
+    gh = torch.full_like(h, float("nan")) if "h" in want else None
+    gw = torch.full_like(w, float("nan")) if "w" in want else None
+    mao.muon_token_logp_backward(h, w, y, lse, c, gh, gw, scale=scale, saved=saved)
+    return gh, gw
+
+
+def _check_backward(h, w, y, c, scale, dtype, gh, gw):
+    hv, wv, E, sums = _bounds(h, w, y, scale, dtype)
+    yv, cv = np.asarray(y.cpu()), _np(c)
+    rh, rw, dz, p = to.token_logp_backward(hv, wv, yv, cv, scale=np.float32(scale))
+    e = PARTS[dtype]
+    off = np.abs(dz) * e + np.abs(scale * cv)[:, None] * p * (2 * e + 2 * E[:, None] + sums)
+    t, v = dz.shape
+    if gh is not None:
+        b = off @ np.abs(wv) + (v / 16 + 32) * U * (np.abs(dz) @ np.abs(wv)) + ROUND[dtype] * np.abs(rh) + 1e-38
+        err = np.abs(_np(gh) - rh)
+        assert np.all(err <= b), ("grad_hidden", float(np.max(err / b)))
+        assert not _np(gh)[yv < 0].any()
+    if gw is not None:
+        b = off.T @ np.abs(hv) + (t / 16 + 32) * U * (np.abs(dz).T @ np.abs(hv)) + ROUND[dtype] * np.abs(rw) + 1e-38
+        err = np.abs(_np(gw) - rw)
+        assert np.all(err <= b), ("grad_head", float(np.max(err / b)))
+
+
+def _saved(mao, h, w):
+    import torch
+    return torch.full((mao.muon_token_logp_saved_bytes(h, w),), 255, dtype=torch.uint8, device="cuda")
+
+
+SHAPES = [(1, 8, 1), (1, 64, 300), (2, 63, 257), (3, 256, 1000), (16, 100, 515), (17, 128, 4096), (33, 72, 2000), (64, 512, 777),
+          (65, 200, 1025), (255, 64, 256), (257, 320, 513), (300, 96, 3001), (513, 65, 129), (1030, 192, 700)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("t,d,v", SHAPES)
+def test_token_logp_shapes(gpu_lib, t, d, v, dtype):
+    import torch
+    print("[token_logp]", t, d, v, dtype, flush=True)
+    h, w, y, c = _inputs(t * 1009 + v, t, d, v, dtype, ignored=0.25 if t > 1 else 0.0)
+    scale = 0.8
+    saved = _saved(gpu_lib, h, w)
+    logp, lse = _forward(gpu_lib, h, w, y, scale)
+    _check_forward(h, w, y, scale, dtype, logp, lse)
+    gh, gw = _backward(gpu_lib, h, w, y, lse, c, scale)
+    _check_backward(h, w, y, c, scale, dtype, gh, gw)
+    logp2, lse2 = _forward(gpu_lib, h, w, y, scale, saved=saved)
+    _check_forward(h, w, y, scale, dtype, logp2, lse2)
+    gh2, gw2 = _backward(gpu_lib, h, w, y, lse2, c, scale, saved=saved)
+    _check_backward(h, w, y, c, scale, dtype, gh2, gw2)
+    # again, the same bits; one gradient alone, the same bits
+    gh3, _ = _backward(gpu_lib, h, w, y, lse2, c, scale, saved=saved, want=("h",))
+    _, gw3 = _backward(gpu_lib, h, w, y, lse2, c, scale, saved=saved, want=("w",))
+    assert torch.equal(gh2, gh3) and torch.equal(gw2, gw3)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("t", [5, 40, 300])
+def test_token_logp_ignored_and_invalid_targets(gpu_lib, dtype, t):
+    import torch
+    print("[token_logp targets]", t, dtype, flush=True)
+    h, w, y, c = _inputs(5, t, 128, 600, dtype, ignored=0.5)
+    y[0] = 3
+    # what ignored tokens hold does not matter
+    base = _forward(gpu_lib, h, w, y)
+    grads = _backward(gpu_lib, h, w, y, base[1], c)
+    dead = y < 0
+    h2, c2 = h.clone(), c.clone()
+    h2[dead] = float("nan")
+    h2[dead.nonzero()[::2, 0]] = float("inf")
+    c2[dead] = float("nan")
+    got = _forward(gpu_lib, h2, w, y)
+    assert torch.equal(got[0], base[0]) and torch.equal(got[1], base[1])
+    again = _backward(gpu_lib, h2, w, y, got[1], c2)
+    assert torch.equal(again[0], grads[0]) and torch.equal(again[1], grads[1])
+    # nothing scored at all
+    none = torch.full_like(y, -1)
+    logp, lse = _forward(gpu_lib, h2, w, none)
+    assert not logp.any() and not lse.any()
+    gh, gw = _backward(gpu_lib, h2, w, none, lse, c2)
+    assert not torch.count_nonzero(gh) and not torch.count_nonzero(gw)
+    # a target beyond the vocabulary is not silently scored
+    y2 = y.clone()
+    y2[0] = 600
+    logp, lse = _forward(gpu_lib, h, w, y2)
+    assert torch.isnan(logp[0]) and torch.equal(logp[1:], base[0][1:]) and torch.isfinite(lse[0])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("t,d,pitch,shift", [(4, 128, 136, 0), (70, 128, 131, 1), (300, 192, 200, 8), (20, 70, 77, 3)])
+def test_token_logp_strides_and_alignment(gpu_lib, dtype, t, d, pitch, shift):
+    import torch
+    print("[token_logp strides]", t, d, pitch, shift, dtype, flush=True)
+    v = 530
+    h, w, y, c = _inputs(6, t, d, v, dtype)
+
+    def wide(x):
+        buf = torch.full((x.shape[0] * pitch + shift,), float("nan"), dtype=x.dtype, device="cuda")
+        view = buf[shift:].view(x.shape[0], pitch)[:, :d]
+        view.copy_(x)
+        return view
+    hw, ww = wide(h), wide(w)
+    logp, lse = _forward(gpu_lib, hw, ww, y)
+    _check_forward(h, w, y, 1.0, dtype, logp, lse)
+    gh, gw = wide(torch.zeros_like(h)), wide(torch.zeros_like(w))
+    gpu_lib.muon_token_logp_backward(hw, ww, y, lse, c, gh, gw)
+    _check_backward(h, w, y, c, 1.0, dtype, gh, gw)
+    # the padding between the rows is untouched
+    tail = gh.as_strided((t - 1, pitch - d), (pitch, 1), gh.storage_offset() + d)
+    assert torch.isnan(tail).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("t", [3, 100, 260])
+def test_token_logp_extreme_logits(gpu_lib, dtype, t):
+    # logits far apart: a certain token (logp tiny but not lost), one far from the best, a whole row of equal logits,
+    # and logits beyond the range of exp
+    import torch
+    d, v = 64, 900
+    h = torch.zeros((t, d), device="cuda")
+    w = torch.zeros((v, d), device="cuda")
+    w[:, 0] = 1.0
+    w[7, 1] = 1.0
+    h[0, 1] = 30.0                 # the target 30 above the rest: logp = -log1p((v - 1) e^-30)
+    h[1, 1] = 200.0                # another token 200 above the target
+    h[2, 0] = 500.0                # every logit 500 (and 0 at token 7's own column 1)
+    y = torch.full((t,), -100, dtype=torch.int64, device="cuda")
+    y[0], y[1], y[2] = 7, 8, 9
+    h, w = h.to(_dt(dtype)), w.to(_dt(dtype))
+    logp, lse = _forward(gpu_lib, h, w, y)
+    ref = [-np.log1p((v - 1) * np.exp(-30.0)), -200.0, -np.log(v)]
+    got = _np(logp)[:3]
+    assert np.all(np.abs(got - ref) <= 1e-5 * np.abs(ref)), (got, ref)
+    c = torch.ones(t, device="cuda")
+    gh, gw = _backward(gpu_lib, h, w, y, lse, c)
+    assert torch.isfinite(gh).all() and torch.isfinite(gw).all()
+    assert abs(float(gh[1, 1]) + 1.0) <= 1e-2        # -p_7 = -1 along column 1
+
+
+def test_token_logp_no_tokens(gpu_lib):
+    import torch
+    h, w, y, c = _inputs(1, 1, 64, 300, "bf16")
+    logp, lse = _forward(gpu_lib, h[:0], w, y[:0])
+    gw = torch.full_like(w, 7.0)
+    gpu_lib.muon_token_logp_backward(h[:0], w, y[:0], lse, c[:0], h[:0].clone(), gw)
+    assert logp.numel() == 0 and not torch.count_nonzero(gw)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_token_logp_gradient_against_differences(gpu_lib, dtype):
+    # d(sum c logp) along a random direction of hidden and of head, by differences of the fp64 oracle
+    t, d, v = 40, 96, 500
+    h, w, y, c = _inputs(9, t, d, v, dtype)
+    _, lse = _forward(gpu_lib, h, w, y)
+    gh, gw = _backward(gpu_lib, h, w, y, lse, c)
+    rng = np.random.default_rng(1)
+    hv, wv, yv, cv = _np(h), _np(w), np.asarray(y.cpu()), _np(c)
+    for val, grad, which in ((hv, _np(gh), 0), (wv, _np(gw), 1)):
+        e = rng.standard_normal(val.shape)
+        step = 1e-5
+
+        def f(s):
+            args = (hv + s * e, wv) if which == 0 else (hv, wv + s * e)
+            return float((cv * to.token_logp(*args, yv)[0]).sum())
+        num = (f(step) - f(-step)) / (2 * step)
+        size = np.sqrt((grad * grad).sum())     # a random direction sees rounding of about |grad| ROUND
+        assert abs((grad * e).sum() - num) <= 8 * max(ROUND[dtype], 2.0 ** -20) * size + 1e-7
+
+
+def test_token_logp_in_a_graph_and_on_another_stream(gpu_lib):
+    import torch
+    h, w, y, c = _inputs(10, 300, 256, 1111, "bf16")
+    for t in (2, 300):
+        h, y, c = h[:t], y[:t], c[:t]
+        saved = _saved(gpu_lib, h, w)
+        need = max(gpu_lib.muon_token_logp_workspace_bytes(h, w),
+                   gpu_lib.muon_token_logp_backward_workspace_bytes(h, w, use_saved=True))
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        def buffers():
+            return [torch.empty(t, device="cuda"), torch.empty(t, device="cuda"), torch.empty_like(h), torch.empty_like(w)]
+        def call(b, stream=None):
+            gpu_lib.muon_token_logp(h, w, y, b[0], b[1], saved=saved, workspace=ws, stream=stream)
+            gpu_lib.muon_token_logp_backward(h, w, y, b[1], c, b[2], b[3], saved=saved, workspace=ws, stream=stream)
+        want, got = buffers(), buffers()
+        call(want)
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        call(got, side)
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call(got)
+        for _ in range(3):
+            for b in got + [saved, ws]:
+                b.zero_()
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(want, got))
+        h, w, y, c = _inputs(10, 300, 256, 1111, "bf16")
