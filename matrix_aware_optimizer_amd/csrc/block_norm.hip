@@ -127,7 +127,7 @@ int backward_parts(const muon_block_norm_backward_args& a) {
 
 }  // namespace
 
-hipError_t launch_block_norm(const muon_block_norm_args& a, int cu_count, hipStream_t s) {
+hipError_t launch_block_norm(const muon_block_norm_args& a, hipStream_t s) {
     if (a.rows == 0) return hipSuccess;
     hipLaunchKernelGGL(block_norm_kernel, dim3(static_cast<unsigned>(a.rows)), dim3(BN_THREADS), 0, s, a);
     return hipGetLastError();

@@ -1,0 +1,239 @@
+// A 256 x 256 tile of C = A B^T on the gfx950 matrix cores, for the products of the
+// vocabulary head (token_logp.hip): both operands bf16, k-contiguous.
+//
+//   C[r][c] = sum_k A[r][k] B[c][k]
+// One workgroup of 8 waves (2 x 4, two a SIMD); a wave owns 128 x 64 of the tile as 4 x 2 blocks
+// of 32 x 32 (v_mfma_f32_32x32x16_bf16, fp32 sums).  A k-step is 64 values of k: 128 bytes of
+// each of the 256 rows of both operands, loaded straight into LDS (16 bytes a lane) in a
+// ring of five 32 KB slabs, A's slab two steps ahead and B's one.  The loads are spread over
+// the step's MFMA groups, fragments are double-buffered in registers, and the barrier that
+// opens a step stands before the last quarter of the one before it, whose MFMAs then cover
+// the new step's first fragment reads.  Rows are XOR-swizzled by 16-byte chunks against bank
+// conflicts.  Each lane's source rows are fixed for the whole tile, so any row may come from
+// anywhere (gathered tokens, rows clamped at an edge); k is a multiple of 64.
+//
+// fp32 operands are split by the caller into three bf16 parts (8 bits each: 24 in all), stored one
+// after the other, and the tile sums the six products whose parts' indexes add to at most 2,
+// small ones first: what is left out is below 2^-24 of the product of the magnitudes.  Six
+// bf16 products take 6 / 2517 of the time unit against 1 / 157 for the fp32 MFMA: 2.7 times
+// less.
+#pragma once
+
+#include "muon_internal.h"
+
+namespace muon {
+
+namespace pt {
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef short i16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+typedef __attribute__((address_space(3))) char lds_byte_t;
+typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
+typedef __attribute__((address_space(3))) u32x2_t lds_u32x2_t;
+typedef __attribute__((address_space(3))) u32x4 lds_u32x4_t;
+
+constexpr int TILE = 256;            // rows and columns of C
+constexpr int THREADS = 512;
+constexpr int NWAVES = 8, WAVES_N = 4;
+constexpr int WM = 128, WN = 64;     // a wave's share
+constexpr int SM = WM / 32, SN = WN / 32;
+constexpr int KS = 64;               // k per step
+constexpr int CHUNKS = 8;            // 16-byte chunks per row and step
+constexpr int SLAB = TILE * CHUNKS;  // chunks of one operand's step
+constexpr int SLOTS = 5;
+constexpr int LDS_CHUNKS = SLOTS * SLAB;             // 160 KB, all of a CU's LDS
+constexpr int HL = SLAB / 64 / NWAVES;               // loads a wave issues per slab
+constexpr int SUB = CHUNKS / 2;                      // MFMA k-slices per step
+constexpr int PB = (SUB - 1) * SM - HL < HL ? (SUB - 1) * SM - HL : HL;   // loads of A(kt + 2) issued before the barrier
+
+typedef f32x16_t Acc[SM][SN];
+
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6)); }
+__device__ __forceinline__ int swz(int row, int c) { return row * CHUNKS + (c ^ ((row >> 1) & 7)); }
+
+// Which row of the slab, and which of its 16-byte chunks, this lane's load j fetches.
+__device__ __forceinline__ int load_row(int j) { return ((wave_id() * HL + j) * 64 + static_cast<int>(threadIdx.x & 63)) / CHUNKS; }
+__device__ __forceinline__ int load_chunk(int j) {
+    const int row = load_row(j);
+    return (static_cast<int>(threadIdx.x) & 7) ^ ((row >> 1) & 7);
+}
+
+// Parts of the operands (bf16: the value itself; fp32: three parts, pitch a_part / b_part
+// bytes) in the order in which their products are summed, two bits a product.
+template <int PARTS> struct Order;
+template <> struct Order<1> { static constexpr int N = 1; static constexpr unsigned A = 0, B = 0; };
+template <> struct Order<3> {
+    static constexpr int N = 6;                       // (2,0) (0,2) (1,1) (1,0) (0,1) (0,0)
+    static constexpr unsigned A = 2u | 0u << 2 | 1u << 4 | 1u << 6 | 0u << 8 | 0u << 10;
+    static constexpr unsigned B = 0u | 2u << 2 | 1u << 4 | 0u << 6 | 1u << 8 | 0u << 10;
+};
+
+// Byte offset of successive k-steps of one operand over the parts' products.
+template <int PARTS> struct Walk {
+    unsigned order;
+    size_t part;
+    int per, left;      // steps per product, steps left in this one
+    size_t off;
+    __device__ Walk(unsigned o, size_t p, size_t k0, int per_) : order(o), part(p), per(per_), left(per_), off(0), base(k0) { begin(); }
+    __device__ __forceinline__ void begin() { off = base + (PARTS > 1 ? (order & 3u) * part : 0); }
+    __device__ __forceinline__ void next() {
+        off += CHUNKS * 16;
+        if constexpr (PARTS > 1) {
+            if (--left == 0) { order >>= 2; left = per; begin(); }
+        }
+    }
+    size_t base;
+};
+
+// acc += the tile's product over `steps` k-steps (per part product) from byte offset k0 of the
+// rows.  srca[j], srcb[j]: this lane's row of load j, already moved to its chunk
+// (load_row, load_chunk).  steps >= 1.  Ends with every LDS read done by this wave; other waves
+// may still read, so a barrier comes before the LDS is used again.
+template <int PARTS>
+__device__ __attribute__((always_inline)) void run(const char* const (&srca)[HL], const char* const (&srcb)[HL],
+                                                   size_t a_part, size_t b_part, size_t k0, int steps, u32x4* lds,
+                                                   Acc& acc) {
+    const int lane = threadIdx.x & 63, wave = wave_id();
+    const int wm = wave / WAVES_N, wn = wave % WAVES_N;
+    const int total = steps * Order<PARTS>::N;
+    Walk<PARTS> wa(Order<PARTS>::A, a_part, k0, steps), wb(Order<PARTS>::B, b_part, k0, steps);
+    auto issue = [&](const char* s, size_t off, int slot, int j) {
+        __builtin_amdgcn_global_load_lds((const void*)(s + off), (lds_ptr_t)(lds + slot * SLAB + (wave * HL + j) * 64), 16, 0, 0);
+    };
+#pragma unroll
+    for (int j = 0; j < HL; ++j) issue(srca[j], wa.off, 0, j);
+    wa.next();
+#pragma unroll
+    for (int j = 0; j < HL; ++j) issue(srcb[j], wb.off, 1, j);
+    wb.next();
+    if (total > 1) {
+#pragma unroll
+        for (int j = 0; j < HL; ++j) issue(srca[j], wa.off, 2, j);
+        wa.next();
+    }
+    const int half = lane >> 5;
+    const int arow = wm * WM + (lane & 31), brow = wn * WN + (lane & 31);
+    u32x4 fa[2][SM], fb[2][SN];
+    if (total > 1)
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(HL) : "memory");
+    else
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    asm volatile("s_barrier" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < SM; ++i) fa[0][i] = lds[swz(arow + i * 32, half)];
+#pragma unroll
+    for (int j = 0; j < SN; ++j) fb[0][j] = lds[SLAB + swz(brow + j * 32, half)];
+
+    int sa = 0;   // slot of A(kt); B(kt) is in the next one
+    for (int kt = 0; kt < total; ++kt) {
+        const int sb = sa + 1 == SLOTS ? 0 : sa + 1;
+        const int s3 = sa >= 2 ? sa - 2 : sa + 3;   // slot of B(kt + 1)
+        const int s4 = sa >= 1 ? sa - 1 : sa + 4;   // slot of A(kt + 2)
+        const int na = sa >= 3 ? sa - 3 : sa + 2;   // slot of A(kt + 1)
+        const u32x4* LA = lds + sa * SLAB;
+        const u32x4* LB = lds + sb * SLAB;
+        const bool more1 = kt + 1 < total, more2 = kt + 2 < total;
+        const size_t offa = wa.off, offb = wb.off;
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int s = 0; s < SUB; ++s) {
+            if (s == SUB - 1 && more1) {
+                // step kt's slabs have been read, this wave's loads of B(kt + 1) and A(kt + 1)
+                // are done, only A(kt + 2) may be in flight
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                if (more2)
+                    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(PB) : "memory");
+                else
+                    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                asm volatile("s_barrier" ::: "memory");
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            const int cn = 2 * (s + 1) + half;
+#pragma unroll
+            for (int i = 0; i < SM; ++i) {
+#pragma unroll
+                for (int j = 0; j < SN; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, fa[s & 1][i]),
+                                                                        __builtin_bit_cast(bf16x8_t, fb[s & 1][j]),
+                                                                        acc[i][j], 0, 0, 0);
+                if (s + 1 < SUB) {
+                    fa[(s + 1) & 1][i] = LA[swz(arow + i * 32, cn)];
+                    if (i < SN) fb[(s + 1) & 1][i] = LB[swz(brow + i * 32, cn)];
+                } else if (more1) {
+                    fa[0][i] = lds[na * SLAB + swz(arow + i * 32, half)];
+                    if (i < SN) fb[0][i] = lds[s3 * SLAB + swz(brow + i * 32, half)];
+                }
+                const int g = s * SM + i;
+                if (g < HL && more1) issue(srcb[g], offb, s3, g);
+                if (g >= HL && g < 2 * HL && more2) issue(srca[g - HL], offa, s4, g - HL);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        wa.next();
+        wb.next();
+        sa = na;
+    }
+}
+
+// Accumulator register 4 g + p of block (i, j) holds, in lane l of wave (wm, wn), C element
+//   row 128 wm + 32 i + 8 g + 4 (l >> 5) + p,  column 64 wn + 32 j + (l & 31).
+// Staging: the tile as bf16 in LDS, column c at c * 512 bytes, its rows in units of 4 (8 bytes),
+// unit u at position u ^ csw(c): a lane's 4 rows are one write, free of bank conflicts, a
+// column is read back in order (16 bytes = 8 rows) and a row through transpose reads.
+__device__ __forceinline__ int csw(int c) { return (c & 31) ^ (((c >> 5) & 1) << 2); }
+
+struct Stage {
+    int wbase[SN];
+    __device__ Stage() {
+        const int lane = threadIdx.x & 63, wave = wave_id();
+        const int wm = wave / WAVES_N, wn = wave % WAVES_N, h = lane >> 5;
+#pragma unroll
+        for (int j = 0; j < SN; ++j) {
+            const int c = wn * WN + 32 * j + (lane & 31);
+            wbase[j] = c * 512 + 256 * wm + 8 * (h ^ csw(c));
+        }
+    }
+    __device__ __forceinline__ void put(lds_byte_t* L, int i, int j, int g, unsigned w0, unsigned w1) const {
+        *(lds_u32x2_t*)(L + (wbase[j] ^ (64 * i + 16 * g))) = u32x2_t{w0, w1};
+    }
+};
+// Rows 8 q .. 8 q + 7 of column c.
+__device__ __forceinline__ u32x4 stage_col8(const lds_byte_t* L, int c, int q) {
+    const int s = csw(c);
+    const u32x4 v = *(const lds_u32x4_t*)(L + (c * 512 + 16 * (q ^ (s >> 1))));
+    return (s & 1) ? u32x4{v.z, v.w, v.x, v.y} : v;
+}
+// Rows 4 u + (lane & 3), columns col0 + 8 ((lane & 15) >> 2) + 32 (lane >> 4) + (0..7) of the 128
+// columns from col0 (0 or 128): 16 bytes of one row a lane.
+__device__ __forceinline__ u32x4 stage_row8(const lds_byte_t* L, int u, int col0) {
+    const int lane = threadIdx.x & 63, grp = lane >> 4, k = lane & 15;
+    const int c = col0 + 32 * grp + 8 * (k & 3) + (k >> 2);
+    const i16x4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(L + (c * 512 + 8 * (u ^ csw(c)))));
+    const i16x4_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(L + ((c + 4) * 512 + 8 * (u ^ csw(c + 4)))));
+    const u32x2_t a2 = __builtin_bit_cast(u32x2_t, a), b2 = __builtin_bit_cast(u32x2_t, b);
+    return u32x4{a2.x, a2.y, b2.x, b2.y};
+}
+
+// Tiles in runs of 32 on one XCD (the hardware deals workgroups round-robin over the 8), a
+// bijection on [0, nb): a run is a 4 x 8 block of tiles whose operand panels share an L2.
+constexpr int XCDS = 8, XCD_RUN = 32, GROUP = 4;
+__device__ __forceinline__ int xcd_remap(int b, int nb) {
+    const int full = (nb / (XCDS * XCD_RUN)) * (XCDS * XCD_RUN);
+    if (b >= full) return b;
+    const int xcd = b % XCDS, slot = b / XCDS;
+    return ((slot / XCD_RUN) * XCDS + xcd) * XCD_RUN + slot % XCD_RUN;
+}
+// Tile t of ta x tb tiles, in groups of GROUP tiles of b, a-major inside a group.
+__device__ __forceinline__ void tile_of(int t, int ta, int tb, int& ia, int& ib) {
+    const int per = GROUP * ta, g = t / per, r = t - g * per, first = g * GROUP;
+    const int size = min(tb - first, GROUP);
+    ia = r / size;
+    ib = first + r - ia * size;
+}
+
+}  // namespace pt
+
+}  // namespace muon

@@ -3,154 +3,1137 @@
 //   z = scale hidden head^T,  lse_i = log sum_j exp(z_ij),  logp_i = z_i,target_i - lse_i
 //   dz_ij = scale grad_logp_i ([j = target_i] - exp(z_ij - lse_i))
 //   grad_hidden = dz head,  grad_head = dz^T hidden
-// z (tokens x vocab, fp32) is formed by a plain tiled product; dz replaces it in place.
+// The work is the three products (2 tokens vocab cols operations each), bound by the matrix
+// cores; everything else is arranged around the 256 x 256 tile of product_tile.h:
+//
+//  - Only scored tokens are worked on: live_kernel lists them on the GPU, the products
+//    gather their rows of hidden, and workgroups beyond the list end at once.
+//  - Logits: C = head hidden^T, vocabulary along the accumulator rows, so that a lane holds 64
+//    logits of one token and the softmax's running maximum and sum need one exchange between
+//    lanes and one between two waves.  Only (maximum, sum) per token and tile leave the tile;
+//    combine_kernel joins them.  With `saved` the tile's exp(z - tile maximum) goes out too, in
+//    the operands' precision.
+//  - Backward: dz comes from `saved` by an elementwise pass, or from the logits' tile formed again.
+//    It is written both token-major and vocabulary-major, and head and hidden are transposed
+//    once, so that both gradients are k-contiguous products (C rows = columns of the gradient,
+//    C columns = its rows).  Few tiles: the sum over k is split over workgroups that leave fp32
+//    tiles, added in order by slab_sum_kernel.
+//  - fp32 operands travel as three bf16 parts (product_tile.h); dz in fp32 calls too.
+//  - Few tokens: few_kernel reads the head once with 16 x 16 MFMAs and no staging.
+//
+// The statistics are kept in base 2 (z2 = z log2(e)): one multiplication and v_exp_f32.  A target's
+// own term stays out of the sum S of its token, logp = -log(1 + S 2^(M - z2_target)), which keeps its
+// relative precision as logp goes to 0.
+#include <algorithm>
+
+#include "product_tile.h"
 #include "train_internal.h"
 
 namespace muon {
 
 namespace {
 
-constexpr int TL_THREADS = 256;
-constexpr int TL_TILE = 64, TL_K = 16;
+using pt::u32x4;
 
-// C[m][n] = scale sum_k A(m, k) B(k, n), A(m, k) at m * am + k * ak (likewise B and C).
-// Rows m (live_m) or terms k (live_k) of a token that is not scored count as zero.
-struct ProductArgs {
-    const void *a, *b;
-    void* c;
-    size_t am, ak, bn, bk, cm;
-    int adt, bdt, cdt;
-    int64_t m, n, k;
-    float scale;
-    const int64_t *live_m, *live_k;
-};
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+constexpr int64_t FEW_TOKENS = 64;          // most tokens of few_kernel
+constexpr int FEW_ROWS = 32;                // vocabulary entries per workgroup of few_kernel
+constexpr int64_t DZ_BYTES = int64_t{4} << 30;   // both layouts of dz, at most: more tokens go in chunks
+constexpr int WORKGROUPS = 256;             // what a product should fill: one workgroup per CU (LDS)
+constexpr int MAX_SPLITS = 16, MIN_SPLIT_STEPS = 8;
 
-__global__ __launch_bounds__(TL_THREADS) void product_kernel(ProductArgs p) {
-    __shared__ float as[TL_K][TL_TILE + 1], bs[TL_K][TL_TILE + 1];
-    const int64_t m0 = static_cast<int64_t>(blockIdx.y) * TL_TILE, n0 = static_cast<int64_t>(blockIdx.x) * TL_TILE;
-    const int tm = threadIdx.x / 16, tn = threadIdx.x % 16;
-    float acc[4][4] = {};
-    for (int64_t k0 = 0; k0 < p.k; k0 += TL_K) {
-        for (int e = threadIdx.x; e < TL_TILE * TL_K; e += TL_THREADS) {
-            const int64_t r = e / TL_K, k = k0 + e % TL_K;
-            const bool lk = k < p.k && (!p.live_k || p.live_k[k] >= 0);
-            as[e % TL_K][r] = lk && m0 + r < p.m ? ld_dt(p.a, (m0 + r) * p.am + k * p.ak, p.adt) : 0.0f;
-            bs[e % TL_K][r] = lk && n0 + r < p.n ? ld_dt(p.b, (n0 + r) * p.bn + k * p.bk, p.bdt) : 0.0f;
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline int64_t up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+
+// x as bf16 parts, exact to 24 bits: the first two truncated (so nothing overflows), the last rounded.
+__device__ __forceinline__ void split3(float x, uint16_t (&p)[3]) {
+    const uint32_t hi = __float_as_uint(x) & 0xffff0000u;
+    const bool fin = (hi & 0x7f800000u) != 0x7f800000u;
+    p[0] = static_cast<uint16_t>((fin ? hi : hi | (x != x ? 0x00400000u : 0u)) >> 16);
+    const float r = fin ? x - __uint_as_float(hi) : 0.0f;
+    const uint32_t mid = __float_as_uint(r) & 0xffff0000u;
+    p[1] = static_cast<uint16_t>(mid >> 16);
+    p[2] = f32_to_bf16(r - __uint_as_float(mid));
+}
+
+// ---------------------------------------------------------------------------
+// The scored tokens, in order
+// ---------------------------------------------------------------------------
+
+constexpr int LIVE_THREADS = 1024, LIVE_PER = 4;
+
+// idx[0 .. count): the tokens with a target >= 0.  logp and lse (forward) of the others are
+// set to 0.  One workgroup: 8 bytes a token, a few microseconds for 8192.
+__global__ __launch_bounds__(LIVE_THREADS) void live_kernel(const int64_t* targets, int64_t tokens, int32_t* idx,
+                                                            int32_t* count, float* logp, float* lse) {
+    __shared__ int sums[LIVE_THREADS / 64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int base = 0;
+    for (int64_t t0 = 0; t0 < tokens; t0 += LIVE_THREADS * LIVE_PER) {
+        bool on[LIVE_PER];
+        int n = 0;
+#pragma unroll
+        for (int e = 0; e < LIVE_PER; ++e) {
+            const int64_t t = t0 + threadIdx.x * LIVE_PER + e;
+            on[e] = t < tokens && targets[t] >= 0;
+            n += on[e];
+            if (logp && t < tokens && !on[e]) { logp[t] = 0.0f; lse[t] = 0.0f; }
+        }
+        int pre = n;   // inclusive prefix in the wave
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int v = __shfl_up(pre, o, 64);
+            if (lane >= o) pre += v;
         }
         __syncthreads();
-        for (int k = 0; k < TL_K; ++k)
-            for (int i = 0; i < 4; ++i)
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(as[k][tm + 16 * i], bs[k][tn + 16 * j], acc[i][j]);
+        if (lane == 63) sums[wave] = pre;
         __syncthreads();
+        int before = base;
+        for (int w = 0; w < LIVE_THREADS / 64; ++w) {
+            if (w < wave) before += sums[w];
+            base += sums[w];
+        }
+        before += pre - n;
+#pragma unroll
+        for (int e = 0; e < LIVE_PER; ++e)
+            if (on[e]) idx[before++] = static_cast<int32_t>(t0 + threadIdx.x * LIVE_PER + e);
     }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int64_t m = m0 + tm + 16 * i, n = n0 + tn + 16 * j;
-            if (m >= p.m || n >= p.n) continue;
-            const bool live = !p.live_m || p.live_m[m] >= 0;
-            st_dt(p.c, m * p.cm + n, live ? p.scale * acc[i][j] : 0.0f, p.cdt);
+    if (threadIdx.x == 0) *count = base;
+}
+
+// The rows of one call's products along the tokens: entries [first, first + most) of the list.
+struct Live {
+    const int32_t* idx;
+    const int32_t* count;
+    int32_t first, most;
+    __device__ int rows() const { return max(0, min(*count - first, most)); }
+};
+
+// Rows of tokens that are not scored.
+__global__ __launch_bounds__(256) void zero_rows_kernel(const int64_t* targets, int64_t tokens, int64_t cols, void* out,
+                                                        int64_t ld, int dt) {
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+    if (t >= tokens || targets[t] >= 0) return;
+    for (int64_t c = threadIdx.x & 63; c < cols; c += 64) st_dt(out, t * ld + c, 0.0f, dt);
+}
+
+// ---------------------------------------------------------------------------
+// Operand copies
+// ---------------------------------------------------------------------------
+
+struct PackArgs {
+    const void* src;
+    size_t ld;             // elements
+    int64_t rows, cols;    // of src (rows: an upper bound where `live` gives them)
+    int use_live;
+    Live live;
+    uint16_t* dst;
+    size_t dst_ld, part;   // elements
+};
+
+// dst[part][r][0 .. dst_ld) = parts of src[row r], zero past its columns.
+template <typename T, int PARTS>
+__global__ __launch_bounds__(256) void pack_kernel(PackArgs a) {
+    const int64_t rows = a.use_live ? a.live.rows() : a.rows;
+    const int64_t per = a.dst_ld / 8, n = rows * per;
+    for (int64_t q = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; q < n; q += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t r = q / per, c = (q - r * per) * 8;
+        const size_t s = static_cast<size_t>(a.use_live ? a.live.idx[a.live.first + r] : r) * a.ld + c;
+        uint16_t v[8][3];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float x = c + e < a.cols ? ld_el<T>(a.src, s + e) : 0.0f;
+            if constexpr (PARTS == 3) split3(x, v[e]);
+            else v[e][0] = f32_to_bf16(x);
+        }
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p) {
+            u32x4 w;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = v[2 * e][p] | static_cast<uint32_t>(v[2 * e + 1][p]) << 16;
+            G(reinterpret_cast<u32x4*>(a.dst + p * a.part + r * a.dst_ld + c))[0] = w;
+        }
+    }
+}
+
+// dst[part][c][r] = parts of src[row r][c] for c < cols, zero for rows past the last up to a multiple of 64.
+template <typename T, int PARTS>
+__global__ __launch_bounds__(256) void pack_transposed_kernel(PackArgs a) {
+    __shared__ float tile[64][65];
+    const int64_t rows = a.use_live ? a.live.rows() : a.rows;
+    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * 64, c0 = static_cast<int64_t>(blockIdx.y) * 64;
+    if (r0 >= rows) return;
+    const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
+    for (int k = y; k < 64; k += 4) {
+        const int64_t r = r0 + k, c = c0 + x;
+        float v = 0.0f;
+        if (r < rows && c < a.cols) v = ld_el<T>(a.src, static_cast<size_t>(a.use_live ? a.live.idx[a.live.first + r] : r) * a.ld + c);
+        tile[k][x] = v;
+    }
+    __syncthreads();
+    // 8 rows of the source a thread: 16 bytes of one row of the copy
+    for (int k = threadIdx.x; k < 64 * 8; k += 256) {
+        const int c = k / 8, r = (k % 8) * 8;
+        if (c0 + c >= a.cols) continue;
+        uint16_t v[8][3];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if constexpr (PARTS == 3) split3(tile[r + e][c], v[e]);
+            else v[e][0] = f32_to_bf16(tile[r + e][c]);
+        }
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p) {
+            u32x4 w;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = v[2 * e][p] | static_cast<uint32_t>(v[2 * e + 1][p]) << 16;
+            G(reinterpret_cast<u32x4*>(a.dst + p * a.part + (c0 + c) * a.dst_ld + r0 + r))[0] = w;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Logits, tile by tile
+// ---------------------------------------------------------------------------
+
+enum LogitsMode { LG_STATS = 0, LG_SAVE = 1, LG_DZ = 2 };
+
+struct LogitsArgs {
+    const char* a;          // head rows (bytes pitch a_ld, parts a_part apart)
+    size_t a_ld, a_part;
+    const char* b;          // hidden rows, by token (gather) or packed by list entry
+    size_t b_ld, b_part;
+    int gather;
+    Live live;
+    const int64_t* targets;
+    int vocab, steps, ta, tb;
+    float scale2;           // scale log2(e)
+    float *m, *s, *zt;      // statistics: tile x list entry (pitch rows_pitch); target logit by list entry
+    size_t rows_pitch;
+    void* e;                // LG_SAVE: exp(z - m), list entry x vocabulary (pitch vp)
+    // LG_DZ
+    const float *lse, *grad_logp;
+    float scale;
+    uint16_t *dz, *dzt;     // dz and its transpose: parts apart, pitches vp and rows_pitch; rows relative to live.first
+    size_t dz_part, dzt_part;
+    size_t vp;
+};
+
+// The staged tile's columns as rows of `dst` (256 values each from column v0), column c at row r0 + c.
+__device__ __forceinline__ void store_cols(const pt::lds_byte_t* L, uint16_t* dst, size_t ld, size_t r0, size_t v0) {
+#pragma unroll 4
+    for (int k = 0; k < 16; ++k) {
+        const int c = 16 * k + static_cast<int>(threadIdx.x >> 5), q = threadIdx.x & 31;
+        __builtin_nontemporal_store(pt::stage_col8(L, c, q), G(reinterpret_cast<u32x4*>(dst + (r0 + c) * ld + v0 + 8 * q)));
+    }
+}
+// The staged tile's rows as rows of `dst`.
+__device__ __forceinline__ void store_rows(const pt::lds_byte_t* L, uint16_t* dst, size_t ld, size_t v0, size_t r0) {
+    const int lane = threadIdx.x & 63, wave = pt::wave_id();
+#pragma unroll 2
+    for (int k = 0; k < 16; ++k) {
+        const int u = 8 * wave + (k >> 1), col0 = 128 * (k & 1);
+        const size_t row = v0 + 4 * u + (lane & 3), col = r0 + col0 + 32 * (lane >> 4) + 8 * ((lane & 15) >> 2);
+        __builtin_nontemporal_store(pt::stage_row8(L, u, col0), G(reinterpret_cast<u32x4*>(dst + row * ld + col)));
+    }
+}
+
+template <int PARTS, int MODE>
+__global__ __launch_bounds__(pt::THREADS, 2) void logits_kernel(LogitsArgs a) {
+    __shared__ u32x4 lds[pt::LDS_CHUNKS];
+    pt::lds_byte_t* L = (pt::lds_byte_t*)lds;
+    const int n = a.live.rows();
+    const int tb = (n + pt::TILE - 1) / pt::TILE, nb = a.ta * tb;
+    if (static_cast<int>(blockIdx.x) >= nb) return;
+    int ia, ib;
+    pt::tile_of(pt::xcd_remap(blockIdx.x, nb), a.ta, tb, ia, ib);
+    const int v0 = ia * pt::TILE, r0 = ib * pt::TILE;
+    const char *sa[pt::HL], *sb[pt::HL];
+#pragma unroll
+    for (int j = 0; j < pt::HL; ++j) {
+        const int row = pt::load_row(j);
+        sa[j] = a.a + static_cast<size_t>(min(v0 + row, a.vocab - 1)) * a.a_ld + pt::load_chunk(j) * 16;
+        int r = min(r0 + row, n - 1);
+        if (a.gather) r = a.live.idx[a.live.first + r];
+        sb[j] = a.b + static_cast<size_t>(r) * a.b_ld + pt::load_chunk(j) * 16;
+    }
+    pt::Acc acc = {};
+    pt::run<PARTS>(sa, sb, a.a_part, a.b_part, 0, a.steps, lds, acc);
+
+    const int lane = threadIdx.x & 63, wave = pt::wave_id();
+    const int wm = wave / pt::WAVES_N, wn = wave % pt::WAVES_N, h = lane >> 5;
+    const int vl = v0 + pt::WM * wm + 4 * h;          // this lane's first vocabulary entry
+    const bool edge = v0 + pt::TILE > a.vocab;        // uniform: entries past the vocabulary
+    lds_barrier();                                    // every wave is done with the operand slabs
+
+    if constexpr (MODE != LG_DZ) {
+        float* smax = reinterpret_cast<float*>(lds);          // [2][256]
+        float* ssum = smax + 2 * pt::TILE;                    // [2][256]
+        int col[pt::SN], y[pt::SN];
+        float mx[pt::SN];
+#pragma unroll
+        for (int j = 0; j < pt::SN; ++j) {
+            col[j] = pt::WN * wn + 32 * j + (lane & 31);
+            const int r = min(r0 + col[j], n - 1);
+            const int64_t t = a.targets[a.live.idx[a.live.first + r]];
+            y[j] = t < a.vocab ? static_cast<int>(t) - vl : -1;
+            mx[j] = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < pt::SM; ++i)
+#pragma unroll
+                for (int q = 0; q < 16; ++q) {
+                    const int dv = 32 * i + 8 * (q >> 2) + (q & 3);
+                    float z = acc[i][j][q] * a.scale2;
+                    if (edge && vl + dv >= a.vocab) z = -INFINITY;
+                    acc[i][j][q] = z;
+                    mx[j] = fmaxf(mx[j], z);
+                }
+            mx[j] = fmaxf(mx[j], __shfl_xor(mx[j], 32, 64));
+            if (h == 0) smax[pt::TILE * wm + col[j]] = mx[j];
+        }
+        lds_barrier();
+#pragma unroll
+        for (int j = 0; j < pt::SN; ++j) {
+            mx[j] = fmaxf(mx[j], smax[pt::TILE * (wm ^ 1) + col[j]]);
+            const float base = mx[j] == -INFINITY ? 0.0f : mx[j];
+            float sum = 0.0f, zt = 0.0f;
+            bool mine = false;
+#pragma unroll
+            for (int i = 0; i < pt::SM; ++i)
+#pragma unroll
+                for (int q = 0; q < 16; ++q) {
+                    const int dv = 32 * i + 8 * (q >> 2) + (q & 3);
+                    const float z = acc[i][j][q], ex = __builtin_amdgcn_exp2f(z - base);
+                    const bool target = dv == y[j];
+                    sum += target ? 0.0f : ex;
+                    if (target) { zt = z; mine = true; }
+                    if (MODE == LG_SAVE) acc[i][j][q] = ex;
+                }
+            sum += __shfl_xor(sum, 32, 64);
+            if (h == 0) ssum[pt::TILE * wm + col[j]] = sum;
+            if (mine && r0 + col[j] < n) a.zt[a.live.first + r0 + col[j]] = zt;
+        }
+        lds_barrier();
+#pragma unroll
+        for (int j = 0; j < pt::SN; ++j)
+            if (wm == 0 && h == 0) {
+                const size_t o = ia * a.rows_pitch + r0 + col[j];
+                a.m[o] = mx[j];
+                a.s[o] = ssum[col[j]] + ssum[pt::TILE + col[j]];
+            }
+        if constexpr (MODE == LG_SAVE) {
+            if constexpr (PARTS == 1) {
+                lds_barrier();
+                const pt::Stage st;
+#pragma unroll
+                for (int i = 0; i < pt::SM; ++i)
+#pragma unroll
+                    for (int j = 0; j < pt::SN; ++j)
+#pragma unroll
+                        for (int g = 0; g < 4; ++g)
+                            st.put(L, i, j, g, pack_bf16x2(acc[i][j][4 * g], acc[i][j][4 * g + 1]),
+                                   pack_bf16x2(acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]));
+                lds_barrier();
+                store_cols(L, static_cast<uint16_t*>(a.e), a.vp, r0, v0);
+            } else {
+                float* e = static_cast<float*>(a.e);
+#pragma unroll
+                for (int j = 0; j < pt::SN; ++j)
+#pragma unroll
+                    for (int i = 0; i < pt::SM; ++i)
+#pragma unroll
+                        for (int g = 0; g < 4; ++g)
+                            st_f4(e + (static_cast<size_t>(r0) + col[j]) * a.vp + vl + 32 * i + 8 * g,
+                                  make_float4(acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]));
+            }
+        }
+    } else {
+        const pt::Stage st;
+#pragma unroll
+        for (int j = 0; j < pt::SN; ++j) {
+            const int r = r0 + pt::WN * wn + 32 * j + (lane & 31);
+            const int tok = a.live.idx[a.live.first + min(r, n - 1)];
+            const int64_t t = a.targets[tok];
+            const int y = t < a.vocab ? static_cast<int>(t) - vl : -1;
+            const float c = r < n ? a.scale * a.grad_logp[tok] : 0.0f, l2 = a.lse[tok] * LOG2E;
+#pragma unroll
+            for (int i = 0; i < pt::SM; ++i)
+#pragma unroll
+                for (int q = 0; q < 16; ++q) {
+                    const int dv = 32 * i + 8 * (q >> 2) + (q & 3);
+                    const float p = __builtin_amdgcn_exp2f(fmaf(acc[i][j][q], a.scale2, -l2));
+                    float d = c * ((dv == y ? 1.0f : 0.0f) - p);
+                    if (c == 0.0f || (edge && vl + dv >= a.vocab)) d = 0.0f;
+                    acc[i][j][q] = d;
+                }
+        }
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p) {
+            if (p > 0) lds_barrier();
+#pragma unroll
+            for (int i = 0; i < pt::SM; ++i)
+#pragma unroll
+                for (int j = 0; j < pt::SN; ++j)
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        if (p + 1 < PARTS) {   // this part, truncated; the rest stays
+                            unsigned w[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                w[e] = __float_as_uint(acc[i][j][4 * g + e]) & 0xffff0000u;
+                                const float rest = acc[i][j][4 * g + e] - __uint_as_float(w[e]);
+                                acc[i][j][4 * g + e] = (w[e] & 0x7f800000u) == 0x7f800000u ? 0.0f : rest;
+                            }
+                            st.put(L, i, j, g, w[0] >> 16 | w[1], w[2] >> 16 | w[3]);
+                        } else {
+                            st.put(L, i, j, g, pack_bf16x2(acc[i][j][4 * g], acc[i][j][4 * g + 1]),
+                                   pack_bf16x2(acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]));
+                        }
+                    }
+            lds_barrier();
+            if (a.dz) store_cols(L, a.dz + p * a.dz_part, a.vp, r0, v0);
+            if (a.dzt) store_rows(L, a.dzt + p * a.dzt_part, a.rows_pitch, v0, r0);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// dz from the kept exp(z - m)
+// ---------------------------------------------------------------------------
+
+struct DzArgs {
+    const void* e;          // list entry x vocabulary, pitch vp
+    const float* m;         // tile x list entry
+    const float* logp;      // list entry
+    size_t m_pitch;
+    Live live;
+    const int64_t* targets;
+    const float *lse, *grad_logp;
+    float scale;
+    int vocab;
+    size_t vp, rows_pitch;
+    uint16_t *dz, *dzt;     // rows relative to live.first
+    size_t dz_part, dzt_part;
+};
+
+// 64 tokens x 64 entries a workgroup.  Reads 2 (fp32: 4) bytes an element and writes 2 x 2 (2 x 6), HBM-bound.
+template <typename T, int PARTS>
+__global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
+    __shared__ uint16_t tile[PARTS][64][72];   // [entry][token]
+    const int n = a.live.rows();
+    const int r0 = blockIdx.y * 64, v0 = blockIdx.x * 64;
+    if (r0 >= static_cast<int>((n + pt::TILE - 1) / pt::TILE * pt::TILE)) return;
+    const int vb = threadIdx.x & 7;            // 8 entries each
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const int rt = (threadIdx.x >> 3) + 32 * half, r = r0 + rt;
+        float c = 0.0f, f = 0.0f, dy = 0.0f;
+        int y = -1;
+        if (r < n) {
+            const int tok = a.live.idx[a.live.first + r];
+            const int64_t t = a.targets[tok];
+            c = a.scale * a.grad_logp[tok];
+            y = t < a.vocab ? static_cast<int>(t) - v0 - 8 * vb : -1;
+            f = c * __builtin_amdgcn_exp2f(a.m[(v0 / pt::TILE) * a.m_pitch + a.live.first + r] - a.lse[tok] * LOG2E);
+            // 1 - p of the target from logp: e is rounded, which 1 - e f would magnify as p goes to 1
+            dy = -c * expm1f(a.logp[a.live.first + r]);
+        }
+        float x[8];
+        const size_t o = (static_cast<size_t>(a.live.first) + min(r, n - 1)) * a.vp + v0 + 8 * vb;
+        if constexpr (sizeof(T) == 2) {
+            const u32x4 w = G(reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.e) + o))[0];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = __uint_as_float((k & 1) ? (w[k >> 1] & 0xffff0000u) : (w[k >> 1] << 16));
+        } else {
+            const float4 w0 = ld_f4(static_cast<const float*>(a.e) + o), w1 = ld_f4(static_cast<const float*>(a.e) + o + 4);
+            x[0] = w0.x; x[1] = w0.y; x[2] = w0.z; x[3] = w0.w;
+            x[4] = w1.x; x[5] = w1.y; x[6] = w1.z; x[7] = w1.w;
+        }
+        uint16_t v[8][3];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float d = c == 0.0f || v0 + 8 * vb + k >= a.vocab ? 0.0f : k == y ? dy : -x[k] * f;
+            if constexpr (PARTS == 3) split3(d, v[k]);
+            else v[k][0] = f32_to_bf16(d);
+        }
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p) {
+            if (a.dz) {
+                u32x4 w;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[k] = v[2 * k][p] | static_cast<uint32_t>(v[2 * k + 1][p]) << 16;
+                G(reinterpret_cast<u32x4*>(a.dz + p * a.dz_part + static_cast<size_t>(r) * a.vp + v0 + 8 * vb))[0] = w;
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) tile[p][8 * vb + k][rt] = v[k][p];
+        }
+    }
+    if (!a.dzt) return;
+    __syncthreads();
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int v = (threadIdx.x >> 3) + 32 * half, q = 8 * (threadIdx.x & 7);
+            const u32x4 w = *reinterpret_cast<const u32x4*>(&tile[p][v][q]);
+            G(reinterpret_cast<u32x4*>(a.dzt + p * a.dzt_part + static_cast<size_t>(v0 + v) * a.rows_pitch + r0 + q))[0] = w;
         }
 }
 
-hipError_t launch_product(const ProductArgs& p, hipStream_t s) {
-    if (p.m == 0 || p.n == 0) return hipSuccess;
-    const dim3 grid(static_cast<unsigned>((p.n + TL_TILE - 1) / TL_TILE), static_cast<unsigned>((p.m + TL_TILE - 1) / TL_TILE));
-    hipLaunchKernelGGL(product_kernel, grid, dim3(TL_THREADS), 0, s, p);
+// ---------------------------------------------------------------------------
+// Gradients: C rows = columns of the gradient, C columns = its rows
+// ---------------------------------------------------------------------------
+
+struct GradArgs {
+    const char* a;          // transposed operand: one row per gradient column
+    size_t a_ld, a_part;
+    const char* b;          // dz (rows = list entries) or its transpose (rows = vocabulary)
+    size_t b_ld, b_part;
+    Live live;
+    int cols, rows;         // rows: vocabulary; for grad_hidden the list gives them
+    int by_token;           // grad_hidden: rows from the list, out rows are its tokens
+    int steps;              // k-steps (by_token: over the vocabulary), else the list gives them
+    int ta, tb, splits;
+    void* out;              // bf16, 16-byte aligned rows: written directly when slab is NULL
+    size_t ld;
+    float* slab;            // fp32 tiles in accumulator layout, [split][tile][32][512] x 16 bytes
+    int add;                // add to what the slab holds (later chunks of tokens)
+};
+
+template <int PARTS>
+__global__ __launch_bounds__(pt::THREADS, 2) void grad_kernel(GradArgs a) {
+    __shared__ u32x4 lds[pt::LDS_CHUNKS];
+    pt::lds_byte_t* L = (pt::lds_byte_t*)lds;
+    const int n = a.live.rows();
+    const int rows = a.by_token ? n : a.rows, all = a.by_token ? a.steps : (n + pt::KS - 1) / pt::KS;
+    const int tb = (rows + pt::TILE - 1) / pt::TILE, nb = a.ta * tb;
+    if (static_cast<int>(blockIdx.x) >= nb) return;
+    const int tile = pt::xcd_remap(blockIdx.x, nb);
+    int ia, ib;
+    pt::tile_of(tile, a.ta, tb, ia, ib);
+    const int c0 = ia * pt::TILE, r0 = ib * pt::TILE;
+    const int split = blockIdx.y;
+    const int k_first = static_cast<int>(static_cast<int64_t>(all) * split / a.splits);
+    const int steps = static_cast<int>(static_cast<int64_t>(all) * (split + 1) / a.splits) - k_first;
+    pt::Acc acc = {};
+    if (steps > 0) {
+        const char *sa[pt::HL], *sb[pt::HL];
+#pragma unroll
+        for (int j = 0; j < pt::HL; ++j) {
+            const int row = pt::load_row(j);
+            sa[j] = a.a + static_cast<size_t>(min(c0 + row, a.cols - 1)) * a.a_ld + pt::load_chunk(j) * 16;
+            sb[j] = a.b + static_cast<size_t>(r0 + row) * a.b_ld + pt::load_chunk(j) * 16;   // padded to the tile
+        }
+        pt::run<PARTS>(sa, sb, a.a_part, a.b_part, static_cast<size_t>(k_first) * (pt::KS * 2), steps, lds, acc);
+    }
+    if (a.slab) {
+        float* s = a.slab + (static_cast<size_t>(split) * a.ta * a.tb + tile) * (pt::TILE * pt::TILE) + threadIdx.x * 4;
+#pragma unroll
+        for (int i = 0; i < pt::SM; ++i)
+#pragma unroll
+            for (int j = 0; j < pt::SN; ++j)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    float* p = s + static_cast<size_t>((i * pt::SN + j) * 4 + g) * (pt::THREADS * 4);
+                    float4 v = make_float4(acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]);
+                    if (a.add) {
+                        const float4 o = ld_f4(p);
+                        v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+                    }
+                    st_f4(p, v);
+                }
+        return;
+    }
+    lds_barrier();
+    const pt::Stage st;
+#pragma unroll
+    for (int i = 0; i < pt::SM; ++i)
+#pragma unroll
+        for (int j = 0; j < pt::SN; ++j)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                st.put(L, i, j, g, pack_bf16x2(acc[i][j][4 * g], acc[i][j][4 * g + 1]),
+                       pack_bf16x2(acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]));
+    lds_barrier();
+    uint16_t* out = static_cast<uint16_t*>(a.out);
+#pragma unroll 4
+    for (int k = 0; k < 16; ++k) {
+        const int c = 16 * k + static_cast<int>(threadIdx.x >> 5), q = threadIdx.x & 31;
+        if (r0 + c >= rows) continue;
+        const size_t row = a.by_token ? a.live.idx[a.live.first + r0 + c] : r0 + c;
+        const u32x4 v = pt::stage_col8(L, c, q);
+        uint16_t* p = out + row * a.ld + c0 + 8 * q;
+        if (c0 + 8 * q + 8 <= a.cols) {
+            G(reinterpret_cast<u32x4*>(p))[0] = v;
+        } else {
+            for (int e = 0; e < 8; ++e)
+                if (c0 + 8 * q + e < a.cols) G(p)[e] = static_cast<uint16_t>(v[e >> 1] >> (16 * (e & 1)));
+        }
+    }
+}
+
+// Sums the splits' tiles in order and writes the gradient; one wave per 32 x 32 block.
+__global__ __launch_bounds__(256) void slab_sum_kernel(GradArgs a, int dt) {
+    __shared__ float tile[4][32][33];   // [wave][gradient row][gradient column]
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int block = blockIdx.x * 4 + wave, t = block / 64, b = block % 64;
+    const int rows = a.by_token ? a.live.rows() : a.rows;
+    const int tb = (rows + pt::TILE - 1) / pt::TILE;
+    if (t >= a.ta * tb) return;
+    int ia, ib;
+    pt::tile_of(t, a.ta, tb, ia, ib);
+    const int w = b / 8, i = (b % 8) / pt::SN, j = b % pt::SN;
+    const int c0 = ia * pt::TILE + pt::WM * (w / pt::WAVES_N) + 32 * i, r0 = ib * pt::TILE + pt::WN * (w % pt::WAVES_N) + 32 * j;
+    if (c0 >= a.cols || r0 >= rows) return;
+    float4 v[4] = {};
+    for (int s = 0; s < a.splits; ++s) {
+        const float* p = a.slab + (static_cast<size_t>(s) * a.ta * a.tb + t) * (pt::TILE * pt::TILE) + (64 * w + lane) * 4;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const float4 x = ld_f4(p + static_cast<size_t>((i * pt::SN + j) * 4 + g) * (pt::THREADS * 4));
+            v[g] = make_float4(v[g].x + x.x, v[g].y + x.y, v[g].z + x.z, v[g].w + x.w);
+        }
+    }
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        float* q = &tile[wave][lane & 31][8 * g + 4 * (lane >> 5)];
+        q[0] = v[g].x; q[1] = v[g].y; q[2] = v[g].z; q[3] = v[g].w;
+    }
+    __builtin_amdgcn_wave_barrier();   // one wave's LDS: its writes come before its reads
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    const int c = c0 + (lane & 31);
+    if (c >= a.cols) return;
+#pragma unroll 4
+    for (int k = 0; k < 16; ++k) {
+        const int r = 2 * k + (lane >> 5);
+        if (r0 + r >= rows) continue;
+        const size_t row = a.by_token ? a.live.idx[a.live.first + r0 + r] : r0 + r;
+        st_dt(a.out, row * a.ld + c, tile[wave][r][lane & 31], dt);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Few tokens: the head is read once
+// ---------------------------------------------------------------------------
+
+typedef float f32x4m_t __attribute__((ext_vector_type(4)));
+
+// 8 values of k of one row from column k, zero past the last column, as bf16 parts.
+template <typename T, int PARTS, bool VEC>
+__device__ __forceinline__ void few_load(const void* base, size_t off, int k, int cols, u32x4 (&out)[PARTS]) {
+    float x[8];
+    if constexpr (sizeof(T) == 2 && VEC) {
+        out[0] = k < cols ? G(reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + off + k))[0] : u32x4{};
+        return;
+    } else if constexpr (VEC) {
+        const float* p = static_cast<const float*>(base) + off + k;
+        const float4 a = k < cols ? ld_f4(p) : float4{}, b = k < cols ? ld_f4(p + 4) : float4{};
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = k + e < cols ? ld_el<T>(base, off + k + e) : 0.0f;
+    }
+    uint16_t v[8][3];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        if constexpr (PARTS == 3) split3(x[e], v[e]);
+        else v[e][0] = f32_to_bf16(x[e]);
+    }
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out[p][e] = v[2 * e][p] | static_cast<uint32_t>(v[2 * e + 1][p]) << 16;
+}
+
+struct FewArgs {
+    const void *head, *hidden;
+    size_t ld_head, ld_hidden;
+    const int64_t* targets;
+    int tokens, cols, vocab, tiles;
+    float scale2;
+    float *m, *s, *zt;      // token x tile; target logit by token
+};
+
+// FEW_ROWS entries x up to 16 NT tokens a workgroup; its four waves take 64 values of k in turn.  Vocabulary
+// along the accumulator rows, tokens along the columns (16 x 16 MFMA).  HBM-bound: the head once,
+// cols x vocab elements; hidden comes from the caches.
+template <typename T, int PARTS, int NT, bool VEC>
+__global__ __launch_bounds__(256) void few_kernel(FewArgs a) {
+    __shared__ float red[4][FEW_ROWS][16 * NT + 1];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int v0 = blockIdx.x * FEW_ROWS, ln = lane & 15, kg = 8 * (lane >> 4);
+    size_t wo[2], ho[NT];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) wo[r] = static_cast<size_t>(min(v0 + 16 * r + ln, a.vocab - 1)) * a.ld_head;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) ho[t] = static_cast<size_t>(min(16 * t + ln, a.tokens - 1)) * a.ld_hidden;
+    f32x4m_t acc[2][NT] = {};
+    constexpr int DEEP = PARTS == 1 && VEC ? 4 : 1;   // 64-value runs of k in flight
+    for (int k0 = 64 * wave; k0 < a.cols; k0 += 256 * DEEP) {
+        u32x4 w[2 * DEEP][2][PARTS], h[2 * DEEP][NT][PARTS];
+#pragma unroll
+        for (int b = 0; b < 2 * DEEP; ++b) {
+            const int k = k0 + 256 * (b >> 1) + 32 * (b & 1) + kg;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) few_load<T, PARTS, VEC>(a.head, wo[r], k, a.cols, w[b][r]);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) few_load<T, PARTS, VEC>(a.hidden, ho[t], k, a.cols, h[b][t]);
+        }
+#pragma unroll
+        for (int b = 0; b < 2 * DEEP; ++b) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int q = 0; q < pt::Order<PARTS>::N; ++q)
+                        acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            __builtin_bit_cast(pt::bf16x8_t, w[b][r][(pt::Order<PARTS>::A >> 2 * q) & 3u]),
+                            __builtin_bit_cast(pt::bf16x8_t, h[b][t][(pt::Order<PARTS>::B >> 2 * q) & 3u]), acc[r][t], 0, 0, 0);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) red[wave][16 * r + 4 * (lane >> 4) + e][16 * t + ln] = acc[r][t][e];
+    __syncthreads();
+    // half a wave per token, a lane per entry
+    for (int t = threadIdx.x >> 5; t < a.tokens; t += 8) {
+        const int r = threadIdx.x & 31, v = v0 + r;
+        const int64_t y = a.targets[t];
+        float z = (red[0][r][t] + red[1][r][t] + red[2][r][t] + red[3][r][t]) * a.scale2;
+        if (v >= a.vocab) z = -INFINITY;
+        float m = z;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 32));
+        float e = __builtin_amdgcn_exp2f(z - (m == -INFINITY ? 0.0f : m));
+        if (v == y) {
+            a.zt[t] = z;
+            e = 0.0f;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) e += __shfl_xor(e, o, 32);
+        if (r == 0) {
+            a.m[static_cast<size_t>(t) * a.tiles + blockIdx.x] = m;
+            a.s[static_cast<size_t>(t) * a.tiles + blockIdx.x] = e;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// lse and logp from the tiles' statistics
+// ---------------------------------------------------------------------------
+
+struct CombineArgs {
+    const float *m, *s, *zt;
+    size_t tile_stride, row_stride;
+    int tiles;
+    const int64_t* targets;
+    int64_t vocab;
+    float *logp, *lse;
+    const int32_t *idx, *count;   // NULL: every token, in order (then unscored ones are zeroed here)
+    int64_t tokens;
+    float* kept;                  // logp by list entry, for the backward pass, or NULL
+};
+
+// 2^(a - b) for a <= b, with equal infinities taken as equal
+__device__ __forceinline__ float pow2_diff(float a, float b) { return a == b ? 1.0f : __builtin_amdgcn_exp2f(a - b); }
+
+// TOK tokens a workgroup, 256 / TOK threads each.
+template <int TOK>
+__global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
+    constexpr int NP = 256 / TOK;
+    __shared__ float sm[NP][TOK], ss[NP][TOK];
+    const int tk = threadIdx.x % TOK, part = threadIdx.x / TOK;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * TOK + tk;
+    const int64_t n = a.idx ? *a.count : a.tokens;
+    float m = -INFINITY, s = 0.0f;
+    if (row < n)
+#pragma unroll 4
+        for (int t = part; t < a.tiles; t += NP) {
+            const size_t o = t * a.tile_stride + row * a.row_stride;
+            const float mt = a.m[o], st = a.s[o], up = fmaxf(m, mt);
+            s = s * pow2_diff(m, up) + st * pow2_diff(mt, up);
+            m = up;
+        }
+    sm[part][tk] = m;
+    ss[part][tk] = s;
+    for (int o = NP / 2; o > 0; o >>= 1) {
+        __syncthreads();
+        if (part < o) {
+            const float m2 = sm[part + o][tk], s2 = ss[part + o][tk], up = fmaxf(m, m2);
+            s = s * pow2_diff(m, up) + s2 * pow2_diff(m2, up);
+            m = up;
+            sm[part][tk] = m;
+            ss[part][tk] = s;
+        }
+    }
+    if (part != 0 || row >= n) return;
+    const int64_t tok = a.idx ? a.idx[row] : row, y = a.targets[tok];
+    float logp, lse = (m + log2f(s)) * LN2;
+    if (y < 0) {
+        logp = lse = 0.0f;
+    } else if (y >= a.vocab) {
+        logp = NAN;
+    } else {
+        const float zt = a.zt[row], d = m - zt;
+        if (s == 0.0f) logp = 0.0f;
+        else if (d < 80.0f) logp = -log1pf(s * __builtin_amdgcn_exp2f(d));
+        else logp = -(d + log2f(s)) * LN2;     // here 1 is nothing beside the sum
+        if (d < 80.0f) lse = zt * LN2 - logp;
+    }
+    a.logp[tok] = logp;
+    a.lse[tok] = lse;
+    if (a.kept) a.kept[row] = logp;
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+
+struct Bump {
+    size_t at = 0;
+    size_t take(size_t bytes) {
+        const size_t o = at;
+        at += (bytes + 255) / 256 * 256;
+        return o;
+    }
+};
+
+// What both directions derive from the shape.
+struct Shape {
+    int64_t tokens, cols, vocab;
+    int parts;
+    int64_t tp, vp, dp;      // padded to the tile, the tile, the k-step
+    int ta;                  // vocabulary tiles
+    bool direct_hidden, direct_head;   // operands that the products can read where they are
+    Shape(int64_t t, int64_t d, int64_t v, int dtype, const void* hidden, int64_t ld_hidden, const void* head, int64_t ld_head)
+        : tokens(t), cols(d), vocab(v), parts(dtype == MUON_BF16 ? 1 : 3), tp(up(std::max<int64_t>(t, 1), pt::TILE)),
+          vp(up(v, pt::TILE)), dp(up(d, pt::KS)), ta(static_cast<int>(vp / pt::TILE)) {
+        const bool ok = dtype == MUON_BF16 && d % pt::KS == 0;
+        direct_hidden = ok && reinterpret_cast<uintptr_t>(hidden) % 16 == 0 && ld_hidden % 8 == 0;
+        direct_head = ok && reinterpret_cast<uintptr_t>(head) % 16 == 0 && ld_head % 8 == 0;
+    }
+};
+
+struct ForwardPlan {
+    Shape sh;
+    bool few;
+    int few_tiles;
+    size_t idx, count, hidden, head, m, s, zt, bytes;
+    explicit ForwardPlan(const muon_token_logp_args& a)
+        : sh(a.tokens, a.cols, a.vocab, a.dtype, a.hidden, a.ld_hidden, a.head, a.ld_head) {
+        few = a.tokens <= FEW_TOKENS && !a.saved;
+        few_tiles = static_cast<int>(ceil_div(a.vocab, FEW_ROWS));
+        Bump b;
+        const size_t part = sizeof(uint16_t) * sh.parts * sh.dp;
+        idx = b.take(few ? 0 : sizeof(int32_t) * sh.tp);
+        count = b.take(sizeof(int32_t));
+        hidden = b.take(few || sh.direct_hidden ? 0 : part * sh.tp);
+        head = b.take(few || sh.direct_head ? 0 : part * sh.vocab);
+        const size_t stats = few ? static_cast<size_t>(a.tokens) * few_tiles : static_cast<size_t>(sh.ta) * sh.tp;
+        m = b.take(a.saved ? 0 : stats * sizeof(float));
+        s = b.take(stats * sizeof(float));
+        zt = b.take(sizeof(float) * sh.tp);
+        bytes = b.at;
+    }
+};
+
+struct SavedPlan {
+    size_t e, m, logp, bytes;
+    SavedPlan(int64_t tokens, int64_t vocab, int dtype) {
+        const int64_t tp = up(std::max<int64_t>(tokens, 1), pt::TILE), vp = up(vocab, pt::TILE);
+        Bump b;
+        e = b.take((dtype == MUON_BF16 ? 2 : 4) * static_cast<size_t>(tp) * vp);
+        m = b.take(sizeof(float) * (vp / pt::TILE) * static_cast<size_t>(tp));
+        logp = b.take(sizeof(float) * static_cast<size_t>(tp));
+        bytes = b.at;
+    }
+};
+
+// How a gradient's product is spread: enough workgroups for the chip, each with a worthwhile run of k.
+int split_count(int64_t tiles, int64_t steps) {
+    const int64_t want = WORKGROUPS / std::max<int64_t>(tiles, 1);
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, MAX_SPLITS, steps / MIN_SPLIT_STEPS})));
+}
+
+struct GradPlan {
+    int ta, tb, splits;
+    bool slab;
+    size_t slab_bytes() const { return slab ? sizeof(float) * pt::TILE * pt::TILE * splits * ta * tb : 0; }
+};
+
+struct BackwardPlan {
+    Shape sh;
+    int64_t chunk;          // list entries at a time
+    int chunks;
+    size_t idx, count, hidden, head, head_t, hidden_t, dz, dzt, slab, bytes;
+    GradPlan gh, gw;
+    explicit BackwardPlan(const muon_token_logp_backward_args& a)
+        : sh(a.tokens, a.cols, a.vocab, a.dtype, a.hidden, a.ld_hidden, a.head, a.ld_head) {
+        const int64_t both = sizeof(uint16_t) * sh.parts * 2 * sh.vp;
+        chunk = std::min(sh.tp, std::max<int64_t>(pt::TILE, DZ_BYTES / both / pt::TILE * pt::TILE));
+        chunks = static_cast<int>(ceil_div(sh.tp, chunk));
+        const int tc = static_cast<int>(ceil_div(sh.cols, pt::TILE));
+        auto direct = [&](const void* p, int64_t ld) {
+            return a.dtype == MUON_BF16 && reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0;
+        };
+        gh.ta = gw.ta = tc;
+        gh.tb = static_cast<int>(chunk / pt::TILE);
+        gw.tb = sh.ta;
+        gh.splits = split_count(static_cast<int64_t>(gh.ta) * gh.tb, sh.vp / pt::KS);
+        gw.splits = split_count(static_cast<int64_t>(gw.ta) * gw.tb, chunk / pt::KS);
+        gh.slab = gh.splits > 1 || !direct(a.grad_hidden, a.ld_grad_hidden);
+        gw.slab = gw.splits > 1 || chunks > 1 || !direct(a.grad_head, a.ld_grad_head);
+        Bump b;
+        const size_t el = sizeof(uint16_t) * sh.parts;
+        idx = b.take(sizeof(int32_t) * sh.tp);
+        count = b.take(sizeof(int32_t));
+        hidden = b.take(a.saved || sh.direct_hidden ? 0 : el * sh.dp * chunk);
+        head = b.take(a.saved || sh.direct_head ? 0 : el * sh.dp * sh.vocab);
+        head_t = b.take(a.grad_hidden ? el * sh.cols * sh.vp : 0);
+        hidden_t = b.take(a.grad_head ? el * sh.cols * chunk : 0);
+        dz = b.take(a.grad_hidden ? el * chunk * sh.vp : 0);
+        dzt = b.take(a.grad_head ? el * chunk * sh.vp : 0);
+        // the slab of grad_head lives through the chunks, so the two do not share one
+        slab = b.take(a.grad_hidden ? gh.slab_bytes() : 0);
+        slab_w = b.take(a.grad_head ? gw.slab_bytes() : 0);
+        bytes = b.at;
+    }
+    size_t slab_w;
+};
+
+hipError_t launch_live(const int64_t* targets, int64_t tokens, int32_t* idx, int32_t* count, float* logp, float* lse,
+                       hipStream_t s) {
+    hipLaunchKernelGGL(live_kernel, dim3(1), dim3(LIVE_THREADS), 0, s, targets, tokens, idx, count, logp, lse);
     return hipGetLastError();
 }
 
-// One workgroup per token.  The target's own term is kept out of the sum:
-// logp = -log(1 + sum_{j != target} exp(z_j - z_target)), which keeps its relative
-// precision as logp goes to 0.
-__global__ __launch_bounds__(TL_THREADS) void logp_rows_kernel(muon_token_logp_args a, const float* z) {
-    __shared__ float red[TL_THREADS / 64], redm[TL_THREADS / 64];
-    const int64_t row = blockIdx.x, y = a.targets[row];
-    if (y < 0) {
-        if (threadIdx.x == 0) { a.logp[row] = 0.0f; a.lse[row] = 0.0f; }
-        return;
-    }
-    const float* zr = z + static_cast<size_t>(row) * a.vocab;
-    float m = -INFINITY;
-    for (int64_t j = threadIdx.x; j < a.vocab; j += TL_THREADS)
-        if (j != y) m = fmaxf(m, zr[j]);
-    for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
-    if ((threadIdx.x & 63) == 0) redm[threadIdx.x >> 6] = m;
-    __syncthreads();
-    for (int w = 0; w < TL_THREADS / 64; ++w) m = fmaxf(m, redm[w]);
-    float s = 0.0f;
-    for (int64_t j = threadIdx.x; j < a.vocab; j += TL_THREADS)
-        if (j != y && m > -INFINITY) s += expf(zr[j] - m);
-    s = block_sum<TL_THREADS>(s, red);
-    if (threadIdx.x != 0) return;
-    if (y >= a.vocab) {
-        a.logp[row] = NAN;
-        a.lse[row] = m + logf(s);
-        return;
-    }
-    const float zy = zr[y], d = m - zy;
-    // s exp(d) overflows for a far-off target: there 1 is nothing beside it
-    const float logp = s == 0.0f ? 0.0f : d < 60.0f ? -log1pf(s * expf(d)) : -(d + logf(s));
-    a.logp[row] = logp;
-    a.lse[row] = zy - logp;
+hipError_t launch_pack(const PackArgs& p, int dtype, hipStream_t s) {
+    const int64_t work = p.rows * static_cast<int64_t>(p.dst_ld / 8);
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(ceil_div(work, 256), 8 * WORKGROUPS)));
+    if (dtype == MUON_BF16) hipLaunchKernelGGL((pack_kernel<uint16_t, 1>), grid, dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((pack_kernel<float, 3>), grid, dim3(256), 0, s, p);
+    return hipGetLastError();
 }
 
-__global__ __launch_bounds__(TL_THREADS) void dlogits_kernel(muon_token_logp_backward_args a, const float* z, float* dz) {
-    const int64_t row = blockIdx.x, y = a.targets[row];
-    const size_t off = static_cast<size_t>(row) * a.vocab;
-    const float c = a.scale * a.grad_logp[row], lse = a.lse[row];
-    for (int64_t j = threadIdx.x; j < a.vocab; j += TL_THREADS)
-        dz[off + j] = y < 0 || c == 0.0f ? 0.0f : c * ((j == y ? 1.0f : 0.0f) - expf(z[off + j] - lse));
+hipError_t launch_pack_transposed(const PackArgs& p, int dtype, hipStream_t s) {
+    const dim3 grid(static_cast<unsigned>(ceil_div(p.rows, 64)), static_cast<unsigned>(ceil_div(p.cols, 64)));
+    if (dtype == MUON_BF16) hipLaunchKernelGGL((pack_transposed_kernel<uint16_t, 1>), grid, dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((pack_transposed_kernel<float, 3>), grid, dim3(256), 0, s, p);
+    return hipGetLastError();
 }
 
-size_t logits_bytes(int64_t tokens, int64_t vocab) { return static_cast<size_t>(tokens) * vocab * sizeof(float); }
+template <int MODE> hipError_t launch_logits(const LogitsArgs& l, int parts, hipStream_t s) {
+    const dim3 grid(static_cast<unsigned>(l.ta) * l.tb);
+    if (parts == 1) hipLaunchKernelGGL((logits_kernel<1, MODE>), grid, dim3(pt::THREADS), 0, s, l);
+    else hipLaunchKernelGGL((logits_kernel<3, MODE>), grid, dim3(pt::THREADS), 0, s, l);
+    return hipGetLastError();
+}
+
+hipError_t launch_grad(const GradArgs& g, int parts, int dtype, bool last, hipStream_t s) {
+    const dim3 grid(static_cast<unsigned>(g.ta) * g.tb, g.splits);
+    if (parts == 1) hipLaunchKernelGGL(grad_kernel<1>, grid, dim3(pt::THREADS), 0, s, g);
+    else hipLaunchKernelGGL(grad_kernel<3>, grid, dim3(pt::THREADS), 0, s, g);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !g.slab || !last) return e;
+    hipLaunchKernelGGL(slab_sum_kernel, dim3(static_cast<unsigned>(g.ta) * g.tb * 16), dim3(256), 0, s, g, dtype);
+    return hipGetLastError();
+}
+
+#define TL_TRY(expr)                       \
+    do {                                   \
+        const hipError_t e_ = (expr);      \
+        if (e_ != hipSuccess) return e_;   \
+    } while (0)
+
+// The logits' operands: packed copies where the products cannot read the caller's rows.
+hipError_t logits_operands(const Shape& sh, const void* hidden, int64_t ld_hidden, const void* head, int64_t ld_head,
+                           int dtype, char* hidden_copy, char* head_copy, bool pack_head, LogitsArgs& l, hipStream_t s) {
+    const size_t row = sizeof(uint16_t) * sh.dp;
+    l.steps = static_cast<int>(sh.dp / pt::KS);
+    l.vocab = static_cast<int>(sh.vocab);
+    l.ta = sh.ta;
+    l.a = sh.direct_head ? static_cast<const char*>(head) : head_copy;
+    l.a_ld = sh.direct_head ? 2 * static_cast<size_t>(ld_head) : row;
+    l.a_part = row * sh.vocab;
+    if (!sh.direct_head && pack_head)
+        TL_TRY(launch_pack({head, static_cast<size_t>(ld_head), sh.vocab, sh.cols, 0, {}, reinterpret_cast<uint16_t*>(head_copy),
+                            static_cast<size_t>(sh.dp), static_cast<size_t>(sh.dp) * sh.vocab}, dtype, s));
+    l.gather = sh.direct_hidden;
+    l.b = sh.direct_hidden ? static_cast<const char*>(hidden) : hidden_copy;
+    l.b_ld = sh.direct_hidden ? 2 * static_cast<size_t>(ld_hidden) : row;
+    l.b_part = row * l.live.most;
+    if (!sh.direct_hidden)
+        TL_TRY(launch_pack({hidden, static_cast<size_t>(ld_hidden), l.live.most, sh.cols, 1, l.live,
+                            reinterpret_cast<uint16_t*>(hidden_copy), static_cast<size_t>(sh.dp),
+                            static_cast<size_t>(sh.dp) * l.live.most}, dtype, s));
+    return hipSuccess;
+}
+
+template <typename T, int PARTS, int NT> hipError_t launch_few_nt(const FewArgs& f, bool vec, hipStream_t s) {
+    const dim3 grid(static_cast<unsigned>(f.tiles));
+    if (vec) hipLaunchKernelGGL((few_kernel<T, PARTS, NT, true>), grid, dim3(256), 0, s, f);
+    else hipLaunchKernelGGL((few_kernel<T, PARTS, NT, false>), grid, dim3(256), 0, s, f);
+    return hipGetLastError();
+}
+template <typename T, int PARTS> hipError_t launch_few(const FewArgs& f, bool vec, hipStream_t s) {
+    if (f.tokens <= 16) return launch_few_nt<T, PARTS, 1>(f, vec, s);
+    if (f.tokens <= 32) return launch_few_nt<T, PARTS, 2>(f, vec, s);
+    return launch_few_nt<T, PARTS, 4>(f, vec, s);
+}
 
 }  // namespace
 
-size_t token_logp_saved_bytes(const muon_token_logp_args& a) { return logits_bytes(a.tokens, a.vocab); }
-size_t token_logp_bytes(const muon_token_logp_args& a) { return logits_bytes(a.tokens, a.vocab); }
-size_t token_logp_backward_bytes(const muon_token_logp_backward_args& a) { return logits_bytes(a.tokens, a.vocab); }
+size_t token_logp_saved_bytes(const muon_token_logp_args& a) { return SavedPlan(a.tokens, a.vocab, a.dtype).bytes; }
+size_t token_logp_bytes(const muon_token_logp_args& a) { return ForwardPlan(a).bytes; }
+size_t token_logp_backward_bytes(const muon_token_logp_backward_args& a) { return BackwardPlan(a).bytes; }
 
-hipError_t launch_token_logp(const muon_token_logp_args& a, void* workspace, int cu_count, hipStream_t s) {
+hipError_t launch_token_logp(const muon_token_logp_args& a, void* workspace, hipStream_t s) {
     if (a.tokens == 0) return hipSuccess;
-    float* z = static_cast<float*>(a.saved ? a.saved : workspace);
-    const ProductArgs p{a.hidden, a.head, z, static_cast<size_t>(a.ld_hidden), 1, static_cast<size_t>(a.ld_head), 1,
-                        static_cast<size_t>(a.vocab), a.dtype, a.dtype, DT_F32, a.tokens, a.vocab, a.cols, a.scale,
-                        nullptr, nullptr};
-    const hipError_t e = launch_product(p, s);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(logp_rows_kernel, dim3(static_cast<unsigned>(a.tokens)), dim3(TL_THREADS), 0, s, a, z);
+    const ForwardPlan pl(a);
+    const Shape& sh = pl.sh;
+    char* ws = static_cast<char*>(workspace);
+    float* m = reinterpret_cast<float*>(ws + pl.m);
+    float* sums = reinterpret_cast<float*>(ws + pl.s);
+    float* zt = reinterpret_cast<float*>(ws + pl.zt);
+    const float scale2 = a.scale * LOG2E;
+    if (pl.few) {
+        const FewArgs f{a.head, a.hidden, static_cast<size_t>(a.ld_head), static_cast<size_t>(a.ld_hidden), a.targets,
+                        static_cast<int>(a.tokens), static_cast<int>(a.cols), static_cast<int>(a.vocab), pl.few_tiles, scale2,
+                        m, sums, zt};
+        const int el = a.dtype == MUON_BF16 ? 2 : 4;   // 16-byte loads of 8 (bf16) or 4 (fp32) elements
+        const bool vec = a.cols % 8 == 0 && reinterpret_cast<uintptr_t>(a.head) % 16 == 0 &&
+                         reinterpret_cast<uintptr_t>(a.hidden) % 16 == 0 && a.ld_head * el % 16 == 0 && a.ld_hidden * el % 16 == 0;
+        TL_TRY(a.dtype == MUON_BF16 ? (launch_few<uint16_t, 1>(f, vec, s)) : (launch_few<float, 3>(f, vec, s)));
+        const CombineArgs c{m, sums, zt, 1, static_cast<size_t>(pl.few_tiles), pl.few_tiles, a.targets, a.vocab, a.logp, a.lse,
+                            nullptr, nullptr, a.tokens, nullptr};
+        hipLaunchKernelGGL(combine_kernel<1>, dim3(static_cast<unsigned>(a.tokens)), dim3(256), 0, s, c);
+        return hipGetLastError();
+    }
+    int32_t* idx = reinterpret_cast<int32_t*>(ws + pl.idx);
+    int32_t* count = reinterpret_cast<int32_t*>(ws + pl.count);
+    TL_TRY(launch_live(a.targets, a.tokens, idx, count, a.logp, a.lse, s));
+    LogitsArgs l{};
+    l.live = {idx, count, 0, static_cast<int32_t>(sh.tp)};
+    TL_TRY(logits_operands(sh, a.hidden, a.ld_hidden, a.head, a.ld_head, a.dtype, ws + pl.hidden, ws + pl.head, true, l, s));
+    l.targets = a.targets;
+    l.tb = static_cast<int>(sh.tp / pt::TILE);
+    l.scale2 = scale2;
+    float* kept = nullptr;
+    if (a.saved) {
+        const SavedPlan sv(a.tokens, a.vocab, a.dtype);
+        kept = reinterpret_cast<float*>(static_cast<char*>(a.saved) + sv.logp);
+        l.e = static_cast<char*>(a.saved) + sv.e;
+        m = reinterpret_cast<float*>(static_cast<char*>(a.saved) + sv.m);
+    }
+    l.m = m;
+    l.s = sums;
+    l.zt = zt;
+    l.rows_pitch = sh.tp;
+    l.vp = sh.vp;
+    TL_TRY(a.saved ? launch_logits<LG_SAVE>(l, sh.parts, s) : launch_logits<LG_STATS>(l, sh.parts, s));
+    const CombineArgs c{m, sums, zt, static_cast<size_t>(sh.tp), 1, sh.ta, a.targets, a.vocab, a.logp, a.lse, idx, count, a.tokens,
+                        kept};
+    hipLaunchKernelGGL(combine_kernel<32>, dim3(static_cast<unsigned>(sh.tp / 32)), dim3(256), 0, s, c);
     return hipGetLastError();
 }
 
-hipError_t launch_token_logp_backward(const muon_token_logp_backward_args& a, void* workspace, int cu_count,
-                                      hipStream_t s) {
-    float* dz = static_cast<float*>(workspace);
-    const float* z = static_cast<const float*>(a.saved ? a.saved : workspace);
-    const size_t ldh = a.ld_hidden, ldw = a.ld_head, v = a.vocab;
-    hipError_t e = hipSuccess;
-    if (!a.saved) {
-        const ProductArgs p{a.hidden, a.head, dz, ldh, 1, ldw, 1, v, a.dtype, a.dtype, DT_F32, a.tokens, a.vocab,
-                            a.cols, a.scale, nullptr, nullptr};
-        e = launch_product(p, s);
-        if (e != hipSuccess) return e;
+hipError_t launch_token_logp_backward(const muon_token_logp_backward_args& a, void* workspace, hipStream_t s) {
+    const BackwardPlan pl(a);
+    const Shape& sh = pl.sh;
+    char* ws = static_cast<char*>(workspace);
+    int32_t* idx = reinterpret_cast<int32_t*>(ws + pl.idx);
+    int32_t* count = reinterpret_cast<int32_t*>(ws + pl.count);
+    TL_TRY(launch_live(a.targets, a.tokens, idx, count, nullptr, nullptr, s));
+    if (a.grad_hidden && a.tokens > 0) {
+        hipLaunchKernelGGL(zero_rows_kernel, dim3(static_cast<unsigned>(ceil_div(a.tokens, 4))), dim3(256), 0, s, a.targets,
+                           a.tokens, a.cols, a.grad_hidden, a.ld_grad_hidden, a.dtype);
+        TL_TRY(hipGetLastError());
+        TL_TRY(launch_pack_transposed({a.head, static_cast<size_t>(a.ld_head), sh.vocab, sh.cols, 0, {},
+                                       reinterpret_cast<uint16_t*>(ws + pl.head_t), static_cast<size_t>(sh.vp),
+                                       static_cast<size_t>(sh.vp) * sh.cols}, a.dtype, s));
     }
-    if (a.tokens > 0) {
-        hipLaunchKernelGGL(dlogits_kernel, dim3(static_cast<unsigned>(a.tokens)), dim3(TL_THREADS), 0, s, a, z, dz);
-        e = hipGetLastError();
-        if (e != hipSuccess) return e;
+    const SavedPlan sv(a.tokens, a.vocab, a.dtype);
+    const size_t vp = sh.vp, dz_part = static_cast<size_t>(pl.chunk) * vp;
+    uint16_t* dz = a.grad_hidden ? reinterpret_cast<uint16_t*>(ws + pl.dz) : nullptr;
+    uint16_t* dzt = a.grad_head ? reinterpret_cast<uint16_t*>(ws + pl.dzt) : nullptr;
+    for (int c = 0; c < pl.chunks; ++c) {
+        const Live live{idx, count, static_cast<int32_t>(c * pl.chunk), static_cast<int32_t>(pl.chunk)};
+        const char* saved = static_cast<const char*>(a.saved);
+        if (saved) {
+            const DzArgs d{saved + sv.e, reinterpret_cast<const float*>(saved + sv.m),
+                           reinterpret_cast<const float*>(saved + sv.logp), static_cast<size_t>(sh.tp), live,
+                           a.targets, a.lse, a.grad_logp, a.scale, static_cast<int>(a.vocab), vp,
+                           static_cast<size_t>(pl.chunk), dz, dzt, dz_part, dz_part};
+            const dim3 grid(static_cast<unsigned>(vp / 64), static_cast<unsigned>(pl.chunk / 64));
+            if (sh.parts == 1) hipLaunchKernelGGL((dz_kernel<uint16_t, 1>), grid, dim3(256), 0, s, d);
+            else hipLaunchKernelGGL((dz_kernel<float, 3>), grid, dim3(256), 0, s, d);
+            TL_TRY(hipGetLastError());
+        } else {
+            LogitsArgs l{};
+            l.live = live;
+            TL_TRY(logits_operands(sh, a.hidden, a.ld_hidden, a.head, a.ld_head, a.dtype, ws + pl.hidden, ws + pl.head, c == 0, l, s));
+            l.targets = a.targets;
+            l.tb = static_cast<int>(pl.chunk / pt::TILE);
+            l.scale2 = a.scale * LOG2E;
+            l.scale = a.scale;
+            l.lse = a.lse;
+            l.grad_logp = a.grad_logp;
+            l.dz = dz;
+            l.dzt = dzt;
+            l.dz_part = l.dzt_part = dz_part;
+            l.vp = vp;
+            l.rows_pitch = pl.chunk;
+            TL_TRY(launch_logits<LG_DZ>(l, sh.parts, s));
+        }
+        if (a.grad_hidden) {
+            GradArgs g{};
+            g.a = ws + pl.head_t;
+            g.a_ld = 2 * vp;
+            g.a_part = 2 * vp * sh.cols;
+            g.b = reinterpret_cast<const char*>(dz);
+            g.b_ld = 2 * vp;
+            g.b_part = 2 * dz_part;
+            g.live = live;
+            g.cols = static_cast<int>(sh.cols);
+            g.by_token = 1;
+            g.steps = static_cast<int>(ceil_div(sh.vocab, pt::KS));
+            g.ta = pl.gh.ta;
+            g.tb = pl.gh.tb;
+            g.splits = pl.gh.splits;
+            g.out = a.grad_hidden;
+            g.ld = a.ld_grad_hidden;
+            g.slab = pl.gh.slab ? reinterpret_cast<float*>(ws + pl.slab) : nullptr;
+            TL_TRY(launch_grad(g, sh.parts, a.dtype, true, s));
+        }
+        if (a.grad_head) {
+            TL_TRY(launch_pack_transposed({a.hidden, static_cast<size_t>(a.ld_hidden), pl.chunk, sh.cols, 1, live,
+                                           reinterpret_cast<uint16_t*>(ws + pl.hidden_t), static_cast<size_t>(pl.chunk),
+                                           static_cast<size_t>(pl.chunk) * sh.cols}, a.dtype, s));
+            GradArgs g{};
+            g.a = ws + pl.hidden_t;
+            g.a_ld = 2 * static_cast<size_t>(pl.chunk);
+            g.a_part = g.a_ld * sh.cols;
+            g.b = reinterpret_cast<const char*>(dzt);
+            g.b_ld = g.a_ld;
+            g.b_part = 2 * dz_part;
+            g.live = live;
+            g.cols = static_cast<int>(sh.cols);
+            g.rows = static_cast<int>(sh.vocab);
+            g.ta = pl.gw.ta;
+            g.tb = pl.gw.tb;
+            g.splits = pl.gw.splits;
+            g.out = a.grad_head;
+            g.ld = a.ld_grad_head;
+            g.slab = pl.gw.slab ? reinterpret_cast<float*>(ws + pl.slab_w) : nullptr;
+            g.add = c > 0;
+            TL_TRY(launch_grad(g, sh.parts, a.dtype, c + 1 == pl.chunks, s));
+        }
     }
-    if (a.grad_hidden) {
-        const ProductArgs p{dz, a.head, a.grad_hidden, v, 1, 1, ldw, static_cast<size_t>(a.ld_grad_hidden), DT_F32, a.dtype,
-                            a.dtype, a.tokens, a.cols, a.vocab, 1.0f, a.targets, nullptr};
-        e = launch_product(p, s);
-        if (e != hipSuccess) return e;
-    }
-    if (a.grad_head) {
-        const ProductArgs p{dz, a.hidden, a.grad_head, 1, v, 1, ldh, static_cast<size_t>(a.ld_grad_head), DT_F32, a.dtype,
-                            a.dtype, a.vocab, a.cols, a.tokens, 1.0f, nullptr, a.targets};
-        e = launch_product(p, s);
-    }
-    return e;
+    return hipSuccess;
 }
 
 }  // namespace muon

@@ -284,7 +284,7 @@ muon_status run_op(Buffers& buf, size_t need, void* ws, size_t ws_bytes, F launc
     MUON_TRY(buf.check_against("the workspace", ws, need));
     int dev = 0, cus = 0;
     MUON_TRY(check_device(&dev, &cus));
-    MUON_TRY(launch(cus));
+    MUON_TRY(launch());
     clear_error();
     return MUON_OK;
 }
@@ -301,7 +301,7 @@ muon_status muon_block_norm(const muon_block_norm_args* a, void* stream) {
     int dev = 0, cus = 0;
     MUON_TRY(check_device(&dev, &cus));
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    MUON_TRY(timed_launch(9, s, "block norm kernel", [&] { return launch_block_norm(*a, cus, s); }));
+    MUON_TRY(timed_launch(9, s, "block norm kernel", [&] { return launch_block_norm(*a, s); }));
     clear_error();
     return MUON_OK;
 }
@@ -315,7 +315,7 @@ muon_status muon_block_norm_backward(const muon_block_norm_backward_args* a, voi
     Buffers buf;
     MUON_TRY(check_norm_backward(a, buf));
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    return run_op(buf, block_norm_backward_bytes(*a), ws, ws_bytes, [&](int) {
+    return run_op(buf, block_norm_backward_bytes(*a), ws, ws_bytes, [&] {
         return timed_launch(9, s, "block norm backward kernels", [&] { return launch_block_norm_backward(*a, ws, s); });
     });
 }
@@ -335,8 +335,8 @@ muon_status muon_token_logp(const muon_token_logp_args* a, void* ws, size_t ws_b
     Buffers buf;
     MUON_TRY(check_logp(a, buf));
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    return run_op(buf, token_logp_bytes(*a), ws, ws_bytes, [&](int cus) {
-        return timed_launch(10, s, "token log-probability kernels", [&] { return launch_token_logp(*a, ws, cus, s); });
+    return run_op(buf, token_logp_bytes(*a), ws, ws_bytes, [&] {
+        return timed_launch(10, s, "token log-probability kernels", [&] { return launch_token_logp(*a, ws, s); });
     });
 }
 
@@ -349,9 +349,9 @@ muon_status muon_token_logp_backward(const muon_token_logp_backward_args* a, voi
     Buffers buf;
     MUON_TRY(check_logp_backward(a, buf));
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    return run_op(buf, token_logp_backward_bytes(*a), ws, ws_bytes, [&](int cus) {
+    return run_op(buf, token_logp_backward_bytes(*a), ws, ws_bytes, [&] {
         return timed_launch(10, s, "token log-probability backward kernels",
-                            [&] { return launch_token_logp_backward(*a, ws, cus, s); });
+                            [&] { return launch_token_logp_backward(*a, ws, s); });
     });
 }
 
@@ -364,7 +364,7 @@ muon_status muon_preference_loss(const muon_preference_args* a, void* ws, size_t
     Buffers buf;
     MUON_TRY(check_preference(a, buf));
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    return run_op(buf, preference_bytes(*a), ws, ws_bytes, [&](int) {
+    return run_op(buf, preference_bytes(*a), ws, ws_bytes, [&] {
         return timed_launch(11, s, "preference loss kernels", [&] { return launch_preference(*a, ws, s); });
     });
 }
@@ -378,7 +378,7 @@ muon_status muon_policy_loss(const muon_policy_args* a, void* ws, size_t ws_byte
     Buffers buf;
     MUON_TRY(check_policy(a, buf));
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    return run_op(buf, policy_bytes(*a), ws, ws_bytes, [&](int) {
+    return run_op(buf, policy_bytes(*a), ws, ws_bytes, [&] {
         return timed_launch(12, s, "policy loss kernels", [&] { return launch_policy(*a, ws, s); });
     });
 }

@@ -48,16 +48,15 @@ template <int NT> __device__ __forceinline__ float block_sum(float v, float* red
     return v;
 }
 
-hipError_t launch_block_norm(const muon_block_norm_args& a, int cu_count, hipStream_t s);
+hipError_t launch_block_norm(const muon_block_norm_args& a, hipStream_t s);
 size_t block_norm_backward_bytes(const muon_block_norm_backward_args& a);
 hipError_t launch_block_norm_backward(const muon_block_norm_backward_args& a, void* workspace, hipStream_t s);
 
 size_t token_logp_saved_bytes(const muon_token_logp_args& a);
 size_t token_logp_bytes(const muon_token_logp_args& a);
-hipError_t launch_token_logp(const muon_token_logp_args& a, void* workspace, int cu_count, hipStream_t s);
+hipError_t launch_token_logp(const muon_token_logp_args& a, void* workspace, hipStream_t s);
 size_t token_logp_backward_bytes(const muon_token_logp_backward_args& a);
-hipError_t launch_token_logp_backward(const muon_token_logp_backward_args& a, void* workspace, int cu_count,
-                                      hipStream_t s);
+hipError_t launch_token_logp_backward(const muon_token_logp_backward_args& a, void* workspace, hipStream_t s);
 
 size_t preference_bytes(const muon_preference_args& a);
 hipError_t launch_preference(const muon_preference_args& a, void* workspace, hipStream_t s);
