@@ -5,148 +5,386 @@
 //   dh = dn wq,  R = dr' + rstd1 (dh - h mean(dh h)),  dr = alpha R,  dg = R a,
 //   da = R g,  dxh = da wp,  dx = rstd0 (dxh - xh mean(dxh xh)),
 //   dwq = sum dn h,  dwp = sum da xh  over the rows.
-// One workgroup per row (forward) or per run of rows (backward), every pass over the
-// row reading it again.
+//
+// HBM-bound: the forward pass reads x and r and writes r' and n, the backward pass reads
+// x, r', dn and dr' and writes dx and dr (a full gate adds one each way); a few operations
+// per byte.  So a row is read once and kept in registers, as fp32, by the NT threads that share it:
+// one wave for rows up to 2048 columns (forward; its sums need no barrier), 256 or 1024 threads
+// for longer ones.  The weights are read again for every row: they come from L2.
+//
+// The backward pass needs mean(dxh xh), and dxh needs mean(dh h) first.  With q = g wp xh,
+//   sum dxh xh = sum (dr' + rstd1 dh) q - rstd1 mean(dh h) sum h q,
+// so the three sums sum dh h, sum (dr' + rstd1 dh) q and sum h q are taken together, one
+// exchange per row instead of two.  Weight gradients stay in registers over a workgroup's rows (a
+// thread keeps its columns) and end in one fp32 partial per workgroup, summed in a fixed order by
+// block_norm_weights_kernel.
+#include <algorithm>
+
 #include "train_internal.h"
 
 namespace muon {
 
 namespace {
 
-constexpr int BN_THREADS = 256;
-constexpr int BN_MAX_PARTS = 256;   // row runs of the backward pass, one partial weight gradient each
+constexpr int64_t BN_WAVES = 4096;  // waves of the backward pass's workgroups, at most: 16 a CU
+constexpr int64_t BN_ROWS = 2;      // rows of a workgroup, at least: each leaves a partial weight gradient to sum
+constexpr int64_t BN_LONG = 8192;   // longest row that one workgroup's registers hold in the backward pass
+constexpr int BN_CHUNK = 2048;      // columns of a longer row a workgroup takes at a time
 
-struct RowIo {
-    int dt, wdt;
-    __device__ float mat(const void* p, size_t i) const { return ld_dt(p, i, dt); }
-    __device__ float wt(const void* p, size_t i) const { return p ? ld_dt(p, i, wdt) : 1.0f; }
-    __device__ float gate(const void* p, int kind, size_t row_off, int c) const {
-        return kind == MUON_GATE_NONE ? 1.0f : kind == MUON_GATE_CHANNEL ? ld_dt(p, c, wdt) : ld_dt(p, row_off + c, dt);
+// Which of the workgroup's rows this thread works on: the same for a whole wave, so that row addresses are
+// scalar.
+template <int NT> __device__ __forceinline__ int row_of_thread() {
+    return __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x / NT));
+}
+
+// The 8 VPT columns of a row that one of its NT threads keeps: VPT runs of 8, NT runs apart.  TAIL: the last
+// run of the row may be short.
+template <int NT, int VPT, bool TAIL> struct Cols {
+    static constexpr int N = 8 * VPT;
+    unsigned cols, t;   // t: the thread's first run
+    __device__ unsigned run(int v) const { return (v * NT + t) * 8; }
+    __device__ bool has(int k) const { return TAIL ? run(k / 8) + k % 8 < cols : run(k / 8) < cols; }
+    template <typename T> __device__ __forceinline__ void load(const void* p, size_t off, float (&o)[N]) const {
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            const auto* q = G(static_cast<const T*>(p) + off);
+            Run<T> w;
+            if (TAIL ? run(v) + 8 <= cols : run(v) < cols) w.load(q, run(v));
+            else if (TAIL && run(v) < cols) w.load(q, run(v), cols - run(v));
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[8 * v + e] = w.get(e);
+        }
+    }
+    template <typename T> __device__ __forceinline__ void store(void* p, size_t off, const float (&o)[N]) const {
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            auto* q = G(static_cast<T*>(p) + off);
+            float w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = o[8 * v + e];
+            if (TAIL ? run(v) + 8 <= cols : run(v) < cols) st_run(q, run(v), w);
+            else if (TAIL && run(v) < cols)
+#pragma unroll
+                for (int e = 0; e < 7; ++e)
+                    if (run(v) + e < cols) st_el<T>(p, off + run(v) + e, w[e]);
+        }
+    }
+    // a weight vector; 1 where there is none
+    __device__ __forceinline__ void weight(const void* p, int dt, float (&o)[N]) const {
+        if (!p) {
+#pragma unroll
+            for (int k = 0; k < N; ++k) o[k] = 1.0f;
+        } else if (dt == DT_BF16) {
+            load<uint16_t>(p, 0, o);
+        } else {
+            load<float>(p, 0, o);
+        }
+    }
+    template <typename T>
+    __device__ __forceinline__ void gate(const void* p, int kind, int wdt, size_t off, float (&o)[N]) const {
+        if (kind == MUON_GATE_FULL) load<T>(p, off, o);
+        else weight(kind == MUON_GATE_CHANNEL ? p : nullptr, wdt, o);
     }
 };
 
-__global__ __launch_bounds__(BN_THREADS) void block_norm_kernel(muon_block_norm_args a) {
-    __shared__ float red[BN_THREADS / 64];
-    const RowIo io{a.dtype, a.weight_dtype};
-    const size_t row = blockIdx.x;
-    const int d = static_cast<int>(a.cols);
-    const size_t xo = row * a.ld_x, ro = row * a.ld_residual, go = row * a.ld_gate;
-    float s0 = 1.0f;
+// Sums over the NT threads of one row, NS at a time, given to all of them.  `red` holds NS floats per
+// wave of the workgroup, twice: rows take the two halves in turn, so one barrier per call is enough.
+template <int NT, int NS, int WAVES>
+__device__ __forceinline__ void row_sums(float (&v)[NS], float* red, int turn) {
+#pragma unroll
+    for (int k = 0; k < NS; ++k)
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) v[k] += __shfl_xor(v[k], o, 64);
+    if constexpr (NT > 64) {
+        float* r = red + (turn & 1) * NS * WAVES;
+        const int wave = threadIdx.x >> 6, first = wave / (NT / 64) * (NT / 64);
+        if ((threadIdx.x & 63) == 0)
+#pragma unroll
+            for (int k = 0; k < NS; ++k) r[k * WAVES + wave] = v[k];
+        lds_barrier();
+#pragma unroll
+        for (int k = 0; k < NS; ++k) {
+            v[k] = r[k * WAVES + first];
+#pragma unroll
+            for (int w = 1; w < NT / 64; ++w) v[k] += r[k * WAVES + first + w];
+        }
+    }
+}
+
+template <typename T, int NT, int VPT, bool TAIL>
+__global__ __launch_bounds__(NT < 256 ? 256 : NT) void block_norm_kernel(muon_block_norm_args a) {
+    constexpr int BLOCK = NT < 256 ? 256 : NT, PER = BLOCK / NT, N = 8 * VPT;
+    __shared__ float red[2 * BLOCK / 64];
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * PER + row_of_thread<NT>();
+    if (NT == 64 && row >= a.rows) return;   // longer rows: one per workgroup, none past the last
+    const Cols<NT, VPT, TAIL> c{static_cast<unsigned>(a.cols), threadIdx.x % NT};
+    const float inv = 1.0f / static_cast<float>(a.cols);
+    float x[N], y[N], w[N], gt[N];
+    c.template load<T>(a.x, row * a.ld_x, x);
+    c.template load<T>(a.residual, row * a.ld_residual, y);
+    c.template gate<T>(a.gate, a.gate_kind, a.weight_dtype, row * a.ld_gate, gt);
+    c.weight(a.post_weight, a.weight_dtype, w);
+    float s0 = 1.0f, s1 = 1.0f;
     if (a.post_weight) {
-        float s = 0.0f;
-        for (int c = threadIdx.x; c < d; c += BN_THREADS) {
-            const float v = io.mat(a.x, xo + c);
-            s += v * v;
-        }
-        s0 = 1.0f / sqrtf(block_sum<BN_THREADS>(s, red) / d + a.eps);
+        float s[1] = {0.0f};
+#pragma unroll
+        for (int k = 0; k < N; ++k) s[0] = fmaf(x[k], x[k], s[0]);
+        row_sums<NT, 1, BLOCK / 64>(s, red, 0);
+        s0 = 1.0f / sqrtf(fmaf(s[0], inv, a.eps));
     }
-    auto joined = [&](int c) {
-        return a.residual_scale * io.mat(a.residual, ro + c) +
-               io.gate(a.gate, a.gate_kind, go, c) * (io.mat(a.x, xo + c) * s0 * io.wt(a.post_weight, c));
-    };
-    float s1 = 1.0f;
+#pragma unroll
+    for (int k = 0; k < N; ++k) y[k] = fmaf(gt[k], x[k] * s0 * w[k], a.residual_scale * y[k]);
+    c.template store<T>(a.out_residual, row * a.ld_out_residual, y);
     if (a.out_norm) {
-        float s = 0.0f;
-        for (int c = threadIdx.x; c < d; c += BN_THREADS) {
-            const float v = joined(c);
-            s += v * v;
-        }
-        s1 = 1.0f / sqrtf(block_sum<BN_THREADS>(s, red) / d + a.eps);
+        c.weight(a.pre_weight, a.weight_dtype, w);
+        float s[1] = {0.0f};
+#pragma unroll
+        for (int k = 0; k < N; ++k) s[0] += c.has(k) ? y[k] * y[k] : 0.0f;
+        row_sums<NT, 1, BLOCK / 64>(s, red, 1);
+        s1 = 1.0f / sqrtf(fmaf(s[0], inv, a.eps));
+#pragma unroll
+        for (int k = 0; k < N; ++k) y[k] = y[k] * s1 * w[k];
+        c.template store<T>(a.out_norm, row * a.ld_out_norm, y);
     }
-    for (int c = threadIdx.x; c < d; c += BN_THREADS) {
-        const float v = joined(c);
-        st_dt(a.out_residual, row * a.ld_out_residual + c, v, a.dtype);
-        if (a.out_norm) st_dt(a.out_norm, row * a.ld_out_norm + c, v * s1 * io.wt(a.pre_weight, c), a.dtype);
-    }
-    if (a.rstd && threadIdx.x == 0) {
+    if (a.rstd && threadIdx.x % NT == 0) {
         a.rstd[row] = s0;
         a.rstd[a.rows + row] = s1;
     }
 }
 
-__global__ __launch_bounds__(BN_THREADS) void block_norm_backward_kernel(muon_block_norm_backward_args a, float* part) {
-    __shared__ float red[BN_THREADS / 64];
-    const RowIo io{a.dtype, a.weight_dtype};
-    const int d = static_cast<int>(a.cols);
-    float* pp = part + static_cast<size_t>(blockIdx.x) * 3 * d;   // post weight, gate, pre weight
-    for (int c = threadIdx.x; c < 3 * d; c += BN_THREADS) pp[c] = 0.0f;
-    __syncthreads();
-    for (size_t row = blockIdx.x; row < static_cast<size_t>(a.rows); row += gridDim.x) {
-        const float s0 = a.rstd[row], s1 = a.rstd[a.rows + row];
-        const size_t xo = row * a.ld_x, ho = row * a.ld_out_residual, no = row * a.ld_grad_norm,
-                     uo = row * a.ld_grad_out_residual, go = row * a.ld_gate;
-        auto hat = [&](int c) { return io.mat(a.out_residual, ho + c) * s1; };
-        auto dhat = [&](int c) { return io.mat(a.grad_norm, no + c) * io.wt(a.pre_weight, c); };
-        float m1 = 0.0f;
+constexpr int bwd_block(int nt) { return nt < 256 ? 256 : nt; }
+
+// What the backward pass reads of one row, and the sums it needs of it.
+template <typename T, typename C> struct BackwardRow {
+    static constexpr int N = C::N;
+    float x[N], h[N], dn[N], tot[N], gt[N], wp[N];   // xh, h, dn, dr' (then dr' + rstd1 dh), gate, wp
+    float s0, s1;
+    __device__ __forceinline__ void load(const muon_block_norm_backward_args& a, const C& c, int64_t row) {
+        c.template load<T>(a.x, row * a.ld_x, x);
+        c.template load<T>(a.out_residual, row * a.ld_out_residual, h);
         if (a.grad_norm) {
-            for (int c = threadIdx.x; c < d; c += BN_THREADS) m1 += dhat(c) * hat(c);
-            m1 = block_sum<BN_THREADS>(m1, red) / d;
+            c.template load<T>(a.grad_norm, row * a.ld_grad_norm, dn);
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; ++k) dn[k] = 0.0f;
         }
-        auto total = [&](int c) {
-            float v = a.grad_out_residual ? io.mat(a.grad_out_residual, uo + c) : 0.0f;
-            if (a.grad_norm) v += s1 * (dhat(c) - hat(c) * m1);
-            return v;
-        };
-        float m0 = 0.0f;
-        if (a.post_weight) {
-            for (int c = threadIdx.x; c < d; c += BN_THREADS)
-                m0 += total(c) * io.gate(a.gate, a.gate_kind, go, c) * io.wt(a.post_weight, c) * (io.mat(a.x, xo + c) * s0);
-            m0 = block_sum<BN_THREADS>(m0, red) / d;
+        if (a.grad_out_residual) {
+            c.template load<T>(a.grad_out_residual, row * a.ld_grad_out_residual, tot);
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; ++k) tot[k] = 0.0f;
         }
-        for (int c = threadIdx.x; c < d; c += BN_THREADS) {
-            const float r = total(c), xh = io.mat(a.x, xo + c) * s0, w = io.wt(a.post_weight, c);
-            const float da = r * io.gate(a.gate, a.gate_kind, go, c);
-            if (a.grad_norm && a.grad_pre_weight) pp[2 * d + c] += io.mat(a.grad_norm, no + c) * hat(c);
-            pp[c] += da * xh;
-            if (a.gate_kind == MUON_GATE_CHANNEL) pp[d + c] += r * xh * w;
-            if (a.gate_kind == MUON_GATE_FULL) st_dt(a.grad_gate, row * a.ld_grad_gate + c, r * xh * w, a.dtype);
-            st_dt(a.grad_x, row * a.ld_grad_x + c, a.post_weight ? s0 * (da * w - xh * m0) : da, a.dtype);
-            st_dt(a.grad_residual, row * a.ld_grad_residual + c, a.residual_scale * r, a.dtype);
+        c.template gate<T>(a.gate, a.gate_kind, a.weight_dtype, row * a.ld_gate, gt);
+        c.weight(a.post_weight, a.weight_dtype, wp);
+        s0 = a.rstd[row];
+        s1 = a.rstd[a.rows + row];
+    }
+    // adds this thread's share of sum dh h, sum (dr' + rstd1 dh) q, sum h q
+    __device__ __forceinline__ void sums(const muon_block_norm_backward_args& a, const C& c, float (&s)[3]) {
+        float wq[N];
+        c.weight(a.pre_weight, a.weight_dtype, wq);
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            x[k] *= s0;
+            h[k] *= s1;
+            const float dh = dn[k] * wq[k], q = gt[k] * wp[k] * x[k];
+            s[0] = fmaf(dh, h[k], s[0]);
+            tot[k] = fmaf(s1, dh, tot[k]);
+            s[1] = fmaf(tot[k], q, s[1]);
+            s[2] = fmaf(h[k], q, s[2]);
         }
+    }
+    // m1 = rstd1 mean(dh h), m0 = mean(dxh xh)
+    static __device__ __forceinline__ void means(const float (&s)[3], float s1, float inv, float& m1, float& m0) {
+        m1 = s1 * (s[0] * inv);
+        m0 = (s[1] - m1 * s[2]) * inv;
+    }
+};
+
+// Rows beyond BN_LONG: m1 and m0 of each, one workgroup a row.
+template <typename T, bool TAIL>
+__global__ __launch_bounds__(1024) void block_norm_means_kernel(muon_block_norm_backward_args a, float* means) {
+    __shared__ float red[2 * 3 * 16];
+    const int64_t row = blockIdx.x;
+    float s[3] = {0.0f, 0.0f, 0.0f}, s1 = 1.0f;
+    for (unsigned c0 = 0; c0 < a.cols; c0 += 8192) {
+        const Cols<1024, 1, TAIL> c{static_cast<unsigned>(a.cols), threadIdx.x + c0 / 8};
+        BackwardRow<T, Cols<1024, 1, TAIL>> r;
+        r.load(a, c, row);
+        r.sums(a, c, s);
+        s1 = r.s1;
+    }
+    row_sums<1024, 3, 16>(s, red, 0);
+    if (threadIdx.x == 0) {
+        float m1, m0;
+        BackwardRow<T, Cols<1024, 1, TAIL>>::means(s, s1, 1.0f / static_cast<float>(a.cols), m1, m0);
+        means[row] = m1;
+        means[a.rows + row] = m0;
     }
 }
 
-// Sums the runs' partial weight gradients in run order.
-__global__ __launch_bounds__(BN_THREADS) void block_norm_weights_kernel(muon_block_norm_backward_args a,
-                                                                        const float* part, int parts) {
-    const int d = static_cast<int>(a.cols);
-    const int c = blockIdx.x * BN_THREADS + threadIdx.x;
-    if (c >= d) return;
-    void* outs[3] = {a.grad_post_weight, a.gate_kind == MUON_GATE_CHANNEL ? a.grad_gate : nullptr, a.grad_pre_weight};
-    for (int k = 0; k < 3; ++k) {
-        if (!outs[k]) continue;
-        float s = 0.0f;
-        for (int p = 0; p < parts; ++p) s += part[(static_cast<size_t>(p) * 3 + k) * d + c];
-        st_dt(outs[k], c, s, a.weight_dtype);
+// GIVEN: the rows' means come from block_norm_means_kernel and blockIdx.y is the run of BN_CHUNK columns.
+template <typename T, int NT, bool TAIL, bool GIVEN>
+__global__ __launch_bounds__(bwd_block(NT), 4) void block_norm_backward_kernel(
+    muon_block_norm_backward_args a, float* part, const float* means) {
+    constexpr int BLOCK = bwd_block(NT), PER = BLOCK / NT, WAVES = BLOCK / 64, N = 8;
+    typedef Cols<NT, 1, TAIL> C;
+    __shared__ float red[2 * 3 * WAVES];
+    __shared__ float join[PER > 1 ? PER * NT * N : 1];
+    const int g = row_of_thread<NT>();
+    const C c{static_cast<unsigned>(a.cols), threadIdx.x % NT + (GIVEN ? blockIdx.y * (BN_CHUNK / 8) : 0)};
+    const float inv = 1.0f / static_cast<float>(a.cols);
+    float swp[N] = {}, sg[N] = {}, swq[N] = {};   // this thread's columns of the weight gradients
+    int turn = 0;
+    for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * PER; r0 < a.rows; r0 += static_cast<int64_t>(gridDim.x) * PER, ++turn) {
+        const bool on = r0 + g < a.rows;
+        const int64_t row = on ? r0 + g : a.rows - 1;
+        BackwardRow<T, C> r;
+        r.load(a, c, row);
+        float s[3] = {0.0f, 0.0f, 0.0f}, m1, m0;
+        r.sums(a, c, s);
+        if constexpr (GIVEN) {
+            m1 = means[row];
+            m0 = means[a.rows + row];
+        } else {
+            row_sums<NT, 3, WAVES>(s, red, turn);
+            r.means(s, r.s1, inv, m1, m0);
+        }
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const float tot = fmaf(-m1, r.h[k], r.tot[k]), da = tot * r.gt[k], xw = r.x[k] * r.wp[k];
+            if (on) {
+                swq[k] = fmaf(r.dn[k], r.h[k], swq[k]);
+                swp[k] = fmaf(da, r.x[k], swp[k]);
+                sg[k] = fmaf(tot, xw, sg[k]);
+            }
+            r.h[k] = a.post_weight ? r.s0 * (da * r.wp[k] - r.x[k] * m0) : da;   // dx
+            r.x[k] = tot * xw;                                                  // dg of this row
+            r.tot[k] = a.residual_scale * tot;
+        }
+        if (on) {
+            c.template store<T>(a.grad_x, row * a.ld_grad_x, r.h);
+            c.template store<T>(a.grad_residual, row * a.ld_grad_residual, r.tot);
+            if (a.gate_kind == MUON_GATE_FULL) c.template store<T>(a.grad_gate, row * a.ld_grad_gate, r.x);
+        }
+    }
+    // the workgroup's rows share its columns: their sums are joined in LDS, in order
+    float* out = part + static_cast<size_t>(blockIdx.x) * 3 * a.cols;
+#pragma unroll
+    for (int which = 0; which < 3; ++which) {
+        float (&s)[N] = which == 0 ? swp : which == 1 ? sg : swq;
+        if (which == 1 && a.gate_kind != MUON_GATE_CHANNEL) continue;
+        if constexpr (PER > 1) {
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < N; ++k) join[(g * N + k) * NT + threadIdx.x % NT] = s[k];
+            __syncthreads();
+            if (g == 0)
+#pragma unroll
+                for (int k = 0; k < N; ++k)
+#pragma unroll
+                    for (int p = 1; p < PER; ++p) s[k] += join[(p * N + k) * NT + threadIdx.x % NT];
+        }
+        if (g == 0) c.template store<float>(out, which * a.cols, s);
     }
 }
 
-int backward_parts(const muon_block_norm_backward_args& a) {
-    return static_cast<int>(a.rows < BN_MAX_PARTS ? a.rows : BN_MAX_PARTS);
+// Sums the workgroups' partial weight gradients in order: 64 columns x 16 runs of partials a workgroup.
+__global__ __launch_bounds__(1024) void block_norm_weights_kernel(muon_block_norm_backward_args a, const float* part,
+                                                                  int parts) {
+    __shared__ float run[16][64];
+    const int which = blockIdx.y;
+    void* out = which == 0 ? a.grad_post_weight
+                           : which == 1 ? (a.gate_kind == MUON_GATE_CHANNEL ? a.grad_gate : nullptr) : a.grad_pre_weight;
+    if (!out) return;
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 64 + (threadIdx.x & 63);
+    const int r = threadIdx.x >> 6, per = (parts + 15) / 16;
+    float s = 0.0f;
+    if (c < a.cols) {
+        const float* p = part + which * a.cols + c;
+#pragma unroll 8
+        for (int k = r * per; k < min(parts, (r + 1) * per); ++k) s += p[static_cast<size_t>(k) * 3 * a.cols];
+    }
+    run[r][threadIdx.x & 63] = s;
+    __syncthreads();
+    if (r != 0 || c >= a.cols) return;
+#pragma unroll
+    for (int k = 1; k < 16; ++k) s += run[k][threadIdx.x];
+    st_dt(out, c, s, a.weight_dtype);
+}
+
+template <typename T, int NT, int VPT> hipError_t forward(const muon_block_norm_args& a, hipStream_t s) {
+    constexpr int BLOCK = NT < 256 ? 256 : NT;
+    const dim3 grid(static_cast<unsigned>((a.rows + BLOCK / NT - 1) / (BLOCK / NT)));
+    if (a.cols % 8) hipLaunchKernelGGL((block_norm_kernel<T, NT, VPT, true>), grid, dim3(BLOCK), 0, s, a);
+    else hipLaunchKernelGGL((block_norm_kernel<T, NT, VPT, false>), grid, dim3(BLOCK), 0, s, a);
+    return hipGetLastError();
+}
+
+template <typename T> hipError_t forward_by_cols(const muon_block_norm_args& a, hipStream_t s) {
+    if (a.cols <= 512) return forward<T, 64, 1>(a, s);
+    if (a.cols <= 1024) return forward<T, 64, 2>(a, s);
+    if (a.cols <= 2048) return forward<T, 64, 4>(a, s);
+    if (a.cols <= 4096) return forward<T, 256, 2>(a, s);
+    if (a.cols <= 8192) return forward<T, 1024, 1>(a, s);
+    if (a.cols <= 16384) return forward<T, 1024, 2>(a, s);
+    return forward<T, 1024, 4>(a, s);
+}
+
+// Threads per row of the backward pass.
+int backward_threads(int64_t cols) { return cols <= 512 ? 64 : cols <= 2048 || cols > BN_LONG ? 256 : cols <= 4096 ? 512 : 1024; }
+int64_t backward_chunks(int64_t cols) { return cols > BN_LONG ? (cols + BN_CHUNK - 1) / BN_CHUNK : 1; }
+int64_t backward_parts(const muon_block_norm_backward_args& a) {
+    const int block = bwd_block(backward_threads(a.cols));
+    const int64_t per = BN_ROWS * (block / backward_threads(a.cols));
+    return std::min((a.rows + per - 1) / per, std::max<int64_t>(1, BN_WAVES / (block / 64) / backward_chunks(a.cols)));
+}
+size_t backward_part_floats(const muon_block_norm_backward_args& a) { return static_cast<size_t>(backward_parts(a)) * 3 * a.cols; }
+
+template <typename T, int NT, bool GIVEN = false>
+hipError_t backward(const muon_block_norm_backward_args& a, float* part, const float* means, hipStream_t s) {
+    const dim3 grid(static_cast<unsigned>(backward_parts(a)), static_cast<unsigned>(backward_chunks(a.cols))), block(bwd_block(NT));
+    if (a.cols % 8) hipLaunchKernelGGL((block_norm_backward_kernel<T, NT, true, GIVEN>), grid, block, 0, s, a, part, means);
+    else hipLaunchKernelGGL((block_norm_backward_kernel<T, NT, false, GIVEN>), grid, block, 0, s, a, part, means);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t backward_by_cols(const muon_block_norm_backward_args& a, float* part, hipStream_t s) {
+    if (a.cols <= 512) return backward<T, 64>(a, part, nullptr, s);
+    if (a.cols <= 2048) return backward<T, 256>(a, part, nullptr, s);
+    if (a.cols <= 4096) return backward<T, 512>(a, part, nullptr, s);
+    if (a.cols <= BN_LONG) return backward<T, 1024>(a, part, nullptr, s);
+    // a row's accumulators and data no longer fit: its means first, then runs of columns (x, r', dn and dr' read twice)
+    float* means = part + backward_part_floats(a);
+    const dim3 grid(static_cast<unsigned>(a.rows));
+    if (a.cols % 8) hipLaunchKernelGGL((block_norm_means_kernel<T, true>), grid, dim3(1024), 0, s, a, means);
+    else hipLaunchKernelGGL((block_norm_means_kernel<T, false>), grid, dim3(1024), 0, s, a, means);
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess ? e : backward<T, 256, true>(a, part, means, s);
 }
 
 }  // namespace
 
 hipError_t launch_block_norm(const muon_block_norm_args& a, hipStream_t s) {
     if (a.rows == 0) return hipSuccess;
-    hipLaunchKernelGGL(block_norm_kernel, dim3(static_cast<unsigned>(a.rows)), dim3(BN_THREADS), 0, s, a);
-    return hipGetLastError();
+    return a.dtype == MUON_BF16 ? forward_by_cols<uint16_t>(a, s) : forward_by_cols<float>(a, s);
 }
 
 size_t block_norm_backward_bytes(const muon_block_norm_backward_args& a) {
-    return static_cast<size_t>(backward_parts(a)) * 3 * a.cols * sizeof(float);
+    return sizeof(float) * (backward_part_floats(a) + (a.cols > BN_LONG ? 2 * static_cast<size_t>(a.rows) : 0));
 }
 
 hipError_t launch_block_norm_backward(const muon_block_norm_backward_args& a, void* workspace, hipStream_t s) {
     float* part = static_cast<float*>(workspace);
-    const int parts = backward_parts(a);
+    const int64_t parts = backward_parts(a);
     if (parts > 0) {
-        hipLaunchKernelGGL(block_norm_backward_kernel, dim3(parts), dim3(BN_THREADS), 0, s, a, part);
-        const hipError_t e = hipGetLastError();
+        const hipError_t e = a.dtype == MUON_BF16 ? backward_by_cols<uint16_t>(a, part, s)
+                                                  : backward_by_cols<float>(a, part, s);
         if (e != hipSuccess) return e;
     }
-    const unsigned grid = static_cast<unsigned>((a.cols + BN_THREADS - 1) / BN_THREADS);
-    hipLaunchKernelGGL(block_norm_weights_kernel, dim3(grid), dim3(BN_THREADS), 0, s, a, part, parts);
+    hipLaunchKernelGGL(block_norm_weights_kernel, dim3(static_cast<unsigned>((a.cols + 63) / 64), 3), dim3(1024), 0, s, a, part,
+                       static_cast<int>(parts));
     return hipGetLastError();
 }
 

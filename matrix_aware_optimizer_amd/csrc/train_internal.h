@@ -32,6 +32,49 @@ __device__ __forceinline__ void st_dt(void* p, size_t i, float v, int dt) {
     else st_el<float>(p, i, v);
 }
 
+// 8 consecutive elements at any element alignment: the hardware takes such accesses whole, so odd widths and
+// pitches cost only the cache lines that a run crosses.
+typedef u32x4_t u32x4_el2 __attribute__((aligned(2)));
+typedef f32x4_t f32x4_el4 __attribute__((aligned(4)));
+template <typename T> using global_t = MUON_GLOBAL T;
+// A run as loaded: converted only where it is used, so that a row's loads are all in flight at once.
+template <typename T> struct Run;
+template <> struct Run<uint16_t> {
+    u32x4_t w = {};
+    __device__ __forceinline__ void load(const global_t<uint16_t>* p, unsigned i) { w = *(const global_t<u32x4_el2>*)(p + i); }
+    __device__ __forceinline__ void load(const global_t<uint16_t>* p, unsigned i, unsigned n) {
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+            if (e < static_cast<int>(n)) w[e >> 1] |= static_cast<uint32_t>(p[i + e]) << (16 * (e & 1));
+    }
+    __device__ __forceinline__ float get(int e) const {
+        return __uint_as_float((e & 1) ? (w[e >> 1] & 0xffff0000u) : (w[e >> 1] << 16));
+    }
+};
+template <> struct Run<float> {
+    f32x4_t w[2] = {};
+    __device__ __forceinline__ void load(const global_t<float>* p, unsigned i) {
+        w[0] = *(const global_t<f32x4_el4>*)(p + i);
+        w[1] = *(const global_t<f32x4_el4>*)(p + i + 4);
+    }
+    __device__ __forceinline__ void load(const global_t<float>* p, unsigned i, unsigned n) {
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+            if (e < static_cast<int>(n)) w[e >> 2][e & 3] = p[i + e];
+    }
+    __device__ __forceinline__ float get(int e) const { return w[e >> 2][e & 3]; }
+};
+__device__ __forceinline__ void st_run(global_t<uint16_t>* p, unsigned i, const float (&o)[8]) {
+    u32x4_t w;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = pack_bf16x2(o[2 * e], o[2 * e + 1]);
+    *(global_t<u32x4_el2>*)(p + i) = w;
+}
+__device__ __forceinline__ void st_run(global_t<float>* p, unsigned i, const float (&o)[8]) {
+    *(global_t<f32x4_el4>*)(p + i) = f32x4_t{o[0], o[1], o[2], o[3]};
+    *(global_t<f32x4_el4>*)(p + i + 4) = f32x4_t{o[4], o[5], o[6], o[7]};
+}
+
 // Sum over a workgroup of NT threads, given to every thread; `red` holds NT / 64 floats.
 // The order of the additions is fixed.  Safe to call again at once with the same `red`.
 template <int NT> __device__ __forceinline__ float block_sum(float v, float* red) {
