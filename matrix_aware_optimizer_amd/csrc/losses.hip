@@ -1,71 +1,223 @@
 // Losses over per-token log-probabilities, with their gradients: the preference loss over
 // pairs of sequences and the clipped policy loss with a KL term (formulas in muon.h).
 //
-// Both are sums over ragged sequences followed by an elementwise gradient.  A first launch
-// reduces each sequence (one workgroup per sequence), one workgroup joins the sequences
-// into the loss and each one's gradient factor, and a last launch writes the gradient.
+// A few bytes and operations a token: HBM-bound for millions of tokens, launch- and
+// latency-bound for thousands.  The work is cut by tokens, not by sequences, so that one long
+// sequence among short ones spreads like any other: a wave takes a unit of 512 tokens, 8 a lane
+// (one 32-byte access each), and walks over the pieces of sequences in its unit.
+//
+// A sequence's sum is put together from its units' in token order, so results do not depend
+// on scheduling.  Per unit u: head[u] is the sum of the piece that starts at the unit's first
+// token, tail[u] that of the piece that starts inside and goes on past its end; a sequence
+// that lies inside a unit, past its first token, has its sum in own[s].  So sequence [lo, hi) is
+//   (lo at a unit's start ? head : hi in the same unit ? own[s] : tail)[its first unit] + head[every later unit].
+//
+// Preference: units -> pairs (loss terms and each sequence's gradient factor) -> gradient.
+// Policy: the number of counted tokens first (1 byte a token, only with a mask), then loss and
+// gradient in one pass over the rest, then the partial sums.  Up to LS_SMALL tokens all steps run in
+// one workgroup and one launch.
+#include <algorithm>
+
 #include "train_internal.h"
 
 namespace muon {
 
 namespace {
 
-constexpr int LS_THREADS = 256;
+constexpr int UNIT = 512, PER = 8;       // tokens of a wave's unit, of a lane
+constexpr int LS_THREADS = 256;          // workgroups of the launches over many units: 4 waves
+constexpr int LS_ONE = 1024;             // the workgroup that does everything: 16 waves
+constexpr int64_t LS_SMALL = 16384;      // tokens up to which it does (two units a wave)
+constexpr int LS_GRID = 1024;            // workgroups of the other launches, at most
+constexpr int LS_COUNTS = 256;           // workgroups that count, at most: one partial each
 
-// Tokens of sequence s, clamped to [0, tokens).
-struct Span {
-    int64_t lo, hi;
-    __device__ Span(const int64_t* offsets, int64_t s, int64_t tokens) {
-        lo = min(max(offsets[s], static_cast<int64_t>(0)), tokens);
-        hi = max(min(max(offsets[s + 1], static_cast<int64_t>(0)), tokens), lo);
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+    return v;
+}
+__device__ __forceinline__ int lane_id() { return threadIdx.x & 63; }
+
+// Tokens t .. t + 7 of a vector of n, zero past its end.
+template <typename T> __device__ __forceinline__ void load_tokens(const void* p, int t, int n, float (&o)[PER]) {
+    Run<T> r;
+    const auto* q = G(static_cast<const T*>(p));
+    if (t + PER <= n) r.load(q, t);
+    else if (t < n) r.load(q, t, n - t);
+#pragma unroll
+    for (int e = 0; e < PER; ++e) o[e] = r.get(e);
+}
+template <typename T> __device__ __forceinline__ void store_tokens(void* p, int t, int n, const float (&o)[PER]) {
+    auto* q = G(static_cast<T*>(p));
+    if (t + PER <= n) {
+        st_run(q, t, o);
+    } else {
+#pragma unroll
+        for (int e = 0; e < PER - 1; ++e)
+            if (t + e < n) st_el<T>(p, t + e, o[e]);
+    }
+}
+// Bit e: token t + e exists and its mask counts it.
+__device__ __forceinline__ unsigned load_mask(const uint8_t* mask, int t, int n) {
+    const unsigned there = t + PER <= n ? 0xffu : t < n ? (1u << (n - t)) - 1u : 0u;
+    if (!mask) return there;
+    unsigned m = 0;
+    typedef u32x2_t u32x2_el1 __attribute__((aligned(1)));
+    if (t + PER <= n) {
+        const u32x2_t w = *(const global_t<u32x2_el1>*)(G(mask) + t);
+#pragma unroll
+        for (int e = 0; e < PER; ++e) m |= ((w[e >> 2] >> (8 * (e & 3))) & 0xffu) ? 1u << e : 0u;
+    } else {
+#pragma unroll
+        for (int e = 0; e < PER - 1; ++e)
+            if (t + e < n && G(mask)[t + e]) m |= 1u << e;
+    }
+    return m;
+}
+
+// The sequences, as offsets clamped to the tokens there are (so no offset makes an access stray).
+struct Sequences {
+    const int64_t* offsets;
+    int count, tokens;
+    __device__ __forceinline__ int at(int k) const {
+        const int64_t v = offsets[k];
+        return static_cast<int>(v < 0 ? 0 : v > tokens ? tokens : v);
+    }
+    // The last k with at(k) <= t, or -1: 64 probes at a time.
+    __device__ __forceinline__ int last_at_most(int t) const {
+        int lo = 0, hi = count + 1;   // the number of such k lies in [lo, hi]
+        while (lo < hi) {
+            const int step = (hi - lo + 63) / 64, k = lo + lane_id() * step;
+            const int c = __popcll(__ballot(k < hi && at(k) <= t));
+            if (c == 0) break;
+            const int next = lo + (c - 1) * step + 1;
+            hi = min(hi, lo + c * step);
+            lo = next;
+        }
+        return lo - 1;
+    }
+    // f(s, a, b, lo, hi, side) for every sequence s = [lo, hi) with a piece [a, b) in [t0, t1).  `side`: value
+    // of extra(s) of that sequence, loaded 63 sequences at a time with the offsets.
+    template <typename E, typename F> __device__ __forceinline__ void pieces(int t0, int t1, E extra, F f) const {
+        for (int s0 = max(last_at_most(t0), 0); s0 < count; s0 += 63) {
+            const int k = min(s0 + lane_id(), count);
+            const int off = at(k);
+            const float ex = extra(min(k, count - 1));
+            const int n = min(63, count - s0);
+            for (int i = 0; i < n; ++i) {
+                const int lo = __builtin_amdgcn_readlane(off, i), hi = max(__builtin_amdgcn_readlane(off, i + 1), lo);
+                if (lo >= t1) return;
+                const int a = max(lo, t0), b = min(hi, t1);
+                if (a < b) f(s0 + i, a, b, lo, hi, __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ex), i)));
+            }
+        }
     }
 };
 
-__device__ __forceinline__ bool counted(const uint8_t* mask, int64_t t) { return !mask || mask[t] != 0; }
+// Bit e: token t + e lies in [a, b).
+__device__ __forceinline__ unsigned in_piece(int t, int a, int b) {
+    const int l = min(max(a - t, 0), PER), h = min(max(b - t, 0), PER);
+    return (1u << h) - (1u << l) & (h > l ? ~0u : 0u);
+}
 
-// Zeros before the first and after the last sequence (workgroup 0 and the last one).
-__device__ void zero_uncovered(void* grad, int dt, const int64_t* offsets, int64_t sequences, int64_t tokens) {
-    if (!grad) return;
-    const int64_t lo = sequences ? min(max(offsets[0], static_cast<int64_t>(0)), tokens) : tokens;
-    const int64_t hi = sequences ? Span(offsets, sequences - 1, tokens).hi : tokens;
-    const int64_t n = static_cast<int64_t>(gridDim.x) * LS_THREADS, i0 = static_cast<int64_t>(blockIdx.x) * LS_THREADS + threadIdx.x;
-    for (int64_t t = i0; t < lo; t += n) st_dt(grad, t, 0.0f, dt);
-    for (int64_t t = hi + i0; t < tokens; t += n) st_dt(grad, t, 0.0f, dt);
+// Sums of sequences by unit: V = float or float2.
+template <typename V> struct UnitSums {
+    V *head, *tail, *own;
+    __device__ __forceinline__ void put(int s, int a, int lo, int hi, V v) const {
+        const int u = a / UNIT;
+        if (a == u * UNIT) head[u] = v;
+        else if (hi <= (u + 1) * UNIT) own[s] = v;
+        else tail[u] = v;
+    }
+    __device__ __forceinline__ V first(int s, int lo, int hi) const {
+        const int u = lo / UNIT;
+        return lo == u * UNIT ? head[u] : hi <= (u + 1) * UNIT ? own[s] : tail[u];
+    }
+};
+__device__ __forceinline__ float add(float a, float b) { return a + b; }
+__device__ __forceinline__ float2 add(float2 a, float2 b) { return make_float2(a.x + b.x, a.y + b.y); }
+__device__ __forceinline__ float wave_total(float v) { return wave_sum(v); }
+__device__ __forceinline__ float2 wave_total(float2 v) { return make_float2(wave_sum(v.x), wave_sum(v.y)); }
+
+// head[first .. last] summed by the wave.
+template <typename V> __device__ __forceinline__ V heads(const UnitSums<V>& q, int first, int last) {
+    V v = {};
+    for (int u = first + lane_id(); u <= last; u += 64) v = add(v, q.head[u]);
+    return wave_total(v);
 }
 
 // ---- preference -------------------------------------------------------------
 
-// sums[s] = { sum of counted log ratios, counted tokens }
-__global__ __launch_bounds__(LS_THREADS) void preference_sums_kernel(muon_preference_args a, float* sums) {
-    __shared__ float red[LS_THREADS / 64];
-    const int64_t s = blockIdx.x;
-    const Span sp(a.offsets, s, a.tokens);
-    float v = 0.0f, c = 0.0f;
-    for (int64_t t = sp.lo + threadIdx.x; t < sp.hi; t += LS_THREADS) {
-        if (!counted(a.mask, t)) continue;
-        v += ld_dt(a.logp, t, a.dtype) - (a.ref_logp ? ld_dt(a.ref_logp, t, a.dtype) : 0.0f);
-        c += 1.0f;
+struct PreferenceState {
+    muon_preference_args a;
+    UnitSums<float2> q;     // { sum of counted log ratios, counted tokens }
+    float* factor;          // gradient factor by sequence
+    float* losses;          // by pair
+    __device__ Sequences seqs() const { return {a.offsets, static_cast<int>(a.sequences), static_cast<int>(a.tokens)}; }
+    __device__ int units() const { return static_cast<int>((a.tokens + UNIT - 1) / UNIT); }
+};
+
+template <typename T> __device__ __forceinline__ void preference_units(const PreferenceState& st, int wave, int waves) {
+    const int n = static_cast<int>(st.a.tokens);
+    for (int u = wave; u < st.units(); u += waves) {
+        const int t0 = u * UNIT, t = t0 + PER * lane_id();
+        float lp[PER], ref[PER] = {};
+        load_tokens<T>(st.a.logp, t, n, lp);
+        if (st.a.ref_logp) load_tokens<T>(st.a.ref_logp, t, n, ref);
+        const unsigned live = load_mask(st.a.mask, t, n);
+        st.seqs().pieces(t0, t0 + UNIT, [](int) { return 0.0f; }, [&](int s, int a, int b, int lo, int hi, float) {
+            const unsigned on = live & in_piece(t, a, b);
+            float v = 0.0f;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) v += (on >> e & 1u) ? lp[e] - ref[e] : 0.0f;
+            v = wave_sum(v);
+            const float c = wave_sum(static_cast<float>(__popc(on)));
+            if (lane_id() == 0) st.q.put(s, a, lo, hi, make_float2(v, c));
+        });
     }
-    v = block_sum<LS_THREADS>(v, red);
-    c = block_sum<LS_THREADS>(c, red);
-    if (threadIdx.x == 0) { sums[2 * s] = v; sums[2 * s + 1] = c; }
+}
+
+// Sum of the sequence that each lane asks for (s < 0: none), short ones lane by lane, long ones by the wave.
+__device__ __forceinline__ float2 lane_sequence_sums(const PreferenceState& st, int s) {
+    const Sequences sq = st.seqs();
+    int lo = 0, hi = 0;
+    if (s >= 0) {
+        lo = sq.at(s);
+        hi = max(sq.at(s + 1), lo);
+    }
+    float2 v = {};
+    const int u0 = lo / UNIT, u1 = hi > lo ? (hi - 1) / UNIT : u0;
+    const bool far = u1 - u0 > 8;
+    if (hi > lo) {
+        v = st.q.first(s, lo, hi);
+        if (!far)
+            for (int u = u0 + 1; u <= u1; ++u) v = add(v, st.q.head[u]);
+    }
+    for (unsigned long long todo = __ballot(far); todo; todo &= todo - 1) {
+        const int l = __ffsll(todo) - 1;
+        const float2 h = heads(st.q, __builtin_amdgcn_readlane(u0, l) + 1, __builtin_amdgcn_readlane(u1, l));
+        if (lane_id() == l) v = add(v, h);
+    }
+    return v;
 }
 
 // log(1 + exp(x)) and 1 / (1 + exp(-x)) for any x
 __device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x))); }
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 
-// The loss and, in place of sums[2 s], the gradient factor of sequence s's counted tokens.
-__global__ __launch_bounds__(LS_THREADS) void preference_pairs_kernel(muon_preference_args a, float* sums) {
-    __shared__ float red[LS_THREADS / 64];
-    const int64_t pairs = a.sequences / 2;
-    float loss = 0.0f;
-    for (int64_t p = threadIdx.x; p < pairs; p += LS_THREADS) {
+__device__ __forceinline__ void preference_pairs(const PreferenceState& st, int wave, int waves) {
+    const muon_preference_args& a = st.a;
+    const int pairs = static_cast<int>(a.sequences / 2);
+    for (int p0 = wave * 64; p0 < pairs; p0 += waves * 64) {
+        const int p = p0 + lane_id();
+        const bool on = p < pairs;
         float w[2], r[2];
+#pragma unroll
         for (int k = 0; k < 2; ++k) {
-            w[k] = a.average ? 1.0f / fmaxf(sums[4 * p + 2 * k + 1], 1.0f) : 1.0f;
-            r[k] = sums[4 * p + 2 * k] * w[k];
-            if (a.rewards) a.rewards[2 * p + k] = a.beta * r[k];
+            const float2 v = lane_sequence_sums(st, on ? 2 * p + k : -1);
+            w[k] = a.average ? 1.0f / fmaxf(v.y, 1.0f) : 1.0f;
+            r[k] = v.x * w[k];
+            if (on && a.rewards) a.rewards[2 * p + k] = a.beta * r[k];
         }
         const float u = r[0] - r[1], h = a.beta * u - a.margin, e = a.label_smoothing;
         float l, du;
@@ -80,32 +232,109 @@ __global__ __launch_bounds__(LS_THREADS) void preference_pairs_kernel(muon_prefe
             l = q * q;
             du = 2.0f * q;
         }
-        loss += l;
         du *= a.grad_scale / static_cast<float>(pairs);
-        sums[4 * p] = du * w[0];
-        sums[4 * p + 2] = -du * w[1];
+        if (on) {
+            st.losses[p] = l;
+            st.factor[2 * p] = du * w[0];
+            st.factor[2 * p + 1] = -du * w[1];
+        }
     }
-    loss = block_sum<LS_THREADS>(loss, red);
-    if (threadIdx.x == 0) *a.loss = pairs ? loss / static_cast<float>(pairs) : 0.0f;
 }
 
-__global__ __launch_bounds__(LS_THREADS) void preference_grad_kernel(muon_preference_args a, const float* sums) {
-    zero_uncovered(a.grad_logp, a.dtype, a.offsets, a.sequences, a.tokens);
-    if (static_cast<int64_t>(blockIdx.x) >= a.sequences) return;
-    const Span sp(a.offsets, blockIdx.x, a.tokens);
-    const float f = sums[2 * static_cast<int64_t>(blockIdx.x)];
-    for (int64_t t = sp.lo + threadIdx.x; t < sp.hi; t += LS_THREADS)
-        st_dt(a.grad_logp, t, counted(a.mask, t) ? f : 0.0f, a.dtype);
+template <int NT> __device__ __forceinline__ void preference_loss(const PreferenceState& st, float* red) {
+    const int pairs = static_cast<int>(st.a.sequences / 2);
+    float v = 0.0f;
+#pragma unroll 4
+    for (int p = threadIdx.x; p < pairs; p += NT) v += st.losses[p];
+    v = block_sum<NT>(v, red);
+    if (threadIdx.x == 0) *st.a.loss = pairs ? v / static_cast<float>(pairs) : 0.0f;
+}
+
+template <typename T> __device__ __forceinline__ void preference_grad(const PreferenceState& st, int wave, int waves) {
+    const int n = static_cast<int>(st.a.tokens);
+    for (int u = wave; u < st.units(); u += waves) {
+        const int t0 = u * UNIT, t = t0 + PER * lane_id();
+        const unsigned live = load_mask(st.a.mask, t, n);
+        float g[PER] = {};
+        st.seqs().pieces(t0, t0 + UNIT, [&](int s) { return st.factor[s]; }, [&](int, int a, int b, int, int, float f) {
+            const unsigned on = live & in_piece(t, a, b);
+#pragma unroll
+            for (int e = 0; e < PER; ++e)
+                if (on >> e & 1u) g[e] = f;
+        });
+        store_tokens<T>(st.a.grad_logp, t, n, g);
+    }
+}
+
+enum PreferenceStep { PF_UNITS = 0, PF_PAIRS = 1, PF_GRAD = 2 };
+
+template <typename T, int STEP> __global__ __launch_bounds__(LS_THREADS) void preference_kernel(PreferenceState st) {
+    __shared__ float red[LS_THREADS / 64];
+    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
+    constexpr int W = LS_THREADS / 64;
+    if (STEP == PF_UNITS) preference_units<T>(st, blockIdx.x * W + wave, gridDim.x * W);
+    else if (STEP == PF_PAIRS) preference_pairs(st, blockIdx.x * W + wave, gridDim.x * W);
+    else if (blockIdx.x == 0) preference_loss<LS_THREADS>(st, red);
+    else preference_grad<T>(st, (blockIdx.x - 1) * W + wave, (gridDim.x - 1) * W);
+}
+
+template <typename T> __global__ __launch_bounds__(LS_ONE) void preference_one_kernel(PreferenceState st) {
+    __shared__ float red[LS_ONE / 64];
+    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
+    preference_units<T>(st, wave, LS_ONE / 64);
+    __syncthreads();
+    preference_pairs(st, wave, LS_ONE / 64);
+    __syncthreads();
+    preference_loss<LS_ONE>(st, red);
+    if (st.a.grad_logp) preference_grad<T>(st, wave, LS_ONE / 64);
 }
 
 // ---- policy -----------------------------------------------------------------
 
+constexpr int PL_SUMS = 5;   // weighted loss, KL, held, rho, counted tokens
+
+struct PolicyState {
+    muon_policy_args a;
+    UnitSums<float> q;      // counted tokens by unit: sequence means with a mask
+    float* counts;          // counted tokens by workgroup of the count: token means with a mask
+    int count_parts;
+    float* sums;            // PL_SUMS by workgroup of the main pass
+    __device__ Sequences seqs() const { return {a.offsets, static_cast<int>(a.sequences), static_cast<int>(a.tokens)}; }
+    __device__ int units() const { return static_cast<int>((a.tokens + UNIT - 1) / UNIT); }
+    __device__ bool by_sequence() const { return a.reduction == MUON_REDUCE_SEQUENCE; }
+};
+
+// With a mask: the counted tokens of every sequence's units, or of all sequences (one partial a workgroup).
+template <int NT>
+__device__ __forceinline__ void policy_counts(const PolicyState& st, int wave, int waves, int block, float* red) {
+    const int n = static_cast<int>(st.a.tokens);
+    const Sequences sq = st.seqs();
+    float total = 0.0f;
+    const int first = sq.count ? sq.at(0) : n, last = sq.count ? sq.at(sq.count) : n;
+    for (int u = wave; u < st.units(); u += waves) {
+        const int t0 = u * UNIT, t = t0 + PER * lane_id();
+        const unsigned live = load_mask(st.a.mask, t, n);
+        if (!st.by_sequence()) {
+            total += static_cast<float>(__popc(live & in_piece(t, first, last)));
+        } else {
+            sq.pieces(t0, t0 + UNIT, [](int) { return 0.0f; }, [&](int s, int a, int b, int lo, int hi, float) {
+                if (lo >= t0 && hi <= t0 + UNIT) return;   // counted again where it is used
+                const float c = wave_sum(static_cast<float>(__popc(live & in_piece(t, a, b))));
+                if (lane_id() == 0) st.q.put(s, a, lo, hi, c);
+            });
+        }
+    }
+    if (st.by_sequence()) return;
+    total = block_sum<NT>(total, red);
+    if (threadIdx.x == 0) st.counts[block] = total;
+}
+
 struct PolicyToken { float loss, grad, kl, held, rho; };
 
-__device__ __forceinline__ PolicyToken policy_token(const muon_policy_args& a, int64_t t, float adv) {
-    const float lp = ld_dt(a.logp, t, a.dtype), lo = 1.0f - a.clip_low, hi = 1.0f + a.clip_high;
+__device__ __forceinline__ PolicyToken policy_token(const muon_policy_args& a, float lp, float old, float ref, float adv) {
+    const float lo = 1.0f - a.clip_low, hi = 1.0f + a.clip_high;
     PolicyToken o;
-    o.rho = expf(lp - ld_dt(a.old_logp, t, a.dtype));
+    o.rho = expf(lp - old);
     float gain = fminf(o.rho * adv, fminf(fmaxf(o.rho, lo), hi) * adv);
     bool held = (adv > 0.0f && o.rho > hi) || (adv < 0.0f && o.rho < lo);
     if (a.dual_clip > 0.0f && adv < 0.0f && o.rho > a.dual_clip) {
@@ -117,98 +346,203 @@ __device__ __forceinline__ PolicyToken policy_token(const muon_policy_args& a, i
     o.grad = held ? 0.0f : -o.rho * adv;
     o.kl = 0.0f;
     if (a.kl != MUON_KL_NONE) {
-        const float q = ld_dt(a.ref_logp, t, a.dtype) - lp;
+        const float q = ref - lp;
         float dk;
         if (a.kl == MUON_KL_K1) { o.kl = -q; dk = 1.0f; }
         else if (a.kl == MUON_KL_K2) { o.kl = 0.5f * q * q; dk = -q; }
         else { const float em = expm1f(q); o.kl = em - q; dk = -em; }
-        o.loss += a.kl_coef * o.kl;
-        o.grad += a.kl_coef * dk;
+        o.loss = fmaf(a.kl_coef, o.kl, o.loss);
+        o.grad = fmaf(a.kl_coef, dk, o.grad);
     }
     return o;
 }
 
-constexpr int PL_SUMS = 5;   // loss, KL, held, rho, counted tokens
-
-__global__ __launch_bounds__(LS_THREADS) void policy_sums_kernel(muon_policy_args a, float* sums) {
-    __shared__ float red[LS_THREADS / 64];
-    const int64_t s = blockIdx.x;
-    const Span sp(a.offsets, s, a.tokens);
-    float v[PL_SUMS] = {};
-    for (int64_t t = sp.lo + threadIdx.x; t < sp.hi; t += LS_THREADS) {
-        if (!counted(a.mask, t)) continue;
-        const PolicyToken o = policy_token(a, t, a.advantages[a.advantage_per_sequence ? s : t]);
-        v[0] += o.loss; v[1] += o.kl; v[2] += o.held; v[3] += o.rho; v[4] += 1.0f;
-    }
-    for (int k = 0; k < PL_SUMS; ++k) {
-        const float x = block_sum<LS_THREADS>(v[k], red);
-        if (threadIdx.x == 0) sums[PL_SUMS * s + k] = x;
-    }
-}
-
-// The loss and the statistics; a sequence's weight replaces its loss sum.
-__global__ __launch_bounds__(LS_THREADS) void policy_join_kernel(muon_policy_args a, float* sums) {
-    __shared__ float red[LS_THREADS / 64];
-    float v[PL_SUMS] = {};
-    for (int64_t s = threadIdx.x; s < a.sequences; s += LS_THREADS) {
-        const float* q = sums + PL_SUMS * s;
-        v[0] += a.reduction == MUON_REDUCE_SEQUENCE ? q[0] / fmaxf(q[4], 1.0f) : q[0];
-        for (int k = 1; k < PL_SUMS; ++k) v[k] += q[k];
-    }
-    for (int k = 0; k < PL_SUMS; ++k) v[k] = block_sum<LS_THREADS>(v[k], red);
-    const float per_token = 1.0f / fmaxf(v[4], 1.0f), per_seq = 1.0f / fmaxf(static_cast<float>(a.sequences), 1.0f);
-    if (threadIdx.x == 0) {
-        *a.loss = v[0] * (a.reduction == MUON_REDUCE_SEQUENCE ? per_seq : per_token);
-        if (a.stats) {
-            a.stats[0] = v[1] * per_token;
-            a.stats[1] = v[2] * per_token;
-            a.stats[2] = v[3] * per_token;
-            a.stats[3] = v[4];
+template <typename T, int NT>
+__device__ __forceinline__ void policy_main(const PolicyState& st, int wave, int waves, int block, float* red) {
+    const muon_policy_args& a = st.a;
+    const int n = static_cast<int>(a.tokens);
+    const Sequences sq = st.seqs();
+    float every = 0.0f;   // token mean: the weight of a token
+    if (!st.by_sequence()) {
+        float total;
+        if (a.mask) {
+            float c = 0.0f;
+            for (int k = lane_id(); k < st.count_parts; k += 64) c += st.counts[k];
+            total = wave_sum(c);
+        } else {
+            total = sq.count ? static_cast<float>(max(sq.at(sq.count) - sq.at(0), 0)) : 0.0f;
         }
+        every = 1.0f / fmaxf(total, 1.0f);
     }
-    for (int64_t s = threadIdx.x; s < a.sequences; s += LS_THREADS)
-        sums[PL_SUMS * s] = a.grad_scale *
-                            (a.reduction == MUON_REDUCE_SEQUENCE ? per_seq / fmaxf(sums[PL_SUMS * s + 4], 1.0f) : per_token);
+    float v[PL_SUMS] = {};
+    for (int u = wave; u < st.units(); u += waves) {
+        const int t0 = u * UNIT, t = t0 + PER * lane_id();
+        float lp[PER], old[PER], ref[PER] = {}, adv[PER] = {}, wt[PER] = {}, g[PER];
+        load_tokens<T>(a.logp, t, n, lp);
+        load_tokens<T>(a.old_logp, t, n, old);
+        if (a.kl != MUON_KL_NONE) load_tokens<T>(a.ref_logp, t, n, ref);
+        if (!a.advantage_per_sequence) load_tokens<float>(a.advantages, t, n, adv);
+        const unsigned live = load_mask(a.mask, t, n);
+        unsigned counted = 0;
+        if (!st.by_sequence() && !a.advantage_per_sequence) {   // nothing here depends on the sequence
+            counted = live & (sq.count ? in_piece(t, sq.at(0), sq.at(sq.count)) : 0u);
+#pragma unroll
+            for (int e = 0; e < PER; ++e) wt[e] = every;
+        } else {
+            sq.pieces(t0, t0 + UNIT, [&](int s) { return a.advantage_per_sequence ? a.advantages[s] : 0.0f; },
+                      [&](int s, int pa, int pb, int lo, int hi, float side) {
+                          const unsigned on = live & in_piece(t, pa, pb);
+                          float w = every;
+                          if (st.by_sequence()) {
+                              float c;
+                              if (!a.mask) c = static_cast<float>(hi - lo);
+                              else if (lo >= t0 && hi <= t0 + UNIT) c = wave_sum(static_cast<float>(__popc(on)));
+                              else c = st.q.first(s, lo, hi) + heads(st.q, lo / UNIT + 1, (hi - 1) / UNIT);
+                              w = 1.0f / (fmaxf(c, 1.0f) * static_cast<float>(sq.count));
+                          }
+                          counted |= on;
+#pragma unroll
+                          for (int e = 0; e < PER; ++e)
+                              if (on >> e & 1u) {
+                                  wt[e] = w;
+                                  if (a.advantage_per_sequence) adv[e] = side;
+                              }
+                      });
+        }
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+            g[e] = 0.0f;
+            if (!(counted >> e & 1u)) continue;
+            const PolicyToken o = policy_token(a, lp[e], old[e], ref[e], adv[e]);
+            v[0] = fmaf(wt[e], o.loss, v[0]);
+            v[1] += o.kl;
+            v[2] += o.held;
+            v[3] += o.rho;
+            v[4] += 1.0f;
+            g[e] = a.grad_scale * wt[e] * o.grad;
+        }
+        if (a.grad_logp) store_tokens<T>(a.grad_logp, t, n, g);
+    }
+#pragma unroll
+    for (int k = 0; k < PL_SUMS; ++k) {
+        const float s = block_sum<NT>(v[k], red);
+        if (threadIdx.x == 0) st.sums[PL_SUMS * block + k] = s;
+    }
 }
 
-__global__ __launch_bounds__(LS_THREADS) void policy_grad_kernel(muon_policy_args a, const float* sums) {
-    zero_uncovered(a.grad_logp, a.dtype, a.offsets, a.sequences, a.tokens);
-    const int64_t s = blockIdx.x;
-    if (s >= a.sequences) return;
-    const Span sp(a.offsets, s, a.tokens);
-    const float f = sums[PL_SUMS * s];
-    for (int64_t t = sp.lo + threadIdx.x; t < sp.hi; t += LS_THREADS) {
-        float g = 0.0f;
-        if (counted(a.mask, t)) g = f * policy_token(a, t, a.advantages[a.advantage_per_sequence ? s : t]).grad;
-        st_dt(a.grad_logp, t, g, a.dtype);
+template <int NT> __device__ __forceinline__ void policy_final(const PolicyState& st, int blocks, float* red) {
+    float v[PL_SUMS] = {};
+    for (int b = threadIdx.x; b < blocks; b += NT)
+#pragma unroll
+        for (int k = 0; k < PL_SUMS; ++k) v[k] += st.sums[PL_SUMS * b + k];
+#pragma unroll
+    for (int k = 0; k < PL_SUMS; ++k) v[k] = block_sum<NT>(v[k], red);
+    if (threadIdx.x != 0) return;
+    *st.a.loss = v[0];
+    if (st.a.stats) {
+        const float per = 1.0f / fmaxf(v[4], 1.0f);
+        st.a.stats[0] = v[1] * per;
+        st.a.stats[1] = v[2] * per;
+        st.a.stats[2] = v[3] * per;
+        st.a.stats[3] = v[4];
     }
 }
 
-unsigned seq_grid(int64_t sequences) { return static_cast<unsigned>(sequences > 0 ? sequences : 1); }
+__global__ __launch_bounds__(LS_THREADS) void policy_counts_kernel(PolicyState st) {
+    __shared__ float red[LS_THREADS / 64];
+    constexpr int W = LS_THREADS / 64;
+    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
+    policy_counts<LS_THREADS>(st, blockIdx.x * W + wave, gridDim.x * W, blockIdx.x, red);
+}
+template <typename T> __global__ __launch_bounds__(LS_THREADS) void policy_main_kernel(PolicyState st) {
+    __shared__ float red[LS_THREADS / 64];
+    constexpr int W = LS_THREADS / 64;
+    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
+    policy_main<T, LS_THREADS>(st, blockIdx.x * W + wave, gridDim.x * W, blockIdx.x, red);
+}
+__global__ __launch_bounds__(LS_ONE) void policy_final_kernel(PolicyState st, int blocks) {
+    __shared__ float red[LS_ONE / 64];
+    policy_final<LS_ONE>(st, blocks, red);
+}
+template <typename T> __global__ __launch_bounds__(LS_ONE) void policy_one_kernel(PolicyState st) {
+    __shared__ float red[LS_ONE / 64];
+    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
+    if (st.a.mask) {
+        policy_counts<LS_ONE>(st, wave, LS_ONE / 64, 0, red);
+        __syncthreads();
+    }
+    policy_main<T, LS_ONE>(st, wave, LS_ONE / 64, 0, red);
+    __syncthreads();
+    policy_final<LS_ONE>(st, 1, red);
+}
+
+// ---- host ---------------------------------------------------------------------
+
+int64_t units_of(int64_t tokens) { return (tokens + UNIT - 1) / UNIT; }
+unsigned grid_for(int64_t waves, int most) {
+    return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>((waves + 3) / 4, most)));
+}
 
 }  // namespace
 
-size_t preference_bytes(const muon_preference_args& a) { return 2 * sizeof(float) * static_cast<size_t>(a.sequences); }
-
-hipError_t launch_preference(const muon_preference_args& a, void* workspace, hipStream_t s) {
-    float* sums = static_cast<float*>(workspace);
-    if (a.sequences > 0)
-        hipLaunchKernelGGL(preference_sums_kernel, dim3(seq_grid(a.sequences)), dim3(LS_THREADS), 0, s, a, sums);
-    hipLaunchKernelGGL(preference_pairs_kernel, dim3(1), dim3(LS_THREADS), 0, s, a, sums);
-    if (a.grad_logp)
-        hipLaunchKernelGGL(preference_grad_kernel, dim3(seq_grid(a.sequences)), dim3(LS_THREADS), 0, s, a, sums);
-    return hipGetLastError();
+size_t preference_bytes(const muon_preference_args& a) {
+    const size_t q = static_cast<size_t>(a.sequences), u = static_cast<size_t>(units_of(a.tokens));
+    return (2 * u + q) * sizeof(float2) + (q + q / 2) * sizeof(float);
 }
 
-size_t policy_bytes(const muon_policy_args& a) { return PL_SUMS * sizeof(float) * static_cast<size_t>(a.sequences); }
+hipError_t launch_preference(const muon_preference_args& a, void* workspace, hipStream_t s) {
+    const size_t q = static_cast<size_t>(a.sequences), u = static_cast<size_t>(units_of(a.tokens));
+    float2* f2 = static_cast<float2*>(workspace);
+    float* f = reinterpret_cast<float*>(f2 + 2 * u + q);
+    const PreferenceState st{a, {f2, f2 + u, f2 + 2 * u}, f, f + q};
+    const bool bf = a.dtype == MUON_BF16;
+    if (a.tokens <= LS_SMALL && a.sequences <= LS_SMALL) {
+        if (bf) hipLaunchKernelGGL(preference_one_kernel<uint16_t>, dim3(1), dim3(LS_ONE), 0, s, st);
+        else hipLaunchKernelGGL(preference_one_kernel<float>, dim3(1), dim3(LS_ONE), 0, s, st);
+        return hipGetLastError();
+    }
+    auto launch = [&](auto kernel, unsigned grid) {
+        hipLaunchKernelGGL(kernel, dim3(grid), dim3(LS_THREADS), 0, s, st);
+        return hipGetLastError();
+    };
+    const unsigned grid = grid_for(u, LS_GRID);
+    hipError_t e = launch(bf ? preference_kernel<uint16_t, PF_UNITS> : preference_kernel<float, PF_UNITS>, grid);
+    if (e == hipSuccess) e = launch(preference_kernel<float, PF_PAIRS>, grid_for((a.sequences / 2 + 63) / 64, LS_GRID));
+    if (e == hipSuccess)
+        e = launch(bf ? preference_kernel<uint16_t, PF_GRAD> : preference_kernel<float, PF_GRAD>, a.grad_logp ? grid + 1 : 1);
+    return e;
+}
+
+size_t policy_bytes(const muon_policy_args& a) {
+    const size_t q = static_cast<size_t>(a.sequences), u = static_cast<size_t>(units_of(a.tokens));
+    return (2 * u + q + LS_COUNTS + PL_SUMS * LS_GRID) * sizeof(float);
+}
 
 hipError_t launch_policy(const muon_policy_args& a, void* workspace, hipStream_t s) {
-    float* sums = static_cast<float*>(workspace);
-    if (a.sequences > 0)
-        hipLaunchKernelGGL(policy_sums_kernel, dim3(seq_grid(a.sequences)), dim3(LS_THREADS), 0, s, a, sums);
-    hipLaunchKernelGGL(policy_join_kernel, dim3(1), dim3(LS_THREADS), 0, s, a, sums);
-    if (a.grad_logp)
-        hipLaunchKernelGGL(policy_grad_kernel, dim3(seq_grid(a.sequences)), dim3(LS_THREADS), 0, s, a, sums);
+    const size_t q = static_cast<size_t>(a.sequences), u = static_cast<size_t>(units_of(a.tokens));
+    float* f = static_cast<float*>(workspace);
+    float* counts = f + 2 * u + q;
+    PolicyState st{a, {f, f + u, f + 2 * u}, counts, 1, counts + LS_COUNTS};
+    const bool bf = a.dtype == MUON_BF16;
+    if (a.tokens <= LS_SMALL) {
+        if (bf) hipLaunchKernelGGL(policy_one_kernel<uint16_t>, dim3(1), dim3(LS_ONE), 0, s, st);
+        else hipLaunchKernelGGL(policy_one_kernel<float>, dim3(1), dim3(LS_ONE), 0, s, st);
+        return hipGetLastError();
+    }
+    hipError_t e = hipSuccess;
+    if (a.mask) {
+        // by sequence every unit has work that waits; counting alone keeps few, deep workgroups
+        st.count_parts = static_cast<int>(grid_for(u, a.reduction == MUON_REDUCE_SEQUENCE ? LS_GRID : LS_COUNTS));
+        hipLaunchKernelGGL(policy_counts_kernel, dim3(st.count_parts), dim3(LS_THREADS), 0, s, st);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    const unsigned grid = grid_for(u, LS_GRID);
+    if (bf) hipLaunchKernelGGL(policy_main_kernel<uint16_t>, dim3(grid), dim3(LS_THREADS), 0, s, st);
+    else hipLaunchKernelGGL(policy_main_kernel<float>, dim3(grid), dim3(LS_THREADS), 0, s, st);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(policy_final_kernel, dim3(1), dim3(LS_ONE), 0, s, st, static_cast<int>(grid));
     return hipGetLastError();
 }
 
