@@ -39,7 +39,9 @@ constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr int64_t FEW_TOKENS = 64;          // most tokens of few_kernel
 constexpr int FEW_ROWS = 32;                // vocabulary entries per workgroup of few_kernel
 constexpr int64_t DZ_BYTES = int64_t{4} << 30;   // both layouts of dz, at most: more tokens go in chunks
-constexpr int WORKGROUPS = 256;             // what a product should fill: one workgroup per CU (LDS)
+constexpr int CUS = 256;
+constexpr int64_t FEW_TILES = 192;          // 256 x 256 tiles below which the smaller tile serves a product
+constexpr int PAD = 256;                    // every buffer of dz, e and their statistics is padded to the larger tile
 constexpr int MAX_SPLITS = 16, MIN_SPLIT_STEPS = 8;
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -109,14 +111,6 @@ struct Live {
     __device__ int rows() const { return max(0, min(*count - first, most)); }
 };
 
-// Rows of tokens that are not scored.
-__global__ __launch_bounds__(256) void zero_rows_kernel(const int64_t* targets, int64_t tokens, int64_t cols, void* out,
-                                                        int64_t ld, int dt) {
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-    if (t >= tokens || targets[t] >= 0) return;
-    for (int64_t c = threadIdx.x & 63; c < cols; c += 64) st_dt(out, t * ld + c, 0.0f, dt);
-}
-
 // ---------------------------------------------------------------------------
 // Operand copies
 // ---------------------------------------------------------------------------
@@ -156,24 +150,28 @@ __global__ __launch_bounds__(256) void pack_kernel(PackArgs a) {
     }
 }
 
-// dst[part][c][r] = parts of src[row r][c] for c < cols, zero for rows past the last up to a multiple of 64.
-template <typename T, int PARTS>
-__global__ __launch_bounds__(256) void pack_transposed_kernel(PackArgs a) {
-    __shared__ float tile[64][65];
+// dst[part][c][r] = parts of src[row r][c] for c < cols, zero for rows past the last up to a multiple of 64: the
+// 64 x 64 tile at (r0, c0), through LDS as fp32, 16-byte accesses on both sides.
+template <typename T, int PARTS> __device__ __forceinline__ void transpose_tile(const PackArgs& a, int64_t r0, int64_t c0, float (&tile)[64][65]) {
     const int64_t rows = a.use_live ? a.live.rows() : a.rows;
-    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * 64, c0 = static_cast<int64_t>(blockIdx.y) * 64;
     if (r0 >= rows) return;
-    const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
-    for (int k = y; k < 64; k += 4) {
-        const int64_t r = r0 + k, c = c0 + x;
-        float v = 0.0f;
-        if (r < rows && c < a.cols) v = ld_el<T>(a.src, static_cast<size_t>(a.use_live ? a.live.idx[a.live.first + r] : r) * a.ld + c);
-        tile[k][x] = v;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const int k = (threadIdx.x >> 3) + 32 * half, x = 8 * (threadIdx.x & 7);
+        const int64_t r = r0 + k, left = a.cols - c0 - x;
+        Run<T> w;
+        if (r < rows && left > 0) {
+            const auto* q = G(static_cast<const T*>(a.src) + static_cast<size_t>(a.use_live ? a.live.idx[a.live.first + r] : r) * a.ld + c0);
+            if (left >= 8) w.load(q, x);
+            else w.load(q, x, static_cast<unsigned>(left));
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) tile[k][x + e] = w.get(e);
     }
     __syncthreads();
-    // 8 rows of the source a thread: 16 bytes of one row of the copy
-    for (int k = threadIdx.x; k < 64 * 8; k += 256) {
-        const int c = k / 8, r = (k % 8) * 8;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const int c = (threadIdx.x >> 3) + 32 * half, r = 8 * (threadIdx.x & 7);
         if (c0 + c >= a.cols) continue;
         uint16_t v[8][3];
 #pragma unroll
@@ -191,6 +189,36 @@ __global__ __launch_bounds__(256) void pack_transposed_kernel(PackArgs a) {
     }
 }
 
+// One launch for what the gradients' products need: the transposes of head and hidden and, for grad_hidden, zeros
+// in the rows of tokens that are not scored.  Each is a run of workgroups; dst NULL or no rows: none.
+struct PrepareArgs {
+    PackArgs head, hidden;
+    int head_blocks, hidden_blocks;   // 64 x 64 tiles, along the rows first
+    int head_rows, hidden_rows;       // of them along the rows
+    const int64_t* targets;
+    int64_t tokens, cols;
+    void* zero;
+    size_t zero_ld;
+    int zero_blocks;
+};
+template <typename T, int PARTS> __global__ __launch_bounds__(256) void prepare_kernel(PrepareArgs a) {
+    __shared__ float tile[64][65];
+    int b = blockIdx.x;
+    if (b < a.head_blocks) {
+        transpose_tile<T, PARTS>(a.head, static_cast<int64_t>(b % a.head_rows) * 64, static_cast<int64_t>(b / a.head_rows) * 64, tile);
+        return;
+    }
+    b -= a.head_blocks;
+    if (b < a.hidden_blocks) {
+        transpose_tile<T, PARTS>(a.hidden, static_cast<int64_t>(b % a.hidden_rows) * 64, static_cast<int64_t>(b / a.hidden_rows) * 64, tile);
+        return;
+    }
+    b -= a.hidden_blocks;
+    for (int64_t t = static_cast<int64_t>(b) * 4 + (threadIdx.x >> 6); t < a.tokens; t += 4 * static_cast<int64_t>(a.zero_blocks))
+        if (a.targets[t] < 0)
+            for (int64_t c = threadIdx.x & 63; c < a.cols; c += 64) st_el<T>(a.zero, t * a.zero_ld + c, 0.0f);
+}
+
 // ---------------------------------------------------------------------------
 // Logits, tile by tile
 // ---------------------------------------------------------------------------
@@ -205,7 +233,7 @@ struct LogitsArgs {
     int gather;
     Live live;
     const int64_t* targets;
-    int vocab, steps, ta, tb;
+    int vocab, steps, tail, ta, tb;   // tail: 16-byte chunks of the last k-step
     float scale2;           // scale log2(e)
     float *m, *s, *zt;      // statistics: tile x list entry (pitch rows_pitch); target logit by list entry
     size_t rows_pitch;
@@ -218,67 +246,69 @@ struct LogitsArgs {
     size_t vp;
 };
 
-// The staged tile's columns as rows of `dst` (256 values each from column v0), column c at row r0 + c.
-__device__ __forceinline__ void store_cols(const pt::lds_byte_t* L, uint16_t* dst, size_t ld, size_t r0, size_t v0) {
+// The staged tile's columns as rows of `dst` (from its column v0), column c at row r0 + c.
+template <typename TL> __device__ __forceinline__ void store_cols(const pt::lds_byte_t* L, uint16_t* dst, size_t ld, size_t r0, size_t v0) {
+    constexpr int Q = TL::SIZE / 8, PER = TL::THREADS / Q;   // chunks of a column, columns at a time
 #pragma unroll 4
-    for (int k = 0; k < 16; ++k) {
-        const int c = 16 * k + static_cast<int>(threadIdx.x >> 5), q = threadIdx.x & 31;
-        __builtin_nontemporal_store(pt::stage_col8(L, c, q), G(reinterpret_cast<u32x4*>(dst + (r0 + c) * ld + v0 + 8 * q)));
+    for (int k = 0; k < TL::SIZE / PER; ++k) {
+        const int c = PER * k + static_cast<int>(threadIdx.x) / Q, q = threadIdx.x % Q;
+        __builtin_nontemporal_store(TL::stage_col8(L, c, q), G(reinterpret_cast<u32x4*>(dst + (r0 + c) * ld + v0 + 8 * q)));
     }
 }
 // The staged tile's rows as rows of `dst`.
-__device__ __forceinline__ void store_rows(const pt::lds_byte_t* L, uint16_t* dst, size_t ld, size_t v0, size_t r0) {
+template <typename TL> __device__ __forceinline__ void store_rows(const pt::lds_byte_t* L, uint16_t* dst, size_t ld, size_t v0, size_t r0) {
     const int lane = threadIdx.x & 63, wave = pt::wave_id();
+    constexpr int H = TL::SIZE / 128, U = TL::SIZE / 4 / TL::NWAVES;   // 128-column halves, row quads a wave
 #pragma unroll 2
-    for (int k = 0; k < 16; ++k) {
-        const int u = 8 * wave + (k >> 1), col0 = 128 * (k & 1);
+    for (int k = 0; k < U * H; ++k) {
+        const int u = U * wave + k / H, col0 = 128 * (k % H);
         const size_t row = v0 + 4 * u + (lane & 3), col = r0 + col0 + 32 * (lane >> 4) + 8 * ((lane & 15) >> 2);
-        __builtin_nontemporal_store(pt::stage_row8(L, u, col0), G(reinterpret_cast<u32x4*>(dst + row * ld + col)));
+        __builtin_nontemporal_store(TL::stage_row8(L, u, col0), G(reinterpret_cast<u32x4*>(dst + row * ld + col)));
     }
 }
 
-template <int PARTS, int MODE>
-__global__ __launch_bounds__(pt::THREADS, 2) void logits_kernel(LogitsArgs a) {
-    __shared__ u32x4 lds[pt::LDS_CHUNKS];
+template <int EDGE, int PARTS, int MODE, bool KTAIL>
+__global__ __launch_bounds__(pt::Tile<EDGE>::THREADS, 2) void logits_kernel(LogitsArgs a) {
+    typedef pt::Tile<EDGE> TL;
+    __shared__ u32x4 lds[TL::LDS_CHUNKS];
     pt::lds_byte_t* L = (pt::lds_byte_t*)lds;
     const int n = a.live.rows();
-    const int tb = (n + pt::TILE - 1) / pt::TILE, nb = a.ta * tb;
+    const int tb = (n + EDGE - 1) / EDGE, nb = a.ta * tb;
     if (static_cast<int>(blockIdx.x) >= nb) return;
     int ia, ib;
     pt::tile_of(pt::xcd_remap(blockIdx.x, nb), a.ta, tb, ia, ib);
-    const int v0 = ia * pt::TILE, r0 = ib * pt::TILE;
-    const char *sa[pt::HL], *sb[pt::HL];
+    const int v0 = ia * EDGE, r0 = ib * EDGE;
+    const char *sa[TL::HL], *sb[TL::HL];
 #pragma unroll
-    for (int j = 0; j < pt::HL; ++j) {
-        const int row = pt::load_row(j);
-        sa[j] = a.a + static_cast<size_t>(min(v0 + row, a.vocab - 1)) * a.a_ld + pt::load_chunk(j) * 16;
+    for (int j = 0; j < TL::HL; ++j) {
+        const int row = TL::load_row(j);
+        sa[j] = a.a + static_cast<size_t>(min(v0 + row, a.vocab - 1)) * a.a_ld + TL::load_chunk(j) * 16;
         int r = min(r0 + row, n - 1);
         if (a.gather) r = a.live.idx[a.live.first + r];
-        sb[j] = a.b + static_cast<size_t>(r) * a.b_ld + pt::load_chunk(j) * 16;
+        sb[j] = a.b + static_cast<size_t>(r) * a.b_ld + TL::load_chunk(j) * 16;
     }
-    pt::Acc acc = {};
-    pt::run<PARTS>(sa, sb, a.a_part, a.b_part, 0, a.steps, lds, acc);
+    typename TL::Acc acc = {};
+    TL::template run<PARTS, KTAIL>(sa, sb, a.a_part, a.b_part, 0, a.steps, a.tail, lds, acc);
 
-    const int lane = threadIdx.x & 63, wave = pt::wave_id();
-    const int wm = wave / pt::WAVES_N, wn = wave % pt::WAVES_N, h = lane >> 5;
-    const int vl = v0 + pt::WM * wm + 4 * h;          // this lane's first vocabulary entry
-    const bool edge = v0 + pt::TILE > a.vocab;        // uniform: entries past the vocabulary
+    const int place = TL::stack_place(), h = (threadIdx.x >> 5) & 1;
+    const int vl = v0 + TL::first_row();              // this lane's first vocabulary entry
+    const bool edge = v0 + EDGE > a.vocab;            // uniform: entries past the vocabulary
     lds_barrier();                                    // every wave is done with the operand slabs
 
     if constexpr (MODE != LG_DZ) {
-        float* smax = reinterpret_cast<float*>(lds);          // [2][256]
-        float* ssum = smax + 2 * pt::TILE;                    // [2][256]
-        int col[pt::SN], y[pt::SN];
-        float mx[pt::SN];
+        float* smax = reinterpret_cast<float*>(lds);          // [STACKED][EDGE]
+        float* ssum = smax + TL::STACKED * EDGE;              // [STACKED][EDGE]
+        int col[TL::SN], y[TL::SN];
+        float mx[TL::SN];
 #pragma unroll
-        for (int j = 0; j < pt::SN; ++j) {
-            col[j] = pt::WN * wn + 32 * j + (lane & 31);
+        for (int j = 0; j < TL::SN; ++j) {
+            col[j] = TL::column(j);
             const int r = min(r0 + col[j], n - 1);
             const int64_t t = a.targets[a.live.idx[a.live.first + r]];
             y[j] = t < a.vocab ? static_cast<int>(t) - vl : -1;
             mx[j] = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < pt::SM; ++i)
+            for (int i = 0; i < TL::SM; ++i)
 #pragma unroll
                 for (int q = 0; q < 16; ++q) {
                     const int dv = 32 * i + 8 * (q >> 2) + (q & 3);
@@ -288,17 +318,18 @@ __global__ __launch_bounds__(pt::THREADS, 2) void logits_kernel(LogitsArgs a) {
                     mx[j] = fmaxf(mx[j], z);
                 }
             mx[j] = fmaxf(mx[j], __shfl_xor(mx[j], 32, 64));
-            if (h == 0) smax[pt::TILE * wm + col[j]] = mx[j];
+            if (h == 0) smax[EDGE * place + col[j]] = mx[j];
         }
         lds_barrier();
 #pragma unroll
-        for (int j = 0; j < pt::SN; ++j) {
-            mx[j] = fmaxf(mx[j], smax[pt::TILE * (wm ^ 1) + col[j]]);
+        for (int j = 0; j < TL::SN; ++j) {
+#pragma unroll
+            for (int p = 0; p < TL::STACKED; ++p) mx[j] = fmaxf(mx[j], smax[EDGE * p + col[j]]);
             const float base = mx[j] == -INFINITY ? 0.0f : mx[j];
             float sum = 0.0f, zt = 0.0f;
             bool mine = false;
 #pragma unroll
-            for (int i = 0; i < pt::SM; ++i)
+            for (int i = 0; i < TL::SM; ++i)
 #pragma unroll
                 for (int q = 0; q < 16; ++q) {
                     const int dv = 32 * i + 8 * (q >> 2) + (q & 3);
@@ -309,54 +340,54 @@ __global__ __launch_bounds__(pt::THREADS, 2) void logits_kernel(LogitsArgs a) {
                     if (MODE == LG_SAVE) acc[i][j][q] = ex;
                 }
             sum += __shfl_xor(sum, 32, 64);
-            if (h == 0) ssum[pt::TILE * wm + col[j]] = sum;
+            if (h == 0) ssum[EDGE * place + col[j]] = sum;
             if (mine && r0 + col[j] < n) a.zt[a.live.first + r0 + col[j]] = zt;
         }
         lds_barrier();
 #pragma unroll
-        for (int j = 0; j < pt::SN; ++j)
-            if (wm == 0 && h == 0) {
+        for (int j = 0; j < TL::SN; ++j)
+            if (place == 0 && h == 0) {
                 const size_t o = ia * a.rows_pitch + r0 + col[j];
+                float sum = ssum[col[j]];
+#pragma unroll
+                for (int p = 1; p < TL::STACKED; ++p) sum += ssum[EDGE * p + col[j]];
                 a.m[o] = mx[j];
-                a.s[o] = ssum[col[j]] + ssum[pt::TILE + col[j]];
+                a.s[o] = sum;
             }
         if constexpr (MODE == LG_SAVE) {
             if constexpr (PARTS == 1) {
                 lds_barrier();
-                const pt::Stage st;
-#pragma unroll
-                for (int i = 0; i < pt::SM; ++i)
-#pragma unroll
-                    for (int j = 0; j < pt::SN; ++j)
-#pragma unroll
-                        for (int g = 0; g < 4; ++g)
-                            st.put(L, i, j, g, pack_bf16x2(acc[i][j][4 * g], acc[i][j][4 * g + 1]),
-                                   pack_bf16x2(acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]));
+                const typename TL::Stage st;
+                st.put_all(L, acc);
                 lds_barrier();
-                store_cols(L, static_cast<uint16_t*>(a.e), a.vp, r0, v0);
+                store_cols<TL>(L, static_cast<uint16_t*>(a.e), a.vp, r0, v0);
             } else {
                 float* e = static_cast<float*>(a.e);
-#pragma unroll
-                for (int j = 0; j < pt::SN; ++j)
-#pragma unroll
-                    for (int i = 0; i < pt::SM; ++i)
-#pragma unroll
-                        for (int g = 0; g < 4; ++g)
-                            st_f4(e + (static_cast<size_t>(r0) + col[j]) * a.vp + vl + 32 * i + 8 * g,
-                                  make_float4(acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]));
+                for (int pass = 0; pass < TL::F32_PASSES; ++pass) {
+                    lds_barrier();
+                    TL::put_f32(L, acc, pass);
+                    lds_barrier();
+                    constexpr int Q = EDGE / 4, PER = TL::THREADS / Q;
+#pragma unroll 4
+                    for (int k = 0; k < 128 / PER; ++k) {
+                        const int c = 128 * pass + PER * k + static_cast<int>(threadIdx.x) / Q, q = threadIdx.x % Q;
+                        __builtin_nontemporal_store(TL::stage_f32(L, c, q),
+                                                    G(reinterpret_cast<u32x4*>(e + (static_cast<size_t>(r0) + c) * a.vp + v0 + 4 * q)));
+                    }
+                }
             }
         }
     } else {
-        const pt::Stage st;
+        const typename TL::Stage st;
 #pragma unroll
-        for (int j = 0; j < pt::SN; ++j) {
-            const int r = r0 + pt::WN * wn + 32 * j + (lane & 31);
+        for (int j = 0; j < TL::SN; ++j) {
+            const int r = r0 + TL::column(j);
             const int tok = a.live.idx[a.live.first + min(r, n - 1)];
             const int64_t t = a.targets[tok];
             const int y = t < a.vocab ? static_cast<int>(t) - vl : -1;
             const float c = r < n ? a.scale * a.grad_logp[tok] : 0.0f, l2 = a.lse[tok] * LOG2E;
 #pragma unroll
-            for (int i = 0; i < pt::SM; ++i)
+            for (int i = 0; i < TL::SM; ++i)
 #pragma unroll
                 for (int q = 0; q < 16; ++q) {
                     const int dv = 32 * i + 8 * (q >> 2) + (q & 3);
@@ -369,13 +400,15 @@ __global__ __launch_bounds__(pt::THREADS, 2) void logits_kernel(LogitsArgs a) {
 #pragma unroll
         for (int p = 0; p < PARTS; ++p) {
             if (p > 0) lds_barrier();
+            if (p + 1 == PARTS) {
+                st.put_all(L, acc);
+            } else {   // this part, truncated; the rest stays
 #pragma unroll
-            for (int i = 0; i < pt::SM; ++i)
+                for (int i = 0; i < TL::SM; ++i)
 #pragma unroll
-                for (int j = 0; j < pt::SN; ++j)
+                    for (int j = 0; j < TL::SN; ++j)
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        if (p + 1 < PARTS) {   // this part, truncated; the rest stays
+                        for (int g = 0; g < 4; ++g) {
                             unsigned w[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
@@ -384,14 +417,11 @@ __global__ __launch_bounds__(pt::THREADS, 2) void logits_kernel(LogitsArgs a) {
                                 acc[i][j][4 * g + e] = (w[e] & 0x7f800000u) == 0x7f800000u ? 0.0f : rest;
                             }
                             st.put(L, i, j, g, w[0] >> 16 | w[1], w[2] >> 16 | w[3]);
-                        } else {
-                            st.put(L, i, j, g, pack_bf16x2(acc[i][j][4 * g], acc[i][j][4 * g + 1]),
-                                   pack_bf16x2(acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]));
                         }
-                    }
+            }
             lds_barrier();
-            if (a.dz) store_cols(L, a.dz + p * a.dz_part, a.vp, r0, v0);
-            if (a.dzt) store_rows(L, a.dzt + p * a.dzt_part, a.rows_pitch, v0, r0);
+            if (a.dz) store_cols<TL>(L, a.dz + p * a.dz_part, a.vp, r0, v0);
+            if (a.dzt) store_rows<TL>(L, a.dzt + p * a.dzt_part, a.rows_pitch, v0, r0);
         }
     }
 }
@@ -405,6 +435,7 @@ struct DzArgs {
     const float* m;         // tile x list entry
     const float* logp;      // list entry
     size_t m_pitch;
+    int m_edge;             // vocabulary entries per tile
     Live live;
     const int64_t* targets;
     const float *lse, *grad_logp;
@@ -421,7 +452,7 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
     __shared__ uint16_t tile[PARTS][64][72];   // [entry][token]
     const int n = a.live.rows();
     const int r0 = blockIdx.y * 64, v0 = blockIdx.x * 64;
-    if (r0 >= static_cast<int>((n + pt::TILE - 1) / pt::TILE * pt::TILE)) return;
+    if (r0 >= (n + PAD - 1) / PAD * PAD) return;
     const int vb = threadIdx.x & 7;            // 8 entries each
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
@@ -433,7 +464,7 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
             const int64_t t = a.targets[tok];
             c = a.scale * a.grad_logp[tok];
             y = t < a.vocab ? static_cast<int>(t) - v0 - 8 * vb : -1;
-            f = c * __builtin_amdgcn_exp2f(a.m[(v0 / pt::TILE) * a.m_pitch + a.live.first + r] - a.lse[tok] * LOG2E);
+            f = c * __builtin_amdgcn_exp2f(a.m[(v0 / a.m_edge) * a.m_pitch + a.live.first + r] - a.lse[tok] * LOG2E);
             // 1 - p of the target from logp: e is rounded, which 1 - e f would magnify as p goes to 1
             dy = -c * expm1f(a.logp[a.live.first + r]);
         }
@@ -493,47 +524,69 @@ struct GradArgs {
     int by_token;           // grad_hidden: rows from the list, out rows are its tokens
     int steps;              // k-steps (by_token: over the vocabulary), else the list gives them
     int ta, tb, splits;
-    void* out;              // bf16, 16-byte aligned rows: written directly when slab is NULL
+    void* out;
     size_t ld;
-    float* slab;            // fp32 tiles in accumulator layout, [split][tile][32][512] x 16 bytes
+    float* slab;            // fp32 tiles in accumulator layout, [split][tile][quads][threads] x 16 bytes, or NULL: write out
     int add;                // add to what the slab holds (later chunks of tokens)
 };
 
-template <int PARTS>
-__global__ __launch_bounds__(pt::THREADS, 2) void grad_kernel(GradArgs a) {
-    __shared__ u32x4 lds[pt::LDS_CHUNKS];
+// A whole 16-byte piece of the output at any element alignment, or the first `left` of its elements.
+__device__ __forceinline__ void st_piece(uint16_t* p, const u32x4& v, int left) {
+    if (left >= 8) {
+        *(global_t<u32x4_el2>*)G(p) = v;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+            if (e < left) G(p)[e] = static_cast<uint16_t>(v[e >> 1] >> (16 * (e & 1)));
+    }
+}
+__device__ __forceinline__ void st_piece(float* p, const u32x4& v, int left) {
+    if (left >= 4) {
+        *(global_t<f32x4_el4>*)G(p) = __builtin_bit_cast(f32x4_t, v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+            if (e < left) G(p)[e] = __uint_as_float(v[e]);
+    }
+}
+
+// T: the gradient's type.
+template <int EDGE, int PARTS, typename T>
+__global__ __launch_bounds__(pt::Tile<EDGE>::THREADS, 2) void grad_kernel(GradArgs a) {
+    typedef pt::Tile<EDGE> TL;
+    __shared__ u32x4 lds[TL::LDS_CHUNKS];
     pt::lds_byte_t* L = (pt::lds_byte_t*)lds;
     const int n = a.live.rows();
     const int rows = a.by_token ? n : a.rows, all = a.by_token ? a.steps : (n + pt::KS - 1) / pt::KS;
-    const int tb = (rows + pt::TILE - 1) / pt::TILE, nb = a.ta * tb;
+    const int tb = (rows + EDGE - 1) / EDGE, nb = a.ta * tb;
     if (static_cast<int>(blockIdx.x) >= nb) return;
     const int tile = pt::xcd_remap(blockIdx.x, nb);
     int ia, ib;
     pt::tile_of(tile, a.ta, tb, ia, ib);
-    const int c0 = ia * pt::TILE, r0 = ib * pt::TILE;
+    const int c0 = ia * EDGE, r0 = ib * EDGE;
     const int split = blockIdx.y;
     const int k_first = static_cast<int>(static_cast<int64_t>(all) * split / a.splits);
     const int steps = static_cast<int>(static_cast<int64_t>(all) * (split + 1) / a.splits) - k_first;
-    pt::Acc acc = {};
+    typename TL::Acc acc = {};
     if (steps > 0) {
-        const char *sa[pt::HL], *sb[pt::HL];
+        const char *sa[TL::HL], *sb[TL::HL];
 #pragma unroll
-        for (int j = 0; j < pt::HL; ++j) {
-            const int row = pt::load_row(j);
-            sa[j] = a.a + static_cast<size_t>(min(c0 + row, a.cols - 1)) * a.a_ld + pt::load_chunk(j) * 16;
-            sb[j] = a.b + static_cast<size_t>(r0 + row) * a.b_ld + pt::load_chunk(j) * 16;   // padded to the tile
+        for (int j = 0; j < TL::HL; ++j) {
+            const int row = TL::load_row(j);
+            sa[j] = a.a + static_cast<size_t>(min(c0 + row, a.cols - 1)) * a.a_ld + TL::load_chunk(j) * 16;
+            sb[j] = a.b + static_cast<size_t>(r0 + row) * a.b_ld + TL::load_chunk(j) * 16;   // padded to the tile
         }
-        pt::run<PARTS>(sa, sb, a.a_part, a.b_part, static_cast<size_t>(k_first) * (pt::KS * 2), steps, lds, acc);
+        TL::template run<PARTS, false>(sa, sb, a.a_part, a.b_part, static_cast<size_t>(k_first) * (pt::KS * 2), steps, 0, lds, acc);
     }
     if (a.slab) {
-        float* s = a.slab + (static_cast<size_t>(split) * a.ta * a.tb + tile) * (pt::TILE * pt::TILE) + threadIdx.x * 4;
+        float* s = a.slab + (static_cast<size_t>(split) * a.ta * a.tb + tile) * (EDGE * EDGE) + threadIdx.x * 4;
 #pragma unroll
-        for (int i = 0; i < pt::SM; ++i)
+        for (int i = 0; i < TL::SM; ++i)
 #pragma unroll
-            for (int j = 0; j < pt::SN; ++j)
+            for (int j = 0; j < TL::SN; ++j)
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    float* p = s + static_cast<size_t>((i * pt::SN + j) * 4 + g) * (pt::THREADS * 4);
+                    float* p = s + static_cast<size_t>((i * TL::SN + j) * 4 + g) * (TL::THREADS * 4);
                     float4 v = make_float4(acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]);
                     if (a.add) {
                         const float4 o = ld_f4(p);
@@ -543,53 +596,53 @@ __global__ __launch_bounds__(pt::THREADS, 2) void grad_kernel(GradArgs a) {
                 }
         return;
     }
-    lds_barrier();
-    const pt::Stage st;
-#pragma unroll
-    for (int i = 0; i < pt::SM; ++i)
-#pragma unroll
-        for (int j = 0; j < pt::SN; ++j)
-#pragma unroll
-            for (int g = 0; g < 4; ++g)
-                st.put(L, i, j, g, pack_bf16x2(acc[i][j][4 * g], acc[i][j][4 * g + 1]),
-                       pack_bf16x2(acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]));
-    lds_barrier();
-    uint16_t* out = static_cast<uint16_t*>(a.out);
-#pragma unroll 4
-    for (int k = 0; k < 16; ++k) {
-        const int c = 16 * k + static_cast<int>(threadIdx.x >> 5), q = threadIdx.x & 31;
-        if (r0 + c >= rows) continue;
-        const size_t row = a.by_token ? a.live.idx[a.live.first + r0 + c] : r0 + c;
-        const u32x4 v = pt::stage_col8(L, c, q);
-        uint16_t* p = out + row * a.ld + c0 + 8 * q;
-        if (c0 + 8 * q + 8 <= a.cols) {
-            G(reinterpret_cast<u32x4*>(p))[0] = v;
+    T* out = static_cast<T*>(a.out);
+    constexpr int E = 16 / sizeof(T), Q = EDGE / E, PER = TL::THREADS / Q;   // elements of a piece, pieces of a row, rows at a time
+    constexpr int PASSES = sizeof(T) == 2 ? 1 : TL::F32_PASSES, COLS = EDGE / PASSES;
+    for (int pass = 0; pass < PASSES; ++pass) {
+        lds_barrier();
+        if constexpr (sizeof(T) == 2) {
+            const typename TL::Stage st;
+            st.put_all(L, acc);
         } else {
-            for (int e = 0; e < 8; ++e)
-                if (c0 + 8 * q + e < a.cols) G(p)[e] = static_cast<uint16_t>(v[e >> 1] >> (16 * (e & 1)));
+            TL::put_f32(L, acc, pass);
+        }
+        lds_barrier();
+#pragma unroll 4
+        for (int k = 0; k < COLS / PER; ++k) {
+            const int c = COLS * pass + PER * k + static_cast<int>(threadIdx.x) / Q, q = threadIdx.x % Q;
+            if (r0 + c >= rows) continue;
+            const size_t row = a.by_token ? a.live.idx[a.live.first + r0 + c] : r0 + c;
+            u32x4 v;
+            if constexpr (sizeof(T) == 2) v = TL::stage_col8(L, c, q);
+            else v = TL::stage_f32(L, c, q);
+            st_piece(out + row * a.ld + c0 + E * q, v, a.cols - c0 - E * q);
         }
     }
 }
 
 // Sums the splits' tiles in order and writes the gradient; one wave per 32 x 32 block.
-__global__ __launch_bounds__(256) void slab_sum_kernel(GradArgs a, int dt) {
+template <int EDGE> __global__ __launch_bounds__(256) void slab_sum_kernel(GradArgs a, int dt) {
+    typedef pt::Tile<EDGE> TL;
+    constexpr int BLOCKS = (EDGE / 32) * (EDGE / 32), PER = TL::SM * TL::SN;   // blocks of a tile, of a wave's share
     __shared__ float tile[4][32][33];   // [wave][gradient row][gradient column]
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int block = blockIdx.x * 4 + wave, t = block / 64, b = block % 64;
+    const int block = blockIdx.x * 4 + wave, t = block / BLOCKS, b = block % BLOCKS;
     const int rows = a.by_token ? a.live.rows() : a.rows;
-    const int tb = (rows + pt::TILE - 1) / pt::TILE;
+    const int tb = (rows + EDGE - 1) / EDGE;
     if (t >= a.ta * tb) return;
     int ia, ib;
     pt::tile_of(t, a.ta, tb, ia, ib);
-    const int w = b / 8, i = (b % 8) / pt::SN, j = b % pt::SN;
-    const int c0 = ia * pt::TILE + pt::WM * (w / pt::WAVES_N) + 32 * i, r0 = ib * pt::TILE + pt::WN * (w % pt::WAVES_N) + 32 * j;
+    const int w = b / PER, i = (b % PER) / TL::SN, j = b % TL::SN;
+    const int c0 = ia * EDGE + TL::share_row(w) + 32 * i, r0 = ib * EDGE + TL::share_col(w) + 32 * j;
     if (c0 >= a.cols || r0 >= rows) return;
     float4 v[4] = {};
+#pragma unroll 4
     for (int s = 0; s < a.splits; ++s) {
-        const float* p = a.slab + (static_cast<size_t>(s) * a.ta * a.tb + t) * (pt::TILE * pt::TILE) + (64 * w + lane) * 4;
+        const float* p = a.slab + (static_cast<size_t>(s) * a.ta * a.tb + t) * (EDGE * EDGE) + (64 * w + lane) * 4;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-            const float4 x = ld_f4(p + static_cast<size_t>((i * pt::SN + j) * 4 + g) * (pt::THREADS * 4));
+            const float4 x = ld_f4(p + static_cast<size_t>((i * TL::SN + j) * 4 + g) * (TL::THREADS * 4));
             v[g] = make_float4(v[g].x + x.x, v[g].y + x.y, v[g].z + x.z, v[g].w + x.w);
         }
     }
@@ -802,19 +855,37 @@ struct Bump {
     }
 };
 
+// Which tile serves a product of so many 256 x 256 tiles.
+int edge_for(int64_t tiles) { return tiles < FEW_TILES ? 128 : 256; }
+
 // What both directions derive from the shape.
 struct Shape {
     int64_t tokens, cols, vocab;
     int parts;
-    int64_t tp, vp, dp;      // padded to the tile, the tile, the k-step
-    int ta;                  // vocabulary tiles
-    bool direct_hidden, direct_head;   // operands that the products can read where they are
+    int64_t tp, vp, dp;      // padded to PAD, PAD, the k-step
+    int edge;                // tile of the logits' product
+    bool direct_hidden, direct_head;   // operands that the products can read where they are: bf16 in whole 16-byte chunks
     Shape(int64_t t, int64_t d, int64_t v, int dtype, const void* hidden, int64_t ld_hidden, const void* head, int64_t ld_head)
-        : tokens(t), cols(d), vocab(v), parts(dtype == MUON_BF16 ? 1 : 3), tp(up(std::max<int64_t>(t, 1), pt::TILE)),
-          vp(up(v, pt::TILE)), dp(up(d, pt::KS)), ta(static_cast<int>(vp / pt::TILE)) {
-        const bool ok = dtype == MUON_BF16 && d % pt::KS == 0;
+        : tokens(t), cols(d), vocab(v), parts(dtype == MUON_BF16 ? 1 : 3), tp(up(std::max<int64_t>(t, 1), PAD)), vp(up(v, PAD)),
+          dp(up(d, pt::KS)), edge(edge_for(tp / PAD * (vp / PAD))) {
+        const bool ok = dtype == MUON_BF16 && d % 8 == 0;
         direct_hidden = ok && reinterpret_cast<uintptr_t>(hidden) % 16 == 0 && ld_hidden % 8 == 0;
         direct_head = ok && reinterpret_cast<uintptr_t>(head) % 16 == 0 && ld_head % 8 == 0;
+    }
+    int ta() const { return static_cast<int>(vp / edge); }
+};
+
+// The buffer that the forward pass keeps: exp(z - m), the tiles' m, logp by list entry, and the list.
+struct SavedPlan {
+    size_t e, m, logp, idx, count, bytes;
+    explicit SavedPlan(const Shape& sh) {
+        Bump b;
+        e = b.take((sh.parts == 1 ? 2 : 4) * static_cast<size_t>(sh.tp) * sh.vp);
+        m = b.take(sizeof(float) * sh.ta() * static_cast<size_t>(sh.tp));
+        logp = b.take(sizeof(float) * static_cast<size_t>(sh.tp));
+        idx = b.take(sizeof(int32_t) * static_cast<size_t>(sh.tp));
+        count = b.take(sizeof(int32_t));
+        bytes = b.at;
     }
 };
 
@@ -829,11 +900,11 @@ struct ForwardPlan {
         few_tiles = static_cast<int>(ceil_div(a.vocab, FEW_ROWS));
         Bump b;
         const size_t part = sizeof(uint16_t) * sh.parts * sh.dp;
-        idx = b.take(few ? 0 : sizeof(int32_t) * sh.tp);
+        idx = b.take(few || a.saved ? 0 : sizeof(int32_t) * sh.tp);
         count = b.take(sizeof(int32_t));
         hidden = b.take(few || sh.direct_hidden ? 0 : part * sh.tp);
         head = b.take(few || sh.direct_head ? 0 : part * sh.vocab);
-        const size_t stats = few ? static_cast<size_t>(a.tokens) * few_tiles : static_cast<size_t>(sh.ta) * sh.tp;
+        const size_t stats = few ? static_cast<size_t>(a.tokens) * few_tiles : static_cast<size_t>(sh.ta()) * sh.tp;
         m = b.take(a.saved ? 0 : stats * sizeof(float));
         s = b.take(stats * sizeof(float));
         zt = b.take(sizeof(float) * sh.tp);
@@ -841,55 +912,38 @@ struct ForwardPlan {
     }
 };
 
-struct SavedPlan {
-    size_t e, m, logp, bytes;
-    SavedPlan(int64_t tokens, int64_t vocab, int dtype) {
-        const int64_t tp = up(std::max<int64_t>(tokens, 1), pt::TILE), vp = up(vocab, pt::TILE);
-        Bump b;
-        e = b.take((dtype == MUON_BF16 ? 2 : 4) * static_cast<size_t>(tp) * vp);
-        m = b.take(sizeof(float) * (vp / pt::TILE) * static_cast<size_t>(tp));
-        logp = b.take(sizeof(float) * static_cast<size_t>(tp));
-        bytes = b.at;
-    }
-};
-
-// How a gradient's product is spread: enough workgroups for the chip, each with a worthwhile run of k.
-int split_count(int64_t tiles, int64_t steps) {
-    const int64_t want = WORKGROUPS / std::max<int64_t>(tiles, 1);
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, MAX_SPLITS, steps / MIN_SPLIT_STEPS})));
-}
-
+// How a gradient's product is tiled and spread: the small tile where the large ones are too few, then
+// the sum over k over enough workgroups for the chip, each with a worthwhile run of k.
 struct GradPlan {
-    int ta, tb, splits;
+    int edge, ta, tb, splits;
     bool slab;
-    size_t slab_bytes() const { return slab ? sizeof(float) * pt::TILE * pt::TILE * splits * ta * tb : 0; }
+    GradPlan(int64_t cols, int64_t rows, int64_t k, bool later_chunks) {
+        edge = edge_for(ceil_div(cols, 256) * ceil_div(rows, 256));
+        ta = static_cast<int>(ceil_div(cols, edge));
+        tb = static_cast<int>(ceil_div(rows, edge));
+        const int64_t tiles = static_cast<int64_t>(ta) * tb;
+        splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({CUS / tiles, MAX_SPLITS, k / pt::KS / MIN_SPLIT_STEPS})));
+        slab = splits > 1 || later_chunks;
+    }
+    size_t slab_bytes() const { return slab ? sizeof(float) * edge * edge * static_cast<size_t>(splits) * ta * tb : 0; }
 };
 
 struct BackwardPlan {
     Shape sh;
     int64_t chunk;          // list entries at a time
     int chunks;
-    size_t idx, count, hidden, head, head_t, hidden_t, dz, dzt, slab, bytes;
     GradPlan gh, gw;
-    explicit BackwardPlan(const muon_token_logp_backward_args& a)
-        : sh(a.tokens, a.cols, a.vocab, a.dtype, a.hidden, a.ld_hidden, a.head, a.ld_head) {
+    size_t idx, count, hidden, head, head_t, hidden_t, dz, dzt, slab, slab_w, bytes;
+    static int64_t chunk_of(const Shape& sh) {
         const int64_t both = sizeof(uint16_t) * sh.parts * 2 * sh.vp;
-        chunk = std::min(sh.tp, std::max<int64_t>(pt::TILE, DZ_BYTES / both / pt::TILE * pt::TILE));
-        chunks = static_cast<int>(ceil_div(sh.tp, chunk));
-        const int tc = static_cast<int>(ceil_div(sh.cols, pt::TILE));
-        auto direct = [&](const void* p, int64_t ld) {
-            return a.dtype == MUON_BF16 && reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0;
-        };
-        gh.ta = gw.ta = tc;
-        gh.tb = static_cast<int>(chunk / pt::TILE);
-        gw.tb = sh.ta;
-        gh.splits = split_count(static_cast<int64_t>(gh.ta) * gh.tb, sh.vp / pt::KS);
-        gw.splits = split_count(static_cast<int64_t>(gw.ta) * gw.tb, chunk / pt::KS);
-        gh.slab = gh.splits > 1 || !direct(a.grad_hidden, a.ld_grad_hidden);
-        gw.slab = gw.splits > 1 || chunks > 1 || !direct(a.grad_head, a.ld_grad_head);
+        return std::min(sh.tp, std::max<int64_t>(PAD, DZ_BYTES / both / PAD * PAD));
+    }
+    explicit BackwardPlan(const muon_token_logp_backward_args& a)
+        : sh(a.tokens, a.cols, a.vocab, a.dtype, a.hidden, a.ld_hidden, a.head, a.ld_head), chunk(chunk_of(sh)),
+          chunks(static_cast<int>(ceil_div(sh.tp, chunk))), gh(sh.cols, chunk, sh.vp, false), gw(sh.cols, sh.vocab, chunk, chunks > 1) {
         Bump b;
         const size_t el = sizeof(uint16_t) * sh.parts;
-        idx = b.take(sizeof(int32_t) * sh.tp);
+        idx = b.take(a.saved ? 0 : sizeof(int32_t) * sh.tp);
         count = b.take(sizeof(int32_t));
         hidden = b.take(a.saved || sh.direct_hidden ? 0 : el * sh.dp * chunk);
         head = b.take(a.saved || sh.direct_head ? 0 : el * sh.dp * sh.vocab);
@@ -902,8 +956,9 @@ struct BackwardPlan {
         slab_w = b.take(a.grad_head ? gw.slab_bytes() : 0);
         bytes = b.at;
     }
-    size_t slab_w;
 };
+
+Shape shape_of(const muon_token_logp_args& a) { return Shape(a.tokens, a.cols, a.vocab, a.dtype, a.hidden, a.ld_hidden, a.head, a.ld_head); }
 
 hipError_t launch_live(const int64_t* targets, int64_t tokens, int32_t* idx, int32_t* count, float* logp, float* lse,
                        hipStream_t s) {
@@ -913,34 +968,39 @@ hipError_t launch_live(const int64_t* targets, int64_t tokens, int32_t* idx, int
 
 hipError_t launch_pack(const PackArgs& p, int dtype, hipStream_t s) {
     const int64_t work = p.rows * static_cast<int64_t>(p.dst_ld / 8);
-    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(ceil_div(work, 256), 8 * WORKGROUPS)));
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(ceil_div(work, 256), 8 * CUS)));
     if (dtype == MUON_BF16) hipLaunchKernelGGL((pack_kernel<uint16_t, 1>), grid, dim3(256), 0, s, p);
     else hipLaunchKernelGGL((pack_kernel<float, 3>), grid, dim3(256), 0, s, p);
     return hipGetLastError();
 }
 
-hipError_t launch_pack_transposed(const PackArgs& p, int dtype, hipStream_t s) {
-    const dim3 grid(static_cast<unsigned>(ceil_div(p.rows, 64)), static_cast<unsigned>(ceil_div(p.cols, 64)));
-    if (dtype == MUON_BF16) hipLaunchKernelGGL((pack_transposed_kernel<uint16_t, 1>), grid, dim3(256), 0, s, p);
-    else hipLaunchKernelGGL((pack_transposed_kernel<float, 3>), grid, dim3(256), 0, s, p);
+template <int EDGE, int MODE> hipError_t launch_logits_edge(const LogitsArgs& l, int parts, hipStream_t s) {
+    const dim3 grid(static_cast<unsigned>(l.ta) * l.tb), block(pt::Tile<EDGE>::THREADS);
+    if (parts == 3) hipLaunchKernelGGL((logits_kernel<EDGE, 3, MODE, false>), grid, block, 0, s, l);
+    else if (l.tail < pt::CHUNKS) hipLaunchKernelGGL((logits_kernel<EDGE, 1, MODE, true>), grid, block, 0, s, l);
+    else hipLaunchKernelGGL((logits_kernel<EDGE, 1, MODE, false>), grid, block, 0, s, l);
     return hipGetLastError();
 }
-
-template <int MODE> hipError_t launch_logits(const LogitsArgs& l, int parts, hipStream_t s) {
-    const dim3 grid(static_cast<unsigned>(l.ta) * l.tb);
-    if (parts == 1) hipLaunchKernelGGL((logits_kernel<1, MODE>), grid, dim3(pt::THREADS), 0, s, l);
-    else hipLaunchKernelGGL((logits_kernel<3, MODE>), grid, dim3(pt::THREADS), 0, s, l);
-    return hipGetLastError();
+template <int MODE> hipError_t launch_logits(const LogitsArgs& l, int edge, int parts, hipStream_t s) {
+    return edge == 256 ? launch_logits_edge<256, MODE>(l, parts, s) : launch_logits_edge<128, MODE>(l, parts, s);
 }
 
-hipError_t launch_grad(const GradArgs& g, int parts, int dtype, bool last, hipStream_t s) {
-    const dim3 grid(static_cast<unsigned>(g.ta) * g.tb, g.splits);
-    if (parts == 1) hipLaunchKernelGGL(grad_kernel<1>, grid, dim3(pt::THREADS), 0, s, g);
-    else hipLaunchKernelGGL(grad_kernel<3>, grid, dim3(pt::THREADS), 0, s, g);
-    hipError_t e = hipGetLastError();
+template <int EDGE> hipError_t launch_grad_edge(const GradArgs& g, int parts, int dtype, bool last, hipStream_t s) {
+    const dim3 grid(static_cast<unsigned>(g.ta) * g.tb, g.splits), block(pt::Tile<EDGE>::THREADS);
+    if (parts == 1) hipLaunchKernelGGL((grad_kernel<EDGE, 1, uint16_t>), grid, block, 0, s, g);
+    else hipLaunchKernelGGL((grad_kernel<EDGE, 3, float>), grid, block, 0, s, g);
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !g.slab || !last) return e;
-    hipLaunchKernelGGL(slab_sum_kernel, dim3(static_cast<unsigned>(g.ta) * g.tb * 16), dim3(256), 0, s, g, dtype);
+    const unsigned blocks = static_cast<unsigned>(g.ta) * g.tb * (EDGE / 32 * (EDGE / 32) / 4);
+    hipLaunchKernelGGL(slab_sum_kernel<EDGE>, dim3(blocks), dim3(256), 0, s, g, dtype);
     return hipGetLastError();
+}
+hipError_t launch_grad(GradArgs g, const GradPlan& pl, float* slab, int parts, int dtype, bool last, hipStream_t s) {
+    g.ta = pl.ta;
+    g.tb = pl.tb;
+    g.splits = pl.splits;
+    g.slab = pl.slab ? slab : nullptr;
+    return pl.edge == 256 ? launch_grad_edge<256>(g, parts, dtype, last, s) : launch_grad_edge<128>(g, parts, dtype, last, s);
 }
 
 #define TL_TRY(expr)                       \
@@ -954,8 +1014,10 @@ hipError_t logits_operands(const Shape& sh, const void* hidden, int64_t ld_hidde
                            int dtype, char* hidden_copy, char* head_copy, bool pack_head, LogitsArgs& l, hipStream_t s) {
     const size_t row = sizeof(uint16_t) * sh.dp;
     l.steps = static_cast<int>(sh.dp / pt::KS);
+    // copies have zeros past the last column; a row read in place has none, so its last step stops there (in both)
+    l.tail = sh.direct_head || sh.direct_hidden ? static_cast<int>(ceil_div(sh.cols - (sh.dp - pt::KS), 8)) : pt::CHUNKS;
     l.vocab = static_cast<int>(sh.vocab);
-    l.ta = sh.ta;
+    l.ta = sh.ta();
     l.a = sh.direct_head ? static_cast<const char*>(head) : head_copy;
     l.a_ld = sh.direct_head ? 2 * static_cast<size_t>(ld_head) : row;
     l.a_part = row * sh.vocab;
@@ -987,7 +1049,7 @@ template <typename T, int PARTS> hipError_t launch_few(const FewArgs& f, bool ve
 
 }  // namespace
 
-size_t token_logp_saved_bytes(const muon_token_logp_args& a) { return SavedPlan(a.tokens, a.vocab, a.dtype).bytes; }
+size_t token_logp_saved_bytes(const muon_token_logp_args& a) { return SavedPlan(shape_of(a)).bytes; }
 size_t token_logp_bytes(const muon_token_logp_args& a) { return ForwardPlan(a).bytes; }
 size_t token_logp_backward_bytes(const muon_token_logp_backward_args& a) { return BackwardPlan(a).bytes; }
 
@@ -1013,29 +1075,32 @@ hipError_t launch_token_logp(const muon_token_logp_args& a, void* workspace, hip
         hipLaunchKernelGGL(combine_kernel<1>, dim3(static_cast<unsigned>(a.tokens)), dim3(256), 0, s, c);
         return hipGetLastError();
     }
+    LogitsArgs l{};
     int32_t* idx = reinterpret_cast<int32_t*>(ws + pl.idx);
     int32_t* count = reinterpret_cast<int32_t*>(ws + pl.count);
+    float* kept = nullptr;
+    if (a.saved) {
+        const SavedPlan sv(sh);
+        char* p = static_cast<char*>(a.saved);
+        l.e = p + sv.e;
+        m = reinterpret_cast<float*>(p + sv.m);
+        kept = reinterpret_cast<float*>(p + sv.logp);
+        idx = reinterpret_cast<int32_t*>(p + sv.idx);
+        count = reinterpret_cast<int32_t*>(p + sv.count);
+    }
     TL_TRY(launch_live(a.targets, a.tokens, idx, count, a.logp, a.lse, s));
-    LogitsArgs l{};
     l.live = {idx, count, 0, static_cast<int32_t>(sh.tp)};
     TL_TRY(logits_operands(sh, a.hidden, a.ld_hidden, a.head, a.ld_head, a.dtype, ws + pl.hidden, ws + pl.head, true, l, s));
     l.targets = a.targets;
-    l.tb = static_cast<int>(sh.tp / pt::TILE);
+    l.tb = static_cast<int>(sh.tp / sh.edge);
     l.scale2 = scale2;
-    float* kept = nullptr;
-    if (a.saved) {
-        const SavedPlan sv(a.tokens, a.vocab, a.dtype);
-        kept = reinterpret_cast<float*>(static_cast<char*>(a.saved) + sv.logp);
-        l.e = static_cast<char*>(a.saved) + sv.e;
-        m = reinterpret_cast<float*>(static_cast<char*>(a.saved) + sv.m);
-    }
     l.m = m;
     l.s = sums;
     l.zt = zt;
     l.rows_pitch = sh.tp;
     l.vp = sh.vp;
-    TL_TRY(a.saved ? launch_logits<LG_SAVE>(l, sh.parts, s) : launch_logits<LG_STATS>(l, sh.parts, s));
-    const CombineArgs c{m, sums, zt, static_cast<size_t>(sh.tp), 1, sh.ta, a.targets, a.vocab, a.logp, a.lse, idx, count, a.tokens,
+    TL_TRY(a.saved ? launch_logits<LG_SAVE>(l, sh.edge, sh.parts, s) : launch_logits<LG_STATS>(l, sh.edge, sh.parts, s));
+    const CombineArgs c{m, sums, zt, static_cast<size_t>(sh.tp), 1, sh.ta(), a.targets, a.vocab, a.logp, a.lse, idx, count, a.tokens,
                         kept};
     hipLaunchKernelGGL(combine_kernel<32>, dim3(static_cast<unsigned>(sh.tp / 32)), dim3(256), 0, s, c);
     return hipGetLastError();
@@ -1044,28 +1109,51 @@ hipError_t launch_token_logp(const muon_token_logp_args& a, void* workspace, hip
 hipError_t launch_token_logp_backward(const muon_token_logp_backward_args& a, void* workspace, hipStream_t s) {
     const BackwardPlan pl(a);
     const Shape& sh = pl.sh;
+    const SavedPlan sv(sh);
     char* ws = static_cast<char*>(workspace);
-    int32_t* idx = reinterpret_cast<int32_t*>(ws + pl.idx);
-    int32_t* count = reinterpret_cast<int32_t*>(ws + pl.count);
-    TL_TRY(launch_live(a.targets, a.tokens, idx, count, nullptr, nullptr, s));
-    if (a.grad_hidden && a.tokens > 0) {
-        hipLaunchKernelGGL(zero_rows_kernel, dim3(static_cast<unsigned>(ceil_div(a.tokens, 4))), dim3(256), 0, s, a.targets,
-                           a.tokens, a.cols, a.grad_hidden, a.ld_grad_hidden, a.dtype);
-        TL_TRY(hipGetLastError());
-        TL_TRY(launch_pack_transposed({a.head, static_cast<size_t>(a.ld_head), sh.vocab, sh.cols, 0, {},
-                                       reinterpret_cast<uint16_t*>(ws + pl.head_t), static_cast<size_t>(sh.vp),
-                                       static_cast<size_t>(sh.vp) * sh.cols}, a.dtype, s));
+    const char* saved = static_cast<const char*>(a.saved);
+    const int32_t* idx = reinterpret_cast<const int32_t*>(saved ? saved + sv.idx : ws + pl.idx);
+    const int32_t* count = reinterpret_cast<const int32_t*>(saved ? saved + sv.count : ws + pl.count);
+    if (!saved || a.tokens == 0) {   // without tokens there was no forward pass to keep the list
+        idx = reinterpret_cast<int32_t*>(ws + pl.idx);
+        count = reinterpret_cast<int32_t*>(ws + pl.count);
+        TL_TRY(launch_live(a.targets, a.tokens, const_cast<int32_t*>(idx), const_cast<int32_t*>(count), nullptr, nullptr, s));
     }
-    const SavedPlan sv(a.tokens, a.vocab, a.dtype);
     const size_t vp = sh.vp, dz_part = static_cast<size_t>(pl.chunk) * vp;
     uint16_t* dz = a.grad_hidden ? reinterpret_cast<uint16_t*>(ws + pl.dz) : nullptr;
     uint16_t* dzt = a.grad_head ? reinterpret_cast<uint16_t*>(ws + pl.dzt) : nullptr;
     for (int c = 0; c < pl.chunks; ++c) {
         const Live live{idx, count, static_cast<int32_t>(c * pl.chunk), static_cast<int32_t>(pl.chunk)};
-        const char* saved = static_cast<const char*>(a.saved);
+        PrepareArgs p{};
+        const int col_tiles = static_cast<int>(ceil_div(sh.cols, 64));
+        if (a.grad_hidden && c == 0) {
+            p.head = {a.head, static_cast<size_t>(a.ld_head), sh.vocab, sh.cols, 0, {}, reinterpret_cast<uint16_t*>(ws + pl.head_t),
+                      vp, vp * sh.cols};
+            p.head_rows = static_cast<int>(ceil_div(sh.vocab, 64));
+            p.head_blocks = p.head_rows * col_tiles;
+            p.targets = a.targets;
+            p.tokens = a.tokens;
+            p.cols = sh.cols;
+            p.zero = a.grad_hidden;
+            p.zero_ld = a.ld_grad_hidden;
+            p.zero_blocks = static_cast<int>(std::min<int64_t>(ceil_div(a.tokens, 4), 4 * CUS));
+        }
+        if (a.grad_head) {
+            p.hidden = {a.hidden, static_cast<size_t>(a.ld_hidden), pl.chunk, sh.cols, 1, live,
+                        reinterpret_cast<uint16_t*>(ws + pl.hidden_t), static_cast<size_t>(pl.chunk),
+                        static_cast<size_t>(pl.chunk) * sh.cols};
+            p.hidden_rows = static_cast<int>(pl.chunk / 64);
+            p.hidden_blocks = p.hidden_rows * col_tiles;
+        }
+        const int prepare = p.head_blocks + p.hidden_blocks + p.zero_blocks;
+        if (prepare > 0) {
+            if (sh.parts == 1) hipLaunchKernelGGL((prepare_kernel<uint16_t, 1>), dim3(prepare), dim3(256), 0, s, p);
+            else hipLaunchKernelGGL((prepare_kernel<float, 3>), dim3(prepare), dim3(256), 0, s, p);
+            TL_TRY(hipGetLastError());
+        }
         if (saved) {
             const DzArgs d{saved + sv.e, reinterpret_cast<const float*>(saved + sv.m),
-                           reinterpret_cast<const float*>(saved + sv.logp), static_cast<size_t>(sh.tp), live,
+                           reinterpret_cast<const float*>(saved + sv.logp), static_cast<size_t>(sh.tp), sh.edge, live,
                            a.targets, a.lse, a.grad_logp, a.scale, static_cast<int>(a.vocab), vp,
                            static_cast<size_t>(pl.chunk), dz, dzt, dz_part, dz_part};
             const dim3 grid(static_cast<unsigned>(vp / 64), static_cast<unsigned>(pl.chunk / 64));
@@ -1077,7 +1165,7 @@ hipError_t launch_token_logp_backward(const muon_token_logp_backward_args& a, vo
             l.live = live;
             TL_TRY(logits_operands(sh, a.hidden, a.ld_hidden, a.head, a.ld_head, a.dtype, ws + pl.hidden, ws + pl.head, c == 0, l, s));
             l.targets = a.targets;
-            l.tb = static_cast<int>(pl.chunk / pt::TILE);
+            l.tb = static_cast<int>(pl.chunk / sh.edge);
             l.scale2 = a.scale * LOG2E;
             l.scale = a.scale;
             l.lse = a.lse;
@@ -1087,50 +1175,37 @@ hipError_t launch_token_logp_backward(const muon_token_logp_backward_args& a, vo
             l.dz_part = l.dzt_part = dz_part;
             l.vp = vp;
             l.rows_pitch = pl.chunk;
-            TL_TRY(launch_logits<LG_DZ>(l, sh.parts, s));
+            TL_TRY(launch_logits<LG_DZ>(l, sh.edge, sh.parts, s));
         }
+        GradArgs g{};
+        g.live = live;
+        g.cols = static_cast<int>(sh.cols);
         if (a.grad_hidden) {
-            GradArgs g{};
             g.a = ws + pl.head_t;
             g.a_ld = 2 * vp;
             g.a_part = 2 * vp * sh.cols;
             g.b = reinterpret_cast<const char*>(dz);
             g.b_ld = 2 * vp;
             g.b_part = 2 * dz_part;
-            g.live = live;
-            g.cols = static_cast<int>(sh.cols);
             g.by_token = 1;
             g.steps = static_cast<int>(ceil_div(sh.vocab, pt::KS));
-            g.ta = pl.gh.ta;
-            g.tb = pl.gh.tb;
-            g.splits = pl.gh.splits;
             g.out = a.grad_hidden;
             g.ld = a.ld_grad_hidden;
-            g.slab = pl.gh.slab ? reinterpret_cast<float*>(ws + pl.slab) : nullptr;
-            TL_TRY(launch_grad(g, sh.parts, a.dtype, true, s));
+            TL_TRY(launch_grad(g, pl.gh, reinterpret_cast<float*>(ws + pl.slab), sh.parts, a.dtype, true, s));
         }
         if (a.grad_head) {
-            TL_TRY(launch_pack_transposed({a.hidden, static_cast<size_t>(a.ld_hidden), pl.chunk, sh.cols, 1, live,
-                                           reinterpret_cast<uint16_t*>(ws + pl.hidden_t), static_cast<size_t>(pl.chunk),
-                                           static_cast<size_t>(pl.chunk) * sh.cols}, a.dtype, s));
-            GradArgs g{};
             g.a = ws + pl.hidden_t;
             g.a_ld = 2 * static_cast<size_t>(pl.chunk);
             g.a_part = g.a_ld * sh.cols;
             g.b = reinterpret_cast<const char*>(dzt);
             g.b_ld = g.a_ld;
             g.b_part = 2 * dz_part;
-            g.live = live;
-            g.cols = static_cast<int>(sh.cols);
+            g.by_token = 0;
             g.rows = static_cast<int>(sh.vocab);
-            g.ta = pl.gw.ta;
-            g.tb = pl.gw.tb;
-            g.splits = pl.gw.splits;
             g.out = a.grad_head;
             g.ld = a.ld_grad_head;
-            g.slab = pl.gw.slab ? reinterpret_cast<float*>(ws + pl.slab_w) : nullptr;
             g.add = c > 0;
-            TL_TRY(launch_grad(g, sh.parts, a.dtype, c + 1 == pl.chunks, s));
+            TL_TRY(launch_grad(g, pl.gw, reinterpret_cast<float*>(ws + pl.slab_w), sh.parts, a.dtype, c + 1 == pl.chunks, s));
         }
     }
     return hipSuccess;

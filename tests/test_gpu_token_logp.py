@@ -271,3 +271,43 @@ def test_token_logp_in_a_graph_and_on_another_stream(gpu_lib):
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(want, got))
         h, w, y, c = _inputs(10, 300, 256, 1111, "bf16")
+
+
+# products with enough 256 x 256 tiles for the chip (the shapes above take the smaller tile), widths that end inside a k-step
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("t,d,v", [(600, 72, 20000), (520, 1100, 16500), (1500, 136, 8200)])
+def test_token_logp_many_tiles(gpu_lib, t, d, v, dtype):
+    import torch
+    print("[token_logp many tiles]", t, d, v, dtype, flush=True)
+    h, w, y, c = _inputs(21, t, d, v, dtype)
+    saved = _saved(gpu_lib, h, w)
+    logp, lse = _forward(gpu_lib, h, w, y, saved=saved)
+    _check_forward(h, w, y, 1.0, dtype, logp, lse)
+    _check_backward(h, w, y, c, 1.0, dtype, *_backward(gpu_lib, h, w, y, lse, c, saved=saved))
+    plain = _forward(gpu_lib, h, w, y)
+    assert torch.equal(plain[0], logp) and torch.equal(plain[1], lse)
+    _check_backward(h, w, y, c, 1.0, dtype, *_backward(gpu_lib, h, w, y, lse, c))
+
+
+@pytest.mark.parametrize("use_saved", [True, False])
+def test_token_logp_tokens_in_chunks(gpu_lib, use_saved):
+    # dz of 6000 tokens x 65536 entries in fp32 is beyond what the backward pass forms at once, so the tokens go in
+    # two chunks whose grad_head adds up; against fp64 on the GPU, by norms: every gradient entry is a sum whose terms
+    # are within a few 2^-21 of exact, and 1e-5 is forty times that
+    import torch
+    t, d, v = 6000, 32, 65536
+    h, w, y, c = _inputs(22, t, d, v, "f32")
+    saved = _saved(gpu_lib, h, w) if use_saved else None
+    _, lse = _forward(gpu_lib, h, w, y, saved=saved)
+    gh, gw = _backward(gpu_lib, h, w, y, lse, c, saved=saved)
+    H, W = h.double(), w.double()
+    rh, rw = torch.zeros_like(H), torch.zeros_like(W)
+    for rows in torch.nonzero(y >= 0)[:, 0].split(1000):
+        dz = -torch.softmax(H[rows] @ W.T, 1)
+        dz[torch.arange(len(rows), device="cuda"), y[rows]] += 1
+        dz *= c[rows].double()[:, None]
+        rh[rows] = dz @ W
+        rw += dz.T @ H[rows]
+    for got, ref in ((gh, rh), (gw, rw)):
+        assert float((got.double() - ref).norm() / ref.norm()) <= 1e-5
+    assert not gh[y < 0].any()
