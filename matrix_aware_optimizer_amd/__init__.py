@@ -23,6 +23,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Iterable, Sequence
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -134,6 +135,8 @@ class MuonProfile(ctypes.Structure):
     _fields_ = [("ms", ctypes.c_double * MUON_KCLASS_COUNT), ("launches", ctypes.c_int64 * MUON_KCLASS_COUNT)]
 
 
+_WORKSPACE_OPS = ("block_norm_backward", "token_logp", "token_logp_backward", "preference_loss", "policy_loss")
+
 # Every symbol include/muon.h declares, with its ctypes signature.
 SIGNATURES = {
     "muon_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(MuonMatrix), ctypes.c_int32, ctypes.POINTER(MuonHparams)]),
@@ -155,23 +158,12 @@ SIGNATURES = {
     "muon_cayley_step": (ctypes.c_int32, [ctypes.POINTER(MuonCayleyMatrix), ctypes.c_int32,
                                           ctypes.POINTER(MuonCayleyHparams), ctypes.c_void_p, ctypes.c_size_t,
                                           ctypes.c_void_p]),
-    "muon_block_norm": (ctypes.c_int32, [ctypes.POINTER(MuonBlockNormArgs), ctypes.c_void_p]),
-    "muon_block_norm_backward_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(MuonBlockNormBackwardArgs)]),
-    "muon_block_norm_backward": (ctypes.c_int32, [ctypes.POINTER(MuonBlockNormBackwardArgs), ctypes.c_void_p,
-                                                  ctypes.c_size_t, ctypes.c_void_p]),
-    "muon_token_logp_saved_bytes": (ctypes.c_size_t, [ctypes.POINTER(MuonTokenLogpArgs)]),
-    "muon_token_logp_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(MuonTokenLogpArgs)]),
-    "muon_token_logp": (ctypes.c_int32, [ctypes.POINTER(MuonTokenLogpArgs), ctypes.c_void_p, ctypes.c_size_t,
-                                         ctypes.c_void_p]),
-    "muon_token_logp_backward_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(MuonTokenLogpBackwardArgs)]),
-    "muon_token_logp_backward": (ctypes.c_int32, [ctypes.POINTER(MuonTokenLogpBackwardArgs), ctypes.c_void_p,
-                                                  ctypes.c_size_t, ctypes.c_void_p]),
-    "muon_preference_loss_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(MuonPreferenceArgs)]),
-    "muon_preference_loss": (ctypes.c_int32, [ctypes.POINTER(MuonPreferenceArgs), ctypes.c_void_p, ctypes.c_size_t,
-                                              ctypes.c_void_p]),
-    "muon_policy_loss_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(MuonPolicyArgs)]),
-    "muon_policy_loss": (ctypes.c_int32, [ctypes.POINTER(MuonPolicyArgs), ctypes.c_void_p, ctypes.c_size_t,
-                                          ctypes.c_void_p]),
+    # the operators' arguments are one struct, by address (a ctypes instance or packed bytes)
+    "muon_block_norm": (ctypes.c_int32, [ctypes.c_void_p, ctypes.c_void_p]),
+    **{f"muon_{op}_workspace_bytes": (ctypes.c_size_t, [ctypes.c_void_p]) for op in _WORKSPACE_OPS},
+    **{f"muon_{op}": (ctypes.c_int32, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p])
+       for op in _WORKSPACE_OPS},
+    "muon_token_logp_saved_bytes": (ctypes.c_size_t, [ctypes.c_void_p]),
     "muon_status_string": (ctypes.c_char_p, [ctypes.c_int32]),
     "muon_last_error_message": (ctypes.c_char_p, []),
     "muon_profile_enable": (ctypes.c_int32, [ctypes.c_int32]),
@@ -522,81 +514,102 @@ def muon_cayley_step(weights, grads, moms, *, lr, beta=0.9, workspace=None, stre
 # --------------------------------------------------------------------------
 # Training operators (norms around a block, token log-probabilities, losses)
 # --------------------------------------------------------------------------
+# These calls come once or more per step, some on a few kilobytes, so the binding keeps its own cost to a few
+# microseconds: arguments go to the library as one packed struct (the layout of the ctypes class of the same name)
+# and the current stream and device come from torch's raw accessors.
+
+def _packer(cls):
+    kinds = {ctypes.c_void_p: "P", ctypes.c_int64: "q", ctypes.c_float: "f", ctypes.c_int32: "i"}
+    return struct.Struct("".join(kinds[t] for _, t in cls._fields_)).pack
+
+
+_pack_norm, _pack_norm_backward = _packer(MuonBlockNormArgs), _packer(MuonBlockNormBackwardArgs)
+_pack_logp, _pack_logp_backward = _packer(MuonTokenLogpArgs), _packer(MuonTokenLogpBackwardArgs)
+_pack_preference, _pack_policy = _packer(MuonPreferenceArgs), _packer(MuonPolicyArgs)
+
 
 def _ptr(t):
-    return None if t is None else t.data_ptr()
+    return 0 if t is None else t.data_ptr()
 
 
-def _same_device(first, *others):
-    """Every tensor on `first`'s device, which has to be the current GPU."""
+def _raw_stream(stream, first, *others):
+    """The stream to launch on; every tensor has to be on ``first``'s device, the current GPU."""
     import torch
-    dev = first.device
-    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors must be on the current GPU, got {dev}")
+    dev = first.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors must be on the current GPU, got {first.device}")
     for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors must share one device, got {dev} and {t.device}")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors must share one device, got {first.device} and {t.device}")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
-def _check_rows(t, what, shape, dtype):
-    """A matrix with unit column stride; returns its row pitch in elements."""
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+def _pitch(t, what, shape, dtype):
+    """Row pitch in elements of a matrix that has to have this shape and dtype and unit column stride."""
+    if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{what} must be {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
     pitch, step = t.stride()
-    if shape[1] > 1 and step != 1:
+    rows, cols = shape
+    if step != 1 and cols > 1:
         raise ValueError(f"{what} must have unit column stride")
-    if shape[0] <= 1:
-        return shape[1]
-    if pitch < shape[1]:
+    if rows <= 1:
+        return cols
+    if pitch < cols:
         raise ValueError(f"{what} has overlapping rows")
     return pitch
 
 
-def _check_vector(t, what, n, dtypes):
+def _check_vector(t, what, n, *dtypes):
     if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous vector of {n}, got {tuple(t.shape)}")
     if t.dtype not in dtypes:
         raise ValueError(f"{what} must be one of {dtypes}, got {t.dtype}")
 
 
-def _call(fn, size_fn, args, workspace, device, stream):
-    """Runs one operator with the caller's workspace or one of its own; returns the workspace."""
-    if workspace is None:
-        need = size_fn(ctypes.byref(args))
-        if need == 0:
-            raise MuonError(MUON_ERR_INVALID_ARG, muon_last_error_message())
-        workspace = _workspace_for(int(need), None, device, stream)
-    elif stream is not None:
-        workspace = _workspace_for(0, workspace, device, stream)
-    _check(fn(ctypes.byref(args), ctypes.c_void_p(workspace.data_ptr()),
-              workspace.numel() * workspace.element_size(), _stream_handle(stream)))
-    return workspace
-
-
-def _size(size_fn, args) -> int:
-    need = size_fn(ctypes.byref(args))
+def _size(size_fn, packed) -> int:
+    need = size_fn(packed)
     if need == 0:
         raise MuonError(MUON_ERR_INVALID_ARG, muon_last_error_message())
     return int(need)
 
 
+def _call(fn, size_fn, packed, workspace, device, stream, raw):
+    """Runs one operator with the caller's workspace or one of its own; returns the workspace."""
+    if workspace is None:
+        workspace = _workspace_for(_size(size_fn, packed), None, device, stream)
+    elif stream is not None:
+        workspace = _workspace_for(0, workspace, device, stream)
+    _check(fn(packed, workspace.data_ptr(), workspace.numel() * workspace.element_size(), raw))
+    return workspace
+
+
 def _norm_weights(x, post_weight, gate, pre_weight):
-    """(weight dtype, gate kind, gate pitch) of the norm's weights, checked against x."""
+    """(weight dtype code, gate kind, gate pitch) of the norm's weights, checked against x."""
     if x.dim() != 2:
         raise ValueError(f"x must be 2-D, got shape {tuple(x.shape)}")
     cols = x.shape[1]
-    kind, ld_gate, wdt = GATE_NONE, cols, None
+    kind, ld_gate, dtype = GATE_NONE, cols, None
+    if post_weight is not None:
+        dtype = post_weight.dtype
+        _check_vector(post_weight, "post_weight", cols, dtype)
     if gate is not None:
-        kind = GATE_CHANNEL if gate.dim() == 1 else GATE_FULL
-        if kind == GATE_FULL:
-            ld_gate = _check_rows(gate, "gate", x.shape, x.dtype)
-    for w, what in ((post_weight, "post_weight"), (gate if kind == GATE_CHANNEL else None, "gate"),
-                    (pre_weight, "pre_weight")):
-        if w is None:
-            continue
-        wdt = w.dtype if wdt is None else wdt
-        _check_vector(w, what, cols, (wdt,))
-    return (_dtype_code(x) if wdt is None else _dtype_code(wdt)), kind, ld_gate
+        if gate.dim() == 1:
+            kind = GATE_CHANNEL
+            dtype = dtype or gate.dtype
+            _check_vector(gate, "gate", cols, dtype)
+        else:
+            kind = GATE_FULL
+            ld_gate = _pitch(gate, "gate", x.shape, x.dtype)
+    if pre_weight is not None:
+        dtype = dtype or pre_weight.dtype
+        _check_vector(pre_weight, "pre_weight", cols, dtype)
+    return _dtype_code(x if dtype is None else dtype), kind, ld_gate
+
+
+def _check_rstd(rstd, rows):
+    import torch
+    if rstd.dtype != torch.float32 or rstd.shape != (2, rows) or not rstd.is_contiguous():
+        raise ValueError(f"rstd must be contiguous float32 of shape (2, {rows})")
 
 
 def muon_block_norm(x, residual, out_residual, out_norm=None, *, post_weight=None, gate=None, pre_weight=None,
@@ -609,20 +622,19 @@ def muon_block_norm(x, residual, out_residual, out_norm=None, *, post_weight=Non
     ``out_norm`` and ``pre_weight`` go together.  ``out_residual`` may be ``residual`` itself.  ``rstd`` (float32,
     2 x rows) keeps the two inverse rms for :func:`muon_block_norm_backward`.
     """
-    import torch
     wdt, kind, ld_gate = _norm_weights(x, post_weight, gate, pre_weight)
-    rows, cols = x.shape
-    if rstd is not None and (rstd.dtype != torch.float32 or rstd.shape != (2, rows) or not rstd.is_contiguous()):
-        raise ValueError(f"rstd must be contiguous float32 of shape (2, {rows})")
-    args = MuonBlockNormArgs(
+    shape, dtype = x.shape, x.dtype
+    rows, cols = shape
+    if rstd is not None:
+        _check_rstd(rstd, rows)
+    packed = _pack_norm(
         x.data_ptr(), residual.data_ptr(), _ptr(post_weight), _ptr(gate), _ptr(pre_weight), out_residual.data_ptr(),
-        _ptr(out_norm), _ptr(rstd), rows, cols, _check_rows(x, "x", x.shape, x.dtype),
-        _check_rows(residual, "residual", x.shape, x.dtype), ld_gate,
-        _check_rows(out_residual, "out_residual", x.shape, x.dtype),
-        cols if out_norm is None else _check_rows(out_norm, "out_norm", x.shape, x.dtype),
-        residual_scale, eps, _dtype_code(x), wdt, kind)
-    _same_device(x, residual, post_weight, gate, pre_weight, out_residual, out_norm, rstd)
-    _check(load().muon_block_norm(ctypes.byref(args), _stream_handle(stream)))
+        _ptr(out_norm), _ptr(rstd), rows, cols, _pitch(x, "x", shape, dtype),
+        _pitch(residual, "residual", shape, dtype), ld_gate, _pitch(out_residual, "out_residual", shape, dtype),
+        cols if out_norm is None else _pitch(out_norm, "out_norm", shape, dtype), residual_scale, eps, _dtype_code(x),
+        wdt, kind)
+    raw = _raw_stream(stream, x, residual, post_weight, gate, pre_weight, out_residual, out_norm, rstd)
+    _check(load().muon_block_norm(packed, raw))
 
 
 def muon_block_norm_backward_workspace_bytes(x, *, post_weight=None, gate=None, pre_weight=None) -> int:
@@ -633,12 +645,12 @@ def muon_block_norm_backward_workspace_bytes(x, *, post_weight=None, gate=None, 
     at = iter(range(1 << 44, 1 << 62, 1 << 44))
 
     def some(t=x):
-        return None if t is None else next(at)
-    args = MuonBlockNormBackwardArgs(
-        some(), some(), some(), some() if pre_weight is not None else None, some(), some(post_weight), some(gate),
+        return 0 if t is None else next(at)
+    packed = _pack_norm_backward(
+        some(), some(), some(), some() if pre_weight is not None else 0, some(), some(post_weight), some(gate),
         some(pre_weight), some(), some(), some(post_weight), some(gate), some(pre_weight), rows, cols,
         cols, cols, cols, cols, cols, cols, cols, cols, 1.0, _dtype_code(x), wdt, kind)
-    return _size(load().muon_block_norm_backward_workspace_bytes, args)
+    return _size(load().muon_block_norm_backward_workspace_bytes, packed)
 
 
 def muon_block_norm_backward(x, out_residual, rstd, grad_norm, grad_x, grad_residual, *, grad_out_residual=None,
@@ -650,23 +662,20 @@ def muon_block_norm_backward(x, out_residual, rstd, grad_norm, grad_x, grad_resi
     ``out_residual`` and ``rstd`` are what it wrote.  ``grad_residual`` may be ``grad_out_residual`` itself.
     Weight gradients are summed over the rows.
     """
-    import torch
     wdt, kind, ld_gate = _norm_weights(x, post_weight, gate, pre_weight)
-    rows, cols = x.shape
-    if rstd.dtype != torch.float32 or rstd.shape != (2, rows) or not rstd.is_contiguous():
-        raise ValueError(f"rstd must be contiguous float32 of shape (2, {rows})")
+    shape, dtype = x.shape, x.dtype
+    rows, cols = shape
+    _check_rstd(rstd, rows)
     for w, g, what in ((post_weight, grad_post_weight, "post_weight"), (pre_weight, grad_pre_weight, "pre_weight"),
                        (gate, grad_gate, "gate")):
         if (w is None) != (g is None):
             raise ValueError(f"{what} and its gradient go together")
-        if g is not None and g.dim() == 1:
-            _check_vector(g, f"gradient of {what}", cols, (w.dtype,))
-            if w.dim() != 1:
-                raise ValueError(f"gradient of {what} must have its shape")
+        if g is not None and w.dim() == 1:
+            _check_vector(g, f"gradient of {what}", cols, w.dtype)
 
     def pitch(t, what):
-        return cols if t is None else _check_rows(t, what, x.shape, x.dtype)
-    args = MuonBlockNormBackwardArgs(
+        return cols if t is None else _pitch(t, what, shape, dtype)
+    packed = _pack_norm_backward(
         x.data_ptr(), out_residual.data_ptr(), rstd.data_ptr(), _ptr(grad_norm), _ptr(grad_out_residual),
         _ptr(post_weight), _ptr(gate), _ptr(pre_weight), grad_x.data_ptr(), grad_residual.data_ptr(),
         _ptr(grad_post_weight), _ptr(grad_gate), _ptr(grad_pre_weight), rows, cols, pitch(x, "x"),
@@ -674,40 +683,48 @@ def muon_block_norm_backward(x, out_residual, rstd, grad_norm, grad_x, grad_resi
         pitch(grad_out_residual, "grad_out_residual"), ld_gate, pitch(grad_x, "grad_x"),
         pitch(grad_residual, "grad_residual"), pitch(grad_gate, "grad_gate") if kind == GATE_FULL else cols,
         residual_scale, _dtype_code(x), wdt, kind)
-    _same_device(x, out_residual, rstd, grad_norm, grad_out_residual, post_weight, gate, pre_weight, grad_x,
-                 grad_residual, grad_post_weight, grad_gate, grad_pre_weight, workspace)
+    raw = _raw_stream(stream, x, out_residual, rstd, grad_norm, grad_out_residual, post_weight, gate, pre_weight,
+                      grad_x, grad_residual, grad_post_weight, grad_gate, grad_pre_weight, workspace)
     lib = load()
-    return _call(lib.muon_block_norm_backward, lib.muon_block_norm_backward_workspace_bytes, args, workspace, x.device,
-                 stream)
+    return _call(lib.muon_block_norm_backward, lib.muon_block_norm_backward_workspace_bytes, packed, workspace,
+                 x.device, stream, raw)
 
 
 def _logp_shape(hidden, head):
-    if hidden.dim() != 2 or head.dim() != 2 or hidden.shape[1] != head.shape[1] or hidden.dtype != head.dtype:
-        raise ValueError(f"hidden {tuple(hidden.shape)} {hidden.dtype} and head {tuple(head.shape)} {head.dtype} "
+    """(tokens, cols, vocab, pitch of hidden, pitch of head, dtype code)."""
+    dtype = hidden.dtype
+    if hidden.dim() != 2 or head.dim() != 2 or hidden.shape[1] != head.shape[1] or head.dtype != dtype:
+        raise ValueError(f"hidden {tuple(hidden.shape)} {dtype} and head {tuple(head.shape)} {head.dtype} "
                          "must be matrices of one dtype and width")
-    return hidden.shape[0], hidden.shape[1], head.shape[0]
+    tokens, cols = hidden.shape
+    return (tokens, cols, head.shape[0], _pitch(hidden, "hidden", hidden.shape, dtype),
+            _pitch(head, "head", head.shape, dtype), _dtype_code(dtype))
 
 
-def _logp_sizes(hidden, head):
-    tokens, cols, vocab = _logp_shape(hidden, head)
-    # sizes only: stand-in addresses, never dereferenced
+def _logp_stand_ins(hidden, head):
+    """Stand-in addresses for calls that ask for sizes, never dereferenced; aligned like the operands."""
     at = [k << 44 for k in range(1, 9)]
-    return tokens, cols, vocab, at
+    return [at[0] + hidden.data_ptr() % 256, at[1] + head.data_ptr() % 256] + at[2:]
 
 
 def muon_token_logp_saved_bytes(hidden, head) -> int:
     """Bytes of the ``saved`` buffer that :func:`muon_token_logp` can keep for the backward pass."""
-    tokens, cols, vocab, at = _logp_sizes(hidden, head)
-    args = MuonTokenLogpArgs(*at[:5], None, tokens, cols, vocab, cols, cols, 1.0, _dtype_code(hidden))
-    return _size(load().muon_token_logp_saved_bytes, args)
+    tokens, cols, vocab, ldh, ldw, code = _logp_shape(hidden, head)
+    return _size(load().muon_token_logp_saved_bytes,
+                 _pack_logp(*_logp_stand_ins(hidden, head)[:5], 0, tokens, cols, vocab, ldh, ldw, 1.0, code))
 
 
 def muon_token_logp_workspace_bytes(hidden, head) -> int:
-    tokens, cols, vocab, at = _logp_sizes(hidden, head)
-    args = MuonTokenLogpArgs(*at[:5], None, tokens, cols, vocab, _check_rows(hidden, "hidden", hidden.shape, hidden.dtype),
-                             _check_rows(head, "head", head.shape, head.dtype), 1.0, _dtype_code(hidden))
-    args.hidden, args.head = hidden.data_ptr() % 256 + at[0], head.data_ptr() % 256 + at[1]
-    return _size(load().muon_token_logp_workspace_bytes, args)
+    tokens, cols, vocab, ldh, ldw, code = _logp_shape(hidden, head)
+    return _size(load().muon_token_logp_workspace_bytes,
+                 _pack_logp(*_logp_stand_ins(hidden, head)[:5], 0, tokens, cols, vocab, ldh, ldw, 1.0, code))
+
+
+def _check_saved(lib, saved, packed):
+    if saved is not None:
+        need, have = lib.muon_token_logp_saved_bytes(packed), saved.numel() * saved.element_size()
+        if have < need:
+            raise MuonError(MUON_ERR_WORKSPACE, f"saved has {have} bytes, {need} needed")
 
 
 def muon_token_logp(hidden, head, targets, logp, lse, *, scale=1.0, saved=None, workspace=None, stream=None):
@@ -718,34 +735,24 @@ def muon_token_logp(hidden, head, targets, logp, lse, *, scale=1.0, saved=None, 
     :func:`muon_token_logp_saved_bytes`) keeps what spares the backward pass the logits' product.
     """
     import torch
-    tokens, cols, vocab = _logp_shape(hidden, head)
-    _check_vector(targets, "targets", tokens, (torch.int64,))
-    _check_vector(logp, "logp", tokens, (torch.float32,))
-    _check_vector(lse, "lse", tokens, (torch.float32,))
-    args = MuonTokenLogpArgs(hidden.data_ptr(), head.data_ptr(), targets.data_ptr(), logp.data_ptr(), lse.data_ptr(),
-                             _ptr(saved), tokens, cols, vocab, _check_rows(hidden, "hidden", hidden.shape, hidden.dtype),
-                             _check_rows(head, "head", head.shape, head.dtype), scale, _dtype_code(hidden))
-    _same_device(head, hidden, targets, logp, lse, saved, workspace)
+    tokens, cols, vocab, ldh, ldw, code = _logp_shape(hidden, head)
+    _check_vector(targets, "targets", tokens, torch.int64)
+    _check_vector(logp, "logp", tokens, torch.float32)
+    _check_vector(lse, "lse", tokens, torch.float32)
+    packed = _pack_logp(hidden.data_ptr(), head.data_ptr(), targets.data_ptr(), logp.data_ptr(), lse.data_ptr(),
+                        _ptr(saved), tokens, cols, vocab, ldh, ldw, scale, code)
+    raw = _raw_stream(stream, head, hidden, targets, logp, lse, saved, workspace)
     lib = load()
-    _check_saved(lib, args, saved)
-    return _call(lib.muon_token_logp, lib.muon_token_logp_workspace_bytes, args, workspace, head.device, stream)
-
-
-def _check_saved(lib, args, saved):
-    if saved is not None:
-        need = lib.muon_token_logp_saved_bytes(ctypes.byref(args))
-        if saved.numel() * saved.element_size() < need:
-            raise MuonError(MUON_ERR_WORKSPACE, f"saved has {saved.numel() * saved.element_size()} bytes, {need} needed")
+    _check_saved(lib, saved, packed)
+    return _call(lib.muon_token_logp, lib.muon_token_logp_workspace_bytes, packed, workspace, head.device, stream, raw)
 
 
 def muon_token_logp_backward_workspace_bytes(hidden, head, *, use_saved=False) -> int:
-    tokens, cols, vocab, at = _logp_sizes(hidden, head)
-    args = MuonTokenLogpBackwardArgs(*at[:5], at[5] if use_saved else None, at[6], at[7], tokens, cols, vocab,
-                                     _check_rows(hidden, "hidden", hidden.shape, hidden.dtype),
-                                     _check_rows(head, "head", head.shape, head.dtype), cols, cols, 1.0,
-                                     _dtype_code(hidden))
-    args.hidden, args.head = hidden.data_ptr() % 256 + at[0], head.data_ptr() % 256 + at[1]
-    return _size(load().muon_token_logp_backward_workspace_bytes, args)
+    tokens, cols, vocab, ldh, ldw, code = _logp_shape(hidden, head)
+    at = _logp_stand_ins(hidden, head)
+    return _size(load().muon_token_logp_backward_workspace_bytes,
+                 _pack_logp_backward(*at[:5], at[5] if use_saved else 0, at[6], at[7], tokens, cols, vocab, ldh, ldw,
+                                     cols, cols, 1.0, code))
 
 
 def muon_token_logp_backward(hidden, head, targets, lse, grad_logp, grad_hidden=None, grad_head=None, *, scale=1.0,
@@ -756,40 +763,40 @@ def muon_token_logp_backward(hidden, head, targets, lse, grad_logp, grad_hidden=
     buffer that the forward call filled for the same inputs, or None: then the logits are formed again.
     """
     import torch
-    tokens, cols, vocab = _logp_shape(hidden, head)
-    _check_vector(targets, "targets", tokens, (torch.int64,))
-    _check_vector(lse, "lse", tokens, (torch.float32,))
-    _check_vector(grad_logp, "grad_logp", tokens, (torch.float32,))
-    args = MuonTokenLogpBackwardArgs(
+    tokens, cols, vocab, ldh, ldw, code = _logp_shape(hidden, head)
+    _check_vector(targets, "targets", tokens, torch.int64)
+    _check_vector(lse, "lse", tokens, torch.float32)
+    _check_vector(grad_logp, "grad_logp", tokens, torch.float32)
+    packed = _pack_logp_backward(
         hidden.data_ptr(), head.data_ptr(), targets.data_ptr(), lse.data_ptr(), grad_logp.data_ptr(), _ptr(saved),
-        _ptr(grad_hidden), _ptr(grad_head), tokens, cols, vocab,
-        _check_rows(hidden, "hidden", hidden.shape, hidden.dtype), _check_rows(head, "head", head.shape, head.dtype),
-        cols if grad_hidden is None else _check_rows(grad_hidden, "grad_hidden", hidden.shape, hidden.dtype),
-        cols if grad_head is None else _check_rows(grad_head, "grad_head", head.shape, head.dtype),
-        scale, _dtype_code(hidden))
-    _same_device(head, hidden, targets, lse, grad_logp, saved, grad_hidden, grad_head, workspace)
+        _ptr(grad_hidden), _ptr(grad_head), tokens, cols, vocab, ldh, ldw,
+        cols if grad_hidden is None else _pitch(grad_hidden, "grad_hidden", hidden.shape, hidden.dtype),
+        cols if grad_head is None else _pitch(grad_head, "grad_head", head.shape, head.dtype), scale, code)
+    raw = _raw_stream(stream, head, hidden, targets, lse, grad_logp, saved, grad_hidden, grad_head, workspace)
     lib = load()
-    _check_saved(lib, MuonTokenLogpArgs(None, None, None, None, None, None, tokens, cols, vocab, cols, cols, scale,
-                                        args.dtype), saved)
-    return _call(lib.muon_token_logp_backward, lib.muon_token_logp_backward_workspace_bytes, args, workspace,
-                 head.device, stream)
+    if saved is not None:
+        _check_saved(lib, saved, _pack_logp(0, 0, 0, 0, 0, 0, tokens, cols, vocab, cols, cols, scale, code))
+    return _call(lib.muon_token_logp_backward, lib.muon_token_logp_backward_workspace_bytes, packed, workspace,
+                 head.device, stream, raw)
 
 
 def _loss_inputs(logp, offsets, mask, loss, grad_logp, *same):
-    """Checks shared by the losses; returns (tokens, sequences)."""
+    """Checks shared by the losses; returns (tokens, sequences, dtype code)."""
     import torch
     n, dt = logp.shape[0] if logp.dim() == 1 else -1, logp.dtype
-    _check_vector(logp, "logp", n, (torch.float32, torch.bfloat16))
-    for t, what in same + ((grad_logp, "grad_logp"),):
+    _check_vector(logp, "logp", n, torch.float32, torch.bfloat16)
+    for t, what in same:
         if t is not None:
-            _check_vector(t, what, n, (dt,))
+            _check_vector(t, what, n, dt)
+    if grad_logp is not None:
+        _check_vector(grad_logp, "grad_logp", n, dt)
     if mask is not None:
-        _check_vector(mask, "mask", n, (torch.uint8, torch.bool))
-    if offsets.dim() != 1 or offsets.numel() < 1 or offsets.dtype != torch.int64 or not offsets.is_contiguous():
+        _check_vector(mask, "mask", n, torch.uint8, torch.bool)
+    if offsets.dim() != 1 or offsets.shape[0] < 1 or offsets.dtype != torch.int64 or not offsets.is_contiguous():
         raise ValueError("offsets must be a contiguous int64 vector of sequences + 1")
     if loss is not None and (loss.numel() != 1 or loss.dtype != torch.float32):
         raise ValueError("loss must be one float32")
-    return n, offsets.shape[0] - 1
+    return n, offsets.shape[0] - 1, _dtype_code(dt)
 
 
 def _choice(table, value, what):
@@ -799,11 +806,9 @@ def _choice(table, value, what):
 
 
 def muon_preference_loss_workspace_bytes(logp, offsets) -> int:
-    n, sequences = _loss_inputs(logp, offsets, None, None, None)
-    at = [k << 44 for k in range(1, 5)]
-    args = MuonPreferenceArgs(at[0], None, None, at[1], at[2], None, at[3], n, sequences, 1.0, 0.0, 0.0, 1.0, 0, 0,
-                              _dtype_code(logp))
-    return _size(load().muon_preference_loss_workspace_bytes, args)
+    n, sequences, code = _loss_inputs(logp, offsets, None, None, None)
+    return _size(load().muon_preference_loss_workspace_bytes,
+                 _pack_preference(1 << 44, 0, 0, 2 << 44, 3 << 44, 0, 4 << 44, n, sequences, 1.0, 0.0, 0.0, 1.0, 0, 0, code))
 
 
 def muon_preference_loss(logp, offsets, loss, grad_logp=None, *, ref_logp=None, mask=None, beta=0.1, kind="sigmoid",
@@ -817,24 +822,23 @@ def muon_preference_loss(logp, offsets, loss, grad_logp=None, *, ref_logp=None, 
     ``beta`` times the log ratios.  ``grad_logp`` is scaled by ``grad_scale``.
     """
     import torch
-    n, sequences = _loss_inputs(logp, offsets, mask, loss, grad_logp, (ref_logp, "ref_logp"))
+    n, sequences, code = _loss_inputs(logp, offsets, mask, loss, grad_logp, (ref_logp, "ref_logp"))
     if rewards is not None:
-        _check_vector(rewards, "rewards", sequences, (torch.float32,))
-    args = MuonPreferenceArgs(logp.data_ptr(), _ptr(ref_logp), _ptr(mask), offsets.data_ptr(), loss.data_ptr(),
+        _check_vector(rewards, "rewards", sequences, torch.float32)
+    packed = _pack_preference(logp.data_ptr(), _ptr(ref_logp), _ptr(mask), offsets.data_ptr(), loss.data_ptr(),
                               _ptr(rewards), _ptr(grad_logp), n, sequences, beta, margin, label_smoothing, grad_scale,
-                              _choice(PREFERENCE_KINDS, kind, "kind"), 1 if average else 0, _dtype_code(logp))
-    _same_device(offsets, logp, ref_logp, mask, loss, rewards, grad_logp, workspace)
+                              _choice(PREFERENCE_KINDS, kind, "kind"), 1 if average else 0, code)
+    raw = _raw_stream(stream, offsets, logp, ref_logp, mask, loss, rewards, grad_logp, workspace)
     lib = load()
-    return _call(lib.muon_preference_loss, lib.muon_preference_loss_workspace_bytes, args, workspace, offsets.device,
-                 stream)
+    return _call(lib.muon_preference_loss, lib.muon_preference_loss_workspace_bytes, packed, workspace, offsets.device,
+                 stream, raw)
 
 
 def muon_policy_loss_workspace_bytes(logp, offsets) -> int:
-    n, sequences = _loss_inputs(logp, offsets, None, None, None)
-    at = [k << 44 for k in range(1, 7)]
-    args = MuonPolicyArgs(at[0], at[1], None, at[2], None, at[3], at[4], None, at[5], n, sequences, 0.2, 0.2, 0.0, 0.0,
-                          1.0, 0, 0, 0, _dtype_code(logp))
-    return _size(load().muon_policy_loss_workspace_bytes, args)
+    n, sequences, code = _loss_inputs(logp, offsets, None, None, None)
+    return _size(load().muon_policy_loss_workspace_bytes,
+                 _pack_policy(1 << 44, 2 << 44, 0, 3 << 44, 0, 4 << 44, 5 << 44, 0, 6 << 44, n, sequences, 0.2, 0.2, 0.0,
+                              0.0, 1.0, 0, 0, 0, code))
 
 
 def muon_policy_loss(logp, old_logp, advantages, offsets, loss, grad_logp=None, *, ref_logp=None, mask=None,
@@ -848,18 +852,19 @@ def muon_policy_loss(logp, old_logp, advantages, offsets, loss, grad_logp=None, 
     ``mask`` and ``grad_scale`` are as in :func:`muon_preference_loss`.
     """
     import torch
-    n, sequences = _loss_inputs(logp, offsets, mask, loss, grad_logp, (old_logp, "old_logp"), (ref_logp, "ref_logp"))
-    _check_vector(advantages, "advantages", sequences if per_sequence else n, (torch.float32,))
+    n, sequences, code = _loss_inputs(logp, offsets, mask, loss, grad_logp, (old_logp, "old_logp"),
+                                      (ref_logp, "ref_logp"))
+    _check_vector(advantages, "advantages", sequences if per_sequence else n, torch.float32)
     if stats is not None:
-        _check_vector(stats, "stats", 4, (torch.float32,))
-    args = MuonPolicyArgs(logp.data_ptr(), old_logp.data_ptr(), _ptr(ref_logp), advantages.data_ptr(), _ptr(mask),
+        _check_vector(stats, "stats", 4, torch.float32)
+    packed = _pack_policy(logp.data_ptr(), old_logp.data_ptr(), _ptr(ref_logp), advantages.data_ptr(), _ptr(mask),
                           offsets.data_ptr(), loss.data_ptr(), _ptr(stats), _ptr(grad_logp), n, sequences, clip_low,
                           clip_high, dual_clip, kl_coef, grad_scale, _choice(KL_KINDS, kl, "kl"),
-                          _choice(LOSS_REDUCTIONS, reduction, "reduction"), 1 if per_sequence else 0,
-                          _dtype_code(logp))
-    _same_device(offsets, logp, old_logp, ref_logp, advantages, mask, loss, stats, grad_logp, workspace)
+                          _choice(LOSS_REDUCTIONS, reduction, "reduction"), 1 if per_sequence else 0, code)
+    raw = _raw_stream(stream, offsets, logp, old_logp, ref_logp, advantages, mask, loss, stats, grad_logp, workspace)
     lib = load()
-    return _call(lib.muon_policy_loss, lib.muon_policy_loss_workspace_bytes, args, workspace, offsets.device, stream)
+    return _call(lib.muon_policy_loss, lib.muon_policy_loss_workspace_bytes, packed, workspace, offsets.device, stream,
+                 raw)
 
 
 def muon_profile_enable(on: bool = True):

@@ -92,9 +92,7 @@ template <int NT, int VPT, bool TAIL> struct Cols {
 template <int NT, int NS, int WAVES>
 __device__ __forceinline__ void row_sums(float (&v)[NS], float* red, int turn) {
 #pragma unroll
-    for (int k = 0; k < NS; ++k)
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) v[k] += __shfl_xor(v[k], o, 64);
+    for (int k = 0; k < NS; ++k) v[k] = wave_sum(v[k]);
     if constexpr (NT > 64) {
         float* r = red + (turn & 1) * NS * WAVES;
         const int wave = threadIdx.x >> 6, first = wave / (NT / 64) * (NT / 64);

@@ -14,8 +14,9 @@
 //
 // Preference: units -> pairs (loss terms and each sequence's gradient factor) -> gradient.
 // Policy: the number of counted tokens first (1 byte a token, only with a mask), then loss and
-// gradient in one pass over the rest, then the partial sums.  Up to LS_SMALL tokens all steps run in
-// one workgroup and one launch.
+// gradient in one pass over the rest, then the partial sums.  Up to LS_SMALL tokens all steps run in one
+// workgroup and one launch: a wave keeps its unit's tokens in registers, the offsets and sums sit in LDS, so
+// memory is waited for once before and once after.
 #include <algorithm>
 
 #include "train_internal.h"
@@ -26,16 +27,12 @@ namespace {
 
 constexpr int UNIT = 512, PER = 8;       // tokens of a wave's unit, of a lane
 constexpr int LS_THREADS = 256;          // workgroups of the launches over many units: 4 waves
-constexpr int LS_ONE = 1024;             // the workgroup that does everything: 16 waves
-constexpr int64_t LS_SMALL = 16384;      // tokens up to which it does (two units a wave)
-constexpr int LS_GRID = 1024;            // workgroups of the other launches, at most
+constexpr int LS_ONE = 1024;             // the workgroup that does everything, at most: 16 waves
+constexpr int64_t LS_SMALL = LS_ONE / 64 * UNIT;   // tokens up to which it does: one unit a wave
+constexpr int LS_SMALL_SEQS = 1024;      // sequences up to which it does: their offsets and sums in LDS
+constexpr int LS_GRID = 1280;            // workgroups of the other launches, at most: 5 a CU, what the registers hold
 constexpr int LS_COUNTS = 256;           // workgroups that count, at most: one partial each
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
-    return v;
-}
 __device__ __forceinline__ int lane_id() { return threadIdx.x & 63; }
 
 // Tokens t .. t + 7 of a vector of n, zero past its end.
@@ -76,11 +73,12 @@ __device__ __forceinline__ unsigned load_mask(const uint8_t* mask, int t, int n)
 }
 
 // The sequences, as offsets clamped to the tokens there are (so no offset makes an access stray).
-struct Sequences {
-    const int64_t* offsets;
+// OFF: int64_t as the caller has them, or int where a workgroup keeps them clamped in LDS.
+template <typename OFF> struct Sequences {
+    const OFF* offsets;
     int count, tokens;
     __device__ __forceinline__ int at(int k) const {
-        const int64_t v = offsets[k];
+        const OFF v = offsets[k];
         return static_cast<int>(v < 0 ? 0 : v > tokens ? tokens : v);
     }
     // The last k with at(k) <= t, or -1: 64 probes at a time.
@@ -148,42 +146,46 @@ template <typename V> __device__ __forceinline__ V heads(const UnitSums<V>& q, i
 
 // ---- preference -------------------------------------------------------------
 
-struct PreferenceState {
+template <typename OFF> struct PreferenceState {
     muon_preference_args a;
+    Sequences<OFF> seqs;
     UnitSums<float2> q;     // { sum of counted log ratios, counted tokens }
     float* factor;          // gradient factor by sequence
     float* losses;          // by pair
-    __device__ Sequences seqs() const { return {a.offsets, static_cast<int>(a.sequences), static_cast<int>(a.tokens)}; }
     __device__ int units() const { return static_cast<int>((a.tokens + UNIT - 1) / UNIT); }
 };
 
-template <typename T> __device__ __forceinline__ void preference_units(const PreferenceState& st, int wave, int waves) {
-    const int n = static_cast<int>(st.a.tokens);
-    for (int u = wave; u < st.units(); u += waves) {
-        const int t0 = u * UNIT, t = t0 + PER * lane_id();
-        float lp[PER], ref[PER] = {};
-        load_tokens<T>(st.a.logp, t, n, lp);
-        if (st.a.ref_logp) load_tokens<T>(st.a.ref_logp, t, n, ref);
-        const unsigned live = load_mask(st.a.mask, t, n);
-        st.seqs().pieces(t0, t0 + UNIT, [](int) { return 0.0f; }, [&](int s, int a, int b, int lo, int hi, float) {
-            const unsigned on = live & in_piece(t, a, b);
-            float v = 0.0f;
-#pragma unroll
-            for (int e = 0; e < PER; ++e) v += (on >> e & 1u) ? lp[e] - ref[e] : 0.0f;
-            v = wave_sum(v);
-            const float c = wave_sum(static_cast<float>(__popc(on)));
-            if (lane_id() == 0) st.q.put(s, a, lo, hi, make_float2(v, c));
-        });
+// What a lane reads of its 8 tokens.
+struct PreferenceTokens {
+    float lp[PER], ref[PER] = {};
+    unsigned live;
+    template <typename T> __device__ __forceinline__ void load(const muon_preference_args& a, int t) {
+        const int n = static_cast<int>(a.tokens);
+        load_tokens<T>(a.logp, t, n, lp);
+        if (a.ref_logp) load_tokens<T>(a.ref_logp, t, n, ref);
+        live = load_mask(a.mask, t, n);
     }
+};
+
+template <typename S> __device__ __forceinline__ void preference_unit(const S& st, int u, const PreferenceTokens& k) {
+    const int t0 = u * UNIT, t = t0 + PER * lane_id();
+    st.seqs.pieces(t0, t0 + UNIT, [](int) { return 0.0f; }, [&](int s, int a, int b, int lo, int hi, float) {
+        const unsigned on = k.live & in_piece(t, a, b);
+        float v = 0.0f;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) v += (on >> e & 1u) ? k.lp[e] - k.ref[e] : 0.0f;
+        v = wave_sum(v);
+        const float c = wave_sum(static_cast<float>(__popc(on)));
+        if (lane_id() == 0) st.q.put(s, a, lo, hi, make_float2(v, c));
+    });
 }
 
 // Sum of the sequence that each lane asks for (s < 0: none), short ones lane by lane, long ones by the wave.
-__device__ __forceinline__ float2 lane_sequence_sums(const PreferenceState& st, int s) {
-    const Sequences sq = st.seqs();
+template <typename S> __device__ __forceinline__ float2 lane_sequence_sums(const S& st, int s) {
     int lo = 0, hi = 0;
     if (s >= 0) {
-        lo = sq.at(s);
-        hi = max(sq.at(s + 1), lo);
+        lo = st.seqs.at(s);
+        hi = max(st.seqs.at(s + 1), lo);
     }
     float2 v = {};
     const int u0 = lo / UNIT, u1 = hi > lo ? (hi - 1) / UNIT : u0;
@@ -205,7 +207,8 @@ __device__ __forceinline__ float2 lane_sequence_sums(const PreferenceState& st, 
 __device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x))); }
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 
-__device__ __forceinline__ void preference_pairs(const PreferenceState& st, int wave, int waves) {
+// A pair a lane: its loss term and its sequences' gradient factors.
+template <typename S> __device__ __forceinline__ void preference_pairs(const S& st, int wave, int waves) {
     const muon_preference_args& a = st.a;
     const int pairs = static_cast<int>(a.sequences / 2);
     for (int p0 = wave * 64; p0 < pairs; p0 += waves * 64) {
@@ -241,92 +244,99 @@ __device__ __forceinline__ void preference_pairs(const PreferenceState& st, int 
     }
 }
 
-template <int NT> __device__ __forceinline__ void preference_loss(const PreferenceState& st, float* red) {
+template <typename S> __device__ __forceinline__ void preference_loss(const S& st, float* red) {
     const int pairs = static_cast<int>(st.a.sequences / 2);
     float v = 0.0f;
 #pragma unroll 4
-    for (int p = threadIdx.x; p < pairs; p += NT) v += st.losses[p];
-    v = block_sum<NT>(v, red);
+    for (int p = threadIdx.x; p < pairs; p += blockDim.x) v += st.losses[p];
+    v = block_sum(v, red);
     if (threadIdx.x == 0) *st.a.loss = pairs ? v / static_cast<float>(pairs) : 0.0f;
 }
 
-template <typename T> __device__ __forceinline__ void preference_grad(const PreferenceState& st, int wave, int waves) {
-    const int n = static_cast<int>(st.a.tokens);
-    for (int u = wave; u < st.units(); u += waves) {
-        const int t0 = u * UNIT, t = t0 + PER * lane_id();
-        const unsigned live = load_mask(st.a.mask, t, n);
-        float g[PER] = {};
-        st.seqs().pieces(t0, t0 + UNIT, [&](int s) { return st.factor[s]; }, [&](int, int a, int b, int, int, float f) {
-            const unsigned on = live & in_piece(t, a, b);
+template <typename T, typename S> __device__ __forceinline__ void preference_grad(const S& st, int u, unsigned live) {
+    const int t0 = u * UNIT, t = t0 + PER * lane_id();
+    float g[PER] = {};
+    st.seqs.pieces(t0, t0 + UNIT, [&](int s) { return st.factor[s]; }, [&](int, int a, int b, int, int, float f) {
+        const unsigned on = live & in_piece(t, a, b);
 #pragma unroll
-            for (int e = 0; e < PER; ++e)
-                if (on >> e & 1u) g[e] = f;
-        });
-        store_tokens<T>(st.a.grad_logp, t, n, g);
-    }
+        for (int e = 0; e < PER; ++e)
+            if (on >> e & 1u) g[e] = f;
+    });
+    store_tokens<T>(st.a.grad_logp, t, static_cast<int>(st.a.tokens), g);
 }
+
+__device__ __forceinline__ int wave_index() { return __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6)); }
 
 enum PreferenceStep { PF_UNITS = 0, PF_PAIRS = 1, PF_GRAD = 2 };
 
-template <typename T, int STEP> __global__ __launch_bounds__(LS_THREADS) void preference_kernel(PreferenceState st) {
+template <typename T, int STEP> __global__ __launch_bounds__(LS_THREADS) void preference_kernel(PreferenceState<int64_t> st) {
     __shared__ float red[LS_THREADS / 64];
-    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
     constexpr int W = LS_THREADS / 64;
-    if (STEP == PF_UNITS) preference_units<T>(st, blockIdx.x * W + wave, gridDim.x * W);
-    else if (STEP == PF_PAIRS) preference_pairs(st, blockIdx.x * W + wave, gridDim.x * W);
-    else if (blockIdx.x == 0) preference_loss<LS_THREADS>(st, red);
-    else preference_grad<T>(st, (blockIdx.x - 1) * W + wave, (gridDim.x - 1) * W);
+    if (STEP == PF_UNITS) {
+        for (int u = blockIdx.x * W + wave_index(); u < st.units(); u += gridDim.x * W) {
+            PreferenceTokens k;
+            k.load<T>(st.a, u * UNIT + PER * lane_id());
+            preference_unit(st, u, k);
+        }
+    } else if (STEP == PF_PAIRS) {
+        preference_pairs(st, blockIdx.x * W + wave_index(), gridDim.x * W);
+    } else if (blockIdx.x == 0) {
+        preference_loss(st, red);
+    } else {
+        for (int u = (blockIdx.x - 1) * W + wave_index(); u < st.units(); u += (gridDim.x - 1) * W)
+            preference_grad<T>(st, u, load_mask(st.a.mask, u * UNIT + PER * lane_id(), static_cast<int>(st.a.tokens)));
+    }
 }
 
-template <typename T> __global__ __launch_bounds__(LS_ONE) void preference_one_kernel(PreferenceState st) {
-    __shared__ float red[LS_ONE / 64];
-    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
-    preference_units<T>(st, wave, LS_ONE / 64);
+// Offsets, clamped, into LDS; a barrier follows.
+__device__ __forceinline__ void offsets_to_lds(const int64_t* offsets, int64_t sequences, int64_t tokens, int* lds) {
+    const Sequences<int64_t> sq{offsets, static_cast<int>(sequences), static_cast<int>(tokens)};
+    for (int k = threadIdx.x; k <= sq.count; k += blockDim.x) lds[k] = sq.at(k);
+}
+
+template <typename T> __global__ __launch_bounds__(LS_ONE) void preference_one_kernel(muon_preference_args a) {
+    constexpr int W = LS_ONE / 64;
+    __shared__ float red[W];
+    __shared__ int offsets[LS_SMALL_SEQS + 1];
+    __shared__ float2 head[W], tail[W], own[LS_SMALL_SEQS];
+    __shared__ float factor[LS_SMALL_SEQS], losses[LS_SMALL_SEQS / 2];
+    const int u = wave_index();
+    const PreferenceState<int> st{a, {offsets, static_cast<int>(a.sequences), static_cast<int>(a.tokens)}, {head, tail, own}, factor, losses};
+    PreferenceTokens k;
+    k.load<T>(a, u * UNIT + PER * lane_id());
+    offsets_to_lds(a.offsets, a.sequences, a.tokens, offsets);
     __syncthreads();
-    preference_pairs(st, wave, LS_ONE / 64);
+    if (u < st.units()) preference_unit(st, u, k);
     __syncthreads();
-    preference_loss<LS_ONE>(st, red);
-    if (st.a.grad_logp) preference_grad<T>(st, wave, LS_ONE / 64);
+    preference_pairs(st, u, blockDim.x / 64);
+    __syncthreads();
+    if (a.grad_logp && u < st.units()) preference_grad<T>(st, u, k.live);
+    preference_loss(st, red);
 }
 
 // ---- policy -----------------------------------------------------------------
 
 constexpr int PL_SUMS = 5;   // weighted loss, KL, held, rho, counted tokens
 
-struct PolicyState {
+template <typename OFF> struct PolicyState {
     muon_policy_args a;
+    Sequences<OFF> seqs;
     UnitSums<float> q;      // counted tokens by unit: sequence means with a mask
-    float* counts;          // counted tokens by workgroup of the count: token means with a mask
-    int count_parts;
-    float* sums;            // PL_SUMS by workgroup of the main pass
-    __device__ Sequences seqs() const { return {a.offsets, static_cast<int>(a.sequences), static_cast<int>(a.tokens)}; }
     __device__ int units() const { return static_cast<int>((a.tokens + UNIT - 1) / UNIT); }
     __device__ bool by_sequence() const { return a.reduction == MUON_REDUCE_SEQUENCE; }
+    // Nothing about a token depends on its sequence.
+    __device__ bool flat() const { return !by_sequence() && !a.advantage_per_sequence; }
+    __device__ unsigned covered(int t) const { return seqs.count ? in_piece(t, seqs.at(0), seqs.at(seqs.count)) : 0u; }
 };
 
-// With a mask: the counted tokens of every sequence's units, or of all sequences (one partial a workgroup).
-template <int NT>
-__device__ __forceinline__ void policy_counts(const PolicyState& st, int wave, int waves, int block, float* red) {
-    const int n = static_cast<int>(st.a.tokens);
-    const Sequences sq = st.seqs();
-    float total = 0.0f;
-    const int first = sq.count ? sq.at(0) : n, last = sq.count ? sq.at(sq.count) : n;
-    for (int u = wave; u < st.units(); u += waves) {
-        const int t0 = u * UNIT, t = t0 + PER * lane_id();
-        const unsigned live = load_mask(st.a.mask, t, n);
-        if (!st.by_sequence()) {
-            total += static_cast<float>(__popc(live & in_piece(t, first, last)));
-        } else {
-            sq.pieces(t0, t0 + UNIT, [](int) { return 0.0f; }, [&](int s, int a, int b, int lo, int hi, float) {
-                if (lo >= t0 && hi <= t0 + UNIT) return;   // counted again where it is used
-                const float c = wave_sum(static_cast<float>(__popc(live & in_piece(t, a, b))));
-                if (lane_id() == 0) st.q.put(s, a, lo, hi, c);
-            });
-        }
-    }
-    if (st.by_sequence()) return;
-    total = block_sum<NT>(total, red);
-    if (threadIdx.x == 0) st.counts[block] = total;
+// Counted tokens of a unit's sequences that go on beyond it (the others are counted where they are used).
+template <typename S> __device__ __forceinline__ void policy_unit_counts(const S& st, int u, unsigned live) {
+    const int t0 = u * UNIT, t = t0 + PER * lane_id();
+    st.seqs.pieces(t0, t0 + UNIT, [](int) { return 0.0f; }, [&](int s, int a, int b, int lo, int hi, float) {
+        if (lo >= t0 && hi <= t0 + UNIT) return;
+        const float c = wave_sum(static_cast<float>(__popc(live & in_piece(t, a, b))));
+        if (lane_id() == 0) st.q.put(s, a, lo, hi, c);
+    });
 }
 
 struct PolicyToken { float loss, grad, kl, held, rho; };
@@ -357,130 +367,187 @@ __device__ __forceinline__ PolicyToken policy_token(const muon_policy_args& a, f
     return o;
 }
 
-template <typename T, int NT>
-__device__ __forceinline__ void policy_main(const PolicyState& st, int wave, int waves, int block, float* red) {
-    const muon_policy_args& a = st.a;
-    const int n = static_cast<int>(a.tokens);
-    const Sequences sq = st.seqs();
-    float every = 0.0f;   // token mean: the weight of a token
-    if (!st.by_sequence()) {
-        float total;
-        if (a.mask) {
-            float c = 0.0f;
-            for (int k = lane_id(); k < st.count_parts; k += 64) c += st.counts[k];
-            total = wave_sum(c);
-        } else {
-            total = sq.count ? static_cast<float>(max(sq.at(sq.count) - sq.at(0), 0)) : 0.0f;
-        }
-        every = 1.0f / fmaxf(total, 1.0f);
-    }
-    float v[PL_SUMS] = {};
-    for (int u = wave; u < st.units(); u += waves) {
-        const int t0 = u * UNIT, t = t0 + PER * lane_id();
-        float lp[PER], old[PER], ref[PER] = {}, adv[PER] = {}, wt[PER] = {}, g[PER];
+// What a lane reads of its 8 tokens, then their weights.
+struct PolicyTokens {
+    float lp[PER], old[PER], ref[PER] = {}, adv[PER] = {}, wt[PER] = {};
+    unsigned live, counted = 0;
+    template <typename T> __device__ __forceinline__ void load(const muon_policy_args& a, int t) {
+        const int n = static_cast<int>(a.tokens);
         load_tokens<T>(a.logp, t, n, lp);
         load_tokens<T>(a.old_logp, t, n, old);
         if (a.kl != MUON_KL_NONE) load_tokens<T>(a.ref_logp, t, n, ref);
         if (!a.advantage_per_sequence) load_tokens<float>(a.advantages, t, n, adv);
-        const unsigned live = load_mask(a.mask, t, n);
-        unsigned counted = 0;
-        if (!st.by_sequence() && !a.advantage_per_sequence) {   // nothing here depends on the sequence
-            counted = live & (sq.count ? in_piece(t, sq.at(0), sq.at(sq.count)) : 0u);
-#pragma unroll
-            for (int e = 0; e < PER; ++e) wt[e] = every;
-        } else {
-            sq.pieces(t0, t0 + UNIT, [&](int s) { return a.advantage_per_sequence ? a.advantages[s] : 0.0f; },
-                      [&](int s, int pa, int pb, int lo, int hi, float side) {
-                          const unsigned on = live & in_piece(t, pa, pb);
-                          float w = every;
-                          if (st.by_sequence()) {
-                              float c;
-                              if (!a.mask) c = static_cast<float>(hi - lo);
-                              else if (lo >= t0 && hi <= t0 + UNIT) c = wave_sum(static_cast<float>(__popc(on)));
-                              else c = st.q.first(s, lo, hi) + heads(st.q, lo / UNIT + 1, (hi - 1) / UNIT);
-                              w = 1.0f / (fmaxf(c, 1.0f) * static_cast<float>(sq.count));
-                          }
-                          counted |= on;
-#pragma unroll
-                          for (int e = 0; e < PER; ++e)
-                              if (on >> e & 1u) {
-                                  wt[e] = w;
-                                  if (a.advantage_per_sequence) adv[e] = side;
-                              }
-                      });
-        }
-#pragma unroll
-        for (int e = 0; e < PER; ++e) {
-            g[e] = 0.0f;
-            if (!(counted >> e & 1u)) continue;
-            const PolicyToken o = policy_token(a, lp[e], old[e], ref[e], adv[e]);
-            v[0] = fmaf(wt[e], o.loss, v[0]);
-            v[1] += o.kl;
-            v[2] += o.held;
-            v[3] += o.rho;
-            v[4] += 1.0f;
-            g[e] = a.grad_scale * wt[e] * o.grad;
-        }
-        if (a.grad_logp) store_tokens<T>(a.grad_logp, t, n, g);
+        live = load_mask(a.mask, t, n);
     }
+};
+
+// Which of the tokens count, their advantages and weights (1 under a token mean, whose weight comes later).  `advantages`: by
+// sequence, if they are.
+template <typename S>
+__device__ __forceinline__ void policy_weights(const S& st, int u, const float* advantages, PolicyTokens& k) {
+    const int t0 = u * UNIT, t = t0 + PER * lane_id();
+    if (st.flat()) {
+        k.counted = k.live & st.covered(t);
 #pragma unroll
-    for (int k = 0; k < PL_SUMS; ++k) {
-        const float s = block_sum<NT>(v[k], red);
-        if (threadIdx.x == 0) st.sums[PL_SUMS * block + k] = s;
+        for (int e = 0; e < PER; ++e) k.wt[e] = 1.0f;
+        return;
     }
+    const bool per_seq = st.a.advantage_per_sequence != 0;
+    st.seqs.pieces(t0, t0 + UNIT, [&](int s) { return per_seq ? advantages[s] : 0.0f; },
+                   [&](int s, int a, int b, int lo, int hi, float side) {
+                       const unsigned on = k.live & in_piece(t, a, b);
+                       float w = 1.0f;
+                       if (st.by_sequence()) {
+                           float c;
+                           if (!st.a.mask) c = static_cast<float>(hi - lo);
+                           else if (lo >= t0 && hi <= t0 + UNIT) c = wave_sum(static_cast<float>(__popc(on)));
+                           else c = st.q.first(s, lo, hi) + heads(st.q, lo / UNIT + 1, (hi - 1) / UNIT);
+                           w = 1.0f / (fmaxf(c, 1.0f) * static_cast<float>(st.seqs.count));
+                       }
+                       k.counted |= on;
+#pragma unroll
+                       for (int e = 0; e < PER; ++e)
+                           if (on >> e & 1u) {
+                               k.wt[e] = w;
+                               if (per_seq) k.adv[e] = side;
+                           }
+                   });
 }
 
-template <int NT> __device__ __forceinline__ void policy_final(const PolicyState& st, int blocks, float* red) {
+// The tokens' sums, and their gradients before the common factor.
+__device__ __forceinline__ void policy_tokens(const muon_policy_args& a, const PolicyTokens& k, float (&v)[PL_SUMS], float (&g)[PER]) {
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+        g[e] = 0.0f;
+        if (!(k.counted >> e & 1u)) continue;
+        const PolicyToken o = policy_token(a, k.lp[e], k.old[e], k.ref[e], k.adv[e]);
+        v[0] = fmaf(k.wt[e], o.loss, v[0]);
+        v[1] += o.kl;
+        v[2] += o.held;
+        v[3] += o.rho;
+        v[4] += 1.0f;
+        g[e] = k.wt[e] * o.grad;
+    }
+}
+template <typename T>
+__device__ __forceinline__ void policy_store(const muon_policy_args& a, int u, float factor, float (&g)[PER]) {
+#pragma unroll
+    for (int e = 0; e < PER; ++e) g[e] *= factor;
+    store_tokens<T>(a.grad_logp, u * UNIT + PER * lane_id(), static_cast<int>(a.tokens), g);
+}
+
+// v: the sums over everything.
+__device__ __forceinline__ void policy_write(const muon_policy_args& a, const float (&v)[PL_SUMS]) {
+    const float per = 1.0f / fmaxf(v[4], 1.0f);
+    *a.loss = a.reduction == MUON_REDUCE_SEQUENCE ? v[0] : v[0] * per;
+    if (!a.stats) return;
+    a.stats[0] = v[1] * per;
+    a.stats[1] = v[2] * per;
+    a.stats[2] = v[3] * per;
+    a.stats[3] = v[4];
+}
+
+// With a mask: the counted tokens of all sequences, one partial a workgroup, or of each one's units.
+__global__ __launch_bounds__(LS_THREADS) void policy_counts_kernel(PolicyState<int64_t> st, float* counts) {
+    __shared__ float red[LS_THREADS / 64];
+    constexpr int W = LS_THREADS / 64;
+    const int n = static_cast<int>(st.a.tokens);
+    float total = 0.0f;
+    for (int u = blockIdx.x * W + wave_index(); u < st.units(); u += gridDim.x * W) {
+        const int t = u * UNIT + PER * lane_id();
+        const unsigned live = load_mask(st.a.mask, t, n);
+        if (st.by_sequence()) policy_unit_counts(st, u, live);
+        else total += static_cast<float>(__popc(live & st.covered(t)));
+    }
+    if (st.by_sequence()) return;
+    total = block_sum(total, red);
+    if (threadIdx.x == 0) counts[blockIdx.x] = total;
+}
+
+// counts: `parts` partial counts (token mean with a mask).  sums: PL_SUMS by workgroup.
+template <typename T>
+__global__ __launch_bounds__(LS_THREADS) void policy_main_kernel(PolicyState<int64_t> st, const float* counts, int parts, float* sums) {
+    constexpr int W = LS_THREADS / 64;
+    __shared__ float red[PL_SUMS * W];
+    const muon_policy_args& a = st.a;
+    float factor = 0.0f;
+    bool known = false;
     float v[PL_SUMS] = {};
-    for (int b = threadIdx.x; b < blocks; b += NT)
-#pragma unroll
-        for (int k = 0; k < PL_SUMS; ++k) v[k] += st.sums[PL_SUMS * b + k];
-#pragma unroll
-    for (int k = 0; k < PL_SUMS; ++k) v[k] = block_sum<NT>(v[k], red);
-    if (threadIdx.x != 0) return;
-    *st.a.loss = v[0];
-    if (st.a.stats) {
-        const float per = 1.0f / fmaxf(v[4], 1.0f);
-        st.a.stats[0] = v[1] * per;
-        st.a.stats[1] = v[2] * per;
-        st.a.stats[2] = v[3] * per;
-        st.a.stats[3] = v[4];
+    for (int u = blockIdx.x * W + wave_index(); u < st.units(); u += gridDim.x * W) {
+        PolicyTokens k;
+        k.load<T>(a, u * UNIT + PER * lane_id());
+        if (!known) {   // once, behind the first unit's loads
+            factor = a.grad_scale;
+            if (!st.by_sequence()) {
+                float total;
+                if (a.mask) {
+                    float c = 0.0f;
+                    for (int p = lane_id(); p < parts; p += 64) c += counts[p];
+                    total = wave_sum(c);
+                } else {
+                    total = st.seqs.count ? static_cast<float>(max(st.seqs.at(st.seqs.count) - st.seqs.at(0), 0)) : 0.0f;
+                }
+                factor /= fmaxf(total, 1.0f);
+            }
+            known = true;
+        }
+        policy_weights(st, u, a.advantages, k);
+        float g[PER];
+        policy_tokens(a, k, v, g);
+        if (a.grad_logp) policy_store<T>(a, u, factor, g);
     }
+    block_sums(v, red);
+    if (threadIdx.x == 0)
+#pragma unroll
+        for (int k = 0; k < PL_SUMS; ++k) sums[PL_SUMS * blockIdx.x + k] = v[k];
 }
 
-__global__ __launch_bounds__(LS_THREADS) void policy_counts_kernel(PolicyState st) {
-    __shared__ float red[LS_THREADS / 64];
-    constexpr int W = LS_THREADS / 64;
-    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
-    policy_counts<LS_THREADS>(st, blockIdx.x * W + wave, gridDim.x * W, blockIdx.x, red);
+__global__ __launch_bounds__(LS_THREADS) void policy_final_kernel(muon_policy_args a, const float* sums, int blocks) {
+    __shared__ float red[PL_SUMS * LS_THREADS / 64];
+    float v[PL_SUMS] = {};
+#pragma unroll 4
+    for (int b = threadIdx.x; b < blocks; b += LS_THREADS)
+#pragma unroll
+        for (int k = 0; k < PL_SUMS; ++k) v[k] += sums[PL_SUMS * b + k];
+    block_sums(v, red);
+    if (threadIdx.x == 0) policy_write(a, v);
 }
-template <typename T> __global__ __launch_bounds__(LS_THREADS) void policy_main_kernel(PolicyState st) {
-    __shared__ float red[LS_THREADS / 64];
-    constexpr int W = LS_THREADS / 64;
-    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
-    policy_main<T, LS_THREADS>(st, blockIdx.x * W + wave, gridDim.x * W, blockIdx.x, red);
-}
-__global__ __launch_bounds__(LS_ONE) void policy_final_kernel(PolicyState st, int blocks) {
-    __shared__ float red[LS_ONE / 64];
-    policy_final<LS_ONE>(st, blocks, red);
-}
-template <typename T> __global__ __launch_bounds__(LS_ONE) void policy_one_kernel(PolicyState st) {
-    __shared__ float red[LS_ONE / 64];
-    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
-    if (st.a.mask) {
-        policy_counts<LS_ONE>(st, wave, LS_ONE / 64, 0, red);
+
+template <typename T> __global__ __launch_bounds__(LS_ONE) void policy_one_kernel(muon_policy_args a) {
+    constexpr int W = LS_ONE / 64;
+    __shared__ float red[PL_SUMS * W];
+    __shared__ int offsets[LS_SMALL_SEQS + 1];
+    __shared__ float head[W], tail[W], own[LS_SMALL_SEQS], adv[LS_SMALL_SEQS];
+    const int u = wave_index();
+    const PolicyState<int> st{a, {offsets, static_cast<int>(a.sequences), static_cast<int>(a.tokens)}, {head, tail, own}};
+    PolicyTokens k;
+    k.load<T>(a, u * UNIT + PER * lane_id());
+    offsets_to_lds(a.offsets, a.sequences, a.tokens, offsets);
+    if (a.advantage_per_sequence)
+        for (int s = threadIdx.x; s < st.seqs.count; s += blockDim.x) adv[s] = a.advantages[s];
+    __syncthreads();
+    if (st.by_sequence() && a.mask) {
+        if (u < st.units()) policy_unit_counts(st, u, k.live);
         __syncthreads();
     }
-    policy_main<T, LS_ONE>(st, wave, LS_ONE / 64, 0, red);
-    __syncthreads();
-    policy_final<LS_ONE>(st, 1, red);
+    float v[PL_SUMS] = {}, g[PER] = {};
+    if (u < st.units()) {
+        policy_weights(st, u, adv, k);
+        policy_tokens(a, k, v, g);
+    }
+    block_sums(v, red);
+    if (a.grad_logp && u < st.units()) policy_store<T>(a, u, st.by_sequence() ? a.grad_scale : a.grad_scale / fmaxf(v[4], 1.0f), g);
+    if (threadIdx.x == 0) policy_write(a, v);
 }
 
 // ---- host ---------------------------------------------------------------------
 
 int64_t units_of(int64_t tokens) { return (tokens + UNIT - 1) / UNIT; }
-unsigned grid_for(int64_t waves, int most) {
-    return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>((waves + 3) / 4, most)));
+unsigned one_block(int64_t tokens) { return static_cast<unsigned>(64 * std::max<int64_t>(1, units_of(tokens))); }
+// Workgroups for so many waves' units: at most `most`, each wave with as many units as any other (or one less).
+unsigned grid_for(int64_t units, int most) {
+    const int64_t rounds = std::max<int64_t>(1, (units + 4 * most - 1) / (4 * most));
+    return static_cast<unsigned>(std::max<int64_t>(1, (units + 4 * rounds - 1) / (4 * rounds)));
 }
 
 }  // namespace
@@ -491,16 +558,17 @@ size_t preference_bytes(const muon_preference_args& a) {
 }
 
 hipError_t launch_preference(const muon_preference_args& a, void* workspace, hipStream_t s) {
+    const bool bf = a.dtype == MUON_BF16;
+    if (a.tokens <= LS_SMALL && a.sequences <= LS_SMALL_SEQS) {
+        if (bf) hipLaunchKernelGGL(preference_one_kernel<uint16_t>, dim3(1), dim3(one_block(a.tokens)), 0, s, a);
+        else hipLaunchKernelGGL(preference_one_kernel<float>, dim3(1), dim3(one_block(a.tokens)), 0, s, a);
+        return hipGetLastError();
+    }
     const size_t q = static_cast<size_t>(a.sequences), u = static_cast<size_t>(units_of(a.tokens));
     float2* f2 = static_cast<float2*>(workspace);
     float* f = reinterpret_cast<float*>(f2 + 2 * u + q);
-    const PreferenceState st{a, {f2, f2 + u, f2 + 2 * u}, f, f + q};
-    const bool bf = a.dtype == MUON_BF16;
-    if (a.tokens <= LS_SMALL && a.sequences <= LS_SMALL) {
-        if (bf) hipLaunchKernelGGL(preference_one_kernel<uint16_t>, dim3(1), dim3(LS_ONE), 0, s, st);
-        else hipLaunchKernelGGL(preference_one_kernel<float>, dim3(1), dim3(LS_ONE), 0, s, st);
-        return hipGetLastError();
-    }
+    const PreferenceState<int64_t> st{a, {a.offsets, static_cast<int>(a.sequences), static_cast<int>(a.tokens)},
+                                      {f2, f2 + u, f2 + 2 * u}, f, f + q};
     auto launch = [&](auto kernel, unsigned grid) {
         hipLaunchKernelGGL(kernel, dim3(grid), dim3(LS_THREADS), 0, s, st);
         return hipGetLastError();
@@ -519,30 +587,32 @@ size_t policy_bytes(const muon_policy_args& a) {
 }
 
 hipError_t launch_policy(const muon_policy_args& a, void* workspace, hipStream_t s) {
+    const bool bf = a.dtype == MUON_BF16;
+    if (a.tokens <= LS_SMALL && a.sequences <= LS_SMALL_SEQS) {
+        if (bf) hipLaunchKernelGGL(policy_one_kernel<uint16_t>, dim3(1), dim3(one_block(a.tokens)), 0, s, a);
+        else hipLaunchKernelGGL(policy_one_kernel<float>, dim3(1), dim3(one_block(a.tokens)), 0, s, a);
+        return hipGetLastError();
+    }
     const size_t q = static_cast<size_t>(a.sequences), u = static_cast<size_t>(units_of(a.tokens));
     float* f = static_cast<float*>(workspace);
     float* counts = f + 2 * u + q;
-    PolicyState st{a, {f, f + u, f + 2 * u}, counts, 1, counts + LS_COUNTS};
-    const bool bf = a.dtype == MUON_BF16;
-    if (a.tokens <= LS_SMALL) {
-        if (bf) hipLaunchKernelGGL(policy_one_kernel<uint16_t>, dim3(1), dim3(LS_ONE), 0, s, st);
-        else hipLaunchKernelGGL(policy_one_kernel<float>, dim3(1), dim3(LS_ONE), 0, s, st);
-        return hipGetLastError();
-    }
+    float* sums = counts + LS_COUNTS;
+    const PolicyState<int64_t> st{a, {a.offsets, static_cast<int>(a.sequences), static_cast<int>(a.tokens)}, {f, f + u, f + 2 * u}};
     hipError_t e = hipSuccess;
+    int parts = 0;
     if (a.mask) {
         // by sequence every unit has work that waits; counting alone keeps few, deep workgroups
-        st.count_parts = static_cast<int>(grid_for(u, a.reduction == MUON_REDUCE_SEQUENCE ? LS_GRID : LS_COUNTS));
-        hipLaunchKernelGGL(policy_counts_kernel, dim3(st.count_parts), dim3(LS_THREADS), 0, s, st);
+        parts = static_cast<int>(grid_for(u, a.reduction == MUON_REDUCE_SEQUENCE ? LS_GRID : LS_COUNTS));
+        hipLaunchKernelGGL(policy_counts_kernel, dim3(parts), dim3(LS_THREADS), 0, s, st, counts);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     const unsigned grid = grid_for(u, LS_GRID);
-    if (bf) hipLaunchKernelGGL(policy_main_kernel<uint16_t>, dim3(grid), dim3(LS_THREADS), 0, s, st);
-    else hipLaunchKernelGGL(policy_main_kernel<float>, dim3(grid), dim3(LS_THREADS), 0, s, st);
+    if (bf) hipLaunchKernelGGL(policy_main_kernel<uint16_t>, dim3(grid), dim3(LS_THREADS), 0, s, st, counts, parts, sums);
+    else hipLaunchKernelGGL(policy_main_kernel<float>, dim3(grid), dim3(LS_THREADS), 0, s, st, counts, parts, sums);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(policy_final_kernel, dim3(1), dim3(LS_ONE), 0, s, st, static_cast<int>(grid));
+    hipLaunchKernelGGL(policy_final_kernel, dim3(1), dim3(LS_THREADS), 0, s, a, sums, static_cast<int>(grid));
     return hipGetLastError();
 }
 

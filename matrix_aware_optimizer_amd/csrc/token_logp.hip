@@ -711,7 +711,7 @@ struct FewArgs {
 // along the accumulator rows, tokens along the columns (16 x 16 MFMA).  HBM-bound: the head once,
 // cols x vocab elements; hidden comes from the caches.
 template <typename T, int PARTS, int NT, bool VEC>
-__global__ __launch_bounds__(256) void few_kernel(FewArgs a) {
+__global__ __launch_bounds__(256, NT == 1 ? 4 : 1) void few_kernel(FewArgs a) {
     __shared__ float red[4][FEW_ROWS][16 * NT + 1];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int v0 = blockIdx.x * FEW_ROWS, ln = lane & 15, kg = 8 * (lane >> 4);

@@ -75,20 +75,43 @@ __device__ __forceinline__ void st_run(global_t<float>* p, unsigned i, const flo
     *(global_t<f32x4_el4>*)(p + i + 4) = f32x4_t{o[4], o[5], o[6], o[7]};
 }
 
-// Sum over a workgroup of NT threads, given to every thread; `red` holds NT / 64 floats.
-// The order of the additions is fixed.  Safe to call again at once with the same `red`.
-template <int NT> __device__ __forceinline__ float block_sum(float v, float* red) {
+// Sum over a wave, the same in every lane, through the lanes' data paths (a few cycles a step, where a shuffle goes through
+// LDS): within rows of 16 lanes, then row 0 to 1 and 2 to 3, then row 1 to 2 and 3; lane 63 ends with all.
+template <int CTRL, int ROWS> __device__ __forceinline__ float dpp_add(float v) {
+    return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xF, false));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+    v = dpp_add<0x111, 0xF>(v);   // row_shr:1
+    v = dpp_add<0x112, 0xF>(v);
+    v = dpp_add<0x114, 0xF>(v);
+    v = dpp_add<0x118, 0xF>(v);
+    v = dpp_add<0x142, 0xA>(v);   // row_bcast:15 into rows 1 and 3
+    v = dpp_add<0x143, 0xC>(v);   // row_bcast:31 into rows 2 and 3
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+
+// Sum over a workgroup, given to every thread; `red` holds a float per wave.  The order of the
+// additions is fixed.  Safe to call again at once with the same `red`.
+template <int N> __device__ __forceinline__ void block_sums(float (&v)[N], float* red) {
+    const int waves = blockDim.x >> 6;
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
-    if constexpr (NT > 64) {
-        lds_barrier();
-        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-        lds_barrier();
-        v = red[0];
+    for (int k = 0; k < N; ++k) v[k] = wave_sum(v[k]);
+    if (waves == 1) return;
+    lds_barrier();
+    if ((threadIdx.x & 63) == 0)
 #pragma unroll
-        for (int w = 1; w < NT / 64; ++w) v += red[w];
+        for (int k = 0; k < N; ++k) red[k * waves + (threadIdx.x >> 6)] = v[k];
+    lds_barrier();
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        v[k] = red[k * waves];
+        for (int w = 1; w < waves; ++w) v[k] += red[k * waves + w];
     }
-    return v;
+}
+__device__ __forceinline__ float block_sum(float v, float* red) {
+    float s[1] = {v};
+    block_sums(s, red);
+    return s[0];
 }
 
 hipError_t launch_block_norm(const muon_block_norm_args& a, hipStream_t s);
