@@ -334,8 +334,11 @@ muon_status muon_token_logp(const muon_token_logp_args* args, void* workspace, s
  *   dz_ij = c_i ([j = target_i] - p_ij),  grad_hidden = dz head,  grad_head = dz^T hidden
  * grad_hidden or grad_head may be NULL (not wanted), not both.  `saved` is what
  * muon_token_logp kept for the same inputs, or NULL.  dz is rounded to the
- * operands' precision (bf16, or as much of fp32 as three bf16 parts hold)
- * before the two products. */
+ * operands' precision before the two products: bf16, or 22 bits for fp32.
+ *
+ * Precision in fp32: the products (not those of up to 64 tokens without `saved`)
+ * take each operand as two fp16 parts under one power-of-two scale, 22 bits for
+ * values down to 2^-28 of the operand's largest finite one, fewer below. */
 typedef struct {
     const void*    hidden;
     const void*    head;

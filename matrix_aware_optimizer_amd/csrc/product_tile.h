@@ -1,9 +1,9 @@
 // Square tiles of C = A B^T on the gfx950 matrix cores, for the products of the
-// vocabulary head (token_logp.hip): both operands bf16, k-contiguous.
+// vocabulary head (token_logp.hip): both operands of 16-bit values, k-contiguous.
 //
 //   C[r][c] = sum_k A[r][k] B[c][k]
 // Tile<256>: 8 waves (2 x 4, two a SIMD); a wave owns 128 x 64 of the tile as 4 x 2 blocks of
-// 32 x 32 (v_mfma_f32_32x32x16_bf16, fp32 sums).
+// 32 x 32 (v_mfma_f32_32x32x16, fp32 sums).
 // Tile<128>: 8 waves, of which 4 (2 x 2 of 64 x 64) take the first half of every k-step and 4 the
 // second; at the end the two sums of each 64 x 64 are exchanged so that each wave keeps 32 x 64.
 // It reads LDS twice as much per product (as long as its MFMAs take), so it serves products with too few
@@ -18,11 +18,11 @@
 // come from anywhere (gathered tokens, rows clamped at an edge).  k is a multiple of 64, or (KTAIL) of 8:
 // then the last step's missing chunks come from 16 bytes of zeros.
 //
-// fp32 operands are split by the caller into three bf16 parts (8 bits each: 24 in all), stored one
-// after the other, and the tile sums the six products whose parts' indexes add to at most 2,
-// small ones first: what is left out is below 2^-24 of the product of the magnitudes.  Six
-// bf16 products take 6 / 2517 of the time unit against 1 / 157 for the fp32 MFMA: 2.7 times
-// less.
+// fp32 operands come as two fp16 parts of 11 bits each, x = (hi + 2^-11 lo) / scale with one power-of-two scale an operand
+// that brings its largest value to 2^14 .. 2^15 (values below 2^-28 of it lose bits: fp16 ends at 2^-24).
+// The tile sums lo hi + hi lo first, multiplies by 2^-11, and goes on with hi hi; lo lo, below 2^-22 of
+// the product of the magnitudes, is left out.  Three fp16 products take 3 / 2517 of the time unit against
+// 1 / 157 for the fp32 MFMA: 5 times less.  (Subnormal fp16 inputs of the MFMA are taken at their value.)
 #pragma once
 
 #include "muon_internal.h"
@@ -32,6 +32,7 @@ namespace muon {
 namespace pt {
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef short i16x4_t __attribute__((ext_vector_type(4)));
@@ -50,15 +51,30 @@ static __device__ const u32x4 zero_chunk = {};   // what a KTAIL product reads p
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6)); }
 __device__ __forceinline__ int swz(int row, int c) { return row * CHUNKS + (c ^ ((row >> 1) & 7)); }
 
-// Parts of the operands (bf16: the value itself; fp32: three parts, pitch a_part / b_part
-// bytes) in the order in which their products are summed, two bits a product.
+// Parts of the operands (bf16: the value itself; fp32: hi and lo, pitch a_part / b_part bytes) in the
+// order in which their products are summed, two bits a product.
 template <int PARTS> struct Order;
 template <> struct Order<1> { static constexpr int N = 1; static constexpr unsigned A = 0, B = 0; };
-template <> struct Order<3> {
-    static constexpr int N = 6;                       // (2,0) (0,2) (1,1) (1,0) (0,1) (0,0)
-    static constexpr unsigned A = 2u | 0u << 2 | 1u << 4 | 1u << 6 | 0u << 8 | 0u << 10;
-    static constexpr unsigned B = 0u | 2u << 2 | 1u << 4 | 0u << 6 | 1u << 8 | 0u << 10;
-};
+template <> struct Order<2> { static constexpr int N = 3; static constexpr unsigned A = 1u, B = 1u << 2; };   // lo hi, hi lo, hi hi
+constexpr float LO_STEP = 1.0f / 2048.0f;   // what lo counts against hi
+
+template <int PARTS> __device__ __forceinline__ void mfma(f32x16_t& acc, const u32x4& a, const u32x4& b) {
+    if constexpr (PARTS == 1)
+        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), acc, 0, 0, 0);
+    else
+        acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), acc, 0, 0, 0);
+}
+// Between the cross products and hi hi.
+template <int PARTS, int M, int N> __device__ __forceinline__ void scale_cross(f32x16_t (&acc)[M][N], int kt, int steps) {
+    if constexpr (PARTS == 2) {
+        if (kt == 2 * steps) {
+#pragma unroll
+            for (int i = 0; i < M; ++i)
+#pragma unroll
+                for (int j = 0; j < N; ++j) acc[i][j] *= LO_STEP;
+        }
+    }
+}
 
 // Byte offset of successive k-steps of one operand over the parts' products.
 template <int PARTS> struct Walk {
@@ -157,6 +173,7 @@ template <int EDGE> struct Tile {
             const u32x4* LB = lds + sb * SLAB;
             const bool more1 = kt + 1 < total, more2 = kt + 2 < total;
             const size_t offa = wa.off, offb = wb.off;
+            scale_cross<PARTS>(acc, kt, steps);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int s = 0; s < SUB; ++s) {
@@ -176,9 +193,7 @@ template <int EDGE> struct Tile {
                 for (int i = 0; i < SM; ++i) {
 #pragma unroll
                     for (int j = 0; j < SN; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, fa[s & 1][i]),
-                                                                            __builtin_bit_cast(bf16x8_t, fb[s & 1][j]),
-                                                                            acc[i][j], 0, 0, 0);
+                        mfma<PARTS>(acc[i][j], fa[s & 1][i], fb[s & 1][j]);
                     if (s + 1 < SUB) {
                         fa[(s + 1) & 1][i] = LA[swz(arow + i * 32, cn)];
                         if (i < SN) fb[(s + 1) & 1][i] = LB[swz(brow + i * 32, cn)];
@@ -249,6 +264,7 @@ template <int EDGE> struct Tile {
         for (int kt = 0; kt < total; ++kt) {
             const int nx = sl + 1 == SLOTS ? 0 : sl + 1, fill = sl == 0 ? SLOTS - 1 : sl - 1;
             const bool more1 = kt + 1 < total, more = kt + DEPTH < total;
+            scale_cross<PARTS>(acc, kt, steps);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int s = 0; s < SLICES; ++s) {
@@ -275,9 +291,7 @@ template <int EDGE> struct Tile {
                     }
 #pragma unroll
                     for (int j = 0; j < SN; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, fa[s & 1][i]),
-                                                                            __builtin_bit_cast(bf16x8_t, fb[s & 1][j]),
-                                                                            acc[i][j], 0, 0, 0);
+                        mfma<PARTS>(acc[i][j], fa[s & 1][i], fb[s & 1][j]);
                     if (more) issue(kt + DEPTH, fill, s * BM + i);
                     __builtin_amdgcn_sched_barrier(0);
                 }

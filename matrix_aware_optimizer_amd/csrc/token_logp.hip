@@ -18,8 +18,10 @@
 //    once, so that both gradients are k-contiguous products (C rows = columns of the gradient,
 //    C columns = its rows).  Few tiles: the sum over k is split over workgroups that leave fp32
 //    tiles, added in order by slab_sum_kernel.
-//  - fp32 operands travel as three bf16 parts (product_tile.h); dz in fp32 calls too.
-//  - Few tokens: few_kernel reads the head once with 16 x 16 MFMAs and no staging.
+//  - fp32 operands travel as two fp16 parts under a scale (product_tile.h), dz in fp32 calls too: absmax_kernel and
+//    scales_kernel find the scales.
+//  - Few tokens: few_kernel reads the head once with 16 x 16 MFMAs and no staging (fp32 as three bf16 parts
+//    there, which need no scale).
 //
 // The statistics are kept in base 2 (z2 = z log2(e)): one multiplication and v_exp_f32.  A target's
 // own term stays out of the sum S of its token, logp = -log(1 + S 2^(M - z2_target)), which keeps its
@@ -47,15 +49,18 @@ constexpr int MAX_SPLITS = 16, MIN_SPLIT_STEPS = 8;
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline int64_t up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 
-// x as bf16 parts, exact to 24 bits: the first two truncated (so nothing overflows), the last rounded.
-__device__ __forceinline__ void split3(float x, uint16_t (&p)[3]) {
-    const uint32_t hi = __float_as_uint(x) & 0xffff0000u;
-    const bool fin = (hi & 0x7f800000u) != 0x7f800000u;
-    p[0] = static_cast<uint16_t>((fin ? hi : hi | (x != x ? 0x00400000u : 0u)) >> 16);
-    const float r = fin ? x - __uint_as_float(hi) : 0.0f;
-    const uint32_t mid = __float_as_uint(r) & 0xffff0000u;
-    p[1] = static_cast<uint16_t>(mid >> 16);
-    p[2] = f32_to_bf16(r - __uint_as_float(mid));
+// x times its operand's scale as fp16 parts (product_tile.h), patterns of 16 bits.  What is not finite is all in the first.
+__device__ __forceinline__ void split2(float x, uint16_t (&p)[2]) {
+    const _Float16 hi = static_cast<_Float16>(x);
+    const float h = static_cast<float>(hi);
+    const _Float16 lo = static_cast<_Float16>(fabsf(h) < INFINITY ? (x - h) * (1.0f / pt::LO_STEP) : 0.0f);
+    p[0] = __builtin_bit_cast(uint16_t, hi);
+    p[1] = __builtin_bit_cast(uint16_t, lo);
+}
+// A value as the 16-bit parts that the products take.
+template <int PARTS> __device__ __forceinline__ void to_parts(float x, float scale, uint16_t (&p)[2]) {
+    if constexpr (PARTS == 1) p[0] = f32_to_bf16(x);
+    else split2(x * scale, p);
 }
 
 // ---------------------------------------------------------------------------
@@ -123,6 +128,7 @@ struct PackArgs {
     Live live;
     uint16_t* dst;
     size_t dst_ld, part;   // elements
+    const float* scale;    // two parts: the operand's scale
 };
 
 // dst[part][r][0 .. dst_ld) = parts of src[row r], zero past its columns.
@@ -130,16 +136,17 @@ template <typename T, int PARTS>
 __global__ __launch_bounds__(256) void pack_kernel(PackArgs a) {
     const int64_t rows = a.use_live ? a.live.rows() : a.rows;
     const int64_t per = a.dst_ld / 8, n = rows * per;
+    const float scale = PARTS == 1 ? 1.0f : *a.scale;
     for (int64_t q = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; q < n; q += static_cast<int64_t>(gridDim.x) * 256) {
         const int64_t r = q / per, c = (q - r * per) * 8;
         const size_t s = static_cast<size_t>(a.use_live ? a.live.idx[a.live.first + r] : r) * a.ld + c;
-        uint16_t v[8][3];
+        uint16_t v[8][2];
+        Run<T> x;
+        const auto* q8 = G(static_cast<const T*>(a.src) + s);
+        if (c + 8 <= a.cols) x.load(q8, 0);
+        else if (c < a.cols) x.load(q8, 0, static_cast<unsigned>(a.cols - c));
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float x = c + e < a.cols ? ld_el<T>(a.src, s + e) : 0.0f;
-            if constexpr (PARTS == 3) split3(x, v[e]);
-            else v[e][0] = f32_to_bf16(x);
-        }
+        for (int e = 0; e < 8; ++e) to_parts<PARTS>(x.get(e), scale, v[e]);
 #pragma unroll
         for (int p = 0; p < PARTS; ++p) {
             u32x4 w;
@@ -155,6 +162,7 @@ __global__ __launch_bounds__(256) void pack_kernel(PackArgs a) {
 template <typename T, int PARTS> __device__ __forceinline__ void transpose_tile(const PackArgs& a, int64_t r0, int64_t c0, float (&tile)[64][65]) {
     const int64_t rows = a.use_live ? a.live.rows() : a.rows;
     if (r0 >= rows) return;
+    const float scale = PARTS == 1 ? 1.0f : *a.scale;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         const int k = (threadIdx.x >> 3) + 32 * half, x = 8 * (threadIdx.x & 7);
@@ -173,12 +181,9 @@ template <typename T, int PARTS> __device__ __forceinline__ void transpose_tile(
     for (int half = 0; half < 2; ++half) {
         const int c = (threadIdx.x >> 3) + 32 * half, r = 8 * (threadIdx.x & 7);
         if (c0 + c >= a.cols) continue;
-        uint16_t v[8][3];
+        uint16_t v[8][2];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if constexpr (PARTS == 3) split3(tile[r + e][c], v[e]);
-            else v[e][0] = f32_to_bf16(tile[r + e][c]);
-        }
+        for (int e = 0; e < 8; ++e) to_parts<PARTS>(tile[r + e][c], scale, v[e]);
 #pragma unroll
         for (int p = 0; p < PARTS; ++p) {
             u32x4 w;
@@ -186,6 +191,85 @@ template <typename T, int PARTS> __device__ __forceinline__ void transpose_tile(
             for (int e = 0; e < 4; ++e) w[e] = v[2 * e][p] | static_cast<uint32_t>(v[2 * e + 1][p]) << 16;
             G(reinterpret_cast<u32x4*>(a.dst + p * a.part + (c0 + c) * a.dst_ld + r0 + r))[0] = w;
         }
+    }
+}
+
+// ---- scales of fp32 operands ----
+
+// Bits of the largest finite |x| over some rows, one partial a workgroup: head_blocks of them for head, the others for the
+// scored rows of hidden.
+constexpr int ABS_HEAD = 1024, ABS_HIDDEN = 128;
+struct AbsMaxArgs {
+    const float *head, *hidden;
+    size_t ld_head, ld_hidden;
+    int64_t vocab, cols;
+    Live live;
+    uint32_t* part;
+};
+__device__ __forceinline__ uint32_t block_max(uint32_t m, uint32_t* red) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), o, 64)));
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+    __syncthreads();
+    for (int w = 0; w < static_cast<int>(blockDim.x >> 6); ++w) m = max(m, red[w]);
+    return m;
+}
+__device__ __forceinline__ uint32_t finite_bits(float x) {
+    const uint32_t b = __float_as_uint(x) & 0x7fffffffu;
+    return b < 0x7f800000u ? b : 0u;
+}
+__global__ __launch_bounds__(256) void absmax_kernel(AbsMaxArgs a) {
+    __shared__ uint32_t red[4];
+    const bool head = blockIdx.x < ABS_HEAD;
+    const int b = head ? blockIdx.x : blockIdx.x - ABS_HEAD, blocks = head ? ABS_HEAD : ABS_HIDDEN;
+    const int64_t rows = head ? a.vocab : a.live.rows(), runs = (a.cols + 7) / 8;
+    uint32_t m = 0;
+    for (int64_t r = 4 * b + static_cast<int>(threadIdx.x >> 6); r < rows; r += 4 * blocks) {
+        const auto* q = G(head ? a.head + static_cast<size_t>(r) * a.ld_head : a.hidden + static_cast<size_t>(a.live.idx[a.live.first + r]) * a.ld_hidden);
+        for (int64_t k = threadIdx.x & 63; k < runs; k += 64) {
+            Run<float> x;
+            if (8 * k + 8 <= a.cols) x.load(q, static_cast<unsigned>(8 * k));
+            else x.load(q, static_cast<unsigned>(8 * k), static_cast<unsigned>(a.cols - 8 * k));
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m = max(m, finite_bits(x.get(e)));
+        }
+    }
+    m = block_max(m, red);
+    if (threadIdx.x == 0) a.part[blockIdx.x] = m;
+}
+// The power of two that brings the largest value to 2^14 .. 2^15.
+__device__ __forceinline__ float scale_of(uint32_t bits) {
+    if (bits == 0) return 1.0f;
+    const int s = min(14 - (static_cast<int>(bits >> 23) - 127), 126);   // at least -113: a normal number both ways
+    return __uint_as_float(static_cast<uint32_t>(s + 127) << 23);
+}
+// operands: scales of hidden and head from absmax_kernel's partials.  dz: that of dz, whose values are at most
+// |scale grad_logp| of their token.  Either may be NULL.
+struct ScalesArgs {
+    const uint32_t* part;
+    float *operands, *dz;
+    Live live;
+    const float* grad_logp;
+    float scale;
+};
+__global__ __launch_bounds__(1024) void scales_kernel(ScalesArgs a) {
+    __shared__ uint32_t red[16];
+    if (a.operands) {
+        const uint32_t w = block_max(threadIdx.x < ABS_HEAD ? a.part[threadIdx.x] : 0u, red);
+        const uint32_t h = block_max(threadIdx.x < ABS_HIDDEN ? a.part[ABS_HEAD + threadIdx.x] : 0u, red);
+        if (threadIdx.x == 0) {
+            a.operands[0] = scale_of(h);
+            a.operands[1] = scale_of(w);
+        }
+    }
+    if (a.dz) {
+        uint32_t m = 0;
+        const int n = a.live.rows();
+#pragma unroll 4
+        for (int r = threadIdx.x; r < n; r += 1024) m = max(m, finite_bits(a.scale * a.grad_logp[a.live.idx[a.live.first + r]]));
+        m = block_max(m, red);
+        if (threadIdx.x == 0) *a.dz = scale_of(m);
     }
 }
 
@@ -235,6 +319,7 @@ struct LogitsArgs {
     const int64_t* targets;
     int vocab, steps, tail, ta, tb;   // tail: 16-byte chunks of the last k-step
     float scale2;           // scale log2(e)
+    const float* scales;    // two parts: of hidden and head
     float *m, *s, *zt;      // statistics: tile x list entry (pitch rows_pitch); target logit by list entry
     size_t rows_pitch;
     void* e;                // LG_SAVE: exp(z - m), list entry x vocabulary (pitch vp)
@@ -243,6 +328,7 @@ struct LogitsArgs {
     float scale;
     uint16_t *dz, *dzt;     // dz and its transpose: parts apart, pitches vp and rows_pitch; rows relative to live.first
     size_t dz_part, dzt_part;
+    const float* dz_scale;  // two parts
     size_t vp;
 };
 
@@ -293,6 +379,8 @@ __global__ __launch_bounds__(pt::Tile<EDGE>::THREADS, 2) void logits_kernel(Logi
     const int place = TL::stack_place(), h = (threadIdx.x >> 5) & 1;
     const int vl = v0 + TL::first_row();              // this lane's first vocabulary entry
     const bool edge = v0 + EDGE > a.vocab;            // uniform: entries past the vocabulary
+    // z2 = (acc k1) k2: the operands' scales taken out one by one, so that neither factor leaves fp32's range
+    const float k1 = PARTS == 1 ? 1.0f : 1.0f / a.scales[0], k2 = PARTS == 1 ? a.scale2 : a.scale2 / a.scales[1];
     lds_barrier();                                    // every wave is done with the operand slabs
 
     if constexpr (MODE != LG_DZ) {
@@ -312,7 +400,7 @@ __global__ __launch_bounds__(pt::Tile<EDGE>::THREADS, 2) void logits_kernel(Logi
 #pragma unroll
                 for (int q = 0; q < 16; ++q) {
                     const int dv = 32 * i + 8 * (q >> 2) + (q & 3);
-                    float z = acc[i][j][q] * a.scale2;
+                    float z = acc[i][j][q] * k1 * k2;
                     if (edge && vl + dv >= a.vocab) z = -INFINITY;
                     acc[i][j][q] = z;
                     mx[j] = fmaxf(mx[j], z);
@@ -391,32 +479,35 @@ __global__ __launch_bounds__(pt::Tile<EDGE>::THREADS, 2) void logits_kernel(Logi
 #pragma unroll
                 for (int q = 0; q < 16; ++q) {
                     const int dv = 32 * i + 8 * (q >> 2) + (q & 3);
-                    const float p = __builtin_amdgcn_exp2f(fmaf(acc[i][j][q], a.scale2, -l2));
+                    const float p = __builtin_amdgcn_exp2f(fmaf(acc[i][j][q] * k1, k2, -l2));
                     float d = c * ((dv == y ? 1.0f : 0.0f) - p);
                     if (c == 0.0f || (edge && vl + dv >= a.vocab)) d = 0.0f;
                     acc[i][j][q] = d;
                 }
         }
+        const float ds = PARTS == 1 ? 1.0f : *a.dz_scale;
 #pragma unroll
         for (int p = 0; p < PARTS; ++p) {
             if (p > 0) lds_barrier();
-            if (p + 1 == PARTS) {
+            if constexpr (PARTS == 1) {
                 st.put_all(L, acc);
-            } else {   // this part, truncated; the rest stays
+            } else {   // first hi, leaving the rest in the accumulators, then lo (split2 in two steps)
 #pragma unroll
                 for (int i = 0; i < TL::SM; ++i)
 #pragma unroll
                     for (int j = 0; j < TL::SN; ++j)
 #pragma unroll
                         for (int g = 0; g < 4; ++g) {
-                            unsigned w[4];
+                            uint32_t w[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                w[e] = __float_as_uint(acc[i][j][4 * g + e]) & 0xffff0000u;
-                                const float rest = acc[i][j][4 * g + e] - __uint_as_float(w[e]);
-                                acc[i][j][4 * g + e] = (w[e] & 0x7f800000u) == 0x7f800000u ? 0.0f : rest;
+                                const float x = acc[i][j][4 * g + e] * (p == 0 ? ds : 1.0f / pt::LO_STEP);
+                                const _Float16 hi = static_cast<_Float16>(x);
+                                const float f = static_cast<float>(hi);
+                                if (p == 0) acc[i][j][4 * g + e] = fabsf(f) < INFINITY ? x - f : 0.0f;
+                                w[e] = __builtin_bit_cast(uint16_t, hi);
                             }
-                            st.put(L, i, j, g, w[0] >> 16 | w[1], w[2] >> 16 | w[3]);
+                            st.put(L, i, j, g, w[0] | w[1] << 16, w[2] | w[3] << 16);
                         }
             }
             lds_barrier();
@@ -444,6 +535,7 @@ struct DzArgs {
     size_t vp, rows_pitch;
     uint16_t *dz, *dzt;     // rows relative to live.first
     size_t dz_part, dzt_part;
+    const float* dz_scale;  // two parts
 };
 
 // 64 tokens x 64 entries a workgroup.  Reads 2 (fp32: 4) bytes an element and writes 2 x 2 (2 x 6), HBM-bound.
@@ -454,6 +546,7 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
     const int r0 = blockIdx.y * 64, v0 = blockIdx.x * 64;
     if (r0 >= (n + PAD - 1) / PAD * PAD) return;
     const int vb = threadIdx.x & 7;            // 8 entries each
+    const float ds = PARTS == 1 ? 1.0f : *a.dz_scale;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         const int rt = (threadIdx.x >> 3) + 32 * half, r = r0 + rt;
@@ -479,13 +572,10 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
             x[0] = w0.x; x[1] = w0.y; x[2] = w0.z; x[3] = w0.w;
             x[4] = w1.x; x[5] = w1.y; x[6] = w1.z; x[7] = w1.w;
         }
-        uint16_t v[8][3];
+        uint16_t v[8][2];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float d = c == 0.0f || v0 + 8 * vb + k >= a.vocab ? 0.0f : k == y ? dy : -x[k] * f;
-            if constexpr (PARTS == 3) split3(d, v[k]);
-            else v[k][0] = f32_to_bf16(d);
-        }
+        for (int k = 0; k < 8; ++k)
+            to_parts<PARTS>(c == 0.0f || v0 + 8 * vb + k >= a.vocab ? 0.0f : k == y ? dy : -x[k] * f, ds, v[k]);
 #pragma unroll
         for (int p = 0; p < PARTS; ++p) {
             if (a.dz) {
@@ -528,6 +618,7 @@ struct GradArgs {
     size_t ld;
     float* slab;            // fp32 tiles in accumulator layout, [split][tile][quads][threads] x 16 bytes, or NULL: write out
     int add;                // add to what the slab holds (later chunks of tokens)
+    const float *scale, *dz_scale;   // two parts: of the transposed operand and of dz
 };
 
 // A whole 16-byte piece of the output at any element alignment, or the first `left` of its elements.
@@ -577,6 +668,15 @@ __global__ __launch_bounds__(pt::Tile<EDGE>::THREADS, 2) void grad_kernel(GradAr
             sb[j] = a.b + static_cast<size_t>(r0 + row) * a.b_ld + TL::load_chunk(j) * 16;   // padded to the tile
         }
         TL::template run<PARTS, false>(sa, sb, a.a_part, a.b_part, static_cast<size_t>(k_first) * (pt::KS * 2), steps, 0, lds, acc);
+    }
+    if constexpr (PARTS == 2) {
+        const float k1 = 1.0f / *a.dz_scale, k2 = 1.0f / *a.scale;
+#pragma unroll
+        for (int i = 0; i < TL::SM; ++i)
+#pragma unroll
+            for (int j = 0; j < TL::SN; ++j)
+#pragma unroll
+                for (int q = 0; q < 16; ++q) acc[i][j][q] = acc[i][j][q] * k1 * k2;
     }
     if (a.slab) {
         float* s = a.slab + (static_cast<size_t>(split) * a.ta * a.tb + tile) * (EDGE * EDGE) + threadIdx.x * 4;
@@ -670,6 +770,24 @@ template <int EDGE> __global__ __launch_bounds__(256) void slab_sum_kernel(GradA
 
 typedef float f32x4m_t __attribute__((ext_vector_type(4)));
 
+// x as three bf16 parts, exact to 24 bits: the first two truncated (so nothing overflows), the last rounded.
+__device__ __forceinline__ void split3(float x, uint16_t (&p)[3]) {
+    const uint32_t hi = __float_as_uint(x) & 0xffff0000u;
+    const bool fin = (hi & 0x7f800000u) != 0x7f800000u;
+    p[0] = static_cast<uint16_t>((fin ? hi : hi | (x != x ? 0x00400000u : 0u)) >> 16);
+    const float r = fin ? x - __uint_as_float(hi) : 0.0f;
+    const uint32_t mid = __float_as_uint(r) & 0xffff0000u;
+    p[1] = static_cast<uint16_t>(mid >> 16);
+    p[2] = f32_to_bf16(r - __uint_as_float(mid));
+}
+// The products of parts that few_kernel sums, small ones first, two bits each: those whose indexes add to at most 2.
+template <int PARTS> struct FewOrder;
+template <> struct FewOrder<1> { static constexpr int N = 1; static constexpr unsigned W = 0, H = 0; };
+template <> struct FewOrder<3> {
+    static constexpr int N = 6;                       // (2,0) (0,2) (1,1) (1,0) (0,1) (0,0)
+    static constexpr unsigned W = 2u | 0u << 2 | 1u << 4 | 1u << 6, H = 0u | 2u << 2 | 1u << 4 | 0u << 6 | 1u << 8;
+};
+
 // 8 values of k of one row from column k, zero past the last column, as bf16 parts.
 template <typename T, int PARTS, bool VEC>
 __device__ __forceinline__ void few_load(const void* base, size_t off, int k, int cols, u32x4 (&out)[PARTS]) {
@@ -721,7 +839,7 @@ __global__ __launch_bounds__(256, NT == 1 ? 4 : 1) void few_kernel(FewArgs a) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) ho[t] = static_cast<size_t>(min(16 * t + ln, a.tokens - 1)) * a.ld_hidden;
     f32x4m_t acc[2][NT] = {};
-    constexpr int DEEP = PARTS == 1 && VEC ? 4 : 1;   // 64-value runs of k in flight
+    constexpr int DEEP = PARTS == 1 && VEC ? 2 : 1;   // 64-value runs of k in flight (4: 31.7 us for one token and 32000 x 2048, 2: 29.1)
     for (int k0 = 64 * wave; k0 < a.cols; k0 += 256 * DEEP) {
         u32x4 w[2 * DEEP][2][PARTS], h[2 * DEEP][NT][PARTS];
 #pragma unroll
@@ -739,10 +857,10 @@ __global__ __launch_bounds__(256, NT == 1 ? 4 : 1) void few_kernel(FewArgs a) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int q = 0; q < pt::Order<PARTS>::N; ++q)
+                    for (int q = 0; q < FewOrder<PARTS>::N; ++q)
                         acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            __builtin_bit_cast(pt::bf16x8_t, w[b][r][(pt::Order<PARTS>::A >> 2 * q) & 3u]),
-                            __builtin_bit_cast(pt::bf16x8_t, h[b][t][(pt::Order<PARTS>::B >> 2 * q) & 3u]), acc[r][t], 0, 0, 0);
+                            __builtin_bit_cast(pt::bf16x8_t, w[b][r][(FewOrder<PARTS>::W >> 2 * q) & 3u]),
+                            __builtin_bit_cast(pt::bf16x8_t, h[b][t][(FewOrder<PARTS>::H >> 2 * q) & 3u]), acc[r][t], 0, 0, 0);
         }
     }
 #pragma unroll
@@ -866,7 +984,7 @@ struct Shape {
     int edge;                // tile of the logits' product
     bool direct_hidden, direct_head;   // operands that the products can read where they are: bf16 in whole 16-byte chunks
     Shape(int64_t t, int64_t d, int64_t v, int dtype, const void* hidden, int64_t ld_hidden, const void* head, int64_t ld_head)
-        : tokens(t), cols(d), vocab(v), parts(dtype == MUON_BF16 ? 1 : 3), tp(up(std::max<int64_t>(t, 1), PAD)), vp(up(v, PAD)),
+        : tokens(t), cols(d), vocab(v), parts(dtype == MUON_BF16 ? 1 : 2), tp(up(std::max<int64_t>(t, 1), PAD)), vp(up(v, PAD)),
           dp(up(d, pt::KS)), edge(edge_for(tp / PAD * (vp / PAD))) {
         const bool ok = dtype == MUON_BF16 && d % 8 == 0;
         direct_hidden = ok && reinterpret_cast<uintptr_t>(hidden) % 16 == 0 && ld_hidden % 8 == 0;
@@ -877,7 +995,7 @@ struct Shape {
 
 // The buffer that the forward pass keeps: exp(z - m), the tiles' m, logp by list entry, and the list.
 struct SavedPlan {
-    size_t e, m, logp, idx, count, bytes;
+    size_t e, m, logp, idx, count, scales, bytes;
     explicit SavedPlan(const Shape& sh) {
         Bump b;
         e = b.take((sh.parts == 1 ? 2 : 4) * static_cast<size_t>(sh.tp) * sh.vp);
@@ -885,6 +1003,7 @@ struct SavedPlan {
         logp = b.take(sizeof(float) * static_cast<size_t>(sh.tp));
         idx = b.take(sizeof(int32_t) * static_cast<size_t>(sh.tp));
         count = b.take(sizeof(int32_t));
+        scales = b.take(2 * sizeof(float));
         bytes = b.at;
     }
 };
@@ -893,7 +1012,7 @@ struct ForwardPlan {
     Shape sh;
     bool few;
     int few_tiles;
-    size_t idx, count, hidden, head, m, s, zt, bytes;
+    size_t idx, count, hidden, head, m, s, zt, absmax, scales, bytes;
     explicit ForwardPlan(const muon_token_logp_args& a)
         : sh(a.tokens, a.cols, a.vocab, a.dtype, a.hidden, a.ld_hidden, a.head, a.ld_head) {
         few = a.tokens <= FEW_TOKENS && !a.saved;
@@ -908,6 +1027,8 @@ struct ForwardPlan {
         m = b.take(a.saved ? 0 : stats * sizeof(float));
         s = b.take(stats * sizeof(float));
         zt = b.take(sizeof(float) * sh.tp);
+        absmax = b.take(few || sh.parts == 1 ? 0 : sizeof(uint32_t) * (ABS_HEAD + ABS_HIDDEN));
+        scales = b.take(few || sh.parts == 1 ? 0 : 2 * sizeof(float));
         bytes = b.at;
     }
 };
@@ -933,7 +1054,7 @@ struct BackwardPlan {
     int64_t chunk;          // list entries at a time
     int chunks;
     GradPlan gh, gw;
-    size_t idx, count, hidden, head, head_t, hidden_t, dz, dzt, slab, slab_w, bytes;
+    size_t idx, count, hidden, head, head_t, hidden_t, dz, dzt, slab, slab_w, absmax, scales, bytes;
     static int64_t chunk_of(const Shape& sh) {
         const int64_t both = sizeof(uint16_t) * sh.parts * 2 * sh.vp;
         return std::min(sh.tp, std::max<int64_t>(PAD, DZ_BYTES / both / PAD * PAD));
@@ -954,6 +1075,8 @@ struct BackwardPlan {
         // the slab of grad_head lives through the chunks, so the two do not share one
         slab = b.take(a.grad_hidden ? gh.slab_bytes() : 0);
         slab_w = b.take(a.grad_head ? gw.slab_bytes() : 0);
+        absmax = b.take(sh.parts == 1 ? 0 : sizeof(uint32_t) * (ABS_HEAD + ABS_HIDDEN));
+        scales = b.take(sh.parts == 1 ? 0 : 3 * sizeof(float));
         bytes = b.at;
     }
 };
@@ -970,13 +1093,13 @@ hipError_t launch_pack(const PackArgs& p, int dtype, hipStream_t s) {
     const int64_t work = p.rows * static_cast<int64_t>(p.dst_ld / 8);
     const dim3 grid(static_cast<unsigned>(std::min<int64_t>(ceil_div(work, 256), 8 * CUS)));
     if (dtype == MUON_BF16) hipLaunchKernelGGL((pack_kernel<uint16_t, 1>), grid, dim3(256), 0, s, p);
-    else hipLaunchKernelGGL((pack_kernel<float, 3>), grid, dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((pack_kernel<float, 2>), grid, dim3(256), 0, s, p);
     return hipGetLastError();
 }
 
 template <int EDGE, int MODE> hipError_t launch_logits_edge(const LogitsArgs& l, int parts, hipStream_t s) {
     const dim3 grid(static_cast<unsigned>(l.ta) * l.tb), block(pt::Tile<EDGE>::THREADS);
-    if (parts == 3) hipLaunchKernelGGL((logits_kernel<EDGE, 3, MODE, false>), grid, block, 0, s, l);
+    if (parts == 2) hipLaunchKernelGGL((logits_kernel<EDGE, 2, MODE, false>), grid, block, 0, s, l);
     else if (l.tail < pt::CHUNKS) hipLaunchKernelGGL((logits_kernel<EDGE, 1, MODE, true>), grid, block, 0, s, l);
     else hipLaunchKernelGGL((logits_kernel<EDGE, 1, MODE, false>), grid, block, 0, s, l);
     return hipGetLastError();
@@ -988,7 +1111,7 @@ template <int MODE> hipError_t launch_logits(const LogitsArgs& l, int edge, int 
 template <int EDGE> hipError_t launch_grad_edge(const GradArgs& g, int parts, int dtype, bool last, hipStream_t s) {
     const dim3 grid(static_cast<unsigned>(g.ta) * g.tb, g.splits), block(pt::Tile<EDGE>::THREADS);
     if (parts == 1) hipLaunchKernelGGL((grad_kernel<EDGE, 1, uint16_t>), grid, block, 0, s, g);
-    else hipLaunchKernelGGL((grad_kernel<EDGE, 3, float>), grid, block, 0, s, g);
+    else hipLaunchKernelGGL((grad_kernel<EDGE, 2, float>), grid, block, 0, s, g);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !g.slab || !last) return e;
     const unsigned blocks = static_cast<unsigned>(g.ta) * g.tb * (EDGE / 32 * (EDGE / 32) / 4);
@@ -1009,6 +1132,21 @@ hipError_t launch_grad(GradArgs g, const GradPlan& pl, float* slab, int parts, i
         if (e_ != hipSuccess) return e_;   \
     } while (0)
 
+// Scales of fp32 operands (part NULL: known already) and of dz (dz NULL: not wanted).
+hipError_t launch_scales(const void* hidden, int64_t ld_hidden, const void* head, int64_t ld_head, const Shape& sh, const Live& live,
+                         uint32_t* part, float* operands, float* dz, const float* grad_logp, float scale, hipStream_t s) {
+    if (part) {
+        const AbsMaxArgs m{static_cast<const float*>(head), static_cast<const float*>(hidden), static_cast<size_t>(ld_head),
+                           static_cast<size_t>(ld_hidden), sh.vocab, sh.cols, live, part};
+        hipLaunchKernelGGL(absmax_kernel, dim3(ABS_HEAD + ABS_HIDDEN), dim3(256), 0, s, m);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    const ScalesArgs c{part, part ? operands : nullptr, dz, live, grad_logp, scale};
+    hipLaunchKernelGGL(scales_kernel, dim3(1), dim3(1024), 0, s, c);
+    return hipGetLastError();
+}
+
 // The logits' operands: packed copies where the products cannot read the caller's rows.
 hipError_t logits_operands(const Shape& sh, const void* hidden, int64_t ld_hidden, const void* head, int64_t ld_head,
                            int dtype, char* hidden_copy, char* head_copy, bool pack_head, LogitsArgs& l, hipStream_t s) {
@@ -1023,7 +1161,7 @@ hipError_t logits_operands(const Shape& sh, const void* hidden, int64_t ld_hidde
     l.a_part = row * sh.vocab;
     if (!sh.direct_head && pack_head)
         TL_TRY(launch_pack({head, static_cast<size_t>(ld_head), sh.vocab, sh.cols, 0, {}, reinterpret_cast<uint16_t*>(head_copy),
-                            static_cast<size_t>(sh.dp), static_cast<size_t>(sh.dp) * sh.vocab}, dtype, s));
+                            static_cast<size_t>(sh.dp), static_cast<size_t>(sh.dp) * sh.vocab, l.scales + 1}, dtype, s));
     l.gather = sh.direct_hidden;
     l.b = sh.direct_hidden ? static_cast<const char*>(hidden) : hidden_copy;
     l.b_ld = sh.direct_hidden ? 2 * static_cast<size_t>(ld_hidden) : row;
@@ -1031,7 +1169,7 @@ hipError_t logits_operands(const Shape& sh, const void* hidden, int64_t ld_hidde
     if (!sh.direct_hidden)
         TL_TRY(launch_pack({hidden, static_cast<size_t>(ld_hidden), l.live.most, sh.cols, 1, l.live,
                             reinterpret_cast<uint16_t*>(hidden_copy), static_cast<size_t>(sh.dp),
-                            static_cast<size_t>(sh.dp) * l.live.most}, dtype, s));
+                            static_cast<size_t>(sh.dp) * l.live.most, l.scales}, dtype, s));
     return hipSuccess;
 }
 
@@ -1090,6 +1228,12 @@ hipError_t launch_token_logp(const muon_token_logp_args& a, void* workspace, hip
     }
     TL_TRY(launch_live(a.targets, a.tokens, idx, count, a.logp, a.lse, s));
     l.live = {idx, count, 0, static_cast<int32_t>(sh.tp)};
+    if (sh.parts == 2) {
+        float* scales = reinterpret_cast<float*>(a.saved ? static_cast<char*>(a.saved) + SavedPlan(sh).scales : ws + pl.scales);
+        TL_TRY(launch_scales(a.hidden, a.ld_hidden, a.head, a.ld_head, sh, l.live, reinterpret_cast<uint32_t*>(ws + pl.absmax), scales,
+                             nullptr, nullptr, 0.0f, s));
+        l.scales = scales;
+    }
     TL_TRY(logits_operands(sh, a.hidden, a.ld_hidden, a.head, a.ld_head, a.dtype, ws + pl.hidden, ws + pl.head, true, l, s));
     l.targets = a.targets;
     l.tb = static_cast<int>(sh.tp / sh.edge);
@@ -1119,6 +1263,16 @@ hipError_t launch_token_logp_backward(const muon_token_logp_backward_args& a, vo
         count = reinterpret_cast<int32_t*>(ws + pl.count);
         TL_TRY(launch_live(a.targets, a.tokens, const_cast<int32_t*>(idx), const_cast<int32_t*>(count), nullptr, nullptr, s));
     }
+    // hidden and head: as the forward pass left them, or found again; dz: over all tokens, since chunks add up
+    const float *scales = nullptr, *dz_scale = nullptr;
+    if (sh.parts == 2) {
+        float* own = reinterpret_cast<float*>(ws + pl.scales);
+        const bool known = saved && a.tokens > 0;
+        scales = known ? reinterpret_cast<const float*>(saved + sv.scales) : own;
+        dz_scale = own + 2;
+        TL_TRY(launch_scales(a.hidden, a.ld_hidden, a.head, a.ld_head, sh, {idx, count, 0, static_cast<int32_t>(sh.tp)},
+                             known ? nullptr : reinterpret_cast<uint32_t*>(ws + pl.absmax), own, own + 2, a.grad_logp, a.scale, s));
+    }
     const size_t vp = sh.vp, dz_part = static_cast<size_t>(pl.chunk) * vp;
     uint16_t* dz = a.grad_hidden ? reinterpret_cast<uint16_t*>(ws + pl.dz) : nullptr;
     uint16_t* dzt = a.grad_head ? reinterpret_cast<uint16_t*>(ws + pl.dzt) : nullptr;
@@ -1128,7 +1282,7 @@ hipError_t launch_token_logp_backward(const muon_token_logp_backward_args& a, vo
         const int col_tiles = static_cast<int>(ceil_div(sh.cols, 64));
         if (a.grad_hidden && c == 0) {
             p.head = {a.head, static_cast<size_t>(a.ld_head), sh.vocab, sh.cols, 0, {}, reinterpret_cast<uint16_t*>(ws + pl.head_t),
-                      vp, vp * sh.cols};
+                      vp, vp * sh.cols, scales ? scales + 1 : nullptr};
             p.head_rows = static_cast<int>(ceil_div(sh.vocab, 64));
             p.head_blocks = p.head_rows * col_tiles;
             p.targets = a.targets;
@@ -1141,28 +1295,30 @@ hipError_t launch_token_logp_backward(const muon_token_logp_backward_args& a, vo
         if (a.grad_head) {
             p.hidden = {a.hidden, static_cast<size_t>(a.ld_hidden), pl.chunk, sh.cols, 1, live,
                         reinterpret_cast<uint16_t*>(ws + pl.hidden_t), static_cast<size_t>(pl.chunk),
-                        static_cast<size_t>(pl.chunk) * sh.cols};
+                        static_cast<size_t>(pl.chunk) * sh.cols, scales};
             p.hidden_rows = static_cast<int>(pl.chunk / 64);
             p.hidden_blocks = p.hidden_rows * col_tiles;
         }
         const int prepare = p.head_blocks + p.hidden_blocks + p.zero_blocks;
         if (prepare > 0) {
             if (sh.parts == 1) hipLaunchKernelGGL((prepare_kernel<uint16_t, 1>), dim3(prepare), dim3(256), 0, s, p);
-            else hipLaunchKernelGGL((prepare_kernel<float, 3>), dim3(prepare), dim3(256), 0, s, p);
+            else hipLaunchKernelGGL((prepare_kernel<float, 2>), dim3(prepare), dim3(256), 0, s, p);
             TL_TRY(hipGetLastError());
         }
         if (saved) {
             const DzArgs d{saved + sv.e, reinterpret_cast<const float*>(saved + sv.m),
                            reinterpret_cast<const float*>(saved + sv.logp), static_cast<size_t>(sh.tp), sh.edge, live,
                            a.targets, a.lse, a.grad_logp, a.scale, static_cast<int>(a.vocab), vp,
-                           static_cast<size_t>(pl.chunk), dz, dzt, dz_part, dz_part};
+                           static_cast<size_t>(pl.chunk), dz, dzt, dz_part, dz_part, dz_scale};
             const dim3 grid(static_cast<unsigned>(vp / 64), static_cast<unsigned>(pl.chunk / 64));
             if (sh.parts == 1) hipLaunchKernelGGL((dz_kernel<uint16_t, 1>), grid, dim3(256), 0, s, d);
-            else hipLaunchKernelGGL((dz_kernel<float, 3>), grid, dim3(256), 0, s, d);
+            else hipLaunchKernelGGL((dz_kernel<float, 2>), grid, dim3(256), 0, s, d);
             TL_TRY(hipGetLastError());
         } else {
             LogitsArgs l{};
             l.live = live;
+            l.scales = scales;
+            l.dz_scale = dz_scale;
             TL_TRY(logits_operands(sh, a.hidden, a.ld_hidden, a.head, a.ld_head, a.dtype, ws + pl.hidden, ws + pl.head, c == 0, l, s));
             l.targets = a.targets;
             l.tb = static_cast<int>(pl.chunk / sh.edge);
@@ -1180,7 +1336,9 @@ hipError_t launch_token_logp_backward(const muon_token_logp_backward_args& a, vo
         GradArgs g{};
         g.live = live;
         g.cols = static_cast<int>(sh.cols);
+        g.dz_scale = dz_scale;
         if (a.grad_hidden) {
+            g.scale = scales ? scales + 1 : nullptr;
             g.a = ws + pl.head_t;
             g.a_ld = 2 * vp;
             g.a_part = 2 * vp * sh.cols;
@@ -1194,6 +1352,7 @@ hipError_t launch_token_logp_backward(const muon_token_logp_backward_args& a, vo
             TL_TRY(launch_grad(g, pl.gh, reinterpret_cast<float*>(ws + pl.slab), sh.parts, a.dtype, true, s));
         }
         if (a.grad_head) {
+            g.scale = scales;
             g.a = ws + pl.hidden_t;
             g.a_ld = 2 * static_cast<size_t>(pl.chunk);
             g.a_part = g.a_ld * sh.cols;

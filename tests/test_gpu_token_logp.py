@@ -273,6 +273,33 @@ def test_token_logp_in_a_graph_and_on_another_stream(gpu_lib):
         h, w, y, c = _inputs(10, 300, 256, 1111, "bf16")
 
 
+@pytest.mark.parametrize("hs,ws", [(1e-20, 1e18), (1e12, 1e-13), (2e-38, 1e36)])
+@pytest.mark.parametrize("t", [20, 150])
+def test_token_logp_fp32_magnitudes(gpu_lib, t, hs, ws):
+    # the logits of ordinary size from operands far from it, and a gradient of 1e-15; then one huge entry of head that
+    # meets zeros of hidden
+    import torch
+    h, w, y, c = _inputs(23, t, 96, 1500, "f32")
+    h, w, c = h * hs, w * ws, c * 1e-15
+    scale = 1.0 / (np.float64(hs) * ws)
+    for big in (False, True):
+        if big and 1e6 * ws > 3e38:
+            break                                              # not an fp32 value
+        if big:
+            h[:, 5] = 0
+            w[7, 5] = 1e6 * ws
+        saved = _saved(gpu_lib, h, w)
+        logp, lse = _forward(gpu_lib, h, w, y, scale, saved=saved)
+        hv, wv = _np(h) / hs, _np(w) / ws                      # the same problem in ordinary size
+        rl, _, _ = to.token_logp(hv, wv, np.asarray(y.cpu()), scale=np.float32(scale) * np.float64(hs) * ws)
+        assert np.all(np.abs(_np(logp) - rl) <= 1e-4)
+        gh, gw = _backward(gpu_lib, h, w, y, lse, c, scale, saved=saved)
+        rh, rw, _, _ = to.token_logp_backward(hv, wv, np.asarray(y.cpu()), _np(c), scale=1.0)
+        for got, ref in ((gh, rh / hs), (gw, rw / ws)):
+            g, ref = _np(got), ref.astype(np.float32).astype(np.float64)   # 1e-56 is 0 in fp32
+            assert np.linalg.norm(g - ref) <= 1e-4 * np.linalg.norm(ref)
+
+
 # products with enough 256 x 256 tiles for the chip (the shapes above take the smaller tile), widths that end inside a k-step
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("t,d,v", [(600, 72, 20000), (520, 1100, 16500), (1500, 136, 8200)])
