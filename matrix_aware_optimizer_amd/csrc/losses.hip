@@ -316,7 +316,9 @@ template <typename T> __global__ __launch_bounds__(LS_ONE) void preference_one_k
 
 // ---- policy -----------------------------------------------------------------
 
-constexpr int PL_SUMS = 5;   // weighted loss, KL, held, rho, counted tokens
+// Weighted loss, KL, held, rho, counted tokens.  Summed in fp64: gains of both signs cancel, and fp32 sums
+// of 32616 tokens lost 1.3e-6 of a loss near 0.
+constexpr int PL_SUMS = 5;
 
 template <typename OFF> struct PolicyState {
     muon_policy_args a;
@@ -339,21 +341,21 @@ template <typename S> __device__ __forceinline__ void policy_unit_counts(const S
     });
 }
 
-struct PolicyToken { float loss, grad, kl, held, rho; };
+struct PolicyToken { double loss; float grad, kl, rho; bool held; };
 
+// The ratio is taken as 1 + expm1, put together in fp64: near 1 a rounded ratio alone would cost a loss that is small against
+// its terms its last digits.
 __device__ __forceinline__ PolicyToken policy_token(const muon_policy_args& a, float lp, float old, float ref, float adv) {
     const float lo = 1.0f - a.clip_low, hi = 1.0f + a.clip_high;
     PolicyToken o;
-    o.rho = expf(lp - old);
-    float gain = fminf(o.rho * adv, fminf(fmaxf(o.rho, lo), hi) * adv);
-    bool held = (adv > 0.0f && o.rho > hi) || (adv < 0.0f && o.rho < lo);
-    if (a.dual_clip > 0.0f && adv < 0.0f && o.rho > a.dual_clip) {
-        gain = a.dual_clip * adv;
-        held = true;
-    }
-    o.held = held ? 1.0f : 0.0f;
-    o.loss = -gain;
-    o.grad = held ? 0.0f : -o.rho * adv;
+    float em = expm1f(lp - old);
+    o.rho = 1.0f + em;
+    const bool above = adv > 0.0f && o.rho > hi, below = adv < 0.0f && o.rho < lo;
+    const bool dual = a.dual_clip > 0.0f && adv < 0.0f && o.rho > a.dual_clip;
+    em = above ? a.clip_high : below ? -a.clip_low : em;
+    o.held = above || below || dual;
+    o.loss = -(dual ? static_cast<double>(a.dual_clip) : 1.0 + static_cast<double>(em)) * static_cast<double>(adv);
+    o.grad = o.held ? 0.0f : -o.rho * adv;
     o.kl = 0.0f;
     if (a.kl != MUON_KL_NONE) {
         const float q = ref - lp;
@@ -361,7 +363,7 @@ __device__ __forceinline__ PolicyToken policy_token(const muon_policy_args& a, f
         if (a.kl == MUON_KL_K1) { o.kl = -q; dk = 1.0f; }
         else if (a.kl == MUON_KL_K2) { o.kl = 0.5f * q * q; dk = -q; }
         else { const float em = expm1f(q); o.kl = em - q; dk = -em; }
-        o.loss = fmaf(a.kl_coef, o.kl, o.loss);
+        o.loss = fma(static_cast<double>(a.kl_coef), static_cast<double>(o.kl), o.loss);
         o.grad = fmaf(a.kl_coef, dk, o.grad);
     }
     return o;
@@ -415,19 +417,24 @@ __device__ __forceinline__ void policy_weights(const S& st, int u, const float* 
 }
 
 // The tokens' sums, and their gradients before the common factor.
-__device__ __forceinline__ void policy_tokens(const muon_policy_args& a, const PolicyTokens& k, float (&v)[PL_SUMS], float (&g)[PER]) {
+__device__ __forceinline__ void policy_tokens(const muon_policy_args& a, const PolicyTokens& k, double (&v)[PL_SUMS], float (&g)[PER]) {
+    float kl = 0.0f, rho = 0.0f;
+    int held = 0;
 #pragma unroll
     for (int e = 0; e < PER; ++e) {
         g[e] = 0.0f;
         if (!(k.counted >> e & 1u)) continue;
         const PolicyToken o = policy_token(a, k.lp[e], k.old[e], k.ref[e], k.adv[e]);
-        v[0] = fmaf(k.wt[e], o.loss, v[0]);
-        v[1] += o.kl;
-        v[2] += o.held;
-        v[3] += o.rho;
-        v[4] += 1.0f;
+        v[0] = fma(static_cast<double>(k.wt[e]), o.loss, v[0]);
+        kl += o.kl;
+        rho += o.rho;
+        held += o.held;
         g[e] = k.wt[e] * o.grad;
     }
+    v[1] += kl;
+    v[2] += held;
+    v[3] += rho;
+    v[4] += __popc(k.counted);
 }
 template <typename T>
 __device__ __forceinline__ void policy_store(const muon_policy_args& a, int u, float factor, float (&g)[PER]) {
@@ -437,14 +444,14 @@ __device__ __forceinline__ void policy_store(const muon_policy_args& a, int u, f
 }
 
 // v: the sums over everything.
-__device__ __forceinline__ void policy_write(const muon_policy_args& a, const float (&v)[PL_SUMS]) {
-    const float per = 1.0f / fmaxf(v[4], 1.0f);
-    *a.loss = a.reduction == MUON_REDUCE_SEQUENCE ? v[0] : v[0] * per;
+__device__ __forceinline__ void policy_write(const muon_policy_args& a, const double (&v)[PL_SUMS]) {
+    const double per = 1.0 / fmax(v[4], 1.0);
+    *a.loss = static_cast<float>(a.reduction == MUON_REDUCE_SEQUENCE ? v[0] : v[0] * per);
     if (!a.stats) return;
-    a.stats[0] = v[1] * per;
-    a.stats[1] = v[2] * per;
-    a.stats[2] = v[3] * per;
-    a.stats[3] = v[4];
+    a.stats[0] = static_cast<float>(v[1] * per);
+    a.stats[1] = static_cast<float>(v[2] * per);
+    a.stats[2] = static_cast<float>(v[3] * per);
+    a.stats[3] = static_cast<float>(v[4]);
 }
 
 // With a mask: the counted tokens of all sequences, one partial a workgroup, or of each one's units.
@@ -466,13 +473,13 @@ __global__ __launch_bounds__(LS_THREADS) void policy_counts_kernel(PolicyState<i
 
 // counts: `parts` partial counts (token mean with a mask).  sums: PL_SUMS by workgroup.
 template <typename T>
-__global__ __launch_bounds__(LS_THREADS) void policy_main_kernel(PolicyState<int64_t> st, const float* counts, int parts, float* sums) {
+__global__ __launch_bounds__(LS_THREADS, LS_GRID / 256) void policy_main_kernel(PolicyState<int64_t> st, const float* counts, int parts, double* sums) {
     constexpr int W = LS_THREADS / 64;
-    __shared__ float red[PL_SUMS * W];
+    __shared__ double red[PL_SUMS * W];
     const muon_policy_args& a = st.a;
     float factor = 0.0f;
     bool known = false;
-    float v[PL_SUMS] = {};
+    double v[PL_SUMS] = {};
     for (int u = blockIdx.x * W + wave_index(); u < st.units(); u += gridDim.x * W) {
         PolicyTokens k;
         k.load<T>(a, u * UNIT + PER * lane_id());
@@ -502,9 +509,9 @@ __global__ __launch_bounds__(LS_THREADS) void policy_main_kernel(PolicyState<int
         for (int k = 0; k < PL_SUMS; ++k) sums[PL_SUMS * blockIdx.x + k] = v[k];
 }
 
-__global__ __launch_bounds__(LS_THREADS) void policy_final_kernel(muon_policy_args a, const float* sums, int blocks) {
-    __shared__ float red[PL_SUMS * LS_THREADS / 64];
-    float v[PL_SUMS] = {};
+__global__ __launch_bounds__(LS_THREADS) void policy_final_kernel(muon_policy_args a, const double* sums, int blocks) {
+    __shared__ double red[PL_SUMS * LS_THREADS / 64];
+    double v[PL_SUMS] = {};
 #pragma unroll 4
     for (int b = threadIdx.x; b < blocks; b += LS_THREADS)
 #pragma unroll
@@ -515,7 +522,7 @@ __global__ __launch_bounds__(LS_THREADS) void policy_final_kernel(muon_policy_ar
 
 template <typename T> __global__ __launch_bounds__(LS_ONE) void policy_one_kernel(muon_policy_args a) {
     constexpr int W = LS_ONE / 64;
-    __shared__ float red[PL_SUMS * W];
+    __shared__ double red[PL_SUMS * W];
     __shared__ int offsets[LS_SMALL_SEQS + 1];
     __shared__ float head[W], tail[W], own[LS_SMALL_SEQS], adv[LS_SMALL_SEQS];
     const int u = wave_index();
@@ -530,13 +537,14 @@ template <typename T> __global__ __launch_bounds__(LS_ONE) void policy_one_kerne
         if (u < st.units()) policy_unit_counts(st, u, k.live);
         __syncthreads();
     }
-    float v[PL_SUMS] = {}, g[PER] = {};
+    double v[PL_SUMS] = {};
+    float g[PER] = {};
     if (u < st.units()) {
         policy_weights(st, u, adv, k);
         policy_tokens(a, k, v, g);
     }
     block_sums(v, red);
-    if (a.grad_logp && u < st.units()) policy_store<T>(a, u, st.by_sequence() ? a.grad_scale : a.grad_scale / fmaxf(v[4], 1.0f), g);
+    if (a.grad_logp && u < st.units()) policy_store<T>(a, u, st.by_sequence() ? a.grad_scale : a.grad_scale / fmaxf(static_cast<float>(v[4]), 1.0f), g);
     if (threadIdx.x == 0) policy_write(a, v);
 }
 
@@ -583,7 +591,7 @@ hipError_t launch_preference(const muon_preference_args& a, void* workspace, hip
 
 size_t policy_bytes(const muon_policy_args& a) {
     const size_t q = static_cast<size_t>(a.sequences), u = static_cast<size_t>(units_of(a.tokens));
-    return (2 * u + q + LS_COUNTS + PL_SUMS * LS_GRID) * sizeof(float);
+    return PL_SUMS * LS_GRID * sizeof(double) + (2 * u + q + LS_COUNTS) * sizeof(float);
 }
 
 hipError_t launch_policy(const muon_policy_args& a, void* workspace, hipStream_t s) {
@@ -594,9 +602,9 @@ hipError_t launch_policy(const muon_policy_args& a, void* workspace, hipStream_t
         return hipGetLastError();
     }
     const size_t q = static_cast<size_t>(a.sequences), u = static_cast<size_t>(units_of(a.tokens));
-    float* f = static_cast<float*>(workspace);
+    double* sums = static_cast<double*>(workspace);
+    float* f = reinterpret_cast<float*>(sums + PL_SUMS * LS_GRID);
     float* counts = f + 2 * u + q;
-    float* sums = counts + LS_COUNTS;
     const PolicyState<int64_t> st{a, {a.offsets, static_cast<int>(a.sequences), static_cast<int>(a.tokens)}, {f, f + u, f + 2 * u}};
     hipError_t e = hipSuccess;
     int parts = 0;

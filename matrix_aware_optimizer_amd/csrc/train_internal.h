@@ -90,9 +90,26 @@ __device__ __forceinline__ float wave_sum(float v) {
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
-// Sum over a workgroup, given to every thread; `red` holds a float per wave.  The order of the
+template <int CTRL, int ROWS> __device__ __forceinline__ double dpp_add(double v) {
+    const unsigned long long b = __double_as_longlong(v);
+    const int lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(b), CTRL, ROWS, 0xF, false);
+    const int hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(b >> 32), CTRL, ROWS, 0xF, false);
+    return v + __hiloint2double(hi, lo);
+}
+__device__ __forceinline__ double wave_sum(double v) {
+    v = dpp_add<0x111, 0xF>(v);
+    v = dpp_add<0x112, 0xF>(v);
+    v = dpp_add<0x114, 0xF>(v);
+    v = dpp_add<0x118, 0xF>(v);
+    v = dpp_add<0x142, 0xA>(v);
+    v = dpp_add<0x143, 0xC>(v);
+    const unsigned long long b = __double_as_longlong(v);
+    return __hiloint2double(__builtin_amdgcn_readlane(static_cast<int>(b >> 32), 63), __builtin_amdgcn_readlane(static_cast<int>(b), 63));
+}
+
+// Sums over a workgroup, given to every thread; `red` holds a value of each sum per wave.  The order of the
 // additions is fixed.  Safe to call again at once with the same `red`.
-template <int N> __device__ __forceinline__ void block_sums(float (&v)[N], float* red) {
+template <int N, typename V> __device__ __forceinline__ void block_sums(V (&v)[N], V* red) {
     const int waves = blockDim.x >> 6;
 #pragma unroll
     for (int k = 0; k < N; ++k) v[k] = wave_sum(v[k]);
