@@ -334,11 +334,13 @@ muon_status muon_token_logp(const muon_token_logp_args* args, void* workspace, s
  *   dz_ij = c_i ([j = target_i] - p_ij),  grad_hidden = dz head,  grad_head = dz^T hidden
  * grad_hidden or grad_head may be NULL (not wanted), not both.  `saved` is what
  * muon_token_logp kept for the same inputs, or NULL.  dz is rounded to the
- * operands' precision before the two products: bf16, or 22 bits for fp32.
+ * operands' precision before the two products: bf16 (up to 64 tokens: two bf16
+ * parts, 2^-16), or 22 bits for fp32.
  *
- * Precision in fp32: the products (not those of up to 64 tokens without `saved`)
- * take each operand as two fp16 parts under one power-of-two scale, 22 bits for
- * values down to 2^-28 of the operand's largest finite one, fewer below. */
+ * Precision in fp32: the products take each operand as two fp16 parts under one
+ * power-of-two scale, 22 bits for values down to 2^-28 of the operand's largest
+ * finite one, fewer below.  Those of a forward pass over up to 64 tokens without
+ * `saved` take three bf16 parts, 24 bits for values down to 2^-109. */
 typedef struct {
     const void*    hidden;
     const void*    head;

@@ -329,7 +329,7 @@ template <int EDGE> struct Tile {
     static constexpr int STACKED = EDGE / (32 * SM);
     static __device__ __forceinline__ int stack_place() { return share_row(wave_id()) / (32 * SM); }
 
-    // Staging as bf16: column c at 2 EDGE c bytes, its rows in units of 4 (8 bytes), unit u at
+    // Staging as 16-bit values: column c at 2 EDGE c bytes, its rows in units of 4 (8 bytes), unit u at
     // position u ^ csw(c): a lane's 4 rows are one write, free of bank conflicts, a column is read
     // back in order (16 bytes = 8 rows) and a row through transpose reads.
     static __device__ __forceinline__ int csw(int c) { return (c & 31) ^ (((c >> 5) & 1) << 2); }
@@ -354,6 +354,19 @@ template <int EDGE> struct Tile {
                     for (int g = 0; g < 4; ++g)
                         put(L, i, j, g, pack_bf16x2(acc[i][j][4 * g], acc[i][j][4 * g + 1]),
                             pack_bf16x2(acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]));
+        }
+        __device__ __forceinline__ void put_all_f16(lds_byte_t* L, const Acc& acc) const {
+            typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+            auto two = [](float a, float b) {
+                return __builtin_bit_cast(unsigned, f16x2_t{static_cast<_Float16>(a), static_cast<_Float16>(b)});
+            };
+#pragma unroll
+            for (int i = 0; i < SM; ++i)
+#pragma unroll
+                for (int j = 0; j < SN; ++j)
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+                        put(L, i, j, g, two(acc[i][j][4 * g], acc[i][j][4 * g + 1]), two(acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]));
         }
     };
     // Rows 8 q .. 8 q + 7 of column c.
@@ -397,6 +410,17 @@ template <int EDGE> struct Tile {
         return *(const lds_u32x4_t*)(L + ((c % 128) * (4 * EDGE) + 16 * (u ^ (c & 31))));
     }
 };
+
+// Takes two operands' scales, powers of two, out of their product at once: either alone might leave fp32's range.
+template <typename TL> __device__ __forceinline__ void unscale(typename TL::Acc& acc, float sa, float sb) {
+    const int e = 254 - static_cast<int>((__float_as_uint(sa) >> 23) + (__float_as_uint(sb) >> 23));
+#pragma unroll
+    for (int i = 0; i < TL::SM; ++i)
+#pragma unroll
+        for (int j = 0; j < TL::SN; ++j)
+#pragma unroll
+            for (int q = 0; q < 16; ++q) acc[i][j][q] = __builtin_amdgcn_ldexpf(acc[i][j][q], e);
+}
 
 // Tiles in runs of 32 on one XCD (the hardware deals workgroups round-robin over the 8), a
 // bijection on [0, nb): a run is a 4 x 8 block of tiles whose operand panels share an L2.

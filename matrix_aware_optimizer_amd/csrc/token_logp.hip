@@ -20,12 +20,14 @@
 //    tiles, added in order by slab_sum_kernel.
 //  - fp32 operands travel as two fp16 parts under a scale (product_tile.h), dz in fp32 calls too: absmax_kernel and
 //    scales_kernel find the scales.
-//  - Few tokens: few_kernel reads the head once with 16 x 16 MFMAs and no staging (fp32 as three bf16 parts
-//    there, which need no scale).
+//  - Few tokens: what counts is the head's way through memory, so each step reads (or writes) it once where it is,
+//    with 16 x 16 MFMAs and no staging (fp32 as three bf16 parts there, which need no scale).
 //
-// The statistics are kept in base 2 (z2 = z log2(e)): one multiplication and v_exp_f32.  A target's
-// own term stays out of the sum S of its token, logp = -log(1 + S 2^(M - z2_target)), which keeps its
-// relative precision as logp goes to 0.
+// The softmax works in base 2: with k' = |scale| log2(e) and acc the product (negated if scale is negative) a tile keeps
+// M = k' max acc, rounded, and sums 2^(k' acc - M), the exponent formed by one fused operation: what M is rounded to
+// cancels, where a rounded k' acc would lose a unit of its own size.  A target's acc is kept as it is and its own term
+// stays out of the sum S of its token, logp = -log(1 + S 2^(M - k' acc_target)), which keeps its relative precision as
+// logp goes to 0.
 #include <algorithm>
 
 #include "product_tile.h"
@@ -62,6 +64,10 @@ template <int PARTS> __device__ __forceinline__ void to_parts(float x, float sca
     if constexpr (PARTS == 1) p[0] = f32_to_bf16(x);
     else split2(x * scale, p);
 }
+
+// k' of the comment above; scale 0 as a number so small that it makes no difference, so that k' times minus infinity stays so.
+__device__ __forceinline__ float rate_of(float scale2) { return fmaxf(fabsf(scale2), 1.17549435e-38f); }
+__device__ __forceinline__ float shown(float m) { return m == -INFINITY ? 0.0f : m; }   // an M to subtract
 
 // ---------------------------------------------------------------------------
 // The scored tokens, in order
@@ -289,6 +295,7 @@ template <typename T, int PARTS> __global__ __launch_bounds__(256) void prepare_
     __shared__ float tile[64][65];
     int b = blockIdx.x;
     if (b < a.head_blocks) {
+        if (a.head.live.rows() == 0) return;   // nothing will read it
         transpose_tile<T, PARTS>(a.head, static_cast<int64_t>(b % a.head_rows) * 64, static_cast<int64_t>(b / a.head_rows) * 64, tile);
         return;
     }
@@ -320,9 +327,9 @@ struct LogitsArgs {
     int vocab, steps, tail, ta, tb;   // tail: 16-byte chunks of the last k-step
     float scale2;           // scale log2(e)
     const float* scales;    // two parts: of hidden and head
-    float *m, *s, *zt;      // statistics: tile x list entry (pitch rows_pitch); target logit by list entry
+    float *m, *s, *zt;      // M and S: tile x list entry (pitch rows_pitch); target's acc by list entry
     size_t rows_pitch;
-    void* e;                // LG_SAVE: exp(z - m), list entry x vocabulary (pitch vp)
+    void* e;                // LG_SAVE: 2^(k' acc - M), list entry x vocabulary (pitch vp), fp16 (bf16 operands) or fp32
     // LG_DZ
     const float *lse, *grad_logp;
     float scale;
@@ -332,12 +339,14 @@ struct LogitsArgs {
     size_t vp;
 };
 
-// The staged tile's columns as rows of `dst` (from its column v0), column c at row r0 + c.
-template <typename TL> __device__ __forceinline__ void store_cols(const pt::lds_byte_t* L, uint16_t* dst, size_t ld, size_t r0, size_t v0) {
+// The staged tile's first `rows` columns as rows of `dst` (from its column v0), column c at row r0 + c.
+template <typename TL>
+__device__ __forceinline__ void store_cols(const pt::lds_byte_t* L, uint16_t* dst, size_t ld, size_t r0, size_t v0, int rows) {
     constexpr int Q = TL::SIZE / 8, PER = TL::THREADS / Q;   // chunks of a column, columns at a time
 #pragma unroll 4
     for (int k = 0; k < TL::SIZE / PER; ++k) {
         const int c = PER * k + static_cast<int>(threadIdx.x) / Q, q = threadIdx.x % Q;
+        if (c >= rows) return;
         __builtin_nontemporal_store(TL::stage_col8(L, c, q), G(reinterpret_cast<u32x4*>(dst + (r0 + c) * ld + v0 + 8 * q)));
     }
 }
@@ -379,8 +388,14 @@ __global__ __launch_bounds__(pt::Tile<EDGE>::THREADS, 2) void logits_kernel(Logi
     const int place = TL::stack_place(), h = (threadIdx.x >> 5) & 1;
     const int vl = v0 + TL::first_row();              // this lane's first vocabulary entry
     const bool edge = v0 + EDGE > a.vocab;            // uniform: entries past the vocabulary
-    // z2 = (acc k1) k2: the operands' scales taken out one by one, so that neither factor leaves fp32's range
-    const float k1 = PARTS == 1 ? 1.0f : 1.0f / a.scales[0], k2 = PARTS == 1 ? a.scale2 : a.scale2 / a.scales[1];
+    const float k = rate_of(a.scale2);
+    if constexpr (PARTS == 2) pt::unscale<TL>(acc, a.scales[0], a.scales[1]);
+    if (a.scale2 < 0.0f) {
+#pragma unroll
+        for (int i = 0; i < TL::SM; ++i)
+#pragma unroll
+            for (int j = 0; j < TL::SN; ++j) acc[i][j] = -acc[i][j];
+    }
     lds_barrier();                                    // every wave is done with the operand slabs
 
     if constexpr (MODE != LG_DZ) {
@@ -395,16 +410,17 @@ __global__ __launch_bounds__(pt::Tile<EDGE>::THREADS, 2) void logits_kernel(Logi
             const int64_t t = a.targets[a.live.idx[a.live.first + r]];
             y[j] = t < a.vocab ? static_cast<int>(t) - vl : -1;
             mx[j] = -INFINITY;
+            if (edge) {
+#pragma unroll
+                for (int i = 0; i < TL::SM; ++i)
+#pragma unroll
+                    for (int q = 0; q < 16; ++q)
+                        if (vl + 32 * i + 8 * (q >> 2) + (q & 3) >= a.vocab) acc[i][j][q] = -INFINITY;
+            }
 #pragma unroll
             for (int i = 0; i < TL::SM; ++i)
 #pragma unroll
-                for (int q = 0; q < 16; ++q) {
-                    const int dv = 32 * i + 8 * (q >> 2) + (q & 3);
-                    float z = acc[i][j][q] * k1 * k2;
-                    if (edge && vl + dv >= a.vocab) z = -INFINITY;
-                    acc[i][j][q] = z;
-                    mx[j] = fmaxf(mx[j], z);
-                }
+                for (int q = 0; q < 16; ++q) mx[j] = fmaxf(mx[j], acc[i][j][q]);
             mx[j] = fmaxf(mx[j], __shfl_xor(mx[j], 32, 64));
             if (h == 0) smax[EDGE * place + col[j]] = mx[j];
         }
@@ -413,7 +429,8 @@ __global__ __launch_bounds__(pt::Tile<EDGE>::THREADS, 2) void logits_kernel(Logi
         for (int j = 0; j < TL::SN; ++j) {
 #pragma unroll
             for (int p = 0; p < TL::STACKED; ++p) mx[j] = fmaxf(mx[j], smax[EDGE * p + col[j]]);
-            const float base = mx[j] == -INFINITY ? 0.0f : mx[j];
+            mx[j] *= k;
+            const float base = shown(mx[j]);
             float sum = 0.0f, zt = 0.0f;
             bool mine = false;
 #pragma unroll
@@ -421,7 +438,7 @@ __global__ __launch_bounds__(pt::Tile<EDGE>::THREADS, 2) void logits_kernel(Logi
 #pragma unroll
                 for (int q = 0; q < 16; ++q) {
                     const int dv = 32 * i + 8 * (q >> 2) + (q & 3);
-                    const float z = acc[i][j][q], ex = __builtin_amdgcn_exp2f(z - base);
+                    const float z = acc[i][j][q], ex = __builtin_amdgcn_exp2f(fmaf(z, k, -base));
                     const bool target = dv == y[j];
                     sum += target ? 0.0f : ex;
                     if (target) { zt = z; mine = true; }
@@ -446,9 +463,9 @@ __global__ __launch_bounds__(pt::Tile<EDGE>::THREADS, 2) void logits_kernel(Logi
             if constexpr (PARTS == 1) {
                 lds_barrier();
                 const typename TL::Stage st;
-                st.put_all(L, acc);
+                st.put_all_f16(L, acc);
                 lds_barrier();
-                store_cols<TL>(L, static_cast<uint16_t*>(a.e), a.vp, r0, v0);
+                store_cols<TL>(L, static_cast<uint16_t*>(a.e), a.vp, r0, v0, n - r0);
             } else {
                 float* e = static_cast<float*>(a.e);
                 for (int pass = 0; pass < TL::F32_PASSES; ++pass) {
@@ -459,6 +476,7 @@ __global__ __launch_bounds__(pt::Tile<EDGE>::THREADS, 2) void logits_kernel(Logi
 #pragma unroll 4
                     for (int k = 0; k < 128 / PER; ++k) {
                         const int c = 128 * pass + PER * k + static_cast<int>(threadIdx.x) / Q, q = threadIdx.x % Q;
+                        if (r0 + c >= n) break;
                         __builtin_nontemporal_store(TL::stage_f32(L, c, q),
                                                     G(reinterpret_cast<u32x4*>(e + (static_cast<size_t>(r0) + c) * a.vp + v0 + 4 * q)));
                     }
@@ -479,7 +497,7 @@ __global__ __launch_bounds__(pt::Tile<EDGE>::THREADS, 2) void logits_kernel(Logi
 #pragma unroll
                 for (int q = 0; q < 16; ++q) {
                     const int dv = 32 * i + 8 * (q >> 2) + (q & 3);
-                    const float p = __builtin_amdgcn_exp2f(fmaf(acc[i][j][q] * k1, k2, -l2));
+                    const float p = __builtin_amdgcn_exp2f(fmaf(acc[i][j][q], k, -l2));
                     float d = c * ((dv == y ? 1.0f : 0.0f) - p);
                     if (c == 0.0f || (edge && vl + dv >= a.vocab)) d = 0.0f;
                     acc[i][j][q] = d;
@@ -504,14 +522,14 @@ __global__ __launch_bounds__(pt::Tile<EDGE>::THREADS, 2) void logits_kernel(Logi
                                 const float x = acc[i][j][4 * g + e] * (p == 0 ? ds : 1.0f / pt::LO_STEP);
                                 const _Float16 hi = static_cast<_Float16>(x);
                                 const float f = static_cast<float>(hi);
-                                if (p == 0) acc[i][j][4 * g + e] = fabsf(f) < INFINITY ? x - f : 0.0f;
                                 w[e] = __builtin_bit_cast(uint16_t, hi);
+                                if (p == 0) acc[i][j][4 * g + e] = fabsf(f) < INFINITY ? x - f : 0.0f;
                             }
                             st.put(L, i, j, g, w[0] | w[1] << 16, w[2] | w[3] << 16);
                         }
             }
             lds_barrier();
-            if (a.dz) store_cols<TL>(L, a.dz + p * a.dz_part, a.vp, r0, v0);
+            if (a.dz) store_cols<TL>(L, a.dz + p * a.dz_part, a.vp, r0, v0, n - r0);
             if (a.dzt) store_rows<TL>(L, a.dzt + p * a.dzt_part, a.rows_pitch, v0, r0);
         }
     }
@@ -524,7 +542,8 @@ __global__ __launch_bounds__(pt::Tile<EDGE>::THREADS, 2) void logits_kernel(Logi
 struct DzArgs {
     const void* e;          // list entry x vocabulary, pitch vp
     const float* m;         // tile x list entry
-    const float* logp;      // list entry
+    const float *logp, *ref, *shift;   // list entry: logp, and p = e 2^(M - k' ref + shift)
+    float scale2;
     size_t m_pitch;
     int m_edge;             // vocabulary entries per tile
     Live live;
@@ -538,15 +557,17 @@ struct DzArgs {
     const float* dz_scale;  // two parts
 };
 
-// 64 tokens x 64 entries a workgroup.  Reads 2 (fp32: 4) bytes an element and writes 2 x 2 (2 x 6), HBM-bound.
-template <typename T, int PARTS>
+// 64 tokens x 64 entries a workgroup.  Reads 2 (fp32: 4) bytes an element and writes 2 x 2 (fp32: 2 x 4), HBM-bound.
+// E: what e is kept in.
+template <typename E, int PARTS>
 __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
     __shared__ uint16_t tile[PARTS][64][72];   // [entry][token]
     const int n = a.live.rows();
     const int r0 = blockIdx.y * 64, v0 = blockIdx.x * 64;
-    if (r0 >= (n + PAD - 1) / PAD * PAD) return;
+    if (r0 >= n) return;
     const int vb = threadIdx.x & 7;            // 8 entries each
-    const float ds = PARTS == 1 ? 1.0f : *a.dz_scale;
+    const float ds = PARTS == 2 ? *a.dz_scale : 1.0f;
+    const float k = rate_of(a.scale2);
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         const int rt = (threadIdx.x >> 3) + 32 * half, r = r0 + rt;
@@ -557,16 +578,17 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
             const int64_t t = a.targets[tok];
             c = a.scale * a.grad_logp[tok];
             y = t < a.vocab ? static_cast<int>(t) - v0 - 8 * vb : -1;
-            f = c * __builtin_amdgcn_exp2f(a.m[(v0 / a.m_edge) * a.m_pitch + a.live.first + r] - a.lse[tok] * LOG2E);
-            // 1 - p of the target from logp: e is rounded, which 1 - e f would magnify as p goes to 1
-            dy = -c * expm1f(a.logp[a.live.first + r]);
+            const int o = a.live.first + r;
+            f = c * __builtin_amdgcn_exp2f(fmaf(-a.ref[o], k, a.m[(v0 / a.m_edge) * a.m_pitch + o]) + a.shift[o]);
+            // 1 - p of the target from logp alone: e is rounded, which 1 - p would magnify as p goes to 1
+            dy = -c * expm1f(a.logp[o]);
         }
         float x[8];
         const size_t o = (static_cast<size_t>(a.live.first) + min(r, n - 1)) * a.vp + v0 + 8 * vb;
-        if constexpr (sizeof(T) == 2) {
-            const u32x4 w = G(reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.e) + o))[0];
+        if constexpr (sizeof(E) == 2) {
+            const pt::f16x8_t w = __builtin_bit_cast(pt::f16x8_t, G(reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.e) + o))[0]);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = __uint_as_float((k & 1) ? (w[k >> 1] & 0xffff0000u) : (w[k >> 1] << 16));
+            for (int q = 0; q < 8; ++q) x[q] = static_cast<float>(w[q]);
         } else {
             const float4 w0 = ld_f4(static_cast<const float*>(a.e) + o), w1 = ld_f4(static_cast<const float*>(a.e) + o + 4);
             x[0] = w0.x; x[1] = w0.y; x[2] = w0.z; x[3] = w0.w;
@@ -574,11 +596,11 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
         }
         uint16_t v[8][2];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            to_parts<PARTS>(c == 0.0f || v0 + 8 * vb + k >= a.vocab ? 0.0f : k == y ? dy : -x[k] * f, ds, v[k]);
+        for (int q = 0; q < 8; ++q)
+            to_parts<PARTS>(c == 0.0f || v0 + 8 * vb + q >= a.vocab ? 0.0f : q == y ? dy : -x[q] * f, ds, v[q]);
 #pragma unroll
         for (int p = 0; p < PARTS; ++p) {
-            if (a.dz) {
+            if (a.dz && r < n) {
                 u32x4 w;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) w[k] = v[2 * k][p] | static_cast<uint32_t>(v[2 * k + 1][p]) << 16;
@@ -607,7 +629,9 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
 struct GradArgs {
     const char* a;          // transposed operand: one row per gradient column
     size_t a_ld, a_part;
-    const char* b;          // dz (rows = list entries) or its transpose (rows = vocabulary)
+    // dz (rows = list entries, whatever memory holds past the last: those columns of C are not stored) or its transpose (rows =
+    // vocabulary, zeros from the last list entry to a whole k-step)
+    const char* b;
     size_t b_ld, b_part;
     Live live;
     int cols, rows;         // rows: vocabulary; for grad_hidden the list gives them
@@ -669,15 +693,7 @@ __global__ __launch_bounds__(pt::Tile<EDGE>::THREADS, 2) void grad_kernel(GradAr
         }
         TL::template run<PARTS, false>(sa, sb, a.a_part, a.b_part, static_cast<size_t>(k_first) * (pt::KS * 2), steps, 0, lds, acc);
     }
-    if constexpr (PARTS == 2) {
-        const float k1 = 1.0f / *a.dz_scale, k2 = 1.0f / *a.scale;
-#pragma unroll
-        for (int i = 0; i < TL::SM; ++i)
-#pragma unroll
-            for (int j = 0; j < TL::SN; ++j)
-#pragma unroll
-                for (int q = 0; q < 16; ++q) acc[i][j][q] = acc[i][j][q] * k1 * k2;
-    }
+    if constexpr (PARTS == 2) pt::unscale<TL>(acc, *a.dz_scale, *a.scale);
     if (a.slab) {
         float* s = a.slab + (static_cast<size_t>(split) * a.ta * a.tb + tile) * (EDGE * EDGE) + threadIdx.x * 4;
 #pragma unroll
@@ -789,31 +805,22 @@ template <> struct FewOrder<3> {
 };
 
 // 8 values of k of one row from column k, zero past the last column, as bf16 parts.
-template <typename T, int PARTS, bool VEC>
-__device__ __forceinline__ void few_load(const void* base, size_t off, int k, int cols, u32x4 (&out)[PARTS]) {
-    float x[8];
-    if constexpr (sizeof(T) == 2 && VEC) {
-        out[0] = k < cols ? G(reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + off + k))[0] : u32x4{};
-        return;
-    } else if constexpr (VEC) {
-        const float* p = static_cast<const float*>(base) + off + k;
-        const float4 a = k < cols ? ld_f4(p) : float4{}, b = k < cols ? ld_f4(p + 4) : float4{};
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+template <typename T, int PARTS> __device__ __forceinline__ void few_load(const void* base, size_t off, int k, int cols, u32x4 (&out)[PARTS]) {
+    Run<T> x;
+    const auto* row = G(static_cast<const T*>(base) + off);
+    if (k + 8 <= cols) x.load(row, k);
+    else if (k < cols) x.load(row, k, cols - k);
+    if constexpr (PARTS == 1) {
+        out[0] = x.w;
     } else {
+        uint16_t v[8][3];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = k + e < cols ? ld_el<T>(base, off + k + e) : 0.0f;
+        for (int e = 0; e < 8; ++e) split3(x.get(e), v[e]);
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) out[p][e] = v[2 * e][p] | static_cast<uint32_t>(v[2 * e + 1][p]) << 16;
     }
-    uint16_t v[8][3];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        if constexpr (PARTS == 3) split3(x[e], v[e]);
-        else v[e][0] = f32_to_bf16(x[e]);
-    }
-#pragma unroll
-    for (int p = 0; p < PARTS; ++p)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) out[p][e] = v[2 * e][p] | static_cast<uint32_t>(v[2 * e + 1][p]) << 16;
 }
 
 struct FewArgs {
@@ -822,15 +829,19 @@ struct FewArgs {
     const int64_t* targets;
     int tokens, cols, vocab, tiles;
     float scale2;
-    float *m, *s, *zt;      // token x tile; target logit by token
+    float *m, *s, *zt;      // M and S: token x tile; target's acc by token
+    uint16_t* e;            // bf16 calls: fp16 2^(k' acc - M), token x vocabulary (pitch vp), or NULL
+    size_t vp;
 };
 
 // FEW_ROWS entries x up to 16 NT tokens a workgroup; its four waves take 64 values of k in turn.  Vocabulary
 // along the accumulator rows, tokens along the columns (16 x 16 MFMA).  HBM-bound: the head once,
 // cols x vocab elements; hidden comes from the caches.
-template <typename T, int PARTS, int NT, bool VEC>
+template <typename T, int PARTS, int NT>
 __global__ __launch_bounds__(256, NT == 1 ? 4 : 1) void few_kernel(FewArgs a) {
-    __shared__ float red[4][FEW_ROWS][16 * NT + 1];
+    constexpr int TOK = 16 * NT, GROUPS = 256 / TOK, PER = FEW_ROWS / GROUPS;   // at the end: threads a token, entries a thread
+    __shared__ float red[4][FEW_ROWS][TOK + 1];
+    __shared__ float part[2][GROUPS][TOK];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int v0 = blockIdx.x * FEW_ROWS, ln = lane & 15, kg = 8 * (lane >> 4);
     size_t wo[2], ho[NT];
@@ -839,16 +850,16 @@ __global__ __launch_bounds__(256, NT == 1 ? 4 : 1) void few_kernel(FewArgs a) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) ho[t] = static_cast<size_t>(min(16 * t + ln, a.tokens - 1)) * a.ld_hidden;
     f32x4m_t acc[2][NT] = {};
-    constexpr int DEEP = PARTS == 1 && VEC ? 2 : 1;   // 64-value runs of k in flight (4: 31.7 us for one token and 32000 x 2048, 2: 29.1)
+    constexpr int DEEP = PARTS == 1 ? 2 : 1;   // 64-value runs of k in flight (4: 31.7 us for one token and 32000 x 2048, 2: 29.1)
     for (int k0 = 64 * wave; k0 < a.cols; k0 += 256 * DEEP) {
         u32x4 w[2 * DEEP][2][PARTS], h[2 * DEEP][NT][PARTS];
 #pragma unroll
         for (int b = 0; b < 2 * DEEP; ++b) {
             const int k = k0 + 256 * (b >> 1) + 32 * (b & 1) + kg;
 #pragma unroll
-            for (int r = 0; r < 2; ++r) few_load<T, PARTS, VEC>(a.head, wo[r], k, a.cols, w[b][r]);
+            for (int r = 0; r < 2; ++r) few_load<T, PARTS>(a.head, wo[r], k, a.cols, w[b][r]);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) few_load<T, PARTS, VEC>(a.hidden, ho[t], k, a.cols, h[b][t]);
+            for (int t = 0; t < NT; ++t) few_load<T, PARTS>(a.hidden, ho[t], k, a.cols, h[b][t]);
         }
 #pragma unroll
         for (int b = 0; b < 2 * DEEP; ++b) {
@@ -870,25 +881,279 @@ __global__ __launch_bounds__(256, NT == 1 ? 4 : 1) void few_kernel(FewArgs a) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) red[wave][16 * r + 4 * (lane >> 4) + e][16 * t + ln] = acc[r][t][e];
     __syncthreads();
-    // half a wave per token, a lane per entry
-    for (int t = threadIdx.x >> 5; t < a.tokens; t += 8) {
-        const int r = threadIdx.x & 31, v = v0 + r;
-        const int64_t y = a.targets[t];
-        float z = (red[0][r][t] + red[1][r][t] + red[2][r][t] + red[3][r][t]) * a.scale2;
-        if (v >= a.vocab) z = -INFINITY;
-        float m = z;
+    const float k = rate_of(a.scale2);
+    const int t = threadIdx.x % TOK, g = threadIdx.x / TOK, v = v0 + PER * g;   // this thread's entries from v on
+    const int64_t y = t < a.tokens ? a.targets[t] - v : -1;
+    float z[PER], m = -INFINITY, sum = 0.0f;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 32));
-        float e = __builtin_amdgcn_exp2f(z - (m == -INFINITY ? 0.0f : m));
-        if (v == y) {
-            a.zt[t] = z;
-            e = 0.0f;
+    for (int r = 0; r < PER; ++r) {
+        z[r] = red[0][PER * g + r][t] + red[1][PER * g + r][t] + red[2][PER * g + r][t] + red[3][PER * g + r][t];
+        if (a.scale2 < 0.0f) z[r] = -z[r];
+        if (v + r >= a.vocab) z[r] = -INFINITY;
+        m = fmaxf(m, z[r]);
+    }
+    part[0][g][t] = m;
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < GROUPS; ++h) m = fmaxf(m, part[0][h][t]);
+    m *= k;
+    uint16_t e16[PER];
+#pragma unroll
+    for (int r = 0; r < PER; ++r) {
+        const float e = __builtin_amdgcn_exp2f(fmaf(z[r], k, -shown(m)));
+        if constexpr (sizeof(T) == 2) e16[r] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(e));
+        if (r == y && v + r < a.vocab) a.zt[t] = z[r];
+        else sum += e;
+    }
+    part[1][g][t] = sum;
+    __syncthreads();
+    if (t >= a.tokens) return;
+    if (sizeof(T) == 2 && a.e) {
+        uint32_t w[PER / 2];
+#pragma unroll
+        for (int r = 0; r < PER / 2; ++r) w[r] = e16[2 * r] | static_cast<uint32_t>(e16[2 * r + 1]) << 16;
+        __builtin_memcpy(__builtin_assume_aligned(a.e + t * a.vp + v, 2 * PER), w, sizeof(w));
+    }
+    if (g == 0) {
+        sum = part[1][0][t];
+#pragma unroll
+        for (int h = 1; h < GROUPS; ++h) sum += part[1][h][t];
+        a.m[static_cast<size_t>(t) * a.tiles + blockIdx.x] = m;
+        a.s[static_cast<size_t>(t) * a.tiles + blockIdx.x] = sum;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Few tokens: gradients, bf16
+// ---------------------------------------------------------------------------
+// Both have gradient columns along the accumulator rows and k (vocabulary entries, or tokens) across rows of an operand that
+// lies k-major.  A lane reads 8 columns (16 bytes) of 8 rows of k, which transposed in its registers are the A
+// fragments of 8 MFMAs: MFMA j takes column 8 p + j of lane group p.  Lane i of 16 takes the run p = 4 (i & 3) + (i >> 2), so
+// that of C row 4 q + e, run 4 e + q, the four lanes q that share a C column hold adjacent runs.
+// dz is formed from e where it is used.  One token's rounded dz would be its whole gradient's error, so dz goes as two
+// bf16 parts, hi + lo.
+
+constexpr int FEW_STRIP = 128;       // gradient columns of a wave
+
+struct FewGradArgs {
+    const void *head, *hidden;
+    size_t ld_head, ld_hidden;
+    const int64_t* targets;
+    int tokens, cols, vocab, tiles, strips, splits;
+    float scale2, scale;
+    const uint16_t* e;                 // token x vocabulary, pitch vp (FewArgs)
+    size_t vp;
+    const float* m;                    // token x tile
+    const float *logp, *ref, *shift;   // by token, as in DzArgs
+    const float* grad_logp;
+    float* slab;                       // [split][strip][j][4 registers of every 16 tokens][lane]
+    void *grad_hidden, *grad_head;     // or NULL
+    size_t ld_grad_hidden, ld_grad_head;
+};
+
+// What dz of a token takes.
+struct FewToken {
+    float c = 0.0f, ref = 0.0f, shift = 0.0f, dy = 0.0f;
+    int y = -1;
+    __device__ __forceinline__ void load(const FewGradArgs& a, int t) {
+        if (t >= a.tokens) return;
+        const int64_t target = a.targets[t];
+        if (target < 0) return;
+        y = target < a.vocab ? static_cast<int>(target) : -1;
+        c = a.scale * a.grad_logp[t];
+        ref = a.ref[t];
+        shift = a.shift[t];
+        dy = -c * expm1f(a.logp[t]);
+    }
+    __device__ __forceinline__ float factor(float m, float k) const { return c * __builtin_amdgcn_exp2f(fmaf(-ref, k, m) + shift); }
+    // e of entry v, times the factor of its tile
+    __device__ __forceinline__ float dz(float e, float f, int v, int vocab) const {
+        return c == 0.0f || v >= vocab ? 0.0f : v == y ? dy : -e * f;
+    }
+};
+__device__ __forceinline__ float e_of(uint32_t x) { return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(x))); }
+__device__ __forceinline__ void hi_lo(float x, uint16_t (&p)[2]) {
+    p[0] = f32_to_bf16(x);
+    p[1] = f32_to_bf16(x - bf16_to_f32(p[0]));
+}
+
+// Column j of 8 rows as an A fragment.
+__device__ __forceinline__ u32x4 few_fragment(const Run<uint16_t> (&r)[8], int j) {
+    u32x4 out;
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+        out[p] = __builtin_amdgcn_perm(r[2 * p + 1].w[j >> 1], r[2 * p].w[j >> 1], (j & 1) ? 0x07060302u : 0x05040100u);
+    return out;
+}
+// a times hi + lo.
+__device__ __forceinline__ void few_mfma(f32x4m_t& acc, const u32x4& a, const u32x4 (&b)[2]) {
+#pragma unroll
+    for (int p = 1; p >= 0; --p)
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(pt::bf16x8_t, a), __builtin_bit_cast(pt::bf16x8_t, b[p]), acc, 0, 0, 0);
+}
+__device__ __forceinline__ int few_column(int lane) { return 8 * (4 * (lane & 3) + ((lane & 15) >> 2)); }   // of the strip
+__device__ __forceinline__ void few_row(Run<uint16_t>& r, const uint16_t* row, int col, int cols) {
+    if (col + 8 <= cols) r.load(G(row), col);
+    else if (col < cols) r.load(G(row), col, cols - col);
+}
+
+// grad_hidden: a strip of columns and a run of vocabulary tiles a workgroup, its four waves taking tiles in turn; their sums
+// are put together in LDS.  HBM-bound: head once.  16 NT tokens.
+template <int NT> __global__ __launch_bounds__(256, NT == 1 ? 3 : 2) void few_hidden_kernel(FewGradArgs a) {
+    constexpr int REGS = 4 * NT;
+    constexpr bool AHEAD = NT <= 2;   // registers for the next tile's rows
+    __shared__ float red[4][REGS][64];
+    const int lane = threadIdx.x & 63, wave = pt::wave_id(), q = lane >> 4;
+    const int strip = blockIdx.x % a.strips, split = blockIdx.x / a.strips;
+    const int col = FEW_STRIP * strip + few_column(lane);
+    const int first = static_cast<int>(static_cast<int64_t>(a.tiles) * split / a.splits);
+    const int last = static_cast<int>(static_cast<int64_t>(a.tiles) * (split + 1) / a.splits);
+    const float k = rate_of(a.scale2);
+    const uint16_t* head = static_cast<const uint16_t*>(a.head);
+    const uint16_t* e = a.e;
+    FewToken tok[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) tok[n].load(a, 16 * n + (lane & 15));
+    struct Chunk {
+        Run<uint16_t> rows[8], e[NT];
+        float m[NT];
+    };
+    auto load = [&](Chunk& c, int tile) {
+        const int v = FEW_ROWS * tile + 8 * q;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            c.rows[r] = Run<uint16_t>{};
+            few_row(c.rows[r], head + static_cast<size_t>(min(v + r, a.vocab - 1)) * a.ld_head, col, a.cols);
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) e += __shfl_xor(e, o, 32);
-        if (r == 0) {
-            a.m[static_cast<size_t>(t) * a.tiles + blockIdx.x] = m;
-            a.s[static_cast<size_t>(t) * a.tiles + blockIdx.x] = e;
+        for (int n = 0; n < NT; ++n) {
+            const int t = min(16 * n + (lane & 15), a.tokens - 1);
+            c.e[n].load(G(e + t * a.vp), v);
+            c.m[n] = a.m[static_cast<size_t>(t) * a.tiles + tile];
+        }
+    };
+    f32x4m_t acc[8][NT] = {};
+    Chunk now, next;
+    if (AHEAD && first + wave < last) load(now, first + wave);
+    for (int tile = first + wave; tile < last; tile += 4) {
+        if (!AHEAD) load(now, tile);
+        else if (tile + 4 < last) load(next, tile + 4);
+        u32x4 b[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const float f = tok[n].factor(now.m[n], k);
+            uint16_t v[8][2];
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                const float x = e_of(now.e[n].w[r >> 1] >> (16 * (r & 1)));
+                hi_lo(tok[n].dz(x, f, FEW_ROWS * tile + 8 * q + r, a.vocab), v[r]);
+            }
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) b[n][p][r] = v[2 * r][p] | static_cast<uint32_t>(v[2 * r + 1][p]) << 16;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const u32x4 w = few_fragment(now.rows, j);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) few_mfma(acc[j][n], w, b[n]);
+        }
+        if (AHEAD) now = next;
+    }
+    float* slab = a.slab + (static_cast<size_t>(split) * a.strips + strip) * (8 * REGS * 64);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) red[wave][4 * n + r][lane] = acc[j][n][r];
+        __syncthreads();
+        for (int x = wave; x < REGS; x += 4)
+            slab[(j * REGS + x) * 64 + lane] = red[0][x][lane] + red[1][x][lane] + red[2][x][lane] + red[3][x][lane];
+    }
+}
+
+// The splits' sums, in order, to grad_hidden; zeros for tokens that are not scored.  An element a thread.
+template <int NT> __global__ __launch_bounds__(256) void few_sum_kernel(FewGradArgs a) {
+    constexpr int REGS = 4 * NT;
+    const int i = blockIdx.x * 256 + threadIdx.x, lane = i & 63, x = (i >> 6) % REGS, js = (i >> 6) / REGS;
+    const int t = 16 * (x >> 2) + (lane & 15), col = FEW_STRIP * (js >> 3) + 8 * (4 * (x & 3) + (lane >> 4)) + (js & 7);
+    if (t >= a.tokens || col >= a.cols) return;
+    const size_t step = static_cast<size_t>(a.strips) * (8 * REGS * 64);
+    float v = 0.0f;
+#pragma unroll 8
+    for (int s = 0; s < a.splits; ++s) v += a.slab[s * step + i];
+    st_el<uint16_t>(a.grad_hidden, t * a.ld_grad_hidden + col, a.targets[t] < 0 ? 0.0f : v);
+}
+
+// grad_head: a tile of FEW_ROWS entries a workgroup, whose dz is formed once in LDS; its waves take strips of columns in turn.
+// Bound by the writes: head's size once.  KS: runs of 32 tokens.
+template <int KS> __global__ __launch_bounds__(256, 2) void few_head_kernel(FewGradArgs a) {
+    constexpr int VB = FEW_ROWS / 16;
+    __shared__ __attribute__((aligned(16))) uint16_t tile[2][FEW_ROWS][32 * KS + 8];   // [entry][token]
+    const int lane = threadIdx.x & 63, wave = pt::wave_id(), q = lane >> 4;
+    const int v0 = blockIdx.x * FEW_ROWS;
+    const float k = rate_of(a.scale2);
+    const uint16_t* e = a.e;
+    const unsigned long long live = __ballot(lane < a.tokens && a.targets[min(lane, max(a.tokens - 1, 0))] >= 0);
+    const int t = threadIdx.x % (32 * KS), r0 = 8 * (threadIdx.x / (32 * KS));   // a token and 8 entries a thread
+    if (r0 < FEW_ROWS) {
+        FewToken tok;
+        Run<uint16_t> x;
+        float f = 0.0f;
+        if (live >> t & 1u) {
+            x.load(G(e + t * a.vp), v0 + r0);
+            tok.load(a, t);
+            f = tok.factor(a.m[static_cast<size_t>(t) * a.tiles + blockIdx.x], k);
+        }
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            uint16_t p[2];
+            hi_lo(tok.dz(e_of(x.w[r >> 1] >> (16 * (r & 1))), f, v0 + r0 + r, a.vocab), p);
+#pragma unroll
+            for (int d = 0; d < 2; ++d) tile[d][r0 + r][t] = p[d];
+        }
+    }
+    __syncthreads();
+    const uint16_t* hidden = static_cast<const uint16_t*>(a.hidden);
+    uint16_t* out = static_cast<uint16_t*>(a.grad_head);
+    for (int strip = blockIdx.y * 4 + wave; strip < a.strips; strip += 4 * gridDim.y) {
+        const int col = FEW_STRIP * strip + few_column(lane);
+        f32x4m_t acc[8][VB] = {};
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            Run<uint16_t> rows[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                const int t = 32 * s + 8 * q + r;
+                if (live >> t & 1u) few_row(rows[r], hidden + t * a.ld_hidden, col, a.cols);   // whatever others hold counts for nothing
+            }
+            u32x4 b[VB][2];
+#pragma unroll
+            for (int n = 0; n < VB; ++n)
+#pragma unroll
+                for (int d = 0; d < 2; ++d) b[n][d] = *reinterpret_cast<const u32x4*>(&tile[d][16 * n + (lane & 15)][32 * s + 8 * q]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const u32x4 w = few_fragment(rows, j);
+#pragma unroll
+                for (int n = 0; n < VB; ++n) few_mfma(acc[j][n], w, b[n]);
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < VB; ++n) {
+            const int v = v0 + 16 * n + (lane & 15);
+            if (v >= a.vocab) continue;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int c = FEW_STRIP * strip + 8 * (4 * r + q);
+                u32x4 w;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(acc[2 * j][n][r], acc[2 * j + 1][n][r]);
+                st_piece(out + static_cast<size_t>(v) * a.ld_grad_head + c, w, a.cols - c);
+            }
         }
     }
 }
@@ -906,7 +1171,8 @@ struct CombineArgs {
     float *logp, *lse;
     const int32_t *idx, *count;   // NULL: every token, in order (then unscored ones are zeroed here)
     int64_t tokens;
-    float* kept;                  // logp by list entry, for the backward pass, or NULL
+    float scale2;
+    float *kept_logp, *kept_ref, *kept_shift;   // by list entry, for the backward pass (DzArgs), or NULL
 };
 
 // 2^(a - b) for a <= b, with equal infinities taken as equal
@@ -920,6 +1186,7 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
     const int tk = threadIdx.x % TOK, part = threadIdx.x / TOK;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * TOK + tk;
     const int64_t n = a.idx ? *a.count : a.tokens;
+    const float k = rate_of(a.scale2);
     float m = -INFINITY, s = 0.0f;
     if (row < n)
 #pragma unroll 4
@@ -943,26 +1210,41 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
     }
     if (part != 0 || row >= n) return;
     const int64_t tok = a.idx ? a.idx[row] : row, y = a.targets[tok];
-    float logp, lse = (m + log2f(s)) * LN2;
+    // s is the sum without the target, if there is one
+    float logp, lse = (m + log2f(s)) * LN2, ref = 0.0f, shift = -(m + log2f(s));
     if (y < 0) {
         logp = lse = 0.0f;
     } else if (y >= a.vocab) {
         logp = NAN;
     } else {
-        const float zt = a.zt[row], d = m - zt;
-        if (s == 0.0f) logp = 0.0f;
-        else if (d < 80.0f) logp = -log1pf(s * __builtin_amdgcn_exp2f(d));
-        else logp = -(d + log2f(s)) * LN2;     // here 1 is nothing beside the sum
-        if (d < 80.0f) lse = zt * LN2 - logp;
+        const float zt = a.zt[row], d = fmaf(-zt, k, m);
+        if (d < 80.0f) {
+            logp = 0.0f - log1pf(s * __builtin_amdgcn_exp2f(d));
+            lse = zt * k * LN2 - logp;
+            ref = zt;
+            shift = logp * LOG2E;
+        } else {
+            logp = -(d + log2f(s)) * LN2;     // here 1 is nothing beside the sum
+        }
     }
     a.logp[tok] = logp;
     a.lse[tok] = lse;
-    if (a.kept) a.kept[row] = logp;
+    if (a.kept_logp) {
+        a.kept_logp[row] = logp;
+        a.kept_ref[row] = ref;
+        a.kept_shift[row] = shift;
+    }
 }
 
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
+
+#define TL_TRY(expr)                       \
+    do {                                   \
+        const hipError_t e_ = (expr);      \
+        if (e_ != hipSuccess) return e_;   \
+    } while (0)
 
 struct Bump {
     size_t at = 0;
@@ -982,10 +1264,13 @@ struct Shape {
     int parts;
     int64_t tp, vp, dp;      // padded to PAD, PAD, the k-step
     int edge;                // tile of the logits' product
+    bool few;                // forward and backward; a forward pass in fp32 that keeps nothing is so too
+    int few_tiles;           // of FEW_ROWS entries
     bool direct_hidden, direct_head;   // operands that the products can read where they are: bf16 in whole 16-byte chunks
     Shape(int64_t t, int64_t d, int64_t v, int dtype, const void* hidden, int64_t ld_hidden, const void* head, int64_t ld_head)
         : tokens(t), cols(d), vocab(v), parts(dtype == MUON_BF16 ? 1 : 2), tp(up(std::max<int64_t>(t, 1), PAD)), vp(up(v, PAD)),
-          dp(up(d, pt::KS)), edge(edge_for(tp / PAD * (vp / PAD))) {
+          dp(up(d, pt::KS)), edge(edge_for(tp / PAD * (vp / PAD))), few(t <= FEW_TOKENS && parts == 1),
+          few_tiles(static_cast<int>(ceil_div(v, FEW_ROWS))) {
         const bool ok = dtype == MUON_BF16 && d % 8 == 0;
         direct_hidden = ok && reinterpret_cast<uintptr_t>(hidden) % 16 == 0 && ld_hidden % 8 == 0;
         direct_head = ok && reinterpret_cast<uintptr_t>(head) % 16 == 0 && ld_head % 8 == 0;
@@ -993,15 +1278,18 @@ struct Shape {
     int ta() const { return static_cast<int>(vp / edge); }
 };
 
-// The buffer that the forward pass keeps: exp(z - m), the tiles' m, logp by list entry, and the list.
+// The buffer that the forward pass keeps: e, the tiles' M, what combine_kernel keeps by token, and (many tokens) the list.
 struct SavedPlan {
-    size_t e, m, logp, idx, count, scales, bytes;
+    size_t e, m, logp, ref, shift, idx, count, scales, bytes;
     explicit SavedPlan(const Shape& sh) {
         Bump b;
-        e = b.take((sh.parts == 1 ? 2 : 4) * static_cast<size_t>(sh.tp) * sh.vp);
-        m = b.take(sizeof(float) * sh.ta() * static_cast<size_t>(sh.tp));
-        logp = b.take(sizeof(float) * static_cast<size_t>(sh.tp));
-        idx = b.take(sizeof(int32_t) * static_cast<size_t>(sh.tp));
+        const size_t rows = static_cast<size_t>(sh.few ? sh.tokens : sh.tp);
+        e = b.take((sh.parts == 1 ? 2 : 4) * rows * sh.vp);
+        m = b.take(sizeof(float) * rows * (sh.few ? sh.few_tiles : sh.ta()));
+        logp = b.take(sizeof(float) * rows);
+        ref = b.take(sizeof(float) * rows);
+        shift = b.take(sizeof(float) * rows);
+        idx = b.take(sh.few ? 0 : sizeof(int32_t) * rows);
         count = b.take(sizeof(int32_t));
         scales = b.take(2 * sizeof(float));
         bytes = b.at;
@@ -1011,19 +1299,17 @@ struct SavedPlan {
 struct ForwardPlan {
     Shape sh;
     bool few;
-    int few_tiles;
     size_t idx, count, hidden, head, m, s, zt, absmax, scales, bytes;
     explicit ForwardPlan(const muon_token_logp_args& a)
         : sh(a.tokens, a.cols, a.vocab, a.dtype, a.hidden, a.ld_hidden, a.head, a.ld_head) {
-        few = a.tokens <= FEW_TOKENS && !a.saved;
-        few_tiles = static_cast<int>(ceil_div(a.vocab, FEW_ROWS));
+        few = sh.few || (a.tokens <= FEW_TOKENS && !a.saved);
         Bump b;
         const size_t part = sizeof(uint16_t) * sh.parts * sh.dp;
         idx = b.take(few || a.saved ? 0 : sizeof(int32_t) * sh.tp);
         count = b.take(sizeof(int32_t));
         hidden = b.take(few || sh.direct_hidden ? 0 : part * sh.tp);
         head = b.take(few || sh.direct_head ? 0 : part * sh.vocab);
-        const size_t stats = few ? static_cast<size_t>(a.tokens) * few_tiles : static_cast<size_t>(sh.ta()) * sh.tp;
+        const size_t stats = few ? static_cast<size_t>(a.tokens) * sh.few_tiles : static_cast<size_t>(sh.ta()) * sh.tp;
         m = b.take(a.saved ? 0 : stats * sizeof(float));
         s = b.take(stats * sizeof(float));
         zt = b.take(sizeof(float) * sh.tp);
@@ -1031,6 +1317,41 @@ struct ForwardPlan {
         scales = b.take(few || sh.parts == 1 ? 0 : 2 * sizeof(float));
         bytes = b.at;
     }
+};
+
+// The backward pass for few tokens: workgroups over the columns and, for grad_hidden, over runs of vocabulary tiles, twice as
+// many as CUs.  Without `saved` a forward pass comes first, into the workspace.
+struct FewPlan {
+    Shape sh;
+    int strips, splits;
+    muon_token_logp_args forward;
+    size_t slab, logp, lse, saved, workspace, bytes;
+    explicit FewPlan(const muon_token_logp_backward_args& a)
+        : sh(a.tokens, a.cols, a.vocab, a.dtype, a.hidden, a.ld_hidden, a.head, a.ld_head), forward{} {
+        strips = static_cast<int>(ceil_div(a.cols, FEW_STRIP));
+        splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(2 * CUS / strips, sh.few_tiles / 8)));
+        Bump b;
+        slab = b.take(a.grad_hidden ? sizeof(float) * FEW_STRIP * static_cast<size_t>(strips) * splits * 16 * blocks() : 0);
+        if (!a.saved) {
+            forward.hidden = a.hidden;
+            forward.head = a.head;
+            forward.targets = a.targets;
+            forward.tokens = a.tokens;
+            forward.cols = a.cols;
+            forward.vocab = a.vocab;
+            forward.ld_hidden = a.ld_hidden;
+            forward.ld_head = a.ld_head;
+            forward.scale = a.scale;
+            forward.dtype = a.dtype;
+            forward.saved = const_cast<void*>(a.head);   // any: there is one
+            logp = b.take(sizeof(float) * a.tokens);
+            lse = b.take(sizeof(float) * a.tokens);
+            saved = b.take(SavedPlan(sh).bytes);
+            workspace = b.take(ForwardPlan(forward).bytes);
+        }
+        bytes = b.at;
+    }
+    int blocks() const { return sh.tokens <= 16 ? 1 : sh.tokens <= 32 ? 2 : 4; }   // of 16 tokens
 };
 
 // How a gradient's product is tiled and spread: the small tile where the large ones are too few, then
@@ -1060,8 +1381,9 @@ struct BackwardPlan {
         return std::min(sh.tp, std::max<int64_t>(PAD, DZ_BYTES / both / PAD * PAD));
     }
     explicit BackwardPlan(const muon_token_logp_backward_args& a)
-        : sh(a.tokens, a.cols, a.vocab, a.dtype, a.hidden, a.ld_hidden, a.head, a.ld_head), chunk(chunk_of(sh)),
-          chunks(static_cast<int>(ceil_div(sh.tp, chunk))), gh(sh.cols, chunk, sh.vp, false), gw(sh.cols, sh.vocab, chunk, chunks > 1) {
+        : sh(a.tokens, a.cols, a.vocab, a.dtype, a.hidden, a.ld_hidden, a.head, a.ld_head),
+          chunk(chunk_of(sh)), chunks(static_cast<int>(ceil_div(sh.tp, chunk))), gh(sh.cols, chunk, sh.vp, false),
+          gw(sh.cols, sh.vocab, chunk, chunks > 1) {
         Bump b;
         const size_t el = sizeof(uint16_t) * sh.parts;
         idx = b.take(a.saved ? 0 : sizeof(int32_t) * sh.tp);
@@ -1081,6 +1403,7 @@ struct BackwardPlan {
     }
 };
 
+bool few_backward(const muon_token_logp_backward_args& a) { return a.tokens <= FEW_TOKENS && a.dtype == MUON_BF16; }
 Shape shape_of(const muon_token_logp_args& a) { return Shape(a.tokens, a.cols, a.vocab, a.dtype, a.hidden, a.ld_hidden, a.head, a.ld_head); }
 
 hipError_t launch_live(const int64_t* targets, int64_t tokens, int32_t* idx, int32_t* count, float* logp, float* lse,
@@ -1126,12 +1449,6 @@ hipError_t launch_grad(GradArgs g, const GradPlan& pl, float* slab, int parts, i
     return pl.edge == 256 ? launch_grad_edge<256>(g, parts, dtype, last, s) : launch_grad_edge<128>(g, parts, dtype, last, s);
 }
 
-#define TL_TRY(expr)                       \
-    do {                                   \
-        const hipError_t e_ = (expr);      \
-        if (e_ != hipSuccess) return e_;   \
-    } while (0)
-
 // Scales of fp32 operands (part NULL: known already) and of dz (dz NULL: not wanted).
 hipError_t launch_scales(const void* hidden, int64_t ld_hidden, const void* head, int64_t ld_head, const Shape& sh, const Live& live,
                          uint32_t* part, float* operands, float* dz, const float* grad_logp, float scale, hipStream_t s) {
@@ -1173,23 +1490,64 @@ hipError_t logits_operands(const Shape& sh, const void* hidden, int64_t ld_hidde
     return hipSuccess;
 }
 
-template <typename T, int PARTS, int NT> hipError_t launch_few_nt(const FewArgs& f, bool vec, hipStream_t s) {
+template <typename T, int PARTS> hipError_t launch_few(const muon_token_logp_args& a, const ForwardPlan& pl, char* ws, hipStream_t s) {
+    const Shape& sh = pl.sh;
+    char* keep = static_cast<char*>(a.saved);
+    const SavedPlan sv(sh);
+    auto kept = [&](size_t o) { return keep ? reinterpret_cast<float*>(keep + o) : nullptr; };
+    FewArgs f{a.head, a.hidden, static_cast<size_t>(a.ld_head), static_cast<size_t>(a.ld_hidden), a.targets,
+                 static_cast<int>(a.tokens), static_cast<int>(a.cols), static_cast<int>(a.vocab), sh.few_tiles, a.scale * LOG2E,
+                 keep ? kept(sv.m) : reinterpret_cast<float*>(ws + pl.m), reinterpret_cast<float*>(ws + pl.s),
+                 reinterpret_cast<float*>(ws + pl.zt), reinterpret_cast<uint16_t*>(kept(sv.e)), static_cast<size_t>(sh.vp)};
     const dim3 grid(static_cast<unsigned>(f.tiles));
-    if (vec) hipLaunchKernelGGL((few_kernel<T, PARTS, NT, true>), grid, dim3(256), 0, s, f);
-    else hipLaunchKernelGGL((few_kernel<T, PARTS, NT, false>), grid, dim3(256), 0, s, f);
+    if (f.tokens <= 16) hipLaunchKernelGGL((few_kernel<T, PARTS, 1>), grid, dim3(256), 0, s, f);
+    else if (f.tokens <= 32) hipLaunchKernelGGL((few_kernel<T, PARTS, 2>), grid, dim3(256), 0, s, f);
+    else hipLaunchKernelGGL((few_kernel<T, PARTS, 4>), grid, dim3(256), 0, s, f);
+    TL_TRY(hipGetLastError());
+    const CombineArgs c{f.m, f.s, f.zt, 1, static_cast<size_t>(sh.few_tiles), sh.few_tiles, a.targets, a.vocab, a.logp, a.lse,
+                        nullptr, nullptr, a.tokens, f.scale2, kept(sv.logp), kept(sv.ref), kept(sv.shift)};
+    hipLaunchKernelGGL(combine_kernel<1>, dim3(static_cast<unsigned>(a.tokens)), dim3(256), 0, s, c);
     return hipGetLastError();
 }
-template <typename T, int PARTS> hipError_t launch_few(const FewArgs& f, bool vec, hipStream_t s) {
-    if (f.tokens <= 16) return launch_few_nt<T, PARTS, 1>(f, vec, s);
-    if (f.tokens <= 32) return launch_few_nt<T, PARTS, 2>(f, vec, s);
-    return launch_few_nt<T, PARTS, 4>(f, vec, s);
+
+template <int NT> hipError_t launch_few_grads_nt(const FewGradArgs& g, const FewPlan& pl, hipStream_t s) {
+    if (g.grad_hidden) {
+        hipLaunchKernelGGL(few_hidden_kernel<NT>, dim3(static_cast<unsigned>(pl.strips) * pl.splits), dim3(256), 0, s, g);
+        TL_TRY(hipGetLastError());
+        hipLaunchKernelGGL(few_sum_kernel<NT>, dim3(static_cast<unsigned>(pl.strips) * (FEW_STRIP * 16 * NT / 256)), dim3(256), 0, s, g);
+        TL_TRY(hipGetLastError());
+    }
+    if (g.grad_head) {
+        // enough workgroups over the columns to fill the chip
+        const int by = std::max(1, std::min((4 * CUS + g.tiles - 1) / g.tiles, (pl.strips + 3) / 4));
+        hipLaunchKernelGGL(few_head_kernel<NT == 4 ? 2 : 1>, dim3(g.tiles, by), dim3(256), 0, s, g);
+        TL_TRY(hipGetLastError());
+    }
+    return hipSuccess;
+}
+hipError_t launch_few_grads(const muon_token_logp_backward_args& a, const FewPlan& pl, const char* saved, float* slab, hipStream_t s) {
+    const SavedPlan sv(pl.sh);
+    auto kept = [&](size_t o) { return reinterpret_cast<const float*>(saved + o); };
+    const FewGradArgs g{a.head, a.hidden, static_cast<size_t>(a.ld_head), static_cast<size_t>(a.ld_hidden), a.targets,
+                        static_cast<int>(a.tokens), static_cast<int>(a.cols), static_cast<int>(a.vocab), pl.sh.few_tiles,
+                        pl.strips, pl.splits, a.scale * LOG2E, a.scale, reinterpret_cast<const uint16_t*>(saved + sv.e), static_cast<size_t>(pl.sh.vp), kept(sv.m),
+                        kept(sv.logp), kept(sv.ref), kept(sv.shift), a.grad_logp, slab,
+                        a.tokens > 0 ? a.grad_hidden : nullptr, a.grad_head, static_cast<size_t>(a.ld_grad_hidden),
+                        static_cast<size_t>(a.ld_grad_head)};
+    switch (pl.blocks()) {
+        case 1: return launch_few_grads_nt<1>(g, pl, s);
+        case 2: return launch_few_grads_nt<2>(g, pl, s);
+        default: return launch_few_grads_nt<4>(g, pl, s);
+    }
 }
 
 }  // namespace
 
 size_t token_logp_saved_bytes(const muon_token_logp_args& a) { return SavedPlan(shape_of(a)).bytes; }
 size_t token_logp_bytes(const muon_token_logp_args& a) { return ForwardPlan(a).bytes; }
-size_t token_logp_backward_bytes(const muon_token_logp_backward_args& a) { return BackwardPlan(a).bytes; }
+size_t token_logp_backward_bytes(const muon_token_logp_backward_args& a) {
+    return few_backward(a) ? FewPlan(a).bytes : BackwardPlan(a).bytes;
+}
 
 hipError_t launch_token_logp(const muon_token_logp_args& a, void* workspace, hipStream_t s) {
     if (a.tokens == 0) return hipSuccess;
@@ -1200,29 +1558,19 @@ hipError_t launch_token_logp(const muon_token_logp_args& a, void* workspace, hip
     float* sums = reinterpret_cast<float*>(ws + pl.s);
     float* zt = reinterpret_cast<float*>(ws + pl.zt);
     const float scale2 = a.scale * LOG2E;
-    if (pl.few) {
-        const FewArgs f{a.head, a.hidden, static_cast<size_t>(a.ld_head), static_cast<size_t>(a.ld_hidden), a.targets,
-                        static_cast<int>(a.tokens), static_cast<int>(a.cols), static_cast<int>(a.vocab), pl.few_tiles, scale2,
-                        m, sums, zt};
-        const int el = a.dtype == MUON_BF16 ? 2 : 4;   // 16-byte loads of 8 (bf16) or 4 (fp32) elements
-        const bool vec = a.cols % 8 == 0 && reinterpret_cast<uintptr_t>(a.head) % 16 == 0 &&
-                         reinterpret_cast<uintptr_t>(a.hidden) % 16 == 0 && a.ld_head * el % 16 == 0 && a.ld_hidden * el % 16 == 0;
-        TL_TRY(a.dtype == MUON_BF16 ? (launch_few<uint16_t, 1>(f, vec, s)) : (launch_few<float, 3>(f, vec, s)));
-        const CombineArgs c{m, sums, zt, 1, static_cast<size_t>(pl.few_tiles), pl.few_tiles, a.targets, a.vocab, a.logp, a.lse,
-                            nullptr, nullptr, a.tokens, nullptr};
-        hipLaunchKernelGGL(combine_kernel<1>, dim3(static_cast<unsigned>(a.tokens)), dim3(256), 0, s, c);
-        return hipGetLastError();
-    }
+    if (pl.few) return a.dtype == MUON_BF16 ? launch_few<uint16_t, 1>(a, pl, ws, s) : launch_few<float, 3>(a, pl, ws, s);
     LogitsArgs l{};
     int32_t* idx = reinterpret_cast<int32_t*>(ws + pl.idx);
     int32_t* count = reinterpret_cast<int32_t*>(ws + pl.count);
-    float* kept = nullptr;
+    float *kept_logp = nullptr, *kept_ref = nullptr, *kept_shift = nullptr;
     if (a.saved) {
         const SavedPlan sv(sh);
         char* p = static_cast<char*>(a.saved);
         l.e = p + sv.e;
         m = reinterpret_cast<float*>(p + sv.m);
-        kept = reinterpret_cast<float*>(p + sv.logp);
+        kept_logp = reinterpret_cast<float*>(p + sv.logp);
+        kept_ref = reinterpret_cast<float*>(p + sv.ref);
+        kept_shift = reinterpret_cast<float*>(p + sv.shift);
         idx = reinterpret_cast<int32_t*>(p + sv.idx);
         count = reinterpret_cast<int32_t*>(p + sv.count);
     }
@@ -1245,12 +1593,28 @@ hipError_t launch_token_logp(const muon_token_logp_args& a, void* workspace, hip
     l.vp = sh.vp;
     TL_TRY(a.saved ? launch_logits<LG_SAVE>(l, sh.edge, sh.parts, s) : launch_logits<LG_STATS>(l, sh.edge, sh.parts, s));
     const CombineArgs c{m, sums, zt, static_cast<size_t>(sh.tp), 1, sh.ta(), a.targets, a.vocab, a.logp, a.lse, idx, count, a.tokens,
-                        kept};
+                        scale2, kept_logp, kept_ref, kept_shift};
     hipLaunchKernelGGL(combine_kernel<32>, dim3(static_cast<unsigned>(sh.tp / 32)), dim3(256), 0, s, c);
     return hipGetLastError();
 }
 
+namespace {
+hipError_t launch_few_backward(const muon_token_logp_backward_args& a, char* ws, hipStream_t s) {
+    FewPlan pl(a);
+    const char* saved = static_cast<const char*>(a.saved);
+    if (!saved) {
+        pl.forward.logp = reinterpret_cast<float*>(ws + pl.logp);
+        pl.forward.lse = reinterpret_cast<float*>(ws + pl.lse);
+        pl.forward.saved = ws + pl.saved;
+        TL_TRY(launch_token_logp(pl.forward, ws + pl.workspace, s));
+        saved = ws + pl.saved;
+    }
+    return launch_few_grads(a, pl, saved, reinterpret_cast<float*>(ws + pl.slab), s);
+}
+}  // namespace
+
 hipError_t launch_token_logp_backward(const muon_token_logp_backward_args& a, void* workspace, hipStream_t s) {
+    if (few_backward(a)) return launch_few_backward(a, static_cast<char*>(workspace), s);
     const BackwardPlan pl(a);
     const Shape& sh = pl.sh;
     const SavedPlan sv(sh);
@@ -1281,7 +1645,7 @@ hipError_t launch_token_logp_backward(const muon_token_logp_backward_args& a, vo
         PrepareArgs p{};
         const int col_tiles = static_cast<int>(ceil_div(sh.cols, 64));
         if (a.grad_hidden && c == 0) {
-            p.head = {a.head, static_cast<size_t>(a.ld_head), sh.vocab, sh.cols, 0, {}, reinterpret_cast<uint16_t*>(ws + pl.head_t),
+            p.head = {a.head, static_cast<size_t>(a.ld_head), sh.vocab, sh.cols, 0, live, reinterpret_cast<uint16_t*>(ws + pl.head_t),
                       vp, vp * sh.cols, scales ? scales + 1 : nullptr};
             p.head_rows = static_cast<int>(ceil_div(sh.vocab, 64));
             p.head_blocks = p.head_rows * col_tiles;
@@ -1307,7 +1671,8 @@ hipError_t launch_token_logp_backward(const muon_token_logp_backward_args& a, vo
         }
         if (saved) {
             const DzArgs d{saved + sv.e, reinterpret_cast<const float*>(saved + sv.m),
-                           reinterpret_cast<const float*>(saved + sv.logp), static_cast<size_t>(sh.tp), sh.edge, live,
+                           reinterpret_cast<const float*>(saved + sv.logp), reinterpret_cast<const float*>(saved + sv.ref),
+                           reinterpret_cast<const float*>(saved + sv.shift), a.scale * LOG2E, static_cast<size_t>(sh.tp), sh.edge, live,
                            a.targets, a.lse, a.grad_logp, a.scale, static_cast<int>(a.vocab), vp,
                            static_cast<size_t>(pl.chunk), dz, dzt, dz_part, dz_part, dz_scale};
             const dim3 grid(static_cast<unsigned>(vp / 64), static_cast<unsigned>(pl.chunk / 64));

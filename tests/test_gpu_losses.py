@@ -251,3 +251,25 @@ def test_losses_in_a_graph_and_on_another_stream(gpu_lib):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("count", [16308, 3000])
+def test_policy_loss_near_zero(gpu_lib, count):
+    # two sequences whose advantages sum to nearly nothing: the loss is far smaller than its terms, whose rounding must not
+    # show.  A term is 1 + expm1(d) times A in fp64: d is exact (both log-probabilities are multiples of 2^-20 below 8), expm1 is
+    # within 2 ulp, so the mean is off by at most 2^-22 of the mean of |expm1(d) A|, and the loss itself is rounded once.
+    import torch
+    rng = np.random.default_rng(5)
+    n = 2 * count
+    old = -np.round(rng.random(n) * 2.0 ** 22) / 2.0 ** 20
+    d = np.round(rng.standard_normal(n) * 0.01 * 2.0 ** 20) / 2.0 ** 20
+    adv = np.array([1.0, -1.0], dtype=np.float32)
+    offsets = torch.tensor([0, count, n], dtype=torch.int64, device="cuda")
+    put = lambda x: torch.from_numpy(x.astype(np.float32)).cuda()
+    loss = torch.empty(1, device="cuda")
+    grad = torch.empty(n, device="cuda")
+    gpu_lib.muon_policy_loss(put(old + d), put(old), put(adv), offsets, loss, grad_logp=grad, reduction="sequence", per_sequence=True,
+                             clip_low=0.2, clip_high=0.28)
+    a = np.repeat(adv.astype(np.float64), count)
+    ref = -(np.exp(d) * a).sum() / n
+    assert abs(float(loss) - ref) <= 2.0 ** -22 * np.abs(np.expm1(d) * a).mean() + 2.0 ** -23 * abs(ref), (float(loss), ref)

@@ -338,3 +338,59 @@ def test_token_logp_tokens_in_chunks(gpu_lib, use_saved):
     for got, ref in ((gh, rh), (gw, rw)):
         assert float((got.double() - ref).norm() / ref.norm()) <= 1e-5
     assert not gh[y < 0].any()
+
+
+# bf16 calls of up to 64 tokens: dz goes as two bf16 parts (2^-16 of it is lost) formed from exp(z - m) in fp16 (2^-11 of it,
+# and 2^-25 of the largest p below fp16's normal range), so the bounds are tighter than in the general case
+@pytest.mark.parametrize("t,d,v", [(1, 7, 33), (15, 131, 4100), (16, 1000, 95), (31, 130, 513), (33, 264, 1027), (64, 77, 2000)])
+@pytest.mark.parametrize("scale", [0.8, -1.3])
+@pytest.mark.parametrize("use_saved", [True, False])
+def test_token_logp_few_tokens_gradients(gpu_lib, t, d, v, scale, use_saved):
+    print("[token_logp few]", t, d, v, scale, use_saved, flush=True)
+    h, w, y, c = _inputs(t * 31 + d, t, d, v, "bf16", ignored=0.25 if t > 1 else 0.0)
+    saved = _saved(gpu_lib, h, w) if use_saved else None
+    logp, lse = _forward(gpu_lib, h, w, y, scale, saved=saved)
+    _check_forward(h, w, y, scale, "bf16", logp, lse)
+    gh, gw = _backward(gpu_lib, h, w, y, lse, c, scale, saved=saved)
+    hv, wv, E, sums = _bounds(h, w, y, scale, "bf16")
+    yv, cv = np.asarray(y.cpu()), _np(c)
+    rh, rw, dz, p = to.token_logp_backward(hv, wv, yv, cv, scale=np.float32(scale))
+    off = np.abs(dz) * 2.0 ** -16 + np.abs(scale * cv)[:, None] * (p * (2.0 ** -11 + 2 * E[:, None] + sums) + 2.0 ** -25 * p.max(1)[:, None])
+    b = off @ np.abs(wv) + (v / 16 + 32) * U * (np.abs(dz) @ np.abs(wv)) + ROUND["bf16"] * np.abs(rh) + 1e-38
+    assert np.all(np.abs(_np(gh) - rh) <= b), float(np.max(np.abs(_np(gh) - rh) / b))
+    b = off.T @ np.abs(hv) + (t / 16 + 32) * U * (np.abs(dz).T @ np.abs(hv)) + ROUND["bf16"] * np.abs(rw) + 1e-38
+    assert np.all(np.abs(_np(gw) - rw) <= b), float(np.max(np.abs(_np(gw) - rw) / b))
+    assert not _np(gh)[yv < 0].any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("t", [3, 70, 300])
+@pytest.mark.parametrize("scale", [-2.0, 0.0])
+@pytest.mark.parametrize("use_saved", [True, False])
+def test_token_logp_scales_of_any_sign(gpu_lib, dtype, t, scale, use_saved):
+    print("[token_logp scale]", t, dtype, scale, use_saved, flush=True)
+    h, w, y, c = _inputs(41, t, 96, 700, dtype)
+    saved = _saved(gpu_lib, h, w) if use_saved else None
+    logp, lse = _forward(gpu_lib, h, w, y, scale, saved=saved)
+    _check_forward(h, w, y, scale, dtype, logp, lse)
+    _check_backward(h, w, y, c, scale, dtype, *_backward(gpu_lib, h, w, y, lse, c, scale, saved=saved))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("t", [4, 90, 300])
+@pytest.mark.parametrize("use_saved", [True, False])
+def test_token_logp_target_far_below_the_best(gpu_lib, dtype, t, use_saved):
+    # logits 300 apart in exact arithmetic: the target's probability is 0 in fp32, the best token's 1
+    import torch
+    h, w, y, c = _inputs(42, t, 64, 500, dtype, ignored=0.0, lift=0.0)
+    h[:, :2], w[:, :2] = 0, 0
+    w[7, 0], w[8, 0] = 16, -16
+    h[0, 0], h[1, 0] = 16, -16                        # 7 wins by 256 (over 8, by 512), or 8 does
+    y[0], y[1], y[2] = 8, 11, 499
+    saved = _saved(gpu_lib, h, w) if use_saved else None
+    logp, lse = _forward(gpu_lib, h, w, y, saved=saved)
+    _check_forward(h, w, y, 1.0, dtype, logp, lse)
+    assert float(logp[0]) < -500 and float(logp[1]) < -200
+    gh, gw = _backward(gpu_lib, h, w, y, lse, c, saved=saved)
+    _check_backward(h, w, y, c, 1.0, dtype, gh, gw)
+    assert torch.isfinite(gh).all() and torch.isfinite(gw).all()
