@@ -18,8 +18,8 @@
 //    once, so that both gradients are k-contiguous products (C rows = columns of the gradient,
 //    C columns = its rows).  Few tiles: the sum over k is split over workgroups that leave fp32
 //    tiles, added in order by slab_sum_kernel.
-//  - fp32 operands travel as two fp16 parts under a scale (product_tile.h), dz in fp32 calls too: absmax_kernel and
-//    scales_kernel find the scales.
+//  - fp32 operands travel as two fp16 parts under a scale (product_tile.h), dz in fp32 calls too: absmax_kernel
+//    finds the largest values, and the kernels that make the copies the scales.
 //  - Few tokens: what counts is the head's way through memory, so each step reads (or writes) it once where it is,
 //    with 16 x 16 MFMAs and no staging (fp32 as three bf16 parts there, which need no scale).
 //
@@ -123,6 +123,81 @@ struct Live {
 };
 
 // ---------------------------------------------------------------------------
+// Scales of fp32 operands
+// ---------------------------------------------------------------------------
+
+// Bits of the largest finite |x| over some rows, one partial a workgroup: head_blocks of them for head, the others for the
+// scored rows of hidden.
+constexpr int ABS_HEAD = 1024, ABS_HIDDEN = 128;
+struct AbsMaxArgs {
+    const float *head, *hidden;
+    size_t ld_head, ld_hidden;
+    int64_t vocab, cols;
+    Live live;
+    uint32_t* part;
+};
+__device__ __forceinline__ uint32_t block_max(uint32_t m, uint32_t* red) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), o, 64)));
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+    __syncthreads();
+    for (int w = 0; w < static_cast<int>(blockDim.x >> 6); ++w) m = max(m, red[w]);
+    return m;
+}
+__device__ __forceinline__ uint32_t finite_bits(float x) {
+    const uint32_t b = __float_as_uint(x) & 0x7fffffffu;
+    return b < 0x7f800000u ? b : 0u;
+}
+__global__ __launch_bounds__(256) void absmax_kernel(AbsMaxArgs a) {
+    __shared__ uint32_t red[4];
+    const bool head = blockIdx.x < ABS_HEAD;
+    const int b = head ? blockIdx.x : blockIdx.x - ABS_HEAD, blocks = head ? ABS_HEAD : ABS_HIDDEN;
+    const int64_t rows = head ? a.vocab : a.live.rows(), runs = (a.cols + 7) / 8;
+    uint32_t m = 0;
+    for (int64_t r = 4 * b + static_cast<int>(threadIdx.x >> 6); r < rows; r += 4 * blocks) {
+        const auto* q = G(head ? a.head + static_cast<size_t>(r) * a.ld_head : a.hidden + static_cast<size_t>(a.live.idx[a.live.first + r]) * a.ld_hidden);
+        for (int64_t k = threadIdx.x & 63; k < runs; k += 64) {
+            Run<float> x;
+            if (8 * k + 8 <= a.cols) x.load(q, static_cast<unsigned>(8 * k));
+            else x.load(q, static_cast<unsigned>(8 * k), static_cast<unsigned>(a.cols - 8 * k));
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m = max(m, finite_bits(x.get(e)));
+        }
+    }
+    m = block_max(m, red);
+    if (threadIdx.x == 0) a.part[blockIdx.x] = m;
+}
+// The power of two that brings the largest value to 2^14 .. 2^15.
+__device__ __forceinline__ float scale_of(uint32_t bits) {
+    if (bits == 0) return 1.0f;
+    const int s = min(14 - (static_cast<int>(bits >> 23) - 127), 126);   // at least -113: a normal number both ways
+    return __uint_as_float(static_cast<uint32_t>(s + 127) << 23);
+}
+// An operand's scale from absmax_kernel's partials, by a workgroup that is about to use it.
+__device__ __forceinline__ float operand_scale(const uint32_t* part, bool head, uint32_t* red) {
+    const int first = head ? 0 : ABS_HEAD, n = head ? ABS_HEAD : ABS_HIDDEN;
+    uint32_t m = 0;
+    for (int k = threadIdx.x; k < n; k += blockDim.x) m = max(m, part[first + k]);
+    return scale_of(block_max(m, red));
+}
+// dz's: no value exceeds |scale grad_logp| of its token.
+struct DzScaleArgs {
+    Live live;
+    const float* grad_logp;
+    float scale;
+    float* out;
+};
+__device__ __forceinline__ void dz_scale(const DzScaleArgs& a, uint32_t* red) {
+    uint32_t m = 0;
+    const int n = a.live.rows();
+#pragma unroll 8
+    for (int r = threadIdx.x; r < n; r += blockDim.x) m = max(m, finite_bits(a.scale * a.grad_logp[a.live.idx[a.live.first + r]]));
+    m = block_max(m, red);
+    if (threadIdx.x == 0) *a.out = scale_of(m);
+}
+
+// ---------------------------------------------------------------------------
 // Operand copies
 // ---------------------------------------------------------------------------
 
@@ -134,16 +209,31 @@ struct PackArgs {
     Live live;
     uint16_t* dst;
     size_t dst_ld, part;   // elements
-    const float* scale;    // two parts: the operand's scale
+    const float* scale;    // two parts, transposes: the operand's scale
 };
 
-// dst[part][r][0 .. dst_ld) = parts of src[row r], zero past its columns.
+// Copies for the logits' product, dst[part][r][0 .. dst_ld) = parts of src[row r], zero past its columns: of head (the first
+// head_blocks workgroups) and of hidden.
+struct PackBothArgs {
+    PackArgs head, hidden;
+    int head_blocks, hidden_blocks;
+    const uint32_t* absmax;   // two parts: absmax_kernel's partials
+    float* scales;            // and where the scales of hidden and head are left
+};
 template <typename T, int PARTS>
-__global__ __launch_bounds__(256) void pack_kernel(PackArgs a) {
+__global__ __launch_bounds__(256) void pack_kernel(PackBothArgs both) {
+    __shared__ uint32_t red[4];
+    const bool head = static_cast<int>(blockIdx.x) < both.head_blocks;
+    const PackArgs& a = head ? both.head : both.hidden;
+    const int block = head ? blockIdx.x : blockIdx.x - both.head_blocks, blocks = head ? both.head_blocks : both.hidden_blocks;
     const int64_t rows = a.use_live ? a.live.rows() : a.rows;
     const int64_t per = a.dst_ld / 8, n = rows * per;
-    const float scale = PARTS == 1 ? 1.0f : *a.scale;
-    for (int64_t q = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; q < n; q += static_cast<int64_t>(gridDim.x) * 256) {
+    float scale = 1.0f;
+    if constexpr (PARTS == 2) {
+        scale = operand_scale(both.absmax, head, red);
+        if (block == 0 && threadIdx.x == 0) both.scales[head] = scale;
+    }
+    for (int64_t q = static_cast<int64_t>(block) * 256 + threadIdx.x; q < n; q += static_cast<int64_t>(blocks) * 256) {
         const int64_t r = q / per, c = (q - r * per) * 8;
         const size_t s = static_cast<size_t>(a.use_live ? a.live.idx[a.live.first + r] : r) * a.ld + c;
         uint16_t v[8][2];
@@ -200,87 +290,8 @@ template <typename T, int PARTS> __device__ __forceinline__ void transpose_tile(
     }
 }
 
-// ---- scales of fp32 operands ----
-
-// Bits of the largest finite |x| over some rows, one partial a workgroup: head_blocks of them for head, the others for the
-// scored rows of hidden.
-constexpr int ABS_HEAD = 1024, ABS_HIDDEN = 128;
-struct AbsMaxArgs {
-    const float *head, *hidden;
-    size_t ld_head, ld_hidden;
-    int64_t vocab, cols;
-    Live live;
-    uint32_t* part;
-};
-__device__ __forceinline__ uint32_t block_max(uint32_t m, uint32_t* red) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), o, 64)));
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
-    __syncthreads();
-    for (int w = 0; w < static_cast<int>(blockDim.x >> 6); ++w) m = max(m, red[w]);
-    return m;
-}
-__device__ __forceinline__ uint32_t finite_bits(float x) {
-    const uint32_t b = __float_as_uint(x) & 0x7fffffffu;
-    return b < 0x7f800000u ? b : 0u;
-}
-__global__ __launch_bounds__(256) void absmax_kernel(AbsMaxArgs a) {
-    __shared__ uint32_t red[4];
-    const bool head = blockIdx.x < ABS_HEAD;
-    const int b = head ? blockIdx.x : blockIdx.x - ABS_HEAD, blocks = head ? ABS_HEAD : ABS_HIDDEN;
-    const int64_t rows = head ? a.vocab : a.live.rows(), runs = (a.cols + 7) / 8;
-    uint32_t m = 0;
-    for (int64_t r = 4 * b + static_cast<int>(threadIdx.x >> 6); r < rows; r += 4 * blocks) {
-        const auto* q = G(head ? a.head + static_cast<size_t>(r) * a.ld_head : a.hidden + static_cast<size_t>(a.live.idx[a.live.first + r]) * a.ld_hidden);
-        for (int64_t k = threadIdx.x & 63; k < runs; k += 64) {
-            Run<float> x;
-            if (8 * k + 8 <= a.cols) x.load(q, static_cast<unsigned>(8 * k));
-            else x.load(q, static_cast<unsigned>(8 * k), static_cast<unsigned>(a.cols - 8 * k));
-#pragma unroll
-            for (int e = 0; e < 8; ++e) m = max(m, finite_bits(x.get(e)));
-        }
-    }
-    m = block_max(m, red);
-    if (threadIdx.x == 0) a.part[blockIdx.x] = m;
-}
-// The power of two that brings the largest value to 2^14 .. 2^15.
-__device__ __forceinline__ float scale_of(uint32_t bits) {
-    if (bits == 0) return 1.0f;
-    const int s = min(14 - (static_cast<int>(bits >> 23) - 127), 126);   // at least -113: a normal number both ways
-    return __uint_as_float(static_cast<uint32_t>(s + 127) << 23);
-}
-// operands: scales of hidden and head from absmax_kernel's partials.  dz: that of dz, whose values are at most
-// |scale grad_logp| of their token.  Either may be NULL.
-struct ScalesArgs {
-    const uint32_t* part;
-    float *operands, *dz;
-    Live live;
-    const float* grad_logp;
-    float scale;
-};
-__global__ __launch_bounds__(1024) void scales_kernel(ScalesArgs a) {
-    __shared__ uint32_t red[16];
-    if (a.operands) {
-        const uint32_t w = block_max(threadIdx.x < ABS_HEAD ? a.part[threadIdx.x] : 0u, red);
-        const uint32_t h = block_max(threadIdx.x < ABS_HIDDEN ? a.part[ABS_HEAD + threadIdx.x] : 0u, red);
-        if (threadIdx.x == 0) {
-            a.operands[0] = scale_of(h);
-            a.operands[1] = scale_of(w);
-        }
-    }
-    if (a.dz) {
-        uint32_t m = 0;
-        const int n = a.live.rows();
-#pragma unroll 4
-        for (int r = threadIdx.x; r < n; r += 1024) m = max(m, finite_bits(a.scale * a.grad_logp[a.live.idx[a.live.first + r]]));
-        m = block_max(m, red);
-        if (threadIdx.x == 0) *a.dz = scale_of(m);
-    }
-}
-
-// One launch for what the gradients' products need: the transposes of head and hidden and, for grad_hidden, zeros
-// in the rows of tokens that are not scored.  Each is a run of workgroups; dst NULL or no rows: none.
+// One launch for what the gradients' products need: the transposes of head and hidden, the scale of dz (two parts) and, for
+// grad_hidden, zeros in the rows of tokens that are not scored.  Each is a run of workgroups.
 struct PrepareArgs {
     PackArgs head, hidden;
     int head_blocks, hidden_blocks;   // 64 x 64 tiles, along the rows first
@@ -290,6 +301,7 @@ struct PrepareArgs {
     void* zero;
     size_t zero_ld;
     int zero_blocks;
+    DzScaleArgs dz;                   // one workgroup, if out is not NULL
 };
 template <typename T, int PARTS> __global__ __launch_bounds__(256) void prepare_kernel(PrepareArgs a) {
     __shared__ float tile[64][65];
@@ -305,6 +317,10 @@ template <typename T, int PARTS> __global__ __launch_bounds__(256) void prepare_
         return;
     }
     b -= a.hidden_blocks;
+    if (PARTS == 2 && a.dz.out && b-- == 0) {
+        dz_scale(a.dz, reinterpret_cast<uint32_t*>(tile));
+        return;
+    }
     for (int64_t t = static_cast<int64_t>(b) * 4 + (threadIdx.x >> 6); t < a.tokens; t += 4 * static_cast<int64_t>(a.zero_blocks))
         if (a.targets[t] < 0)
             for (int64_t c = threadIdx.x & 63; c < a.cols; c += 64) st_el<T>(a.zero, t * a.zero_ld + c, 0.0f);
@@ -1412,14 +1428,6 @@ hipError_t launch_live(const int64_t* targets, int64_t tokens, int32_t* idx, int
     return hipGetLastError();
 }
 
-hipError_t launch_pack(const PackArgs& p, int dtype, hipStream_t s) {
-    const int64_t work = p.rows * static_cast<int64_t>(p.dst_ld / 8);
-    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(ceil_div(work, 256), 8 * CUS)));
-    if (dtype == MUON_BF16) hipLaunchKernelGGL((pack_kernel<uint16_t, 1>), grid, dim3(256), 0, s, p);
-    else hipLaunchKernelGGL((pack_kernel<float, 2>), grid, dim3(256), 0, s, p);
-    return hipGetLastError();
-}
-
 template <int EDGE, int MODE> hipError_t launch_logits_edge(const LogitsArgs& l, int parts, hipStream_t s) {
     const dim3 grid(static_cast<unsigned>(l.ta) * l.tb), block(pt::Tile<EDGE>::THREADS);
     if (parts == 2) hipLaunchKernelGGL((logits_kernel<EDGE, 2, MODE, false>), grid, block, 0, s, l);
@@ -1449,45 +1457,43 @@ hipError_t launch_grad(GradArgs g, const GradPlan& pl, float* slab, int parts, i
     return pl.edge == 256 ? launch_grad_edge<256>(g, parts, dtype, last, s) : launch_grad_edge<128>(g, parts, dtype, last, s);
 }
 
-// Scales of fp32 operands (part NULL: known already) and of dz (dz NULL: not wanted).
-hipError_t launch_scales(const void* hidden, int64_t ld_hidden, const void* head, int64_t ld_head, const Shape& sh, const Live& live,
-                         uint32_t* part, float* operands, float* dz, const float* grad_logp, float scale, hipStream_t s) {
-    if (part) {
-        const AbsMaxArgs m{static_cast<const float*>(head), static_cast<const float*>(hidden), static_cast<size_t>(ld_head),
-                           static_cast<size_t>(ld_hidden), sh.vocab, sh.cols, live, part};
-        hipLaunchKernelGGL(absmax_kernel, dim3(ABS_HEAD + ABS_HIDDEN), dim3(256), 0, s, m);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    const ScalesArgs c{part, part ? operands : nullptr, dz, live, grad_logp, scale};
-    hipLaunchKernelGGL(scales_kernel, dim3(1), dim3(1024), 0, s, c);
+hipError_t launch_absmax(const void* hidden, int64_t ld_hidden, const void* head, int64_t ld_head, const Shape& sh, const Live& live,
+                         uint32_t* part, hipStream_t s) {
+    const AbsMaxArgs m{static_cast<const float*>(head), static_cast<const float*>(hidden), static_cast<size_t>(ld_head),
+                       static_cast<size_t>(ld_hidden), sh.vocab, sh.cols, live, part};
+    hipLaunchKernelGGL(absmax_kernel, dim3(ABS_HEAD + ABS_HIDDEN), dim3(256), 0, s, m);
     return hipGetLastError();
 }
 
-// The logits' operands: packed copies where the products cannot read the caller's rows.
+// The logits' operands: packed copies where the products cannot read the caller's rows.  absmax: two parts.
 hipError_t logits_operands(const Shape& sh, const void* hidden, int64_t ld_hidden, const void* head, int64_t ld_head,
-                           int dtype, char* hidden_copy, char* head_copy, bool pack_head, LogitsArgs& l, hipStream_t s) {
+                           int dtype, char* hidden_copy, char* head_copy, bool pack_head, const uint32_t* absmax, float* scales,
+                           LogitsArgs& l, hipStream_t s) {
     const size_t row = sizeof(uint16_t) * sh.dp;
     l.steps = static_cast<int>(sh.dp / pt::KS);
     // copies have zeros past the last column; a row read in place has none, so its last step stops there (in both)
     l.tail = sh.direct_head || sh.direct_hidden ? static_cast<int>(ceil_div(sh.cols - (sh.dp - pt::KS), 8)) : pt::CHUNKS;
     l.vocab = static_cast<int>(sh.vocab);
     l.ta = sh.ta();
+    l.scales = scales;
     l.a = sh.direct_head ? static_cast<const char*>(head) : head_copy;
     l.a_ld = sh.direct_head ? 2 * static_cast<size_t>(ld_head) : row;
     l.a_part = row * sh.vocab;
-    if (!sh.direct_head && pack_head)
-        TL_TRY(launch_pack({head, static_cast<size_t>(ld_head), sh.vocab, sh.cols, 0, {}, reinterpret_cast<uint16_t*>(head_copy),
-                            static_cast<size_t>(sh.dp), static_cast<size_t>(sh.dp) * sh.vocab, l.scales + 1}, dtype, s));
     l.gather = sh.direct_hidden;
     l.b = sh.direct_hidden ? static_cast<const char*>(hidden) : hidden_copy;
     l.b_ld = sh.direct_hidden ? 2 * static_cast<size_t>(ld_hidden) : row;
     l.b_part = row * l.live.most;
-    if (!sh.direct_hidden)
-        TL_TRY(launch_pack({hidden, static_cast<size_t>(ld_hidden), l.live.most, sh.cols, 1, l.live,
-                            reinterpret_cast<uint16_t*>(hidden_copy), static_cast<size_t>(sh.dp),
-                            static_cast<size_t>(sh.dp) * l.live.most, l.scales}, dtype, s));
-    return hipSuccess;
+    const size_t dp = static_cast<size_t>(sh.dp);
+    auto blocks = [&](int64_t rows) { return static_cast<int>(std::min<int64_t>(ceil_div(rows * sh.dp / 8, 256), 8 * CUS)); };
+    const PackBothArgs p{{head, static_cast<size_t>(ld_head), sh.vocab, sh.cols, 0, {}, reinterpret_cast<uint16_t*>(head_copy), dp, dp * sh.vocab, nullptr},
+                         {hidden, static_cast<size_t>(ld_hidden), l.live.most, sh.cols, 1, l.live, reinterpret_cast<uint16_t*>(hidden_copy), dp,
+                          dp * l.live.most, nullptr},
+                         sh.direct_head || !pack_head ? 0 : blocks(sh.vocab), sh.direct_hidden ? 0 : blocks(l.live.most), absmax, scales};
+    if (p.head_blocks + p.hidden_blocks == 0) return hipSuccess;
+    const dim3 grid(p.head_blocks + p.hidden_blocks);
+    if (dtype == MUON_BF16) hipLaunchKernelGGL((pack_kernel<uint16_t, 1>), grid, dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((pack_kernel<float, 2>), grid, dim3(256), 0, s, p);
+    return hipGetLastError();
 }
 
 template <typename T, int PARTS> hipError_t launch_few(const muon_token_logp_args& a, const ForwardPlan& pl, char* ws, hipStream_t s) {
@@ -1576,13 +1582,10 @@ hipError_t launch_token_logp(const muon_token_logp_args& a, void* workspace, hip
     }
     TL_TRY(launch_live(a.targets, a.tokens, idx, count, a.logp, a.lse, s));
     l.live = {idx, count, 0, static_cast<int32_t>(sh.tp)};
-    if (sh.parts == 2) {
-        float* scales = reinterpret_cast<float*>(a.saved ? static_cast<char*>(a.saved) + SavedPlan(sh).scales : ws + pl.scales);
-        TL_TRY(launch_scales(a.hidden, a.ld_hidden, a.head, a.ld_head, sh, l.live, reinterpret_cast<uint32_t*>(ws + pl.absmax), scales,
-                             nullptr, nullptr, 0.0f, s));
-        l.scales = scales;
-    }
-    TL_TRY(logits_operands(sh, a.hidden, a.ld_hidden, a.head, a.ld_head, a.dtype, ws + pl.hidden, ws + pl.head, true, l, s));
+    uint32_t* absmax = reinterpret_cast<uint32_t*>(ws + pl.absmax);
+    float* scales = reinterpret_cast<float*>(a.saved ? static_cast<char*>(a.saved) + SavedPlan(sh).scales : ws + pl.scales);
+    if (sh.parts == 2) TL_TRY(launch_absmax(a.hidden, a.ld_hidden, a.head, a.ld_head, sh, l.live, absmax, s));
+    TL_TRY(logits_operands(sh, a.hidden, a.ld_hidden, a.head, a.ld_head, a.dtype, ws + pl.hidden, ws + pl.head, true, absmax, scales, l, s));
     l.targets = a.targets;
     l.tb = static_cast<int>(sh.tp / sh.edge);
     l.scale2 = scale2;
@@ -1627,26 +1630,28 @@ hipError_t launch_token_logp_backward(const muon_token_logp_backward_args& a, vo
         count = reinterpret_cast<int32_t*>(ws + pl.count);
         TL_TRY(launch_live(a.targets, a.tokens, const_cast<int32_t*>(idx), const_cast<int32_t*>(count), nullptr, nullptr, s));
     }
-    // hidden and head: as the forward pass left them, or found again; dz: over all tokens, since chunks add up
-    const float *scales = nullptr, *dz_scale = nullptr;
-    if (sh.parts == 2) {
-        float* own = reinterpret_cast<float*>(ws + pl.scales);
-        const bool known = saved && a.tokens > 0;
-        scales = known ? reinterpret_cast<const float*>(saved + sv.scales) : own;
-        dz_scale = own + 2;
-        TL_TRY(launch_scales(a.hidden, a.ld_hidden, a.head, a.ld_head, sh, {idx, count, 0, static_cast<int32_t>(sh.tp)},
-                             known ? nullptr : reinterpret_cast<uint32_t*>(ws + pl.absmax), own, own + 2, a.grad_logp, a.scale, s));
-    }
+    // scales of hidden and head: as the forward pass left them, or found again; of dz: over all tokens, since chunks add up
+    float* own = reinterpret_cast<float*>(ws + pl.scales);
+    uint32_t* absmax = reinterpret_cast<uint32_t*>(ws + pl.absmax);
+    const float* scales = saved && a.tokens > 0 ? reinterpret_cast<const float*>(saved + sv.scales) : own;
+    float* dz_scale = own + 2;
+    const Live everyone{idx, count, 0, static_cast<int32_t>(sh.tp)};
+    if (sh.parts == 2 && !saved) TL_TRY(launch_absmax(a.hidden, a.ld_hidden, a.head, a.ld_head, sh, everyone, absmax, s));
     const size_t vp = sh.vp, dz_part = static_cast<size_t>(pl.chunk) * vp;
     uint16_t* dz = a.grad_hidden ? reinterpret_cast<uint16_t*>(ws + pl.dz) : nullptr;
     uint16_t* dzt = a.grad_head ? reinterpret_cast<uint16_t*>(ws + pl.dzt) : nullptr;
     for (int c = 0; c < pl.chunks; ++c) {
         const Live live{idx, count, static_cast<int32_t>(c * pl.chunk), static_cast<int32_t>(pl.chunk)};
+        LogitsArgs l{};
+        l.live = live;
+        if (!saved)
+            TL_TRY(logits_operands(sh, a.hidden, a.ld_hidden, a.head, a.ld_head, a.dtype, ws + pl.hidden, ws + pl.head, c == 0, absmax, own, l, s));
         PrepareArgs p{};
+        if (sh.parts == 2 && c == 0) p.dz = {everyone, a.grad_logp, a.scale, dz_scale};
         const int col_tiles = static_cast<int>(ceil_div(sh.cols, 64));
         if (a.grad_hidden && c == 0) {
             p.head = {a.head, static_cast<size_t>(a.ld_head), sh.vocab, sh.cols, 0, live, reinterpret_cast<uint16_t*>(ws + pl.head_t),
-                      vp, vp * sh.cols, scales ? scales + 1 : nullptr};
+                      vp, vp * sh.cols, scales + 1};
             p.head_rows = static_cast<int>(ceil_div(sh.vocab, 64));
             p.head_blocks = p.head_rows * col_tiles;
             p.targets = a.targets;
@@ -1663,7 +1668,7 @@ hipError_t launch_token_logp_backward(const muon_token_logp_backward_args& a, vo
             p.hidden_rows = static_cast<int>(pl.chunk / 64);
             p.hidden_blocks = p.hidden_rows * col_tiles;
         }
-        const int prepare = p.head_blocks + p.hidden_blocks + p.zero_blocks;
+        const int prepare = p.head_blocks + p.hidden_blocks + p.zero_blocks + (p.dz.out ? 1 : 0);
         if (prepare > 0) {
             if (sh.parts == 1) hipLaunchKernelGGL((prepare_kernel<uint16_t, 1>), dim3(prepare), dim3(256), 0, s, p);
             else hipLaunchKernelGGL((prepare_kernel<float, 2>), dim3(prepare), dim3(256), 0, s, p);
@@ -1680,11 +1685,7 @@ hipError_t launch_token_logp_backward(const muon_token_logp_backward_args& a, vo
             else hipLaunchKernelGGL((dz_kernel<float, 2>), grid, dim3(256), 0, s, d);
             TL_TRY(hipGetLastError());
         } else {
-            LogitsArgs l{};
-            l.live = live;
-            l.scales = scales;
             l.dz_scale = dz_scale;
-            TL_TRY(logits_operands(sh, a.hidden, a.ld_hidden, a.head, a.ld_head, a.dtype, ws + pl.hidden, ws + pl.head, c == 0, l, s));
             l.targets = a.targets;
             l.tb = static_cast<int>(pl.chunk / sh.edge);
             l.scale2 = a.scale * LOG2E;
@@ -1703,7 +1704,7 @@ hipError_t launch_token_logp_backward(const muon_token_logp_backward_args& a, vo
         g.cols = static_cast<int>(sh.cols);
         g.dz_scale = dz_scale;
         if (a.grad_hidden) {
-            g.scale = scales ? scales + 1 : nullptr;
+            g.scale = scales + 1;
             g.a = ws + pl.head_t;
             g.a_ld = 2 * vp;
             g.a_part = 2 * vp * sh.cols;
