@@ -715,9 +715,11 @@ def muon_token_logp_saved_bytes(hidden, head) -> int:
 
 
 def muon_token_logp_workspace_bytes(hidden, head) -> int:
+    """Workspace of :func:`muon_token_logp` for these operands, with ``saved`` or without."""
     tokens, cols, vocab, ldh, ldw, code = _logp_shape(hidden, head)
-    return _size(load().muon_token_logp_workspace_bytes,
-                 _pack_logp(*_logp_stand_ins(hidden, head)[:5], 0, tokens, cols, vocab, ldh, ldw, 1.0, code))
+    at = _logp_stand_ins(hidden, head)
+    size = load().muon_token_logp_workspace_bytes
+    return max(_size(size, _pack_logp(*at[:5], saved, tokens, cols, vocab, ldh, ldw, 1.0, code)) for saved in (0, at[5]))
 
 
 def _check_saved(lib, saved, packed):
