@@ -9,8 +9,11 @@
 // HBM-bound: the forward pass reads x and r and writes r' and n, the backward pass reads
 // x, r', dn and dr' and writes dx and dr (a full gate adds one each way); a few operations
 // per byte.  So a row is read once and kept in registers, as fp32, by the NT threads that share it:
-// one wave for rows up to 2048 columns (forward; its sums need no barrier), 256 or 1024 threads
-// for longer ones.  The weights are read again for every row: they come from L2.
+// one wave for rows up to 1024 columns (forward; its sums need no barrier), 256 or 1024 threads
+// for longer ones (1003 x 1407 fp32, both passes: 31.5 us, 34.2 with one wave a row; 8192 x 2048 bf16 the same with
+// either).  The weights are read again for every row: they come from L2.
+// 8192 x 2048 bf16: forward 24 us (134 MB, 5.6 TB/s), backward 45 us (201 MB, 4.5 TB/s) and 5.7 us for the weights' partials;
+// one row: 3.8 us, a launch's length.
 //
 // The backward pass needs mean(dxh xh), and dxh needs mean(dh h) first.  With q = g wp xh,
 //   sum dxh xh = sum (dr' + rstd1 dh) q - rstd1 mean(dh h) sum h q,
@@ -26,8 +29,10 @@ namespace muon {
 
 namespace {
 
-constexpr int64_t BN_WAVES = 4096;  // waves of the backward pass's workgroups, at most: 16 a CU
-constexpr int64_t BN_ROWS = 2;      // rows of a workgroup, at least: each leaves a partial weight gradient to sum
+// Waves of the backward pass's workgroups, at most: 16 a CU (8192 x 2048 bf16, both passes: 78 us; 8 a CU 83, 32 a CU 89).
+constexpr int64_t BN_WAVES = 4096;
+// Rows of a workgroup, at least: each leaves a partial weight gradient to sum (1003 x 1407 fp32: 34 us; one row 36, eight 52).
+constexpr int64_t BN_ROWS = 2;
 constexpr int64_t BN_LONG = 8192;   // longest row that one workgroup's registers hold in the backward pass
 constexpr int BN_CHUNK = 2048;      // columns of a longer row a workgroup takes at a time
 
@@ -322,7 +327,7 @@ template <typename T, int NT, int VPT> hipError_t forward(const muon_block_norm_
 template <typename T> hipError_t forward_by_cols(const muon_block_norm_args& a, hipStream_t s) {
     if (a.cols <= 512) return forward<T, 64, 1>(a, s);
     if (a.cols <= 1024) return forward<T, 64, 2>(a, s);
-    if (a.cols <= 2048) return forward<T, 64, 4>(a, s);
+    if (a.cols <= 2048) return forward<T, 256, 1>(a, s);
     if (a.cols <= 4096) return forward<T, 256, 2>(a, s);
     if (a.cols <= 8192) return forward<T, 1024, 1>(a, s);
     if (a.cols <= 16384) return forward<T, 1024, 2>(a, s);

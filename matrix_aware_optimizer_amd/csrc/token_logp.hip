@@ -40,12 +40,17 @@ namespace {
 using pt::u32x4;
 
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
-constexpr int64_t FEW_TOKENS = 64;          // most tokens of few_kernel
+// Most tokens of the few_ kernels (48 tokens x 2048 x 32000 bf16, forward and backward: 141 us, 208 with the tiles' kernels).
+constexpr int64_t FEW_TOKENS = 64;
 constexpr int FEW_ROWS = 32;                // vocabulary entries per workgroup of few_kernel
 constexpr int64_t DZ_BYTES = int64_t{4} << 30;   // both layouts of dz, at most: more tokens go in chunks
 constexpr int CUS = 256;
-constexpr int64_t FEW_TILES = 192;          // 256 x 256 tiles below which the smaller tile serves a product
+// 256 x 256 tiles below which the smaller tile serves a product: some 3/4 of the CUs.  2000 x 1024 x 8192, both passes: 138 us, at a
+// bound of 96 154; 8192 x 2048 x 32000: 2480, at 512 2835; 777 x 1000 x 32003: 270, at 512 303.
+constexpr int64_t FEW_TILES = 192;
 constexpr int PAD = 256;                    // every buffer of dz, e and their statistics is padded to the larger tile
+// Runs of k of a product with few tiles, at most, and k-steps of one, at least: 300 x 512 x 8000, both passes, 60 us; 61 with 8
+// runs or 16 steps, 60 with 32 runs or 4 steps.
 constexpr int MAX_SPLITS = 16, MIN_SPLIT_STEPS = 8;
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -378,6 +383,9 @@ template <typename TL> __device__ __forceinline__ void store_rows(const pt::lds_
     }
 }
 
+// 6144 scored tokens x 2048 x 32000 bf16, keeping e: 752 us, 1071 TFLOP/s (a library product of 8192^3 reaches 1534); the
+// statistics, exponentials and 0.4 GB of e take the difference to the gradients' products.  512 x 1024 x 8192 fp32 (128-tile):
+// 41 us, 3 x 209 TFLOP/s: two rounds of workgroups, bound by LDS reads.
 template <int EDGE, int PARTS, int MODE, bool KTAIL>
 __global__ __launch_bounds__(pt::Tile<EDGE>::THREADS, 2) void logits_kernel(LogitsArgs a) {
     typedef pt::Tile<EDGE> TL;
@@ -573,8 +581,8 @@ struct DzArgs {
     const float* dz_scale;  // two parts
 };
 
-// 64 tokens x 64 entries a workgroup.  Reads 2 (fp32: 4) bytes an element and writes 2 x 2 (fp32: 2 x 4), HBM-bound.
-// E: what e is kept in.
+// 64 tokens x 64 entries a workgroup.  Reads 2 (fp32: 4) bytes an element and writes 2 x 2 (fp32: 2 x 4), HBM-bound
+// (6144 x 32000 bf16: 1.2 GB in 220 us, 5.4 TB/s).  E: what e is kept in.
 template <typename E, int PARTS>
 __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
     __shared__ uint16_t tile[PARTS][64][72];   // [entry][token]
@@ -681,7 +689,8 @@ __device__ __forceinline__ void st_piece(float* p, const u32x4& v, int left) {
     }
 }
 
-// T: the gradient's type.
+// T: the gradient's type.  6144 tokens x 2048 x 32000 bf16: 630 us (grad_hidden) and 790 us (grad_head, 8 tiles by 125),
+// 1279 and 1019 TFLOP/s.
 template <int EDGE, int PARTS, typename T>
 __global__ __launch_bounds__(pt::Tile<EDGE>::THREADS, 2) void grad_kernel(GradArgs a) {
     typedef pt::Tile<EDGE> TL;
@@ -852,7 +861,8 @@ struct FewArgs {
 
 // FEW_ROWS entries x up to 16 NT tokens a workgroup; its four waves take 64 values of k in turn.  Vocabulary
 // along the accumulator rows, tokens along the columns (16 x 16 MFMA).  HBM-bound: the head once,
-// cols x vocab elements; hidden comes from the caches.
+// cols x vocab elements (one token x 2048 x 32000: 25.6 us, 5.1 TB/s); hidden comes from the caches, and for 64 tokens
+// that is what it waits for (52 us).
 template <typename T, int PARTS, int NT>
 __global__ __launch_bounds__(256, NT == 1 ? 4 : 1) void few_kernel(FewArgs a) {
     constexpr int TOK = 16 * NT, GROUPS = 256 / TOK, PER = FEW_ROWS / GROUPS;   // at the end: threads a token, entries a thread
@@ -1014,7 +1024,8 @@ __device__ __forceinline__ void few_row(Run<uint16_t>& r, const uint16_t* row, i
 }
 
 // grad_hidden: a strip of columns and a run of vocabulary tiles a workgroup, its four waves taking tiles in turn; their sums
-// are put together in LDS.  HBM-bound: head once.  16 NT tokens.
+// are put together in LDS.  HBM-bound: head once (2 tokens x 2048 x 32000: 24 us, 5.5 TB/s, from the
+// last-level cache in part; 6 x 3176 x 52257: 127 us, 2.6 TB/s, where few_kernel's plain rows reach 2.8).  16 NT tokens.
 template <int NT> __global__ __launch_bounds__(256, NT == 1 ? 3 : 2) void few_hidden_kernel(FewGradArgs a) {
     constexpr int REGS = 4 * NT;
     constexpr bool AHEAD = NT <= 2;   // registers for the next tile's rows
@@ -1105,7 +1116,8 @@ template <int NT> __global__ __launch_bounds__(256) void few_sum_kernel(FewGradA
 }
 
 // grad_head: a tile of FEW_ROWS entries a workgroup, whose dz is formed once in LDS; its waves take strips of columns in turn.
-// Bound by the writes: head's size once.  KS: runs of 32 tokens.
+// Bound by the writes: head's size once (2 tokens x 2048 x 32000: 31 us, 4.2 TB/s; 6 x 3176 x 52257: 66 us, 5 TB/s).  KS: runs
+// of 32 tokens (64 tokens: 51 us, the products and their operands' way through L2).
 template <int KS> __global__ __launch_bounds__(256, 2) void few_head_kernel(FewGradArgs a) {
     constexpr int VB = FEW_ROWS / 16;
     __shared__ __attribute__((aligned(16))) uint16_t tile[2][FEW_ROWS][32 * KS + 8];   // [entry][token]
@@ -1280,7 +1292,7 @@ struct Shape {
     int parts;
     int64_t tp, vp, dp;      // padded to PAD, PAD, the k-step
     int edge;                // tile of the logits' product
-    bool few;                // forward and backward; a forward pass in fp32 that keeps nothing is so too
+    bool few;                // forward and backward as for few tokens; a forward pass that keeps nothing has its own rule
     int few_tiles;           // of FEW_ROWS entries
     bool direct_hidden, direct_head;   // operands that the products can read where they are: bf16 in whole 16-byte chunks
     Shape(int64_t t, int64_t d, int64_t v, int dtype, const void* hidden, int64_t ld_hidden, const void* head, int64_t ld_head)
@@ -1318,7 +1330,11 @@ struct ForwardPlan {
     size_t idx, count, hidden, head, m, s, zt, absmax, scales, bytes;
     explicit ForwardPlan(const muon_token_logp_args& a)
         : sh(a.tokens, a.cols, a.vocab, a.dtype, a.hidden, a.ld_hidden, a.head, a.ld_head) {
-        few = sh.few || (a.tokens <= FEW_TOKENS && !a.saved);
+        // Beyond 32 tokens few_kernel waits more on hidden than on a head of many tiles, and the large tile takes over where it
+        // can read both in place (48 tokens x 2048 bf16: 32000 entries 50 against 35 us, 16000 29 against 29, 8000 19
+        // against 27; fp32 or copies: 126 against 234 us)
+        const bool large = sh.direct_head && sh.direct_hidden && a.tokens > 32 && sh.few_tiles > 2 * CUS;
+        few = a.saved ? sh.few : a.tokens <= FEW_TOKENS && !large;
         Bump b;
         const size_t part = sizeof(uint16_t) * sh.parts * sh.dp;
         idx = b.take(few || a.saved ? 0 : sizeof(int32_t) * sh.tp);
@@ -1335,8 +1351,8 @@ struct ForwardPlan {
     }
 };
 
-// The backward pass for few tokens: workgroups over the columns and, for grad_hidden, over runs of vocabulary tiles, twice as
-// many as CUs.  Without `saved` a forward pass comes first, into the workspace.
+// The backward pass for few tokens: workgroups over the columns and, for grad_hidden, over runs of vocabulary tiles, as
+// many as the chip holds at once (registers).  Without `saved` a forward pass comes first, into the workspace.
 struct FewPlan {
     Shape sh;
     int strips, splits;
@@ -1344,8 +1360,9 @@ struct FewPlan {
     size_t slab, logp, lse, saved, workspace, bytes;
     explicit FewPlan(const muon_token_logp_backward_args& a)
         : sh(a.tokens, a.cols, a.vocab, a.dtype, a.hidden, a.ld_hidden, a.head, a.ld_head), forward{} {
+        // (6 tokens x 3176 x 52257: 302 us for both passes, 322 with two workgroups a CU, 394 with one; 2 x 2048 x 32000: 90, 88, 91)
         strips = static_cast<int>(ceil_div(a.cols, FEW_STRIP));
-        splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(2 * CUS / strips, sh.few_tiles / 8)));
+        splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((blocks() == 1 ? 3 : 2) * CUS / strips, sh.few_tiles / 8)));
         Bump b;
         slab = b.take(a.grad_hidden ? sizeof(float) * FEW_STRIP * static_cast<size_t>(strips) * splits * 16 * blocks() : 0);
         if (!a.saved) {
