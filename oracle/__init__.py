@@ -26,7 +26,9 @@ Sources (cited by page title and section; the page text is Chinese):
 
 Modules: ``muon_oracle`` (the Muon step), ``jacobi_svd`` (a pin for it),
 ``adamw_oracle`` (AdamW for the non-matrix parameters), ``cayley_oracle``
-(Muon-Cayley on the Stiefel manifold).
+(Muon-Cayley on the Stiefel manifold), ``train_oracle`` (norms around a block,
+token log-probabilities, preference and policy losses; pinned by
+``tests/test_train_oracle_pins.py``).
 
 Parity status: every function here is pinned by ``tests/test_oracle_pins.py``
 against closed forms, invariants, a hand-written Jacobi SVD, library routines
