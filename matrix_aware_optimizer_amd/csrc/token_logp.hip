@@ -11,8 +11,9 @@
 //  - Logits: C = head hidden^T, vocabulary along the accumulator rows, so that a lane holds 64
 //    logits of one token and the softmax's running maximum and sum need one exchange between
 //    lanes and one between two waves.  Only (maximum, sum) per token and tile leave the tile;
-//    combine_kernel joins them.  With `saved` the tile's exp(z - tile maximum) goes out too, in
-//    the operands' precision.
+//    combine_kernel joins them.  With `saved` the tile's exp(z - tile maximum) goes out too: in fp16 in
+//    bf16 calls (values of at most 1: 11 bits where bf16 keeps 8; what falls below 2^-24 of its tile's maximum is 0), else
+//    in fp32.
 //  - Backward: dz comes from `saved` by an elementwise pass, or from the logits' tile formed again.
 //    It is written both token-major and vocabulary-major, and head and hidden are transposed
 //    once, so that both gradients are k-contiguous products (C rows = columns of the gradient,
