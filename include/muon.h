@@ -335,12 +335,13 @@ muon_status muon_token_logp(const muon_token_logp_args* args, void* workspace, s
  * grad_hidden or grad_head may be NULL (not wanted), not both.  `saved` is what
  * muon_token_logp kept for the same inputs, or NULL.  dz is rounded to the
  * operands' precision before the two products: bf16 (up to 64 tokens: two bf16
- * parts, 2^-16), or 22 bits for fp32.
+ * parts, 2^-16), or 22 bits for fp32 (up to 64 tokens: 24).
  *
  * Precision in fp32: the products take each operand as two fp16 parts under one
  * power-of-two scale, 22 bits for values down to 2^-28 of the operand's largest
- * finite one, fewer below.  Those of a forward pass over up to 64 tokens without
- * `saved` take three bf16 parts, 24 bits for values down to 2^-109. */
+ * finite one, fewer below.  Those of up to 64 tokens take three bf16 parts, 24
+ * bits for values down to 2^-109; hidden is scaled for them first in a backward
+ * pass and in a forward pass with `saved`. */
 typedef struct {
     const void*    hidden;
     const void*    head;

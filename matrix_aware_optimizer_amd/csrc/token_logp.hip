@@ -22,7 +22,8 @@
 //  - fp32 operands travel as two fp16 parts under a scale (product_tile.h), dz in fp32 calls too: absmax_kernel
 //    finds the largest values, and the kernels that make the copies the scales.
 //  - Few tokens: what counts is the head's way through memory, so each step reads (or writes) it once where it is,
-//    with 16 x 16 MFMAs and no staging (fp32 as three bf16 parts there, which need no scale).
+//    with 16 x 16 MFMAs and no staging (fp32 as three bf16 parts there: exact down to 2^-109, so that only hidden, which
+//    is small and quickly looked through, gets a scale).
 //
 // The softmax works in base 2: with k' = |scale| log2(e) and acc the product (negated if scale is negative) a tile keeps
 // M = k' max acc, rounded, and sums 2^(k' acc - M), the exponent formed by one fused operation: what M is rounded to
@@ -41,7 +42,8 @@ namespace {
 using pt::u32x4;
 
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
-// Most tokens of the few_ kernels (48 tokens x 2048 x 32000 bf16, forward and backward: 141 us, 208 with the tiles' kernels).
+// Most tokens of the few_ kernels (forward and backward, 48 tokens x 2048 x 32000 bf16: 141 us,
+// 208 with the tiles' kernels; 40 tokens in fp32: 372, 574; 12 tokens x 2048 x 65536 in fp32: 402, 966).
 constexpr int64_t FEW_TOKENS = 64;
 constexpr int FEW_ROWS = 32;                // vocabulary entries per workgroup of few_kernel
 constexpr int64_t DZ_BYTES = int64_t{4} << 30;   // both layouts of dz, at most: more tokens go in chunks
@@ -157,12 +159,13 @@ __device__ __forceinline__ uint32_t finite_bits(float x) {
 }
 __global__ __launch_bounds__(256) void absmax_kernel(AbsMaxArgs a) {
     __shared__ uint32_t red[4];
-    const bool head = blockIdx.x < ABS_HEAD;
-    const int b = head ? blockIdx.x : blockIdx.x - ABS_HEAD, blocks = head ? ABS_HEAD : ABS_HIDDEN;
-    const int64_t rows = head ? a.vocab : a.live.rows(), runs = (a.cols + 7) / 8;
+    const int block = blockIdx.x + (gridDim.x == ABS_HIDDEN ? ABS_HEAD : 0);   // a launch for hidden alone
+    const bool head = block < ABS_HEAD;
+    const int b = head ? block : block - ABS_HEAD, blocks = head ? ABS_HEAD : ABS_HIDDEN;
+    const int64_t rows = head ? a.vocab : a.live.idx ? a.live.rows() : a.live.most, runs = (a.cols + 7) / 8;
     uint32_t m = 0;
     for (int64_t r = 4 * b + static_cast<int>(threadIdx.x >> 6); r < rows; r += 4 * blocks) {
-        const auto* q = G(head ? a.head + static_cast<size_t>(r) * a.ld_head : a.hidden + static_cast<size_t>(a.live.idx[a.live.first + r]) * a.ld_hidden);
+        const auto* q = G(head ? a.head + static_cast<size_t>(r) * a.ld_head : a.hidden + static_cast<size_t>(a.live.idx ? a.live.idx[a.live.first + r] : r) * a.ld_hidden);
         for (int64_t k = threadIdx.x & 63; k < runs; k += 64) {
             Run<float> x;
             if (8 * k + 8 <= a.cols) x.load(q, static_cast<unsigned>(8 * k));
@@ -172,7 +175,7 @@ __global__ __launch_bounds__(256) void absmax_kernel(AbsMaxArgs a) {
         }
     }
     m = block_max(m, red);
-    if (threadIdx.x == 0) a.part[blockIdx.x] = m;
+    if (threadIdx.x == 0) a.part[block] = m;
 }
 // The power of two that brings the largest value to 2^14 .. 2^15.
 __device__ __forceinline__ float scale_of(uint32_t bits) {
@@ -180,12 +183,15 @@ __device__ __forceinline__ float scale_of(uint32_t bits) {
     const int s = min(14 - (static_cast<int>(bits >> 23) - 127), 126);   // at least -113: a normal number both ways
     return __uint_as_float(static_cast<uint32_t>(s + 127) << 23);
 }
+__device__ __forceinline__ int exponent_of(float scale) { return static_cast<int>(__float_as_uint(scale) >> 23) - 127; }
 // An operand's scale from absmax_kernel's partials, by a workgroup that is about to use it.
 __device__ __forceinline__ float operand_scale(const uint32_t* part, bool head, uint32_t* red) {
     const int first = head ? 0 : ABS_HEAD, n = head ? ABS_HEAD : ABS_HIDDEN;
     uint32_t m = 0;
     for (int k = threadIdx.x; k < n; k += blockDim.x) m = max(m, part[first + k]);
-    return scale_of(block_max(m, red));
+    m = block_max(m, red);
+    __syncthreads();   // `red` may be used again
+    return scale_of(m);
 }
 // dz's: no value exceeds |scale grad_logp| of its token.
 struct DzScaleArgs {
@@ -830,8 +836,8 @@ template <> struct FewOrder<3> {
     static constexpr unsigned W = 2u | 0u << 2 | 1u << 4 | 1u << 6, H = 0u | 2u << 2 | 1u << 4 | 0u << 6 | 1u << 8;
 };
 
-// 8 values of k of one row from column k, zero past the last column, as bf16 parts.
-template <typename T, int PARTS> __device__ __forceinline__ void few_load(const void* base, size_t off, int k, int cols, u32x4 (&out)[PARTS]) {
+// 8 values of k of one row from column k, zero past the last column, as bf16 parts (of x scale in fp32).
+template <typename T, int PARTS> __device__ __forceinline__ void few_load(const void* base, size_t off, int k, int cols, float scale, u32x4 (&out)[PARTS]) {
     Run<T> x;
     const auto* row = G(static_cast<const T*>(base) + off);
     if (k + 8 <= cols) x.load(row, k);
@@ -841,7 +847,7 @@ template <typename T, int PARTS> __device__ __forceinline__ void few_load(const 
     } else {
         uint16_t v[8][3];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) split3(x.get(e), v[e]);
+        for (int e = 0; e < 8; ++e) split3(x.get(e) * scale, v[e]);
 #pragma unroll
         for (int p = 0; p < PARTS; ++p)
 #pragma unroll
@@ -856,8 +862,9 @@ struct FewArgs {
     int tokens, cols, vocab, tiles;
     float scale2;
     float *m, *s, *zt;      // M and S: token x tile; target's acc by token
-    uint16_t* e;            // bf16 calls: fp16 2^(k' acc - M), token x vocabulary (pitch vp), or NULL
+    void* e;                // 2^(k' acc - M), token x vocabulary (pitch vp), fp16 in bf16 calls, else fp32; or NULL
     size_t vp;
+    const uint32_t* absmax; // fp32: absmax_kernel's partials for hidden, or NULL: hidden as it is
 };
 
 // FEW_ROWS entries x up to 16 NT tokens a workgroup; its four waves take 64 values of k in turn.  Vocabulary
@@ -876,6 +883,7 @@ __global__ __launch_bounds__(256, NT == 1 ? 4 : 1) void few_kernel(FewArgs a) {
     for (int r = 0; r < 2; ++r) wo[r] = static_cast<size_t>(min(v0 + 16 * r + ln, a.vocab - 1)) * a.ld_head;
 #pragma unroll
     for (int t = 0; t < NT; ++t) ho[t] = static_cast<size_t>(min(16 * t + ln, a.tokens - 1)) * a.ld_hidden;
+    const float hs = PARTS == 1 || !a.absmax ? 1.0f : operand_scale(a.absmax, false, reinterpret_cast<uint32_t*>(red));
     f32x4m_t acc[2][NT] = {};
     constexpr int DEEP = PARTS == 1 ? 2 : 1;   // 64-value runs of k in flight (4: 31.7 us for one token and 32000 x 2048, 2: 29.1)
     for (int k0 = 64 * wave; k0 < a.cols; k0 += 256 * DEEP) {
@@ -884,9 +892,9 @@ __global__ __launch_bounds__(256, NT == 1 ? 4 : 1) void few_kernel(FewArgs a) {
         for (int b = 0; b < 2 * DEEP; ++b) {
             const int k = k0 + 256 * (b >> 1) + 32 * (b & 1) + kg;
 #pragma unroll
-            for (int r = 0; r < 2; ++r) few_load<T, PARTS>(a.head, wo[r], k, a.cols, w[b][r]);
+            for (int r = 0; r < 2; ++r) few_load<T, PARTS>(a.head, wo[r], k, a.cols, 1.0f, w[b][r]);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) few_load<T, PARTS>(a.hidden, ho[t], k, a.cols, h[b][t]);
+            for (int t = 0; t < NT; ++t) few_load<T, PARTS>(a.hidden, ho[t], k, a.cols, hs, h[b][t]);
         }
 #pragma unroll
         for (int b = 0; b < 2 * DEEP; ++b) {
@@ -915,6 +923,7 @@ __global__ __launch_bounds__(256, NT == 1 ? 4 : 1) void few_kernel(FewArgs a) {
 #pragma unroll
     for (int r = 0; r < PER; ++r) {
         z[r] = red[0][PER * g + r][t] + red[1][PER * g + r][t] + red[2][PER * g + r][t] + red[3][PER * g + r][t];
+        if constexpr (PARTS == 3) z[r] = __builtin_amdgcn_ldexpf(z[r], -exponent_of(hs));
         if (a.scale2 < 0.0f) z[r] = -z[r];
         if (v + r >= a.vocab) z[r] = -INFINITY;
         m = fmaxf(m, z[r]);
@@ -929,6 +938,7 @@ __global__ __launch_bounds__(256, NT == 1 ? 4 : 1) void few_kernel(FewArgs a) {
     for (int r = 0; r < PER; ++r) {
         const float e = __builtin_amdgcn_exp2f(fmaf(z[r], k, -shown(m)));
         if constexpr (sizeof(T) == 2) e16[r] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(e));
+        else if (a.e && t < a.tokens) static_cast<float*>(a.e)[t * a.vp + v + r] = e;
         if (r == y && v + r < a.vocab) a.zt[t] = z[r];
         else sum += e;
     }
@@ -939,7 +949,7 @@ __global__ __launch_bounds__(256, NT == 1 ? 4 : 1) void few_kernel(FewArgs a) {
         uint32_t w[PER / 2];
 #pragma unroll
         for (int r = 0; r < PER / 2; ++r) w[r] = e16[2 * r] | static_cast<uint32_t>(e16[2 * r + 1]) << 16;
-        __builtin_memcpy(__builtin_assume_aligned(a.e + t * a.vp + v, 2 * PER), w, sizeof(w));
+        __builtin_memcpy(__builtin_assume_aligned(static_cast<uint16_t*>(a.e) + t * a.vp + v, 2 * PER), w, sizeof(w));
     }
     if (g == 0) {
         sum = part[1][0][t];
@@ -951,14 +961,14 @@ __global__ __launch_bounds__(256, NT == 1 ? 4 : 1) void few_kernel(FewArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Few tokens: gradients, bf16
+// Few tokens: gradients
 // ---------------------------------------------------------------------------
 // Both have gradient columns along the accumulator rows and k (vocabulary entries, or tokens) across rows of an operand that
-// lies k-major.  A lane reads 8 columns (16 bytes) of 8 rows of k, which transposed in its registers are the A
+// lies k-major.  A lane reads 8 columns (16 bytes in bf16) of 8 rows of k, which transposed in its registers are the A
 // fragments of 8 MFMAs: MFMA j takes column 8 p + j of lane group p.  Lane i of 16 takes the run p = 4 (i & 3) + (i >> 2), so
 // that of C row 4 q + e, run 4 e + q, the four lanes q that share a C column hold adjacent runs.
 // dz is formed from e where it is used.  One token's rounded dz would be its whole gradient's error, so dz goes as two
-// bf16 parts, hi + lo.
+// bf16 parts, hi + lo (fp32: three, as everything here; there hidden is scaled).
 
 constexpr int FEW_STRIP = 128;       // gradient columns of a wave
 
@@ -968,7 +978,7 @@ struct FewGradArgs {
     const int64_t* targets;
     int tokens, cols, vocab, tiles, strips, splits;
     float scale2, scale;
-    const uint16_t* e;                 // token x vocabulary, pitch vp (FewArgs)
+    const void* e;                     // token x vocabulary, pitch vp (FewArgs)
     size_t vp;
     const float* m;                    // token x tile
     const float *logp, *ref, *shift;   // by token, as in DzArgs
@@ -976,6 +986,7 @@ struct FewGradArgs {
     float* slab;                       // [split][strip][j][4 registers of every 16 tokens][lane]
     void *grad_hidden, *grad_head;     // or NULL
     size_t ld_grad_hidden, ld_grad_head;
+    const uint32_t* absmax;            // fp32: absmax_kernel's partials for hidden
 };
 
 // What dz of a token takes.
@@ -998,38 +1009,60 @@ struct FewToken {
         return c == 0.0f || v >= vocab ? 0.0f : v == y ? dy : -e * f;
     }
 };
-__device__ __forceinline__ float e_of(uint32_t x) { return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(x))); }
-__device__ __forceinline__ void hi_lo(float x, uint16_t (&p)[2]) {
+// e of entry r of a run
+__device__ __forceinline__ float e_of(const Run<uint16_t>& x, int r) {
+    return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(x.w[r >> 1] >> (16 * (r & 1)))));
+}
+__device__ __forceinline__ float e_of(const Run<float>& x, int r) { return x.get(r); }
+// Parts of dz: hi + lo, or three.
+template <int PARTS> struct DzParts { static constexpr int N = PARTS == 1 ? 2 : 3; };
+__device__ __forceinline__ void dz_parts(float x, uint16_t (&p)[2]) {
     p[0] = f32_to_bf16(x);
     p[1] = f32_to_bf16(x - bf16_to_f32(p[0]));
 }
+__device__ __forceinline__ void dz_parts(float x, uint16_t (&p)[3]) { split3(x, p); }
 
-// Column j of 8 rows as an A fragment.
-__device__ __forceinline__ u32x4 few_fragment(const Run<uint16_t> (&r)[8], int j) {
-    u32x4 out;
+// Column j of 8 rows (times scale, in fp32) as an A fragment.
+__device__ __forceinline__ void few_fragment(const Run<uint16_t> (&r)[8], int j, float, u32x4 (&out)[1]) {
 #pragma unroll
     for (int p = 0; p < 4; ++p)
-        out[p] = __builtin_amdgcn_perm(r[2 * p + 1].w[j >> 1], r[2 * p].w[j >> 1], (j & 1) ? 0x07060302u : 0x05040100u);
-    return out;
+        out[0][p] = __builtin_amdgcn_perm(r[2 * p + 1].w[j >> 1], r[2 * p].w[j >> 1], (j & 1) ? 0x07060302u : 0x05040100u);
 }
-// a times hi + lo.
-__device__ __forceinline__ void few_mfma(f32x4m_t& acc, const u32x4& a, const u32x4 (&b)[2]) {
+__device__ __forceinline__ void few_fragment(const Run<float> (&r)[8], int j, float scale, u32x4 (&out)[3]) {
+    uint16_t v[8][3];
 #pragma unroll
-    for (int p = 1; p >= 0; --p)
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(pt::bf16x8_t, a), __builtin_bit_cast(pt::bf16x8_t, b[p]), acc, 0, 0, 0);
+    for (int k = 0; k < 8; ++k) split3(r[k].get(j) * scale, v[k]);
+#pragma unroll
+    for (int p = 0; p < 3; ++p)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out[p][e] = v[2 * e][p] | static_cast<uint32_t>(v[2 * e + 1][p]) << 16;
+}
+// a times b over their parts, small products first.
+template <int PARTS>
+__device__ __forceinline__ void few_mfma(f32x4m_t& acc, const u32x4 (&a)[PARTS], const u32x4 (&b)[DzParts<PARTS>::N]) {
+    constexpr int N = PARTS == 1 ? 2 : FewOrder<3>::N;
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+        const int pa = PARTS == 1 ? 0 : (FewOrder<3>::W >> 2 * q) & 3u, pb = PARTS == 1 ? 1 - q : (FewOrder<3>::H >> 2 * q) & 3u;
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(pt::bf16x8_t, a[pa]), __builtin_bit_cast(pt::bf16x8_t, b[pb]),
+                                                      acc, 0, 0, 0);
+    }
 }
 __device__ __forceinline__ int few_column(int lane) { return 8 * (4 * (lane & 3) + ((lane & 15) >> 2)); }   // of the strip
-__device__ __forceinline__ void few_row(Run<uint16_t>& r, const uint16_t* row, int col, int cols) {
+template <typename T> __device__ __forceinline__ void few_row(Run<T>& r, const T* row, int col, int cols) {
     if (col + 8 <= cols) r.load(G(row), col);
     else if (col < cols) r.load(G(row), col, cols - col);
 }
 
 // grad_hidden: a strip of columns and a run of vocabulary tiles a workgroup, its four waves taking tiles in turn; their sums
 // are put together in LDS.  HBM-bound: head once (2 tokens x 2048 x 32000: 24 us, 5.5 TB/s, from the
-// last-level cache in part; 6 x 3176 x 52257: 127 us, 2.6 TB/s, where few_kernel's plain rows reach 2.8).  16 NT tokens.
-template <int NT> __global__ __launch_bounds__(256, NT == 1 ? 3 : 2) void few_hidden_kernel(FewGradArgs a) {
-    constexpr int REGS = 4 * NT;
-    constexpr bool AHEAD = NT <= 2;   // registers for the next tile's rows
+// last-level cache in part; 6 x 3176 x 52257: 127 us, 2.6 TB/s, where few_kernel's plain rows reach 2.8).  16 NT tokens, the
+// registers allowing; blockIdx.y: which of them.
+template <typename T, int PARTS, int NT>
+__global__ __launch_bounds__(256, NT == 1 ? 3 : 2) void few_hidden_kernel(FewGradArgs a) {
+    constexpr int REGS = 4 * NT, DP = DzParts<PARTS>::N;
+    constexpr bool AHEAD = PARTS == 1 && NT <= 2;   // registers for the next tile's rows
+    const int t0 = 16 * NT * blockIdx.y;
     __shared__ float red[4][REGS][64];
     const int lane = threadIdx.x & 63, wave = pt::wave_id(), q = lane >> 4;
     const int strip = blockIdx.x % a.strips, split = blockIdx.x / a.strips;
@@ -1037,25 +1070,25 @@ template <int NT> __global__ __launch_bounds__(256, NT == 1 ? 3 : 2) void few_hi
     const int first = static_cast<int>(static_cast<int64_t>(a.tiles) * split / a.splits);
     const int last = static_cast<int>(static_cast<int64_t>(a.tiles) * (split + 1) / a.splits);
     const float k = rate_of(a.scale2);
-    const uint16_t* head = static_cast<const uint16_t*>(a.head);
-    const uint16_t* e = a.e;
+    const T* head = static_cast<const T*>(a.head);
+    const T* e = static_cast<const T*>(a.e);
     FewToken tok[NT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) tok[n].load(a, 16 * n + (lane & 15));
+    for (int n = 0; n < NT; ++n) tok[n].load(a, t0 + 16 * n + (lane & 15));
     struct Chunk {
-        Run<uint16_t> rows[8], e[NT];
+        Run<T> rows[8], e[NT];
         float m[NT];
     };
     auto load = [&](Chunk& c, int tile) {
         const int v = FEW_ROWS * tile + 8 * q;
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
-            c.rows[r] = Run<uint16_t>{};
+            c.rows[r] = Run<T>{};
             few_row(c.rows[r], head + static_cast<size_t>(min(v + r, a.vocab - 1)) * a.ld_head, col, a.cols);
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int t = min(16 * n + (lane & 15), a.tokens - 1);
+            const int t = min(t0 + 16 * n + (lane & 15), a.tokens - 1);
             c.e[n].load(G(e + t * a.vp), v);
             c.m[n] = a.m[static_cast<size_t>(t) * a.tiles + tile];
         }
@@ -1066,30 +1099,31 @@ template <int NT> __global__ __launch_bounds__(256, NT == 1 ? 3 : 2) void few_hi
     for (int tile = first + wave; tile < last; tile += 4) {
         if (!AHEAD) load(now, tile);
         else if (tile + 4 < last) load(next, tile + 4);
-        u32x4 b[NT][2];
+        u32x4 b[NT][DP];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const float f = tok[n].factor(now.m[n], k);
-            uint16_t v[8][2];
+            uint16_t v[8][DP];
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
-                const float x = e_of(now.e[n].w[r >> 1] >> (16 * (r & 1)));
-                hi_lo(tok[n].dz(x, f, FEW_ROWS * tile + 8 * q + r, a.vocab), v[r]);
+                dz_parts(tok[n].dz(e_of(now.e[n], r), f, FEW_ROWS * tile + 8 * q + r, a.vocab), v[r]);
             }
 #pragma unroll
-            for (int p = 0; p < 2; ++p)
+            for (int p = 0; p < DP; ++p)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) b[n][p][r] = v[2 * r][p] | static_cast<uint32_t>(v[2 * r + 1][p]) << 16;
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const u32x4 w = few_fragment(now.rows, j);
+            u32x4 w[PARTS];
+            few_fragment(now.rows, j, 1.0f, w);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) few_mfma(acc[j][n], w, b[n]);
+            for (int n = 0; n < NT; ++n) few_mfma<PARTS>(acc[j][n], w, b[n]);
         }
         if (AHEAD) now = next;
     }
-    float* slab = a.slab + (static_cast<size_t>(split) * a.strips + strip) * (8 * REGS * 64);
+    const int all = REGS * gridDim.y;
+    float* slab = a.slab + (static_cast<size_t>(split) * a.strips + strip) * (8 * all * 64) + REGS * blockIdx.y * 64;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         __syncthreads();
@@ -1099,13 +1133,13 @@ template <int NT> __global__ __launch_bounds__(256, NT == 1 ? 3 : 2) void few_hi
             for (int r = 0; r < 4; ++r) red[wave][4 * n + r][lane] = acc[j][n][r];
         __syncthreads();
         for (int x = wave; x < REGS; x += 4)
-            slab[(j * REGS + x) * 64 + lane] = red[0][x][lane] + red[1][x][lane] + red[2][x][lane] + red[3][x][lane];
+            slab[(j * all + x) * 64 + lane] = red[0][x][lane] + red[1][x][lane] + red[2][x][lane] + red[3][x][lane];
     }
 }
 
 // The splits' sums, in order, to grad_hidden; zeros for tokens that are not scored.  An element a thread.
-template <int NT> __global__ __launch_bounds__(256) void few_sum_kernel(FewGradArgs a) {
-    constexpr int REGS = 4 * NT;
+template <typename T, int BLOCKS> __global__ __launch_bounds__(256) void few_sum_kernel(FewGradArgs a) {
+    constexpr int REGS = 4 * BLOCKS;
     const int i = blockIdx.x * 256 + threadIdx.x, lane = i & 63, x = (i >> 6) % REGS, js = (i >> 6) / REGS;
     const int t = 16 * (x >> 2) + (lane & 15), col = FEW_STRIP * (js >> 3) + 8 * (4 * (x & 3) + (lane >> 4)) + (js & 7);
     if (t >= a.tokens || col >= a.cols) return;
@@ -1113,24 +1147,25 @@ template <int NT> __global__ __launch_bounds__(256) void few_sum_kernel(FewGradA
     float v = 0.0f;
 #pragma unroll 8
     for (int s = 0; s < a.splits; ++s) v += a.slab[s * step + i];
-    st_el<uint16_t>(a.grad_hidden, t * a.ld_grad_hidden + col, a.targets[t] < 0 ? 0.0f : v);
+    st_el<T>(a.grad_hidden, t * a.ld_grad_hidden + col, a.targets[t] < 0 ? 0.0f : v);
 }
 
 // grad_head: a tile of FEW_ROWS entries a workgroup, whose dz is formed once in LDS; its waves take strips of columns in turn.
 // Bound by the writes: head's size once (2 tokens x 2048 x 32000: 31 us, 4.2 TB/s; 6 x 3176 x 52257: 66 us, 5 TB/s).  KS: runs
 // of 32 tokens (64 tokens: 51 us, the products and their operands' way through L2).
-template <int KS> __global__ __launch_bounds__(256, 2) void few_head_kernel(FewGradArgs a) {
-    constexpr int VB = FEW_ROWS / 16;
-    __shared__ __attribute__((aligned(16))) uint16_t tile[2][FEW_ROWS][32 * KS + 8];   // [entry][token]
+template <typename T, int PARTS, int KS> __global__ __launch_bounds__(256, 2) void few_head_kernel(FewGradArgs a) {
+    constexpr int DP = DzParts<PARTS>::N, VB = FEW_ROWS / 16;
+    __shared__ __attribute__((aligned(16))) uint16_t tile[DP][FEW_ROWS][32 * KS + 8];   // [entry][token]
     const int lane = threadIdx.x & 63, wave = pt::wave_id(), q = lane >> 4;
     const int v0 = blockIdx.x * FEW_ROWS;
     const float k = rate_of(a.scale2);
-    const uint16_t* e = a.e;
+    const T* e = static_cast<const T*>(a.e);
+    const float hs = PARTS == 1 ? 1.0f : operand_scale(a.absmax, false, reinterpret_cast<uint32_t*>(tile));
     const unsigned long long live = __ballot(lane < a.tokens && a.targets[min(lane, max(a.tokens - 1, 0))] >= 0);
     const int t = threadIdx.x % (32 * KS), r0 = 8 * (threadIdx.x / (32 * KS));   // a token and 8 entries a thread
     if (r0 < FEW_ROWS) {
         FewToken tok;
-        Run<uint16_t> x;
+        Run<T> x;
         float f = 0.0f;
         if (live >> t & 1u) {
             x.load(G(e + t * a.vp), v0 + r0);
@@ -1139,36 +1174,37 @@ template <int KS> __global__ __launch_bounds__(256, 2) void few_head_kernel(FewG
         }
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
-            uint16_t p[2];
-            hi_lo(tok.dz(e_of(x.w[r >> 1] >> (16 * (r & 1))), f, v0 + r0 + r, a.vocab), p);
+            uint16_t p[DP];
+            dz_parts(tok.dz(e_of(x, r), f, v0 + r0 + r, a.vocab), p);
 #pragma unroll
-            for (int d = 0; d < 2; ++d) tile[d][r0 + r][t] = p[d];
+            for (int d = 0; d < DP; ++d) tile[d][r0 + r][t] = p[d];
         }
     }
     __syncthreads();
-    const uint16_t* hidden = static_cast<const uint16_t*>(a.hidden);
-    uint16_t* out = static_cast<uint16_t*>(a.grad_head);
+    const T* hidden = static_cast<const T*>(a.hidden);
+    T* out = static_cast<T*>(a.grad_head);
     for (int strip = blockIdx.y * 4 + wave; strip < a.strips; strip += 4 * gridDim.y) {
         const int col = FEW_STRIP * strip + few_column(lane);
         f32x4m_t acc[8][VB] = {};
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-            Run<uint16_t> rows[8];
+            Run<T> rows[8];
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
                 const int t = 32 * s + 8 * q + r;
                 if (live >> t & 1u) few_row(rows[r], hidden + t * a.ld_hidden, col, a.cols);   // whatever others hold counts for nothing
             }
-            u32x4 b[VB][2];
+            u32x4 b[VB][DP];
 #pragma unroll
             for (int n = 0; n < VB; ++n)
 #pragma unroll
-                for (int d = 0; d < 2; ++d) b[n][d] = *reinterpret_cast<const u32x4*>(&tile[d][16 * n + (lane & 15)][32 * s + 8 * q]);
+                for (int d = 0; d < DP; ++d) b[n][d] = *reinterpret_cast<const u32x4*>(&tile[d][16 * n + (lane & 15)][32 * s + 8 * q]);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const u32x4 w = few_fragment(rows, j);
+                u32x4 w[PARTS];
+                few_fragment(rows, j, hs, w);
 #pragma unroll
-                for (int n = 0; n < VB; ++n) few_mfma(acc[j][n], w, b[n]);
+                for (int n = 0; n < VB; ++n) few_mfma<PARTS>(acc[j][n], w, b[n]);
             }
         }
 #pragma unroll
@@ -1178,10 +1214,22 @@ template <int KS> __global__ __launch_bounds__(256, 2) void few_head_kernel(FewG
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int c = FEW_STRIP * strip + 8 * (4 * r + q);
-                u32x4 w;
+                T* p = out + static_cast<size_t>(v) * a.ld_grad_head + c;
+                if constexpr (sizeof(T) == 2) {
+                    u32x4 w;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(acc[2 * j][n][r], acc[2 * j + 1][n][r]);
-                st_piece(out + static_cast<size_t>(v) * a.ld_grad_head + c, w, a.cols - c);
+                    for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(acc[2 * j][n][r], acc[2 * j + 1][n][r]);
+                    st_piece(p, w, a.cols - c);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        u32x4 w;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            w[j] = __float_as_uint(__builtin_amdgcn_ldexpf(acc[4 * h + j][n][r], -exponent_of(hs)));
+                        st_piece(p + 4 * h, w, a.cols - c - 4 * h);
+                    }
+                }
             }
         }
     }
@@ -1298,7 +1346,7 @@ struct Shape {
     bool direct_hidden, direct_head;   // operands that the products can read where they are: bf16 in whole 16-byte chunks
     Shape(int64_t t, int64_t d, int64_t v, int dtype, const void* hidden, int64_t ld_hidden, const void* head, int64_t ld_head)
         : tokens(t), cols(d), vocab(v), parts(dtype == MUON_BF16 ? 1 : 2), tp(up(std::max<int64_t>(t, 1), PAD)), vp(up(v, PAD)),
-          dp(up(d, pt::KS)), edge(edge_for(tp / PAD * (vp / PAD))), few(t <= FEW_TOKENS && parts == 1),
+          dp(up(d, pt::KS)), edge(edge_for(tp / PAD * (vp / PAD))), few(t <= FEW_TOKENS),
           few_tiles(static_cast<int>(ceil_div(v, FEW_ROWS))) {
         const bool ok = dtype == MUON_BF16 && d % 8 == 0;
         direct_hidden = ok && reinterpret_cast<uintptr_t>(hidden) % 16 == 0 && ld_hidden % 8 == 0;
@@ -1346,7 +1394,7 @@ struct ForwardPlan {
         m = b.take(a.saved ? 0 : stats * sizeof(float));
         s = b.take(stats * sizeof(float));
         zt = b.take(sizeof(float) * sh.tp);
-        absmax = b.take(few || sh.parts == 1 ? 0 : sizeof(uint32_t) * (ABS_HEAD + ABS_HIDDEN));
+        absmax = b.take(sh.parts == 1 ? 0 : sizeof(uint32_t) * (ABS_HEAD + ABS_HIDDEN));
         scales = b.take(few || sh.parts == 1 ? 0 : 2 * sizeof(float));
         bytes = b.at;
     }
@@ -1358,7 +1406,7 @@ struct FewPlan {
     Shape sh;
     int strips, splits;
     muon_token_logp_args forward;
-    size_t slab, logp, lse, saved, workspace, bytes;
+    size_t slab, absmax, logp, lse, saved, workspace, bytes;
     explicit FewPlan(const muon_token_logp_backward_args& a)
         : sh(a.tokens, a.cols, a.vocab, a.dtype, a.hidden, a.ld_hidden, a.head, a.ld_head), forward{} {
         // (6 tokens x 3176 x 52257: 302 us for both passes, 322 with two workgroups a CU, 394 with one; 2 x 2048 x 32000: 90, 88, 91)
@@ -1366,6 +1414,7 @@ struct FewPlan {
         splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((blocks() == 1 ? 3 : 2) * CUS / strips, sh.few_tiles / 8)));
         Bump b;
         slab = b.take(a.grad_hidden ? sizeof(float) * FEW_STRIP * static_cast<size_t>(strips) * splits * 16 * blocks() : 0);
+        absmax = b.take(sh.parts == 1 ? 0 : sizeof(uint32_t) * (ABS_HEAD + ABS_HIDDEN));
         if (!a.saved) {
             forward.hidden = a.hidden;
             forward.head = a.head;
@@ -1437,7 +1486,7 @@ struct BackwardPlan {
     }
 };
 
-bool few_backward(const muon_token_logp_backward_args& a) { return a.tokens <= FEW_TOKENS && a.dtype == MUON_BF16; }
+bool few_backward(const muon_token_logp_backward_args& a) { return a.tokens <= FEW_TOKENS; }
 Shape shape_of(const muon_token_logp_args& a) { return Shape(a.tokens, a.cols, a.vocab, a.dtype, a.hidden, a.ld_hidden, a.head, a.ld_head); }
 
 hipError_t launch_live(const int64_t* targets, int64_t tokens, int32_t* idx, int32_t* count, float* logp, float* lse,
@@ -1483,6 +1532,14 @@ hipError_t launch_absmax(const void* hidden, int64_t ld_hidden, const void* head
     return hipGetLastError();
 }
 
+// That of hidden alone, every row of it (few tokens).
+hipError_t launch_hidden_absmax(const void* hidden, int64_t ld_hidden, const Shape& sh, uint32_t* part, hipStream_t s) {
+    const AbsMaxArgs m{nullptr, static_cast<const float*>(hidden), 0, static_cast<size_t>(ld_hidden), 0, sh.cols,
+                       {nullptr, nullptr, 0, static_cast<int32_t>(sh.tokens)}, part};
+    hipLaunchKernelGGL(absmax_kernel, dim3(ABS_HIDDEN), dim3(256), 0, s, m);
+    return hipGetLastError();
+}
+
 // The logits' operands: packed copies where the products cannot read the caller's rows.  absmax: two parts.
 hipError_t logits_operands(const Shape& sh, const void* hidden, int64_t ld_hidden, const void* head, int64_t ld_head,
                            int dtype, char* hidden_copy, char* head_copy, bool pack_head, const uint32_t* absmax, float* scales,
@@ -1522,7 +1579,10 @@ template <typename T, int PARTS> hipError_t launch_few(const muon_token_logp_arg
     FewArgs f{a.head, a.hidden, static_cast<size_t>(a.ld_head), static_cast<size_t>(a.ld_hidden), a.targets,
                  static_cast<int>(a.tokens), static_cast<int>(a.cols), static_cast<int>(a.vocab), sh.few_tiles, a.scale * LOG2E,
                  keep ? kept(sv.m) : reinterpret_cast<float*>(ws + pl.m), reinterpret_cast<float*>(ws + pl.s),
-                 reinterpret_cast<float*>(ws + pl.zt), reinterpret_cast<uint16_t*>(kept(sv.e)), static_cast<size_t>(sh.vp)};
+                 reinterpret_cast<float*>(ws + pl.zt), kept(sv.e), static_cast<size_t>(sh.vp),
+                 keep ? reinterpret_cast<uint32_t*>(ws + pl.absmax) : nullptr};
+    // for the gradients' sake; without them its launch (4 us of 51) costs more than values below 2^-109 are worth
+    if (PARTS == 3 && keep) TL_TRY(launch_hidden_absmax(a.hidden, a.ld_hidden, sh, reinterpret_cast<uint32_t*>(ws + pl.absmax), s));
     const dim3 grid(static_cast<unsigned>(f.tiles));
     if (f.tokens <= 16) hipLaunchKernelGGL((few_kernel<T, PARTS, 1>), grid, dim3(256), 0, s, f);
     else if (f.tokens <= 32) hipLaunchKernelGGL((few_kernel<T, PARTS, 2>), grid, dim3(256), 0, s, f);
@@ -1534,34 +1594,38 @@ template <typename T, int PARTS> hipError_t launch_few(const muon_token_logp_arg
     return hipGetLastError();
 }
 
-template <int NT> hipError_t launch_few_grads_nt(const FewGradArgs& g, const FewPlan& pl, hipStream_t s) {
+template <typename T, int PARTS, int NT>
+hipError_t launch_few_grads_nt(const FewGradArgs& g, const FewPlan& pl, hipStream_t s) {
     if (g.grad_hidden) {
-        hipLaunchKernelGGL(few_hidden_kernel<NT>, dim3(static_cast<unsigned>(pl.strips) * pl.splits), dim3(256), 0, s, g);
+        constexpr int AT_ONCE = PARTS == 3 && NT == 4 ? 2 : NT;
+        hipLaunchKernelGGL((few_hidden_kernel<T, PARTS, AT_ONCE>), dim3(static_cast<unsigned>(pl.strips) * pl.splits, NT / AT_ONCE),
+                           dim3(256), 0, s, g);
         TL_TRY(hipGetLastError());
-        hipLaunchKernelGGL(few_sum_kernel<NT>, dim3(static_cast<unsigned>(pl.strips) * (FEW_STRIP * 16 * NT / 256)), dim3(256), 0, s, g);
+        hipLaunchKernelGGL((few_sum_kernel<T, NT>), dim3(static_cast<unsigned>(pl.strips) * (FEW_STRIP * 16 * NT / 256)), dim3(256), 0, s, g);
         TL_TRY(hipGetLastError());
     }
     if (g.grad_head) {
         // enough workgroups over the columns to fill the chip
         const int by = std::max(1, std::min((4 * CUS + g.tiles - 1) / g.tiles, (pl.strips + 3) / 4));
-        hipLaunchKernelGGL(few_head_kernel<NT == 4 ? 2 : 1>, dim3(g.tiles, by), dim3(256), 0, s, g);
+        hipLaunchKernelGGL((few_head_kernel<T, PARTS, NT == 4 ? 2 : 1>), dim3(g.tiles, by), dim3(256), 0, s, g);
         TL_TRY(hipGetLastError());
     }
     return hipSuccess;
 }
-hipError_t launch_few_grads(const muon_token_logp_backward_args& a, const FewPlan& pl, const char* saved, float* slab, hipStream_t s) {
+template <typename T, int PARTS>
+hipError_t launch_few_grads(const muon_token_logp_backward_args& a, const FewPlan& pl, const char* saved, float* slab, uint32_t* absmax, hipStream_t s) {
     const SavedPlan sv(pl.sh);
     auto kept = [&](size_t o) { return reinterpret_cast<const float*>(saved + o); };
     const FewGradArgs g{a.head, a.hidden, static_cast<size_t>(a.ld_head), static_cast<size_t>(a.ld_hidden), a.targets,
                         static_cast<int>(a.tokens), static_cast<int>(a.cols), static_cast<int>(a.vocab), pl.sh.few_tiles,
-                        pl.strips, pl.splits, a.scale * LOG2E, a.scale, reinterpret_cast<const uint16_t*>(saved + sv.e), static_cast<size_t>(pl.sh.vp), kept(sv.m),
+                        pl.strips, pl.splits, a.scale * LOG2E, a.scale, saved + sv.e, static_cast<size_t>(pl.sh.vp), kept(sv.m),
                         kept(sv.logp), kept(sv.ref), kept(sv.shift), a.grad_logp, slab,
                         a.tokens > 0 ? a.grad_hidden : nullptr, a.grad_head, static_cast<size_t>(a.ld_grad_hidden),
-                        static_cast<size_t>(a.ld_grad_head)};
+                        static_cast<size_t>(a.ld_grad_head), absmax};
     switch (pl.blocks()) {
-        case 1: return launch_few_grads_nt<1>(g, pl, s);
-        case 2: return launch_few_grads_nt<2>(g, pl, s);
-        default: return launch_few_grads_nt<4>(g, pl, s);
+        case 1: return launch_few_grads_nt<T, PARTS, 1>(g, pl, s);
+        case 2: return launch_few_grads_nt<T, PARTS, 2>(g, pl, s);
+        default: return launch_few_grads_nt<T, PARTS, 4>(g, pl, s);
     }
 }
 
@@ -1630,7 +1694,11 @@ hipError_t launch_few_backward(const muon_token_logp_backward_args& a, char* ws,
         TL_TRY(launch_token_logp(pl.forward, ws + pl.workspace, s));
         saved = ws + pl.saved;
     }
-    return launch_few_grads(a, pl, saved, reinterpret_cast<float*>(ws + pl.slab), s);
+    float* slab = reinterpret_cast<float*>(ws + pl.slab);
+    uint32_t* absmax = reinterpret_cast<uint32_t*>(ws + pl.absmax);
+    if (a.dtype == MUON_BF16) return launch_few_grads<uint16_t, 1>(a, pl, saved, slab, absmax, s);
+    TL_TRY(launch_hidden_absmax(a.hidden, a.ld_hidden, pl.sh, absmax, s));
+    return launch_few_grads<float, 3>(a, pl, saved, slab, absmax, s);
 }
 }  // namespace
 
@@ -1643,15 +1711,11 @@ hipError_t launch_token_logp_backward(const muon_token_logp_backward_args& a, vo
     const char* saved = static_cast<const char*>(a.saved);
     const int32_t* idx = reinterpret_cast<const int32_t*>(saved ? saved + sv.idx : ws + pl.idx);
     const int32_t* count = reinterpret_cast<const int32_t*>(saved ? saved + sv.count : ws + pl.count);
-    if (!saved || a.tokens == 0) {   // without tokens there was no forward pass to keep the list
-        idx = reinterpret_cast<int32_t*>(ws + pl.idx);
-        count = reinterpret_cast<int32_t*>(ws + pl.count);
-        TL_TRY(launch_live(a.targets, a.tokens, const_cast<int32_t*>(idx), const_cast<int32_t*>(count), nullptr, nullptr, s));
-    }
+    if (!saved) TL_TRY(launch_live(a.targets, a.tokens, const_cast<int32_t*>(idx), const_cast<int32_t*>(count), nullptr, nullptr, s));
     // scales of hidden and head: as the forward pass left them, or found again; of dz: over all tokens, since chunks add up
     float* own = reinterpret_cast<float*>(ws + pl.scales);
     uint32_t* absmax = reinterpret_cast<uint32_t*>(ws + pl.absmax);
-    const float* scales = saved && a.tokens > 0 ? reinterpret_cast<const float*>(saved + sv.scales) : own;
+    const float* scales = saved ? reinterpret_cast<const float*>(saved + sv.scales) : own;
     float* dz_scale = own + 2;
     const Live everyone{idx, count, 0, static_cast<int32_t>(sh.tp)};
     if (sh.parts == 2 && !saved) TL_TRY(launch_absmax(a.hidden, a.ld_hidden, a.head, a.ld_head, sh, everyone, absmax, s));
