@@ -333,7 +333,9 @@ muon_status muon_token_logp(const muon_token_logp_args* args, void* workspace, s
 /* With c_i = scale * grad_logp_i and p_ij = exp(z_ij - lse_i):
  *   dz_ij = c_i ([j = target_i] - p_ij),  grad_hidden = dz head,  grad_head = dz^T hidden
  * grad_hidden or grad_head may be NULL (not wanted), not both.  `saved` is what
- * muon_token_logp kept for the same inputs, or NULL.  dz is rounded to the
+ * muon_token_logp kept for the same inputs, or NULL: then the logits are formed
+ * again, and lse with them (a rounded lse does not hold a certain token's
+ * 1 - p; what the argument holds is not used).  dz is rounded to the
  * operands' precision before the two products: bf16 (up to 64 tokens: two bf16
  * parts, 2^-16), or 22 bits for fp32 (up to 64 tokens: 24).
  *
@@ -346,7 +348,7 @@ typedef struct {
     const void*    hidden;
     const void*    head;
     const int64_t* targets;
-    const float*   lse;
+    const float*   lse;         /* tokens, as muon_token_logp wrote it for the same inputs */
     const float*   grad_logp;
     const void*    saved;
     void* grad_hidden;        /* tokens x cols or NULL, dtype */

@@ -35,10 +35,8 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
-typedef short i16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 typedef __attribute__((address_space(3))) char lds_byte_t;
-typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
 typedef __attribute__((address_space(3))) u32x2_t lds_u32x2_t;
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4_t;
 
@@ -330,8 +328,8 @@ template <int EDGE> struct Tile {
     static __device__ __forceinline__ int stack_place() { return share_row(wave_id()) / (32 * SM); }
 
     // Staging as 16-bit values: column c at 2 EDGE c bytes, its rows in units of 4 (8 bytes), unit u at
-    // position u ^ csw(c): a lane's 4 rows are one write, free of bank conflicts, a column is read
-    // back in order (16 bytes = 8 rows) and a row through transpose reads.
+    // position u ^ csw(c): a lane's 4 rows are one write, free of bank conflicts, and a column is read
+    // back in order (16 bytes = 8 rows).
     static __device__ __forceinline__ int csw(int c) { return (c & 31) ^ (((c >> 5) & 1) << 2); }
     struct Stage {
         int wbase[SN];
@@ -375,18 +373,6 @@ template <int EDGE> struct Tile {
         const u32x4 v = *(const lds_u32x4_t*)(L + (c * (2 * EDGE) + 16 * (q ^ (s >> 1))));
         return (s & 1) ? u32x4{v.z, v.w, v.x, v.y} : v;
     }
-    // Rows 4 u + (lane & 3), columns col0 + 8 ((lane & 15) >> 2) + 32 (lane >> 4) + (0..7) of the 128
-    // columns from col0: 16 bytes of one row a lane.
-    static __device__ __forceinline__ u32x4 stage_row8(const lds_byte_t* L, int u, int col0) {
-        const int lane = threadIdx.x & 63, grp = lane >> 4, k = lane & 15;
-        const int c = col0 + 32 * grp + 8 * (k & 3) + (k >> 2);
-        const i16x4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(L + (c * (2 * EDGE) + 8 * (u ^ csw(c)))));
-        const i16x4_t b =
-            __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(L + ((c + 4) * (2 * EDGE) + 8 * (u ^ csw(c + 4)))));
-        const u32x2_t a2 = __builtin_bit_cast(u32x2_t, a), b2 = __builtin_bit_cast(u32x2_t, b);
-        return u32x4{a2.x, a2.y, b2.x, b2.y};
-    }
-
     // Staging as fp32, 128 columns at a time (pass = c / 128): column c at 4 EDGE (c % 128) bytes, its rows in
     // units of 4 (16 bytes), unit u at position u ^ (c & 31).
     static constexpr int F32_PASSES = EDGE / 128;

@@ -14,8 +14,10 @@
 //    combine_kernel joins them.  With `saved` the tile's exp(z - tile maximum) goes out too: in fp16 in
 //    bf16 calls (values of at most 1: 11 bits where bf16 keeps 8; what falls below 2^-24 of its tile's maximum is 0), else
 //    in fp32.
-//  - Backward: dz comes from `saved` by an elementwise pass, or from the logits' tile formed again.
-//    It is written both token-major and vocabulary-major, and head and hidden are transposed
+//  - Backward: dz comes from `saved` by an elementwise pass; without `saved` the logits' product comes first again, for a
+//    chunk of tokens at a time.  The target's own dz is -c expm1(logp): 1 - exp(z - lse) from a rounded lse would be off by
+//    1e-6, all there is of a certain token's gradient.
+//    dz is written both token-major and vocabulary-major, and head and hidden are transposed
 //    once, so that both gradients are k-contiguous products (C rows = columns of the gradient,
 //    C columns = its rows).  Few tiles: the sum over k is split over workgroups that leave fp32
 //    tiles, added in order by slab_sum_kernel.
@@ -46,7 +48,7 @@ constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 // 208 with the tiles' kernels; 40 tokens in fp32: 372, 574; 12 tokens x 2048 x 65536 in fp32: 402, 966).
 constexpr int64_t FEW_TOKENS = 64;
 constexpr int FEW_ROWS = 32;                // vocabulary entries per workgroup of few_kernel
-constexpr int64_t DZ_BYTES = int64_t{4} << 30;   // both layouts of dz, at most: more tokens go in chunks
+constexpr int64_t DZ_BYTES = int64_t{4} << 30;   // both layouts of dz (without `saved`: and e), at most: more tokens go in chunks
 constexpr int CUS = 256;
 // 256 x 256 tiles below which the smaller tile serves a product: some 3/4 of the CUs.  2000 x 1024 x 8192, both passes: 138 us, at a
 // bound of 96 154; 8192 x 2048 x 32000: 2480, at 512 2835; 777 x 1000 x 32003: 270, at 512 303.
@@ -342,7 +344,7 @@ template <typename T, int PARTS> __global__ __launch_bounds__(256) void prepare_
 // Logits, tile by tile
 // ---------------------------------------------------------------------------
 
-enum LogitsMode { LG_STATS = 0, LG_SAVE = 1, LG_DZ = 2 };
+enum LogitsMode { LG_STATS = 0, LG_SAVE = 1 };
 
 struct LogitsArgs {
     const char* a;          // head rows (bytes pitch a_ld, parts a_part apart)
@@ -355,15 +357,10 @@ struct LogitsArgs {
     int vocab, steps, tail, ta, tb;   // tail: 16-byte chunks of the last k-step
     float scale2;           // scale log2(e)
     const float* scales;    // two parts: of hidden and head
-    float *m, *s, *zt;      // M and S: tile x list entry (pitch rows_pitch); target's acc by list entry
+    float *m, *s;           // M and S: tile x list entry from live.first on (pitch rows_pitch)
+    float* zt;              // target's acc by list entry
     size_t rows_pitch;
-    void* e;                // LG_SAVE: 2^(k' acc - M), list entry x vocabulary (pitch vp), fp16 (bf16 operands) or fp32
-    // LG_DZ
-    const float *lse, *grad_logp;
-    float scale;
-    uint16_t *dz, *dzt;     // dz and its transpose: parts apart, pitches vp and rows_pitch; rows relative to live.first
-    size_t dz_part, dzt_part;
-    const float* dz_scale;  // two parts
+    void* e;                // LG_SAVE: 2^(k' acc - M), list entry from live.first on x vocabulary (pitch vp), fp16 (bf16 operands) or fp32
     size_t vp;
 };
 
@@ -378,18 +375,6 @@ __device__ __forceinline__ void store_cols(const pt::lds_byte_t* L, uint16_t* ds
         __builtin_nontemporal_store(TL::stage_col8(L, c, q), G(reinterpret_cast<u32x4*>(dst + (r0 + c) * ld + v0 + 8 * q)));
     }
 }
-// The staged tile's rows as rows of `dst`.
-template <typename TL> __device__ __forceinline__ void store_rows(const pt::lds_byte_t* L, uint16_t* dst, size_t ld, size_t v0, size_t r0) {
-    const int lane = threadIdx.x & 63, wave = pt::wave_id();
-    constexpr int H = TL::SIZE / 128, U = TL::SIZE / 4 / TL::NWAVES;   // 128-column halves, row quads a wave
-#pragma unroll 2
-    for (int k = 0; k < U * H; ++k) {
-        const int u = U * wave + k / H, col0 = 128 * (k % H);
-        const size_t row = v0 + 4 * u + (lane & 3), col = r0 + col0 + 32 * (lane >> 4) + 8 * ((lane & 15) >> 2);
-        __builtin_nontemporal_store(TL::stage_row8(L, u, col0), G(reinterpret_cast<u32x4*>(dst + row * ld + col)));
-    }
-}
-
 // 6144 scored tokens x 2048 x 32000 bf16, keeping e: 752 us, 1071 TFLOP/s (a library product of 8192^3 reaches 1534); the
 // statistics, exponentials and 0.4 GB of e take the difference to the gradients' products.  512 x 1024 x 8192 fp32 (128-tile):
 // 41 us, 3 x 209 TFLOP/s: two rounds of workgroups, bound by LDS reads.
@@ -429,139 +414,88 @@ __global__ __launch_bounds__(pt::Tile<EDGE>::THREADS, 2) void logits_kernel(Logi
     }
     lds_barrier();                                    // every wave is done with the operand slabs
 
-    if constexpr (MODE != LG_DZ) {
-        float* smax = reinterpret_cast<float*>(lds);          // [STACKED][EDGE]
-        float* ssum = smax + TL::STACKED * EDGE;              // [STACKED][EDGE]
-        int col[TL::SN], y[TL::SN];
-        float mx[TL::SN];
+    float* smax = reinterpret_cast<float*>(lds);          // [STACKED][EDGE]
+    float* ssum = smax + TL::STACKED * EDGE;              // [STACKED][EDGE]
+    int col[TL::SN], y[TL::SN];
+    float mx[TL::SN];
 #pragma unroll
-        for (int j = 0; j < TL::SN; ++j) {
-            col[j] = TL::column(j);
-            const int r = min(r0 + col[j], n - 1);
-            const int64_t t = a.targets[a.live.idx[a.live.first + r]];
-            y[j] = t < a.vocab ? static_cast<int>(t) - vl : -1;
-            mx[j] = -INFINITY;
-            if (edge) {
-#pragma unroll
-                for (int i = 0; i < TL::SM; ++i)
-#pragma unroll
-                    for (int q = 0; q < 16; ++q)
-                        if (vl + 32 * i + 8 * (q >> 2) + (q & 3) >= a.vocab) acc[i][j][q] = -INFINITY;
-            }
+    for (int j = 0; j < TL::SN; ++j) {
+        col[j] = TL::column(j);
+        const int r = min(r0 + col[j], n - 1);
+        const int64_t t = a.targets[a.live.idx[a.live.first + r]];
+        y[j] = t < a.vocab ? static_cast<int>(t) - vl : -1;
+        mx[j] = -INFINITY;
+        if (edge) {
 #pragma unroll
             for (int i = 0; i < TL::SM; ++i)
 #pragma unroll
-                for (int q = 0; q < 16; ++q) mx[j] = fmaxf(mx[j], acc[i][j][q]);
-            mx[j] = fmaxf(mx[j], __shfl_xor(mx[j], 32, 64));
-            if (h == 0) smax[EDGE * place + col[j]] = mx[j];
+                for (int q = 0; q < 16; ++q)
+                    if (vl + 32 * i + 8 * (q >> 2) + (q & 3) >= a.vocab) acc[i][j][q] = -INFINITY;
         }
-        lds_barrier();
 #pragma unroll
-        for (int j = 0; j < TL::SN; ++j) {
+        for (int i = 0; i < TL::SM; ++i)
 #pragma unroll
-            for (int p = 0; p < TL::STACKED; ++p) mx[j] = fmaxf(mx[j], smax[EDGE * p + col[j]]);
-            mx[j] *= k;
-            const float base = shown(mx[j]);
-            float sum = 0.0f, zt = 0.0f;
-            bool mine = false;
+            for (int q = 0; q < 16; ++q) mx[j] = fmaxf(mx[j], acc[i][j][q]);
+        mx[j] = fmaxf(mx[j], __shfl_xor(mx[j], 32, 64));
+        if (h == 0) smax[EDGE * place + col[j]] = mx[j];
+    }
+    lds_barrier();
 #pragma unroll
-            for (int i = 0; i < TL::SM; ++i)
+    for (int j = 0; j < TL::SN; ++j) {
 #pragma unroll
-                for (int q = 0; q < 16; ++q) {
-                    const int dv = 32 * i + 8 * (q >> 2) + (q & 3);
-                    const float z = acc[i][j][q], ex = __builtin_amdgcn_exp2f(fmaf(z, k, -base));
-                    const bool target = dv == y[j];
-                    sum += target ? 0.0f : ex;
-                    if (target) { zt = z; mine = true; }
-                    if (MODE == LG_SAVE) acc[i][j][q] = ex;
-                }
-            sum += __shfl_xor(sum, 32, 64);
-            if (h == 0) ssum[EDGE * place + col[j]] = sum;
-            if (mine && r0 + col[j] < n) a.zt[a.live.first + r0 + col[j]] = zt;
-        }
-        lds_barrier();
+        for (int p = 0; p < TL::STACKED; ++p) mx[j] = fmaxf(mx[j], smax[EDGE * p + col[j]]);
+        mx[j] *= k;
+        const float base = shown(mx[j]);
+        float sum = 0.0f, zt = 0.0f;
+        bool mine = false;
 #pragma unroll
-        for (int j = 0; j < TL::SN; ++j)
-            if (place == 0 && h == 0) {
-                const size_t o = ia * a.rows_pitch + r0 + col[j];
-                float sum = ssum[col[j]];
+        for (int i = 0; i < TL::SM; ++i)
 #pragma unroll
-                for (int p = 1; p < TL::STACKED; ++p) sum += ssum[EDGE * p + col[j]];
-                a.m[o] = mx[j];
-                a.s[o] = sum;
+            for (int q = 0; q < 16; ++q) {
+                const int dv = 32 * i + 8 * (q >> 2) + (q & 3);
+                const float z = acc[i][j][q], ex = __builtin_amdgcn_exp2f(fmaf(z, k, -base));
+                const bool target = dv == y[j];
+                sum += target ? 0.0f : ex;
+                if (target) { zt = z; mine = true; }
+                if (MODE == LG_SAVE) acc[i][j][q] = ex;
             }
-        if constexpr (MODE == LG_SAVE) {
-            if constexpr (PARTS == 1) {
-                lds_barrier();
-                const typename TL::Stage st;
-                st.put_all_f16(L, acc);
-                lds_barrier();
-                store_cols<TL>(L, static_cast<uint16_t*>(a.e), a.vp, r0, v0, n - r0);
-            } else {
-                float* e = static_cast<float*>(a.e);
-                for (int pass = 0; pass < TL::F32_PASSES; ++pass) {
-                    lds_barrier();
-                    TL::put_f32(L, acc, pass);
-                    lds_barrier();
-                    constexpr int Q = EDGE / 4, PER = TL::THREADS / Q;
-#pragma unroll 4
-                    for (int k = 0; k < 128 / PER; ++k) {
-                        const int c = 128 * pass + PER * k + static_cast<int>(threadIdx.x) / Q, q = threadIdx.x % Q;
-                        if (r0 + c >= n) break;
-                        __builtin_nontemporal_store(TL::stage_f32(L, c, q),
-                                                    G(reinterpret_cast<u32x4*>(e + (static_cast<size_t>(r0) + c) * a.vp + v0 + 4 * q)));
-                    }
-                }
-            }
+        sum += __shfl_xor(sum, 32, 64);
+        if (h == 0) ssum[EDGE * place + col[j]] = sum;
+        if (mine && r0 + col[j] < n) a.zt[a.live.first + r0 + col[j]] = zt;
+    }
+    lds_barrier();
+#pragma unroll
+    for (int j = 0; j < TL::SN; ++j)
+        if (place == 0 && h == 0) {
+            const size_t o = ia * a.rows_pitch + r0 + col[j];
+            float sum = ssum[col[j]];
+#pragma unroll
+            for (int p = 1; p < TL::STACKED; ++p) sum += ssum[EDGE * p + col[j]];
+            a.m[o] = mx[j];
+            a.s[o] = sum;
         }
-    } else {
-        const typename TL::Stage st;
-#pragma unroll
-        for (int j = 0; j < TL::SN; ++j) {
-            const int r = r0 + TL::column(j);
-            const int tok = a.live.idx[a.live.first + min(r, n - 1)];
-            const int64_t t = a.targets[tok];
-            const int y = t < a.vocab ? static_cast<int>(t) - vl : -1;
-            const float c = r < n ? a.scale * a.grad_logp[tok] : 0.0f, l2 = a.lse[tok] * LOG2E;
-#pragma unroll
-            for (int i = 0; i < TL::SM; ++i)
-#pragma unroll
-                for (int q = 0; q < 16; ++q) {
-                    const int dv = 32 * i + 8 * (q >> 2) + (q & 3);
-                    const float p = __builtin_amdgcn_exp2f(fmaf(acc[i][j][q], k, -l2));
-                    float d = c * ((dv == y ? 1.0f : 0.0f) - p);
-                    if (c == 0.0f || (edge && vl + dv >= a.vocab)) d = 0.0f;
-                    acc[i][j][q] = d;
-                }
-        }
-        const float ds = PARTS == 1 ? 1.0f : *a.dz_scale;
-#pragma unroll
-        for (int p = 0; p < PARTS; ++p) {
-            if (p > 0) lds_barrier();
-            if constexpr (PARTS == 1) {
-                st.put_all(L, acc);
-            } else {   // first hi, leaving the rest in the accumulators, then lo (split2 in two steps)
-#pragma unroll
-                for (int i = 0; i < TL::SM; ++i)
-#pragma unroll
-                    for (int j = 0; j < TL::SN; ++j)
-#pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float x = acc[i][j][4 * g + e] * (p == 0 ? ds : 1.0f / pt::LO_STEP);
-                                const _Float16 hi = static_cast<_Float16>(x);
-                                const float f = static_cast<float>(hi);
-                                w[e] = __builtin_bit_cast(uint16_t, hi);
-                                if (p == 0) acc[i][j][4 * g + e] = fabsf(f) < INFINITY ? x - f : 0.0f;
-                            }
-                            st.put(L, i, j, g, w[0] | w[1] << 16, w[2] | w[3] << 16);
-                        }
-            }
+    if constexpr (MODE == LG_SAVE) {
+        if constexpr (PARTS == 1) {
             lds_barrier();
-            if (a.dz) store_cols<TL>(L, a.dz + p * a.dz_part, a.vp, r0, v0, n - r0);
-            if (a.dzt) store_rows<TL>(L, a.dzt + p * a.dzt_part, a.rows_pitch, v0, r0);
+            const typename TL::Stage st;
+            st.put_all_f16(L, acc);
+            lds_barrier();
+            store_cols<TL>(L, static_cast<uint16_t*>(a.e), a.vp, r0, v0, n - r0);
+        } else {
+            float* e = static_cast<float*>(a.e);
+            for (int pass = 0; pass < TL::F32_PASSES; ++pass) {
+                lds_barrier();
+                TL::put_f32(L, acc, pass);
+                lds_barrier();
+                constexpr int Q = EDGE / 4, PER = TL::THREADS / Q;
+#pragma unroll 4
+                for (int k = 0; k < 128 / PER; ++k) {
+                    const int c = 128 * pass + PER * k + static_cast<int>(threadIdx.x) / Q, q = threadIdx.x % Q;
+                    if (r0 + c >= n) break;
+                    __builtin_nontemporal_store(TL::stage_f32(L, c, q),
+                                                G(reinterpret_cast<u32x4*>(e + (static_cast<size_t>(r0) + c) * a.vp + v0 + 4 * q)));
+                }
+            }
         }
     }
 }
@@ -571,15 +505,16 @@ __global__ __launch_bounds__(pt::Tile<EDGE>::THREADS, 2) void logits_kernel(Logi
 // ---------------------------------------------------------------------------
 
 struct DzArgs {
-    const void* e;          // list entry x vocabulary, pitch vp
-    const float* m;         // tile x list entry
+    const void* e;          // list entry from `kept` on x vocabulary, pitch vp
+    const float* m;         // tile x list entry from `kept` on
+    int kept;
     const float *logp, *ref, *shift;   // list entry: logp, and p = e 2^(M - k' ref + shift)
     float scale2;
     size_t m_pitch;
     int m_edge;             // vocabulary entries per tile
     Live live;
     const int64_t* targets;
-    const float *lse, *grad_logp;
+    const float* grad_logp;
     float scale;
     int vocab;
     size_t vp, rows_pitch;
@@ -610,12 +545,12 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
             c = a.scale * a.grad_logp[tok];
             y = t < a.vocab ? static_cast<int>(t) - v0 - 8 * vb : -1;
             const int o = a.live.first + r;
-            f = c * __builtin_amdgcn_exp2f(fmaf(-a.ref[o], k, a.m[(v0 / a.m_edge) * a.m_pitch + o]) + a.shift[o]);
+            f = c * __builtin_amdgcn_exp2f(fmaf(-a.ref[o], k, a.m[(v0 / a.m_edge) * a.m_pitch + o - a.kept]) + a.shift[o]);
             // 1 - p of the target from logp alone: e is rounded, which 1 - p would magnify as p goes to 1
             dy = -c * expm1f(a.logp[o]);
         }
         float x[8];
-        const size_t o = (static_cast<size_t>(a.live.first) + min(r, n - 1)) * a.vp + v0 + 8 * vb;
+        const size_t o = static_cast<size_t>(a.live.first - a.kept + min(r, n - 1)) * a.vp + v0 + 8 * vb;
         if constexpr (sizeof(E) == 2) {
             const pt::f16x8_t w = __builtin_bit_cast(pt::f16x8_t, G(reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.e) + o))[0]);
 #pragma unroll
@@ -1245,8 +1180,8 @@ struct CombineArgs {
     int tiles;
     const int64_t* targets;
     int64_t vocab;
-    float *logp, *lse;
-    const int32_t *idx, *count;   // NULL: every token, in order (then unscored ones are zeroed here)
+    float *logp, *lse;            // or NULL: what is kept is enough
+    Live live;                    // no list: every token, in order (then unscored ones are zeroed here)
     int64_t tokens;
     float scale2;
     float *kept_logp, *kept_ref, *kept_shift;   // by list entry, for the backward pass (DzArgs), or NULL
@@ -1262,7 +1197,7 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
     __shared__ float sm[NP][TOK], ss[NP][TOK];
     const int tk = threadIdx.x % TOK, part = threadIdx.x / TOK;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * TOK + tk;
-    const int64_t n = a.idx ? *a.count : a.tokens;
+    const int64_t n = a.live.idx ? a.live.rows() : a.tokens;
     const float k = rate_of(a.scale2);
     float m = -INFINITY, s = 0.0f;
     if (row < n)
@@ -1286,7 +1221,7 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
         }
     }
     if (part != 0 || row >= n) return;
-    const int64_t tok = a.idx ? a.idx[row] : row, y = a.targets[tok];
+    const int64_t entry = a.live.first + row, tok = a.live.idx ? a.live.idx[entry] : row, y = a.targets[tok];
     // s is the sum without the target, if there is one
     float logp, lse = (m + log2f(s)) * LN2, ref = 0.0f, shift = -(m + log2f(s));
     if (y < 0) {
@@ -1294,7 +1229,7 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
     } else if (y >= a.vocab) {
         logp = NAN;
     } else {
-        const float zt = a.zt[row], d = fmaf(-zt, k, m);
+        const float zt = a.zt[entry], d = fmaf(-zt, k, m);
         if (d < 80.0f) {
             logp = 0.0f - log1pf(s * __builtin_amdgcn_exp2f(d));
             lse = zt * k * LN2 - logp;
@@ -1304,12 +1239,14 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
             logp = -(d + log2f(s)) * LN2;     // here 1 is nothing beside the sum
         }
     }
-    a.logp[tok] = logp;
-    a.lse[tok] = lse;
+    if (a.logp) {
+        a.logp[tok] = logp;
+        a.lse[tok] = lse;
+    }
     if (a.kept_logp) {
-        a.kept_logp[row] = logp;
-        a.kept_ref[row] = ref;
-        a.kept_shift[row] = shift;
+        a.kept_logp[entry] = logp;
+        a.kept_ref[entry] = ref;
+        a.kept_shift[entry] = shift;
     }
 }
 
@@ -1459,13 +1396,14 @@ struct BackwardPlan {
     int chunks;
     GradPlan gh, gw;
     size_t idx, count, hidden, head, head_t, hidden_t, dz, dzt, slab, slab_w, absmax, scales, bytes;
-    static int64_t chunk_of(const Shape& sh) {
-        const int64_t both = sizeof(uint16_t) * sh.parts * 2 * sh.vp;
-        return std::min(sh.tp, std::max<int64_t>(PAD, DZ_BYTES / both / PAD * PAD));
+    size_t e, m, s, zt, logp, ref, shift;   // without `saved`: e, M and S of a chunk, the rest by list entry
+    static int64_t chunk_of(const Shape& sh, bool saved) {
+        const int64_t row = sizeof(uint16_t) * sh.parts * (saved ? 2 : 3) * sh.vp;   // e takes as much as dz
+        return std::min(sh.tp, std::max<int64_t>(PAD, DZ_BYTES / row / PAD * PAD));
     }
     explicit BackwardPlan(const muon_token_logp_backward_args& a)
         : sh(a.tokens, a.cols, a.vocab, a.dtype, a.hidden, a.ld_hidden, a.head, a.ld_head),
-          chunk(chunk_of(sh)), chunks(static_cast<int>(ceil_div(sh.tp, chunk))), gh(sh.cols, chunk, sh.vp, false),
+          chunk(chunk_of(sh, a.saved != nullptr)), chunks(static_cast<int>(ceil_div(sh.tp, chunk))), gh(sh.cols, chunk, sh.vp, false),
           gw(sh.cols, sh.vocab, chunk, chunks > 1) {
         Bump b;
         const size_t el = sizeof(uint16_t) * sh.parts;
@@ -1482,6 +1420,14 @@ struct BackwardPlan {
         slab_w = b.take(a.grad_head ? gw.slab_bytes() : 0);
         absmax = b.take(sh.parts == 1 ? 0 : sizeof(uint32_t) * (ABS_HEAD + ABS_HIDDEN));
         scales = b.take(sh.parts == 1 ? 0 : 3 * sizeof(float));
+        const size_t by_chunk = a.saved ? 0 : static_cast<size_t>(chunk), by_entry = a.saved ? 0 : sizeof(float) * sh.tp;
+        e = b.take(el * by_chunk * sh.vp);
+        m = b.take(sizeof(float) * by_chunk * sh.ta());
+        s = b.take(sizeof(float) * by_chunk * sh.ta());
+        zt = b.take(by_entry);
+        logp = b.take(by_entry);
+        ref = b.take(by_entry);
+        shift = b.take(by_entry);
         bytes = b.at;
     }
 };
@@ -1589,7 +1535,7 @@ template <typename T, int PARTS> hipError_t launch_few(const muon_token_logp_arg
     else hipLaunchKernelGGL((few_kernel<T, PARTS, 4>), grid, dim3(256), 0, s, f);
     TL_TRY(hipGetLastError());
     const CombineArgs c{f.m, f.s, f.zt, 1, static_cast<size_t>(sh.few_tiles), sh.few_tiles, a.targets, a.vocab, a.logp, a.lse,
-                        nullptr, nullptr, a.tokens, f.scale2, kept(sv.logp), kept(sv.ref), kept(sv.shift)};
+                        {}, a.tokens, f.scale2, kept(sv.logp), kept(sv.ref), kept(sv.shift)};
     hipLaunchKernelGGL(combine_kernel<1>, dim3(static_cast<unsigned>(a.tokens)), dim3(256), 0, s, c);
     return hipGetLastError();
 }
@@ -1677,7 +1623,7 @@ hipError_t launch_token_logp(const muon_token_logp_args& a, void* workspace, hip
     l.rows_pitch = sh.tp;
     l.vp = sh.vp;
     TL_TRY(a.saved ? launch_logits<LG_SAVE>(l, sh.edge, sh.parts, s) : launch_logits<LG_STATS>(l, sh.edge, sh.parts, s));
-    const CombineArgs c{m, sums, zt, static_cast<size_t>(sh.tp), 1, sh.ta(), a.targets, a.vocab, a.logp, a.lse, idx, count, a.tokens,
+    const CombineArgs c{m, sums, zt, static_cast<size_t>(sh.tp), 1, sh.ta(), a.targets, a.vocab, a.logp, a.lse, l.live, a.tokens,
                         scale2, kept_logp, kept_ref, kept_shift};
     hipLaunchKernelGGL(combine_kernel<32>, dim3(static_cast<unsigned>(sh.tp / 32)), dim3(256), 0, s, c);
     return hipGetLastError();
@@ -1720,14 +1666,30 @@ hipError_t launch_token_logp_backward(const muon_token_logp_backward_args& a, vo
     const Live everyone{idx, count, 0, static_cast<int32_t>(sh.tp)};
     if (sh.parts == 2 && !saved) TL_TRY(launch_absmax(a.hidden, a.ld_hidden, a.head, a.ld_head, sh, everyone, absmax, s));
     const size_t vp = sh.vp, dz_part = static_cast<size_t>(pl.chunk) * vp;
+    auto at = [&](size_t o) { return reinterpret_cast<float*>(ws + o); };
     uint16_t* dz = a.grad_hidden ? reinterpret_cast<uint16_t*>(ws + pl.dz) : nullptr;
     uint16_t* dzt = a.grad_head ? reinterpret_cast<uint16_t*>(ws + pl.dzt) : nullptr;
     for (int c = 0; c < pl.chunks; ++c) {
         const Live live{idx, count, static_cast<int32_t>(c * pl.chunk), static_cast<int32_t>(pl.chunk)};
         LogitsArgs l{};
         l.live = live;
-        if (!saved)
+        if (!saved) {
             TL_TRY(logits_operands(sh, a.hidden, a.ld_hidden, a.head, a.ld_head, a.dtype, ws + pl.hidden, ws + pl.head, c == 0, absmax, own, l, s));
+            l.targets = a.targets;
+            l.tb = static_cast<int>(pl.chunk / sh.edge);
+            l.scale2 = a.scale * LOG2E;
+            l.m = at(pl.m);
+            l.s = at(pl.s);
+            l.zt = at(pl.zt);
+            l.rows_pitch = pl.chunk;
+            l.e = ws + pl.e;
+            l.vp = vp;
+            TL_TRY(launch_logits<LG_SAVE>(l, sh.edge, sh.parts, s));
+            const CombineArgs f{l.m, l.s, l.zt, static_cast<size_t>(pl.chunk), 1, sh.ta(), a.targets, a.vocab, nullptr, nullptr, live,
+                                a.tokens, l.scale2, at(pl.logp), at(pl.ref), at(pl.shift)};
+            hipLaunchKernelGGL(combine_kernel<32>, dim3(static_cast<unsigned>(pl.chunk / 32)), dim3(256), 0, s, f);
+            TL_TRY(hipGetLastError());
+        }
         PrepareArgs p{};
         if (sh.parts == 2 && c == 0) p.dz = {everyone, a.grad_logp, a.scale, dz_scale};
         const int col_tiles = static_cast<int>(ceil_div(sh.cols, 64));
@@ -1756,31 +1718,15 @@ hipError_t launch_token_logp_backward(const muon_token_logp_backward_args& a, vo
             else hipLaunchKernelGGL((prepare_kernel<float, 2>), dim3(prepare), dim3(256), 0, s, p);
             TL_TRY(hipGetLastError());
         }
-        if (saved) {
-            const DzArgs d{saved + sv.e, reinterpret_cast<const float*>(saved + sv.m),
-                           reinterpret_cast<const float*>(saved + sv.logp), reinterpret_cast<const float*>(saved + sv.ref),
-                           reinterpret_cast<const float*>(saved + sv.shift), a.scale * LOG2E, static_cast<size_t>(sh.tp), sh.edge, live,
-                           a.targets, a.lse, a.grad_logp, a.scale, static_cast<int>(a.vocab), vp,
-                           static_cast<size_t>(pl.chunk), dz, dzt, dz_part, dz_part, dz_scale};
-            const dim3 grid(static_cast<unsigned>(vp / 64), static_cast<unsigned>(pl.chunk / 64));
-            if (sh.parts == 1) hipLaunchKernelGGL((dz_kernel<uint16_t, 1>), grid, dim3(256), 0, s, d);
-            else hipLaunchKernelGGL((dz_kernel<float, 2>), grid, dim3(256), 0, s, d);
-            TL_TRY(hipGetLastError());
-        } else {
-            l.dz_scale = dz_scale;
-            l.targets = a.targets;
-            l.tb = static_cast<int>(pl.chunk / sh.edge);
-            l.scale2 = a.scale * LOG2E;
-            l.scale = a.scale;
-            l.lse = a.lse;
-            l.grad_logp = a.grad_logp;
-            l.dz = dz;
-            l.dzt = dzt;
-            l.dz_part = l.dzt_part = dz_part;
-            l.vp = vp;
-            l.rows_pitch = pl.chunk;
-            TL_TRY(launch_logits<LG_DZ>(l, sh.edge, sh.parts, s));
-        }
+        auto kept = [&](size_t o, size_t without) { return reinterpret_cast<const float*>(saved ? saved + o : ws + without); };
+        const DzArgs d{kept(sv.e, pl.e), kept(sv.m, pl.m), saved ? 0 : live.first, kept(sv.logp, pl.logp), kept(sv.ref, pl.ref),
+                       kept(sv.shift, pl.shift), a.scale * LOG2E, static_cast<size_t>(saved ? sh.tp : pl.chunk), sh.edge, live, a.targets,
+                       a.grad_logp, a.scale, static_cast<int>(a.vocab), vp, static_cast<size_t>(pl.chunk), dz, dzt, dz_part, dz_part,
+                       dz_scale};
+        const dim3 grid(static_cast<unsigned>(vp / 64), static_cast<unsigned>(pl.chunk / 64));
+        if (sh.parts == 1) hipLaunchKernelGGL((dz_kernel<uint16_t, 1>), grid, dim3(256), 0, s, d);
+        else hipLaunchKernelGGL((dz_kernel<float, 2>), grid, dim3(256), 0, s, d);
+        TL_TRY(hipGetLastError());
         GradArgs g{};
         g.live = live;
         g.cols = static_cast<int>(sh.cols);

@@ -394,3 +394,31 @@ def test_token_logp_target_far_below_the_best(gpu_lib, dtype, t, use_saved):
     gh, gw = _backward(gpu_lib, h, w, y, lse, c, saved=saved)
     _check_backward(h, w, y, c, 1.0, dtype, gh, gw)
     assert torch.isfinite(gh).all() and torch.isfinite(gw).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("t", [20, 100, 300])
+@pytest.mark.parametrize("use_saved", [True, False])
+def test_token_logp_gradient_of_certain_tokens(gpu_lib, dtype, t, use_saved):
+    # Token i's target stands x_i above v - 1 equal logits of 0, in exact arithmetic, and column 1 of head holds nothing but
+    # the target: grad_hidden[i, 1] = c_i (1 - p) = -c_i expm1(logp), from 6e-3 down to 2e-6 of c_i.  Its relative error: the sum
+    # of v terms (v / 64 + 64) u, 2^(k x) with k x rounded at 32 (2^-19 ln 2), dz's and the output's rounding.
+    import torch
+    print("[token_logp certain]", t, dtype, use_saved, flush=True)
+    d, v = 64, 900
+    x = torch.tensor([12.0, 16.0, 18.5, 20.0], device="cuda").repeat(t // 4)
+    h, w = torch.zeros((t, d), device="cuda"), torch.zeros((v, d), device="cuda")
+    w[7, 1] = 1.0
+    h[:, 1] = x
+    h, w = h.to(_dt(dtype)), w.to(_dt(dtype))
+    y = torch.full((t,), 7, dtype=torch.int64, device="cuda")
+    c = torch.linspace(0.5, 1.0, t, device="cuda")
+    saved = _saved(gpu_lib, h, w) if use_saved else None
+    logp, lse = _forward(gpu_lib, h, w, y, saved=saved)
+    gh, gw = _backward(gpu_lib, h, w, y, lse, c, saved=saved)
+    rest = (v - 1) * np.exp(-_np(x))
+    ref = _np(c) * rest / (1 + rest)
+    tol = (v / 64 + 64) * U + 2.0 ** -19 + PARTS[dtype] + ROUND[dtype]
+    err = np.abs(_np(gh)[:, 1] - ref) / ref
+    assert err.max() <= tol, (float(err.max()), tol)
+    assert abs(_np(gw)[7, 1] - (ref * _np(x)).sum()) <= tol * (ref * _np(x)).sum()
