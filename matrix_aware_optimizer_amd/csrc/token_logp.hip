@@ -12,8 +12,9 @@
 //    logits of one token and the softmax's running maximum and sum need one exchange between
 //    lanes and one between two waves.  Only (maximum, sum) per token and tile leave the tile;
 //    combine_kernel joins them.  With `saved` the tile's exp(z - tile maximum) goes out too: in fp16 in
-//    bf16 calls (values of at most 1: 11 bits where bf16 keeps 8; what falls below 2^-24 of its tile's maximum is 0), else
-//    in fp32.
+//    bf16 calls (values of at most 1: 11 bits where bf16 keeps 8, fewer below 2^-14 of the tile's maximum, 0 below 2^-25), else
+//    in fp32.  Neither maximum nor sum counts the token's target: beside a certain target the other entries of its tile keep
+//    their bits, and the target's own gradient comes from logp.
 //  - Backward: dz comes from `saved` by an elementwise pass; without `saved` the logits' product comes first again, for a
 //    chunk of tokens at a time.  The target's own dz is -c expm1(logp): 1 - exp(z - lse) from a rounded lse would be off by
 //    1e-6, all there is of a certain token's gradient.
@@ -30,7 +31,7 @@
 // The softmax works in base 2: with k' = |scale| log2(e) and acc the product (negated if scale is negative) a tile keeps
 // M = k' max acc, rounded, and sums 2^(k' acc - M), the exponent formed by one fused operation: what M is rounded to
 // cancels, where a rounded k' acc would lose a unit of its own size.  A target's acc is kept as it is and its own term
-// stays out of the sum S of its token, logp = -log(1 + S 2^(M - k' acc_target)), which keeps its relative precision as
+// stays out of M and the sum S of its token, logp = -log(1 + S 2^(M - k' acc_target)), which keeps its relative precision as
 // logp goes to 0.
 #include <algorithm>
 
@@ -416,14 +417,16 @@ __global__ __launch_bounds__(pt::Tile<EDGE>::THREADS, 2) void logits_kernel(Logi
 
     float* smax = reinterpret_cast<float*>(lds);          // [STACKED][EDGE]
     float* ssum = smax + TL::STACKED * EDGE;              // [STACKED][EDGE]
-    int col[TL::SN], y[TL::SN];
+    int col[TL::SN];
     float mx[TL::SN];
 #pragma unroll
     for (int j = 0; j < TL::SN; ++j) {
         col[j] = TL::column(j);
         const int r = min(r0 + col[j], n - 1);
         const int64_t t = a.targets[a.live.idx[a.live.first + r]];
-        y[j] = t < a.vocab ? static_cast<int>(t) - vl : -1;
+        const int y = t < a.vocab ? static_cast<int>(t) - vl : -1;
+        float zt = 0.0f;
+        bool mine = false;
         mx[j] = -INFINITY;
         if (edge) {
 #pragma unroll
@@ -435,9 +438,17 @@ __global__ __launch_bounds__(pt::Tile<EDGE>::THREADS, 2) void logits_kernel(Logi
 #pragma unroll
         for (int i = 0; i < TL::SM; ++i)
 #pragma unroll
-            for (int q = 0; q < 16; ++q) mx[j] = fmaxf(mx[j], acc[i][j][q]);
+            for (int q = 0; q < 16; ++q) {
+                if (32 * i + 8 * (q >> 2) + (q & 3) == y) {   // the target goes out by itself
+                    zt = acc[i][j][q];
+                    mine = true;
+                    acc[i][j][q] = -INFINITY;
+                }
+                mx[j] = fmaxf(mx[j], acc[i][j][q]);
+            }
         mx[j] = fmaxf(mx[j], __shfl_xor(mx[j], 32, 64));
         if (h == 0) smax[EDGE * place + col[j]] = mx[j];
+        if (mine && r0 + col[j] < n) a.zt[a.live.first + r0 + col[j]] = zt;
     }
     lds_barrier();
 #pragma unroll
@@ -446,22 +457,17 @@ __global__ __launch_bounds__(pt::Tile<EDGE>::THREADS, 2) void logits_kernel(Logi
         for (int p = 0; p < TL::STACKED; ++p) mx[j] = fmaxf(mx[j], smax[EDGE * p + col[j]]);
         mx[j] *= k;
         const float base = shown(mx[j]);
-        float sum = 0.0f, zt = 0.0f;
-        bool mine = false;
+        float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < TL::SM; ++i)
 #pragma unroll
             for (int q = 0; q < 16; ++q) {
-                const int dv = 32 * i + 8 * (q >> 2) + (q & 3);
-                const float z = acc[i][j][q], ex = __builtin_amdgcn_exp2f(fmaf(z, k, -base));
-                const bool target = dv == y[j];
-                sum += target ? 0.0f : ex;
-                if (target) { zt = z; mine = true; }
+                const float ex = __builtin_amdgcn_exp2f(fmaf(acc[i][j][q], k, -base));
+                sum += ex;
                 if (MODE == LG_SAVE) acc[i][j][q] = ex;
             }
         sum += __shfl_xor(sum, 32, 64);
         if (h == 0) ssum[EDGE * place + col[j]] = sum;
-        if (mine && r0 + col[j] < n) a.zt[a.live.first + r0 + col[j]] = zt;
     }
     lds_barrier();
 #pragma unroll
@@ -860,7 +866,12 @@ __global__ __launch_bounds__(256, NT == 1 ? 4 : 1) void few_kernel(FewArgs a) {
         z[r] = red[0][PER * g + r][t] + red[1][PER * g + r][t] + red[2][PER * g + r][t] + red[3][PER * g + r][t];
         if constexpr (PARTS == 3) z[r] = __builtin_amdgcn_ldexpf(z[r], -exponent_of(hs));
         if (a.scale2 < 0.0f) z[r] = -z[r];
-        if (v + r >= a.vocab) z[r] = -INFINITY;
+        if (v + r >= a.vocab) {
+            z[r] = -INFINITY;
+        } else if (r == y) {   // the target goes out by itself
+            a.zt[t] = z[r];
+            z[r] = -INFINITY;
+        }
         m = fmaxf(m, z[r]);
     }
     part[0][g][t] = m;
@@ -874,8 +885,7 @@ __global__ __launch_bounds__(256, NT == 1 ? 4 : 1) void few_kernel(FewArgs a) {
         const float e = __builtin_amdgcn_exp2f(fmaf(z[r], k, -shown(m)));
         if constexpr (sizeof(T) == 2) e16[r] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(e));
         else if (a.e && t < a.tokens) static_cast<float*>(a.e)[t * a.vp + v + r] = e;
-        if (r == y && v + r < a.vocab) a.zt[t] = z[r];
-        else sum += e;
+        sum += e;
     }
     part[1][g][t] = sum;
     __syncthreads();

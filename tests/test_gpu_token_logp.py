@@ -422,3 +422,40 @@ def test_token_logp_gradient_of_certain_tokens(gpu_lib, dtype, t, use_saved):
     err = np.abs(_np(gh)[:, 1] - ref) / ref
     assert err.max() <= tol, (float(err.max()), tol)
     assert abs(_np(gw)[7, 1] - (ref * _np(x)).sum()) <= tol * (ref * _np(x)).sum()
+
+
+@pytest.mark.parametrize("t,v,dtype", [(20, 100, "bf16"), (20, 900, "bf16"), (100, 100, "bf16"), (300, 900, "bf16"),
+                                       (600, 17000, "bf16"), (20, 100, "f32"), (20, 900, "f32")])
+@pytest.mark.parametrize("use_saved", [True, False])
+def test_token_logp_gradients_beside_a_certain_target(gpu_lib, dtype, t, v, use_saved):
+    # The target stands 12 to 24 above entries of logits 0 .. -3 (exact arithmetic): column 0 of grad_hidden sums over the other
+    # entries of the target's tile alone, and the rows of grad_head hold one entry's share each.  Relative to fp64, term by
+    # term of one sign: exp(z - m) in fp16 2^-11, then as in test_token_logp_gradient_of_certain_tokens.
+    import torch
+    print("[token_logp beside]", t, v, dtype, use_saved, flush=True)
+    d = 64
+    x = torch.tensor([12.0, 16.0, 20.0, 24.0], device="cuda").repeat(t // 4)
+    h, w = torch.zeros((t, d), device="cuda"), torch.zeros((v, d), device="cuda")
+    w[:100, 0] = 1.0
+    w[7, 0], w[7, 1] = 0.0, 1.0
+    w[:, 2] = -(torch.arange(v, device="cuda") % 4).float()
+    w[7, 2] = 0.0
+    h[:, 1], h[:, 2] = x, 1.0
+    h, w = h.to(_dt(dtype)), w.to(_dt(dtype))
+    y = torch.full((t,), 7, dtype=torch.int64, device="cuda")
+    c = torch.linspace(0.5, 1.0, t, device="cuda")
+    saved = _saved(gpu_lib, h, w) if use_saved else None
+    logp, lse = _forward(gpu_lib, h, w, y, saved=saved)
+    z = _np(h) @ _np(w).T
+    others = np.exp(z)
+    others[:, 7] = 0.0
+    rest = others.sum(1) * np.exp(-_np(x))
+    assert np.all(np.abs(_np(logp) + np.log1p(rest)) <= ((v / 64 + 64) * U + 2.0 ** -19) * rest)
+    gh, gw = _backward(gpu_lib, h, w, y, lse, c, saved=saved)
+    dz = -_np(c)[:, None] * others * np.exp(-_np(x))[:, None] / (1 + rest)[:, None]
+    tol = (v / 64 + 64) * U + 2.0 ** -19 + PARTS[dtype] + ROUND[dtype] + (2.0 ** -11 if dtype == "bf16" else 0.0)
+    ref = dz @ _np(w)[:, 0]
+    assert np.all(np.abs(_np(gh)[:, 0] - ref) <= tol * np.abs(ref)), float(np.max(np.abs(_np(gh)[:, 0] / ref - 1)))
+    ref = dz.sum(0)
+    keep = np.arange(v) != 7
+    assert np.all(np.abs(_np(gw)[:, 2] - ref)[keep] <= (tol + (t / 16) * U) * np.abs(ref)[keep])
