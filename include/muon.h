@@ -341,7 +341,9 @@ muon_status muon_token_logp(const muon_token_logp_args* args, void* workspace, s
  *
  * Precision in fp32: the products take each operand as two fp16 parts under one
  * power-of-two scale, 22 bits for values down to 2^-28 of the operand's largest
- * finite one, fewer below.  Those of up to 64 tokens take three bf16 parts, 24
+ * finite one, fewer below; dz has a scale for each token, so that a token's row of
+ * grad_hidden keeps its bits beside tokens with larger gradients (in grad_head a
+ * token counts with 22 bits down to 2^-28 of the largest).  Those of up to 64 tokens take three bf16 parts, 24
  * bits for values down to 2^-109; hidden is scaled for them first in a backward
  * pass and in a forward pass with `saved`. */
 typedef struct {

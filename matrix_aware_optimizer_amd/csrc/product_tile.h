@@ -397,15 +397,17 @@ template <int EDGE> struct Tile {
     }
 };
 
-// Takes two operands' scales, powers of two, out of their product at once: either alone might leave fp32's range.
-template <typename TL> __device__ __forceinline__ void unscale(typename TL::Acc& acc, float sa, float sb) {
-    const int e = 254 - static_cast<int>((__float_as_uint(sa) >> 23) + (__float_as_uint(sb) >> 23));
+// The accumulators of column j times 2^e[j]: both operands' scales, powers of two, at once (either alone might leave fp32's range).
+template <typename TL> __device__ __forceinline__ void unscale(typename TL::Acc& acc, const int (&e)[TL::SN]) {
 #pragma unroll
     for (int i = 0; i < TL::SM; ++i)
 #pragma unroll
         for (int j = 0; j < TL::SN; ++j)
 #pragma unroll
-            for (int q = 0; q < 16; ++q) acc[i][j][q] = __builtin_amdgcn_ldexpf(acc[i][j][q], e);
+            for (int q = 0; q < 16; ++q) {
+                acc[i][j][q] = __builtin_amdgcn_ldexpf(acc[i][j][q], e[j]);
+                asm volatile("" : "+v"(acc[i][j][q]));   // here and in place
+            }
 }
 
 // Tiles in runs of 32 on one XCD (the hardware deals workgroups round-robin over the 8), a

@@ -22,8 +22,10 @@
 //    once, so that both gradients are k-contiguous products (C rows = columns of the gradient,
 //    C columns = its rows).  Few tiles: the sum over k is split over workgroups that leave fp32
 //    tiles, added in order by slab_sum_kernel.
-//  - fp32 operands travel as two fp16 parts under a scale (product_tile.h), dz in fp32 calls too: absmax_kernel
-//    finds the largest values, and the kernels that make the copies the scales.
+//  - fp32 operands travel as two fp16 parts under a scale (product_tile.h): absmax_kernel finds the largest values, and the
+//    kernels that make the copies the scales.  So does dz in fp32 calls, under a scale for each token that its own largest entry
+//    gives, -c expm1(logp) of the target: a token's gradient keeps its bits beside tokens with larger ones.  grad_hidden takes
+//    the tokens' scales out of its columns; for grad_head they are taken out of hidden's copy before the product.
 //  - Few tokens: what counts is the head's way through memory, so each step reads (or writes) it once where it is,
 //    with 16 x 16 MFMAs and no staging (fp32 as three bf16 parts there: exact down to 2^-109, so that only hidden, which
 //    is small and quickly looked through, gets a scale).
@@ -196,12 +198,12 @@ __device__ __forceinline__ float operand_scale(const uint32_t* part, bool head, 
     __syncthreads();   // `red` may be used again
     return scale_of(m);
 }
-// dz's: no value exceeds |scale grad_logp| of its token.
+// Exponent of the smallest scale that dz of any token can get: no value exceeds |scale grad_logp| of its token.
 struct DzScaleArgs {
     Live live;
     const float* grad_logp;
     float scale;
-    float* out;
+    int32_t* out;
 };
 __device__ __forceinline__ void dz_scale(const DzScaleArgs& a, uint32_t* red) {
     uint32_t m = 0;
@@ -209,8 +211,34 @@ __device__ __forceinline__ void dz_scale(const DzScaleArgs& a, uint32_t* red) {
 #pragma unroll 8
     for (int r = threadIdx.x; r < n; r += blockDim.x) m = max(m, finite_bits(a.scale * a.grad_logp[a.live.idx[a.live.first + r]]));
     m = block_max(m, red);
-    if (threadIdx.x == 0) *a.out = scale_of(m);
+    if (threadIdx.x == 0) *a.out = exponent_of(scale_of(m));
 }
+
+// What dz of a list entry takes.  dz_y = -c expm1(logp) of the target is minus the sum of the entry's other values, so none is larger.
+struct DzTokenArgs {
+    Live live;
+    const int64_t* targets;
+    const float *logp, *grad_logp;   // logp: by list entry
+    float scale;
+    int vocab;
+    const int32_t* least;            // two parts: dz_scale's
+};
+struct DzToken {
+    int64_t target;
+    float c, logp;
+    __device__ __forceinline__ void load(const DzTokenArgs& a, int tok, int entry) {
+        target = a.targets[tok];
+        c = a.scale * a.grad_logp[tok];
+        logp = a.logp[entry];
+    }
+    __device__ __forceinline__ bool valid(const DzTokenArgs& a) const { return target < a.vocab; }
+    __device__ __forceinline__ float dy() const { return -c * expm1f(logp); }
+    // Exponent of the token's scale.
+    __device__ __forceinline__ int exponent(const DzTokenArgs& a) const {
+        const uint32_t largest = finite_bits(valid(a) ? dy() : c);   // 0 also where it is not finite
+        return largest ? max(*a.least, exponent_of(scale_of(largest))) : *a.least;
+    }
+};
 
 // ---------------------------------------------------------------------------
 // Operand copies
@@ -224,7 +252,7 @@ struct PackArgs {
     Live live;
     uint16_t* dst;
     size_t dst_ld, part;   // elements
-    const float* scale;    // two parts, transposes: the operand's scale
+    const float* scale;    // transposes: the operand's scale (two parts)
 };
 
 // Copies for the logits' product, dst[part][r][0 .. dst_ld) = parts of src[row r], zero past its columns: of head (the first
@@ -271,16 +299,14 @@ __global__ __launch_bounds__(256) void pack_kernel(PackBothArgs both) {
 // dst[part][c][r] = parts of src[row r][c] for c < cols, zero for rows past the last up to a multiple of 64: the
 // 64 x 64 tile at (r0, c0), through LDS as fp32, 16-byte accesses on both sides.
 template <typename T, int PARTS> __device__ __forceinline__ void transpose_tile(const PackArgs& a, int64_t r0, int64_t c0, float (&tile)[64][65]) {
-    const int64_t rows = a.use_live ? a.live.rows() : a.rows;
-    if (r0 >= rows) return;
     const float scale = PARTS == 1 ? 1.0f : *a.scale;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         const int k = (threadIdx.x >> 3) + 32 * half, x = 8 * (threadIdx.x & 7);
         const int64_t r = r0 + k, left = a.cols - c0 - x;
         Run<T> w;
-        if (r < rows && left > 0) {
-            const auto* q = G(static_cast<const T*>(a.src) + static_cast<size_t>(a.use_live ? a.live.idx[a.live.first + r] : r) * a.ld + c0);
+        if (r < a.rows && left > 0) {
+            const auto* q = G(static_cast<const T*>(a.src) + static_cast<size_t>(r) * a.ld + c0);
             if (left >= 8) w.load(q, x);
             else w.load(q, x, static_cast<unsigned>(left));
         }
@@ -305,12 +331,12 @@ template <typename T, int PARTS> __device__ __forceinline__ void transpose_tile(
     }
 }
 
-// One launch for what the gradients' products need: the transposes of head and hidden, the scale of dz (two parts) and, for
-// grad_hidden, zeros in the rows of tokens that are not scored.  Each is a run of workgroups.
+// One launch for what comes before dz: the transpose of head, the least scale of dz (two parts) and, for grad_hidden, zeros in
+// the rows of tokens that are not scored.  Each is a run of workgroups.
 struct PrepareArgs {
-    PackArgs head, hidden;
-    int head_blocks, hidden_blocks;   // 64 x 64 tiles, along the rows first
-    int head_rows, hidden_rows;       // of them along the rows
+    PackArgs head;
+    int head_blocks, head_rows;       // 64 x 64 tiles, along the rows first; of them along the rows
+    Live live;
     const int64_t* targets;
     int64_t tokens, cols;
     void* zero;
@@ -322,16 +348,11 @@ template <typename T, int PARTS> __global__ __launch_bounds__(256) void prepare_
     __shared__ float tile[64][65];
     int b = blockIdx.x;
     if (b < a.head_blocks) {
-        if (a.head.live.rows() == 0) return;   // nothing will read it
+        if (a.live.rows() == 0) return;   // nothing will read it
         transpose_tile<T, PARTS>(a.head, static_cast<int64_t>(b % a.head_rows) * 64, static_cast<int64_t>(b / a.head_rows) * 64, tile);
         return;
     }
     b -= a.head_blocks;
-    if (b < a.hidden_blocks) {
-        transpose_tile<T, PARTS>(a.hidden, static_cast<int64_t>(b % a.hidden_rows) * 64, static_cast<int64_t>(b / a.hidden_rows) * 64, tile);
-        return;
-    }
-    b -= a.hidden_blocks;
     if (PARTS == 2 && a.dz.out && b-- == 0) {
         dz_scale(a.dz, reinterpret_cast<uint32_t*>(tile));
         return;
@@ -406,7 +427,12 @@ __global__ __launch_bounds__(pt::Tile<EDGE>::THREADS, 2) void logits_kernel(Logi
     const int vl = v0 + TL::first_row();              // this lane's first vocabulary entry
     const bool edge = v0 + EDGE > a.vocab;            // uniform: entries past the vocabulary
     const float k = rate_of(a.scale2);
-    if constexpr (PARTS == 2) pt::unscale<TL>(acc, a.scales[0], a.scales[1]);
+    if constexpr (PARTS == 2) {
+        int e[TL::SN];
+#pragma unroll
+        for (int j = 0; j < TL::SN; ++j) e[j] = -exponent_of(a.scales[0]) - exponent_of(a.scales[1]);
+        pt::unscale<TL>(acc, e);
+    }
     if (a.scale2 < 0.0f) {
 #pragma unroll
         for (int i = 0; i < TL::SM; ++i)
@@ -425,8 +451,9 @@ __global__ __launch_bounds__(pt::Tile<EDGE>::THREADS, 2) void logits_kernel(Logi
         const int r = min(r0 + col[j], n - 1);
         const int64_t t = a.targets[a.live.idx[a.live.first + r]];
         const int y = t < a.vocab ? static_cast<int>(t) - vl : -1;
+        // this lane holds entries 8 n .. 8 n + 3 of its share
+        const bool mine = y >= 0 && y < 32 * TL::SM && (y & 4) == 0 && r0 + col[j] < n;
         float zt = 0.0f;
-        bool mine = false;
         mx[j] = -INFINITY;
         if (edge) {
 #pragma unroll
@@ -439,16 +466,15 @@ __global__ __launch_bounds__(pt::Tile<EDGE>::THREADS, 2) void logits_kernel(Logi
         for (int i = 0; i < TL::SM; ++i)
 #pragma unroll
             for (int q = 0; q < 16; ++q) {
-                if (32 * i + 8 * (q >> 2) + (q & 3) == y) {   // the target goes out by itself
-                    zt = acc[i][j][q];
-                    mine = true;
-                    acc[i][j][q] = -INFINITY;
-                }
+                const bool target = 32 * i + 8 * (q >> 2) + (q & 3) == y;   // goes out by itself
+                zt = target ? acc[i][j][q] : zt;
+                acc[i][j][q] = target ? -INFINITY : acc[i][j][q];
                 mx[j] = fmaxf(mx[j], acc[i][j][q]);
+                if (q % 4 == 3) __builtin_amdgcn_sched_barrier(0);          // else the compares' masks pile up
             }
         mx[j] = fmaxf(mx[j], __shfl_xor(mx[j], 32, 64));
         if (h == 0) smax[EDGE * place + col[j]] = mx[j];
-        if (mine && r0 + col[j] < n) a.zt[a.live.first + r0 + col[j]] = zt;
+        if (mine) a.zt[a.live.first + r0 + col[j]] = zt;
     }
     lds_barrier();
 #pragma unroll
@@ -510,69 +536,95 @@ __global__ __launch_bounds__(pt::Tile<EDGE>::THREADS, 2) void logits_kernel(Logi
 // dz from the kept exp(z - m)
 // ---------------------------------------------------------------------------
 
+// e of entry r of a run
+__device__ __forceinline__ float e_of(const Run<uint16_t>& x, int r) {
+    return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(x.w[r >> 1] >> (16 * (r & 1)))));
+}
+__device__ __forceinline__ float e_of(const Run<float>& x, int r) { return x.get(r); }
+
 struct DzArgs {
     const void* e;          // list entry from `kept` on x vocabulary, pitch vp
     const float* m;         // tile x list entry from `kept` on
     int kept;
-    const float *logp, *ref, *shift;   // list entry: logp, and p = e 2^(M - k' ref + shift)
+    const float *ref, *shift;   // list entry: p = e 2^(M - k' ref + shift)
     float scale2;
     size_t m_pitch;
     int m_edge;             // vocabulary entries per tile
-    Live live;
-    const int64_t* targets;
-    const float* grad_logp;
-    float scale;
-    int vocab;
+    DzTokenArgs tok;
     size_t vp, rows_pitch;
     uint16_t *dz, *dzt;     // rows relative to live.first
     size_t dz_part, dzt_part;
-    const float* dz_scale;  // two parts
+    int32_t* exponents;     // two parts: of the tokens' scales, by row of dz
+    PackArgs hidden;        // the transpose of hidden for grad_head, by workgroups past the vocabulary's
 };
 
-// 64 tokens x 64 entries a workgroup.  Reads 2 (fp32: 4) bytes an element and writes 2 x 2 (fp32: 2 x 4), HBM-bound
+// 64 tokens x 64 entries a workgroup, or 64 tokens x 64 columns of hidden.  Reads 2 (fp32: 4) bytes an element and writes 2 x 2 (fp32: 2 x 4), HBM-bound
 // (6144 x 32000 bf16: 1.2 GB in 220 us, 5.4 TB/s).  E: what e is kept in.
 template <typename E, int PARTS>
 __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
-    __shared__ uint16_t tile[PARTS][64][72];   // [entry][token]
-    const int n = a.live.rows();
-    const int r0 = blockIdx.y * 64, v0 = blockIdx.x * 64;
+    __shared__ uint16_t tile[PARTS][64][72];   // [entry or column][token]
+    const int n = a.tok.live.rows();
+    // dz's tiles along the vocabulary first, then hidden's along the tokens first (neighbours write one run of a row)
+    const int across = static_cast<int>(a.vp / 64), down = static_cast<int>(a.rows_pitch / 64);
+    const int past = static_cast<int>(blockIdx.x) - across * down;
+    const int r0 = 64 * (past < 0 ? static_cast<int>(blockIdx.x) / across : past % down);
+    const int v0 = 64 * (static_cast<int>(blockIdx.x) % across), c0 = past < 0 ? 0 : 64 * (past / down);
     if (r0 >= n) return;
     const int vb = threadIdx.x & 7;            // 8 entries each
-    const float ds = PARTS == 2 ? *a.dz_scale : 1.0f;
     const float k = rate_of(a.scale2);
+    // everything that comes from far first: it waits for nothing
+    Run<E> x[2];
+    int tok[2];
+    DzToken t[2];
+    float m[2], ref[2], shift[2];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const int r = min(r0 + static_cast<int>(threadIdx.x >> 3) + 32 * half, n - 1), entry = a.tok.live.first + r;
+        tok[half] = a.tok.live.idx[entry];
+        if (past < 0) {
+            x[half].load(G(static_cast<const E*>(a.e)) + static_cast<size_t>(entry - a.kept) * a.vp, v0 + 8 * vb);
+            m[half] = a.m[(v0 / a.m_edge) * a.m_pitch + entry - a.kept];
+            ref[half] = a.ref[entry];
+            shift[half] = a.shift[entry];
+        }
+    }
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+        t[half].load(a.tok, tok[half], a.tok.live.first + min(r0 + static_cast<int>(threadIdx.x >> 3) + 32 * half, n - 1));
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         const int rt = (threadIdx.x >> 3) + 32 * half, r = r0 + rt;
-        float c = 0.0f, f = 0.0f, dy = 0.0f;
-        int y = -1;
-        if (r < n) {
-            const int tok = a.live.idx[a.live.first + r];
-            const int64_t t = a.targets[tok];
-            c = a.scale * a.grad_logp[tok];
-            y = t < a.vocab ? static_cast<int>(t) - v0 - 8 * vb : -1;
-            const int o = a.live.first + r;
-            f = c * __builtin_amdgcn_exp2f(fmaf(-a.ref[o], k, a.m[(v0 / a.m_edge) * a.m_pitch + o - a.kept]) + a.shift[o]);
-            // 1 - p of the target from logp alone: e is rounded, which 1 - p would magnify as p goes to 1
-            dy = -c * expm1f(a.logp[o]);
-        }
-        float x[8];
-        const size_t o = static_cast<size_t>(a.live.first - a.kept + min(r, n - 1)) * a.vp + v0 + 8 * vb;
-        if constexpr (sizeof(E) == 2) {
-            const pt::f16x8_t w = __builtin_bit_cast(pt::f16x8_t, G(reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.e) + o))[0]);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) x[q] = static_cast<float>(w[q]);
-        } else {
-            const float4 w0 = ld_f4(static_cast<const float*>(a.e) + o), w1 = ld_f4(static_cast<const float*>(a.e) + o + 4);
-            x[0] = w0.x; x[1] = w0.y; x[2] = w0.z; x[3] = w0.w;
-            x[4] = w1.x; x[5] = w1.y; x[6] = w1.z; x[7] = w1.w;
-        }
         uint16_t v[8][2];
+        int exponent = 0;
+        if constexpr (PARTS == 2) exponent = t[half].exponent(a.tok);
+        if (past >= 0) {   // hidden under its scale, times the least of dz over the token's own: at most 1
+            const int up = PARTS == 2 ? exponent_of(*a.hidden.scale) + *a.tok.least - exponent : 0;
+            const int64_t left = r < n ? a.hidden.cols - c0 - 8 * vb : 0;
+            const auto* q = G(static_cast<const E*>(a.hidden.src) + static_cast<size_t>(tok[half]) * a.hidden.ld + c0);
+            if (left >= 8) x[half].load(q, 8 * vb);
+            else if (left > 0) x[half].load(q, 8 * vb, static_cast<unsigned>(left));
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-            to_parts<PARTS>(c == 0.0f || v0 + 8 * vb + q >= a.vocab ? 0.0f : q == y ? dy : -x[q] * f, ds, v[q]);
+            for (int q = 0; q < 8; ++q) {
+                const float h = x[half].get(q);
+                to_parts<PARTS>(PARTS == 2 ? __builtin_amdgcn_ldexpf(h, up) : h, 1.0f, v[q]);
+            }
+        } else {
+            const int y = t[half].valid(a.tok) ? static_cast<int>(t[half].target) - v0 - 8 * vb : -1;
+            const float c = t[half].c;
+            float f = c * __builtin_amdgcn_exp2f(fmaf(-ref[half], k, m[half]) + shift[half]), dy = t[half].dy();
+            if constexpr (PARTS == 2) {   // under the token's scale
+                f = __builtin_amdgcn_ldexpf(f, exponent);
+                dy = __builtin_amdgcn_ldexpf(dy, exponent);
+                if (v0 == 0 && vb == 0 && r < n) a.exponents[r] = exponent;
+            }
+            const bool none = r >= n || c == 0.0f;
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                to_parts<PARTS>(none || v0 + 8 * vb + q >= a.tok.vocab ? 0.0f : q == y ? dy : -e_of(x[half], q) * f, 1.0f, v[q]);
+        }
 #pragma unroll
         for (int p = 0; p < PARTS; ++p) {
-            if (a.dz && r < n) {
+            if (a.dz && r < n && past < 0) {
                 u32x4 w;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) w[k] = v[2 * k][p] | static_cast<uint32_t>(v[2 * k + 1][p]) << 16;
@@ -583,14 +635,18 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
         }
     }
     if (!a.dzt) return;
+    uint16_t* out = past < 0 ? a.dzt + static_cast<size_t>(v0) * a.rows_pitch : a.hidden.dst + static_cast<size_t>(c0) * a.rows_pitch;
+    const size_t part = past < 0 ? a.dzt_part : a.hidden.part;
+    const int64_t rows = past < 0 ? 64 : a.hidden.cols - c0;
     __syncthreads();
 #pragma unroll
     for (int p = 0; p < PARTS; ++p)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int v = (threadIdx.x >> 3) + 32 * half, q = 8 * (threadIdx.x & 7);
+            if (v >= rows) continue;
             const u32x4 w = *reinterpret_cast<const u32x4*>(&tile[p][v][q]);
-            G(reinterpret_cast<u32x4*>(a.dzt + p * a.dzt_part + static_cast<size_t>(v0 + v) * a.rows_pitch + r0 + q))[0] = w;
+            G(reinterpret_cast<u32x4*>(out + p * part + static_cast<size_t>(v) * a.rows_pitch + r0 + q))[0] = w;
         }
 }
 
@@ -614,7 +670,8 @@ struct GradArgs {
     size_t ld;
     float* slab;            // fp32 tiles in accumulator layout, [split][tile][quads][threads] x 16 bytes, or NULL: write out
     int add;                // add to what the slab holds (later chunks of tokens)
-    const float *scale, *dz_scale;   // two parts: of the transposed operand and of dz
+    const float* scale;              // two parts: of the transposed operand
+    const int32_t* exponents;        // and of dz: by row (by_token), or the least
 };
 
 // A whole 16-byte piece of the output at any element alignment, or the first `left` of its elements.
@@ -666,7 +723,13 @@ __global__ __launch_bounds__(pt::Tile<EDGE>::THREADS, 2) void grad_kernel(GradAr
         }
         TL::template run<PARTS, false>(sa, sb, a.a_part, a.b_part, static_cast<size_t>(k_first) * (pt::KS * 2), steps, 0, lds, acc);
     }
-    if constexpr (PARTS == 2) pt::unscale<TL>(acc, *a.dz_scale, *a.scale);
+    if constexpr (PARTS == 2) {
+        const int up = exponent_of(*a.scale);
+        int e[TL::SN];
+#pragma unroll
+        for (int j = 0; j < TL::SN; ++j) e[j] = -up - a.exponents[a.by_token ? min(r0 + TL::column(j), n - 1) : 0];
+        pt::unscale<TL>(acc, e);
+    }
     if (a.slab) {
         float* s = a.slab + (static_cast<size_t>(split) * a.ta * a.tb + tile) * (EDGE * EDGE) + threadIdx.x * 4;
 #pragma unroll
@@ -954,11 +1017,6 @@ struct FewToken {
         return c == 0.0f || v >= vocab ? 0.0f : v == y ? dy : -e * f;
     }
 };
-// e of entry r of a run
-__device__ __forceinline__ float e_of(const Run<uint16_t>& x, int r) {
-    return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(x.w[r >> 1] >> (16 * (r & 1)))));
-}
-__device__ __forceinline__ float e_of(const Run<float>& x, int r) { return x.get(r); }
 // Parts of dz: hi + lo, or three.
 template <int PARTS> struct DzParts { static constexpr int N = PARTS == 1 ? 2 : 3; };
 __device__ __forceinline__ void dz_parts(float x, uint16_t (&p)[2]) {
@@ -1405,7 +1463,7 @@ struct BackwardPlan {
     int64_t chunk;          // list entries at a time
     int chunks;
     GradPlan gh, gw;
-    size_t idx, count, hidden, head, head_t, hidden_t, dz, dzt, slab, slab_w, absmax, scales, bytes;
+    size_t idx, count, hidden, head, head_t, hidden_t, dz, dzt, slab, slab_w, absmax, scales, exponents, bytes;
     size_t e, m, s, zt, logp, ref, shift;   // without `saved`: e, M and S of a chunk, the rest by list entry
     static int64_t chunk_of(const Shape& sh, bool saved) {
         const int64_t row = sizeof(uint16_t) * sh.parts * (saved ? 2 : 3) * sh.vp;   // e takes as much as dz
@@ -1430,6 +1488,7 @@ struct BackwardPlan {
         slab_w = b.take(a.grad_head ? gw.slab_bytes() : 0);
         absmax = b.take(sh.parts == 1 ? 0 : sizeof(uint32_t) * (ABS_HEAD + ABS_HIDDEN));
         scales = b.take(sh.parts == 1 ? 0 : 3 * sizeof(float));
+        exponents = b.take(sh.parts == 1 ? 0 : sizeof(int32_t) * chunk);
         const size_t by_chunk = a.saved ? 0 : static_cast<size_t>(chunk), by_entry = a.saved ? 0 : sizeof(float) * sh.tp;
         e = b.take(el * by_chunk * sh.vp);
         m = b.take(sizeof(float) * by_chunk * sh.ta());
@@ -1668,11 +1727,11 @@ hipError_t launch_token_logp_backward(const muon_token_logp_backward_args& a, vo
     const int32_t* idx = reinterpret_cast<const int32_t*>(saved ? saved + sv.idx : ws + pl.idx);
     const int32_t* count = reinterpret_cast<const int32_t*>(saved ? saved + sv.count : ws + pl.count);
     if (!saved) TL_TRY(launch_live(a.targets, a.tokens, const_cast<int32_t*>(idx), const_cast<int32_t*>(count), nullptr, nullptr, s));
-    // scales of hidden and head: as the forward pass left them, or found again; of dz: over all tokens, since chunks add up
+    // scales of hidden and head: as the forward pass left them, or found again; the least of dz: over all tokens, since chunks add up
     float* own = reinterpret_cast<float*>(ws + pl.scales);
     uint32_t* absmax = reinterpret_cast<uint32_t*>(ws + pl.absmax);
     const float* scales = saved ? reinterpret_cast<const float*>(saved + sv.scales) : own;
-    float* dz_scale = own + 2;
+    int32_t* least = reinterpret_cast<int32_t*>(own + 2);
     const Live everyone{idx, count, 0, static_cast<int32_t>(sh.tp)};
     if (sh.parts == 2 && !saved) TL_TRY(launch_absmax(a.hidden, a.ld_hidden, a.head, a.ld_head, sh, everyone, absmax, s));
     const size_t vp = sh.vp, dz_part = static_cast<size_t>(pl.chunk) * vp;
@@ -1701,7 +1760,8 @@ hipError_t launch_token_logp_backward(const muon_token_logp_backward_args& a, vo
             TL_TRY(hipGetLastError());
         }
         PrepareArgs p{};
-        if (sh.parts == 2 && c == 0) p.dz = {everyone, a.grad_logp, a.scale, dz_scale};
+        p.live = live;
+        if (sh.parts == 2 && c == 0) p.dz = {everyone, a.grad_logp, a.scale, least};
         const int col_tiles = static_cast<int>(ceil_div(sh.cols, 64));
         if (a.grad_hidden && c == 0) {
             p.head = {a.head, static_cast<size_t>(a.ld_head), sh.vocab, sh.cols, 0, live, reinterpret_cast<uint16_t*>(ws + pl.head_t),
@@ -1715,33 +1775,30 @@ hipError_t launch_token_logp_backward(const muon_token_logp_backward_args& a, vo
             p.zero_ld = a.ld_grad_hidden;
             p.zero_blocks = static_cast<int>(std::min<int64_t>(ceil_div(a.tokens, 4), 4 * CUS));
         }
-        if (a.grad_head) {
-            p.hidden = {a.hidden, static_cast<size_t>(a.ld_hidden), pl.chunk, sh.cols, 1, live,
-                        reinterpret_cast<uint16_t*>(ws + pl.hidden_t), static_cast<size_t>(pl.chunk),
-                        static_cast<size_t>(pl.chunk) * sh.cols, scales};
-            p.hidden_rows = static_cast<int>(pl.chunk / 64);
-            p.hidden_blocks = p.hidden_rows * col_tiles;
-        }
-        const int prepare = p.head_blocks + p.hidden_blocks + p.zero_blocks + (p.dz.out ? 1 : 0);
+        const int prepare = p.head_blocks + p.zero_blocks + (p.dz.out ? 1 : 0);
         if (prepare > 0) {
             if (sh.parts == 1) hipLaunchKernelGGL((prepare_kernel<uint16_t, 1>), dim3(prepare), dim3(256), 0, s, p);
             else hipLaunchKernelGGL((prepare_kernel<float, 2>), dim3(prepare), dim3(256), 0, s, p);
             TL_TRY(hipGetLastError());
         }
         auto kept = [&](size_t o, size_t without) { return reinterpret_cast<const float*>(saved ? saved + o : ws + without); };
-        const DzArgs d{kept(sv.e, pl.e), kept(sv.m, pl.m), saved ? 0 : live.first, kept(sv.logp, pl.logp), kept(sv.ref, pl.ref),
-                       kept(sv.shift, pl.shift), a.scale * LOG2E, static_cast<size_t>(saved ? sh.tp : pl.chunk), sh.edge, live, a.targets,
-                       a.grad_logp, a.scale, static_cast<int>(a.vocab), vp, static_cast<size_t>(pl.chunk), dz, dzt, dz_part, dz_part,
-                       dz_scale};
-        const dim3 grid(static_cast<unsigned>(vp / 64), static_cast<unsigned>(pl.chunk / 64));
+        const PackArgs hidden_t{a.hidden, static_cast<size_t>(a.ld_hidden), pl.chunk, sh.cols, 1, live, reinterpret_cast<uint16_t*>(ws + pl.hidden_t),
+                                static_cast<size_t>(pl.chunk), static_cast<size_t>(pl.chunk) * sh.cols, scales};
+        const DzTokenArgs tok{live, a.targets, kept(sv.logp, pl.logp), a.grad_logp, a.scale, static_cast<int>(a.vocab),
+                              sh.parts == 2 ? least : nullptr};
+        int32_t* exponents = reinterpret_cast<int32_t*>(ws + pl.exponents);
+        const DzArgs d{kept(sv.e, pl.e), kept(sv.m, pl.m), saved ? 0 : live.first, kept(sv.ref, pl.ref), kept(sv.shift, pl.shift),
+                       a.scale * LOG2E, static_cast<size_t>(saved ? sh.tp : pl.chunk), sh.edge, tok, vp, static_cast<size_t>(pl.chunk),
+                       dz, dzt, dz_part, dz_part, exponents, hidden_t};
+        const dim3 grid(static_cast<unsigned>(vp / 64 + (a.grad_head ? col_tiles : 0)) * static_cast<unsigned>(pl.chunk / 64));
         if (sh.parts == 1) hipLaunchKernelGGL((dz_kernel<uint16_t, 1>), grid, dim3(256), 0, s, d);
         else hipLaunchKernelGGL((dz_kernel<float, 2>), grid, dim3(256), 0, s, d);
         TL_TRY(hipGetLastError());
         GradArgs g{};
         g.live = live;
         g.cols = static_cast<int>(sh.cols);
-        g.dz_scale = dz_scale;
         if (a.grad_hidden) {
+            g.exponents = exponents;
             g.scale = scales + 1;
             g.a = ws + pl.head_t;
             g.a_ld = 2 * vp;
@@ -1756,6 +1813,7 @@ hipError_t launch_token_logp_backward(const muon_token_logp_backward_args& a, vo
             TL_TRY(launch_grad(g, pl.gh, reinterpret_cast<float*>(ws + pl.slab), sh.parts, a.dtype, true, s));
         }
         if (a.grad_head) {
+            g.exponents = least;
             g.scale = scales;
             g.a = ws + pl.hidden_t;
             g.a_ld = 2 * static_cast<size_t>(pl.chunk);

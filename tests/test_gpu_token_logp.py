@@ -425,7 +425,8 @@ def test_token_logp_gradient_of_certain_tokens(gpu_lib, dtype, t, use_saved):
 
 
 @pytest.mark.parametrize("t,v,dtype", [(20, 100, "bf16"), (20, 900, "bf16"), (100, 100, "bf16"), (300, 900, "bf16"),
-                                       (600, 17000, "bf16"), (20, 100, "f32"), (20, 900, "f32")])
+                                       (600, 17000, "bf16"), (20, 100, "f32"), (20, 900, "f32"), (100, 100, "f32"),
+                                       (300, 900, "f32"), (600, 17000, "f32")])
 @pytest.mark.parametrize("use_saved", [True, False])
 def test_token_logp_gradients_beside_a_certain_target(gpu_lib, dtype, t, v, use_saved):
     # The target stands 12 to 24 above entries of logits 0 .. -3 (exact arithmetic): column 0 of grad_hidden sums over the other
@@ -459,3 +460,19 @@ def test_token_logp_gradients_beside_a_certain_target(gpu_lib, dtype, t, v, use_
     ref = dz.sum(0)
     keep = np.arange(v) != 7
     assert np.all(np.abs(_np(gw)[:, 2] - ref)[keep] <= (tol + (t / 16) * U) * np.abs(ref)[keep])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("t,v", [(40, 500), (100, 500), (300, 2000)])
+@pytest.mark.parametrize("use_saved", [True, False])
+def test_token_logp_gradients_of_uneven_tokens(gpu_lib, dtype, t, v, use_saved):
+    # incoming gradients from 1 down to 1e-14, tokens from unsure to certain: the bounds are relative to each token's own c, so
+    # a token's row of grad_hidden may not lose bits beside the others
+    import torch
+    print("[token_logp uneven]", t, v, dtype, use_saved, flush=True)
+    h, w, y, _ = _inputs(51, t, 96, v, dtype, ignored=0.2, lift=15.0)
+    c = (torch.logspace(0, -14, t, dtype=torch.float64) * (1 - 2 * (torch.arange(t) % 2))).float().cuda()
+    saved = _saved(gpu_lib, h, w) if use_saved else None
+    logp, lse = _forward(gpu_lib, h, w, y, saved=saved)
+    _check_forward(h, w, y, 1.0, dtype, logp, lse)
+    _check_backward(h, w, y, c, 1.0, dtype, *_backward(gpu_lib, h, w, y, lse, c, saved=saved))
