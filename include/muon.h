@@ -335,17 +335,20 @@ muon_status muon_token_logp(const muon_token_logp_args* args, void* workspace, s
  * grad_hidden or grad_head may be NULL (not wanted), not both.  `saved` is what
  * muon_token_logp kept for the same inputs, or NULL: then the logits are formed
  * again, and lse with them (a rounded lse does not hold a certain token's
- * 1 - p; what the argument holds is not used).  dz is rounded to the
- * operands' precision before the two products: bf16 (up to 64 tokens: two bf16
- * parts, 2^-16), or 22 bits for fp32 (up to 64 tokens: 24).
+ * 1 - p; what the argument holds is not used).
  *
- * Precision in fp32: the products take each operand as two fp16 parts under one
- * power-of-two scale, 22 bits for values down to 2^-28 of the operand's largest
- * finite one, fewer below; dz has a scale for each token, so that a token's row of
- * grad_hidden keeps its bits beside tokens with larger gradients (in grad_head a
- * token counts with 22 bits down to 2^-28 of the largest).  Those of up to 64 tokens take three bf16 parts, 24
- * bits for values down to 2^-109; hidden is scaled for them first in a backward
- * pass and in a forward pass with `saved`. */
+ * Precision.  Up to 64 tokens: dz as two bf16 parts (2^-16) in bf16 calls; in fp32
+ * dz, hidden and head as three (24 bits for values down to 2^-109; hidden is scaled
+ * for them first in a backward pass and in a forward pass with `saved`).
+ * More tokens: dz as fp16 under a power-of-two scale for each token, in bf16 calls
+ * one part (11 bits), in fp32 calls two (22), and hidden and head, for the gradients'
+ * products, as one part (exact for bf16 values) or two under one scale each; all
+ * this for values down to 2^-28 of the operand's largest finite one (of the token's
+ * largest in dz; in grad_head a token counts so down to 2^-28 of the largest
+ * token), fewer bits below and none below 2^-39.  bf16 calls form dz from
+ * exp(z - M) in fp16, M the maximum of up to 256 neighbouring entries without the
+ * target: 11 bits down to 2^-14, none below 2^-25.  The logits' product takes
+ * bf16 operands as they are. */
 typedef struct {
     const void*    hidden;
     const void*    head;

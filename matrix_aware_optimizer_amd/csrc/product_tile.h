@@ -49,15 +49,16 @@ static __device__ const u32x4 zero_chunk = {};   // what a KTAIL product reads p
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6)); }
 __device__ __forceinline__ int swz(int row, int c) { return row * CHUNKS + (c ^ ((row >> 1) & 7)); }
 
-// Parts of the operands (bf16: the value itself; fp32: hi and lo, pitch a_part / b_part bytes) in the
+// Parts of the operands (one: the value itself; fp32: hi and lo, pitch a_part / b_part bytes) in the
 // order in which their products are summed, two bits a product.
 template <int PARTS> struct Order;
 template <> struct Order<1> { static constexpr int N = 1; static constexpr unsigned A = 0, B = 0; };
 template <> struct Order<2> { static constexpr int N = 3; static constexpr unsigned A = 1u, B = 1u << 2; };   // lo hi, hi lo, hi hi
 constexpr float LO_STEP = 1.0f / 2048.0f;   // what lo counts against hi
 
-template <int PARTS> __device__ __forceinline__ void mfma(f32x16_t& acc, const u32x4& a, const u32x4& b) {
-    if constexpr (PARTS == 1)
+// V: bf16x8_t or f16x8_t, what the operands hold.
+template <typename V> __device__ __forceinline__ void mfma(f32x16_t& acc, const u32x4& a, const u32x4& b) {
+    if constexpr (__is_same(V, bf16x8_t))
         acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), acc, 0, 0, 0);
     else
         acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), acc, 0, 0, 0);
@@ -119,13 +120,13 @@ template <int EDGE> struct Tile {
     // the rows.  srca[j], srcb[j]: this lane's row of load j, already moved to its chunk (load_row,
     // load_chunk).  steps >= 1.  KTAIL: the last step has `tail` chunks.  Ends with every LDS read
     // of this wave done; other waves may still read, so a barrier comes before the LDS is used again.
-    template <int PARTS, bool KTAIL>
+    template <typename V, int PARTS, bool KTAIL>
     static __device__ __attribute__((always_inline)) void run(const char* const (&srca)[HL], const char* const (&srcb)[HL],
                                                               size_t a_part, size_t b_part, size_t k0, int steps, int tail,
                                                               u32x4* lds, Acc& acc) {
-        static_assert(PARTS == 1 || !KTAIL, "parts are packed to whole steps");
+        static_assert(PARTS == 1 || (!KTAIL && __is_same(V, f16x8_t)), "two parts are fp16, packed to whole steps");
         if constexpr (EDGE == 128) {
-            run_deep<PARTS, KTAIL>(srca, srcb, a_part, b_part, k0, steps, tail, lds, acc);
+            run_deep<V, PARTS, KTAIL>(srca, srcb, a_part, b_part, k0, steps, tail, lds, acc);
             return;
         }
         const int lane = threadIdx.x & 63, wave = wave_id();
@@ -191,7 +192,7 @@ template <int EDGE> struct Tile {
                 for (int i = 0; i < SM; ++i) {
 #pragma unroll
                     for (int j = 0; j < SN; ++j)
-                        mfma<PARTS>(acc[i][j], fa[s & 1][i], fb[s & 1][j]);
+                        mfma<V>(acc[i][j], fa[s & 1][i], fb[s & 1][j]);
                     if (s + 1 < SUB) {
                         fa[(s + 1) & 1][i] = LA[swz(arow + i * 32, cn)];
                         if (i < SN) fb[(s + 1) & 1][i] = LB[swz(brow + i * 32, cn)];
@@ -213,7 +214,7 @@ template <int EDGE> struct Tile {
 
     // Tile<128>: both operands DEPTH steps ahead.  Step kt lives in slot kt % SLOTS of each operand's ring, and while it
     // is worked on the slots of step kt - 1 take step kt + DEPTH.
-    template <int PARTS, bool KTAIL>
+    template <typename V, int PARTS, bool KTAIL>
     static __device__ __attribute__((always_inline)) void run_deep(const char* const (&srca)[HL], const char* const (&srcb)[HL],
                                                                    size_t a_part, size_t b_part, size_t k0, int steps, int tail,
                                                                    u32x4* lds, Acc& out) {
@@ -289,7 +290,7 @@ template <int EDGE> struct Tile {
                     }
 #pragma unroll
                     for (int j = 0; j < SN; ++j)
-                        mfma<PARTS>(acc[i][j], fa[s & 1][i], fb[s & 1][j]);
+                        mfma<V>(acc[i][j], fa[s & 1][i], fb[s & 1][j]);
                     if (more) issue(kt + DEPTH, fill, s * BM + i);
                     __builtin_amdgcn_sched_barrier(0);
                 }

@@ -6,7 +6,7 @@
 // The work is the three products (2 tokens vocab cols operations each), bound by the matrix
 // cores; everything else is arranged around the 256 x 256 tile of product_tile.h:
 //
-//  - Only scored tokens are worked on: live_kernel lists them on the GPU, the products
+//  - Only scored tokens are worked on: scan_kernel lists them on the GPU, the products
 //    gather their rows of hidden, and workgroups beyond the list end at once.
 //  - Logits: C = head hidden^T, vocabulary along the accumulator rows, so that a lane holds 64
 //    logits of one token and the softmax's running maximum and sum need one exchange between
@@ -22,10 +22,13 @@
 //    once, so that both gradients are k-contiguous products (C rows = columns of the gradient,
 //    C columns = its rows).  Few tiles: the sum over k is split over workgroups that leave fp32
 //    tiles, added in order by slab_sum_kernel.
-//  - fp32 operands travel as two fp16 parts under a scale (product_tile.h): absmax_kernel finds the largest values, and the
-//    kernels that make the copies the scales.  So does dz in fp32 calls, under a scale for each token that its own largest entry
-//    gives, -c expm1(logp) of the target: a token's gradient keeps its bits beside tokens with larger ones.  grad_hidden takes
-//    the tokens' scales out of its columns; for grad_head they are taken out of hidden's copy before the product.
+//  - fp32 operands travel as two fp16 parts under a scale (product_tile.h): scan_kernel finds the largest values, and the
+//    kernels that make the copies the scales.  dz does so too, in bf16 calls in one part: 11 bits of it where bf16 would keep 8
+//    (6144 x 2048 x 32000, error of a gradient before its own rounding to bf16 in parts of its norm: 2e-4, in bf16 1.6e-3).  The
+//    matrix cores take one type, so the transposed copies of bf16 operands are fp16 under a scale as well, exact down to
+//    2^-29 of the operand's largest value; what that costs is a look through head for it.  dz has a scale for each token, that its own
+//    largest entry gives, -c expm1(logp) of the target: a token's gradient keeps its bits beside tokens with larger ones.
+//    grad_hidden takes the tokens' scales out of its columns; for grad_head they are taken out of hidden's copy before the product.
 //  - Few tokens: what counts is the head's way through memory, so each step reads (or writes) it once where it is,
 //    with 16 x 16 MFMAs and no staging (fp32 as three bf16 parts there: exact down to 2^-109, so that only hidden, which
 //    is small and quickly looked through, gets a scale).
@@ -36,6 +39,7 @@
 // stays out of M and the sum S of its token, logp = -log(1 + S 2^(M - k' acc_target)), which keeps its relative precision as
 // logp goes to 0.
 #include <algorithm>
+#include <type_traits>
 
 #include "product_tile.h"
 #include "train_internal.h"
@@ -72,10 +76,10 @@ __device__ __forceinline__ void split2(float x, uint16_t (&p)[2]) {
     p[0] = __builtin_bit_cast(uint16_t, hi);
     p[1] = __builtin_bit_cast(uint16_t, lo);
 }
-// A value as the 16-bit parts that the products take.
-template <int PARTS> __device__ __forceinline__ void to_parts(float x, float scale, uint16_t (&p)[2]) {
-    if constexpr (PARTS == 1) p[0] = f32_to_bf16(x);
-    else split2(x * scale, p);
+// A value, scaled, as the fp16 parts that the gradients' products take.
+template <int PARTS> __device__ __forceinline__ void half_parts(float x, uint16_t (&p)[2]) {
+    if constexpr (PARTS == 1) p[0] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(x));
+    else split2(x, p);
 }
 
 // k' of the comment above; scale 0 as a number so small that it makes no difference, so that k' times minus infinity stays so.
@@ -90,8 +94,7 @@ constexpr int LIVE_THREADS = 1024, LIVE_PER = 4;
 
 // idx[0 .. count): the tokens with a target >= 0.  logp and lse (forward) of the others are
 // set to 0.  One workgroup: 8 bytes a token, a few microseconds for 8192.
-__global__ __launch_bounds__(LIVE_THREADS) void live_kernel(const int64_t* targets, int64_t tokens, int32_t* idx,
-                                                            int32_t* count, float* logp, float* lse) {
+__device__ __forceinline__ void list_live(const int64_t* targets, int64_t tokens, int32_t* idx, int32_t* count, float* logp, float* lse) {
     __shared__ int sums[LIVE_THREADS / 64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     int base = 0;
@@ -136,17 +139,17 @@ struct Live {
 };
 
 // ---------------------------------------------------------------------------
-// Scales of fp32 operands
+// Scales of operands in fp16
 // ---------------------------------------------------------------------------
 
-// Bits of the largest finite |x| over some rows, one partial a workgroup: head_blocks of them for head, the others for the
-// scored rows of hidden.
-constexpr int ABS_HEAD = 1024, ABS_HIDDEN = 128;
+// Bits of the largest finite |x| over the rows of head and the scored rows of hidden, one partial a workgroup: the first
+// ABS_HEAD of them for head, the others for hidden.
+constexpr int ABS_HEAD = 512, ABS_HIDDEN = 128, ABS_ROWS = 4;   // ABS_ROWS: rows a wave has in flight
 struct AbsMaxArgs {
-    const float *head, *hidden;
+    const void *head, *hidden;
     size_t ld_head, ld_hidden;
-    int64_t vocab, cols;
-    Live live;
+    int64_t vocab, tokens, cols;
+    const int64_t* targets;   // or NULL: every row of hidden
     uint32_t* part;
 };
 __device__ __forceinline__ uint32_t block_max(uint32_t m, uint32_t* red) {
@@ -162,25 +165,73 @@ __device__ __forceinline__ uint32_t finite_bits(float x) {
     const uint32_t b = __float_as_uint(x) & 0x7fffffffu;
     return b < 0x7f800000u ? b : 0u;
 }
-__global__ __launch_bounds__(256) void absmax_kernel(AbsMaxArgs a) {
-    __shared__ uint32_t red[4];
-    const int block = blockIdx.x + (gridDim.x == ABS_HIDDEN ? ABS_HEAD : 0);   // a launch for hidden alone
+// The largest magnitude of a run so far, as bits (bf16: of two values a word), infinities and NaN included.
+__device__ __forceinline__ uint32_t largest_bits(const Run<uint16_t>& x, uint32_t m) {
+    typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        m = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, m), __builtin_bit_cast(u16x2_t, x.w[e] & 0x7fff7fffu)));
+    return m;
+}
+__device__ __forceinline__ uint32_t largest_bits(const Run<float>& x, uint32_t m) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(x.get(e)) & 0x7fffffffu);
+    return m;
+}
+template <typename T> __device__ __forceinline__ void find_absmax(const AbsMaxArgs& a, int block, uint32_t* red) {
     const bool head = block < ABS_HEAD;
     const int b = head ? block : block - ABS_HEAD, blocks = head ? ABS_HEAD : ABS_HIDDEN;
-    const int64_t rows = head ? a.vocab : a.live.idx ? a.live.rows() : a.live.most, runs = (a.cols + 7) / 8;
+    const int waves = blockDim.x >> 6, wave = pt::wave_id();
+    const int64_t rows = head ? a.vocab : a.tokens, runs = (a.cols + 7) / 8;
+    const size_t ld = head ? a.ld_head : a.ld_hidden;
+    const auto* base = G(static_cast<const T*>(head ? a.head : a.hidden));
+    // rows from `wave` on, f(run) on each run of 8 columns of those that count
+    auto over = [&](auto f) {
+        for (int64_t r = ABS_ROWS * (static_cast<int64_t>(waves) * b + wave); r < rows; r += ABS_ROWS * static_cast<int64_t>(waves) * blocks) {
+            bool on[ABS_ROWS];
+#pragma unroll
+            for (int i = 0; i < ABS_ROWS; ++i) on[i] = r + i < rows && (head || !a.targets || a.targets[r + i] >= 0);
+            for (int64_t k = threadIdx.x & 63; k < runs; k += 64) {
+                Run<T> x[ABS_ROWS];
+#pragma unroll
+                for (int i = 0; i < ABS_ROWS; ++i) {
+                    if (!on[i]) continue;
+                    const auto* q = base + static_cast<size_t>(r + i) * ld;
+                    if (8 * k + 8 <= a.cols) x[i].load(q, static_cast<unsigned>(8 * k));
+                    else x[i].load(q, static_cast<unsigned>(8 * k), static_cast<unsigned>(a.cols - 8 * k));
+                }
+#pragma unroll
+                for (int i = 0; i < ABS_ROWS; ++i) f(x[i]);
+            }
+        }
+    };
     uint32_t m = 0;
-    for (int64_t r = 4 * b + static_cast<int>(threadIdx.x >> 6); r < rows; r += 4 * blocks) {
-        const auto* q = G(head ? a.head + static_cast<size_t>(r) * a.ld_head : a.hidden + static_cast<size_t>(a.live.idx ? a.live.idx[a.live.first + r] : r) * a.ld_hidden);
-        for (int64_t k = threadIdx.x & 63; k < runs; k += 64) {
-            Run<float> x;
-            if (8 * k + 8 <= a.cols) x.load(q, static_cast<unsigned>(8 * k));
-            else x.load(q, static_cast<unsigned>(8 * k), static_cast<unsigned>(a.cols - 8 * k));
+    over([&](const Run<T>& x) { m = largest_bits(x, m); });
+    if constexpr (sizeof(T) == 2) m = max(m << 16, m & 0xffff0000u);
+    if (__any(m >= 0x7f800000u)) {   // not finite: again, with a look at each value
+        m = 0;
+        over([&](const Run<T>& x) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) m = max(m, finite_bits(x.get(e)));
-        }
+        });
     }
     m = block_max(m, red);
     if (threadIdx.x == 0) a.part[block] = m;
+}
+// What the products wait for, side by side: the list (the first workgroup, if wanted) and the largest values.
+struct ScanArgs {
+    int list;               // 1: with the list
+    const int64_t* targets;
+    int64_t tokens;
+    int32_t *idx, *count;
+    float *logp, *lse;
+    int first, blocks;      // workgroups for the largest values, from `first` on (ABS_HEAD: hidden alone)
+    AbsMaxArgs absmax;
+};
+template <typename T> __global__ __launch_bounds__(LIVE_THREADS) void scan_kernel(ScanArgs a) {
+    __shared__ uint32_t red[LIVE_THREADS / 64];
+    if (a.list && blockIdx.x == 0) list_live(a.targets, a.tokens, a.idx, a.count, a.logp, a.lse);
+    else find_absmax<T>(a.absmax, a.first + static_cast<int>(blockIdx.x) - a.list, red);
 }
 // The power of two that brings the largest value to 2^14 .. 2^15.
 __device__ __forceinline__ float scale_of(uint32_t bits) {
@@ -189,7 +240,7 @@ __device__ __forceinline__ float scale_of(uint32_t bits) {
     return __uint_as_float(static_cast<uint32_t>(s + 127) << 23);
 }
 __device__ __forceinline__ int exponent_of(float scale) { return static_cast<int>(__float_as_uint(scale) >> 23) - 127; }
-// An operand's scale from absmax_kernel's partials, by a workgroup that is about to use it.
+// An operand's scale from scan_kernel's partials, by a workgroup that is about to use it.
 __device__ __forceinline__ float operand_scale(const uint32_t* part, bool head, uint32_t* red) {
     const int first = head ? 0 : ABS_HEAD, n = head ? ABS_HEAD : ABS_HIDDEN;
     uint32_t m = 0;
@@ -221,7 +272,7 @@ struct DzTokenArgs {
     const float *logp, *grad_logp;   // logp: by list entry
     float scale;
     int vocab;
-    const int32_t* least;            // two parts: dz_scale's
+    const int32_t* least;            // dz_scale's
 };
 struct DzToken {
     int64_t target;
@@ -252,7 +303,7 @@ struct PackArgs {
     Live live;
     uint16_t* dst;
     size_t dst_ld, part;   // elements
-    const float* scale;    // transposes: the operand's scale (two parts)
+    const float* scale;    // transposes: the operand's scale
 };
 
 // Copies for the logits' product, dst[part][r][0 .. dst_ld) = parts of src[row r], zero past its columns: of head (the first
@@ -260,7 +311,7 @@ struct PackArgs {
 struct PackBothArgs {
     PackArgs head, hidden;
     int head_blocks, hidden_blocks;
-    const uint32_t* absmax;   // two parts: absmax_kernel's partials
+    const uint32_t* absmax;   // two parts: scan_kernel's partials
     float* scales;            // and where the scales of hidden and head are left
 };
 template <typename T, int PARTS>
@@ -285,7 +336,10 @@ __global__ __launch_bounds__(256) void pack_kernel(PackBothArgs both) {
         if (c + 8 <= a.cols) x.load(q8, 0);
         else if (c < a.cols) x.load(q8, 0, static_cast<unsigned>(a.cols - c));
 #pragma unroll
-        for (int e = 0; e < 8; ++e) to_parts<PARTS>(x.get(e), scale, v[e]);
+        for (int e = 0; e < 8; ++e) {
+            if constexpr (PARTS == 1) v[e][0] = f32_to_bf16(x.get(e));
+            else split2(x.get(e) * scale, v[e]);
+        }
 #pragma unroll
         for (int p = 0; p < PARTS; ++p) {
             u32x4 w;
@@ -296,10 +350,10 @@ __global__ __launch_bounds__(256) void pack_kernel(PackBothArgs both) {
     }
 }
 
-// dst[part][c][r] = parts of src[row r][c] for c < cols, zero for rows past the last up to a multiple of 64: the
+// dst[part][c][r] = fp16 parts of src[row r][c] for c < cols, zero for rows past the last up to a multiple of 64: the
 // 64 x 64 tile at (r0, c0), through LDS as fp32, 16-byte accesses on both sides.
 template <typename T, int PARTS> __device__ __forceinline__ void transpose_tile(const PackArgs& a, int64_t r0, int64_t c0, float (&tile)[64][65]) {
-    const float scale = PARTS == 1 ? 1.0f : *a.scale;
+    const float scale = *a.scale;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         const int k = (threadIdx.x >> 3) + 32 * half, x = 8 * (threadIdx.x & 7);
@@ -320,7 +374,7 @@ template <typename T, int PARTS> __device__ __forceinline__ void transpose_tile(
         if (c0 + c >= a.cols) continue;
         uint16_t v[8][2];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) to_parts<PARTS>(tile[r + e][c], scale, v[e]);
+        for (int e = 0; e < 8; ++e) half_parts<PARTS>(tile[r + e][c] * scale, v[e]);
 #pragma unroll
         for (int p = 0; p < PARTS; ++p) {
             u32x4 w;
@@ -331,7 +385,7 @@ template <typename T, int PARTS> __device__ __forceinline__ void transpose_tile(
     }
 }
 
-// One launch for what comes before dz: the transpose of head, the least scale of dz (two parts) and, for grad_hidden, zeros in
+// One launch for what comes before dz: the transpose of head, the least scale of dz and, for grad_hidden, zeros in
 // the rows of tokens that are not scored.  Each is a run of workgroups.
 struct PrepareArgs {
     PackArgs head;
@@ -347,16 +401,16 @@ struct PrepareArgs {
 template <typename T, int PARTS> __global__ __launch_bounds__(256) void prepare_kernel(PrepareArgs a) {
     __shared__ float tile[64][65];
     int b = blockIdx.x;
+    if (a.dz.out && b-- == 0) {   // first: it takes the longest
+        dz_scale(a.dz, reinterpret_cast<uint32_t*>(tile));
+        return;
+    }
     if (b < a.head_blocks) {
         if (a.live.rows() == 0) return;   // nothing will read it
         transpose_tile<T, PARTS>(a.head, static_cast<int64_t>(b % a.head_rows) * 64, static_cast<int64_t>(b / a.head_rows) * 64, tile);
         return;
     }
     b -= a.head_blocks;
-    if (PARTS == 2 && a.dz.out && b-- == 0) {
-        dz_scale(a.dz, reinterpret_cast<uint32_t*>(tile));
-        return;
-    }
     for (int64_t t = static_cast<int64_t>(b) * 4 + (threadIdx.x >> 6); t < a.tokens; t += 4 * static_cast<int64_t>(a.zero_blocks))
         if (a.targets[t] < 0)
             for (int64_t c = threadIdx.x & 63; c < a.cols; c += 64) st_el<T>(a.zero, t * a.zero_ld + c, 0.0f);
@@ -421,7 +475,8 @@ __global__ __launch_bounds__(pt::Tile<EDGE>::THREADS, 2) void logits_kernel(Logi
         sb[j] = a.b + static_cast<size_t>(r) * a.b_ld + TL::load_chunk(j) * 16;
     }
     typename TL::Acc acc = {};
-    TL::template run<PARTS, KTAIL>(sa, sb, a.a_part, a.b_part, 0, a.steps, a.tail, lds, acc);
+    typedef std::conditional_t<PARTS == 1, pt::bf16x8_t, pt::f16x8_t> Of;
+    TL::template run<Of, PARTS, KTAIL>(sa, sb, a.a_part, a.b_part, 0, a.steps, a.tail, lds, acc);
 
     const int place = TL::stack_place(), h = (threadIdx.x >> 5) & 1;
     const int vl = v0 + TL::first_row();              // this lane's first vocabulary entry
@@ -554,7 +609,7 @@ struct DzArgs {
     size_t vp, rows_pitch;
     uint16_t *dz, *dzt;     // rows relative to live.first
     size_t dz_part, dzt_part;
-    int32_t* exponents;     // two parts: of the tokens' scales, by row of dz
+    int32_t* exponents;     // of the tokens' scales, by row of dz
     PackArgs hidden;        // the transpose of hidden for grad_head, by workgroups past the vocabulary's
 };
 
@@ -595,32 +650,26 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
     for (int half = 0; half < 2; ++half) {
         const int rt = (threadIdx.x >> 3) + 32 * half, r = r0 + rt;
         uint16_t v[8][2];
-        int exponent = 0;
-        if constexpr (PARTS == 2) exponent = t[half].exponent(a.tok);
+        const int exponent = t[half].exponent(a.tok);
         if (past >= 0) {   // hidden under its scale, times the least of dz over the token's own: at most 1
-            const int up = PARTS == 2 ? exponent_of(*a.hidden.scale) + *a.tok.least - exponent : 0;
+            const int up = exponent_of(*a.hidden.scale) + *a.tok.least - exponent;
             const int64_t left = r < n ? a.hidden.cols - c0 - 8 * vb : 0;
             const auto* q = G(static_cast<const E*>(a.hidden.src) + static_cast<size_t>(tok[half]) * a.hidden.ld + c0);
             if (left >= 8) x[half].load(q, 8 * vb);
             else if (left > 0) x[half].load(q, 8 * vb, static_cast<unsigned>(left));
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const float h = x[half].get(q);
-                to_parts<PARTS>(PARTS == 2 ? __builtin_amdgcn_ldexpf(h, up) : h, 1.0f, v[q]);
-            }
+            for (int q = 0; q < 8; ++q) half_parts<PARTS>(__builtin_amdgcn_ldexpf(x[half].get(q), up), v[q]);
         } else {
             const int y = t[half].valid(a.tok) ? static_cast<int>(t[half].target) - v0 - 8 * vb : -1;
             const float c = t[half].c;
-            float f = c * __builtin_amdgcn_exp2f(fmaf(-ref[half], k, m[half]) + shift[half]), dy = t[half].dy();
-            if constexpr (PARTS == 2) {   // under the token's scale
-                f = __builtin_amdgcn_ldexpf(f, exponent);
-                dy = __builtin_amdgcn_ldexpf(dy, exponent);
-                if (v0 == 0 && vb == 0 && r < n) a.exponents[r] = exponent;
-            }
+            // under the token's scale
+            const float f = __builtin_amdgcn_ldexpf(c * __builtin_amdgcn_exp2f(fmaf(-ref[half], k, m[half]) + shift[half]), exponent);
+            const float dy = __builtin_amdgcn_ldexpf(t[half].dy(), exponent);
+            if (v0 == 0 && vb == 0 && r < n) a.exponents[r] = exponent;
             const bool none = r >= n || c == 0.0f;
 #pragma unroll
             for (int q = 0; q < 8; ++q)
-                to_parts<PARTS>(none || v0 + 8 * vb + q >= a.tok.vocab ? 0.0f : q == y ? dy : -e_of(x[half], q) * f, 1.0f, v[q]);
+                half_parts<PARTS>(none || v0 + 8 * vb + q >= a.tok.vocab ? 0.0f : q == y ? dy : -e_of(x[half], q) * f, v[q]);
         }
 #pragma unroll
         for (int p = 0; p < PARTS; ++p) {
@@ -670,8 +719,8 @@ struct GradArgs {
     size_t ld;
     float* slab;            // fp32 tiles in accumulator layout, [split][tile][quads][threads] x 16 bytes, or NULL: write out
     int add;                // add to what the slab holds (later chunks of tokens)
-    const float* scale;              // two parts: of the transposed operand
-    const int32_t* exponents;        // and of dz: by row (by_token), or the least
+    const float* scale;              // of the transposed operand
+    const int32_t* exponents;        // of dz's scales: by row (by_token), or the least
 };
 
 // A whole 16-byte piece of the output at any element alignment, or the first `left` of its elements.
@@ -721,15 +770,13 @@ __global__ __launch_bounds__(pt::Tile<EDGE>::THREADS, 2) void grad_kernel(GradAr
             sa[j] = a.a + static_cast<size_t>(min(c0 + row, a.cols - 1)) * a.a_ld + TL::load_chunk(j) * 16;
             sb[j] = a.b + static_cast<size_t>(r0 + row) * a.b_ld + TL::load_chunk(j) * 16;   // padded to the tile
         }
-        TL::template run<PARTS, false>(sa, sb, a.a_part, a.b_part, static_cast<size_t>(k_first) * (pt::KS * 2), steps, 0, lds, acc);
+        TL::template run<pt::f16x8_t, PARTS, false>(sa, sb, a.a_part, a.b_part, static_cast<size_t>(k_first) * (pt::KS * 2), steps, 0, lds, acc);
     }
-    if constexpr (PARTS == 2) {
-        const int up = exponent_of(*a.scale);
-        int e[TL::SN];
+    const int up = exponent_of(*a.scale);
+    int down[TL::SN];
 #pragma unroll
-        for (int j = 0; j < TL::SN; ++j) e[j] = -up - a.exponents[a.by_token ? min(r0 + TL::column(j), n - 1) : 0];
-        pt::unscale<TL>(acc, e);
-    }
+    for (int j = 0; j < TL::SN; ++j) down[j] = -up - a.exponents[a.by_token ? min(r0 + TL::column(j), n - 1) : 0];
+    pt::unscale<TL>(acc, down);
     if (a.slab) {
         float* s = a.slab + (static_cast<size_t>(split) * a.ta * a.tb + tile) * (EDGE * EDGE) + threadIdx.x * 4;
 #pragma unroll
@@ -868,7 +915,7 @@ struct FewArgs {
     float *m, *s, *zt;      // M and S: token x tile; target's acc by token
     void* e;                // 2^(k' acc - M), token x vocabulary (pitch vp), fp16 in bf16 calls, else fp32; or NULL
     size_t vp;
-    const uint32_t* absmax; // fp32: absmax_kernel's partials for hidden, or NULL: hidden as it is
+    const uint32_t* absmax; // fp32: scan_kernel's partials for hidden, or NULL: hidden as it is
 };
 
 // FEW_ROWS entries x up to 16 NT tokens a workgroup; its four waves take 64 values of k in turn.  Vocabulary
@@ -994,7 +1041,7 @@ struct FewGradArgs {
     float* slab;                       // [split][strip][j][4 registers of every 16 tokens][lane]
     void *grad_hidden, *grad_head;     // or NULL
     size_t ld_grad_hidden, ld_grad_head;
-    const uint32_t* absmax;            // fp32: absmax_kernel's partials for hidden
+    const uint32_t* absmax;            // fp32: scan_kernel's partials for hidden
 };
 
 // What dz of a token takes.
@@ -1253,6 +1300,8 @@ struct CombineArgs {
     int64_t tokens;
     float scale2;
     float *kept_logp, *kept_ref, *kept_shift;   // by list entry, for the backward pass (DzArgs), or NULL
+    const uint32_t* absmax;       // scan_kernel's partials, or NULL: the scales of hidden and head are known or not needed
+    float* scales;
 };
 
 // 2^(a - b) for a <= b, with equal infinities taken as equal
@@ -1265,6 +1314,14 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
     __shared__ float sm[NP][TOK], ss[NP][TOK];
     const int tk = threadIdx.x % TOK, part = threadIdx.x / TOK;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * TOK + tk;
+    if (a.absmax && blockIdx.x == 0) {
+        uint32_t* red = reinterpret_cast<uint32_t*>(&sm[0][0]);
+        const float hidden = operand_scale(a.absmax, false, red), head = operand_scale(a.absmax, true, red);
+        if (threadIdx.x == 0) {
+            a.scales[0] = hidden;
+            a.scales[1] = head;
+        }
+    }
     const int64_t n = a.live.idx ? a.live.rows() : a.tokens;
     const float k = rate_of(a.scale2);
     float m = -INFINITY, s = 0.0f;
@@ -1399,7 +1456,7 @@ struct ForwardPlan {
         m = b.take(a.saved ? 0 : stats * sizeof(float));
         s = b.take(stats * sizeof(float));
         zt = b.take(sizeof(float) * sh.tp);
-        absmax = b.take(sh.parts == 1 ? 0 : sizeof(uint32_t) * (ABS_HEAD + ABS_HIDDEN));
+        absmax = b.take(sh.parts == 2 || (a.saved && !few) ? sizeof(uint32_t) * (ABS_HEAD + ABS_HIDDEN) : 0);
         scales = b.take(few || sh.parts == 1 ? 0 : 2 * sizeof(float));
         bytes = b.at;
     }
@@ -1486,9 +1543,9 @@ struct BackwardPlan {
         // the slab of grad_head lives through the chunks, so the two do not share one
         slab = b.take(a.grad_hidden ? gh.slab_bytes() : 0);
         slab_w = b.take(a.grad_head ? gw.slab_bytes() : 0);
-        absmax = b.take(sh.parts == 1 ? 0 : sizeof(uint32_t) * (ABS_HEAD + ABS_HIDDEN));
-        scales = b.take(sh.parts == 1 ? 0 : 3 * sizeof(float));
-        exponents = b.take(sh.parts == 1 ? 0 : sizeof(int32_t) * chunk);
+        absmax = b.take(a.saved ? 0 : sizeof(uint32_t) * (ABS_HEAD + ABS_HIDDEN));
+        scales = b.take(3 * sizeof(float));
+        exponents = b.take(sizeof(int32_t) * chunk);
         const size_t by_chunk = a.saved ? 0 : static_cast<size_t>(chunk), by_entry = a.saved ? 0 : sizeof(float) * sh.tp;
         e = b.take(el * by_chunk * sh.vp);
         m = b.take(sizeof(float) * by_chunk * sh.ta());
@@ -1504,9 +1561,21 @@ struct BackwardPlan {
 bool few_backward(const muon_token_logp_backward_args& a) { return a.tokens <= FEW_TOKENS; }
 Shape shape_of(const muon_token_logp_args& a) { return Shape(a.tokens, a.cols, a.vocab, a.dtype, a.hidden, a.ld_hidden, a.head, a.ld_head); }
 
-hipError_t launch_live(const int64_t* targets, int64_t tokens, int32_t* idx, int32_t* count, float* logp, float* lse,
-                       hipStream_t s) {
-    hipLaunchKernelGGL(live_kernel, dim3(1), dim3(LIVE_THREADS), 0, s, targets, tokens, idx, count, logp, lse);
+// The list of scored tokens and, with `part`, the largest values of both operands.
+hipError_t launch_scan(int dtype, const void* hidden, int64_t ld_hidden, const void* head, int64_t ld_head, const Shape& sh,
+                       const int64_t* targets, int32_t* idx, int32_t* count, float* logp, float* lse, uint32_t* part, hipStream_t s) {
+    const ScanArgs a{1, targets, sh.tokens, idx, count, logp, lse, 0, part ? ABS_HEAD + ABS_HIDDEN : 0,
+                     {head, hidden, static_cast<size_t>(ld_head), static_cast<size_t>(ld_hidden), sh.vocab, sh.tokens, sh.cols, targets, part}};
+    if (dtype == MUON_BF16) hipLaunchKernelGGL(scan_kernel<uint16_t>, dim3(1 + a.blocks), dim3(LIVE_THREADS), 0, s, a);
+    else hipLaunchKernelGGL(scan_kernel<float>, dim3(1 + a.blocks), dim3(LIVE_THREADS), 0, s, a);
+    return hipGetLastError();
+}
+
+// The largest value of hidden alone, over every row of it (few tokens).
+hipError_t launch_hidden_absmax(const void* hidden, int64_t ld_hidden, const Shape& sh, uint32_t* part, hipStream_t s) {
+    const ScanArgs a{0, nullptr, 0, nullptr, nullptr, nullptr, nullptr, ABS_HEAD, ABS_HIDDEN,
+                     {nullptr, hidden, 0, static_cast<size_t>(ld_hidden), 0, sh.tokens, sh.cols, nullptr, part}};
+    hipLaunchKernelGGL(scan_kernel<float>, dim3(a.blocks), dim3(LIVE_THREADS), 0, s, a);
     return hipGetLastError();
 }
 
@@ -1537,22 +1606,6 @@ hipError_t launch_grad(GradArgs g, const GradPlan& pl, float* slab, int parts, i
     g.splits = pl.splits;
     g.slab = pl.slab ? slab : nullptr;
     return pl.edge == 256 ? launch_grad_edge<256>(g, parts, dtype, last, s) : launch_grad_edge<128>(g, parts, dtype, last, s);
-}
-
-hipError_t launch_absmax(const void* hidden, int64_t ld_hidden, const void* head, int64_t ld_head, const Shape& sh, const Live& live,
-                         uint32_t* part, hipStream_t s) {
-    const AbsMaxArgs m{static_cast<const float*>(head), static_cast<const float*>(hidden), static_cast<size_t>(ld_head),
-                       static_cast<size_t>(ld_hidden), sh.vocab, sh.cols, live, part};
-    hipLaunchKernelGGL(absmax_kernel, dim3(ABS_HEAD + ABS_HIDDEN), dim3(256), 0, s, m);
-    return hipGetLastError();
-}
-
-// That of hidden alone, every row of it (few tokens).
-hipError_t launch_hidden_absmax(const void* hidden, int64_t ld_hidden, const Shape& sh, uint32_t* part, hipStream_t s) {
-    const AbsMaxArgs m{nullptr, static_cast<const float*>(hidden), 0, static_cast<size_t>(ld_hidden), 0, sh.cols,
-                       {nullptr, nullptr, 0, static_cast<int32_t>(sh.tokens)}, part};
-    hipLaunchKernelGGL(absmax_kernel, dim3(ABS_HIDDEN), dim3(256), 0, s, m);
-    return hipGetLastError();
 }
 
 // The logits' operands: packed copies where the products cannot read the caller's rows.  absmax: two parts.
@@ -1604,7 +1657,7 @@ template <typename T, int PARTS> hipError_t launch_few(const muon_token_logp_arg
     else hipLaunchKernelGGL((few_kernel<T, PARTS, 4>), grid, dim3(256), 0, s, f);
     TL_TRY(hipGetLastError());
     const CombineArgs c{f.m, f.s, f.zt, 1, static_cast<size_t>(sh.few_tiles), sh.few_tiles, a.targets, a.vocab, a.logp, a.lse,
-                        {}, a.tokens, f.scale2, kept(sv.logp), kept(sv.ref), kept(sv.shift)};
+                        {}, a.tokens, f.scale2, kept(sv.logp), kept(sv.ref), kept(sv.shift), nullptr, nullptr};
     hipLaunchKernelGGL(combine_kernel<1>, dim3(static_cast<unsigned>(a.tokens)), dim3(256), 0, s, c);
     return hipGetLastError();
 }
@@ -1677,11 +1730,10 @@ hipError_t launch_token_logp(const muon_token_logp_args& a, void* workspace, hip
         idx = reinterpret_cast<int32_t*>(p + sv.idx);
         count = reinterpret_cast<int32_t*>(p + sv.count);
     }
-    TL_TRY(launch_live(a.targets, a.tokens, idx, count, a.logp, a.lse, s));
+    uint32_t* absmax = sh.parts == 2 || a.saved ? reinterpret_cast<uint32_t*>(ws + pl.absmax) : nullptr;
+    TL_TRY(launch_scan(a.dtype, a.hidden, a.ld_hidden, a.head, a.ld_head, sh, a.targets, idx, count, a.logp, a.lse, absmax, s));
     l.live = {idx, count, 0, static_cast<int32_t>(sh.tp)};
-    uint32_t* absmax = reinterpret_cast<uint32_t*>(ws + pl.absmax);
     float* scales = reinterpret_cast<float*>(a.saved ? static_cast<char*>(a.saved) + SavedPlan(sh).scales : ws + pl.scales);
-    if (sh.parts == 2) TL_TRY(launch_absmax(a.hidden, a.ld_hidden, a.head, a.ld_head, sh, l.live, absmax, s));
     TL_TRY(logits_operands(sh, a.hidden, a.ld_hidden, a.head, a.ld_head, a.dtype, ws + pl.hidden, ws + pl.head, true, absmax, scales, l, s));
     l.targets = a.targets;
     l.tb = static_cast<int>(sh.tp / sh.edge);
@@ -1693,7 +1745,7 @@ hipError_t launch_token_logp(const muon_token_logp_args& a, void* workspace, hip
     l.vp = sh.vp;
     TL_TRY(a.saved ? launch_logits<LG_SAVE>(l, sh.edge, sh.parts, s) : launch_logits<LG_STATS>(l, sh.edge, sh.parts, s));
     const CombineArgs c{m, sums, zt, static_cast<size_t>(sh.tp), 1, sh.ta(), a.targets, a.vocab, a.logp, a.lse, l.live, a.tokens,
-                        scale2, kept_logp, kept_ref, kept_shift};
+                        scale2, kept_logp, kept_ref, kept_shift, sh.parts == 1 ? absmax : nullptr, scales};
     hipLaunchKernelGGL(combine_kernel<32>, dim3(static_cast<unsigned>(sh.tp / 32)), dim3(256), 0, s, c);
     return hipGetLastError();
 }
@@ -1726,14 +1778,15 @@ hipError_t launch_token_logp_backward(const muon_token_logp_backward_args& a, vo
     const char* saved = static_cast<const char*>(a.saved);
     const int32_t* idx = reinterpret_cast<const int32_t*>(saved ? saved + sv.idx : ws + pl.idx);
     const int32_t* count = reinterpret_cast<const int32_t*>(saved ? saved + sv.count : ws + pl.count);
-    if (!saved) TL_TRY(launch_live(a.targets, a.tokens, const_cast<int32_t*>(idx), const_cast<int32_t*>(count), nullptr, nullptr, s));
     // scales of hidden and head: as the forward pass left them, or found again; the least of dz: over all tokens, since chunks add up
     float* own = reinterpret_cast<float*>(ws + pl.scales);
     uint32_t* absmax = reinterpret_cast<uint32_t*>(ws + pl.absmax);
     const float* scales = saved ? reinterpret_cast<const float*>(saved + sv.scales) : own;
     int32_t* least = reinterpret_cast<int32_t*>(own + 2);
     const Live everyone{idx, count, 0, static_cast<int32_t>(sh.tp)};
-    if (sh.parts == 2 && !saved) TL_TRY(launch_absmax(a.hidden, a.ld_hidden, a.head, a.ld_head, sh, everyone, absmax, s));
+    if (!saved)
+        TL_TRY(launch_scan(a.dtype, a.hidden, a.ld_hidden, a.head, a.ld_head, sh, a.targets, const_cast<int32_t*>(idx),
+                           const_cast<int32_t*>(count), nullptr, nullptr, absmax, s));
     const size_t vp = sh.vp, dz_part = static_cast<size_t>(pl.chunk) * vp;
     auto at = [&](size_t o) { return reinterpret_cast<float*>(ws + o); };
     uint16_t* dz = a.grad_hidden ? reinterpret_cast<uint16_t*>(ws + pl.dz) : nullptr;
@@ -1755,13 +1808,13 @@ hipError_t launch_token_logp_backward(const muon_token_logp_backward_args& a, vo
             l.vp = vp;
             TL_TRY(launch_logits<LG_SAVE>(l, sh.edge, sh.parts, s));
             const CombineArgs f{l.m, l.s, l.zt, static_cast<size_t>(pl.chunk), 1, sh.ta(), a.targets, a.vocab, nullptr, nullptr, live,
-                                a.tokens, l.scale2, at(pl.logp), at(pl.ref), at(pl.shift)};
+                                a.tokens, l.scale2, at(pl.logp), at(pl.ref), at(pl.shift), sh.parts == 1 ? absmax : nullptr, own};
             hipLaunchKernelGGL(combine_kernel<32>, dim3(static_cast<unsigned>(pl.chunk / 32)), dim3(256), 0, s, f);
             TL_TRY(hipGetLastError());
         }
         PrepareArgs p{};
         p.live = live;
-        if (sh.parts == 2 && c == 0) p.dz = {everyone, a.grad_logp, a.scale, least};
+        if (c == 0) p.dz = {everyone, a.grad_logp, a.scale, least};
         const int col_tiles = static_cast<int>(ceil_div(sh.cols, 64));
         if (a.grad_hidden && c == 0) {
             p.head = {a.head, static_cast<size_t>(a.ld_head), sh.vocab, sh.cols, 0, live, reinterpret_cast<uint16_t*>(ws + pl.head_t),
@@ -1784,8 +1837,7 @@ hipError_t launch_token_logp_backward(const muon_token_logp_backward_args& a, vo
         auto kept = [&](size_t o, size_t without) { return reinterpret_cast<const float*>(saved ? saved + o : ws + without); };
         const PackArgs hidden_t{a.hidden, static_cast<size_t>(a.ld_hidden), pl.chunk, sh.cols, 1, live, reinterpret_cast<uint16_t*>(ws + pl.hidden_t),
                                 static_cast<size_t>(pl.chunk), static_cast<size_t>(pl.chunk) * sh.cols, scales};
-        const DzTokenArgs tok{live, a.targets, kept(sv.logp, pl.logp), a.grad_logp, a.scale, static_cast<int>(a.vocab),
-                              sh.parts == 2 ? least : nullptr};
+        const DzTokenArgs tok{live, a.targets, kept(sv.logp, pl.logp), a.grad_logp, a.scale, static_cast<int>(a.vocab), least};
         int32_t* exponents = reinterpret_cast<int32_t*>(ws + pl.exponents);
         const DzArgs d{kept(sv.e, pl.e), kept(sv.m, pl.m), saved ? 0 : live.first, kept(sv.ref, pl.ref), kept(sv.shift, pl.shift),
                        a.scale * LOG2E, static_cast<size_t>(saved ? sh.tp : pl.chunk), sh.edge, tok, vp, static_cast<size_t>(pl.chunk),

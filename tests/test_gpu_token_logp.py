@@ -476,3 +476,24 @@ def test_token_logp_gradients_of_uneven_tokens(gpu_lib, dtype, t, v, use_saved):
     logp, lse = _forward(gpu_lib, h, w, y, saved=saved)
     _check_forward(h, w, y, 1.0, dtype, logp, lse)
     _check_backward(h, w, y, c, 1.0, dtype, *_backward(gpu_lib, h, w, y, lse, c, saved=saved))
+
+
+@pytest.mark.parametrize("t,d,v", [(65, 200, 1025), (300, 256, 3000), (1030, 192, 700), (600, 72, 20000)])
+@pytest.mark.parametrize("use_saved", [True, False])
+def test_token_logp_bf16_gradients_cost_little_more_than_their_rounding(gpu_lib, t, d, v, use_saved):
+    # dz and exp(z - m) carry 11 bits: each entry of dz is off by at most 2^-12 + 2^-12 of itself, so the gradients, as sums of
+    # independent errors, by less than 2^-11 of the root of the sum of their terms' squares (twice that square here, for
+    # chance), beside the rounding of the output (its square within 10 %).  With 8 bits in dz the squares come to twice that.
+    import torch
+    print("[token_logp bits]", t, d, v, use_saved, flush=True)
+    h, w, y, c = _inputs(61, t, d, v, "bf16")
+    saved = _saved(gpu_lib, h, w) if use_saved else None
+    _, lse = _forward(gpu_lib, h, w, y, saved=saved)
+    gh, gw = _backward(gpu_lib, h, w, y, lse, c, saved=saved)
+    hv, wv, yv = _np(h), _np(w), np.asarray(y.cpu())
+    rh, rw, dz, _ = to.token_logp_backward(hv, wv, yv, _np(c))
+    hv = np.where((yv >= 0)[:, None], hv, 0.0)
+    for got, ref, terms in ((gh, rh, (dz ** 2) @ (wv ** 2)), (gw, rw, (dz ** 2).T @ (hv ** 2))):
+        rounded = _np(torch.from_numpy(ref).to(torch.bfloat16))
+        most = 1.1 * ((rounded - ref) ** 2).sum() + 2 * 2.0 ** -22 * terms.sum()
+        assert ((_np(got) - ref) ** 2).sum() <= most, float(((_np(got) - ref) ** 2).sum() / most)
