@@ -149,7 +149,7 @@ struct AbsMaxArgs {
     const void *head, *hidden;
     size_t ld_head, ld_hidden;
     int64_t vocab, tokens, cols;
-    const int64_t* targets;   // or NULL: every row of hidden
+    const int64_t* targets;
     uint32_t* part;
 };
 __device__ __forceinline__ uint32_t block_max(uint32_t m, uint32_t* red) {
@@ -190,7 +190,7 @@ template <typename T> __device__ __forceinline__ void find_absmax(const AbsMaxAr
         for (int64_t r = ABS_ROWS * (static_cast<int64_t>(waves) * b + wave); r < rows; r += ABS_ROWS * static_cast<int64_t>(waves) * blocks) {
             bool on[ABS_ROWS];
 #pragma unroll
-            for (int i = 0; i < ABS_ROWS; ++i) on[i] = r + i < rows && (head || !a.targets || a.targets[r + i] >= 0);
+            for (int i = 0; i < ABS_ROWS; ++i) on[i] = r + i < rows && (head || a.targets[r + i] >= 0);
             for (int64_t k = threadIdx.x & 63; k < runs; k += 64) {
                 Run<T> x[ABS_ROWS];
 #pragma unroll
@@ -1571,10 +1571,10 @@ hipError_t launch_scan(int dtype, const void* hidden, int64_t ld_hidden, const v
     return hipGetLastError();
 }
 
-// The largest value of hidden alone, over every row of it (few tokens).
-hipError_t launch_hidden_absmax(const void* hidden, int64_t ld_hidden, const Shape& sh, uint32_t* part, hipStream_t s) {
+// The largest value of hidden's scored rows alone (few tokens).
+hipError_t launch_hidden_absmax(const void* hidden, int64_t ld_hidden, const Shape& sh, const int64_t* targets, uint32_t* part, hipStream_t s) {
     const ScanArgs a{0, nullptr, 0, nullptr, nullptr, nullptr, nullptr, ABS_HEAD, ABS_HIDDEN,
-                     {nullptr, hidden, 0, static_cast<size_t>(ld_hidden), 0, sh.tokens, sh.cols, nullptr, part}};
+                     {nullptr, hidden, 0, static_cast<size_t>(ld_hidden), 0, sh.tokens, sh.cols, targets, part}};
     hipLaunchKernelGGL(scan_kernel<float>, dim3(a.blocks), dim3(LIVE_THREADS), 0, s, a);
     return hipGetLastError();
 }
@@ -1650,7 +1650,7 @@ template <typename T, int PARTS> hipError_t launch_few(const muon_token_logp_arg
                  reinterpret_cast<float*>(ws + pl.zt), kept(sv.e), static_cast<size_t>(sh.vp),
                  keep ? reinterpret_cast<uint32_t*>(ws + pl.absmax) : nullptr};
     // for the gradients' sake; without them its launch (4 us of 51) costs more than values below 2^-109 are worth
-    if (PARTS == 3 && keep) TL_TRY(launch_hidden_absmax(a.hidden, a.ld_hidden, sh, reinterpret_cast<uint32_t*>(ws + pl.absmax), s));
+    if (PARTS == 3 && keep) TL_TRY(launch_hidden_absmax(a.hidden, a.ld_hidden, sh, a.targets, reinterpret_cast<uint32_t*>(ws + pl.absmax), s));
     const dim3 grid(static_cast<unsigned>(f.tiles));
     if (f.tokens <= 16) hipLaunchKernelGGL((few_kernel<T, PARTS, 1>), grid, dim3(256), 0, s, f);
     else if (f.tokens <= 32) hipLaunchKernelGGL((few_kernel<T, PARTS, 2>), grid, dim3(256), 0, s, f);
@@ -1764,7 +1764,7 @@ hipError_t launch_few_backward(const muon_token_logp_backward_args& a, char* ws,
     float* slab = reinterpret_cast<float*>(ws + pl.slab);
     uint32_t* absmax = reinterpret_cast<uint32_t*>(ws + pl.absmax);
     if (a.dtype == MUON_BF16) return launch_few_grads<uint16_t, 1>(a, pl, saved, slab, absmax, s);
-    TL_TRY(launch_hidden_absmax(a.hidden, a.ld_hidden, pl.sh, absmax, s));
+    TL_TRY(launch_hidden_absmax(a.hidden, a.ld_hidden, pl.sh, a.targets, absmax, s));
     return launch_few_grads<float, 3>(a, pl, saved, slab, absmax, s);
 }
 }  // namespace

@@ -497,3 +497,25 @@ def test_token_logp_bf16_gradients_cost_little_more_than_their_rounding(gpu_lib,
         rounded = _np(torch.from_numpy(ref).to(torch.bfloat16))
         most = 1.1 * ((rounded - ref) ** 2).sum() + 2 * 2.0 ** -22 * terms.sum()
         assert ((_np(got) - ref) ** 2).sum() <= most, float(((_np(got) - ref) ** 2).sum() / most)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("t", [5, 40, 300])
+@pytest.mark.parametrize("use_saved", [True, False])
+def test_token_logp_huge_values_in_unscored_rows(gpu_lib, dtype, t, use_saved):
+    # finite values near the type's end in rows that are not scored: the same bits as without them
+    import torch
+    print("[token_logp huge]", t, dtype, use_saved, flush=True)
+    h, w, y, c = _inputs(71, t, 128, 600, dtype, ignored=0.4)
+    y[0], y[1] = 3, -100
+    huge = h.clone()
+    dead = (y < 0).nonzero()[:, 0]
+    huge[dead] = torch.finfo(_dt(dtype)).min
+    huge[dead[::2], 1::3] = torch.finfo(_dt(dtype)).max
+    out = []
+    for x in (h, huge):
+        saved = _saved(gpu_lib, x, w) if use_saved else None
+        logp, lse = _forward(gpu_lib, x, w, y, saved=saved)
+        out.append((logp, lse, *_backward(gpu_lib, x, w, y, lse, c, saved=saved)))
+    for a, b in zip(*out):
+        assert torch.equal(a, b)
