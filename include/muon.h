@@ -444,16 +444,20 @@ const char* muon_status_string(int32_t status);
 const char* muon_last_error_message(void);
 
 /* Optional per-kernel timing with HIP events recorded on the launch stream.
- * While enabled, every launch of muon_step / muon_ns is bracketed by two
- * events; muon_profile_read synchronizes them and returns, per kernel class,
+ * While enabled, every launch is bracketed by two
+ * events; reading synchronizes them and returns, per kernel class,
  * the summed duration in milliseconds and the number of launches, then
- * resets the counters.  Classes: 0 momentum+norm, 1 norm finalize, 2 Gram,
+ * resets the counters of all classes.  muon_profile_read returns the first
+ * MUON_KCLASS_COUNT classes, those of the optimizer steps (its struct does not
+ * grow), muon_profile_read_classes the first `classes` into two arrays of that
+ * length (either may be NULL).  Classes: 0 momentum+norm, 1 norm finalize, 2 Gram,
  * 3 polynomial, 4 update, 5 apply, 6 AdamW, 7 Muon-Cayley (all its kernels),
  * 8 the last update of muon_step, which also applies decay and the step to W,
  * 9 block norm (both directions), 10 token log-probabilities (both directions),
  * 11 preference loss, 12 policy loss.
  * Host-side bookkeeping only. */
-#define MUON_KCLASS_COUNT 13
+#define MUON_KCLASS_COUNT 9
+#define MUON_KCLASS_ALL   13
 typedef struct {
     double  ms[MUON_KCLASS_COUNT];
     int64_t launches[MUON_KCLASS_COUNT];
@@ -461,6 +465,7 @@ typedef struct {
 
 muon_status muon_profile_enable(int32_t on);
 muon_status muon_profile_read(muon_profile* out);
+muon_status muon_profile_read_classes(int32_t classes, double* ms, int64_t* launches);
 
 /* Library version as major*10000 + minor*100 + patch. */
 int32_t muon_version(void);

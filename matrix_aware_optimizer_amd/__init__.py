@@ -16,7 +16,8 @@ The names mirror the C entry points:
 ``muon_token_logp_backward_workspace_bytes``, ``muon_preference_loss``,
 ``muon_preference_loss_workspace_bytes``, ``muon_policy_loss``,
 ``muon_policy_loss_workspace_bytes``, ``muon_status_string``,
-``muon_last_error_message``, ``muon_profile_enable``, ``muon_profile_read``,
+``muon_last_error_message``, ``muon_profile_enable``, ``muon_profile_read``
+(C: ``muon_profile_read`` and ``muon_profile_read_classes``),
 ``muon_version``.
 """
 from __future__ import annotations
@@ -44,7 +45,7 @@ GATE_NONE, GATE_CHANNEL, GATE_FULL = 0, 1, 2
 PREFERENCE_KINDS = {"sigmoid": 0, "hinge": 1, "squared": 2}
 KL_KINDS = {"none": 0, "k1": 1, "k2": 2, "k3": 3}
 LOSS_REDUCTIONS = {"token": 0, "sequence": 1}
-MUON_KCLASS_COUNT = 13
+MUON_KCLASS_COUNT = 9
 KERNEL_CLASSES = ("momentum_norm", "norm_finalize", "gram", "poly", "update", "apply", "adamw", "cayley",
                   "update_apply", "block_norm", "token_logp", "preference_loss", "policy_loss")
 
@@ -168,6 +169,8 @@ SIGNATURES = {
     "muon_last_error_message": (ctypes.c_char_p, []),
     "muon_profile_enable": (ctypes.c_int32, [ctypes.c_int32]),
     "muon_profile_read": (ctypes.c_int32, [ctypes.POINTER(MuonProfile)]),
+    "muon_profile_read_classes": (ctypes.c_int32, [ctypes.c_int32, ctypes.POINTER(ctypes.c_double),
+                                                   ctypes.POINTER(ctypes.c_int64)]),
     "muon_version": (ctypes.c_int32, []),
 }
 
@@ -874,6 +877,7 @@ def muon_profile_enable(on: bool = True):
 
 
 def muon_profile_read() -> dict:
-    prof = MuonProfile()
-    _check(load().muon_profile_read(ctypes.byref(prof)))
-    return {name: {"ms": prof.ms[i], "launches": int(prof.launches[i])} for i, name in enumerate(KERNEL_CLASSES)}
+    n = len(KERNEL_CLASSES)
+    ms, launches = (ctypes.c_double * n)(), (ctypes.c_int64 * n)()
+    _check(load().muon_profile_read_classes(n, ms, launches))
+    return {name: {"ms": ms[i], "launches": int(launches[i])} for i, name in enumerate(KERNEL_CLASSES)}

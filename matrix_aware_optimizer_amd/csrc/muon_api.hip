@@ -1051,26 +1051,33 @@ muon_status muon_profile_enable(int32_t on) {
 
 muon_status muon_profile_read(muon_profile* out) {
     if (!out) return fail(MUON_ERR_INVALID_ARG, "out is NULL");
+    return muon_profile_read_classes(MUON_KCLASS_COUNT, out->ms, out->launches);
+}
+
+muon_status muon_profile_read_classes(int32_t classes, double* ms, int64_t* launches) {
+    if (classes < 0 || classes > MUON_KCLASS_ALL) return fail(MUON_ERR_INVALID_ARG, "%d kernel classes of %d", classes, MUON_KCLASS_ALL);
     std::vector<ProfRec> recs;
     {
         std::lock_guard<std::mutex> lk(g_mu);
         recs.swap(g_prof.recs);
     }
-    std::memset(out, 0, sizeof(*out));
+    if (ms) std::fill_n(ms, classes, 0.0);
+    if (launches) std::fill_n(launches, classes, int64_t{0});
     muon_status st = MUON_OK;
     for (const ProfRec& r : recs) {
         hipError_t e = hipEventSynchronize(r.b);
-        float ms = 0.0f;
-        if (e == hipSuccess) e = hipEventElapsedTime(&ms, r.a, r.b);
+        float t = 0.0f;
+        if (e == hipSuccess) e = hipEventElapsedTime(&t, r.a, r.b);
         if (e != hipSuccess && st == MUON_OK) st = hip_fail(e, "hipEventElapsedTime");
-        out->ms[r.cls] += ms;
-        out->launches[r.cls] += 1;
+        if (r.cls >= classes) continue;
+        if (ms) ms[r.cls] += t;
+        if (launches) launches[r.cls] += 1;
     }
     std::lock_guard<std::mutex> lk(g_mu);
     for (const ProfRec& r : recs) { g_prof.pool.push_back(r.a); g_prof.pool.push_back(r.b); }
     return st;
 }
 
-int32_t muon_version(void) { return 100; }
+int32_t muon_version(void) { return 200; }
 
 }  // extern "C"

@@ -175,3 +175,21 @@ def test_binding_refuses_wrong_tensors():
     with pytest.raises(ValueError, match="loss"):
         mao.muon_policy_loss(f, f, f, o, torch.zeros(2))
 
+
+
+def test_profile_read_fills_what_its_first_callers_allocate():
+    # muon_profile is two arrays of the nine classes that the optimizer steps have (144 bytes): a program built with it has no
+    # more behind the pointer.  The other classes come through muon_profile_read_classes.
+    lib = mao.load()
+    room = (ctypes.c_uint8 * 512)(*([0xA5] * 512))
+    assert lib.muon_profile_read(ctypes.cast(room, ctypes.POINTER(mao.MuonProfile))) == mao.MUON_OK
+    assert bytes(room[:144]) == bytes(144) and set(room[144:]) == {0xA5}
+    assert ctypes.sizeof(mao.MuonProfile) == 144
+    n = len(mao.KERNEL_CLASSES)
+    ms, launches = (ctypes.c_double * (n + 1))(*([7.0] * (n + 1))), (ctypes.c_int64 * (n + 1))(*([7] * (n + 1)))
+    assert lib.muon_profile_read_classes(n, ms, launches) == mao.MUON_OK
+    assert not any(ms[:n]) and not any(launches[:n]) and ms[n] == 7.0 and launches[n] == 7
+    assert lib.muon_profile_read_classes(n, None, None) == mao.MUON_OK
+    for bad in (-1, n + 1):
+        assert lib.muon_profile_read_classes(bad, ms, launches) == mao.MUON_ERR_INVALID_ARG
+    assert mao.muon_version() > 100          # how a program tells that the other classes and the operators are there
