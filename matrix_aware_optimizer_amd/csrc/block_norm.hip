@@ -114,11 +114,12 @@ __device__ __forceinline__ void row_sums(float (&v)[NS], float* red, int turn) {
     }
 }
 
+// row0: the launch's first row.
 template <typename T, int NT, int VPT, bool TAIL>
-__global__ __launch_bounds__(NT < 256 ? 256 : NT) void block_norm_kernel(muon_block_norm_args a) {
+__global__ __launch_bounds__(NT < 256 ? 256 : NT) void block_norm_kernel(muon_block_norm_args a, int64_t row0) {
     constexpr int BLOCK = NT < 256 ? 256 : NT, PER = BLOCK / NT, N = 8 * VPT;
     __shared__ float red[2 * BLOCK / 64];
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * PER + row_of_thread<NT>();
+    const int64_t row = row0 + static_cast<int64_t>(blockIdx.x) * PER + row_of_thread<NT>();
     if (NT == 64 && row >= a.rows) return;   // longer rows: one per workgroup, none past the last
     const Cols<NT, VPT, TAIL> c{static_cast<unsigned>(a.cols), threadIdx.x % NT};
     const float inv = 1.0f / static_cast<float>(a.cols);
@@ -204,11 +205,11 @@ template <typename T, typename C> struct BackwardRow {
     }
 };
 
-// Rows beyond BN_LONG: m1 and m0 of each, one workgroup a row.
+// Rows beyond BN_LONG: m1 and m0 of each, one workgroup a row, from row0 on.
 template <typename T, bool TAIL>
-__global__ __launch_bounds__(1024) void block_norm_means_kernel(muon_block_norm_backward_args a, float* means) {
+__global__ __launch_bounds__(1024) void block_norm_means_kernel(muon_block_norm_backward_args a, float* means, int64_t row0) {
     __shared__ float red[2 * 3 * 16];
-    const int64_t row = blockIdx.x;
+    const int64_t row = row0 + blockIdx.x;
     float s[3] = {0.0f, 0.0f, 0.0f}, s1 = 1.0f;
     for (unsigned c0 = 0; c0 < a.cols; c0 += 8192) {
         const Cols<1024, 1, TAIL> c{static_cast<unsigned>(a.cols), threadIdx.x + c0 / 8};
@@ -316,12 +317,24 @@ __global__ __launch_bounds__(1024) void block_norm_weights_kernel(muon_block_nor
     st_dt(out, c, s, a.weight_dtype);
 }
 
+// launch(first row, grid) for `per` rows a workgroup of `threads`: as many launches as it takes, since one holds fewer than 2^32
+// threads (at 64 columns beyond 2^26 rows, at 8192 beyond 2^22).
+template <typename F> hipError_t in_launches(int64_t rows, int per, int threads, F launch) {
+    const int64_t most = (int64_t{1} << 31) / threads * per;
+    for (int64_t row0 = 0; row0 < rows; row0 += most) {
+        launch(row0, dim3(static_cast<unsigned>((std::min(rows - row0, most) + per - 1) / per)));
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
 template <typename T, int NT, int VPT> hipError_t forward(const muon_block_norm_args& a, hipStream_t s) {
     constexpr int BLOCK = NT < 256 ? 256 : NT;
-    const dim3 grid(static_cast<unsigned>((a.rows + BLOCK / NT - 1) / (BLOCK / NT)));
-    if (a.cols % 8) hipLaunchKernelGGL((block_norm_kernel<T, NT, VPT, true>), grid, dim3(BLOCK), 0, s, a);
-    else hipLaunchKernelGGL((block_norm_kernel<T, NT, VPT, false>), grid, dim3(BLOCK), 0, s, a);
-    return hipGetLastError();
+    return in_launches(a.rows, BLOCK / NT, BLOCK, [&](int64_t row0, dim3 grid) {
+        if (a.cols % 8) hipLaunchKernelGGL((block_norm_kernel<T, NT, VPT, true>), grid, dim3(BLOCK), 0, s, a, row0);
+        else hipLaunchKernelGGL((block_norm_kernel<T, NT, VPT, false>), grid, dim3(BLOCK), 0, s, a, row0);
+    });
 }
 
 template <typename T> hipError_t forward_by_cols(const muon_block_norm_args& a, hipStream_t s) {
@@ -360,10 +373,10 @@ hipError_t backward_by_cols(const muon_block_norm_backward_args& a, float* part,
     if (a.cols <= BN_LONG) return backward<T, 1024>(a, part, nullptr, s);
     // a row's accumulators and data no longer fit: its means first, then runs of columns (x, r', dn and dr' read twice)
     float* means = part + backward_part_floats(a);
-    const dim3 grid(static_cast<unsigned>(a.rows));
-    if (a.cols % 8) hipLaunchKernelGGL((block_norm_means_kernel<T, true>), grid, dim3(1024), 0, s, a, means);
-    else hipLaunchKernelGGL((block_norm_means_kernel<T, false>), grid, dim3(1024), 0, s, a, means);
-    const hipError_t e = hipGetLastError();
+    const hipError_t e = in_launches(a.rows, 1, 1024, [&](int64_t row0, dim3 grid) {
+        if (a.cols % 8) hipLaunchKernelGGL((block_norm_means_kernel<T, true>), grid, dim3(1024), 0, s, a, means, row0);
+        else hipLaunchKernelGGL((block_norm_means_kernel<T, false>), grid, dim3(1024), 0, s, a, means, row0);
+    });
     return e != hipSuccess ? e : backward<T, 256, true>(a, part, means, s);
 }
 

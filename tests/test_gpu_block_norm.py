@@ -255,3 +255,31 @@ def test_block_norm_on_another_stream_and_in_a_graph(gpu_lib):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, ref))
+
+
+@pytest.mark.parametrize("rows,cols", [((1 << 26) + 5, 8), ((1 << 24) + 3, 1032), ((1 << 22) + 3, 4100)])
+def test_block_norm_more_rows_than_a_launch_has_threads(gpu_lib, rows, cols):
+    # 64, 256 and 1024 threads a row: 2^32 threads are more than one launch takes.  The same 64 rows over and over: each has the bits
+    # that it has in a small call.
+    import torch
+    print("[block_norm rows]", rows, cols, flush=True)
+    need = rows * cols * 2 * 3
+    if torch.cuda.mem_get_info()[0] < need + (16 << 30):
+        pytest.skip(f"{need >> 30} GB needed")
+    period, full = 64, rows // 64
+    ten, _ = _case(np.random.default_rng(8), period, cols, "bf16", "bf16", "channel")
+    want = _forward(gpu_lib, ten)
+    wide = {}
+    for k in ("x", "residual"):
+        wide[k] = torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda")
+        wide[k][:full * period].view(full, period, cols).copy_(ten[k].expand(full, period, cols))
+        wide[k][full * period:] = ten[k][:rows - full * period]
+    rstd = torch.zeros((2, rows), device="cuda")
+    norm = torch.zeros((rows, cols), dtype=torch.bfloat16, device="cuda")
+    gpu_lib.muon_block_norm(wide["x"], wide["residual"], wide["residual"], norm, post_weight=ten["post_weight"], gate=ten["gate"],
+                            pre_weight=ten["pre_weight"], rstd=rstd, residual_scale=ALPHA, eps=EPS)
+    for got, ref in ((wide["residual"], want[0]), (norm, want[1]), (rstd[0][:, None], want[2][0][:, None]), (rstd[1][:, None], want[2][1][:, None])):
+        for a in range(0, full, 1 << 14):
+            part = got[a * period:min(full, a + (1 << 14)) * period]
+            assert bool((part.reshape(-1, period, part.shape[1]) == ref).all())
+        assert torch.equal(got[full * period:], ref[:rows - full * period])
