@@ -86,6 +86,13 @@ template <int PARTS> __device__ __forceinline__ void half_parts(float x, uint16_
 __device__ __forceinline__ float rate_of(float scale2) { return fmaxf(fabsf(scale2), 1.17549435e-38f); }
 __device__ __forceinline__ float shown(float m) { return m == -INFINITY ? 0.0f : m; }   // an M to subtract
 
+// Workgroups in a row, whatever their number: a launch holds fewer than 2^32 threads along x, so the row goes on along y.
+__device__ __forceinline__ int64_t block_in_row() { return static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x; }
+dim3 row_of_blocks(int64_t blocks, int threads) {
+    const int64_t x = std::max<int64_t>(1, std::min(blocks, (int64_t{1} << 31) / threads));
+    return dim3(static_cast<unsigned>(x), static_cast<unsigned>(std::max<int64_t>(1, (blocks + x - 1) / x)));
+}
+
 // ---------------------------------------------------------------------------
 // The scored tokens, in order
 // ---------------------------------------------------------------------------
@@ -461,9 +468,10 @@ __global__ __launch_bounds__(pt::Tile<EDGE>::THREADS, 2) void logits_kernel(Logi
     pt::lds_byte_t* L = (pt::lds_byte_t*)lds;
     const int n = a.live.rows();
     const int tb = (n + EDGE - 1) / EDGE, nb = a.ta * tb;
-    if (static_cast<int>(blockIdx.x) >= nb) return;
+    const int64_t block = block_in_row();
+    if (block >= nb) return;
     int ia, ib;
-    pt::tile_of(pt::xcd_remap(blockIdx.x, nb), a.ta, tb, ia, ib);
+    pt::tile_of(pt::xcd_remap(static_cast<int>(block), nb), a.ta, tb, ia, ib);
     const int v0 = ia * EDGE, r0 = ib * EDGE;
     const char *sa[TL::HL], *sb[TL::HL];
 #pragma unroll
@@ -1313,8 +1321,8 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
     constexpr int NP = 256 / TOK;
     __shared__ float sm[NP][TOK], ss[NP][TOK];
     const int tk = threadIdx.x % TOK, part = threadIdx.x / TOK;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * TOK + tk;
-    if (a.absmax && blockIdx.x == 0) {
+    const int64_t row = block_in_row() * TOK + tk;
+    if (a.absmax && block_in_row() == 0) {
         uint32_t* red = reinterpret_cast<uint32_t*>(&sm[0][0]);
         const float hidden = operand_scale(a.absmax, false, red), head = operand_scale(a.absmax, true, red);
         if (threadIdx.x == 0) {
@@ -1580,7 +1588,7 @@ hipError_t launch_hidden_absmax(const void* hidden, int64_t ld_hidden, const Sha
 }
 
 template <int EDGE, int MODE> hipError_t launch_logits_edge(const LogitsArgs& l, int parts, hipStream_t s) {
-    const dim3 grid(static_cast<unsigned>(l.ta) * l.tb), block(pt::Tile<EDGE>::THREADS);
+    const dim3 grid = row_of_blocks(static_cast<int64_t>(l.ta) * l.tb, pt::Tile<EDGE>::THREADS), block(pt::Tile<EDGE>::THREADS);
     if (parts == 2) hipLaunchKernelGGL((logits_kernel<EDGE, 2, MODE, false>), grid, block, 0, s, l);
     else if (l.tail < pt::CHUNKS) hipLaunchKernelGGL((logits_kernel<EDGE, 1, MODE, true>), grid, block, 0, s, l);
     else hipLaunchKernelGGL((logits_kernel<EDGE, 1, MODE, false>), grid, block, 0, s, l);
@@ -1746,7 +1754,7 @@ hipError_t launch_token_logp(const muon_token_logp_args& a, void* workspace, hip
     TL_TRY(a.saved ? launch_logits<LG_SAVE>(l, sh.edge, sh.parts, s) : launch_logits<LG_STATS>(l, sh.edge, sh.parts, s));
     const CombineArgs c{m, sums, zt, static_cast<size_t>(sh.tp), 1, sh.ta(), a.targets, a.vocab, a.logp, a.lse, l.live, a.tokens,
                         scale2, kept_logp, kept_ref, kept_shift, sh.parts == 1 ? absmax : nullptr, scales};
-    hipLaunchKernelGGL(combine_kernel<32>, dim3(static_cast<unsigned>(sh.tp / 32)), dim3(256), 0, s, c);
+    hipLaunchKernelGGL(combine_kernel<32>, row_of_blocks(sh.tp / 32, 256), dim3(256), 0, s, c);
     return hipGetLastError();
 }
 
@@ -1809,7 +1817,7 @@ hipError_t launch_token_logp_backward(const muon_token_logp_backward_args& a, vo
             TL_TRY(launch_logits<LG_SAVE>(l, sh.edge, sh.parts, s));
             const CombineArgs f{l.m, l.s, l.zt, static_cast<size_t>(pl.chunk), 1, sh.ta(), a.targets, a.vocab, nullptr, nullptr, live,
                                 a.tokens, l.scale2, at(pl.logp), at(pl.ref), at(pl.shift), sh.parts == 1 ? absmax : nullptr, own};
-            hipLaunchKernelGGL(combine_kernel<32>, dim3(static_cast<unsigned>(pl.chunk / 32)), dim3(256), 0, s, f);
+            hipLaunchKernelGGL(combine_kernel<32>, row_of_blocks(pl.chunk / 32, 256), dim3(256), 0, s, f);
             TL_TRY(hipGetLastError());
         }
         PrepareArgs p{};

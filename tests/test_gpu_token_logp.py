@@ -519,3 +519,37 @@ def test_token_logp_huge_values_in_unscored_rows(gpu_lib, dtype, t, use_saved):
         out.append((logp, lse, *_backward(gpu_lib, x, w, y, lse, c, saved=saved)))
     for a, b in zip(*out):
         assert torch.equal(a, b)
+
+
+def test_token_logp_more_tiles_than_a_launch_has_threads(gpu_lib):
+    # 2^23 tiles of 512 threads; tokens from the first, middle and last tiles against the oracle
+    import torch
+    t, d, v = 1 << 20, 8, (1 << 19) + 1
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("40 GB needed")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    h, w = (torch.randn(s, generator=g, device="cuda").bfloat16() for s in ((t, d), (v, d)))
+    y = torch.randint(0, v, (t,), generator=g, device="cuda")
+    logp, lse = _forward(gpu_lib, h, w, y)
+    pick = torch.cat([torch.arange(a, a + 8, device="cuda") for a in (0, 255, t // 2 - 4, t - 8)])
+    _check_forward(h[pick], w, y[pick], 1.0, "bf16", logp[pick], lse[pick])
+    assert torch.isfinite(logp).all() and torch.isfinite(lse).all()
+
+
+def test_token_logp_more_tokens_than_a_launch_has_threads(gpu_lib):
+    # 2^29 tokens: eight threads a token where the tiles' statistics are joined
+    import torch
+    t, d, v = (1 << 29) + 7, 8, 3
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("60 GB needed")
+    period = 1 << 16
+    hp, w, yp, _ = _inputs(81, period, d, v, "bf16")
+    base = _forward(gpu_lib, hp, w, yp)
+    _check_forward(hp, w, yp, 1.0, "bf16", *base)
+    h, y = torch.empty((t, d), dtype=torch.bfloat16, device="cuda"), torch.empty((t,), dtype=torch.int64, device="cuda")
+    full = t // period
+    h[:full * period].view(full, period, d).copy_(hp.expand(full, period, d))
+    y[:full * period].view(full, period).copy_(yp.expand(full, period))
+    h[full * period:], y[full * period:] = hp[:t - full * period], yp[:t - full * period]
+    for got, ref in zip(_forward(gpu_lib, h, w, y), base):
+        assert bool((got[:full * period].view(full, period) == ref).all()) and torch.equal(got[full * period:], ref[:t - full * period])
