@@ -234,8 +234,8 @@ muon_status muon_cayley_step(const muon_cayley_matrix* mats, int32_t n, const mu
  *    unit column stride; vectors are contiguous;
  *  - every output element is written by every call (nothing accumulates into
  *    what a buffer held before), and results are the same bits on every run;
- *  - sums, softmax statistics and norms are held in fp32; an output is rounded
- *    once (RNE) to its dtype;
+ *  - sums, softmax statistics and norms are held in fp32, the losses' sums in fp64;
+ *    an output is rounded once (RNE) to its dtype;
  *  - the calls allocate nothing and copy nothing from the host, so they can be
  *    captured in a HIP graph.
  * =========================================================================== */

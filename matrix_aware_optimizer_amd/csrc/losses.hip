@@ -126,7 +126,7 @@ __device__ __forceinline__ unsigned in_piece(int t, int a, int b) {
     return (1u << h) - (1u << l) & (h > l ? ~0u : 0u);
 }
 
-// Sums of sequences by unit: V = float or float2.
+// Sums of sequences by unit: V = float or double2.
 template <typename V> struct UnitSums {
     V *head, *tail, *own;
     __device__ __forceinline__ void put(int s, int a, int lo, int hi, V v) const {
@@ -141,9 +141,9 @@ template <typename V> struct UnitSums {
     }
 };
 __device__ __forceinline__ float add(float a, float b) { return a + b; }
-__device__ __forceinline__ float2 add(float2 a, float2 b) { return make_float2(a.x + b.x, a.y + b.y); }
+__device__ __forceinline__ double2 add(double2 a, double2 b) { return make_double2(a.x + b.x, a.y + b.y); }
 __device__ __forceinline__ float wave_total(float v) { return wave_sum(v); }
-__device__ __forceinline__ float2 wave_total(float2 v) { return make_float2(wave_sum(v.x), wave_sum(v.y)); }
+__device__ __forceinline__ double2 wave_total(double2 v) { return make_double2(wave_sum(v.x), wave_sum(v.y)); }
 
 // head[first .. last] summed by the wave.
 template <typename V> __device__ __forceinline__ V heads(const UnitSums<V>& q, int first, int last) {
@@ -154,10 +154,13 @@ template <typename V> __device__ __forceinline__ V heads(const UnitSums<V>& q, i
 
 // ---- preference -------------------------------------------------------------
 
+// Log ratios are summed and subtracted in fp64: without a reference a pair's difference may be a millionth of its two sums
+// (60000 tokens each: fp32 sums were off by 4e-3 of a log-probability).
+
 template <typename OFF> struct PreferenceState {
     muon_preference_args a;
     Sequences<OFF> seqs;
-    UnitSums<float2> q;     // { sum of counted log ratios, counted tokens }
+    UnitSums<double2> q;    // { sum of counted log ratios, counted tokens }
     float* factor;          // gradient factor by sequence
     float* losses;          // by pair
     __device__ int units() const { return static_cast<int>((a.tokens + UNIT - 1) / UNIT); }
@@ -179,33 +182,40 @@ template <typename S> __device__ __forceinline__ void preference_unit(const S& s
     const int t0 = u * UNIT, t = t0 + PER * lane_id();
     st.seqs.pieces(t0, t0 + UNIT, [](int) { return 0.0f; }, [&](int s, int a, int b, int lo, int hi, float) {
         const unsigned on = k.live & in_piece(t, a, b);
-        float v = 0.0f;
+        double v = 0.0;
 #pragma unroll
-        for (int e = 0; e < PER; ++e) v += (on >> e & 1u) ? k.lp[e] - k.ref[e] : 0.0f;
+        for (int e = 0; e < PER; ++e) v += (on >> e & 1u) ? static_cast<double>(k.lp[e]) - static_cast<double>(k.ref[e]) : 0.0;
         v = wave_sum(v);
         const float c = wave_sum(static_cast<float>(__popc(on)));
-        if (lane_id() == 0) st.q.put(s, a, lo, hi, make_float2(v, c));
+        if (lane_id() == 0) st.q.put(s, a, lo, hi, make_double2(v, c));
     });
 }
 
 // Sum of the sequence that each lane asks for (s < 0: none), short ones lane by lane, long ones by the wave.
-template <typename S> __device__ __forceinline__ float2 lane_sequence_sums(const S& st, int s) {
+template <typename S> __device__ __forceinline__ double2 lane_sequence_sums(const S& st, int s) {
     int lo = 0, hi = 0;
     if (s >= 0) {
         lo = st.seqs.at(s);
         hi = max(st.seqs.at(s + 1), lo);
     }
-    float2 v = {};
+    double2 v = {};
+    constexpr int NEAR = 8;   // units past the first, whose sums a lane loads at once
     const int u0 = lo / UNIT, u1 = hi > lo ? (hi - 1) / UNIT : u0;
-    const bool far = u1 - u0 > 8;
+    const bool far = u1 - u0 > NEAR;
     if (hi > lo) {
         v = st.q.first(s, lo, hi);
-        if (!far)
-            for (int u = u0 + 1; u <= u1; ++u) v = add(v, st.q.head[u]);
+        if (!far && u1 > u0) {
+            double2 h[NEAR];
+#pragma unroll
+            for (int k = 0; k < NEAR; ++k) h[k] = st.q.head[min(u0 + 1 + k, u1)];
+#pragma unroll
+            for (int k = 0; k < NEAR; ++k)
+                if (u0 + 1 + k <= u1) v = add(v, h[k]);
+        }
     }
     for (unsigned long long todo = __ballot(far); todo; todo &= todo - 1) {
         const int l = __ffsll(todo) - 1;
-        const float2 h = heads(st.q, __builtin_amdgcn_readlane(u0, l) + 1, __builtin_amdgcn_readlane(u1, l));
+        const double2 h = heads(st.q, __builtin_amdgcn_readlane(u0, l) + 1, __builtin_amdgcn_readlane(u1, l));
         if (lane_id() == l) v = add(v, h);
     }
     return v;
@@ -222,15 +232,18 @@ template <typename S> __device__ __forceinline__ void preference_pairs(const S& 
     for (int p0 = wave * 64; p0 < pairs; p0 += waves * 64) {
         const int p = p0 + lane_id();
         const bool on = p < pairs;
-        float w[2], r[2];
+        float w[2];
+        double r[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const float2 v = lane_sequence_sums(st, on ? 2 * p + k : -1);
-            w[k] = a.average ? 1.0f / fmaxf(v.y, 1.0f) : 1.0f;
-            r[k] = v.x * w[k];
-            if (on && a.rewards) a.rewards[2 * p + k] = a.beta * r[k];
+            const double2 v = lane_sequence_sums(st, on ? 2 * p + k : -1);
+            const double n = fmax(v.y, 1.0);
+            w[k] = a.average ? 1.0f / static_cast<float>(n) : 1.0f;
+            r[k] = a.average ? v.x / n : v.x;
+            if (on && a.rewards) a.rewards[2 * p + k] = static_cast<float>(a.beta * r[k]);
         }
-        const float u = r[0] - r[1], h = a.beta * u - a.margin, e = a.label_smoothing;
+        const double u = r[0] - r[1];
+        const float h = static_cast<float>(a.beta * u - a.margin), e = a.label_smoothing;
         float l, du;
         if (a.kind == MUON_PREFERENCE_SIGMOID) {
             l = (1.0f - e) * softplus(-h) + e * softplus(h);
@@ -239,7 +252,7 @@ template <typename S> __device__ __forceinline__ void preference_pairs(const S& 
             l = fmaxf(1.0f - h, 0.0f);
             du = h < 1.0f ? -a.beta : 0.0f;
         } else {
-            const float q = u - 0.5f / a.beta;
+            const float q = static_cast<float>(u - 0.5 / a.beta);
             l = q * q;
             du = 2.0f * q;
         }
@@ -306,7 +319,7 @@ template <typename T> __global__ __launch_bounds__(LS_ONE) void preference_one_k
     constexpr int W = LS_ONE / 64;
     __shared__ float red[W];
     __shared__ int offsets[LS_SMALL_SEQS + 1];
-    __shared__ float2 head[W], tail[W], own[LS_SMALL_SEQS];
+    __shared__ double2 head[W], tail[W], own[LS_SMALL_SEQS];
     __shared__ float factor[LS_SMALL_SEQS], losses[LS_SMALL_SEQS / 2];
     const int u = wave_index();
     const PreferenceState<int> st{a, {offsets, static_cast<int>(a.sequences), static_cast<int>(a.tokens)}, {head, tail, own}, factor, losses};
@@ -570,7 +583,7 @@ unsigned grid_for(int64_t units, int most) {
 
 size_t preference_bytes(const muon_preference_args& a) {
     const size_t q = static_cast<size_t>(a.sequences), u = static_cast<size_t>(units_of(a.tokens));
-    return (2 * u + q) * sizeof(float2) + (q + q / 2) * sizeof(float);
+    return (2 * u + q) * sizeof(double2) + (q + q / 2) * sizeof(float);
 }
 
 hipError_t launch_preference(const muon_preference_args& a, void* workspace, hipStream_t s) {
@@ -581,7 +594,7 @@ hipError_t launch_preference(const muon_preference_args& a, void* workspace, hip
         return hipGetLastError();
     }
     const size_t q = static_cast<size_t>(a.sequences), u = static_cast<size_t>(units_of(a.tokens));
-    float2* f2 = static_cast<float2*>(workspace);
+    double2* f2 = static_cast<double2*>(workspace);
     float* f = reinterpret_cast<float*>(f2 + 2 * u + q);
     const PreferenceState<int64_t> st{a, {a.offsets, static_cast<int>(a.sequences), static_cast<int>(a.tokens)},
                                       {f2, f2 + u, f2 + 2 * u}, f, f + q};

@@ -273,3 +273,25 @@ def test_policy_loss_near_zero(gpu_lib, count):
     a = np.repeat(adv.astype(np.float64), count)
     ref = -(np.exp(d) * a).sum() / n
     assert abs(float(loss) - ref) <= 2.0 ** -22 * np.abs(np.expm1(d) * a).mean() + 2.0 ** -23 * abs(ref), (float(loss), ref)
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "hinge", "squared"])
+@pytest.mark.parametrize("count", [4000, 61003])
+def test_preference_loss_of_nearly_equal_sequences(gpu_lib, kind, count):
+    # No reference, two sequences of `count` tokens whose sums (some -1.3 count) differ by 0.25005: log-probabilities are multiples of
+    # 2^-16 below 8, so fp64 sums are exact, u is, and beta u - margin, the loss and its slope are rounded a few times at
+    # their own size (h up to 1: 32 u of loss + 1).
+    import torch
+    rng = np.random.default_rng(12)
+    a = -np.round(rng.random(count) * 2.6 * 65536) / 65536
+    b = rng.permutation(a)
+    b[0] -= 16387 / 65536
+    off = torch.tensor([0, count, 2 * count], dtype=torch.int64, device="cuda")
+    logp = torch.from_numpy(np.concatenate([a, b]).astype(np.float32)).cuda()
+    kw = dict(beta=2.0, kind=kind, label_smoothing=0.1 if kind == "sigmoid" else 0.0, margin=0.05)
+    o = to.preference_loss(_np(logp), [0, count, 2 * count], **{k: float(np.float32(v)) if isinstance(v, float) else v for k, v in kw.items()})
+    assert abs(o["u"][0] - 16387 / 65536) < 1e-9
+    loss, grad = torch.empty(1, device="cuda"), torch.empty_like(logp)
+    gpu_lib.muon_preference_loss(logp, off, loss, grad, **kw)
+    assert abs(float(loss) - o["loss"]) <= 32 * U * (o["loss"] + 1), (float(loss), o["loss"])
+    assert np.all(np.abs(_np(grad) - o["grad"]) <= 32 * U * (np.abs(o["grad"]) + 1))
