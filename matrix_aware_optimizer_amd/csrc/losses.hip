@@ -40,6 +40,10 @@ constexpr int LS_SMALL_SEQS = 1024;      // sequences up to which it does: their
 // Workgroups of the other launches, at most: 5 a CU, what the registers hold (policy, 2048 sequences: 26 us; 2 a CU: 29).
 constexpr int LS_GRID = 1280;
 constexpr int LS_COUNTS = 1024;          // workgroups that count, at most: one partial each (256: 1 us more)
+// Units beyond which the counts of sequences are joined by a launch of their own; up to it each unit adds up the others of its
+// sequence itself, at most 64 loads a lane, which grows with the square of a sequence (one sequence of 1.0, 2.1, 4.2, 16.9 million
+// tokens: 23, 36, 86, 897 us; joined 20, 28, 39, 111; six of 1.35 million in all: 19, joined 28).
+constexpr int64_t LS_JOIN = 4096;
 
 __device__ __forceinline__ int lane_id() { return threadIdx.x & 63; }
 
@@ -148,6 +152,7 @@ __device__ __forceinline__ double2 wave_total(double2 v) { return make_double2(w
 // head[first .. last] summed by the wave.
 template <typename V> __device__ __forceinline__ V heads(const UnitSums<V>& q, int first, int last) {
     V v = {};
+#pragma unroll 8
     for (int u = first + lane_id(); u <= last; u += 64) v = add(v, q.head[u]);
     return wave_total(v);
 }
@@ -158,6 +163,7 @@ template <typename V> __device__ __forceinline__ V heads(const UnitSums<V>& q, i
 // (60000 tokens each: fp32 sums were off by 4e-3 of a log-probability).
 
 template <typename OFF> struct PreferenceState {
+    typedef double2 Sum;
     muon_preference_args a;
     Sequences<OFF> seqs;
     UnitSums<double2> q;    // { sum of counted log ratios, counted tokens }
@@ -192,20 +198,21 @@ template <typename S> __device__ __forceinline__ void preference_unit(const S& s
 }
 
 // Sum of the sequence that each lane asks for (s < 0: none), short ones lane by lane, long ones by the wave.
-template <typename S> __device__ __forceinline__ double2 lane_sequence_sums(const S& st, int s) {
+template <typename S> __device__ __forceinline__ typename S::Sum lane_sequence_sums(const S& st, int s) {
+    typedef typename S::Sum Sum;
     int lo = 0, hi = 0;
     if (s >= 0) {
         lo = st.seqs.at(s);
         hi = max(st.seqs.at(s + 1), lo);
     }
-    double2 v = {};
+    Sum v = {};
     constexpr int NEAR = 8;   // units past the first, whose sums a lane loads at once
     const int u0 = lo / UNIT, u1 = hi > lo ? (hi - 1) / UNIT : u0;
     const bool far = u1 - u0 > NEAR;
     if (hi > lo) {
         v = st.q.first(s, lo, hi);
         if (!far && u1 > u0) {
-            double2 h[NEAR];
+            Sum h[NEAR];
 #pragma unroll
             for (int k = 0; k < NEAR; ++k) h[k] = st.q.head[min(u0 + 1 + k, u1)];
 #pragma unroll
@@ -215,7 +222,7 @@ template <typename S> __device__ __forceinline__ double2 lane_sequence_sums(cons
     }
     for (unsigned long long todo = __ballot(far); todo; todo &= todo - 1) {
         const int l = __ffsll(todo) - 1;
-        const double2 h = heads(st.q, __builtin_amdgcn_readlane(u0, l) + 1, __builtin_amdgcn_readlane(u1, l));
+        const Sum h = heads(st.q, __builtin_amdgcn_readlane(u0, l) + 1, __builtin_amdgcn_readlane(u1, l));
         if (lane_id() == l) v = add(v, h);
     }
     return v;
@@ -342,9 +349,11 @@ template <typename T> __global__ __launch_bounds__(LS_ONE) void preference_one_k
 constexpr int PL_SUMS = 5;
 
 template <typename OFF> struct PolicyState {
+    typedef float Sum;
     muon_policy_args a;
     Sequences<OFF> seqs;
     UnitSums<float> q;      // counted tokens by unit: sequence means with a mask
+    bool joined = false;    // own[s] holds the whole count of every sequence that goes beyond a unit
     __device__ int units() const { return static_cast<int>((a.tokens + UNIT - 1) / UNIT); }
     __device__ bool by_sequence() const { return a.reduction == MUON_REDUCE_SEQUENCE; }
     // Nothing about a token depends on its sequence.
@@ -424,6 +433,7 @@ __device__ __forceinline__ void policy_weights(const S& st, int u, const float* 
                            float c;
                            if (!st.a.mask) c = static_cast<float>(hi - lo);
                            else if (lo >= t0 && hi <= t0 + UNIT) c = wave_sum(static_cast<float>(__popc(on)));
+                           else if (st.joined) c = st.q.own[s];
                            else c = st.q.first(s, lo, hi) + heads(st.q, lo / UNIT + 1, (hi - 1) / UNIT);
                            w = 1.0f / (fmaxf(c, 1.0f) * static_cast<float>(st.seqs.count));
                        }
@@ -490,6 +500,17 @@ __global__ __launch_bounds__(LS_THREADS) void policy_counts_kernel(PolicyState<i
     if (st.by_sequence()) return;
     total = block_sum(total, red);
     if (threadIdx.x == 0) counts[blockIdx.x] = total;
+}
+
+// The counts of the sequences that go beyond a unit, each put together once.
+__global__ __launch_bounds__(LS_THREADS) void policy_join_kernel(PolicyState<int64_t> st) {
+    constexpr int W = LS_THREADS / 64;
+    for (int s0 = (blockIdx.x * W + wave_index()) * 64; s0 < st.seqs.count; s0 += gridDim.x * W * 64) {
+        const int s = s0 + lane_id(), lo = st.seqs.at(min(s, st.seqs.count - 1)), hi = st.seqs.at(min(s, st.seqs.count - 1) + 1);
+        const bool on = s < st.seqs.count && hi > lo && hi > (lo / UNIT + 1) * UNIT;
+        const float c = lane_sequence_sums(st, on ? s : -1);
+        if (on) st.q.own[s] = c;
+    }
 }
 
 // counts: `parts` partial counts (token mean with a mask).  sums: PL_SUMS by workgroup.
@@ -626,7 +647,7 @@ hipError_t launch_policy(const muon_policy_args& a, void* workspace, hipStream_t
     double* sums = static_cast<double*>(workspace);
     float* f = reinterpret_cast<float*>(sums + PL_SUMS * LS_GRID);
     float* counts = f + 2 * u + q;
-    const PolicyState<int64_t> st{a, {a.offsets, static_cast<int>(a.sequences), static_cast<int>(a.tokens)}, {f, f + u, f + 2 * u}};
+    PolicyState<int64_t> st{a, {a.offsets, static_cast<int>(a.sequences), static_cast<int>(a.tokens)}, {f, f + u, f + 2 * u}};
     hipError_t e = hipSuccess;
     int parts = 0;
     if (a.mask) {
@@ -635,6 +656,12 @@ hipError_t launch_policy(const muon_policy_args& a, void* workspace, hipStream_t
         hipLaunchKernelGGL(policy_counts_kernel, dim3(parts), dim3(LS_THREADS), 0, s, st, counts);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
+        st.joined = a.reduction == MUON_REDUCE_SEQUENCE && static_cast<int64_t>(u) > LS_JOIN;
+        if (st.joined) {
+            hipLaunchKernelGGL(policy_join_kernel, dim3(grid_for((a.sequences + 63) / 64, LS_GRID)), dim3(LS_THREADS), 0, s, st);
+            e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
     }
     const unsigned grid = grid_for(u, LS_GRID);
     if (bf) hipLaunchKernelGGL(policy_main_kernel<uint16_t>, dim3(grid), dim3(LS_THREADS), 0, s, st, counts, parts, sums);

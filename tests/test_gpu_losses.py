@@ -295,3 +295,44 @@ def test_preference_loss_of_nearly_equal_sequences(gpu_lib, kind, count):
     gpu_lib.muon_preference_loss(logp, off, loss, grad, **kw)
     assert abs(float(loss) - o["loss"]) <= 32 * U * (o["loss"] + 1), (float(loss), o["loss"])
     assert np.all(np.abs(_np(grad) - o["grad"]) <= 32 * U * (np.abs(o["grad"]) + 1))
+
+
+def test_policy_loss_sequence_mean_takes_time_by_its_tokens(gpu_lib):
+    # one masked sequence of 2^25 tokens among short ones: a mean within each sequence may cost more than one over all tokens (a
+    # count of its own), not a multiple that grows with the sequence; and both means against sums in fp64
+    import torch
+    n = 1 << 25
+    off = torch.tensor([0, 700, n - 5000, n - 4096, n], dtype=torch.int64, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(4)
+    old = -torch.rand(n, generator=g, device="cuda")
+    lp = old + 0.05 * torch.randn(n, generator=g, device="cuda")
+    mask = (torch.rand(n, generator=g, device="cuda") < 0.8).to(torch.uint8)
+    adv = torch.tensor([1.0, -0.5, 0.25, 2.0], device="cuda")
+    loss, grad = torch.empty(1, device="cuda"), torch.empty_like(lp)
+    ws = torch.empty(gpu_lib.muon_policy_loss_workspace_bytes(lp, off), dtype=torch.uint8, device="cuda")
+    ms = {}
+    a = torch.repeat_interleave(adv, off.diff()).double()
+    rho = torch.exp(lp.double() - old.double())
+    term = -torch.minimum(rho * a, rho.clamp(1 - 0.2, 1 + 0.2) * a) * mask
+    edges = [int(v) for v in off]
+    counts = torch.stack([mask[i:j].sum() for i, j in zip(edges, edges[1:])]).double()
+    want = {"token": term.sum() / counts.sum(),
+            "sequence": sum(term[i:j].sum() / k for i, j, k in zip(edges, edges[1:], counts)) / 4}
+    for reduction in ("token", "sequence"):
+        call = lambda: gpu_lib.muon_policy_loss(lp, old, adv, off, loss, grad, mask=mask, reduction=reduction, per_sequence=True, workspace=ws)
+        call()
+        assert abs(float(loss) - float(want[reduction])) <= 1e-6
+        first, last = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        best = []
+        for _ in range(5):
+            first.record()
+            call()
+            last.record()
+            torch.cuda.synchronize()
+            best.append(first.elapsed_time(last))
+        ms[reduction] = min(best)
+        w = 1 / counts.sum() if reduction == "token" else torch.repeat_interleave(1 / (4 * counts), off.diff())
+        ref = torch.where((a > 0) & (rho > 1.2) | (a < 0) & (rho < 0.8), 0.0, -rho * a) * mask * w
+        off_by = (grad.double() - ref).abs() > 1e-5 * ref.abs()
+        assert int(off_by.sum()) <= 64        # ratios within rounding of a clipping bound
+    assert ms["sequence"] <= 3 * ms["token"] + 0.1, ms
