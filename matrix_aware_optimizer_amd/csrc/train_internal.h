@@ -10,23 +10,13 @@
 
 namespace muon {
 
-// One element, as fp32, of a buffer of float or bf16 (uint16_t) values.
-template <typename T> __device__ __forceinline__ float ld_el(const void* p, size_t i);
-template <> __device__ __forceinline__ float ld_el<float>(const void* p, size_t i) {
-    return G(static_cast<const float*>(p))[i];
-}
-template <> __device__ __forceinline__ float ld_el<uint16_t>(const void* p, size_t i) {
-    return bf16_to_f32(G(static_cast<const uint16_t*>(p))[i]);
-}
+// One element, from fp32, of a buffer of float or bf16 (uint16_t) values.
 template <typename T> __device__ __forceinline__ void st_el(void* p, size_t i, float v);
 template <> __device__ __forceinline__ void st_el<float>(void* p, size_t i, float v) { G(static_cast<float*>(p))[i] = v; }
 template <> __device__ __forceinline__ void st_el<uint16_t>(void* p, size_t i, float v) {
     G(static_cast<uint16_t*>(p))[i] = f32_to_bf16(v);
 }
 // The same with the dtype as a (uniform) value.
-__device__ __forceinline__ float ld_dt(const void* p, size_t i, int dt) {
-    return dt == DT_BF16 ? ld_el<uint16_t>(p, i) : ld_el<float>(p, i);
-}
 __device__ __forceinline__ void st_dt(void* p, size_t i, float v, int dt) {
     if (dt == DT_BF16) st_el<uint16_t>(p, i, v);
     else st_el<float>(p, i, v);
