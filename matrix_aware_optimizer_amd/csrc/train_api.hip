@@ -18,8 +18,16 @@ size_t elem_size(int32_t dtype) { return dtype == MUON_BF16 ? 2 : 4; }
 struct Buffers {
     struct Buf {
         uintptr_t lo, hi;
+        size_t pitch, width;   // of a matrix's rows, in bytes; a vector is one row
         bool out;
         const char* name;
+        // No byte in common.  Matrices of one pitch may lie in each other's gaps (column ranges of one buffer).
+        bool apart(const Buf& o) const {
+            if (lo >= o.hi || o.lo >= hi) return true;
+            if (pitch != o.pitch || width > pitch || o.width > pitch) return false;
+            const size_t after = (o.lo >= lo ? o.lo - lo : pitch - (lo - o.lo) % pitch) % pitch;
+            return after >= width && after + o.width <= pitch;
+        }
     };
     Buf b[24];
     int n = 0;
@@ -28,6 +36,9 @@ struct Buffers {
 
     // `optional`: NULL is fine.  Buffers of no elements need no pointer.
     void add(const char* name, const void* p, size_t bytes, size_t align, bool out, bool optional = false) {
+        rows(name, p, bytes, bytes, bytes, align, out, optional);
+    }
+    void rows(const char* name, const void* p, size_t bytes, size_t pitch, size_t width, size_t align, bool out, bool optional) {
         if (bad || bytes == 0) return;
         if (!p) {
             if (!optional) { bad = name; why = "is NULL"; }
@@ -35,20 +46,20 @@ struct Buffers {
         }
         const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
         if (lo % align) { bad = name; why = "is misaligned"; return; }
-        b[n++] = {lo, lo + bytes, out, name};
+        b[n++] = {lo, lo + bytes, pitch, width, out, name};
     }
     void matrix(const char* name, const void* p, int64_t rows, int64_t cols, int64_t ld, size_t es, bool out,
                 bool optional = false) {
         if (bad || rows == 0 || (optional && !p)) return;
         if (ld < cols || ld > (int64_t{1} << 40)) { bad = name; why = "has a row pitch below its columns or beyond 2^40"; return; }
-        add(name, p, (static_cast<size_t>(rows - 1) * ld + cols) * es, es, out);
+        this->rows(name, p, (static_cast<size_t>(rows - 1) * ld + cols) * es, ld * es, cols * es, es, out, false);
     }
     // The same buffer as input and output, with the same pitch, is an in-place call.
     muon_status check(const void* in_place_in = nullptr, const void* in_place_out = nullptr) const {
         if (bad) return fail(MUON_ERR_INVALID_ARG, "%s %s", bad, why);
         for (int i = 0; i < n; ++i)
             for (int j = i + 1; j < n; ++j) {
-                if (!(b[i].out || b[j].out) || b[i].lo >= b[j].hi || b[j].lo >= b[i].hi) continue;
+                if (!(b[i].out || b[j].out) || b[i].apart(b[j])) continue;
                 const uintptr_t pi = reinterpret_cast<uintptr_t>(in_place_in), po = reinterpret_cast<uintptr_t>(in_place_out);
                 if (pi && pi == po && b[i].lo == pi && b[j].lo == pi && b[i].hi == b[j].hi && b[i].out != b[j].out) continue;
                 return fail(MUON_ERR_INVALID_ARG, "%s and %s overlap", b[i].name, b[j].name);

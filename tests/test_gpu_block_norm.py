@@ -283,3 +283,30 @@ def test_block_norm_more_rows_than_a_launch_has_threads(gpu_lib, rows, cols):
             part = got[a * period:min(full, a + (1 << 14)) * period]
             assert bool((part.reshape(-1, period, part.shape[1]) == ref).all())
         assert torch.equal(got[full * period:], ref[:rows - full * period])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_block_norm_on_column_ranges_of_one_buffer(gpu_lib, dtype):
+    # every matrix of a call a range of columns of one wide buffer
+    import torch
+    rows, cols = 37, 301
+    ten, _ = _case(np.random.default_rng(21), rows, cols, dtype, dtype, "full")
+    want = _forward(gpu_lib, ten)
+    back = _backward(gpu_lib, ten, want[0], want[2])
+    wide = torch.full((rows, 8 * cols), float("nan"), dtype=_dt(dtype), device="cuda")
+    part = [wide[:, k * cols:(k + 1) * cols] for k in range(8)]
+    for k, name in enumerate(("x", "residual", "gate")):
+        part[k].copy_(ten[name])
+    rstd = torch.empty_like(want[2])
+    gpu_lib.muon_block_norm(part[0], part[1], part[3], part[4], post_weight=ten["post_weight"], gate=part[2], pre_weight=ten["pre_weight"],
+                            rstd=rstd, residual_scale=ALPHA, eps=EPS)
+    assert torch.equal(part[3], want[0]) and torch.equal(part[4], want[1]) and torch.equal(rstd, want[2])
+    part[1].copy_(ten["grad_norm"])
+    part[4].copy_(ten["grad_out_residual"])
+    weights = {k: torch.empty_like(ten[k]) for k in ("post_weight", "pre_weight")}
+    gpu_lib.muon_block_norm_backward(part[0], part[3], rstd, part[1], part[5], part[6], grad_out_residual=part[4], post_weight=ten["post_weight"],
+                                     gate=part[2], pre_weight=ten["pre_weight"], grad_post_weight=weights["post_weight"], grad_gate=part[7],
+                                     grad_pre_weight=weights["pre_weight"], residual_scale=ALPHA)
+    for got, name in ((part[5], "grad_x"), (part[6], "grad_residual"), (part[7], "grad_gate"), (weights["post_weight"], "grad_post_weight"),
+                      (weights["pre_weight"], "grad_pre_weight")):
+        assert torch.equal(got, back[name]), name

@@ -193,3 +193,18 @@ def test_profile_read_fills_what_its_first_callers_allocate():
     for bad in (-1, n + 1):
         assert lib.muon_profile_read_classes(bad, ms, launches) == mao.MUON_ERR_INVALID_ARG
     assert mao.muon_version() > 100          # how a program tells that the other classes and the operators are there
+
+
+def test_column_ranges_of_one_buffer_do_not_overlap():
+    # matrices of 64 bf16 columns in rows of 192: side by side they share no element, one column further in they do
+    pitch = dict(ld_out_residual=192, ld_out_norm=192, ld_x=192)
+    for base in (AT[5], AT[5] + 128, AT[5] + 256):          # also where the second starts before the first, in its previous row
+        for other in (AT[5], AT[5] + 128, AT[5] + 256):
+            status = _status(_norm(out_residual=base, out_norm=other, x=AT[0], **pitch))
+            assert (status == mao.MUON_ERR_INVALID_ARG) == (base == other), mao.muon_last_error_message()
+    assert _status(_norm(out_residual=AT[5], out_norm=AT[5] + 126, **pitch)) == mao.MUON_ERR_INVALID_ARG
+    assert _status(_norm(out_residual=AT[5] + 384 * 2, out_norm=AT[5] + 256 + 2, **pitch)) == mao.MUON_ERR_INVALID_ARG   # into the next row
+    assert _status(_norm(out_residual=AT[5], out_norm=AT[5] + 128, **{**pitch, "ld_out_norm": 191})) == mao.MUON_ERR_INVALID_ARG
+    assert _status(_norm(x=AT[5] + 128, out_residual=AT[5], **pitch)) != mao.MUON_ERR_INVALID_ARG
+    assert _status(_norm_backward(grad_x=AT[9], grad_residual=AT[9] + 128, ld_grad_x=128, ld_grad_residual=128)) != mao.MUON_ERR_INVALID_ARG
+    assert _status(_logp_backward(grad_hidden=AT[6], hidden=AT[6] + 128, ld_hidden=128, ld_grad_hidden=128)) != mao.MUON_ERR_INVALID_ARG
