@@ -381,7 +381,8 @@ muon_status muon_token_logp_backward(const muon_token_logp_backward_args* args, 
  * pairs' mean:
  *   r_s = sum_t mask_t (logp_t - ref_logp_t)   [/ number of counted tokens]
  *   u = r_2p - r_2p+1,  h = beta u - margin
- *   SIGMOID  -(1 - e) log sigma(h) - e log sigma(-h)     e = label_smoothing
+ *   SIGMOID  -(1 - e) log sigma(h) - e log sigma(-h)     e = label_smoothing; a
+ *            term whose share is 0 is 0 for infinite h too
  *   HINGE    max(0, 1 - h)
  *   SQUARED  (u - 1 / (2 beta))^2                        beta != 0, margin unused */
 typedef enum { MUON_PREFERENCE_SIGMOID = 0, MUON_PREFERENCE_HINGE = 1, MUON_PREFERENCE_SQUARED = 2 } muon_preference_kind;

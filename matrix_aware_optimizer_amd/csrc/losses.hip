@@ -253,7 +253,8 @@ template <typename S> __device__ __forceinline__ void preference_pairs(const S& 
         const float h = static_cast<float>(a.beta * u - a.margin), e = a.label_smoothing;
         float l, du;
         if (a.kind == MUON_PREFERENCE_SIGMOID) {
-            l = (1.0f - e) * softplus(-h) + e * softplus(h);
+            // a share of 0 counts for nothing, also where its term is infinite
+            l = (e < 1.0f ? (1.0f - e) * softplus(-h) : 0.0f) + (e > 0.0f ? e * softplus(h) : 0.0f);
             du = a.beta * (e * sigmoid(h) - (1.0f - e) * sigmoid(-h));
         } else if (a.kind == MUON_PREFERENCE_HINGE) {
             l = fmaxf(1.0f - h, 0.0f);

@@ -336,3 +336,25 @@ def test_policy_loss_sequence_mean_takes_time_by_its_tokens(gpu_lib):
         off_by = (grad.double() - ref).abs() > 1e-5 * ref.abs()
         assert int(off_by.sum()) <= 64        # ratios within rounding of a clipping bound
     assert ms["sequence"] <= 3 * ms["token"] + 0.1, ms
+
+
+@pytest.mark.parametrize("smoothing", [0.0, 0.1, 1.0])
+def test_preference_loss_of_impossible_answers(gpu_lib, smoothing):
+    # an answer with a token of probability 0: rejected, nothing is left to learn (loss and slope 0 but for the smoothing's share, which
+    # is infinite); chosen, the loss is infinite and the slope its limit
+    import torch
+    inf = float("inf")
+    off = torch.tensor([0, 3, 5, 8, 10], dtype=torch.int64, device="cuda")
+    for pair, h in ((0, inf), (1, -inf)):
+        logp = torch.full((10,), -1.0, device="cuda")
+        logp[4 if pair == 0 else 6] = -inf
+        loss, grad, rewards = torch.empty(1, device="cuda"), torch.empty_like(logp), torch.empty(4, device="cuda")
+        gpu_lib.muon_preference_loss(logp, off, loss, grad, beta=0.5, label_smoothing=smoothing, rewards=rewards)
+        share = smoothing if h > 0 else 1 - smoothing       # of the term that is infinite
+        other = to.preference_loss(np.full(10, -1.0), [0, 3, 5, 8, 10], beta=0.5, label_smoothing=smoothing)["losses"][1 - pair]
+        want = inf if share > 0 else other / 2
+        assert float(loss) == want or abs(float(loss) - want) <= 32 * U, (float(loss), want)
+        slope = 0.5 * (smoothing if h > 0 else smoothing - 1)
+        a = 0 if pair == 0 else 5
+        assert np.all(np.abs(_np(grad)[a:a + 3] - slope / 2) <= 8 * U) and np.all(np.abs(_np(grad)[a + 3:a + 5] + slope / 2) <= 8 * U)
+        assert torch.isfinite(grad).all() and float(rewards[1 if pair == 0 else 2]) == -inf
