@@ -1322,13 +1322,10 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
     __shared__ float sm[NP][TOK], ss[NP][TOK];
     const int tk = threadIdx.x % TOK, part = threadIdx.x / TOK;
     const int64_t row = block_in_row() * TOK + tk;
-    if (a.absmax && block_in_row() == 0) {
-        uint32_t* red = reinterpret_cast<uint32_t*>(&sm[0][0]);
-        const float hidden = operand_scale(a.absmax, false, red), head = operand_scale(a.absmax, true, red);
-        if (threadIdx.x == 0) {
-            a.scales[0] = hidden;
-            a.scales[1] = head;
-        }
+    if (a.absmax && block_in_row() < 2) {   // there are at least PAD / TOK
+        const bool head = block_in_row() == 1;
+        const float scale = operand_scale(a.absmax, head, reinterpret_cast<uint32_t*>(&sm[0][0]));
+        if (threadIdx.x == 0) a.scales[head] = scale;
     }
     const int64_t n = a.live.idx ? a.live.rows() : a.tokens;
     const float k = rate_of(a.scale2);
