@@ -348,7 +348,8 @@ muon_status muon_token_logp(const muon_token_logp_args* args, void* workspace, s
  * token), fewer bits below and none below 2^-39.  bf16 calls form dz from
  * exp(z - M) in fp16, M the maximum of up to 256 neighbouring entries without the
  * target: 11 bits down to 2^-14, none below 2^-25.  The logits' product takes
- * bf16 operands as they are. */
+ * bf16 operands as they are.  fp32 operands of scored tokens have to be finite: an
+ * infinity makes NaN of its logits. */
 typedef struct {
     const void*    hidden;
     const void*    head;

@@ -8,12 +8,16 @@
 //
 // HBM-bound: the forward pass reads x and r and writes r' and n, the backward pass reads
 // x, r', dn and dr' and writes dx and dr (a full gate adds one each way); a few operations
-// per byte.  So a row is read once and kept in registers, as fp32, by the NT threads that share it:
+// per byte.  So a row is read once and kept, as fp32, by the NT threads that share it, in registers but for 16385 columns and
+// more (6 to 116 values a thread go through scratch there):
 // one wave for rows up to 1024 columns (forward; its sums need no barrier), 256 or 1024 threads
 // for longer ones (1003 x 1407 fp32, both passes: 31.5 us, 34.2 with one wave a row; 8192 x 2048 bf16 the same with
 // either).  The weights are read again for every row: they come from L2.
-// 8192 x 2048 bf16: forward 24 us (134 MB, 5.6 TB/s), backward 45 us (201 MB, 4.5 TB/s) and 5.7 us for the weights' partials;
-// one row: 3.8 us, a launch's length.
+// 8192 x 2048 bf16: forward 24 - 26 us (134 MB, 5.4 TB/s), backward 45 us (201 MB, 4.5 TB/s) and 5.7 us for the weights' partials; fp32
+// 55 (4.9 TB/s), 85 (4.8) and 6.5; one row: 2.7 - 3.8 us, a launch's length.  The backward kernel is held to 128 registers, 4 waves a
+// SIMD: its forms for odd widths, for 2049 to 4096 columns and most in fp32 keep 2 to 19 values a thread in scratch (8192 x 4096 bf16: 105
+// us, 3.8 TB/s).  Odd widths cost more than that, in both passes, by accesses that are not aligned: 1003 x 1407 fp32 31 us, x 1408 25;
+// 8192 x 2047 bf16 168 us, x 2048 78.
 //
 // The backward pass needs mean(dxh xh), and dxh needs mean(dh h) first.  With q = g wp xh,
 //   sum dxh xh = sum (dr' + rstd1 dh) q - rstd1 mean(dh h) sum h q,

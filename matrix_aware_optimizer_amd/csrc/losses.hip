@@ -15,13 +15,13 @@
 // Preference: units -> pairs (loss terms and each sequence's gradient factor) -> gradient.
 // Policy: the number of counted tokens first (1 byte a token, only with a mask), then loss and
 // gradient in one pass over the rest, then the partial sums.  Up to LS_SMALL tokens all steps run in one
-// workgroup and one launch: a wave keeps its unit's tokens in registers, the offsets and sums sit in LDS, so
-// memory is waited for once before and once after.
+// workgroup and one launch: a wave keeps its unit's tokens in registers, the offsets and sums sit in LDS.  (The state that
+// the steps pass on, arguments and LDS addresses, lies in scratch there: 168 and 184 bytes a lane.)
 //
-// Preference, 1.18 M tokens in 256 pairs (15 MB): three launches of 4.5 us, each little more than its latency; 8 sequences in one
-// launch 8.5 us (three: 16).  Policy, 2.36 M tokens in 2048 sequences (42 MB): 17.4 us (2.4 TB/s) after 5.2 us of counting and
+// Preference, 1.18 M tokens in 256 pairs (15 MB): three launches of 4.9, 5.5 and 4.5 us, each little more than its latency; 8 sequences
+// in one launch 9.4 us (three: 16).  Policy, 2.36 M tokens in 2048 sequences (42 MB): 18 us (2.3 TB/s) after 4 - 5 us of counting and
 // before 4 us of sums: the search for a unit's sequences, their offsets and advantages, then its tokens are loads that wait for each
-// other.  1.35 M tokens in 6 sequences: 12.5 us + 3.8 + 3.8.
+// other.  1.35 M tokens in 6 sequences: 13 us + 3.9 + 3.8.
 #include <algorithm>
 
 #include "train_internal.h"
@@ -33,8 +33,8 @@ namespace {
 constexpr int UNIT = 512, PER = 8;       // tokens of a wave's unit, of a lane
 constexpr int LS_THREADS = 256;          // workgroups of the launches over many units: 4 waves
 constexpr int LS_ONE = 1024;             // the workgroup that does everything, at most: 16 waves
-// Tokens up to which it does: one unit a wave (6 pairs of up to 1024 tokens: 12 us, 16 with the launches over many units; 12
-// policy sequences: 16 us, 18).
+// Tokens up to which it does: one unit a wave (6 pairs of up to 1024 tokens: 12.8 us, 16 with the launches over many units; 12
+// policy sequences of up to 1000: 16.6 us, 18).
 constexpr int64_t LS_SMALL = LS_ONE / 64 * UNIT;
 constexpr int LS_SMALL_SEQS = 1024;      // sequences up to which it does: their offsets and sums in LDS
 // Workgroups of the other launches, at most: 5 a CU, what the registers hold (policy, 2048 sequences: 26 us; 2 a CU: 29).

@@ -24,7 +24,7 @@
 //    tiles, added in order by slab_sum_kernel.
 //  - fp32 operands travel as two fp16 parts under a scale (product_tile.h): scan_kernel finds the largest values, and the
 //    kernels that make the copies the scales.  dz does so too, in bf16 calls in one part: 11 bits of it where bf16 would keep 8
-//    (6144 x 2048 x 32000, error of a gradient before its own rounding to bf16 in parts of its norm: 2e-4, in bf16 1.6e-3).  The
+//    (6144 x 2048 x 32000: a gradient's error with its own rounding 0.0017 of its norm, as if dz were exact; 0.0024 in bf16).  The
 //    matrix cores take one type, so the transposed copies of bf16 operands are fp16 under a scale as well, exact down to
 //    2^-29 of the operand's largest value; what that costs is a look through head for it.  dz has a scale for each token, that its own
 //    largest entry gives, -c expm1(logp) of the target: a token's gradient keeps its bits beside tokens with larger ones.
@@ -51,18 +51,18 @@ namespace {
 using pt::u32x4;
 
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
-// Most tokens of the few_ kernels (forward and backward, 48 tokens x 2048 x 32000 bf16: 141 us,
-// 208 with the tiles' kernels; 40 tokens in fp32: 372, 574; 12 tokens x 2048 x 65536 in fp32: 402, 966).
+// Most tokens of the few_ kernels (forward and backward, 48 tokens x 2048 x 32000 bf16: 142 us,
+// 224 with the tiles' kernels; 64: 147, 229; 40 tokens in fp32: 378, 574; 12 tokens x 2048 x 65536 in fp32: 404, 1217).
 constexpr int64_t FEW_TOKENS = 64;
 constexpr int FEW_ROWS = 32;                // vocabulary entries per workgroup of few_kernel
 constexpr int64_t DZ_BYTES = int64_t{4} << 30;   // both layouts of dz (without `saved`: and e), at most: more tokens go in chunks
 constexpr int CUS = 256;
-// 256 x 256 tiles below which the smaller tile serves a product: some 3/4 of the CUs.  2000 x 1024 x 8192, both passes: 138 us, at a
-// bound of 96 154; 8192 x 2048 x 32000: 2480, at 512 2835; 777 x 1000 x 32003: 270, at 512 303.
+// 256 x 256 tiles below which the smaller tile serves a product: some 3/4 of the CUs.  2000 x 1024 x 8192, both passes: 188 us, at a
+// bound of 96 198; 8192 (6144 scored) x 2048 x 32000: 2556, at 512 2930; 777 x 1000 x 32003: 296, at 512 330.
 constexpr int64_t FEW_TILES = 192;
 constexpr int PAD = 256;                    // every buffer of dz, e and their statistics is padded to the larger tile
-// Runs of k of a product with few tiles, at most, and k-steps of one, at least: 300 x 512 x 8000, both passes, 60 us; 61 with 8
-// runs or 16 steps, 60 with 32 runs or 4 steps.
+// Runs of k of a product with few tiles, at most, and k-steps of one, at least: 300 x 512 x 8000, both passes, 69 us; 67 with 8
+// runs or 16 steps, 69 with 32 runs or 4 steps.
 constexpr int MAX_SPLITS = 16, MIN_SPLIT_STEPS = 8;
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -458,9 +458,10 @@ __device__ __forceinline__ void store_cols(const pt::lds_byte_t* L, uint16_t* ds
         __builtin_nontemporal_store(TL::stage_col8(L, c, q), G(reinterpret_cast<u32x4*>(dst + (r0 + c) * ld + v0 + 8 * q)));
     }
 }
-// 6144 scored tokens x 2048 x 32000 bf16, keeping e: 752 us, 1071 TFLOP/s (a library product of 8192^3 reaches 1534); the
-// statistics, exponentials and 0.4 GB of e take the difference to the gradients' products.  512 x 1024 x 8192 fp32 (128-tile):
-// 41 us, 3 x 209 TFLOP/s: two rounds of workgroups, bound by LDS reads.
+
+// 6144 scored tokens x 2048 x 32000 bf16, keeping e: 755 - 790 us, 1020 - 1066 TFLOP/s (a library product of 8192^3 reaches 1534): 32 k-steps
+// a tile, and nothing runs under a tile's first loads, statistics and 0.4 GB of e, since a workgroup takes the CU's LDS.  512 x 1024 x 8192
+// fp32 (128-tile): 42 us, 3 x 205 TFLOP/s: 256 tiles, one round, bound by LDS reads.
 template <int EDGE, int PARTS, int MODE, bool KTAIL>
 __global__ __launch_bounds__(pt::Tile<EDGE>::THREADS, 2) void logits_kernel(LogitsArgs a) {
     typedef pt::Tile<EDGE> TL;
@@ -621,8 +622,8 @@ struct DzArgs {
     PackArgs hidden;        // the transpose of hidden for grad_head, by workgroups past the vocabulary's
 };
 
-// 64 tokens x 64 entries a workgroup, or 64 tokens x 64 columns of hidden.  Reads 2 (fp32: 4) bytes an element and writes 2 x 2 (fp32: 2 x 4), HBM-bound
-// (6144 x 32000 bf16: 1.2 GB in 220 us, 5.4 TB/s).  E: what e is kept in.
+// 64 tokens x 64 entries a workgroup, or 64 tokens x 64 columns of hidden.  Reads 2 (fp32: 4) bytes an element and writes 2 x 2
+// (fp32: 2 x 4), HBM-bound (6144 x 32000 bf16 and 2048 columns of hidden: 1.28 GB in 250 us, 5.1 TB/s).  E: what e is kept in.
 template <typename E, int PARTS>
 __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
     __shared__ uint16_t tile[PARTS][64][72];   // [entry or column][token]
@@ -751,8 +752,8 @@ __device__ __forceinline__ void st_piece(float* p, const u32x4& v, int left) {
     }
 }
 
-// T: the gradient's type.  6144 tokens x 2048 x 32000 bf16: 630 us (grad_hidden) and 790 us (grad_head, 8 tiles by 125),
-// 1279 and 1019 TFLOP/s.
+// T: the gradient's type.  6144 tokens x 2048 x 32000 bf16: 795 us (grad_hidden: 24 x 8 tiles of 500 steps, a quarter of the CUs without
+// one) and 690 us (grad_head: 125 x 8 tiles of 96 steps, 665 with bf16 operands: the clock), 1013 and 1167 TFLOP/s.
 template <int EDGE, int PARTS, typename T>
 __global__ __launch_bounds__(pt::Tile<EDGE>::THREADS, 2) void grad_kernel(GradArgs a) {
     typedef pt::Tile<EDGE> TL;
