@@ -626,7 +626,7 @@ struct DzArgs {
 // (fp32: 2 x 4), HBM-bound (6144 x 32000 bf16 and 2048 columns of hidden: 1.28 GB in 250 us, 5.1 TB/s).  E: what e is kept in.
 template <typename E, int PARTS>
 __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
-    __shared__ uint16_t tile[PARTS][64][72];   // [entry or column][token]
+    __shared__ __attribute__((aligned(16))) uint16_t tile[PARTS][64][72];   // [entry or column][token]
     const int n = a.tok.live.rows();
     // dz's tiles along the vocabulary first, then hidden's along the tokens first (neighbours write one run of a row)
     const int across = static_cast<int>(a.vp / 64), down = static_cast<int>(a.rows_pitch / 64);
