@@ -80,7 +80,8 @@ def draw(rng):
         chosen = rng.choice([1, 2, 4, 6, 8, rng.randint(1, 8)])
         tokens = _log_int(rng, 1, max(1, 8192 * 2048 * 6 // (cols * chosen)))
         return _experts(None, rng.choice(["bf16", "bf16", "f32"]), tokens, cols,
-                        rng.choice([8, 64, rng.randint(1, 256)]), chosen, rng.choice([0.0, 0.1]), rng.choice(["fwd", "both", "both"]))
+                        rng.choice([8, 64, rng.randint(1, 256)]), chosen, rng.choice([0.0, 0.1]),
+                        rng.choice(["fwd", "both", "both"]))
     dtype = rng.choice(["bf16", "bf16", "bf16", "f32"])
     width = rng.choice([64, 128, 8 * rng.randint(2, 16), rng.randint(9, 128)])
     kv_heads = rng.choice([1, 2, 4, 8, rng.randint(1, 8)])
