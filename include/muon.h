@@ -13,7 +13,9 @@
  * operators that make the gradients in a preference or policy step: norms
  * around a block (muon_block_norm), token log-probabilities over a vocabulary
  * head (muon_token_logp) and two losses on them (muon_preference_loss,
- * muon_policy_loss).
+ * muon_policy_loss); and the operators inside a block, between the matrices that
+ * the step updates: attention (muon_attention) and the tokens' way to the experts
+ * and back (muon_expert_sort, muon_expert_combine).
  * Sources, cited by page title and section:
  *   [Muon优化器] linsight.cn/f25d614e.html -- the industrial Muon class
  *     (momentum, Nesterov, decay and apply), zeropower_via_newtonschulz
@@ -440,6 +442,166 @@ typedef struct {
 size_t muon_policy_loss_workspace_bytes(const muon_policy_args* args);
 muon_status muon_policy_loss(const muon_policy_args* args, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ===========================================================================
+ * Operators inside a block.  The training operators' conventions hold.
+ * ======================================================================== */
+
+/* --- Attention over packed sequences ---------------------------------------
+ * Sequence s holds queries offsets[s] .. offsets[s + 1) - 1 and keys
+ * key_offsets[s] .. key_offsets[s + 1) - 1 (device memory, non-decreasing;
+ * values outside are taken as the nearest bound, empty sequences are fine).
+ * Query i of n_q stands at key position a = i + n_k - n_q: the last query at the
+ * last key.  Key j is seen by it if its key_mask is not 0, j <= a if `causal`,
+ * and |j - a| < window if window > 0.  With h' = h / (heads / kv_heads), over the
+ * seen keys:
+ *   z_ij  = scale q_i.k_j + bias[bucket_map[clamp(j - a, -reach, reach) + reach]][h]
+ *   lse_i = log sum_j exp(z_ij),   out_i = sum_j exp(z_ij - lse_i) v_j
+ * A query that sees no key, and a row of no sequence, gets out = 0 and
+ * lse = -infinity.  Keys that are masked, and the rows of no sequence, reach
+ * nothing, whatever they hold.  A bucket outside [0, buckets) adds 0.
+ *
+ * q and out are queries x heads x width, k and v keys x kv_heads x width, with
+ * unit stride along width and any pitch ld_* from token to token and hs_* from
+ * head to head (0 for a broadcast input); lse is queries x heads, contiguous.
+ *
+ * Precision.  Products of the inputs are summed in fp32 and never rounded; bf16
+ * calls take the probabilities (and dz below) into their products as two bf16
+ * parts, 16 bits.  `out_low` is what rounding took from `out`: with it the
+ * backward pass has out in 16 bits, which it needs where a row sees almost
+ * only one key. */
+#define MUON_MAX_HEAD_WIDTH 128
+#define MUON_MAX_HEADS      4096
+#define MUON_MAX_REACH      4096
+#define MUON_MAX_BUCKETS    8193
+
+typedef struct {
+    const void*    q;
+    const void*    k;
+    const void*    v;
+    const int64_t* offsets;      /* sequences + 1, or NULL: one sequence of all */
+    const int64_t* key_offsets;  /* sequences + 1, or NULL: as offsets */
+    const uint8_t* key_mask;     /* keys, or NULL (all seen) */
+    const void*    bias;         /* buckets x heads, contiguous, or NULL */
+    const int32_t* bucket_map;   /* 2 reach + 1; NULL exactly if bias is */
+    void*  out;
+    float* lse;
+    void*  out_low;              /* like out, or NULL */
+    int64_t queries, keys, sequences;   /* >= 0; sequences >= 1, and 1 without offsets */
+    int64_t ld_q, hs_q, ld_k, hs_k, ld_v, hs_v, ld_out, hs_out, ld_out_low, hs_out_low;
+    int64_t window;              /* 0: none */
+    float   scale;               /* finite */
+    int32_t heads, kv_heads;     /* heads a multiple of kv_heads */
+    int32_t width;               /* 1 <= width <= MUON_MAX_HEAD_WIDTH */
+    int32_t buckets, reach;      /* with bias: 1 <= buckets <= MUON_MAX_BUCKETS, 0 <= reach <= MUON_MAX_REACH */
+    int32_t causal;
+    int32_t dtype;               /* muon_dtype of every matrix and of bias */
+} muon_attention_args;
+
+size_t muon_attention_workspace_bytes(const muon_attention_args* args);
+muon_status muon_attention(const muon_attention_args* args, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Its gradients, from grad_out; the probabilities are formed again.  out, lse and
+ * out_low (which may be NULL) are the forward call's.  With p_ij = exp(z_ij - lse_i):
+ *   delta_i = grad_out_i.out_i,   dz_ij = p_ij (grad_out_i.v_j - delta_i)
+ *   grad_q = scale dz k,  grad_k = scale dz^T q,  grad_v = p^T grad_out  (k, v: over the heads that share one)
+ *   grad_bias[b][h] = sum of dz over the pairs of bucket b
+ * Rows of no sequence and masked keys get 0. */
+typedef struct {
+    const void*    q;
+    const void*    k;
+    const void*    v;
+    const int64_t* offsets;
+    const int64_t* key_offsets;
+    const uint8_t* key_mask;
+    const void*    bias;
+    const int32_t* bucket_map;
+    const void*    out;
+    const float*   lse;
+    const void*    out_low;
+    const void*    grad_out;
+    void* grad_q;
+    void* grad_k;
+    void* grad_v;
+    void* grad_bias;             /* like bias; NULL exactly if bias is */
+    int64_t queries, keys, sequences;
+    int64_t ld_q, hs_q, ld_k, hs_k, ld_v, hs_v, ld_out, hs_out, ld_out_low, hs_out_low, ld_grad_out, hs_grad_out,
+        ld_grad_q, hs_grad_q, ld_grad_k, hs_grad_k, ld_grad_v, hs_grad_v;
+    int64_t window;
+    float   scale;
+    int32_t heads, kv_heads, width, buckets, reach, causal, dtype;
+} muon_attention_backward_args;
+
+size_t muon_attention_backward_workspace_bytes(const muon_attention_backward_args* args);
+muon_status muon_attention_backward(const muon_attention_backward_args* args, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+
+/* --- Tokens sorted by expert, and back --------------------------------------
+ * experts[t][c] is the c-th expert that token t goes to; a value outside
+ * [0, num_experts) is a choice that was dropped.  The others, in the order of
+ * their experts and within one expert in the order of t and c, take rows 0, 1, ..
+ * of `sorted`:
+ *   slots[t][c] = that row, or -1;  sorted[slots[t][c]] = x[t]
+ *   offsets[e] .. offsets[e + 1) - 1 are the rows of expert e
+ * `sorted` has tokens * chosen rows; those behind offsets[num_experts] get 0. */
+#define MUON_MAX_EXPERTS 2048
+#define MUON_MAX_CHOSEN  64
+
+typedef struct {
+    const void*    x;           /* tokens x cols */
+    const int64_t* experts;     /* tokens x chosen */
+    void*    sorted;            /* tokens * chosen x cols */
+    int32_t* slots;             /* tokens x chosen */
+    int64_t* offsets;           /* num_experts + 1 */
+    int64_t tokens, cols;       /* tokens * chosen <= MUON_MAX_TOKENS, 1 <= cols <= MUON_MAX_DIM */
+    int64_t ld_x, ld_sorted;
+    int32_t chosen, num_experts, dtype;
+} muon_expert_sort_args;
+
+size_t muon_expert_sort_workspace_bytes(const muon_expert_sort_args* args);
+muon_status muon_expert_sort(const muon_expert_sort_args* args, void* workspace, size_t workspace_bytes, void* stream);
+
+/* grad_x[t] = sum over c of grad_sorted[slots[t][c]].  A slot outside
+ * [0, tokens * chosen) is one of a dropped choice, here and below. */
+typedef struct {
+    const void*    grad_sorted; /* tokens * chosen x cols */
+    const int32_t* slots;       /* tokens x chosen */
+    void*   grad_x;             /* tokens x cols */
+    int64_t tokens, cols, ld_grad_sorted, ld_grad_x;
+    int32_t chosen, dtype;
+} muon_expert_sort_backward_args;
+
+muon_status muon_expert_sort_backward(const muon_expert_sort_backward_args* args, void* stream);
+
+/* out[t] = sum over c of weights[t][c] y[slots[t][c]], y the experts' outputs in
+ * the order of muon_expert_sort. */
+typedef struct {
+    const void*    y;           /* tokens * chosen x cols */
+    const int32_t* slots;
+    const float*   weights;     /* tokens x chosen */
+    void*   out;                /* tokens x cols */
+    int64_t tokens, cols, ld_y, ld_out;
+    int32_t chosen, dtype;
+} muon_expert_combine_args;
+
+muon_status muon_expert_combine(const muon_expert_combine_args* args, void* stream);
+
+/* Its gradients: grad_y[slots[t][c]] = weights[t][c] grad_out[t] (rows behind
+ * offsets[num_experts] get 0) and grad_weights[t][c] = grad_out[t].y[slots[t][c]]
+ * (0 for a dropped choice).  slots and offsets as muon_expert_sort wrote them. */
+typedef struct {
+    const void*    grad_out;    /* tokens x cols */
+    const void*    y;
+    const int32_t* slots;
+    const float*   weights;
+    const int64_t* offsets;     /* num_experts + 1 */
+    void*  grad_y;              /* tokens * chosen x cols */
+    float* grad_weights;        /* tokens x chosen */
+    int64_t tokens, cols, ld_grad_out, ld_y, ld_grad_y;
+    int32_t chosen, num_experts, dtype;
+} muon_expert_combine_backward_args;
+
+muon_status muon_expert_combine_backward(const muon_expert_combine_backward_args* args, void* stream);
+
 /* Static description of a status code. */
 const char* muon_status_string(int32_t status);
 /* Detail of the calling thread's last failure ("" if none). */
@@ -456,10 +618,11 @@ const char* muon_last_error_message(void);
  * 3 polynomial, 4 update, 5 apply, 6 AdamW, 7 Muon-Cayley (all its kernels),
  * 8 the last update of muon_step, which also applies decay and the step to W,
  * 9 block norm (both directions), 10 token log-probabilities (both directions),
- * 11 preference loss, 12 policy loss.
+ * 11 preference loss, 12 policy loss, 13 attention (both directions), 14 tokens
+ * to experts and back (all four calls).
  * Host-side bookkeeping only. */
 #define MUON_KCLASS_COUNT 9
-#define MUON_KCLASS_ALL   13
+#define MUON_KCLASS_ALL   15
 typedef struct {
     double  ms[MUON_KCLASS_COUNT];
     int64_t launches[MUON_KCLASS_COUNT];

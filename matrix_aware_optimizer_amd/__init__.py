@@ -15,7 +15,12 @@ The names mirror the C entry points:
 ``muon_token_logp_saved_bytes``, ``muon_token_logp_workspace_bytes``,
 ``muon_token_logp_backward_workspace_bytes``, ``muon_preference_loss``,
 ``muon_preference_loss_workspace_bytes``, ``muon_policy_loss``,
-``muon_policy_loss_workspace_bytes``, ``muon_status_string``,
+``muon_policy_loss_workspace_bytes``, ``muon_attention``,
+``muon_attention_workspace_bytes``, ``muon_attention_backward``,
+``muon_attention_backward_workspace_bytes``, ``muon_expert_sort``,
+``muon_expert_sort_workspace_bytes``, ``muon_expert_sort_backward``,
+``muon_expert_combine``, ``muon_expert_combine_backward``,
+``muon_status_string``,
 ``muon_last_error_message``, ``muon_profile_enable``, ``muon_profile_read``
 (C: ``muon_profile_read`` and ``muon_profile_read_classes``),
 ``muon_version``.
@@ -47,7 +52,7 @@ KL_KINDS = {"none": 0, "k1": 1, "k2": 2, "k3": 3}
 LOSS_REDUCTIONS = {"token": 0, "sequence": 1}
 MUON_KCLASS_COUNT = 9
 KERNEL_CLASSES = ("momentum_norm", "norm_finalize", "gram", "poly", "update", "apply", "adamw", "cayley",
-                  "update_apply", "block_norm", "token_logp", "preference_loss", "policy_loss")
+                  "update_apply", "block_norm", "token_logp", "preference_loss", "policy_loss", "attention", "experts")
 
 
 class MuonMatrix(ctypes.Structure):
@@ -132,11 +137,49 @@ class MuonPolicyArgs(ctypes.Structure):
                         ("i", "kl reduction advantage_per_sequence dtype")])
 
 
+_HEADS = "ld_q hs_q ld_k hs_k ld_v hs_v ld_out hs_out ld_out_low hs_out_low"
+
+
+class MuonAttentionArgs(ctypes.Structure):
+    _fields_ = _fields([("p", "q k v offsets key_offsets key_mask bias bucket_map out lse out_low"),
+                        ("q", "queries keys sequences " + _HEADS + " window"), ("f", "scale"),
+                        ("i", "heads kv_heads width buckets reach causal dtype")])
+
+
+class MuonAttentionBackwardArgs(ctypes.Structure):
+    _fields_ = _fields([("p", "q k v offsets key_offsets key_mask bias bucket_map out lse out_low grad_out grad_q grad_k "
+                              "grad_v grad_bias"),
+                        ("q", "queries keys sequences " + _HEADS + " ld_grad_out hs_grad_out ld_grad_q hs_grad_q "
+                              "ld_grad_k hs_grad_k ld_grad_v hs_grad_v window"),
+                        ("f", "scale"), ("i", "heads kv_heads width buckets reach causal dtype")])
+
+
+class MuonExpertSortArgs(ctypes.Structure):
+    _fields_ = _fields([("p", "x experts sorted slots offsets"), ("q", "tokens cols ld_x ld_sorted"),
+                        ("i", "chosen num_experts dtype")])
+
+
+class MuonExpertSortBackwardArgs(ctypes.Structure):
+    _fields_ = _fields([("p", "grad_sorted slots grad_x"), ("q", "tokens cols ld_grad_sorted ld_grad_x"),
+                        ("i", "chosen dtype")])
+
+
+class MuonExpertCombineArgs(ctypes.Structure):
+    _fields_ = _fields([("p", "y slots weights out"), ("q", "tokens cols ld_y ld_out"), ("i", "chosen dtype")])
+
+
+class MuonExpertCombineBackwardArgs(ctypes.Structure):
+    _fields_ = _fields([("p", "grad_out y slots weights offsets grad_y grad_weights"),
+                        ("q", "tokens cols ld_grad_out ld_y ld_grad_y"), ("i", "chosen num_experts dtype")])
+
+
 class MuonProfile(ctypes.Structure):
     _fields_ = [("ms", ctypes.c_double * MUON_KCLASS_COUNT), ("launches", ctypes.c_int64 * MUON_KCLASS_COUNT)]
 
 
-_WORKSPACE_OPS = ("block_norm_backward", "token_logp", "token_logp_backward", "preference_loss", "policy_loss")
+_WORKSPACE_OPS = ("block_norm_backward", "token_logp", "token_logp_backward", "preference_loss", "policy_loss",
+                  "attention", "attention_backward", "expert_sort")
+_PLAIN_OPS = ("block_norm", "expert_sort_backward", "expert_combine", "expert_combine_backward")
 
 # Every symbol include/muon.h declares, with its ctypes signature.
 SIGNATURES = {
@@ -160,7 +203,7 @@ SIGNATURES = {
                                           ctypes.POINTER(MuonCayleyHparams), ctypes.c_void_p, ctypes.c_size_t,
                                           ctypes.c_void_p]),
     # the operators' arguments are one struct, by address (a ctypes instance or packed bytes)
-    "muon_block_norm": (ctypes.c_int32, [ctypes.c_void_p, ctypes.c_void_p]),
+    **{f"muon_{op}": (ctypes.c_int32, [ctypes.c_void_p, ctypes.c_void_p]) for op in _PLAIN_OPS},
     **{f"muon_{op}_workspace_bytes": (ctypes.c_size_t, [ctypes.c_void_p]) for op in _WORKSPACE_OPS},
     **{f"muon_{op}": (ctypes.c_int32, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p])
        for op in _WORKSPACE_OPS},
@@ -523,12 +566,15 @@ def muon_cayley_step(weights, grads, moms, *, lr, beta=0.9, workspace=None, stre
 
 def _packer(cls):
     kinds = {ctypes.c_void_p: "P", ctypes.c_int64: "q", ctypes.c_float: "f", ctypes.c_int32: "i"}
-    return struct.Struct("".join(kinds[t] for _, t in cls._fields_)).pack
+    return struct.Struct("".join(kinds[t] for _, t in cls._fields_) + "0q").pack      # to a whole struct, its padding too
 
 
 _pack_norm, _pack_norm_backward = _packer(MuonBlockNormArgs), _packer(MuonBlockNormBackwardArgs)
 _pack_logp, _pack_logp_backward = _packer(MuonTokenLogpArgs), _packer(MuonTokenLogpBackwardArgs)
 _pack_preference, _pack_policy = _packer(MuonPreferenceArgs), _packer(MuonPolicyArgs)
+_pack_attention, _pack_attention_backward = _packer(MuonAttentionArgs), _packer(MuonAttentionBackwardArgs)
+_pack_sort, _pack_sort_backward = _packer(MuonExpertSortArgs), _packer(MuonExpertSortBackwardArgs)
+_pack_combine, _pack_combine_backward = _packer(MuonExpertCombineArgs), _packer(MuonExpertCombineBackwardArgs)
 
 
 def _ptr(t):
@@ -551,8 +597,10 @@ def _pitch(t, what, shape, dtype):
     """Row pitch in elements of a matrix that has to have this shape and dtype and unit column stride."""
     if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{what} must be {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    pitch, step = t.stride()
     rows, cols = shape
+    if rows == 0:
+        return cols
+    pitch, step = t.stride()
     if step != 1 and cols > 1:
         raise ValueError(f"{what} must have unit column stride")
     if rows <= 1:
@@ -870,6 +918,246 @@ def muon_policy_loss(logp, old_logp, advantages, offsets, loss, grad_logp=None, 
     lib = load()
     return _call(lib.muon_policy_loss, lib.muon_policy_loss_workspace_bytes, packed, workspace, offsets.device, stream,
                  raw)
+
+
+# --------------------------------------------------------------------------
+# Operators inside a block (attention, tokens to experts and back)
+# --------------------------------------------------------------------------
+
+def _heads(t, what, shape, dtype):
+    """Pitches (token, head) in elements of a tokens x heads x width tensor of this shape and dtype, unit stride along width."""
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if shape[0] == 0:
+        return shape[1] * shape[2], shape[2]
+    ld, hs, step = t.stride()
+    if step != 1 and shape[2] > 1:
+        raise ValueError(f"{what} must have unit stride along the head width")
+    # the stride of a dimension of one is nobody's
+    hs = shape[2] if shape[1] <= 1 else hs
+    return (shape[1] * hs if shape[0] <= 1 else ld), hs
+
+
+def _attention_shape(q, k, v, offsets, key_offsets, key_mask, bias, bucket_map):
+    """(queries, keys, sequences, heads, kv_heads, width, buckets, reach, dtype code)."""
+    import torch
+    if q.dim() != 3 or k.dim() != 3 or q.shape[2] != k.shape[2] or (v is not None and v.shape != k.shape):
+        raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)} and v must be tokens x heads x width, k and v of one shape")
+    (queries, heads, width), (keys, kv_heads) = q.shape, k.shape[:2]
+    sequences = 1
+    for t, what in ((offsets, "offsets"), (key_offsets, "key_offsets")):
+        if t is not None:
+            if t.dim() != 1 or t.shape[0] < 2 or t.dtype != torch.int64 or not t.is_contiguous():
+                raise ValueError(f"{what} must be a contiguous int64 vector of sequences + 1")
+            if what == "key_offsets" and (offsets is None or t.shape != offsets.shape):
+                raise ValueError("key_offsets must have the length of offsets")
+            sequences = t.shape[0] - 1
+    if key_mask is not None:
+        _check_vector(key_mask, "key_mask", keys, torch.uint8, torch.bool)
+    buckets = reach = 0
+    if (bias is None) != (bucket_map is None):
+        raise ValueError("bias and bucket_map go together")
+    if bias is not None:
+        if bias.dim() != 2 or bias.shape[1] != heads or bias.dtype != q.dtype or not bias.is_contiguous():
+            raise ValueError(f"bias must be contiguous {q.dtype} of buckets x {heads} heads, got {bias.dtype} {tuple(bias.shape)}")
+        if bucket_map.dim() != 1 or bucket_map.shape[0] % 2 != 1 or bucket_map.dtype != torch.int32 or not bucket_map.is_contiguous():
+            raise ValueError("bucket_map must be a contiguous int32 vector of 2 reach + 1")
+        buckets, reach = bias.shape[0], bucket_map.shape[0] // 2
+    return queries, keys, sequences, heads, kv_heads, width, buckets, reach, _dtype_code(q)
+
+
+def _attention_scale(scale, width):
+    return width ** -0.5 if scale is None else scale
+
+
+def muon_attention_workspace_bytes(q, k, *, sequences=1) -> int:
+    """Workspace of :func:`muon_attention` for these shapes."""
+    n, m, _, heads, kv_heads, width, _, _, code = _attention_shape(q, k, None, None, None, None, None, None)
+    # sizes only: distinct stand-in addresses, never dereferenced
+    at = [j << 44 for j in range(1, 8)]
+    lq, lk = heads * width, kv_heads * width
+    return _size(load().muon_attention_workspace_bytes,
+                 _pack_attention(at[0], at[1], at[2], at[3], 0, 0, 0, 0, at[4], at[5], 0, n, m, sequences, lq, width, lk,
+                                 width, lk, width, lq, width, 0, 0, 0, 1.0, heads, kv_heads, width, 0, 0, 0, code))
+
+
+def muon_attention(q, k, v, out, lse, *, offsets=None, key_offsets=None, key_mask=None, bias=None, bucket_map=None,
+                   scale=None, causal=False, window=0, out_low=None, workspace=None, stream=None):
+    """Softmax attention over packed sequences, with a learned relative position bias where one is given.
+
+    ``q`` and ``out`` are queries x heads x width, ``k`` and ``v`` keys x kv_heads x width (heads a multiple of
+    kv_heads), of any token and head strides; ``lse`` is float32, queries x heads.  Sequence s is
+    ``q[offsets[s]:offsets[s + 1]]`` over ``k[key_offsets[s]:key_offsets[s + 1]]`` (int64 on the GPU; ``key_offsets``
+    None: the same as ``offsets``; both None: one sequence).  The last query of a sequence stands at its last key;
+    ``causal`` hides the keys behind a query, ``window`` those at that distance or farther, ``key_mask`` 0 a key.
+    ``scale`` defaults to ``width ** -0.5``.  ``bias[b, h]`` (buckets x heads, like q) is added at the distances whose
+    entry of ``bucket_map`` (int32, for the distances key - query from -reach to reach, farther ones as those) is b.
+    ``out_low`` (like out) keeps what rounding took from ``out`` for :func:`muon_attention_backward`.
+    """
+    import torch
+    n, m, sequences, heads, kv_heads, width, buckets, reach, code = _attention_shape(
+        q, k, v, offsets, key_offsets, key_mask, bias, bucket_map)
+    shape, dtype = q.shape, q.dtype
+    if offsets is not None and key_offsets is None and n != m:
+        raise ValueError("queries and keys differ: key_offsets is needed")
+    if lse.dtype != torch.float32 or lse.shape != shape[:2] or not lse.is_contiguous():
+        raise ValueError(f"lse must be contiguous float32 of shape {tuple(shape[:2])}")
+    packed = _pack_attention(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(offsets), _ptr(key_offsets), _ptr(key_mask), _ptr(bias),
+        _ptr(bucket_map), out.data_ptr(), lse.data_ptr(), _ptr(out_low), n, m, sequences, *_heads(q, "q", shape, dtype),
+        *_heads(k, "k", k.shape, dtype), *_heads(v, "v", k.shape, dtype), *_heads(out, "out", shape, dtype),
+        *((0, 0) if out_low is None else _heads(out_low, "out_low", shape, dtype)), window,
+        _attention_scale(scale, width), heads, kv_heads, width, buckets, reach, 1 if causal else 0, code)
+    raw = _raw_stream(stream, q, k, v, offsets, key_offsets, key_mask, bias, bucket_map, out, lse, out_low, workspace)
+    lib = load()
+    return _call(lib.muon_attention, lib.muon_attention_workspace_bytes, packed, workspace, q.device, stream, raw)
+
+
+def muon_attention_backward_workspace_bytes(q, k, *, sequences=1, bias=None, bucket_map=None) -> int:
+    """Workspace of :func:`muon_attention_backward` for these shapes."""
+    n, m, _, heads, kv_heads, width, buckets, reach, code = _attention_shape(q, k, None, None, None, None, bias, bucket_map)
+    at = [j << 44 for j in range(1, 16)]
+    lq, lk, b = heads * width, kv_heads * width, bias is not None
+    return _size(load().muon_attention_backward_workspace_bytes, _pack_attention_backward(
+        at[0], at[1], at[2], at[3], 0, 0, at[4] if b else 0, at[5] if b else 0, at[6], at[7], 0, at[8], at[9], at[10],
+        at[11], at[12] if b else 0, n, m, sequences, lq, width, lk, width, lk, width, lq, width, 0, 0, lq, width, lq, width,
+        lk, width, lk, width, 0, 1.0, heads, kv_heads, width, buckets, reach, 0, code))
+
+
+def muon_attention_backward(q, k, v, out, lse, grad_out, grad_q, grad_k, grad_v, *, offsets=None, key_offsets=None,
+                            key_mask=None, bias=None, bucket_map=None, grad_bias=None, scale=None, causal=False, window=0,
+                            out_low=None, workspace=None, stream=None):
+    """Gradients of :func:`muon_attention` for the gradient ``grad_out`` of its ``out``.
+
+    The arguments that it shares with the forward call are that call's, ``out``, ``lse`` and ``out_low`` (which may be
+    None) what it wrote.  ``grad_k`` and ``grad_v`` are summed over the heads that share a key head, ``grad_bias`` over
+    all pairs of a bucket.
+    """
+    import torch
+    n, m, sequences, heads, kv_heads, width, buckets, reach, code = _attention_shape(
+        q, k, v, offsets, key_offsets, key_mask, bias, bucket_map)
+    shape, dtype = q.shape, q.dtype
+    if offsets is not None and key_offsets is None and n != m:
+        raise ValueError("queries and keys differ: key_offsets is needed")
+    if lse.dtype != torch.float32 or lse.shape != shape[:2] or not lse.is_contiguous():
+        raise ValueError(f"lse must be contiguous float32 of shape {tuple(shape[:2])}")
+    if (bias is None) != (grad_bias is None):
+        raise ValueError("bias and its gradient go together")
+    if bias is not None and (grad_bias.shape != bias.shape or grad_bias.dtype != dtype or not grad_bias.is_contiguous()):
+        raise ValueError(f"grad_bias must be like bias, contiguous {dtype} of shape {tuple(bias.shape)}")
+    packed = _pack_attention_backward(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(offsets), _ptr(key_offsets), _ptr(key_mask), _ptr(bias),
+        _ptr(bucket_map), out.data_ptr(), lse.data_ptr(), _ptr(out_low), grad_out.data_ptr(), grad_q.data_ptr(),
+        grad_k.data_ptr(), grad_v.data_ptr(), _ptr(grad_bias), n, m, sequences, *_heads(q, "q", shape, dtype),
+        *_heads(k, "k", k.shape, dtype), *_heads(v, "v", k.shape, dtype), *_heads(out, "out", shape, dtype),
+        *((0, 0) if out_low is None else _heads(out_low, "out_low", shape, dtype)),
+        *_heads(grad_out, "grad_out", shape, dtype), *_heads(grad_q, "grad_q", shape, dtype),
+        *_heads(grad_k, "grad_k", k.shape, dtype), *_heads(grad_v, "grad_v", k.shape, dtype), window,
+        _attention_scale(scale, width), heads, kv_heads, width, buckets, reach, 1 if causal else 0, code)
+    raw = _raw_stream(stream, q, k, v, offsets, key_offsets, key_mask, bias, bucket_map, out, lse, out_low, grad_out, grad_q,
+                      grad_k, grad_v, grad_bias, workspace)
+    lib = load()
+    return _call(lib.muon_attention_backward, lib.muon_attention_backward_workspace_bytes, packed, workspace, q.device,
+                 stream, raw)
+
+
+def _choices(t, what, tokens, dtype):
+    """The number of choices a token of a contiguous tokens x chosen tensor."""
+    if t.dim() != 2 or t.shape[0] != tokens or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous {dtype} of {tokens} tokens x choices, got {t.dtype} {tuple(t.shape)}")
+    return t.shape[1]
+
+
+def _matrix_shape(t, what):
+    if t.dim() != 2:
+        raise ValueError(f"{what} must be 2-D, got shape {tuple(t.shape)}")
+    return t.shape
+
+
+def muon_expert_sort_workspace_bytes(x, experts, num_experts) -> int:
+    """Workspace of :func:`muon_expert_sort` for these shapes."""
+    import torch
+    tokens, cols = _matrix_shape(x, "x")
+    chosen = _choices(experts, "experts", tokens, torch.int64)
+    at = [j << 44 for j in range(1, 6)]
+    return _size(load().muon_expert_sort_workspace_bytes,
+                 _pack_sort(*at, tokens, cols, cols, cols, chosen, num_experts, _dtype_code(x)))
+
+
+def muon_expert_sort(x, experts, sorted_x, slots, offsets, *, workspace=None, stream=None):
+    """Every token's row once for each expert that it goes to, in the order of the experts.
+
+    ``experts`` (int64, tokens x chosen) names them; a value outside the experts is a dropped choice.  ``sorted_x``
+    has tokens * chosen rows: expert e's are ``sorted_x[offsets[e]:offsets[e + 1]]`` (``offsets``: int64, experts + 1),
+    within it in the order of the tokens and their choices; rows behind the last are 0.  ``slots`` (int32, like
+    ``experts``) is each choice's row, -1 for a dropped one.
+    """
+    import torch
+    tokens, cols = _matrix_shape(x, "x")
+    chosen = _choices(experts, "experts", tokens, torch.int64)
+    if _choices(slots, "slots", tokens, torch.int32) != chosen:
+        raise ValueError("slots must have the shape of experts")
+    if offsets.dim() != 1 or offsets.shape[0] < 2 or offsets.dtype != torch.int64 or not offsets.is_contiguous():
+        raise ValueError("offsets must be a contiguous int64 vector of experts + 1")
+    packed = _pack_sort(x.data_ptr(), experts.data_ptr(), sorted_x.data_ptr(), slots.data_ptr(), offsets.data_ptr(), tokens,
+                        cols, _pitch(x, "x", x.shape, x.dtype), _pitch(sorted_x, "sorted_x", (tokens * chosen, cols), x.dtype),
+                        chosen, offsets.shape[0] - 1, _dtype_code(x))
+    raw = _raw_stream(stream, x, experts, sorted_x, slots, offsets, workspace)
+    lib = load()
+    return _call(lib.muon_expert_sort, lib.muon_expert_sort_workspace_bytes, packed, workspace, x.device, stream, raw)
+
+
+def muon_expert_sort_backward(grad_sorted, slots, grad_x, *, stream=None):
+    """Gradient of :func:`muon_expert_sort` with respect to ``x``: the sum of a token's rows of ``grad_sorted``."""
+    import torch
+    tokens, cols = _matrix_shape(grad_x, "grad_x")
+    chosen = _choices(slots, "slots", tokens, torch.int32)
+    packed = _pack_sort_backward(
+        grad_sorted.data_ptr(), slots.data_ptr(), grad_x.data_ptr(), tokens, cols,
+        _pitch(grad_sorted, "grad_sorted", (tokens * chosen, cols), grad_x.dtype),
+        _pitch(grad_x, "grad_x", grad_x.shape, grad_x.dtype), chosen, _dtype_code(grad_x))
+    raw = _raw_stream(stream, grad_x, grad_sorted, slots)
+    _check(load().muon_expert_sort_backward(packed, raw))
+
+
+def muon_expert_combine(y, slots, weights, out, *, stream=None):
+    """``out[t]`` = the sum of ``weights[t, c] * y[slots[t, c]]`` over a token's choices that were not dropped.
+
+    ``y`` holds the experts' outputs in the order of :func:`muon_expert_sort`; ``weights`` is float32, tokens x chosen.
+    """
+    import torch
+    tokens, cols = _matrix_shape(out, "out")
+    chosen = _choices(slots, "slots", tokens, torch.int32)
+    if _choices(weights, "weights", tokens, torch.float32) != chosen:
+        raise ValueError("weights must have the shape of slots")
+    packed = _pack_combine(y.data_ptr(), slots.data_ptr(), weights.data_ptr(), out.data_ptr(), tokens, cols,
+                           _pitch(y, "y", (tokens * chosen, cols), out.dtype), _pitch(out, "out", out.shape, out.dtype),
+                           chosen, _dtype_code(out))
+    raw = _raw_stream(stream, out, y, slots, weights)
+    _check(load().muon_expert_combine(packed, raw))
+
+
+def muon_expert_combine_backward(grad_out, y, slots, weights, offsets, grad_y, grad_weights, *, stream=None):
+    """Gradients of :func:`muon_expert_combine`; ``slots`` and ``offsets`` are what :func:`muon_expert_sort` wrote.
+
+    Rows of ``grad_y`` behind the last expert's are 0, and ``grad_weights`` (float32, like ``weights``) is 0 for a
+    dropped choice.
+    """
+    import torch
+    tokens, cols = _matrix_shape(grad_out, "grad_out")
+    chosen = _choices(slots, "slots", tokens, torch.int32)
+    for t, what in ((weights, "weights"), (grad_weights, "grad_weights")):
+        if _choices(t, what, tokens, torch.float32) != chosen:
+            raise ValueError(f"{what} must have the shape of slots")
+    if offsets.dim() != 1 or offsets.shape[0] < 2 or offsets.dtype != torch.int64 or not offsets.is_contiguous():
+        raise ValueError("offsets must be a contiguous int64 vector of experts + 1")
+    rows, dtype = (tokens * chosen, cols), grad_out.dtype
+    packed = _pack_combine_backward(
+        grad_out.data_ptr(), y.data_ptr(), slots.data_ptr(), weights.data_ptr(), offsets.data_ptr(), grad_y.data_ptr(),
+        grad_weights.data_ptr(), tokens, cols, _pitch(grad_out, "grad_out", grad_out.shape, dtype), _pitch(y, "y", rows, dtype),
+        _pitch(grad_y, "grad_y", rows, dtype), chosen, offsets.shape[0] - 1, _dtype_code(grad_out))
+    raw = _raw_stream(stream, grad_out, y, slots, weights, offsets, grad_y, grad_weights)
+    _check(load().muon_expert_combine_backward(packed, raw))
 
 
 def muon_profile_enable(on: bool = True):

@@ -1,0 +1,1020 @@
+// Attention over packed sequences, forward and backward (formulas: muon.h), on the matrix cores.
+//
+// Forward and grad_q: a workgroup of 4 waves takes 128 queries of one head, a wave 32 of them, and walks over the keys a tile
+// at a time.  The scores are formed transposed, S^T = K Q^T: a lane then holds one query's scores, so the softmax's maximum and
+// sum are a lane's own business but for one exchange with lane l ^ 32, a rescale is a factor a lane, and the
+// probabilities are at once the operand of O^T = V^T P^T (attention_tile.h).
+// grad_k and grad_v: a workgroup takes 128 keys of one key head, a wave 32 of them, and walks over the queries of every head that
+// shares it; S = Q K^T comes out with one key a lane, ready for dV^T = dO^T P and dK^T = Q^T dS.  Two kernels form the
+// scores twice (7 products where one kernel would need 5), but no sum is shared between workgroups: no atomics, the
+// same bits on every run, and shared key heads add up in registers.
+//
+// Both tiles of a walk are double-buffered in LDS; a step's loads are issued before the step before it is computed, with
+// one barrier a step.  Two workgroups run on a CU.
+#include <algorithm>
+
+#include "attention_tile.h"
+
+namespace muon {
+
+namespace {
+
+using namespace at;
+
+constexpr int AT_THREADS = 256, AT_WAVES = 4, AT_ROWS = 128;   // rows (queries or keys) a workgroup
+constexpr int AT_MAX_SPLITS = 64;
+
+// Rows of a walked tile.
+template <typename T> constexpr int walk_rows() { return sizeof(T) == 2 ? 64 : 32; }
+
+struct Common {
+    muon_attention_args a;
+    int64_t unit0;        // first unit of this launch
+    int64_t units;        // of the whole call: span_units x heads x splits
+    int splits;
+    int vec_in, vec_out;  // rows come in whole 16-byte chunks
+    int window;           // 0: none
+    int gqa;              // heads / kv_heads
+};
+struct ForwardArgs {
+    Common c;
+    float* part;          // splits > 1: out before its division, [split][query][head][width], then maximum and sum, [split][query][head]
+};
+struct BackwardArgs {
+    Common c;             // c.a.out, out_low: the forward call's
+    const void* grad_out;
+    void* grad_q;
+    void* grad_k;
+    void* grad_v;
+    int64_t ld_do, hs_do, ld_dq, hs_dq, ld_dk, hs_dk, ld_dv, hs_dv;
+    float* delta;         // query x head
+    float* part;          // splits > 1: sums of each split
+    float* bias_part;     // [head][slot][2 reach + 1], a slot per wave
+    int64_t slots;
+};
+
+// Which unit of the axis, head and split a workgroup has.  Heads go fastest, and where they allow it in runs that share an XCD
+// (workgroups go to XCDs in turn), so that a key head's rows stay in one L2; units from the end first: under a causal mask
+// they are the longest.
+__device__ __forceinline__ void decode(int64_t id, int heads, int splits, int64_t axis, int& u, int& head, int& split) {
+    const int hs = heads * splits;
+    const int64_t r = id / hs;
+    int k = static_cast<int>(id - r * hs);
+    if (hs % 8 == 0) k = (k % 8) * (hs / 8) + k / 8;
+    head = k / splits;
+    split = k - head * splits;
+    u = static_cast<int>(axis - 1 - r);
+}
+
+// Bias of a head at distance j - a.
+template <typename T> __device__ __forceinline__ int bucket_at(const muon_attention_args& a, int dist) {
+    const int r = a.reach, d = dist < -r ? -r : dist > r ? r : dist;
+    return G(a.bucket_map)[d + r];
+}
+template <typename T> __device__ __forceinline__ float bias_value(const muon_attention_args& a, int bucket, int head) {
+    const bool ok = static_cast<unsigned>(bucket) < static_cast<unsigned>(a.buckets);
+    return ok ? ld_el<T>(static_cast<const T*>(a.bias), static_cast<size_t>(bucket) * a.heads + head) : 0.0f;
+}
+
+// Bias over the distances between a tile of rows and one of keys, a buffer of it a tile.  The bucket of the tile after next
+// and the value of the next one are under way while a tile is computed.
+template <typename T, int N> struct BiasWindow {
+    static_assert(N <= AT_THREADS, "one distance a thread");
+    int bucket = 0;
+    float value = 0.0f;
+    __device__ __forceinline__ void ask(const muon_attention_args& a, int first) { if (static_cast<int>(threadIdx.x) < N) bucket = bucket_at<T>(a, first + static_cast<int>(threadIdx.x)); }
+    __device__ __forceinline__ void fetch(const muon_attention_args& a, int head) { if (static_cast<int>(threadIdx.x) < N) value = bias_value<T>(a, bucket, head); }
+    __device__ __forceinline__ void put(lds_float_t* buf) const { if (static_cast<int>(threadIdx.x) < N) buf[threadIdx.x] = value; }
+};
+
+// Keys that a lane's query sees are lo .. lo + span - 1; how a wave's 32 queries stand to a tile of keys.
+struct Sight {
+    int lo;
+    unsigned span;
+    __device__ __forceinline__ void set(int l, int h) { lo = l; span = h > l ? h - l : 0; }
+};
+enum { NOTHING = 0, SOME = 1, ALL = 2 };
+// Queries at key positions a0 .. a1, keys j0 .. j1, all of them within the sequence.
+__device__ __forceinline__ int tile_sight(int a0, int a1, int j0, int j1, bool causal, int window) {
+    if (causal && j0 > a1) return NOTHING;
+    if (window && (j1 <= a0 - window || j0 >= a1 + window)) return NOTHING;
+    if (causal && j1 > a0) return SOME;
+    if (window && (j0 <= a1 - window || j1 >= a0 + window)) return SOME;
+    return ALL;
+}
+// Scores outside a lane's sight to -infinity: register i stands for place at + 8 (i / 4) + i % 4 (4 h is in `at`); bits: the
+// key mask of those places.
+__device__ __forceinline__ void hide(f32x16_t& s, const Sight& v, int at) {
+    const int t = at - v.lo;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[i] = static_cast<unsigned>(t + 8 * (i >> 2) + (i & 3)) < v.span ? s[i] : NEG_INF;
+}
+__device__ __forceinline__ void hide_masked(f32x16_t& s, uint32_t bits) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[i] = (bits >> (8 * (i >> 2) + (i & 3))) & 1u ? s[i] : NEG_INF;
+}
+
+// Walk of a wave's 32 queries over tiles of keys: what the forward and the grad_q kernel share.
+template <typename T, int DP> struct KeyWalk {
+    static constexpr int BN = walk_rows<T>(), NB = BN / 32, KS = DP / 16;
+    static constexpr int TILE = BN * Row<T, DP>::BYTES;
+    static constexpr int WIN = AT_ROWS + BN;          // distances between 128 queries and a tile of keys (one to spare)
+    const muon_attention_args& a;
+    Span sp;
+    int head, wave_at;                                // this wave's first query in its sequence
+    int off;                                          // key position of query 0
+    int first, last;                                  // tiles
+    const T* kbase;
+    const T* vbase;
+    uint64_t pending;
+
+    __device__ __forceinline__ KeyWalk(const Common& c, const Span& s, int h, int split) : a(c.a), sp(s), head(h) {
+        wave_at = sp.at + 32 * wave_id();
+        off = sp.other_len - sp.len;
+        const int a0 = sp.at + off, a1 = sp.at + min(sp.rows, AT_ROWS) - 1 + off;
+        int lo = 0, hi = sp.other_len;
+        if (a.causal) hi = min(hi, a1 + 1);
+        if (c.window) { lo = max(lo, a0 - c.window + 1); hi = min(hi, a1 + c.window); }
+        const int t0 = lo / BN, n = hi > lo ? (hi + BN - 1) / BN - t0 : 0;
+        first = t0 + static_cast<int>(static_cast<int64_t>(n) * split / c.splits);
+        last = t0 + static_cast<int>(static_cast<int64_t>(n) * (split + 1) / c.splits);
+        const int kv = head / c.gqa;
+        kbase = static_cast<const T*>(a.k) + static_cast<int64_t>(sp.other) * a.ld_k + static_cast<int64_t>(kv) * a.hs_k;
+        vbase = static_cast<const T*>(a.v) + static_cast<int64_t>(sp.other) * a.ld_v + static_cast<int64_t>(kv) * a.hs_v;
+    }
+    // What this lane's key of tile t is worth: its mask byte.
+    __device__ __forceinline__ unsigned key_byte(int t) const {
+        const int j = t * BN + static_cast<int>(threadIdx.x & 63);
+        const bool in = j < sp.other_len && static_cast<int>(threadIdx.x & 63) < BN;
+        return in ? (a.key_mask ? G(a.key_mask)[sp.other + j] : 1u) : 0u;
+    }
+    __device__ __forceinline__ void load(int t, lds_byte_t* k, lds_byte_t* v, uint64_t live, bool vec) const {
+        const int64_t j = static_cast<int64_t>(t) * BN;
+        load_tile<T, DP, BN, AT_THREADS>(k, kbase + j * a.ld_k, a.ld_k, a.width, live, vec);
+        load_tile<T, DP, BN, AT_THREADS>(v, vbase + j * a.ld_v, a.ld_v, a.width, live, vec);
+    }
+    __device__ __forceinline__ Sight sight(const Common& c, int at) const {      // of the query at place `at`
+        const int p = at + off;
+        int lo = 0, hi = sp.other_len;
+        if (a.causal) hi = min(hi, p + 1);
+        if (c.window) { lo = max(lo, p - c.window + 1); hi = min(hi, p + c.window); }
+        Sight s;
+        s.set(lo, at < sp.len ? hi : lo);
+        return s;
+    }
+    // Scores of tile t (raw products) with what the wave sees of it; false if nothing.
+    __device__ __forceinline__ int seen(const Common& c, int t, uint64_t live) const {
+        const int j0 = t * BN, a0 = wave_at + off, a1 = a0 + 31;
+        constexpr uint64_t full = BN == 64 ? ~0ull : (1ull << (BN & 63)) - 1;
+        const int s = wave_at >= sp.len ? NOTHING : tile_sight(a0, a1, j0, j0 + BN - 1, a.causal, c.window);
+        return s == ALL && live != full ? SOME : s;
+    }
+    // Distance of the window's first entry for tile t.
+    __device__ __forceinline__ int window_first(int t) const { return t * BN - (sp.at + AT_ROWS - 1 + off); }
+    // z = scale x + bias (natural units) for one block; w: the tile's window, NULL: `far` everywhere.
+    __device__ __forceinline__ void add_bias(f32x16_t& s, float scale, const lds_float_t* w, float far, int nb) const {
+        const int lane = threadIdx.x & 63;
+        if (w) {
+            // entry of key 32 nb + 8 (i / 4) + 4 h + i % 4 and query 32 wave + l % 32
+            const lds_float_t* p = w + (AT_ROWS - 1 - 32 * wave_id() - (lane & 31)) + 32 * nb + 4 * (lane >> 5);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[i] = fmaf(s[i], scale, p[8 * (i >> 2) + (i & 3)]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[i] = fmaf(s[i], scale, far);
+        }
+    }
+    // Is the bias one value over this wave's part of tile t?  -1 / 1: the one below / above, 0: no.
+    __device__ __forceinline__ int far(int t) const {
+        const int j0 = t * BN, a0 = wave_at + off;
+        if (j0 + BN - 1 - a0 <= -a.reach) return -1;
+        return j0 - (a0 + 31) >= a.reach ? 1 : 0;
+    }
+};
+
+// ---- forward --------------------------------------------------------------------
+
+template <typename T, int DP, bool BIAS>
+__global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 ? 2 : 1) void attention_forward_kernel(ForwardArgs f) {
+    typedef KeyWalk<T, DP> W;
+    constexpr int NB = W::NB, KS = W::KS, DB = DP / 32;
+    __shared__ u32x4_t lds[4 * W::TILE / 16];
+    __shared__ float win[BIAS ? 2 * W::WIN : 1];
+    const Common& c = f.c;
+    const muon_attention_args& a = c.a;
+    int u, head, split;
+    decode(c.unit0 + blockIdx.x, a.heads, c.splits, span_units(a.queries, a.sequences, AT_ROWS), u, head, split);
+    Span sp;
+    if (!find_span<AT_ROWS>(a.offsets, a.key_offsets, static_cast<int>(a.sequences), static_cast<int>(a.queries), static_cast<int>(a.keys), u, sp)) return;
+    const W w(c, sp, head, split);
+    const int lane = threadIdx.x & 63, place = w.wave_at + (lane & 31);
+    const bool row_ok = place < sp.len;
+    const int64_t row = sp.start - sp.at + place;
+    const Sight sight = w.sight(c, place);
+    lds_byte_t* buf = (lds_byte_t*)lds;
+    lds_float_t* wbuf = (lds_float_t*)win;
+
+    // a negative scale goes into q's sign and a scale of 0 into q, so that the largest score is the largest product
+    Frag<T> qf[KS];
+    {
+        const T* q = static_cast<const T*>(a.q) + row * a.ld_q + static_cast<int64_t>(head) * a.hs_q;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            qf[ks] = global_frag<T>(q, 16 * ks + 8 * (lane >> 5), a.width, row_ok && a.scale != 0.0f);
+            if (a.scale < 0.0f) {
+                if constexpr (sizeof(T) == 2) qf[ks].w ^= 0x80008000u;
+                else { qf[ks].w[0] = -qf[ks].w[0]; qf[ks].w[1] = -qf[ks].w[1]; }
+            }
+        }
+    }
+    const float scale = a.scale == 0.0f ? 1.0f : fabsf(a.scale), unit = BIAS ? LOG2E : scale * LOG2E;     // from what s holds to powers of two
+    const float slack = 8.0f / LOG2E * (BIAS ? 1.0f : LOG2E);                    // 8 powers of two, in m's units
+
+    f32x16_t o[DB] = {};
+    float m = NEG_INF, l = 0.0f;      // BIAS: natural units, else powers of two; l: this lane's half of the row
+    BiasWindow<T, W::WIN> bw;
+    float far_lo = 0.0f, far_hi = 0.0f;
+    unsigned byte = 0;
+    uint64_t live = 0, next = 0;
+    if (w.first < w.last) {
+        next = __ballot(w.key_byte(w.first) != 0);
+        w.load(w.first, buf, buf + W::TILE, next, c.vec_in);
+        byte = w.key_byte(w.first + 1);
+        if constexpr (BIAS) {
+            far_lo = bias_value<T>(a, bucket_at<T>(a, -a.reach), head);
+            far_hi = bias_value<T>(a, bucket_at<T>(a, a.reach), head);
+            bw.ask(a, w.window_first(w.first));
+            bw.fetch(a, head);
+            bw.put(wbuf);
+            bw.ask(a, w.window_first(w.first + 1));
+        }
+    }
+    for (int t = w.first; t < w.last; ++t) {
+        const int b = (t - w.first) & 1;
+        tile_barrier();
+        live = next;
+        if (t + 1 < w.last) {
+            next = __ballot(byte != 0);
+            w.load(t + 1, buf + 2 * W::TILE * (b ^ 1), buf + 2 * W::TILE * (b ^ 1) + W::TILE, next, c.vec_in);
+            byte = w.key_byte(t + 2);
+            if constexpr (BIAS) {
+                bw.fetch(a, head);
+                bw.ask(a, w.window_first(t + 2));
+            }
+        }
+        const int seen = w.seen(c, t, live);
+        if (seen != NOTHING) {
+            const lds_byte_t* kt = buf + 2 * W::TILE * b;
+            const lds_byte_t* vt = kt + W::TILE;
+            f32x16_t s[NB] = {};
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) mma(s[nb], row_frag<T, DP>(kt, 32 * nb, ks), qf[ks]);
+            if constexpr (BIAS) {
+                const int far = w.far(t);
+                const lds_float_t* p = far ? nullptr : wbuf + b * W::WIN;
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) w.add_bias(s[nb], scale, p, far < 0 ? far_lo : far_hi, nb);
+            }
+            if (seen == SOME) {
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    hide(s[nb], sight, t * W::BN + 32 * nb + 4 * (lane >> 5));
+                    if (a.key_mask) hide_masked(s[nb], static_cast<uint32_t>(live >> (32 * nb + 4 * (lane >> 5))));
+                }
+            }
+            float top = NEG_INF;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) top = fmaxf(top, s[nb][i]);
+            top = half_max(top);
+            if constexpr (!BIAS) top *= unit;
+            // The reference follows the maximum only when it has grown by more than 2^8: the terms stay below 2^8, and
+            // most tiles need no rescale.
+            if (__any(top > m + slack)) {
+                const float r = top > m + slack ? top : m;
+                const float f2 = r == m ? 1.0f : exp2_((m - r) * (BIAS ? LOG2E : 1.0f));
+                m = r;
+                l *= f2;
+#pragma unroll
+                for (int db = 0; db < DB; ++db) o[db] *= f2;
+            }
+            const float ref = m == NEG_INF ? 0.0f : m;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    s[nb][i] = BIAS ? exp2_((s[nb][i] - ref) * unit) : exp2_(fmaf(s[nb][i], unit, -ref));
+                    l += s[nb][i];
+                }
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const Parts<T> p(s[nb], g);
+#pragma unroll
+                    for (int db = 0; db < DB; ++db) p.mma_to(o[db], col_frag<T, DP>(vt, 32 * nb + 16 * g, db));
+                }
+        }
+        if constexpr (BIAS)
+            if (t + 1 < w.last) bw.put(wbuf + (b ^ 1) * W::WIN);
+    }
+    l = half_sum(l);
+    if (!row_ok) return;
+    if (c.splits > 1) {
+        const int64_t at = row * a.heads + head, n = a.queries * a.heads;
+        float* o_part = f.part + (split * n + at) * a.width;
+        float* ml = f.part + c.splits * n * a.width + (split * n + at) * 2;
+        store_rows<float>(o, 1.0f, o_part, static_cast<float*>(nullptr), a.width, a.width % 4 == 0);
+        if (lane < 32) {
+            G(ml)[0] = m;
+            G(ml)[1] = l;
+        }
+        return;
+    }
+    T* out = static_cast<T*>(a.out) + row * a.ld_out + static_cast<int64_t>(head) * a.hs_out;
+    T* low = a.out_low ? static_cast<T*>(a.out_low) + row * a.ld_out_low + static_cast<int64_t>(head) * a.hs_out_low : nullptr;
+    store_rows<T>(o, l == 0.0f ? 0.0f : 1.0f / l, out, low, a.width, c.vec_out);
+    if (lane < 32) G(a.lse)[row * a.heads + head] = l == 0.0f ? NEG_INF : (BIAS ? m : m * LN2) + __logf(l);
+}
+
+// Joins the splits of a row: a wave each.
+template <typename T, bool BIAS> __global__ __launch_bounds__(256) void attention_join_kernel(ForwardArgs f, int64_t row0) {
+    const Common& c = f.c;
+    const muon_attention_args& a = c.a;
+    const int64_t n = a.queries * a.heads, at = row0 + static_cast<int64_t>(blockIdx.x) * 4 + wave_id();
+    if (at >= n) return;
+    const int lane = threadIdx.x & 63;
+    const float* ml = f.part + c.splits * n * a.width;
+    float m = NEG_INF, l = 0.0f;
+    if (lane < c.splits) {
+        m = G(ml)[(lane * n + at) * 2];
+        l = G(ml)[(lane * n + at) * 2 + 1];
+    }
+    float top = m;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+    const float unit = BIAS ? LOG2E : 1.0f;
+    const float f2 = m == top || l == 0.0f ? (l == 0.0f ? 0.0f : 1.0f) : exp2_((m - top) * unit);
+    const float sum = wave_sum(l * f2);
+    float v[2] = {};
+    for (int s = 0; s < c.splits; ++s) {
+        const float fs = __shfl(f2, s);
+        const float* p = f.part + (s * n + at) * a.width;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (lane + 64 * k < a.width && fs != 0.0f) v[k] = fmaf(G(p)[lane + 64 * k], fs, v[k]);
+    }
+    const int64_t row = at / a.heads;
+    const int head = static_cast<int>(at - row * a.heads);
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        if (lane + 64 * k < a.width) {
+            const float x = v[k] * inv;
+            st_el<T>(a.out, row * a.ld_out + static_cast<int64_t>(head) * a.hs_out + lane + 64 * k, x);
+            if (a.out_low)
+                st_el<T>(a.out_low, row * a.ld_out_low + static_cast<int64_t>(head) * a.hs_out_low + lane + 64 * k,
+                         sizeof(T) == 2 ? x - bf16_to_f32(f32_to_bf16(x)) : 0.0f);
+        }
+    if (lane == 0) G(a.lse)[at] = sum == 0.0f ? NEG_INF : (BIAS ? top : top * LN2) + __logf(sum);
+}
+
+// ---- grad_q, and the bias's gradient --------------------------------------------
+
+// Sums of dz over the distances that a wave meets.  A tile's dz is added up in 128 places of LDS by distance modulo 128, the
+// two halves of the wave apart: an instruction then meets no place twice, and a wave's own adds come in order, so the sums are the
+// same on every run.  The walk moves by a tile's keys, so that as many of the smallest distances are complete after a tile and go to
+// the wave's slot.  Distances beyond the reach have one bucket a side and add up in registers.
+struct BiasSums {
+    lds_float_t* place;      // 2 x 128, this wave's own
+    float* slot;             // 2 reach + 1
+    int reach, begin, next;  // distances written to the slot: begin .. next - 1; next: the first one in `place`
+    bool any;
+    float below, above;
+    __device__ __forceinline__ void start(lds_float_t* p, float* s, int r) {
+        place = p;
+        slot = s;
+        reach = r;
+        begin = next = 0;
+        any = false;
+        below = above = 0.0f;
+        for (int i = threadIdx.x & 63; i < 256; i += 64) place[i] = 0.0f;
+    }
+    // one block of dz: register i at distance dist + 8 (i / 4) + i % 4
+    __device__ __forceinline__ void add(const f32x16_t& dz, int dist) {
+        lds_float_t* p = place + 128 * ((threadIdx.x & 63) >> 5);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) __builtin_amdgcn_ds_faddf(p + ((dist + 8 * (i >> 2) + (i & 3)) & 127), dz[i], 0, 0, false);
+    }
+    __device__ __forceinline__ void flush(int n) {
+        const int lane = threadIdx.x & 63;
+        if (lane < n) {
+            const int dist = next + lane;
+            lds_float_t* p = place + (dist & 127);
+            const float v = p[0] + p[128];
+            p[0] = 0.0f;
+            p[128] = 0.0f;
+            if (dist <= -reach) below += v;
+            else if (dist >= reach) above += v;
+            else G(slot)[dist + reach] = v;
+        }
+        next += n;
+    }
+    __device__ __forceinline__ void finish() {
+        if (any) flush(32);
+        const int lane = threadIdx.x & 63;
+        for (int i = 1 + lane; i < 2 * reach; i += 64)
+            if (!any || i - reach < begin || i - reach >= next) G(slot)[i] = 0.0f;
+        below = wave_sum(below);
+        above = wave_sum(above);
+        if (lane == 0) {
+            if (reach == 0) {
+                G(slot)[0] = below + above;
+            } else {
+                G(slot)[0] = below;
+                G(slot)[2 * reach] = above;
+            }
+        }
+    }
+};
+
+template <typename T, int DP, bool BIAS>
+__global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 ? 2 : 1) void attention_grad_q_kernel(BackwardArgs f) {
+    typedef KeyWalk<T, DP> W;
+    constexpr int NB = W::NB, KS = W::KS, DB = DP / 32;
+    __shared__ u32x4_t lds[4 * W::TILE / 16];
+    __shared__ float win[BIAS ? 2 * W::WIN + AT_WAVES * 256 : 1];
+    const Common& c = f.c;
+    const muon_attention_args& a = c.a;
+    int u, head, split;
+    const int64_t axis = span_units(a.queries, a.sequences, AT_ROWS);
+    decode(c.unit0 + blockIdx.x, a.heads, c.splits, axis, u, head, split);
+    lds_float_t* wbuf = (lds_float_t*)win;
+    BiasSums sums;
+    if constexpr (BIAS) {
+        const int64_t slot = head * f.slots + (static_cast<int64_t>(u) * c.splits + split) * AT_WAVES + wave_id();
+        sums.start(wbuf + 2 * W::WIN + 256 * wave_id(), f.bias_part + slot * (2 * a.reach + 1), a.reach);
+    }
+    Span sp;
+    if (!find_span<AT_ROWS>(a.offsets, a.key_offsets, static_cast<int>(a.sequences), static_cast<int>(a.queries), static_cast<int>(a.keys), u, sp)) {
+        if constexpr (BIAS) sums.finish();
+        return;
+    }
+    const W w(c, sp, head, split);
+    const int lane = threadIdx.x & 63, place = w.wave_at + (lane & 31);
+    const int64_t row = sp.start - sp.at + place;
+    const Sight sight = w.sight(c, place);
+    lds_byte_t* buf = (lds_byte_t*)lds;
+
+    // a query that sees no key takes no part, whatever its rows hold
+    const float lse = place < sp.len ? G(a.lse)[row * a.heads + head] : NEG_INF;
+    const bool row_ok = lse != NEG_INF;
+    Frag<T> qf[KS], df[KS];
+    float delta = 0.0f;
+    {
+        const int h = lane >> 5;
+        const T* q = static_cast<const T*>(a.q) + row * a.ld_q + static_cast<int64_t>(head) * a.hs_q;
+        const T* d = static_cast<const T*>(f.grad_out) + row * f.ld_do + static_cast<int64_t>(head) * f.hs_do;
+        const T* out = static_cast<const T*>(a.out) + row * a.ld_out + static_cast<int64_t>(head) * a.hs_out;
+        const T* low = static_cast<const T*>(a.out_low) + row * a.ld_out_low + static_cast<int64_t>(head) * a.hs_out_low;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            const int e0 = 16 * ks + 8 * h;
+            qf[ks] = global_frag<T>(q, e0, a.width, row_ok);
+            df[ks] = global_frag<T>(d, e0, a.width, row_ok);
+            const Frag<T> of = global_frag<T>(out, e0, a.width, row_ok);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) delta = fmaf(frag_get(df[ks], e), frag_get(of, e), delta);
+            if (a.out_low) {
+                const Frag<T> lf = global_frag<T>(low, e0, a.width, row_ok);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) delta = fmaf(frag_get(df[ks], e), frag_get(lf, e), delta);
+            }
+        }
+        delta = half_sum(delta);
+        if (place < sp.len && lane < 32 && split == 0) G(f.delta)[row * a.heads + head] = delta;
+    }
+    const float unit = BIAS ? LOG2E : a.scale * LOG2E;
+    const float ref = row_ok ? (BIAS ? lse : lse * LOG2E) : 0.0f;
+
+    f32x16_t o[DB] = {};
+    BiasWindow<T, W::WIN> bw;
+    float far_lo = 0.0f, far_hi = 0.0f;
+    unsigned byte = 0;
+    uint64_t live = 0, next = 0;
+    if (w.first < w.last) {
+        next = __ballot(w.key_byte(w.first) != 0);
+        w.load(w.first, buf, buf + W::TILE, next, c.vec_in);
+        byte = w.key_byte(w.first + 1);
+        if constexpr (BIAS) {
+            far_lo = bias_value<T>(a, bucket_at<T>(a, -a.reach), head);
+            far_hi = bias_value<T>(a, bucket_at<T>(a, a.reach), head);
+            bw.ask(a, w.window_first(w.first));
+            bw.fetch(a, head);
+            bw.put(wbuf);
+            bw.ask(a, w.window_first(w.first + 1));
+        }
+    }
+    for (int t = w.first; t < w.last; ++t) {
+        const int b = (t - w.first) & 1;
+        tile_barrier();
+        live = next;
+        if (t + 1 < w.last) {
+            next = __ballot(byte != 0);
+            w.load(t + 1, buf + 2 * W::TILE * (b ^ 1), buf + 2 * W::TILE * (b ^ 1) + W::TILE, next, c.vec_in);
+            byte = w.key_byte(t + 2);
+            if constexpr (BIAS) {
+                bw.fetch(a, head);
+                bw.ask(a, w.window_first(t + 2));
+            }
+        }
+        const int seen = w.seen(c, t, live);
+        if (seen != NOTHING) {
+            const lds_byte_t* kt = buf + 2 * W::TILE * b;
+            const lds_byte_t* vt = kt + W::TILE;
+            f32x16_t s[NB] = {}, dp[NB] = {};
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    mma(s[nb], row_frag<T, DP>(kt, 32 * nb, ks), qf[ks]);
+                    mma(dp[nb], row_frag<T, DP>(vt, 32 * nb, ks), df[ks]);
+                }
+            const int far = BIAS ? w.far(t) : 0;
+            if constexpr (BIAS) {
+                const lds_float_t* p = far ? nullptr : wbuf + b * W::WIN;
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) w.add_bias(s[nb], a.scale, p, far < 0 ? far_lo : far_hi, nb);
+            }
+            if (seen == SOME) {
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    hide(s[nb], sight, t * W::BN + 32 * nb + 4 * (lane >> 5));
+                    if (a.key_mask) hide_masked(s[nb], static_cast<uint32_t>(live >> (32 * nb + 4 * (lane >> 5))));
+                }
+            }
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float z = s[nb][i];
+                    // -infinity: what a scale of either sign makes of a hidden score is a probability of 0
+                    const float p = z == NEG_INF ? 0.0f : BIAS ? exp2_((z - ref) * unit) : exp2_(fmaf(z, unit, -ref));
+                    s[nb][i] = p * (dp[nb][i] - delta);
+                }
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const Parts<T> p(s[nb], g);
+#pragma unroll
+                    for (int db = 0; db < DB; ++db) p.mma_to(o[db], col_frag<T, DP>(kt, 32 * nb + 16 * g, db));
+                }
+            if constexpr (BIAS) {
+                if (far == 0) {
+                    const int d0 = t * W::BN - (w.wave_at + 31 + w.off);      // the tile's smallest distance
+                    if (!sums.any) {
+                        sums.any = true;
+                        sums.begin = sums.next = d0;
+                    }
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) sums.add(s[nb], t * W::BN + 32 * nb + 4 * (lane >> 5) - (place + w.off));
+                    sums.flush(W::BN);
+                } else {
+                    float v = 0.0f;
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v += s[nb][i];
+                    if (far < 0) sums.below += v;
+                    else sums.above += v;
+                }
+            }
+        }
+        if constexpr (BIAS)
+            if (t + 1 < w.last) bw.put(wbuf + (b ^ 1) * W::WIN);
+    }
+    if constexpr (BIAS) sums.finish();
+    if (place >= sp.len) return;
+    if (c.splits > 1) {
+        const int64_t at = row * a.heads + head, n = a.queries * a.heads;
+        store_rows<float>(o, 1.0f, f.part + (split * n + at) * a.width, static_cast<float*>(nullptr), a.width, a.width % 4 == 0);
+        return;
+    }
+    store_rows<T>(o, a.scale, static_cast<T*>(f.grad_q) + row * f.ld_dq + static_cast<int64_t>(head) * f.hs_dq, static_cast<T*>(nullptr), a.width, c.vec_out);
+}
+
+// Adds up the slots of one head for 64 distances, then those of a bucket.  The orders are fixed; sums in fp64: they have up to
+// millions of terms of either sign.
+__global__ __launch_bounds__(256) void attention_bias_slots_kernel(const float* part, int64_t slots, int entries, double* sums) {
+    __shared__ double red[4][64];
+    const int lane = threadIdx.x & 63, wave = wave_id(), d = blockIdx.x * 64 + lane, head = blockIdx.y;
+    double v = 0.0;
+    if (d < entries)
+        for (int64_t s = wave; s < slots; s += 4) v += G(part)[(head * slots + s) * entries + d];
+    red[wave][lane] = v;
+    __syncthreads();
+    if (wave == 0 && d < entries) G(sums)[static_cast<int64_t>(head) * entries + d] = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+}
+template <typename T> __global__ __launch_bounds__(64) void attention_bias_kernel(const int32_t* map, const double* sums, int entries, int heads, void* grad) {
+    const int bucket = blockIdx.x, head = blockIdx.y;
+    double v = 0.0;
+    for (int d = threadIdx.x; d < entries; d += 64)
+        if (G(map)[d] == bucket) v += G(sums)[static_cast<int64_t>(head) * entries + d];
+    v = wave_sum(v);
+    if (threadIdx.x == 0) st_el<T>(grad, static_cast<size_t>(bucket) * heads + head, static_cast<float>(v));
+}
+
+// out[row][head][d] = scale * sum over the splits of part[split][row][head][d], for one matrix.
+template <typename T> __global__ __launch_bounds__(256) void attention_sum_kernel(const float* part, int64_t split_pitch, int splits, int64_t rows, int heads,
+                                                                                 int width, float scale, void* out, int64_t ld, int64_t hs, int64_t base) {
+    const int64_t i = base + static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= rows * heads * width) return;
+    float v = 0.0f;
+    for (int s = 0; s < splits; ++s) v += G(part)[s * split_pitch + i];
+    const int64_t at = i / width, row = at / heads;
+    st_el<T>(out, row * ld + (at - row * heads) * hs + (i - at * width), v * scale);
+}
+
+// ---- grad_k and grad_v ------------------------------------------------------------
+
+template <typename T, int DP, bool BIAS>
+__global__ __launch_bounds__(AT_THREADS, 1) void attention_grad_kv_kernel(BackwardArgs f) {
+    constexpr int BQ = walk_rows<T>(), RB = BQ / 32, KS = DP / 16, DB = DP / 32, TILE = BQ * Row<T, DP>::BYTES, WIN = AT_ROWS + BQ;
+    __shared__ u32x4_t lds[4 * TILE / 16];
+    __shared__ f32x4_t stat[2 * 2 * BQ / 4];           // [buffer][lse or delta][row]
+    __shared__ float win[BIAS ? 2 * WIN : 1];
+    const Common& c = f.c;
+    const muon_attention_args& a = c.a;
+    int u, kv, split;
+    decode(c.unit0 + blockIdx.x, a.kv_heads, c.splits, span_units(a.keys, a.sequences, AT_ROWS), u, kv, split);
+    Span sp;
+    if (!find_span<AT_ROWS>(a.key_offsets, a.offsets, static_cast<int>(a.sequences), static_cast<int>(a.keys), static_cast<int>(a.queries), u, sp)) return;
+    const int lane = threadIdx.x & 63, wave = wave_id(), h = lane >> 5;
+    const int wave_at = sp.at + 32 * wave, place = wave_at + (lane & 31), nq = sp.other_len, off = sp.len - nq;
+    const int64_t row = sp.start - sp.at + place;
+    const bool in = place < sp.len, key_ok = in && (!a.key_mask || G(a.key_mask)[in ? row : 0] != 0);
+    lds_byte_t* buf = (lds_byte_t*)lds;
+    lds_float_t* stats = (lds_float_t*)stat;
+    lds_float_t* wbuf = (lds_float_t*)win;
+
+    // queries that see this lane's key: places lo .. lo + span - 1
+    Sight sight;
+    {
+        int lo = 0, hi = nq;
+        if (a.causal) lo = max(lo, place - off);
+        if (c.window) { lo = max(lo, place - c.window + 1 - off); hi = min(hi, place + c.window - off); }
+        sight.set(lo, key_ok ? hi : lo);
+    }
+    const bool keys_all = __all(key_ok);
+    Frag<T> kf[KS], vf[KS];
+    {
+        const T* k = static_cast<const T*>(a.k) + row * a.ld_k + static_cast<int64_t>(kv) * a.hs_k;
+        const T* v = static_cast<const T*>(a.v) + row * a.ld_v + static_cast<int64_t>(kv) * a.hs_v;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            kf[ks] = global_frag<T>(k, 16 * ks + 8 * h, a.width, key_ok);
+            vf[ks] = global_frag<T>(v, 16 * ks + 8 * h, a.width, key_ok);
+        }
+    }
+    // the walk: tiles first .. first + n - 1 of the queries, for every head that shares this key head
+    int lo = 0, hi = nq;
+    {
+        const int j1 = sp.at + min(sp.rows, AT_ROWS) - 1;
+        if (a.causal) lo = max(lo, sp.at - off);
+        if (c.window) { lo = max(lo, sp.at - c.window + 1 - off); hi = min(hi, j1 + c.window - off); }
+    }
+    const int first = lo / BQ, n = hi > lo ? (hi + BQ - 1) / BQ - first : 0;
+    const int64_t steps = static_cast<int64_t>(n) * c.gqa;
+    const int64_t it0 = steps * split / c.splits, it1 = steps * (split + 1) / c.splits;
+    struct At {
+        int head, t;
+        int64_t left;             // steps from here on
+    };
+    auto after = [&](At w) {
+        --w.left;
+        if (++w.t == first + n) {
+            w.t = first;
+            ++w.head;
+        }
+        return w;
+    };
+    At now{kv * c.gqa, first, it1 - it0};
+    if (it1 > it0) {
+        const int g = static_cast<int>(it0 / n);
+        now.head += g;
+        now.t += static_cast<int>(it0 - static_cast<int64_t>(g) * n);
+    }
+    // lse of this lane's row of a step (and its delta): -infinity where there is nothing to see
+    auto ask = [&](const At& w, float& l, float& d) {
+        l = NEG_INF;
+        d = 0.0f;
+        if (w.left <= 0) return;
+        const int i = w.t * BQ + lane;
+        if (lane < BQ && i < nq) {
+            const int64_t at = static_cast<int64_t>(sp.other + i) * a.heads + w.head;
+            l = G(a.lse)[at];
+            d = G(f.delta)[at];
+        }
+    };
+    auto load = [&](const At& w, int b, float l, float d) {
+        const uint64_t live = __ballot(l != NEG_INF);
+        const int64_t i0 = static_cast<int64_t>(sp.other) + static_cast<int64_t>(w.t) * BQ;
+        load_tile<T, DP, BQ, AT_THREADS>(buf + 2 * TILE * b, static_cast<const T*>(a.q) + i0 * a.ld_q + static_cast<int64_t>(w.head) * a.hs_q, a.ld_q, a.width, live, c.vec_in);
+        load_tile<T, DP, BQ, AT_THREADS>(buf + 2 * TILE * b + TILE, static_cast<const T*>(f.grad_out) + i0 * f.ld_do + static_cast<int64_t>(w.head) * f.hs_do, f.ld_do, a.width, live, c.vec_in);
+        if (wave == 0 && lane < BQ) {
+            stats[2 * BQ * b + lane] = l == NEG_INF ? 0.0f : BIAS ? l : l * LOG2E;
+            stats[2 * BQ * b + BQ + lane] = l == NEG_INF ? 0.0f : d;
+        }
+    };
+    // distance of the window's first entry for tile t: that of this workgroup's first key and the tile's last query
+    auto window_first = [&](int t) { return sp.at - (t * BQ + BQ - 1 + off); };
+
+    const float unit = BIAS ? LOG2E : a.scale * LOG2E;
+    f32x16_t dk[DB] = {}, dv[DB] = {};
+    BiasWindow<T, WIN> bw;
+    float lse = 0.0f, delta = 0.0f;
+    if (now.left > 0) {
+        ask(now, lse, delta);
+        load(now, 0, lse, delta);
+        ask(after(now), lse, delta);
+        if constexpr (BIAS) {
+            bw.ask(a, window_first(now.t));
+            bw.fetch(a, now.head);
+            bw.put(wbuf);
+            bw.ask(a, window_first(after(now).t));
+        }
+    }
+    int b = 0;
+    for (; now.left > 0; now = after(now), b ^= 1) {
+        const At next = after(now);
+        tile_barrier();
+        if (next.left > 0) {
+            load(next, b ^ 1, lse, delta);
+            ask(after(next), lse, delta);
+            if constexpr (BIAS) {
+                bw.fetch(a, next.head);
+                bw.ask(a, window_first(after(next).t));
+            }
+        }
+        const lds_byte_t* qt = buf + 2 * TILE * b;
+        const lds_byte_t* dt = qt + TILE;
+        const lds_float_t* st = stats + 2 * BQ * b;
+        const int i0 = now.t * BQ;
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) {
+            const int r0 = i0 + 32 * rb, a0 = r0 + off;
+            int seen = r0 >= nq || wave_at >= sp.len ? NOTHING : tile_sight(a0, a0 + 31, wave_at, wave_at + 31, a.causal, c.window);
+            if (seen == NOTHING) continue;
+            if (r0 + 31 >= nq || !keys_all) seen = SOME;
+            f32x16_t s = {}, dp = {};
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                mma(s, row_frag<T, DP>(qt, 32 * rb, ks), kf[ks]);
+                mma(dp, row_frag<T, DP>(dt, 32 * rb, ks), vf[ks]);
+            }
+            if constexpr (BIAS) {
+                // entry of key 32 wave + l % 32 and query 32 rb + 8 (i / 4) + 4 h + i % 4 of the tile
+                const lds_float_t* p = wbuf + b * WIN + (BQ - 1 - 32 * rb - 4 * h) + 32 * wave + (lane & 31);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[i] = fmaf(s[i], a.scale, p[-(8 * (i >> 2) + (i & 3))]);
+            }
+            if (seen == SOME) hide(s, sight, r0 + 4 * h);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const f32x4_t ref = *(const lds_f32x4_t*)(st + 32 * rb + 8 * q + 4 * h), dl = *(const lds_f32x4_t*)(st + BQ + 32 * rb + 8 * q + 4 * h);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float z = s[4 * q + e];
+                    const float p = z == NEG_INF ? 0.0f : BIAS ? exp2_((z - ref[e]) * unit) : exp2_(fmaf(z, unit, -ref[e]));
+                    s[4 * q + e] = p;
+                    dp[4 * q + e] = p * (dp[4 * q + e] - dl[e]);
+                }
+            }
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const Parts<T> p(s, g), d(dp, g);
+#pragma unroll
+                for (int db = 0; db < DB; ++db) {
+                    p.mma_to(dv[db], col_frag<T, DP>(dt, 32 * rb + 16 * g, db));
+                    d.mma_to(dk[db], col_frag<T, DP>(qt, 32 * rb + 16 * g, db));
+                }
+            }
+        }
+        if constexpr (BIAS)
+            if (next.left > 0) bw.put(wbuf + (b ^ 1) * WIN);
+    }
+    if (!in) return;
+    if (c.splits > 1) {
+        const int64_t at = row * a.kv_heads + kv, total = a.keys * a.kv_heads;
+        float* p = f.part + (2 * split * total + at) * a.width;
+        store_rows<float>(dk, 1.0f, p, static_cast<float*>(nullptr), a.width, a.width % 4 == 0);
+        store_rows<float>(dv, 1.0f, p + total * a.width, static_cast<float*>(nullptr), a.width, a.width % 4 == 0);
+        return;
+    }
+    store_rows<T>(dk, a.scale, static_cast<T*>(f.grad_k) + row * f.ld_dk + static_cast<int64_t>(kv) * f.hs_dk, static_cast<T*>(nullptr), a.width, c.vec_out);
+    store_rows<T>(dv, 1.0f, static_cast<T*>(f.grad_v) + row * f.ld_dv + static_cast<int64_t>(kv) * f.hs_dv, static_cast<T*>(nullptr), a.width, c.vec_out);
+}
+
+// ---- host -------------------------------------------------------------------------
+
+// Few units of an axis leave CUs idle: their walks are split until about two workgroups a CU have work, while a part keeps `least`
+// tiles on average.
+int plan_splits(int64_t rows, int64_t sequences, int heads, int64_t walk, int tile, int least) {
+    const int64_t units = (rows / AT_ROWS + sequences) * heads;
+    const int64_t tiles = std::max<int64_t>(1, walk / sequences / tile);
+    const int64_t want = std::min<int64_t>({512 / std::max<int64_t>(1, units), tiles / least, AT_MAX_SPLITS});
+    return static_cast<int>(std::max<int64_t>(1, want));
+}
+int tile_rows(int dtype) { return dtype == MUON_BF16 ? walk_rows<uint16_t>() : walk_rows<float>(); }
+
+int forward_splits(const muon_attention_args& a) { return plan_splits(a.queries, a.sequences, a.heads, a.keys, tile_rows(a.dtype), 4); }
+struct BackwardPlan {
+    int q_splits, kv_splits;
+    int64_t slots;                                  // of the bias's partial sums, per head
+    size_t delta, q_part, kv_part, bias_part, bias_sums, bytes;   // offsets
+};
+BackwardPlan plan_backward(const muon_attention_backward_args& a) {
+    BackwardPlan p{};
+    const int tr = tile_rows(a.dtype);
+    p.q_splits = plan_splits(a.queries, a.sequences, a.heads, a.keys, tr, 4);
+    p.kv_splits = plan_splits(a.keys, a.sequences, a.kv_heads, a.queries * (a.heads / a.kv_heads), tr, 4);
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at += (bytes + 255) / 256 * 256;
+        return here;
+    };
+    const size_t q = static_cast<size_t>(a.queries) * a.heads, k = static_cast<size_t>(a.keys) * a.kv_heads;
+    p.delta = take(q * 4);
+    // one after the other: the partial sums of grad_q are added up before those of grad_k and grad_v are written
+    p.q_part = p.kv_part = at;
+    take(std::max(p.q_splits > 1 ? p.q_splits * q * a.width * 4 : 0, p.kv_splits > 1 ? 2 * p.kv_splits * k * a.width * 4 : 0));
+    if (a.bias) {
+        const size_t entries = 2 * static_cast<size_t>(a.reach) + 1;
+        p.slots = span_units(a.queries, a.sequences, AT_ROWS) * p.q_splits * AT_WAVES;
+        p.bias_part = take(p.slots * a.heads * entries * 4);
+        p.bias_sums = take(a.heads * entries * 8);
+    }
+    p.bytes = at;
+    return p;
+}
+
+bool whole(const void* p, int64_t ld, int64_t hs, int64_t es) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * es % 16 == 0 && hs * es % 16 == 0;
+}
+int64_t elem(int dtype) { return dtype == MUON_BF16 ? 2 : 4; }
+
+Common common_args(const muon_attention_args& a, int splits) {
+    Common c{};
+    c.a = a;
+    if (!c.a.key_offsets) c.a.key_offsets = c.a.offsets;
+    c.splits = splits;
+    c.window = static_cast<int>(std::min<int64_t>(a.window, (1 << 30) - 1));
+    c.gqa = a.heads / a.kv_heads;
+    return c;
+}
+
+// A launch holds at most 2^32 - 1 threads.
+template <typename F> hipError_t in_launches(int64_t blocks, F launch) {
+    constexpr int64_t MOST = int64_t{1} << 23;
+    for (int64_t b = 0; b < blocks; b += MOST) {
+        const hipError_t e = launch(b, static_cast<unsigned>(std::min(MOST, blocks - b)));
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+template <typename T, int DP, bool BIAS> hipError_t run_forward(ForwardArgs f, hipStream_t s) {
+    hipError_t e = in_launches(f.c.units, [&](int64_t base, unsigned n) {
+        f.c.unit0 = base;
+        hipLaunchKernelGGL((attention_forward_kernel<T, DP, BIAS>), dim3(n), dim3(AT_THREADS), 0, s, f);
+        return hipGetLastError();
+    });
+    if (e != hipSuccess || f.c.splits == 1) return e;
+    return in_launches((f.c.a.queries * f.c.a.heads + 3) / 4, [&](int64_t base, unsigned n) {
+        hipLaunchKernelGGL((attention_join_kernel<T, BIAS>), dim3(n), dim3(256), 0, s, f, base * 4);
+        return hipGetLastError();
+    });
+}
+
+template <typename T> hipError_t run_sum(const float* part, int64_t pitch, int splits, int64_t rows, int heads, int width, float scale, void* out, int64_t ld,
+                                         int64_t hs, hipStream_t s) {
+    return in_launches((rows * heads * width + 255) / 256, [&](int64_t base, unsigned n) {
+        hipLaunchKernelGGL((attention_sum_kernel<T>), dim3(n), dim3(256), 0, s, part, pitch, splits, rows, heads, width, scale, out, ld, hs, base * 256);
+        return hipGetLastError();
+    });
+}
+
+template <typename T, int DP, bool BIAS>
+hipError_t run_backward(BackwardArgs f, const BackwardPlan& p, const muon_attention_backward_args& b, char* ws, hipStream_t s) {
+    const muon_attention_args& a = f.c.a;
+    hipError_t e;
+    if (a.queries > 0) {
+        f.c.splits = p.q_splits;
+        f.part = reinterpret_cast<float*>(ws + p.q_part);
+        e = in_launches(span_units(a.queries, a.sequences, AT_ROWS) * a.heads * p.q_splits, [&](int64_t base, unsigned n) {
+            f.c.unit0 = base;
+            hipLaunchKernelGGL((attention_grad_q_kernel<T, DP, BIAS>), dim3(n), dim3(AT_THREADS), 0, s, f);
+            return hipGetLastError();
+        });
+        if (e != hipSuccess) return e;
+        if (p.q_splits > 1) {
+            e = run_sum<T>(f.part, a.queries * a.heads * a.width, p.q_splits, a.queries, a.heads, a.width, a.scale, f.grad_q, f.ld_dq, f.hs_dq, s);
+            if (e != hipSuccess) return e;
+        }
+    }
+    if constexpr (BIAS) {
+        const int entries = 2 * a.reach + 1;
+        double* sums = reinterpret_cast<double*>(ws + p.bias_sums);
+        hipLaunchKernelGGL(attention_bias_slots_kernel, dim3((entries + 63) / 64, a.heads), dim3(256), 0, s, f.bias_part, a.queries > 0 ? p.slots : 0, entries, sums);
+        hipLaunchKernelGGL((attention_bias_kernel<T>), dim3(a.buckets, a.heads), dim3(64), 0, s, a.bucket_map, sums, entries, a.heads, b.grad_bias);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    if (a.keys == 0) return hipSuccess;
+    f.c.splits = p.kv_splits;
+    f.part = reinterpret_cast<float*>(ws + p.kv_part);
+    e = in_launches(span_units(a.keys, a.sequences, AT_ROWS) * a.kv_heads * p.kv_splits, [&](int64_t base, unsigned n) {
+        f.c.unit0 = base;
+        hipLaunchKernelGGL((attention_grad_kv_kernel<T, DP, BIAS>), dim3(n), dim3(AT_THREADS), 0, s, f);
+        return hipGetLastError();
+    });
+    if (e != hipSuccess || p.kv_splits == 1) return e;
+    const int64_t total = a.keys * a.kv_heads * a.width;
+    e = run_sum<T>(f.part, 2 * total, p.kv_splits, a.keys, a.kv_heads, a.width, a.scale, f.grad_k, f.ld_dk, f.hs_dk, s);
+    if (e != hipSuccess) return e;
+    return run_sum<T>(f.part + total, 2 * total, p.kv_splits, a.keys, a.kv_heads, a.width, 1.0f, f.grad_v, f.ld_dv, f.hs_dv, s);
+}
+
+// Calls f with the tile width and whether there is a bias, as types.
+template <typename F> hipError_t dispatch(int dtype, int width, bool bias, F f) {
+    auto by_bias = [&](auto t, auto dp) { return bias ? f(t, dp, std::true_type{}) : f(t, dp, std::false_type{}); };
+    auto by_width = [&](auto t) {
+        return width <= 64 ? by_bias(t, std::integral_constant<int, 64>{}) : by_bias(t, std::integral_constant<int, 128>{});
+    };
+    return dtype == MUON_BF16 ? by_width(uint16_t{}) : by_width(float{});
+}
+
+}  // namespace
+
+size_t attention_bytes(const muon_attention_args& a) {
+    const int s = forward_splits(a);
+    return s > 1 ? static_cast<size_t>(s) * a.queries * a.heads * (a.width + 2) * sizeof(float) : 0;
+}
+
+hipError_t launch_attention(const muon_attention_args& a, void* workspace, hipStream_t s) {
+    if (a.queries == 0) return hipSuccess;
+    ForwardArgs f{};
+    f.c = common_args(a, forward_splits(a));
+    f.c.units = at::span_units(a.queries, a.sequences, AT_ROWS) * a.heads * f.c.splits;
+    const int64_t es = elem(a.dtype);
+    const bool w = a.width * es % 16 == 0;
+    f.c.vec_in = w && whole(a.k, a.ld_k, a.hs_k, es) && whole(a.v, a.ld_v, a.hs_v, es);
+    f.c.vec_out = w && whole(a.out, a.ld_out, a.hs_out, es) && (!a.out_low || whole(a.out_low, a.ld_out_low, a.hs_out_low, es));
+    f.part = static_cast<float*>(workspace);
+    return dispatch(a.dtype, a.width, a.bias != nullptr, [&](auto t, auto dp, auto bias) {
+        return run_forward<decltype(t), decltype(dp)::value, decltype(bias)::value>(f, s);
+    });
+}
+
+size_t attention_backward_bytes(const muon_attention_backward_args& a) { return plan_backward(a).bytes; }
+
+hipError_t launch_attention_backward(const muon_attention_backward_args& b, void* workspace, hipStream_t s) {
+    const BackwardPlan p = plan_backward(b);
+    muon_attention_args a{};
+    a.q = b.q; a.k = b.k; a.v = b.v;
+    a.offsets = b.offsets; a.key_offsets = b.key_offsets; a.key_mask = b.key_mask;
+    a.bias = b.bias; a.bucket_map = b.bucket_map;
+    a.out = const_cast<void*>(b.out); a.lse = const_cast<float*>(b.lse); a.out_low = const_cast<void*>(b.out_low);
+    a.queries = b.queries; a.keys = b.keys; a.sequences = b.sequences;
+    a.ld_q = b.ld_q; a.hs_q = b.hs_q; a.ld_k = b.ld_k; a.hs_k = b.hs_k; a.ld_v = b.ld_v; a.hs_v = b.hs_v;
+    a.ld_out = b.ld_out; a.hs_out = b.hs_out; a.ld_out_low = b.ld_out_low; a.hs_out_low = b.hs_out_low;
+    a.window = b.window; a.scale = b.scale;
+    a.heads = b.heads; a.kv_heads = b.kv_heads; a.width = b.width;
+    a.buckets = b.buckets; a.reach = b.reach; a.causal = b.causal; a.dtype = b.dtype;
+    BackwardArgs f{};
+    f.c = common_args(a, 1);
+    const int64_t es = elem(a.dtype);
+    const bool w = a.width * es % 16 == 0;
+    f.c.vec_in = w && whole(a.q, a.ld_q, a.hs_q, es) && whole(a.k, a.ld_k, a.hs_k, es) && whole(a.v, a.ld_v, a.hs_v, es) && whole(b.grad_out, b.ld_grad_out, b.hs_grad_out, es);
+    f.c.vec_out = w && whole(b.grad_q, b.ld_grad_q, b.hs_grad_q, es) && whole(b.grad_k, b.ld_grad_k, b.hs_grad_k, es) && whole(b.grad_v, b.ld_grad_v, b.hs_grad_v, es);
+    f.grad_out = b.grad_out;
+    f.grad_q = b.grad_q; f.grad_k = b.grad_k; f.grad_v = b.grad_v;
+    f.ld_do = b.ld_grad_out; f.hs_do = b.hs_grad_out;
+    f.ld_dq = b.ld_grad_q; f.hs_dq = b.hs_grad_q;
+    f.ld_dk = b.ld_grad_k; f.hs_dk = b.hs_grad_k;
+    f.ld_dv = b.ld_grad_v; f.hs_dv = b.hs_grad_v;
+    char* ws = static_cast<char*>(workspace);
+    f.delta = reinterpret_cast<float*>(ws + p.delta);
+    f.bias_part = reinterpret_cast<float*>(ws + p.bias_part);
+    f.slots = p.slots;
+    return dispatch(a.dtype, a.width, a.bias != nullptr, [&](auto t, auto dp, auto bias) {
+        return run_backward<decltype(t), decltype(dp)::value, decltype(bias)::value>(f, p, b, ws, s);
+    });
+}
+
+}  // namespace muon

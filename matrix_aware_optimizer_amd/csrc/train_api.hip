@@ -21,12 +21,16 @@ struct Buffers {
         size_t pitch, width;   // of a matrix's rows, in bytes; a vector is one row
         bool out;
         const char* name;
+        size_t pitch2, width2;   // the same bytes, or more, as other rows (a head each); 0: none
         // No byte in common.  Matrices of one pitch may lie in each other's gaps (column ranges of one buffer).
         bool apart(const Buf& o) const {
             if (lo >= o.hi || o.lo >= hi) return true;
-            if (pitch != o.pitch || width > pitch || o.width > pitch) return false;
-            const size_t after = (o.lo >= lo ? o.lo - lo : pitch - (lo - o.lo) % pitch) % pitch;
-            return after >= width && after + o.width <= pitch;
+            return in_gaps(o, pitch, width, o.pitch, o.width) || (pitch2 && in_gaps(o, pitch2, width2, o.pitch2, o.width2));
+        }
+        bool in_gaps(const Buf& o, size_t p, size_t w, size_t op, size_t ow) const {
+            if (p != op || w > p || ow > p) return false;
+            const size_t after = (o.lo >= lo ? o.lo - lo : p - (lo - o.lo) % p) % p;
+            return after >= w && after + ow <= p;
         }
     };
     Buf b[24];
@@ -46,7 +50,30 @@ struct Buffers {
         }
         const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
         if (lo % align) { bad = name; why = "is misaligned"; return; }
-        b[n++] = {lo, lo + bytes, pitch, width, out, name};
+        b[n++] = {lo, lo + bytes, pitch, width, out, name, 0, 0};
+    }
+    // rows x heads x width with pitches ld and hs: an input's may be anything (0: broadcast), an output's elements are apart.
+    void heads(const char* name, const void* p, int64_t rows, int64_t heads, int64_t width, int64_t ld, int64_t hs, size_t es, bool out,
+               bool optional = false) {
+        if (bad || rows == 0 || (optional && !p)) return;
+        constexpr int64_t MOST = int64_t{1} << 40;
+        if (rows == 1) ld = 0;
+        if (heads == 1) hs = 0;
+        if (ld < 0 || hs < 0 || ld > MOST || hs > MOST) { bad = name; why = "has a negative pitch or one beyond 2^40"; return; }
+        const __int128 span = static_cast<__int128>(rows - 1) * ld + static_cast<__int128>(heads - 1) * hs + width;
+        if (span > MOST * 65536) { bad = name; why = "spans more than 2^56 elements"; return; }
+        const bool by_row = (heads == 1 || hs >= width) && (rows == 1 || ld >= (heads - 1) * hs + width);
+        const bool by_head = (rows == 1 || ld >= width) && (heads == 1 || static_cast<__int128>(hs) >= static_cast<__int128>(rows - 1) * ld + width);
+        if (out && !by_row && !by_head) { bad = name; why = "has overlapping rows or heads"; return; }
+        const size_t bytes = static_cast<size_t>(span) * es;
+        const int before = n;
+        if (by_row && rows > 1) this->rows(name, p, bytes, ld * es, ((heads - 1) * hs + width) * es, es, out, false);
+        else if (by_head && heads > 1) this->rows(name, p, bytes, hs * es, ((rows - 1) * ld + width) * es, es, out, false);
+        else this->rows(name, p, bytes, bytes, bytes, es, out, false);
+        if (n > before && heads > 1 && rows > 1 && hs >= width && ld % hs == 0) {
+            b[n - 1].pitch2 = hs * es;
+            b[n - 1].width2 = width * es;
+        }
     }
     void matrix(const char* name, const void* p, int64_t rows, int64_t cols, int64_t ld, size_t es, bool out,
                 bool optional = false) {
@@ -288,6 +315,142 @@ muon_status check_policy(const muon_policy_args* a, Buffers& buf) {
     return buf.check();
 }
 
+// ---- attention ------------------------------------------------------------------
+
+// A and the backward pass's arguments share the fields that are looked at here.
+template <typename A> muon_status check_attention_shape(const A* a) {
+    MUON_TRY(check_dtype(a->dtype, "dtype"));
+    MUON_TRY(check_finite({a->scale}, "scale"));
+    if (a->queries < 0 || a->keys < 0 || a->sequences < 1 || a->width < 1 || a->heads < 1 || a->kv_heads < 1 || a->window < 0)
+        return fail(MUON_ERR_INVALID_ARG, "%lld queries and %lld keys in %lld sequences, %d and %d heads of width %d, window %lld",
+                    (long long)a->queries, (long long)a->keys, (long long)a->sequences, a->heads, a->kv_heads, a->width, (long long)a->window);
+    if (a->heads % a->kv_heads) return fail(MUON_ERR_INVALID_ARG, "%d heads are not a multiple of %d", a->heads, a->kv_heads);
+    if (!a->offsets && (a->sequences != 1 || a->key_offsets))
+        return fail(MUON_ERR_INVALID_ARG, "without offsets there is one sequence, and no key_offsets");
+    if (a->queries > MUON_MAX_TOKENS || a->keys > MUON_MAX_TOKENS || a->sequences > MUON_MAX_TOKENS || a->heads > MUON_MAX_HEADS ||
+        a->width > MUON_MAX_HEAD_WIDTH)
+        return fail(MUON_ERR_UNSUPPORTED, "%lld queries, %lld keys, %lld sequences, %d heads of width %d: beyond %lld, %d, %d", (long long)a->queries,
+                    (long long)a->keys, (long long)a->sequences, a->heads, a->width, (long long)MUON_MAX_TOKENS, MUON_MAX_HEADS, MUON_MAX_HEAD_WIDTH);
+    if ((a->bias != nullptr) != (a->bucket_map != nullptr)) return fail(MUON_ERR_INVALID_ARG, "bias and bucket_map go together");
+    if (a->bias) {
+        if (a->buckets < 1 || a->reach < 0) return fail(MUON_ERR_INVALID_ARG, "%d buckets, reach %d", a->buckets, a->reach);
+        if (a->buckets > MUON_MAX_BUCKETS || a->reach > MUON_MAX_REACH)
+            return fail(MUON_ERR_UNSUPPORTED, "%d buckets, reach %d: beyond %d, %d", a->buckets, a->reach, MUON_MAX_BUCKETS, MUON_MAX_REACH);
+    }
+    return MUON_OK;
+}
+
+template <typename A> void attention_inputs(const A* a, Buffers& buf) {
+    const size_t es = elem_size(a->dtype);
+    buf.heads("q", a->q, a->queries, a->heads, a->width, a->ld_q, a->hs_q, es, false);
+    buf.heads("k", a->k, a->keys, a->kv_heads, a->width, a->ld_k, a->hs_k, es, false);
+    buf.heads("v", a->v, a->keys, a->kv_heads, a->width, a->ld_v, a->hs_v, es, false);
+    buf.add("offsets", a->offsets, (static_cast<size_t>(a->sequences) + 1) * 8, 8, false, true);
+    buf.add("key_offsets", a->key_offsets, (static_cast<size_t>(a->sequences) + 1) * 8, 8, false, true);
+    buf.add("key_mask", a->key_mask, static_cast<size_t>(a->keys), 1, false, true);
+    if (a->bias) {
+        buf.add("bias", a->bias, static_cast<size_t>(a->buckets) * a->heads * es, es, false);
+        buf.add("bucket_map", a->bucket_map, (2 * static_cast<size_t>(a->reach) + 1) * 4, 4, false);
+    }
+}
+
+muon_status check_attention(const muon_attention_args* a, Buffers& buf) {
+    if (!a) return fail(MUON_ERR_INVALID_ARG, "args is NULL");
+    MUON_TRY(check_attention_shape(a));
+    const size_t es = elem_size(a->dtype);
+    attention_inputs(a, buf);
+    buf.heads("out", a->out, a->queries, a->heads, a->width, a->ld_out, a->hs_out, es, true);
+    buf.add("lse", a->lse, static_cast<size_t>(a->queries) * a->heads * 4, 4, true);
+    buf.heads("out_low", a->out_low, a->queries, a->heads, a->width, a->ld_out_low, a->hs_out_low, es, true, true);
+    return buf.check();
+}
+
+muon_status check_attention_backward(const muon_attention_backward_args* a, Buffers& buf) {
+    if (!a) return fail(MUON_ERR_INVALID_ARG, "args is NULL");
+    MUON_TRY(check_attention_shape(a));
+    if ((a->bias != nullptr) != (a->grad_bias != nullptr)) return fail(MUON_ERR_INVALID_ARG, "bias and its gradient go together");
+    const size_t es = elem_size(a->dtype);
+    attention_inputs(a, buf);
+    buf.heads("out", a->out, a->queries, a->heads, a->width, a->ld_out, a->hs_out, es, false);
+    buf.add("lse", a->lse, static_cast<size_t>(a->queries) * a->heads * 4, 4, false);
+    buf.heads("out_low", a->out_low, a->queries, a->heads, a->width, a->ld_out_low, a->hs_out_low, es, false, true);
+    buf.heads("grad_out", a->grad_out, a->queries, a->heads, a->width, a->ld_grad_out, a->hs_grad_out, es, false);
+    buf.heads("grad_q", a->grad_q, a->queries, a->heads, a->width, a->ld_grad_q, a->hs_grad_q, es, true);
+    buf.heads("grad_k", a->grad_k, a->keys, a->kv_heads, a->width, a->ld_grad_k, a->hs_grad_k, es, true);
+    buf.heads("grad_v", a->grad_v, a->keys, a->kv_heads, a->width, a->ld_grad_v, a->hs_grad_v, es, true);
+    if (a->bias) buf.add("grad_bias", a->grad_bias, static_cast<size_t>(a->buckets) * a->heads * es, es, true);
+    return buf.check();
+}
+
+// ---- tokens to experts and back -----------------------------------------------------
+
+muon_status check_expert_shape(int64_t tokens, int64_t cols, int32_t chosen, int32_t num_experts, int32_t dtype) {
+    MUON_TRY(check_dtype(dtype, "dtype"));
+    if (tokens < 0 || cols < 1 || chosen < 1 || num_experts < 1)
+        return fail(MUON_ERR_INVALID_ARG, "%lld tokens of %lld columns to %d of %d experts", (long long)tokens, (long long)cols, chosen, num_experts);
+    if (chosen > MUON_MAX_CHOSEN || num_experts > MUON_MAX_EXPERTS || cols > MUON_MAX_DIM || tokens > MUON_MAX_TOKENS / chosen)
+        return fail(MUON_ERR_UNSUPPORTED, "%lld tokens of %lld columns to %d of %d experts: beyond %lld choices, %d, %d, %d", (long long)tokens,
+                    (long long)cols, chosen, num_experts, (long long)MUON_MAX_TOKENS, MUON_MAX_DIM, MUON_MAX_CHOSEN, MUON_MAX_EXPERTS);
+    return MUON_OK;
+}
+
+muon_status check_expert_sort(const muon_expert_sort_args* a, Buffers& buf) {
+    if (!a) return fail(MUON_ERR_INVALID_ARG, "args is NULL");
+    MUON_TRY(check_expert_shape(a->tokens, a->cols, a->chosen, a->num_experts, a->dtype));
+    const size_t es = elem_size(a->dtype), n = static_cast<size_t>(a->tokens) * a->chosen;
+    buf.matrix("x", a->x, a->tokens, a->cols, a->ld_x, es, false);
+    buf.add("experts", a->experts, n * 8, 8, false);
+    buf.matrix("sorted", a->sorted, n, a->cols, a->ld_sorted, es, true);
+    buf.add("slots", a->slots, n * 4, 4, true);
+    buf.add("offsets", a->offsets, (static_cast<size_t>(a->num_experts) + 1) * 8, 8, true);
+    return buf.check();
+}
+
+muon_status check_expert_sort_backward(const muon_expert_sort_backward_args* a, Buffers& buf) {
+    if (!a) return fail(MUON_ERR_INVALID_ARG, "args is NULL");
+    MUON_TRY(check_expert_shape(a->tokens, a->cols, a->chosen, 1, a->dtype));
+    const size_t es = elem_size(a->dtype), n = static_cast<size_t>(a->tokens) * a->chosen;
+    buf.matrix("grad_sorted", a->grad_sorted, n, a->cols, a->ld_grad_sorted, es, false);
+    buf.add("slots", a->slots, n * 4, 4, false);
+    buf.matrix("grad_x", a->grad_x, a->tokens, a->cols, a->ld_grad_x, es, true);
+    return buf.check();
+}
+
+muon_status check_expert_combine(const muon_expert_combine_args* a, Buffers& buf) {
+    if (!a) return fail(MUON_ERR_INVALID_ARG, "args is NULL");
+    MUON_TRY(check_expert_shape(a->tokens, a->cols, a->chosen, 1, a->dtype));
+    const size_t es = elem_size(a->dtype), n = static_cast<size_t>(a->tokens) * a->chosen;
+    buf.matrix("y", a->y, n, a->cols, a->ld_y, es, false);
+    buf.add("slots", a->slots, n * 4, 4, false);
+    buf.add("weights", a->weights, n * 4, 4, false);
+    buf.matrix("out", a->out, a->tokens, a->cols, a->ld_out, es, true);
+    return buf.check();
+}
+
+muon_status check_expert_combine_backward(const muon_expert_combine_backward_args* a, Buffers& buf) {
+    if (!a) return fail(MUON_ERR_INVALID_ARG, "args is NULL");
+    MUON_TRY(check_expert_shape(a->tokens, a->cols, a->chosen, a->num_experts, a->dtype));
+    const size_t es = elem_size(a->dtype), n = static_cast<size_t>(a->tokens) * a->chosen;
+    buf.matrix("grad_out", a->grad_out, a->tokens, a->cols, a->ld_grad_out, es, false);
+    buf.matrix("y", a->y, n, a->cols, a->ld_y, es, false);
+    buf.add("slots", a->slots, n * 4, 4, false);
+    buf.add("weights", a->weights, n * 4, 4, false);
+    buf.add("offsets", a->offsets, (static_cast<size_t>(a->num_experts) + 1) * 8, 8, false);
+    buf.matrix("grad_y", a->grad_y, n, a->cols, a->ld_grad_y, es, true);
+    buf.add("grad_weights", a->grad_weights, n * 4, 4, true);
+    return buf.check();
+}
+
+// One launch sequence without a workspace.
+template <typename F> muon_status run_plain(int cls, const char* what, void* stream, F launch) {
+    int dev = 0, cus = 0;
+    MUON_TRY(check_device(&dev, &cus));
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    MUON_TRY(timed_launch(cls, s, what, [&] { return launch(s); }));
+    clear_error();
+    return MUON_OK;
+}
+
 // Runs one operator: workspace and device checks, then the launches.
 template <typename F>
 muon_status run_op(Buffers& buf, size_t need, void* ws, size_t ws_bytes, F launch) {
@@ -392,6 +555,66 @@ muon_status muon_policy_loss(const muon_policy_args* a, void* ws, size_t ws_byte
     return run_op(buf, policy_bytes(*a), ws, ws_bytes, [&] {
         return timed_launch(12, s, "policy loss kernels", [&] { return launch_policy(*a, ws, s); });
     });
+}
+
+size_t muon_attention_workspace_bytes(const muon_attention_args* a) {
+    Buffers buf;
+    return check_attention(a, buf) == MUON_OK ? at_least_one(attention_bytes(*a)) : 0;
+}
+
+muon_status muon_attention(const muon_attention_args* a, void* ws, size_t ws_bytes, void* stream) {
+    Buffers buf;
+    MUON_TRY(check_attention(a, buf));
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    return run_op(buf, attention_bytes(*a), ws, ws_bytes, [&] {
+        return timed_launch(13, s, "attention kernels", [&] { return launch_attention(*a, ws, s); });
+    });
+}
+
+size_t muon_attention_backward_workspace_bytes(const muon_attention_backward_args* a) {
+    Buffers buf;
+    return check_attention_backward(a, buf) == MUON_OK ? at_least_one(attention_backward_bytes(*a)) : 0;
+}
+
+muon_status muon_attention_backward(const muon_attention_backward_args* a, void* ws, size_t ws_bytes, void* stream) {
+    Buffers buf;
+    MUON_TRY(check_attention_backward(a, buf));
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    return run_op(buf, attention_backward_bytes(*a), ws, ws_bytes, [&] {
+        return timed_launch(13, s, "attention backward kernels", [&] { return launch_attention_backward(*a, ws, s); });
+    });
+}
+
+size_t muon_expert_sort_workspace_bytes(const muon_expert_sort_args* a) {
+    Buffers buf;
+    return check_expert_sort(a, buf) == MUON_OK ? at_least_one(expert_sort_bytes(*a)) : 0;
+}
+
+muon_status muon_expert_sort(const muon_expert_sort_args* a, void* ws, size_t ws_bytes, void* stream) {
+    Buffers buf;
+    MUON_TRY(check_expert_sort(a, buf));
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    return run_op(buf, expert_sort_bytes(*a), ws, ws_bytes, [&] {
+        return timed_launch(14, s, "expert sort kernels", [&] { return launch_expert_sort(*a, ws, s); });
+    });
+}
+
+muon_status muon_expert_sort_backward(const muon_expert_sort_backward_args* a, void* stream) {
+    Buffers buf;
+    MUON_TRY(check_expert_sort_backward(a, buf));
+    return run_plain(14, "expert sort backward kernel", stream, [&](hipStream_t s) { return launch_expert_sort_backward(*a, s); });
+}
+
+muon_status muon_expert_combine(const muon_expert_combine_args* a, void* stream) {
+    Buffers buf;
+    MUON_TRY(check_expert_combine(a, buf));
+    return run_plain(14, "expert combine kernel", stream, [&](hipStream_t s) { return launch_expert_combine(*a, s); });
+}
+
+muon_status muon_expert_combine_backward(const muon_expert_combine_backward_args* a, void* stream) {
+    Buffers buf;
+    MUON_TRY(check_expert_combine_backward(a, buf));
+    return run_plain(14, "expert combine backward kernel", stream, [&](hipStream_t s) { return launch_expert_combine_backward(*a, s); });
 }
 
 }  // extern "C"

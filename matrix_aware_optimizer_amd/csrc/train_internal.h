@@ -1,5 +1,5 @@
 // Internal types of the training operators (block_norm.hip, token_logp.hip,
-// losses.hip) and their host side (train_api.hip).
+// losses.hip, attention.hip, experts.hip) and their host side (train_api.hip).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -135,5 +135,16 @@ size_t preference_bytes(const muon_preference_args& a);
 hipError_t launch_preference(const muon_preference_args& a, void* workspace, hipStream_t s);
 size_t policy_bytes(const muon_policy_args& a);
 hipError_t launch_policy(const muon_policy_args& a, void* workspace, hipStream_t s);
+
+size_t attention_bytes(const muon_attention_args& a);
+hipError_t launch_attention(const muon_attention_args& a, void* workspace, hipStream_t s);
+size_t attention_backward_bytes(const muon_attention_backward_args& a);
+hipError_t launch_attention_backward(const muon_attention_backward_args& a, void* workspace, hipStream_t s);
+
+size_t expert_sort_bytes(const muon_expert_sort_args& a);
+hipError_t launch_expert_sort(const muon_expert_sort_args& a, void* workspace, hipStream_t s);
+hipError_t launch_expert_sort_backward(const muon_expert_sort_backward_args& a, hipStream_t s);
+hipError_t launch_expert_combine(const muon_expert_combine_args& a, hipStream_t s);
+hipError_t launch_expert_combine_backward(const muon_expert_combine_backward_args& a, hipStream_t s);
 
 }  // namespace muon
