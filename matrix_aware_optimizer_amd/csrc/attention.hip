@@ -171,10 +171,10 @@ template <typename T, int DP> struct KeyWalk {
     }
     // Distance of the window's first entry for tile t.
     __device__ __forceinline__ int window_first(int t) const { return t * BN - (sp.at + AT_ROWS - 1 + off); }
-    // z = scale x + bias (natural units) for one block; w: the tile's window, NULL: `far` everywhere.
-    __device__ __forceinline__ void add_bias(f32x16_t& s, float scale, const lds_float_t* w, float far, int nb) const {
+    // z = scale x + bias (natural units) for one block; w: the tile's window; near == 0: `far` everywhere.
+    __device__ __forceinline__ void add_bias(f32x16_t& s, float scale, const lds_float_t* w, bool near, float far, int nb) const {
         const int lane = threadIdx.x & 63;
-        if (w) {
+        if (near) {
             // entry of key 32 nb + 8 (i / 4) + 4 h + i % 4 and query 32 wave + l % 32
             const lds_float_t* p = w + (AT_ROWS - 1 - 32 * wave_id() - (lane & 31)) + 32 * nb + 4 * (lane >> 5);
 #pragma unroll
@@ -220,7 +220,7 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 ? 2 : 1) void attention_
         const T* q = static_cast<const T*>(a.q) + row * a.ld_q + static_cast<int64_t>(head) * a.hs_q;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-            qf[ks] = global_frag<T>(q, 16 * ks + 8 * (lane >> 5), a.width, row_ok && a.scale != 0.0f);
+            qf[ks] = global_frag<T>(q, 16 * ks + 8 * (lane >> 5), a.width, row_ok && a.scale != 0.0f, c.vec_in);
             if (a.scale < 0.0f) {
                 if constexpr (sizeof(T) == 2) qf[ks].w ^= 0x80008000u;
                 else { qf[ks].w[0] = -qf[ks].w[0]; qf[ks].w[1] = -qf[ks].w[1]; }
@@ -237,17 +237,24 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 ? 2 : 1) void attention_
     unsigned byte = 0;
     uint64_t live = 0, next = 0;
     if (w.first < w.last) {
-        next = __ballot(w.key_byte(w.first) != 0);
-        w.load(w.first, buf, buf + W::TILE, next, c.vec_in);
+        // loads come back in order: what others wait for goes first
+        const unsigned first_byte = w.key_byte(w.first);
         byte = w.key_byte(w.first + 1);
+        int lo_bucket = 0, hi_bucket = 0;
         if constexpr (BIAS) {
-            far_lo = bias_value<T>(a, bucket_at<T>(a, -a.reach), head);
-            far_hi = bias_value<T>(a, bucket_at<T>(a, a.reach), head);
             bw.ask(a, w.window_first(w.first));
+            lo_bucket = bucket_at<T>(a, -a.reach);
+            hi_bucket = bucket_at<T>(a, a.reach);
+        }
+        next = __ballot(first_byte != 0);
+        if constexpr (BIAS) {
             bw.fetch(a, head);
-            bw.put(wbuf);
+            far_lo = bias_value<T>(a, lo_bucket, head);
+            far_hi = bias_value<T>(a, hi_bucket, head);
             bw.ask(a, w.window_first(w.first + 1));
         }
+        w.load(w.first, buf, buf + W::TILE, next, c.vec_in);
+        if constexpr (BIAS) bw.put(wbuf);
     }
     for (int t = w.first; t < w.last; ++t) {
         const int b = (t - w.first) & 1;
@@ -273,9 +280,8 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 ? 2 : 1) void attention_
                 for (int nb = 0; nb < NB; ++nb) mma(s[nb], row_frag<T, DP>(kt, 32 * nb, ks), qf[ks]);
             if constexpr (BIAS) {
                 const int far = w.far(t);
-                const lds_float_t* p = far ? nullptr : wbuf + b * W::WIN;
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb) w.add_bias(s[nb], scale, p, far < 0 ? far_lo : far_hi, nb);
+                for (int nb = 0; nb < NB; ++nb) w.add_bias(s[nb], scale, wbuf + b * W::WIN, far == 0, far < 0 ? far_lo : far_hi, nb);
             }
             if (seen == SOME) {
 #pragma unroll
@@ -359,13 +365,23 @@ template <typename T, bool BIAS> __global__ __launch_bounds__(256) void attentio
     const float unit = BIAS ? LOG2E : 1.0f;
     const float f2 = m == top || l == 0.0f ? (l == 0.0f ? 0.0f : 1.0f) : exp2_((m - top) * unit);
     const float sum = wave_sum(l * f2);
+    // eight splits' values are asked for before the first is added; a split of no key holds zeros
     float v[2] = {};
-    for (int s = 0; s < c.splits; ++s) {
-        const float fs = __shfl(f2, s);
-        const float* p = f.part + (s * n + at) * a.width;
+    const int d0 = min(lane, a.width - 1), d1 = min(lane + 64, a.width - 1);
+    for (int s0 = 0; s0 < c.splits; s0 += 8) {
+        float x[8][2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-            if (lane + 64 * k < a.width && fs != 0.0f) v[k] = fmaf(G(p)[lane + 64 * k], fs, v[k]);
+        for (int s = 0; s < 8; ++s) {
+            const float* p = f.part + (min(s0 + s, c.splits - 1) * n + at) * a.width;
+            x[s][0] = G(p)[d0];
+            x[s][1] = G(p)[d1];
+        }
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+            const float fs = s0 + s < c.splits ? __shfl(f2, s0 + s) : 0.0f;
+            v[0] = fmaf(x[s][0], fs, v[0]);
+            v[1] = fmaf(x[s][1], fs, v[1]);
+        }
     }
     const int64_t row = at / a.heads;
     const int head = static_cast<int>(at - row * a.heads);
@@ -384,47 +400,57 @@ template <typename T, bool BIAS> __global__ __launch_bounds__(256) void attentio
 
 // ---- grad_q, and the bias's gradient --------------------------------------------
 
-// Sums of dz over the distances that a wave meets.  A tile's dz is added up in 128 places of LDS by distance modulo 128, the
-// two halves of the wave apart: an instruction then meets no place twice, and a wave's own adds come in order, so the sums are the
-// same on every run.  The walk moves by a tile's keys, so that as many of the smallest distances are complete after a tile and go to
-// the wave's slot.  Distances beyond the reach have one bucket a side and add up in registers.
+// Sums of dz over the distances that a wave meets.  A 32 x 32 block of dz goes to LDS with query q's row moved right by 31 - q, so
+// that a distance is a column: lane c adds up column c (what a row does not reach stays 0).  The next block's distances
+// begin 32 further on, so 32 sums are complete after a block and go to the wave's slot; the others move down by 32 lanes.  Distances
+// beyond the reach have one bucket a side and add up in registers.  The order of the additions is fixed.  (Adding to LDS
+// by its float atomics took 700 cycles an instruction.)
 struct BiasSums {
-    lds_float_t* place;      // 2 x 128, this wave's own
+    static constexpr int ROOM = 32 * 64;   // floats a wave
+    lds_float_t* room;       // [query][64]
     float* slot;             // 2 reach + 1
-    int reach, begin, next;  // distances written to the slot: begin .. next - 1; next: the first one in `place`
+    int reach, begin, next;  // distances written to the slot: begin .. next - 1
     bool any;
-    float below, above;
+    float carry, below, above;
     __device__ __forceinline__ void start(lds_float_t* p, float* s, int r) {
-        place = p;
+        room = p;
         slot = s;
         reach = r;
         begin = next = 0;
         any = false;
-        below = above = 0.0f;
-        for (int i = threadIdx.x & 63; i < 256; i += 64) place[i] = 0.0f;
+        carry = below = above = 0.0f;
+        for (int i = 0; i < 32; ++i) room[64 * i + (threadIdx.x & 63)] = 0.0f;
     }
-    // one block of dz: register i at distance dist + 8 (i / 4) + i % 4
-    __device__ __forceinline__ void add(const f32x16_t& dz, int dist) {
-        lds_float_t* p = place + 128 * ((threadIdx.x & 63) >> 5);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) __builtin_amdgcn_ds_faddf(p + ((dist + 8 * (i >> 2) + (i & 3)) & 127), dz[i], 0, 0, false);
-    }
-    __device__ __forceinline__ void flush(int n) {
-        const int lane = threadIdx.x & 63;
-        if (lane < n) {
-            const int dist = next + lane;
-            lds_float_t* p = place + (dist & 127);
-            const float v = p[0] + p[128];
-            p[0] = 0.0f;
-            p[128] = 0.0f;
+    // lanes 0 .. 31 hold the sums of distances next ..
+    __device__ __forceinline__ void flush(float v) {
+        const int lane = threadIdx.x & 63, dist = next + lane;
+        if (lane < 32) {
             if (dist <= -reach) below += v;
             else if (dist >= reach) above += v;
             else G(slot)[dist + reach] = v;
         }
-        next += n;
+        next += 32;
+    }
+    // one block of dz; dist: the distance of its first key from its last query
+    __device__ __forceinline__ void add(const f32x16_t& dz, int dist) {
+        const int lane = threadIdx.x & 63, q = lane & 31;
+        if (!any) {
+            any = true;
+            begin = next = dist;
+        }
+        lds_float_t* p = room + 64 * q + 31 - q + 4 * (lane >> 5);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) p[8 * (i >> 2) + (i & 3)] = dz[i];
+        float v[4] = {};
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i & 3] += room[64 * i + lane];
+        const float sum = (v[0] + v[1]) + (v[2] + v[3]) + carry;
+        flush(sum);
+        const float up = __shfl_xor(sum, 32);
+        carry = lane < 32 ? up : 0.0f;
     }
     __device__ __forceinline__ void finish() {
-        if (any) flush(32);
+        if (any) flush(carry);
         const int lane = threadIdx.x & 63;
         for (int i = 1 + lane; i < 2 * reach; i += 64)
             if (!any || i - reach < begin || i - reach >= next) G(slot)[i] = 0.0f;
@@ -446,7 +472,7 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 ? 2 : 1) void attention_
     typedef KeyWalk<T, DP> W;
     constexpr int NB = W::NB, KS = W::KS, DB = DP / 32;
     __shared__ u32x4_t lds[4 * W::TILE / 16];
-    __shared__ float win[BIAS ? 2 * W::WIN + AT_WAVES * 256 : 1];
+    __shared__ float win[BIAS ? 2 * W::WIN + AT_WAVES * BiasSums::ROOM : 1];
     const Common& c = f.c;
     const muon_attention_args& a = c.a;
     int u, head, split;
@@ -456,7 +482,7 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 ? 2 : 1) void attention_
     BiasSums sums;
     if constexpr (BIAS) {
         const int64_t slot = head * f.slots + (static_cast<int64_t>(u) * c.splits + split) * AT_WAVES + wave_id();
-        sums.start(wbuf + 2 * W::WIN + 256 * wave_id(), f.bias_part + slot * (2 * a.reach + 1), a.reach);
+        sums.start(wbuf + 2 * W::WIN + BiasSums::ROOM * wave_id(), f.bias_part + slot * (2 * a.reach + 1), a.reach);
     }
     Span sp;
     if (!find_span<AT_ROWS>(a.offsets, a.key_offsets, static_cast<int>(a.sequences), static_cast<int>(a.queries), static_cast<int>(a.keys), u, sp)) {
@@ -483,13 +509,13 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 ? 2 : 1) void attention_
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
             const int e0 = 16 * ks + 8 * h;
-            qf[ks] = global_frag<T>(q, e0, a.width, row_ok);
-            df[ks] = global_frag<T>(d, e0, a.width, row_ok);
-            const Frag<T> of = global_frag<T>(out, e0, a.width, row_ok);
+            qf[ks] = global_frag<T>(q, e0, a.width, row_ok, c.vec_in);
+            df[ks] = global_frag<T>(d, e0, a.width, row_ok, c.vec_in);
+            const Frag<T> of = global_frag<T>(out, e0, a.width, row_ok, c.vec_in);
 #pragma unroll
             for (int e = 0; e < 8; ++e) delta = fmaf(frag_get(df[ks], e), frag_get(of, e), delta);
             if (a.out_low) {
-                const Frag<T> lf = global_frag<T>(low, e0, a.width, row_ok);
+                const Frag<T> lf = global_frag<T>(low, e0, a.width, row_ok, c.vec_in);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) delta = fmaf(frag_get(df[ks], e), frag_get(lf, e), delta);
             }
@@ -506,17 +532,24 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 ? 2 : 1) void attention_
     unsigned byte = 0;
     uint64_t live = 0, next = 0;
     if (w.first < w.last) {
-        next = __ballot(w.key_byte(w.first) != 0);
-        w.load(w.first, buf, buf + W::TILE, next, c.vec_in);
+        // loads come back in order: what others wait for goes first
+        const unsigned first_byte = w.key_byte(w.first);
         byte = w.key_byte(w.first + 1);
+        int lo_bucket = 0, hi_bucket = 0;
         if constexpr (BIAS) {
-            far_lo = bias_value<T>(a, bucket_at<T>(a, -a.reach), head);
-            far_hi = bias_value<T>(a, bucket_at<T>(a, a.reach), head);
             bw.ask(a, w.window_first(w.first));
+            lo_bucket = bucket_at<T>(a, -a.reach);
+            hi_bucket = bucket_at<T>(a, a.reach);
+        }
+        next = __ballot(first_byte != 0);
+        if constexpr (BIAS) {
             bw.fetch(a, head);
-            bw.put(wbuf);
+            far_lo = bias_value<T>(a, lo_bucket, head);
+            far_hi = bias_value<T>(a, hi_bucket, head);
             bw.ask(a, w.window_first(w.first + 1));
         }
+        w.load(w.first, buf, buf + W::TILE, next, c.vec_in);
+        if constexpr (BIAS) bw.put(wbuf);
     }
     for (int t = w.first; t < w.last; ++t) {
         const int b = (t - w.first) & 1;
@@ -545,9 +578,8 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 ? 2 : 1) void attention_
                 }
             const int far = BIAS ? w.far(t) : 0;
             if constexpr (BIAS) {
-                const lds_float_t* p = far ? nullptr : wbuf + b * W::WIN;
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb) w.add_bias(s[nb], a.scale, p, far < 0 ? far_lo : far_hi, nb);
+                for (int nb = 0; nb < NB; ++nb) w.add_bias(s[nb], a.scale, wbuf + b * W::WIN, far == 0, far < 0 ? far_lo : far_hi, nb);
             }
             if (seen == SOME) {
 #pragma unroll
@@ -575,14 +607,8 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 ? 2 : 1) void attention_
                 }
             if constexpr (BIAS) {
                 if (far == 0) {
-                    const int d0 = t * W::BN - (w.wave_at + 31 + w.off);      // the tile's smallest distance
-                    if (!sums.any) {
-                        sums.any = true;
-                        sums.begin = sums.next = d0;
-                    }
 #pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) sums.add(s[nb], t * W::BN + 32 * nb + 4 * (lane >> 5) - (place + w.off));
-                    sums.flush(W::BN);
+                    for (int nb = 0; nb < NB; ++nb) sums.add(s[nb], t * W::BN + 32 * nb - (w.wave_at + 31 + w.off));
                 } else {
                     float v = 0.0f;
 #pragma unroll
@@ -634,6 +660,7 @@ template <typename T> __global__ __launch_bounds__(256) void attention_sum_kerne
     const int64_t i = base + static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
     if (i >= rows * heads * width) return;
     float v = 0.0f;
+#pragma unroll 8
     for (int s = 0; s < splits; ++s) v += G(part)[s * split_pitch + i];
     const int64_t at = i / width, row = at / heads;
     st_el<T>(out, row * ld + (at - row * heads) * hs + (i - at * width), v * scale);
@@ -676,8 +703,8 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attention_grad_kv_kernel(Backwa
         const T* v = static_cast<const T*>(a.v) + row * a.ld_v + static_cast<int64_t>(kv) * a.hs_v;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-            kf[ks] = global_frag<T>(k, 16 * ks + 8 * h, a.width, key_ok);
-            vf[ks] = global_frag<T>(v, 16 * ks + 8 * h, a.width, key_ok);
+            kf[ks] = global_frag<T>(k, 16 * ks + 8 * h, a.width, key_ok, c.vec_in);
+            vf[ks] = global_frag<T>(v, 16 * ks + 8 * h, a.width, key_ok, c.vec_in);
         }
     }
     // the walk: tiles first .. first + n - 1 of the queries, for every head that shares this key head
@@ -831,7 +858,7 @@ int plan_splits(int64_t rows, int64_t sequences, int heads, int64_t walk, int ti
 }
 int tile_rows(int dtype) { return dtype == MUON_BF16 ? walk_rows<uint16_t>() : walk_rows<float>(); }
 
-int forward_splits(const muon_attention_args& a) { return plan_splits(a.queries, a.sequences, a.heads, a.keys, tile_rows(a.dtype), 4); }
+int forward_splits(const muon_attention_args& a) { return plan_splits(a.queries, a.sequences, a.heads, a.keys, tile_rows(a.dtype), 2); }
 struct BackwardPlan {
     int q_splits, kv_splits;
     int64_t slots;                                  // of the bias's partial sums, per head
@@ -840,8 +867,8 @@ struct BackwardPlan {
 BackwardPlan plan_backward(const muon_attention_backward_args& a) {
     BackwardPlan p{};
     const int tr = tile_rows(a.dtype);
-    p.q_splits = plan_splits(a.queries, a.sequences, a.heads, a.keys, tr, 4);
-    p.kv_splits = plan_splits(a.keys, a.sequences, a.kv_heads, a.queries * (a.heads / a.kv_heads), tr, 4);
+    p.q_splits = plan_splits(a.queries, a.sequences, a.heads, a.keys, tr, 2);
+    p.kv_splits = plan_splits(a.keys, a.sequences, a.kv_heads, a.queries * (a.heads / a.kv_heads), tr, 2);
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t here = at;
@@ -973,7 +1000,7 @@ hipError_t launch_attention(const muon_attention_args& a, void* workspace, hipSt
     f.c.units = at::span_units(a.queries, a.sequences, AT_ROWS) * a.heads * f.c.splits;
     const int64_t es = elem(a.dtype);
     const bool w = a.width * es % 16 == 0;
-    f.c.vec_in = w && whole(a.k, a.ld_k, a.hs_k, es) && whole(a.v, a.ld_v, a.hs_v, es);
+    f.c.vec_in = w && whole(a.q, a.ld_q, a.hs_q, es) && whole(a.k, a.ld_k, a.hs_k, es) && whole(a.v, a.ld_v, a.hs_v, es);
     f.c.vec_out = w && whole(a.out, a.ld_out, a.hs_out, es) && (!a.out_low || whole(a.out_low, a.ld_out_low, a.hs_out_low, es));
     f.part = static_cast<float*>(workspace);
     return dispatch(a.dtype, a.width, a.bias != nullptr, [&](auto t, auto dp, auto bias) {
@@ -1000,7 +1027,8 @@ hipError_t launch_attention_backward(const muon_attention_backward_args& b, void
     f.c = common_args(a, 1);
     const int64_t es = elem(a.dtype);
     const bool w = a.width * es % 16 == 0;
-    f.c.vec_in = w && whole(a.q, a.ld_q, a.hs_q, es) && whole(a.k, a.ld_k, a.hs_k, es) && whole(a.v, a.ld_v, a.hs_v, es) && whole(b.grad_out, b.ld_grad_out, b.hs_grad_out, es);
+    f.c.vec_in = w && whole(a.q, a.ld_q, a.hs_q, es) && whole(a.k, a.ld_k, a.hs_k, es) && whole(a.v, a.ld_v, a.hs_v, es) && whole(b.grad_out, b.ld_grad_out, b.hs_grad_out, es) &&
+                 whole(b.out, b.ld_out, b.hs_out, es) && (!b.out_low || whole(b.out_low, b.ld_out_low, b.hs_out_low, es));
     f.c.vec_out = w && whole(b.grad_q, b.ld_grad_q, b.hs_grad_q, es) && whole(b.grad_k, b.ld_grad_k, b.hs_grad_k, es) && whole(b.grad_v, b.ld_grad_v, b.hs_grad_v, es);
     f.grad_out = b.grad_out;
     f.grad_q = b.grad_q; f.grad_k = b.grad_k; f.grad_v = b.grad_v;

@@ -163,15 +163,23 @@ template <typename T> __device__ __forceinline__ u32x4_t ld_part(const T* p, int
     return w;
 }
 
-// B operand straight from global memory: values e0 .. e0 + 7 of a row of `width`, zeros behind it.
-template <typename T> __device__ __forceinline__ Frag<T> global_frag(const T* row, int e0, int width, bool ok) {
+// B operand straight from global memory: values e0 .. e0 + 7 of a row of `width`, zeros behind it.  vec (the same for the whole
+// wave): the row comes in whole 16-byte chunks; a load is then one unconditional access, and a row's loads are all in
+// flight at once, where two ways for a lane to get its register would make each wait for the one before.
+template <typename T> __device__ __forceinline__ Frag<T> global_frag(const T* row, int e0, int width, bool ok, bool vec) {
     Frag<T> f;
-    if constexpr (sizeof(T) == 2) {
-        f.w = ld_part<T>(row + e0, ok ? width - e0 : 0);
-    } else {
+    constexpr int N = sizeof(T) / 2, PER = 16 / sizeof(T);
+    u32x4_t w[N];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) f.w[k] = __builtin_bit_cast(f32x4_t, ld_part<T>(row + e0 + 4 * k, ok ? width - e0 - 4 * k : 0));
+    for (int k = 0; k < N; ++k) {
+        const int e = e0 + PER * k;
+        if (vec) w[k] = *(const MUON_GLOBAL u32x4_t*)G(ok && e < width ? static_cast<const void*>(row + e) : static_cast<const void*>(&zero_chunk));
+        else w[k] = ld_part<T>(row + e, ok ? width - e : 0);
     }
+    if constexpr (sizeof(T) == 2) f.w = w[0];
+    else
+#pragma unroll
+        for (int k = 0; k < 2; ++k) f.w[k] = __builtin_bit_cast(f32x4_t, w[k]);
     return f;
 }
 __device__ __forceinline__ float frag_get(const Frag<uint16_t>& f, int e) {
@@ -264,18 +272,32 @@ __device__ __forceinline__ int bound(const int64_t* offsets, int sequences, int 
 template <int BM>
 __device__ __forceinline__ bool find_span(const int64_t* offsets, const int64_t* others, int sequences, int rows, int other_rows, int u, Span& sp) {
     const int lane = threadIdx.x & 63;
-    int lo = 0, hi = sequences + 1;
-    while (hi > lo) {
-        const int step = (hi - lo + 63) / 64;
-        const int64_t s = lo + static_cast<int64_t>(lane + 1) * step;
-        const bool below = s <= hi && bound(offsets, sequences, rows, static_cast<int>(s)) / BM + s <= u;
-        const int n = __popcll(__ballot(below));
-        lo += n * step;
-        hi = hi < lo + step - 1 ? hi : lo + step - 1;
+    int s, b0, b1, o0, o1;
+    if (sequences <= 61) {
+        // every bound of both axes at once, one trip to memory
+        const int mine = bound(offsets, sequences, rows, lane), other = bound(others, sequences, other_rows, lane);
+        s = __popcll(__ballot(lane >= 1 && lane <= sequences + 1 && mine / BM + lane <= u));
+        b0 = __builtin_amdgcn_readlane(mine, s);
+        b1 = __builtin_amdgcn_readlane(mine, s + 1);
+        o0 = __builtin_amdgcn_readlane(other, s);
+        o1 = __builtin_amdgcn_readlane(other, s + 1);
+    } else {
+        int lo = 0, hi = sequences + 1;
+        while (hi > lo) {
+            const int step = (hi - lo + 63) / 64;
+            const int64_t at = lo + static_cast<int64_t>(lane + 1) * step;
+            const bool below = at <= hi && bound(offsets, sequences, rows, static_cast<int>(at)) / BM + at <= u;
+            const int n = __popcll(__ballot(below));
+            lo += n * step;
+            hi = hi < lo + step - 1 ? hi : lo + step - 1;
+        }
+        s = __builtin_amdgcn_readfirstlane(lo);
+        b0 = bound(offsets, sequences, rows, s);
+        b1 = bound(offsets, sequences, rows, s + 1);
+        o0 = bound(others, sequences, other_rows, s);
+        o1 = bound(others, sequences, other_rows, s + 1);
     }
-    lo = __builtin_amdgcn_readfirstlane(lo);
-    const int b0 = bound(offsets, sequences, rows, lo), b1 = bound(offsets, sequences, rows, lo + 1);
-    const int j = u - (b0 / BM + lo);
+    const int j = u - (b0 / BM + s);
     sp.len = b1 - b0;
     if (j < 0 || sp.len <= 0 || static_cast<int64_t>(j) * BM >= sp.len) return false;
     sp.at = j * BM;
@@ -283,8 +305,7 @@ __device__ __forceinline__ bool find_span(const int64_t* offsets, const int64_t*
     sp.rows = sp.len - sp.at;
     sp.other = 0;
     sp.other_len = 0;
-    if (lo >= 1 && lo <= sequences) {
-        const int o0 = bound(others, sequences, other_rows, lo), o1 = bound(others, sequences, other_rows, lo + 1);
+    if (s >= 1 && s <= sequences) {
         sp.other = o0;
         sp.other_len = o1 > o0 ? o1 - o0 : 0;
     }

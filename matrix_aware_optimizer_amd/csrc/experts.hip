@@ -15,7 +15,7 @@ namespace {
 
 constexpr int EX_THREADS = 256, EX_WAVES = 4;
 constexpr int EX_CHUNK = 512, EX_PER = EX_CHUNK / EX_THREADS;   // choices a chunk, a lane
-constexpr int EX_SHARE = 32;                                    // choices a workgroup copies
+constexpr int EX_MOST_SHARES = EX_CHUNK / EX_WAVES, EX_WORKGROUPS = 1024;   // workgroups a chunk; as many in all, where they have rows
 constexpr int EX_DIRECT = 128;                                  // chunks whose counts every workgroup adds up by itself
 
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6)); }
@@ -36,6 +36,12 @@ template <typename T> __device__ __forceinline__ void zero_row(T* row, int64_t c
             for (int64_t e = i; e < cols; ++e) st_el<T>(row, e, 0.0f);
         }
     }
+}
+
+// Columns at .. at + 7 of a row of `cols`, as many as there are.
+template <typename T> __device__ __forceinline__ void load_run(Run<T>& r, const global_t<T>* row, int64_t at, int64_t cols) {
+    if (at + 8 <= cols) r.load(row + at, 0);
+    else if (at < cols) r.load(row + at, 0, static_cast<unsigned>(cols - at));
 }
 
 struct SortArgs {
@@ -87,7 +93,8 @@ template <typename T> __global__ __launch_bounds__(EX_THREADS) void expert_place
     const muon_expert_sort_args& a = s.a;
     const int E = a.num_experts, lane = threadIdx.x & 63, wave = wave_id();
     const int64_t n = a.tokens * a.chosen, block = s.block0 + blockIdx.x, chunk = block / shares;
-    const int share = static_cast<int>(block - chunk * shares);
+    const int share = static_cast<int>(block - chunk * shares), span = EX_CHUNK / shares;
+    if (block != 0 && chunk * EX_CHUNK + share * span >= n) return;
     int* hist = lds;                         // [wave][E + 1], then the choices of the waves before
     int* first = hist + EX_WAVES * (E + 1);  // E + 1: where the expert's choices of this chunk begin
     int* place = first + E + 1;              // EX_CHUNK
@@ -172,7 +179,6 @@ template <typename T> __global__ __launch_bounds__(EX_THREADS) void expert_place
     __syncthreads();
 
     // this workgroup's share of the rows; of row i itself, if it lies behind the last one taken
-    const int span = EX_CHUNK / shares;
     for (int k = wave; k < span; k += EX_WAVES) {
         const int64_t i = chunk * EX_CHUNK + share * span + k;
         if (i >= n) break;
@@ -182,20 +188,18 @@ template <typename T> __global__ __launch_bounds__(EX_THREADS) void expert_place
         const global_t<T>* src = G(static_cast<const T*>(a.x) + i / a.chosen * a.ld_x);
         global_t<T>* dst = G(static_cast<T*>(a.sorted) + slot * a.ld_sorted);
         for (int64_t c = 8 * lane; c < a.cols; c += 4 * 512) {
-            u32x4_t w[4][sizeof(T) / 2];
+            Run<T> r[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                if (c + 512 * q + 8 <= a.cols)
-#pragma unroll
-                    for (int p = 0; p < static_cast<int>(sizeof(T) / 2); ++p) w[q][p] = *(const global_t<u32x4_el2>*)(src + c + 512 * q + p * (16 / sizeof(T)));
+            for (int q = 0; q < 4; ++q) load_run(r[q], src, c + 512 * q, a.cols);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int64_t at = c + 512 * q;
                 if (at + 8 <= a.cols) {
-#pragma unroll
-                    for (int p = 0; p < static_cast<int>(sizeof(T) / 2); ++p) *(global_t<u32x4_el2>*)(dst + at + p * (16 / sizeof(T))) = w[q][p];
+                    r[q].store(dst + at);
                 } else {
-                    for (int64_t e = at; e < a.cols; ++e) dst[e] = src[e];
+#pragma unroll
+                    for (int e = 0; e < 7; ++e)
+                        if (at + e < a.cols) st_el<T>(static_cast<T*>(a.sorted) + slot * a.ld_sorted, at + e, r[q].get(e));
                 }
             }
         }
@@ -275,14 +279,8 @@ template <typename T> __global__ __launch_bounds__(EX_THREADS) void expert_scatt
             Run<T> gr[4], yr[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const int64_t at = c + 512 * q;
-                if (at + 8 <= a.cols) {
-                    gr[q].load(g + at, 0);
-                    yr[q].load(y + at, 0);
-                } else if (at < a.cols) {
-                    gr[q].load(g + at, 0, static_cast<unsigned>(a.cols - at));
-                    yr[q].load(y + at, 0, static_cast<unsigned>(a.cols - at));
-                }
+                load_run(gr[q], g, c + 512 * q, a.cols);
+                load_run(yr[q], y, c + 512 * q, a.cols);
             }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -359,7 +357,8 @@ hipError_t launch_expert_sort(const muon_expert_sort_args& a, void* workspace, h
             if (e != hipSuccess) return e;
         }
     }
-    const int shares = EX_CHUNK / EX_SHARE;
+    int shares = 4;
+    while (shares < EX_MOST_SHARES && shares * g.chunks < EX_WORKGROUPS) shares *= 2;
     const size_t lds = ((EX_WAVES + 1) * (a.num_experts + 1) + EX_CHUNK + EX_WAVES) * sizeof(int);
     return in_launches(static_cast<int64_t>(g.chunks) * shares, [&](int64_t b, unsigned blocks) {
         g.block0 = b;

@@ -37,6 +37,7 @@ template <> struct Run<uint16_t> {
         for (int e = 0; e < 7; ++e)
             if (e < static_cast<int>(n)) w[e >> 1] |= static_cast<uint32_t>(p[i + e]) << (16 * (e & 1));
     }
+    __device__ __forceinline__ void store(global_t<uint16_t>* p) const { *(global_t<u32x4_el2>*)p = w; }
     __device__ __forceinline__ float get(int e) const {
         return __uint_as_float((e & 1) ? (w[e >> 1] & 0xffff0000u) : (w[e >> 1] << 16));
     }
@@ -51,6 +52,10 @@ template <> struct Run<float> {
 #pragma unroll
         for (int e = 0; e < 7; ++e)
             if (e < static_cast<int>(n)) w[e >> 2][e & 3] = p[i + e];
+    }
+    __device__ __forceinline__ void store(global_t<float>* p) const {
+        *(global_t<f32x4_el4>*)p = w[0];
+        *(global_t<f32x4_el4>*)(p + 4) = w[1];
     }
     __device__ __forceinline__ float get(int e) const { return w[e >> 2][e & 3]; }
 };
