@@ -54,16 +54,16 @@ struct BackwardArgs {
 };
 
 // Which unit of the axis, head and split a workgroup has.  Heads go fastest, and where they allow it in runs that share an XCD
-// (workgroups go to XCDs in turn), so that a key head's rows stay in one L2; units from the end first: under a causal mask
-// they are the longest.
-__device__ __forceinline__ void decode(int64_t id, int heads, int splits, int64_t axis, int& u, int& head, int& split) {
+// (workgroups go to XCDs in turn), so that a key head's rows stay in one L2.  The units that walk the longest under a causal mask
+// come first: the last queries, the first keys (16384 tokens, grad_k and grad_v the other way round: half as long again).
+__device__ __forceinline__ void decode(int64_t id, int heads, int splits, int64_t axis, bool from_end, int& u, int& head, int& split) {
     const int hs = heads * splits;
     const int64_t r = id / hs;
     int k = static_cast<int>(id - r * hs);
     if (hs % 8 == 0) k = (k % 8) * (hs / 8) + k / 8;
     head = k / splits;
     split = k - head * splits;
-    u = static_cast<int>(axis - 1 - r);
+    u = static_cast<int>(from_end ? axis - 1 - r : r);
 }
 
 // Bias of a head at distance j - a.
@@ -198,12 +198,12 @@ template <typename T, int DP, bool BIAS>
 __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 ? 2 : 1) void attention_forward_kernel(ForwardArgs f) {
     typedef KeyWalk<T, DP> W;
     constexpr int NB = W::NB, KS = W::KS, DB = DP / 32;
-    __shared__ u32x4_t lds[4 * W::TILE / 16];
+    __shared__ __attribute__((aligned(512))) u32x4_t lds[4 * W::TILE / 16];
     __shared__ float win[BIAS ? 2 * W::WIN : 1];
     const Common& c = f.c;
     const muon_attention_args& a = c.a;
     int u, head, split;
-    decode(c.unit0 + blockIdx.x, a.heads, c.splits, span_units(a.queries, a.sequences, AT_ROWS), u, head, split);
+    decode(c.unit0 + blockIdx.x, a.heads, c.splits, span_units(a.queries, a.sequences, AT_ROWS), true, u, head, split);
     Span sp;
     if (!find_span<AT_ROWS>(a.offsets, a.key_offsets, static_cast<int>(a.sequences), static_cast<int>(a.queries), static_cast<int>(a.keys), u, sp)) return;
     const W w(c, sp, head, split);
@@ -212,6 +212,7 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 ? 2 : 1) void attention_
     const int64_t row = sp.start - sp.at + place;
     const Sight sight = w.sight(c, place);
     lds_byte_t* buf = (lds_byte_t*)lds;
+    Lanes<T, DP> lanes;
     lds_float_t* wbuf = (lds_float_t*)win;
 
     // a negative scale goes into q's sign and a scale of 0 into q, so that the largest score is the largest product
@@ -271,13 +272,13 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 ? 2 : 1) void attention_
         }
         const int seen = w.seen(c, t, live);
         if (seen != NOTHING) {
-            const lds_byte_t* kt = buf + 2 * W::TILE * b;
-            const lds_byte_t* vt = kt + W::TILE;
+            const unsigned kt = lds_at(buf) + 2 * W::TILE * b, vt = kt + W::TILE;
+            lanes.fresh();
             f32x16_t s[NB] = {};
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb) mma(s[nb], row_frag<T, DP>(kt, 32 * nb, ks), qf[ks]);
+                for (int nb = 0; nb < NB; ++nb) mma(s[nb], row_frag<T, DP>(kt, lanes, 32 * nb, ks), qf[ks]);
             if constexpr (BIAS) {
                 const int far = w.far(t);
 #pragma unroll
@@ -321,7 +322,7 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 ? 2 : 1) void attention_
                 for (int g = 0; g < 2; ++g) {
                     const Parts<T> p(s[nb], g);
 #pragma unroll
-                    for (int db = 0; db < DB; ++db) p.mma_to(o[db], col_frag<T, DP>(vt, 32 * nb + 16 * g, db));
+                    for (int db = 0; db < DB; ++db) p.mma_to(o[db], col_frag<T, DP>(vt, lanes, 32 * nb + 16 * g, db));
                 }
         }
         if constexpr (BIAS)
@@ -468,16 +469,16 @@ struct BiasSums {
 };
 
 template <typename T, int DP, bool BIAS>
-__global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 ? 2 : 1) void attention_grad_q_kernel(BackwardArgs f) {
+__global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 && !(BIAS && DP == 128) ? 2 : 1) void attention_grad_q_kernel(BackwardArgs f) {
     typedef KeyWalk<T, DP> W;
     constexpr int NB = W::NB, KS = W::KS, DB = DP / 32;
-    __shared__ u32x4_t lds[4 * W::TILE / 16];
+    __shared__ __attribute__((aligned(512))) u32x4_t lds[4 * W::TILE / 16];
     __shared__ float win[BIAS ? 2 * W::WIN + AT_WAVES * BiasSums::ROOM : 1];
     const Common& c = f.c;
     const muon_attention_args& a = c.a;
     int u, head, split;
     const int64_t axis = span_units(a.queries, a.sequences, AT_ROWS);
-    decode(c.unit0 + blockIdx.x, a.heads, c.splits, axis, u, head, split);
+    decode(c.unit0 + blockIdx.x, a.heads, c.splits, axis, true, u, head, split);
     lds_float_t* wbuf = (lds_float_t*)win;
     BiasSums sums;
     if constexpr (BIAS) {
@@ -494,6 +495,7 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 ? 2 : 1) void attention_
     const int64_t row = sp.start - sp.at + place;
     const Sight sight = w.sight(c, place);
     lds_byte_t* buf = (lds_byte_t*)lds;
+    Lanes<T, DP> lanes;
 
     // a query that sees no key takes no part, whatever its rows hold
     const float lse = place < sp.len ? G(a.lse)[row * a.heads + head] : NEG_INF;
@@ -566,57 +568,47 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 ? 2 : 1) void attention_
         }
         const int seen = w.seen(c, t, live);
         if (seen != NOTHING) {
-            const lds_byte_t* kt = buf + 2 * W::TILE * b;
-            const lds_byte_t* vt = kt + W::TILE;
-            f32x16_t s[NB] = {}, dp[NB] = {};
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-                    mma(s[nb], row_frag<T, DP>(kt, 32 * nb, ks), qf[ks]);
-                    mma(dp[nb], row_frag<T, DP>(vt, 32 * nb, ks), df[ks]);
-                }
+            const unsigned kt = lds_at(buf) + 2 * W::TILE * b;
             const int far = BIAS ? w.far(t) : 0;
-            if constexpr (BIAS) {
+            // a block of 32 keys at a time: all of a tile at once does not fit the registers of two waves a SIMD
+#pragma unroll 1
+            for (int nb = 0; nb < NB; ++nb) {
+                const unsigned kb = kt + 32 * nb * Row<T, DP>::BYTES, vb = kb + W::TILE;
+                lanes.fresh();
+                f32x16_t s = {}, dp = {};
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb) w.add_bias(s[nb], a.scale, wbuf + b * W::WIN, far == 0, far < 0 ? far_lo : far_hi, nb);
-            }
-            if (seen == SOME) {
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-                    hide(s[nb], sight, t * W::BN + 32 * nb + 4 * (lane >> 5));
-                    if (a.key_mask) hide_masked(s[nb], static_cast<uint32_t>(live >> (32 * nb + 4 * (lane >> 5))));
+                for (int ks = 0; ks < KS; ++ks) {
+                    mma(s, row_frag<T, DP>(kb, lanes, 0, ks), qf[ks]);
+                    mma(dp, row_frag<T, DP>(vb, lanes, 0, ks), df[ks]);
                 }
-            }
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
+                if constexpr (BIAS) w.add_bias(s, a.scale, wbuf + b * W::WIN, far == 0, far < 0 ? far_lo : far_hi, nb);
+                if (seen == SOME) {
+                    hide(s, sight, t * W::BN + 32 * nb + 4 * (lane >> 5));
+                    if (a.key_mask) hide_masked(s, static_cast<uint32_t>(live >> (32 * nb + 4 * (lane >> 5))));
+                }
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float z = s[nb][i];
+                    const float z = s[i];
                     // -infinity: what a scale of either sign makes of a hidden score is a probability of 0
                     const float p = z == NEG_INF ? 0.0f : BIAS ? exp2_((z - ref) * unit) : exp2_(fmaf(z, unit, -ref));
-                    s[nb][i] = p * (dp[nb][i] - delta);
+                    s[i] = p * (dp[i] - delta);
                 }
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
-                    const Parts<T> p(s[nb], g);
+                    const Parts<T> p(s, g);
 #pragma unroll
-                    for (int db = 0; db < DB; ++db) p.mma_to(o[db], col_frag<T, DP>(kt, 32 * nb + 16 * g, db));
+                    for (int db = 0; db < DB; ++db) p.mma_to(o[db], col_frag<T, DP>(kb, lanes, 16 * g, db));
                 }
-            if constexpr (BIAS) {
-                if (far == 0) {
+                if constexpr (BIAS) {
+                    if (far == 0) {
+                        sums.add(s, t * W::BN + 32 * nb - (w.wave_at + 31 + w.off));
+                    } else {
+                        float v = 0.0f;
 #pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) sums.add(s[nb], t * W::BN + 32 * nb - (w.wave_at + 31 + w.off));
-                } else {
-                    float v = 0.0f;
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) v += s[nb][i];
-                    if (far < 0) sums.below += v;
-                    else sums.above += v;
+                        for (int i = 0; i < 16; ++i) v += s[i];
+                        if (far < 0) sums.below += v;
+                        else sums.above += v;
+                    }
                 }
             }
         }
@@ -668,23 +660,36 @@ template <typename T> __global__ __launch_bounds__(256) void attention_sum_kerne
 
 // ---- grad_k and grad_v ------------------------------------------------------------
 
+// In bf16 a workgroup has 8 waves: 4 take the first 32 queries of each tile and 4 the second, for the same 128 keys, and add up at
+// the end.  Two waves a SIMD fill each other's waits (one a SIMD, with twice the registers: 23 % of the MFMA rate); to fit in 256
+// registers beside both accumulators, v's fragments are read from LDS where DP is 128.  In fp32 the tiles leave no
+// room for that.
+template <typename T, int DP> struct KvShape {
+    static constexpr int GROUPS = sizeof(T) == 2 ? 2 : 1, THREADS = AT_THREADS * GROUPS;
+    static constexpr bool V_LDS = sizeof(T) == 2 && DP == 128;
+};
+
 template <typename T, int DP, bool BIAS>
-__global__ __launch_bounds__(AT_THREADS, 1) void attention_grad_kv_kernel(BackwardArgs f) {
-    constexpr int BQ = walk_rows<T>(), RB = BQ / 32, KS = DP / 16, DB = DP / 32, TILE = BQ * Row<T, DP>::BYTES, WIN = AT_ROWS + BQ;
-    __shared__ u32x4_t lds[4 * TILE / 16];
+__global__ __launch_bounds__((KvShape<T, DP>::THREADS), 1) void attention_grad_kv_kernel(BackwardArgs f) {
+    constexpr int BQ = walk_rows<T>(), GROUPS = KvShape<T, DP>::GROUPS, THREADS = KvShape<T, DP>::THREADS, RB = BQ / 32 / GROUPS;
+    constexpr int KS = DP / 16, DB = DP / 32, TILE = BQ * Row<T, DP>::BYTES, WIN = AT_ROWS + BQ;
+    constexpr bool V_LDS = KvShape<T, DP>::V_LDS;
+    constexpr int VTILE = V_LDS ? AT_ROWS * Row<T, DP>::BYTES : 0;
+    __shared__ __attribute__((aligned(512))) u32x4_t lds[(4 * TILE + VTILE) / 16];
     __shared__ f32x4_t stat[2 * 2 * BQ / 4];           // [buffer][lse or delta][row]
     __shared__ float win[BIAS ? 2 * WIN : 1];
     const Common& c = f.c;
     const muon_attention_args& a = c.a;
     int u, kv, split;
-    decode(c.unit0 + blockIdx.x, a.kv_heads, c.splits, span_units(a.keys, a.sequences, AT_ROWS), u, kv, split);
+    decode(c.unit0 + blockIdx.x, a.kv_heads, c.splits, span_units(a.keys, a.sequences, AT_ROWS), false, u, kv, split);
     Span sp;
     if (!find_span<AT_ROWS>(a.key_offsets, a.offsets, static_cast<int>(a.sequences), static_cast<int>(a.keys), static_cast<int>(a.queries), u, sp)) return;
-    const int lane = threadIdx.x & 63, wave = wave_id(), h = lane >> 5;
+    const int lane = threadIdx.x & 63, wave = wave_id() % AT_WAVES, group = wave_id() / AT_WAVES, h = lane >> 5;
     const int wave_at = sp.at + 32 * wave, place = wave_at + (lane & 31), nq = sp.other_len, off = sp.len - nq;
     const int64_t row = sp.start - sp.at + place;
     const bool in = place < sp.len, key_ok = in && (!a.key_mask || G(a.key_mask)[in ? row : 0] != 0);
     lds_byte_t* buf = (lds_byte_t*)lds;
+    Lanes<T, DP> lanes;
     lds_float_t* stats = (lds_float_t*)stat;
     lds_float_t* wbuf = (lds_float_t*)win;
 
@@ -697,14 +702,24 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attention_grad_kv_kernel(Backwa
         sight.set(lo, key_ok ? hi : lo);
     }
     const bool keys_all = __all(key_ok);
-    Frag<T> kf[KS], vf[KS];
+    Frag<T> kf[KS], vf[V_LDS ? 1 : KS];
+    const unsigned vt = lds_at(buf) + 4 * TILE + 32 * wave * Row<T, DP>::BYTES;
+    if constexpr (V_LDS) {
+        for (int b = 0; b < AT_ROWS; b += 64) {
+            const int j = sp.at + b + lane;
+            const int64_t first = sp.start + b;
+            const uint64_t live = __ballot(j < sp.len && (!a.key_mask || G(a.key_mask)[j < sp.len ? first + lane : 0] != 0));
+            load_tile<T, DP, 64, THREADS>(buf + 4 * TILE + b * Row<T, DP>::BYTES,
+                                          static_cast<const T*>(a.v) + first * a.ld_v + static_cast<int64_t>(kv) * a.hs_v, a.ld_v, a.width, live, c.vec_in);
+        }
+    }
     {
         const T* k = static_cast<const T*>(a.k) + row * a.ld_k + static_cast<int64_t>(kv) * a.hs_k;
         const T* v = static_cast<const T*>(a.v) + row * a.ld_v + static_cast<int64_t>(kv) * a.hs_v;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
             kf[ks] = global_frag<T>(k, 16 * ks + 8 * h, a.width, key_ok, c.vec_in);
-            vf[ks] = global_frag<T>(v, 16 * ks + 8 * h, a.width, key_ok, c.vec_in);
+            if constexpr (!V_LDS) vf[ks] = global_frag<T>(v, 16 * ks + 8 * h, a.width, key_ok, c.vec_in);
         }
     }
     // the walk: tiles first .. first + n - 1 of the queries, for every head that shares this key head
@@ -750,9 +765,9 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attention_grad_kv_kernel(Backwa
     auto load = [&](const At& w, int b, float l, float d) {
         const uint64_t live = __ballot(l != NEG_INF);
         const int64_t i0 = static_cast<int64_t>(sp.other) + static_cast<int64_t>(w.t) * BQ;
-        load_tile<T, DP, BQ, AT_THREADS>(buf + 2 * TILE * b, static_cast<const T*>(a.q) + i0 * a.ld_q + static_cast<int64_t>(w.head) * a.hs_q, a.ld_q, a.width, live, c.vec_in);
-        load_tile<T, DP, BQ, AT_THREADS>(buf + 2 * TILE * b + TILE, static_cast<const T*>(f.grad_out) + i0 * f.ld_do + static_cast<int64_t>(w.head) * f.hs_do, f.ld_do, a.width, live, c.vec_in);
-        if (wave == 0 && lane < BQ) {
+        load_tile<T, DP, BQ, THREADS>(buf + 2 * TILE * b, static_cast<const T*>(a.q) + i0 * a.ld_q + static_cast<int64_t>(w.head) * a.hs_q, a.ld_q, a.width, live, c.vec_in);
+        load_tile<T, DP, BQ, THREADS>(buf + 2 * TILE * b + TILE, static_cast<const T*>(f.grad_out) + i0 * f.ld_do + static_cast<int64_t>(w.head) * f.hs_do, f.ld_do, a.width, live, c.vec_in);
+        if (wave_id() == 0 && lane < BQ) {
             stats[2 * BQ * b + lane] = l == NEG_INF ? 0.0f : BIAS ? l : l * LOG2E;
             stats[2 * BQ * b + BQ + lane] = l == NEG_INF ? 0.0f : d;
         }
@@ -787,12 +802,13 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attention_grad_kv_kernel(Backwa
                 bw.ask(a, window_first(after(next).t));
             }
         }
-        const lds_byte_t* qt = buf + 2 * TILE * b;
-        const lds_byte_t* dt = qt + TILE;
+        const unsigned qt = lds_at(buf) + 2 * TILE * b, dt = qt + TILE;
+        lanes.fresh();
         const lds_float_t* st = stats + 2 * BQ * b;
         const int i0 = now.t * BQ;
 #pragma unroll
-        for (int rb = 0; rb < RB; ++rb) {
+        for (int rr = 0; rr < RB; ++rr) {
+            const int rb = RB * group + rr;
             const int r0 = i0 + 32 * rb, a0 = r0 + off;
             int seen = r0 >= nq || wave_at >= sp.len ? NOTHING : tile_sight(a0, a0 + 31, wave_at, wave_at + 31, a.causal, c.window);
             if (seen == NOTHING) continue;
@@ -800,8 +816,9 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attention_grad_kv_kernel(Backwa
             f32x16_t s = {}, dp = {};
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-                mma(s, row_frag<T, DP>(qt, 32 * rb, ks), kf[ks]);
-                mma(dp, row_frag<T, DP>(dt, 32 * rb, ks), vf[ks]);
+                mma(s, row_frag<T, DP>(qt, lanes, 32 * rb, ks), kf[ks]);
+                if constexpr (V_LDS) mma(dp, row_frag<T, DP>(dt, lanes, 32 * rb, ks), row_frag<T, DP>(vt, lanes, 0, ks));
+                else mma(dp, row_frag<T, DP>(dt, lanes, 32 * rb, ks), vf[ks]);
             }
             if constexpr (BIAS) {
                 // entry of key 32 wave + l % 32 and query 32 rb + 8 (i / 4) + 4 h + i % 4 of the tile
@@ -826,13 +843,38 @@ __global__ __launch_bounds__(AT_THREADS, 1) void attention_grad_kv_kernel(Backwa
                 const Parts<T> p(s, g), d(dp, g);
 #pragma unroll
                 for (int db = 0; db < DB; ++db) {
-                    p.mma_to(dv[db], col_frag<T, DP>(dt, 32 * rb + 16 * g, db));
-                    d.mma_to(dk[db], col_frag<T, DP>(qt, 32 * rb + 16 * g, db));
+                    p.mma_to(dv[db], col_frag<T, DP>(dt, lanes, 32 * rb + 16 * g, db));
+                    d.mma_to(dk[db], col_frag<T, DP>(qt, lanes, 32 * rb + 16 * g, db));
                 }
             }
         }
         if constexpr (BIAS)
             if (next.left > 0) bw.put(wbuf + (b ^ 1) * WIN);
+    }
+    if constexpr (GROUPS == 2) {
+        // the second group's sums through the tiles' LDS, one matrix at a time
+        lds_f32x4_t* room = (lds_f32x4_t*)lds + wave * 64 * 4 * DB + lane;
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            f32x16_t (&acc)[DB] = m ? dv : dk;
+            tile_barrier();
+            if (group == 1)
+#pragma unroll
+                for (int db = 0; db < DB; ++db)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) room[64 * (4 * db + q)] = f32x4_t{acc[db][4 * q], acc[db][4 * q + 1], acc[db][4 * q + 2], acc[db][4 * q + 3]};
+            tile_barrier();
+            if (group == 0)
+#pragma unroll
+                for (int db = 0; db < DB; ++db)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const f32x4_t v = room[64 * (4 * db + q)];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[db][4 * q + e] += v[e];
+                    }
+        }
+        if (group == 1) return;
     }
     if (!in) return;
     if (c.splits > 1) {
@@ -967,7 +1009,7 @@ hipError_t run_backward(BackwardArgs f, const BackwardPlan& p, const muon_attent
     f.part = reinterpret_cast<float*>(ws + p.kv_part);
     e = in_launches(span_units(a.keys, a.sequences, AT_ROWS) * a.kv_heads * p.kv_splits, [&](int64_t base, unsigned n) {
         f.c.unit0 = base;
-        hipLaunchKernelGGL((attention_grad_kv_kernel<T, DP, BIAS>), dim3(n), dim3(AT_THREADS), 0, s, f);
+        hipLaunchKernelGGL((attention_grad_kv_kernel<T, DP, BIAS>), dim3(n), dim3(KvShape<T, DP>::THREADS), 0, s, f);
         return hipGetLastError();
     });
     if (e != hipSuccess || p.kv_splits == 1) return e;

@@ -101,42 +101,57 @@ template <typename T, int DP> struct Row {
     }
 };
 
-// A operand: rows row0 + l % 32 of the tile, step ks along them.  row0 a multiple of 32.
-template <typename T, int DP> __device__ __forceinline__ Frag<T> row_frag(const lds_byte_t* tile, int row0, int ks) {
+// Where a lane reads in a tile: byte addresses for step 0 of row_frag and block 0 of col_frag.  A tile starts at a multiple
+// of 512 bytes, so the chunk of another step or block is one exclusive or away.  fresh() keeps the compiler from holding every such
+// address in a register of its own through the whole loop.
+template <typename T, int DP> struct Lanes {
+    unsigned row, col;
+    __device__ __forceinline__ Lanes() {
+        typedef Row<T, DP> R;
+        const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+        if constexpr (R::ES == 2) {
+            row = r * R::BYTES + ((h ^ R::swizzle(r)) << 4);
+            // ds_read_b64_tr_b16: 16 lanes read 4 rows of 16 values, lane i gets column i of them
+            const int i16 = lane & 15, g16 = lane >> 4, cr = 4 * (g16 >> 1) + (i16 >> 2);
+            col = cr * R::BYTES + (((2 * (g16 & 1) + ((i16 & 3) >> 1)) ^ R::swizzle(cr)) << 4) + (i16 & 1) * 8;
+        } else {
+            row = r * R::BYTES + (((2 * h) ^ R::swizzle(r)) << 4);
+            col = 4 * h * R::BYTES + (((r >> 2) ^ (h << 3)) << 4) + (r & 3) * 4;
+        }
+    }
+    __device__ __forceinline__ void fresh() { asm volatile("" : "+v"(row), "+v"(col)); }
+};
+__device__ __forceinline__ unsigned lds_at(const lds_byte_t* p) { return static_cast<unsigned>(reinterpret_cast<uintptr_t>(p)); }
+template <typename V> __device__ __forceinline__ V ld_lds(unsigned at) { return *(const __attribute__((address_space(3))) V*)static_cast<uintptr_t>(at); }
+
+// A operand: rows row0 + l % 32 of the tile at `tile`, step ks along them.  row0 a multiple of 32.
+template <typename T, int DP> __device__ __forceinline__ Frag<T> row_frag(unsigned tile, const Lanes<T, DP>& w, int row0, int ks) {
     typedef Row<T, DP> R;
-    const int lane = threadIdx.x & 63, row = lane & 31, h = lane >> 5, sw = R::swizzle(row);
-    const lds_byte_t* p = tile + (row0 + row) * R::BYTES;
     Frag<T> f;
     if constexpr (R::ES == 2) {
-        f.w = *(const lds_u32x4_t*)(p + ((2 * ks + h) ^ sw) * 16);
+        f.w = ld_lds<u32x4_t>(((tile + w.row) ^ (ks << 5)) + row0 * R::BYTES);
     } else {
-        f.w[0] = *(const lds_f32x4_t*)(p + ((4 * ks + 2 * h) ^ sw) * 16);
-        f.w[1] = *(const lds_f32x4_t*)(p + ((4 * ks + 2 * h + 1) ^ sw) * 16);
+        f.w[0] = ld_lds<f32x4_t>(((tile + w.row) ^ (ks << 6)) + row0 * R::BYTES);
+        f.w[1] = ld_lds<f32x4_t>(((tile + w.row) ^ (ks << 6) ^ 16) + row0 * R::BYTES);
     }
     return f;
 }
 
 // A operand, transposed: column 32 db + l % 32 of the tile at the rows row0 + 8 (j / 4) + 4 h + j % 4.  row0 a multiple of 16.
-template <typename T, int DP> __device__ __forceinline__ Frag<T> col_frag(const lds_byte_t* tile, int row0, int db) {
+template <typename T, int DP> __device__ __forceinline__ Frag<T> col_frag(unsigned tile, const Lanes<T, DP>& w, int row0, int db) {
     typedef Row<T, DP> R;
-    const int lane = threadIdx.x & 63;
     Frag<T> f;
     if constexpr (R::ES == 2) {
-        // ds_read_b64_tr_b16: 16 lanes read 4 rows of 16 values, lane i gets column i of them
-        const int i16 = lane & 15, g16 = lane >> 4;
-        const int row = 4 * (g16 >> 1) + (i16 >> 2), c = 4 * db + 2 * (g16 & 1) + ((i16 & 3) >> 1);
-        const lds_byte_t* p = tile + (row0 + row) * R::BYTES + (i16 & 1) * 8;
-        const i16x4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(p + (c ^ R::swizzle(row)) * 16));
-        const i16x4_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(p + 8 * R::BYTES + (c ^ R::swizzle(row + 8)) * 16));
+        const unsigned p = (tile + w.col) ^ (db << 6);
+        const i16x4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)static_cast<uintptr_t>(p + row0 * R::BYTES));
+        const i16x4_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)static_cast<uintptr_t>((p ^ 32) + (row0 + 8) * R::BYTES));
         const u32x2_t a2 = __builtin_bit_cast(u32x2_t, a), b2 = __builtin_bit_cast(u32x2_t, b);
         f.w = u32x4_t{a2.x, a2.y, b2.x, b2.y};
     } else {
-        const int col = 32 * db + (lane & 31), h = lane >> 5;
+        // swizzle(row) of the row of slot j is j + 8 h
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int row = 8 * (j >> 2) + 4 * h + (j & 3);
-            f.w[j >> 2][j & 3] = *(const lds_float_t*)(tile + (row0 + row) * R::BYTES + ((col >> 2) ^ R::swizzle(row)) * 16 + (col & 3) * 4);
-        }
+        for (int j = 0; j < 8; ++j)
+            f.w[j >> 2][j & 3] = ld_lds<float>(((tile + w.col) ^ (db << 7) ^ (j << 4)) + (row0 + 8 * (j >> 2) + (j & 3)) * R::BYTES);
     }
     return f;
 }
