@@ -24,8 +24,9 @@ using namespace at;
 constexpr int AT_THREADS = 256, AT_WAVES = 4, AT_ROWS = 128;   // rows (queries or keys) a workgroup
 constexpr int AT_MAX_SPLITS = 64;
 
-// Rows of a walked tile.
+// Rows of a walked tile: of keys, and of queries for grad_k and grad_v.
 template <typename T> constexpr int walk_rows() { return sizeof(T) == 2 ? 64 : 32; }
+constexpr int KV_ROWS = 32;
 
 struct Common {
     muon_attention_args a;
@@ -54,17 +55,23 @@ struct BackwardArgs {
 };
 
 // Which unit of the axis, head and split a workgroup has.  Heads go fastest, and where they allow it in runs that share an XCD
-// (workgroups go to XCDs in turn), so that a key head's rows stay in one L2.  The units that walk the longest under a causal mask
-// come first: the last queries, the first keys (16384 tokens, grad_k and grad_v the other way round: half as long again).
-__device__ __forceinline__ void decode(int64_t id, int heads, int splits, int64_t axis, bool from_end, int& u, int& head, int& split) {
+// (workgroups go to XCDs in turn), so that a key head's rows stay in one L2.
+__device__ __forceinline__ void decode(int64_t id, int heads, int splits, int& u, int& head, int& split) {
     const int hs = heads * splits;
-    const int64_t r = id / hs;
-    int k = static_cast<int>(id - r * hs);
+    u = static_cast<int>(id / hs);
+    int k = static_cast<int>(id - static_cast<int64_t>(u) * hs);
     if (hs % 8 == 0) k = (k % 8) * (hs / 8) + k / 8;
     head = k / splits;
     split = k - head * splits;
-    u = static_cast<int>(from_end ? axis - 1 - r : r);
 }
+
+// A negative scale goes into the sign of one factor of the scores and a scale of 0 into its values: then a score that is hidden, at
+// -infinity, stays there under the (positive) factor that remains.
+template <typename T> __device__ __forceinline__ void negate(Frag<T>& f) {
+    if constexpr (sizeof(T) == 2) f.w ^= 0x80008000u;
+    else { f.w[0] = -f.w[0]; f.w[1] = -f.w[1]; }
+}
+__device__ __forceinline__ float size_of(float scale) { return scale == 0.0f ? 1.0f : fabsf(scale); }
 
 // Bias of a head at distance j - a.
 template <typename T> __device__ __forceinline__ int bucket_at(const muon_attention_args& a, int dist) {
@@ -203,9 +210,9 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 ? 2 : 1) void attention_
     const Common& c = f.c;
     const muon_attention_args& a = c.a;
     int u, head, split;
-    decode(c.unit0 + blockIdx.x, a.heads, c.splits, span_units(a.queries, a.sequences, AT_ROWS), true, u, head, split);
+    decode(c.unit0 + blockIdx.x, a.heads, c.splits, u, head, split);
     Span sp;
-    if (!find_span<AT_ROWS>(a.offsets, a.key_offsets, static_cast<int>(a.sequences), static_cast<int>(a.queries), static_cast<int>(a.keys), u, sp)) return;
+    if (!find_span<AT_ROWS, false>(a.offsets, a.key_offsets, static_cast<int>(a.sequences), static_cast<int>(a.queries), static_cast<int>(a.keys), a.causal, u, sp)) return;
     const W w(c, sp, head, split);
     const int lane = threadIdx.x & 63, place = w.wave_at + (lane & 31);
     const bool row_ok = place < sp.len;
@@ -215,20 +222,16 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 ? 2 : 1) void attention_
     Lanes<T, DP> lanes;
     lds_float_t* wbuf = (lds_float_t*)win;
 
-    // a negative scale goes into q's sign and a scale of 0 into q, so that the largest score is the largest product
     Frag<T> qf[KS];
     {
         const T* q = static_cast<const T*>(a.q) + row * a.ld_q + static_cast<int64_t>(head) * a.hs_q;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
             qf[ks] = global_frag<T>(q, 16 * ks + 8 * (lane >> 5), a.width, row_ok && a.scale != 0.0f, c.vec_in);
-            if (a.scale < 0.0f) {
-                if constexpr (sizeof(T) == 2) qf[ks].w ^= 0x80008000u;
-                else { qf[ks].w[0] = -qf[ks].w[0]; qf[ks].w[1] = -qf[ks].w[1]; }
-            }
+            if (a.scale < 0.0f) negate<T>(qf[ks]);
         }
     }
-    const float scale = a.scale == 0.0f ? 1.0f : fabsf(a.scale), unit = BIAS ? LOG2E : scale * LOG2E;     // from what s holds to powers of two
+    const float scale = size_of(a.scale), unit = BIAS ? LOG2E : scale * LOG2E;     // from what s holds to powers of two
     const float slack = 8.0f / LOG2E * (BIAS ? 1.0f : LOG2E);                    // 8 powers of two, in m's units
 
     f32x16_t o[DB] = {};
@@ -477,8 +480,7 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 && !(BIAS && DP == 128) 
     const Common& c = f.c;
     const muon_attention_args& a = c.a;
     int u, head, split;
-    const int64_t axis = span_units(a.queries, a.sequences, AT_ROWS);
-    decode(c.unit0 + blockIdx.x, a.heads, c.splits, axis, true, u, head, split);
+    decode(c.unit0 + blockIdx.x, a.heads, c.splits, u, head, split);
     lds_float_t* wbuf = (lds_float_t*)win;
     BiasSums sums;
     if constexpr (BIAS) {
@@ -486,7 +488,7 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 && !(BIAS && DP == 128) 
         sums.start(wbuf + 2 * W::WIN + BiasSums::ROOM * wave_id(), f.bias_part + slot * (2 * a.reach + 1), a.reach);
     }
     Span sp;
-    if (!find_span<AT_ROWS>(a.offsets, a.key_offsets, static_cast<int>(a.sequences), static_cast<int>(a.queries), static_cast<int>(a.keys), u, sp)) {
+    if (!find_span<AT_ROWS, false>(a.offsets, a.key_offsets, static_cast<int>(a.sequences), static_cast<int>(a.queries), static_cast<int>(a.keys), a.causal, u, sp)) {
         if constexpr (BIAS) sums.finish();
         return;
     }
@@ -511,7 +513,8 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 && !(BIAS && DP == 128) 
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
             const int e0 = 16 * ks + 8 * h;
-            qf[ks] = global_frag<T>(q, e0, a.width, row_ok, c.vec_in);
+            qf[ks] = global_frag<T>(q, e0, a.width, row_ok && a.scale != 0.0f, c.vec_in);
+            if (a.scale < 0.0f) negate<T>(qf[ks]);
             df[ks] = global_frag<T>(d, e0, a.width, row_ok, c.vec_in);
             const Frag<T> of = global_frag<T>(out, e0, a.width, row_ok, c.vec_in);
 #pragma unroll
@@ -525,7 +528,7 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 && !(BIAS && DP == 128) 
         delta = half_sum(delta);
         if (place < sp.len && lane < 32 && split == 0) G(f.delta)[row * a.heads + head] = delta;
     }
-    const float unit = BIAS ? LOG2E : a.scale * LOG2E;
+    const float scale = size_of(a.scale), unit = BIAS ? LOG2E : scale * LOG2E;
     const float ref = row_ok ? (BIAS ? lse : lse * LOG2E) : 0.0f;
 
     f32x16_t o[DB] = {};
@@ -571,7 +574,7 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 && !(BIAS && DP == 128) 
             const unsigned kt = lds_at(buf) + 2 * W::TILE * b;
             const int far = BIAS ? w.far(t) : 0;
             // a block of 32 keys at a time: all of a tile at once does not fit the registers of two waves a SIMD
-#pragma unroll 1
+#pragma unroll DP == 64 ? NB : 1
             for (int nb = 0; nb < NB; ++nb) {
                 const unsigned kb = kt + 32 * nb * Row<T, DP>::BYTES, vb = kb + W::TILE;
                 lanes.fresh();
@@ -581,16 +584,14 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 && !(BIAS && DP == 128) 
                     mma(s, row_frag<T, DP>(kb, lanes, 0, ks), qf[ks]);
                     mma(dp, row_frag<T, DP>(vb, lanes, 0, ks), df[ks]);
                 }
-                if constexpr (BIAS) w.add_bias(s, a.scale, wbuf + b * W::WIN, far == 0, far < 0 ? far_lo : far_hi, nb);
+                if constexpr (BIAS) w.add_bias(s, scale, wbuf + b * W::WIN, far == 0, far < 0 ? far_lo : far_hi, nb);
                 if (seen == SOME) {
                     hide(s, sight, t * W::BN + 32 * nb + 4 * (lane >> 5));
                     if (a.key_mask) hide_masked(s, static_cast<uint32_t>(live >> (32 * nb + 4 * (lane >> 5))));
                 }
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float z = s[i];
-                    // -infinity: what a scale of either sign makes of a hidden score is a probability of 0
-                    const float p = z == NEG_INF ? 0.0f : BIAS ? exp2_((z - ref) * unit) : exp2_(fmaf(z, unit, -ref));
+                    const float p = BIAS ? exp2_((s[i] - ref) * unit) : exp2_(fmaf(s[i], unit, -ref));
                     s[i] = p * (dp[i] - delta);
                 }
 #pragma unroll
@@ -627,15 +628,27 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 && !(BIAS && DP == 128) 
 
 // Adds up the slots of one head for 64 distances, then those of a bucket.  The orders are fixed; sums in fp64: they have up to
 // millions of terms of either sign.
-__global__ __launch_bounds__(256) void attention_bias_slots_kernel(const float* part, int64_t slots, int entries, double* sums) {
-    __shared__ double red[4][64];
-    const int lane = threadIdx.x & 63, wave = wave_id(), d = blockIdx.x * 64 + lane, head = blockIdx.y;
+__global__ __launch_bounds__(1024) void attention_bias_slots_kernel(const float* part, int64_t slots, int entries, double* sums) {
+    __shared__ double red[16][64];
+    const int lane = threadIdx.x & 63, wave = wave_id(), head = blockIdx.y;
+    const int d = min(static_cast<int>(blockIdx.x) * 64 + lane, entries - 1);
     double v = 0.0;
-    if (d < entries)
-        for (int64_t s = wave; s < slots; s += 4) v += G(part)[(head * slots + s) * entries + d];
+    const float* p = part + head * slots * entries + d;
+    int64_t s = wave;
+    for (; s + 7 * 16 < slots; s += 8 * 16) {
+        float x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = G(p)[(s + 16 * k) * entries];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v += x[k];
+    }
+    for (; s < slots; s += 16) v += G(p)[s * entries];
     red[wave][lane] = v;
     __syncthreads();
-    if (wave == 0 && d < entries) G(sums)[static_cast<int64_t>(head) * entries + d] = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+    if (wave == 0) {
+        for (int k = 1; k < 16; ++k) v += red[k][lane];
+        if (static_cast<int>(blockIdx.x) * 64 + lane < entries) G(sums)[static_cast<int64_t>(head) * entries + d] = v;
+    }
 }
 template <typename T> __global__ __launch_bounds__(64) void attention_bias_kernel(const int32_t* map, const double* sums, int entries, int heads, void* grad) {
     const int bucket = blockIdx.x, head = blockIdx.y;
@@ -660,18 +673,17 @@ template <typename T> __global__ __launch_bounds__(256) void attention_sum_kerne
 
 // ---- grad_k and grad_v ------------------------------------------------------------
 
-// In bf16 a workgroup has 8 waves: 4 take the first 32 queries of each tile and 4 the second, for the same 128 keys, and add up at
-// the end.  Two waves a SIMD fill each other's waits (one a SIMD, with twice the registers: 23 % of the MFMA rate); to fit in 256
-// registers beside both accumulators, v's fragments are read from LDS where DP is 128.  In fp32 the tiles leave no
-// room for that.
+// Two waves a SIMD, of workgroups that share no barrier, fill each other's waits.  In bf16 with DP 128 that takes v's fragments out of
+// LDS (both accumulators, k's fragments and a block's scores fill 256 registers), and tiles of 32 queries, so that two
+// workgroups fit a CU's LDS.
 template <typename T, int DP> struct KvShape {
-    static constexpr int GROUPS = sizeof(T) == 2 ? 2 : 1, THREADS = AT_THREADS * GROUPS;
     static constexpr bool V_LDS = sizeof(T) == 2 && DP == 128;
+    static constexpr int WAVES = sizeof(T) == 2 ? 2 : 1;      // a SIMD
 };
 
 template <typename T, int DP, bool BIAS>
-__global__ __launch_bounds__((KvShape<T, DP>::THREADS), 1) void attention_grad_kv_kernel(BackwardArgs f) {
-    constexpr int BQ = walk_rows<T>(), GROUPS = KvShape<T, DP>::GROUPS, THREADS = KvShape<T, DP>::THREADS, RB = BQ / 32 / GROUPS;
+__global__ __launch_bounds__(AT_THREADS, (KvShape<T, DP>::WAVES)) void attention_grad_kv_kernel(BackwardArgs f) {
+    constexpr int BQ = KV_ROWS;
     constexpr int KS = DP / 16, DB = DP / 32, TILE = BQ * Row<T, DP>::BYTES, WIN = AT_ROWS + BQ;
     constexpr bool V_LDS = KvShape<T, DP>::V_LDS;
     constexpr int VTILE = V_LDS ? AT_ROWS * Row<T, DP>::BYTES : 0;
@@ -681,10 +693,10 @@ __global__ __launch_bounds__((KvShape<T, DP>::THREADS), 1) void attention_grad_k
     const Common& c = f.c;
     const muon_attention_args& a = c.a;
     int u, kv, split;
-    decode(c.unit0 + blockIdx.x, a.kv_heads, c.splits, span_units(a.keys, a.sequences, AT_ROWS), false, u, kv, split);
+    decode(c.unit0 + blockIdx.x, a.kv_heads, c.splits, u, kv, split);
     Span sp;
-    if (!find_span<AT_ROWS>(a.key_offsets, a.offsets, static_cast<int>(a.sequences), static_cast<int>(a.keys), static_cast<int>(a.queries), u, sp)) return;
-    const int lane = threadIdx.x & 63, wave = wave_id() % AT_WAVES, group = wave_id() / AT_WAVES, h = lane >> 5;
+    if (!find_span<AT_ROWS, true>(a.key_offsets, a.offsets, static_cast<int>(a.sequences), static_cast<int>(a.keys), static_cast<int>(a.queries), a.causal, u, sp)) return;
+    const int lane = threadIdx.x & 63, wave = wave_id(), h = lane >> 5;
     const int wave_at = sp.at + 32 * wave, place = wave_at + (lane & 31), nq = sp.other_len, off = sp.len - nq;
     const int64_t row = sp.start - sp.at + place;
     const bool in = place < sp.len, key_ok = in && (!a.key_mask || G(a.key_mask)[in ? row : 0] != 0);
@@ -709,7 +721,7 @@ __global__ __launch_bounds__((KvShape<T, DP>::THREADS), 1) void attention_grad_k
             const int j = sp.at + b + lane;
             const int64_t first = sp.start + b;
             const uint64_t live = __ballot(j < sp.len && (!a.key_mask || G(a.key_mask)[j < sp.len ? first + lane : 0] != 0));
-            load_tile<T, DP, 64, THREADS>(buf + 4 * TILE + b * Row<T, DP>::BYTES,
+            load_tile<T, DP, 64, AT_THREADS>(buf + 4 * TILE + b * Row<T, DP>::BYTES,
                                           static_cast<const T*>(a.v) + first * a.ld_v + static_cast<int64_t>(kv) * a.hs_v, a.ld_v, a.width, live, c.vec_in);
         }
     }
@@ -718,7 +730,8 @@ __global__ __launch_bounds__((KvShape<T, DP>::THREADS), 1) void attention_grad_k
         const T* v = static_cast<const T*>(a.v) + row * a.ld_v + static_cast<int64_t>(kv) * a.hs_v;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-            kf[ks] = global_frag<T>(k, 16 * ks + 8 * h, a.width, key_ok, c.vec_in);
+            kf[ks] = global_frag<T>(k, 16 * ks + 8 * h, a.width, key_ok && a.scale != 0.0f, c.vec_in);
+            if (a.scale < 0.0f) negate<T>(kf[ks]);
             if constexpr (!V_LDS) vf[ks] = global_frag<T>(v, 16 * ks + 8 * h, a.width, key_ok, c.vec_in);
         }
     }
@@ -765,9 +778,9 @@ __global__ __launch_bounds__((KvShape<T, DP>::THREADS), 1) void attention_grad_k
     auto load = [&](const At& w, int b, float l, float d) {
         const uint64_t live = __ballot(l != NEG_INF);
         const int64_t i0 = static_cast<int64_t>(sp.other) + static_cast<int64_t>(w.t) * BQ;
-        load_tile<T, DP, BQ, THREADS>(buf + 2 * TILE * b, static_cast<const T*>(a.q) + i0 * a.ld_q + static_cast<int64_t>(w.head) * a.hs_q, a.ld_q, a.width, live, c.vec_in);
-        load_tile<T, DP, BQ, THREADS>(buf + 2 * TILE * b + TILE, static_cast<const T*>(f.grad_out) + i0 * f.ld_do + static_cast<int64_t>(w.head) * f.hs_do, f.ld_do, a.width, live, c.vec_in);
-        if (wave_id() == 0 && lane < BQ) {
+        load_tile<T, DP, BQ, AT_THREADS>(buf + 2 * TILE * b, static_cast<const T*>(a.q) + i0 * a.ld_q + static_cast<int64_t>(w.head) * a.hs_q, a.ld_q, a.width, live, c.vec_in);
+        load_tile<T, DP, BQ, AT_THREADS>(buf + 2 * TILE * b + TILE, static_cast<const T*>(f.grad_out) + i0 * f.ld_do + static_cast<int64_t>(w.head) * f.hs_do, f.ld_do, a.width, live, c.vec_in);
+        if (wave == 0 && lane < BQ) {
             stats[2 * BQ * b + lane] = l == NEG_INF ? 0.0f : BIAS ? l : l * LOG2E;
             stats[2 * BQ * b + BQ + lane] = l == NEG_INF ? 0.0f : d;
         }
@@ -775,7 +788,7 @@ __global__ __launch_bounds__((KvShape<T, DP>::THREADS), 1) void attention_grad_k
     // distance of the window's first entry for tile t: that of this workgroup's first key and the tile's last query
     auto window_first = [&](int t) { return sp.at - (t * BQ + BQ - 1 + off); };
 
-    const float unit = BIAS ? LOG2E : a.scale * LOG2E;
+    const float scale = size_of(a.scale), unit = BIAS ? LOG2E : scale * LOG2E;
     f32x16_t dk[DB] = {}, dv[DB] = {};
     BiasWindow<T, WIN> bw;
     float lse = 0.0f, delta = 0.0f;
@@ -806,34 +819,30 @@ __global__ __launch_bounds__((KvShape<T, DP>::THREADS), 1) void attention_grad_k
         lanes.fresh();
         const lds_float_t* st = stats + 2 * BQ * b;
         const int i0 = now.t * BQ;
-#pragma unroll
-        for (int rr = 0; rr < RB; ++rr) {
-            const int rb = RB * group + rr;
-            const int r0 = i0 + 32 * rb, a0 = r0 + off;
-            int seen = r0 >= nq || wave_at >= sp.len ? NOTHING : tile_sight(a0, a0 + 31, wave_at, wave_at + 31, a.causal, c.window);
-            if (seen == NOTHING) continue;
-            if (r0 + 31 >= nq || !keys_all) seen = SOME;
+        int seen = wave_at >= sp.len ? NOTHING : tile_sight(i0 + off, i0 + off + 31, wave_at, wave_at + 31, a.causal, c.window);
+        if (seen != NOTHING) {
+            if (i0 + 31 >= nq || !keys_all) seen = SOME;
             f32x16_t s = {}, dp = {};
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-                mma(s, row_frag<T, DP>(qt, lanes, 32 * rb, ks), kf[ks]);
-                if constexpr (V_LDS) mma(dp, row_frag<T, DP>(dt, lanes, 32 * rb, ks), row_frag<T, DP>(vt, lanes, 0, ks));
-                else mma(dp, row_frag<T, DP>(dt, lanes, 32 * rb, ks), vf[ks]);
+                mma(s, row_frag<T, DP>(qt, lanes, 0, ks), kf[ks]);
+                if constexpr (V_LDS) mma(dp, row_frag<T, DP>(dt, lanes, 0, ks), row_frag<T, DP>(vt, lanes, 0, ks));
+                else mma(dp, row_frag<T, DP>(dt, lanes, 0, ks), vf[ks]);
             }
             if constexpr (BIAS) {
-                // entry of key 32 wave + l % 32 and query 32 rb + 8 (i / 4) + 4 h + i % 4 of the tile
-                const lds_float_t* p = wbuf + b * WIN + (BQ - 1 - 32 * rb - 4 * h) + 32 * wave + (lane & 31);
+                // entry of key 32 wave + l % 32 and query 8 (i / 4) + 4 h + i % 4 of the tile
+                const lds_float_t* p = wbuf + b * WIN + (BQ - 1 - 4 * h) + 32 * wave + (lane & 31);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) s[i] = fmaf(s[i], a.scale, p[-(8 * (i >> 2) + (i & 3))]);
+                for (int i = 0; i < 16; ++i) s[i] = fmaf(s[i], scale, p[-(8 * (i >> 2) + (i & 3))]);
             }
-            if (seen == SOME) hide(s, sight, r0 + 4 * h);
+            if (seen == SOME) hide(s, sight, i0 + 4 * h);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const f32x4_t ref = *(const lds_f32x4_t*)(st + 32 * rb + 8 * q + 4 * h), dl = *(const lds_f32x4_t*)(st + BQ + 32 * rb + 8 * q + 4 * h);
+                const f32x4_t ref = *(const lds_f32x4_t*)(st + 8 * q + 4 * h), dl = *(const lds_f32x4_t*)(st + BQ + 8 * q + 4 * h);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float z = s[4 * q + e];
-                    const float p = z == NEG_INF ? 0.0f : BIAS ? exp2_((z - ref[e]) * unit) : exp2_(fmaf(z, unit, -ref[e]));
+                    const float p = BIAS ? exp2_((z - ref[e]) * unit) : exp2_(fmaf(z, unit, -ref[e]));
                     s[4 * q + e] = p;
                     dp[4 * q + e] = p * (dp[4 * q + e] - dl[e]);
                 }
@@ -843,38 +852,13 @@ __global__ __launch_bounds__((KvShape<T, DP>::THREADS), 1) void attention_grad_k
                 const Parts<T> p(s, g), d(dp, g);
 #pragma unroll
                 for (int db = 0; db < DB; ++db) {
-                    p.mma_to(dv[db], col_frag<T, DP>(dt, lanes, 32 * rb + 16 * g, db));
-                    d.mma_to(dk[db], col_frag<T, DP>(qt, lanes, 32 * rb + 16 * g, db));
+                    p.mma_to(dv[db], col_frag<T, DP>(dt, lanes, 16 * g, db));
+                    d.mma_to(dk[db], col_frag<T, DP>(qt, lanes, 16 * g, db));
                 }
             }
         }
         if constexpr (BIAS)
             if (next.left > 0) bw.put(wbuf + (b ^ 1) * WIN);
-    }
-    if constexpr (GROUPS == 2) {
-        // the second group's sums through the tiles' LDS, one matrix at a time
-        lds_f32x4_t* room = (lds_f32x4_t*)lds + wave * 64 * 4 * DB + lane;
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-            f32x16_t (&acc)[DB] = m ? dv : dk;
-            tile_barrier();
-            if (group == 1)
-#pragma unroll
-                for (int db = 0; db < DB; ++db)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) room[64 * (4 * db + q)] = f32x4_t{acc[db][4 * q], acc[db][4 * q + 1], acc[db][4 * q + 2], acc[db][4 * q + 3]};
-            tile_barrier();
-            if (group == 0)
-#pragma unroll
-                for (int db = 0; db < DB; ++db)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const f32x4_t v = room[64 * (4 * db + q)];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[db][4 * q + e] += v[e];
-                    }
-        }
-        if (group == 1) return;
     }
     if (!in) return;
     if (c.splits > 1) {
@@ -890,17 +874,19 @@ __global__ __launch_bounds__((KvShape<T, DP>::THREADS), 1) void attention_grad_k
 
 // ---- host -------------------------------------------------------------------------
 
-// Few units of an axis leave CUs idle: their walks are split until about two workgroups a CU have work, while a part keeps `least`
-// tiles on average.
-int plan_splits(int64_t rows, int64_t sequences, int heads, int64_t walk, int tile, int least) {
+// Few units of an axis leave CUs idle: their walks are split until about two workgroups a CU have work, while a part keeps two
+// tiles on average.  Walks so long that a part keeps 64 tiles are split until there are eight workgroups a CU, so that the
+// longest under a causal mask do not end alone (16384 tokens, 4 key heads, grad_k and grad_v: 5.8 ms in one part).
+int plan_splits(int64_t rows, int64_t sequences, int heads, int64_t walk, int tile) {
     const int64_t units = (rows / AT_ROWS + sequences) * heads;
     const int64_t tiles = std::max<int64_t>(1, walk / sequences / tile);
-    const int64_t want = std::min<int64_t>({512 / std::max<int64_t>(1, units), tiles / least, AT_MAX_SPLITS});
-    return static_cast<int>(std::max<int64_t>(1, want));
+    const int64_t n = std::max<int64_t>(1, units);
+    const int64_t want = std::max(std::min(512 / n, tiles / 2), std::min(2048 / n, tiles / 64));
+    return static_cast<int>(std::min<int64_t>(std::max<int64_t>(1, want), AT_MAX_SPLITS));
 }
 int tile_rows(int dtype) { return dtype == MUON_BF16 ? walk_rows<uint16_t>() : walk_rows<float>(); }
 
-int forward_splits(const muon_attention_args& a) { return plan_splits(a.queries, a.sequences, a.heads, a.keys, tile_rows(a.dtype), 2); }
+int forward_splits(const muon_attention_args& a) { return plan_splits(a.queries, a.sequences, a.heads, a.keys, tile_rows(a.dtype)); }
 struct BackwardPlan {
     int q_splits, kv_splits;
     int64_t slots;                                  // of the bias's partial sums, per head
@@ -909,8 +895,8 @@ struct BackwardPlan {
 BackwardPlan plan_backward(const muon_attention_backward_args& a) {
     BackwardPlan p{};
     const int tr = tile_rows(a.dtype);
-    p.q_splits = plan_splits(a.queries, a.sequences, a.heads, a.keys, tr, 2);
-    p.kv_splits = plan_splits(a.keys, a.sequences, a.kv_heads, a.queries * (a.heads / a.kv_heads), tr, 2);
+    p.q_splits = plan_splits(a.queries, a.sequences, a.heads, a.keys, tr);
+    p.kv_splits = plan_splits(a.keys, a.sequences, a.kv_heads, a.queries * (a.heads / a.kv_heads), KV_ROWS);
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t here = at;
@@ -999,7 +985,7 @@ hipError_t run_backward(BackwardArgs f, const BackwardPlan& p, const muon_attent
     if constexpr (BIAS) {
         const int entries = 2 * a.reach + 1;
         double* sums = reinterpret_cast<double*>(ws + p.bias_sums);
-        hipLaunchKernelGGL(attention_bias_slots_kernel, dim3((entries + 63) / 64, a.heads), dim3(256), 0, s, f.bias_part, a.queries > 0 ? p.slots : 0, entries, sums);
+        hipLaunchKernelGGL(attention_bias_slots_kernel, dim3((entries + 63) / 64, a.heads), dim3(1024), 0, s, f.bias_part, a.queries > 0 ? p.slots : 0, entries, sums);
         hipLaunchKernelGGL((attention_bias_kernel<T>), dim3(a.buckets, a.heads), dim3(64), 0, s, a.bucket_map, sums, entries, a.heads, b.grad_bias);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
@@ -1009,7 +995,7 @@ hipError_t run_backward(BackwardArgs f, const BackwardPlan& p, const muon_attent
     f.part = reinterpret_cast<float*>(ws + p.kv_part);
     e = in_launches(span_units(a.keys, a.sequences, AT_ROWS) * a.kv_heads * p.kv_splits, [&](int64_t base, unsigned n) {
         f.c.unit0 = base;
-        hipLaunchKernelGGL((attention_grad_kv_kernel<T, DP, BIAS>), dim3(n), dim3(KvShape<T, DP>::THREADS), 0, s, f);
+        hipLaunchKernelGGL((attention_grad_kv_kernel<T, DP, BIAS>), dim3(n), dim3(AT_THREADS), 0, s, f);
         return hipGetLastError();
     });
     if (e != hipSuccess || p.kv_splits == 1) return e;
