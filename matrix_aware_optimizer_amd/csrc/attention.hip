@@ -23,6 +23,12 @@ using namespace at;
 
 constexpr int AT_THREADS = 256, AT_WAVES = 4, AT_ROWS = 128;   // rows (queries or keys) a workgroup
 constexpr int AT_MAX_SPLITS = 64;
+constexpr int64_t AT_CUS = 256;
+constexpr int64_t AT_BUCKET_READS = 65536;                      // values of the bias's slots that a workgroup adds up for a bucket
+
+// fp32 products take 16 times as long as bf16's: steps and blocks of columns that a narrow head does not have are left out (72 of
+// 128: 4 of 11 of a tile's products).
+template <typename T> __device__ __forceinline__ bool beyond(int column, int width) { return sizeof(T) == 4 && column >= width; }
 
 // Rows of a walked tile: of keys, and of queries for grad_k and grad_v.
 template <typename T> constexpr int walk_rows() { return sizeof(T) == 2 ? 64 : 32; }
@@ -48,10 +54,13 @@ struct BackwardArgs {
     void* grad_k;
     void* grad_v;
     int64_t ld_do, hs_do, ld_dq, hs_dq, ld_dk, hs_dk, ld_dv, hs_dv;
-    float* delta;         // query x head
-    float* part;          // splits > 1: sums of each split
+    float* delta;         // query x head; NULL where one launch does all
+    int q_splits, kv_splits;
+    float* q_part;        // splits > 1: sums of each split
+    float* kv_part;
     float* bias_part;     // [head][slot][2 reach + 1], a slot per wave
     int64_t slots;
+    int64_t q_blocks;     // one launch for all: its first blocks make grad_q
 };
 
 // Which unit of the axis, head and split a workgroup has.  Heads go fastest, and where they allow it in runs that share an XCD
@@ -135,7 +144,7 @@ template <typename T, int DP> struct KeyWalk {
     const T* vbase;
     uint64_t pending;
 
-    __device__ __forceinline__ KeyWalk(const Common& c, const Span& s, int h, int split) : a(c.a), sp(s), head(h) {
+    __device__ __forceinline__ KeyWalk(const Common& c, const Span& s, int h, int split, int splits) : a(c.a), sp(s), head(h) {
         wave_at = sp.at + 32 * wave_id();
         off = sp.other_len - sp.len;
         const int a0 = sp.at + off, a1 = sp.at + min(sp.rows, AT_ROWS) - 1 + off;
@@ -143,8 +152,8 @@ template <typename T, int DP> struct KeyWalk {
         if (a.causal) hi = min(hi, a1 + 1);
         if (c.window) { lo = max(lo, a0 - c.window + 1); hi = min(hi, a1 + c.window); }
         const int t0 = lo / BN, n = hi > lo ? (hi + BN - 1) / BN - t0 : 0;
-        first = t0 + static_cast<int>(static_cast<int64_t>(n) * split / c.splits);
-        last = t0 + static_cast<int>(static_cast<int64_t>(n) * (split + 1) / c.splits);
+        first = t0 + static_cast<int>(static_cast<int64_t>(n) * split / splits);
+        last = t0 + static_cast<int>(static_cast<int64_t>(n) * (split + 1) / splits);
         const int kv = head / c.gqa;
         kbase = static_cast<const T*>(a.k) + static_cast<int64_t>(sp.other) * a.ld_k + static_cast<int64_t>(kv) * a.hs_k;
         vbase = static_cast<const T*>(a.v) + static_cast<int64_t>(sp.other) * a.ld_v + static_cast<int64_t>(kv) * a.hs_v;
@@ -213,7 +222,7 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 ? 2 : 1) void attention_
     decode(c.unit0 + blockIdx.x, a.heads, c.splits, u, head, split);
     Span sp;
     if (!find_span<AT_ROWS, false>(a.offsets, a.key_offsets, static_cast<int>(a.sequences), static_cast<int>(a.queries), static_cast<int>(a.keys), a.causal, u, sp)) return;
-    const W w(c, sp, head, split);
+    const W w(c, sp, head, split, c.splits);
     const int lane = threadIdx.x & 63, place = w.wave_at + (lane & 31);
     const bool row_ok = place < sp.len;
     const int64_t row = sp.start - sp.at + place;
@@ -280,8 +289,9 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 ? 2 : 1) void attention_
             f32x16_t s[NB] = {};
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks)
+                if (!beyond<T>(16 * ks, a.width))
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb) mma(s[nb], row_frag<T, DP>(kt, lanes, 32 * nb, ks), qf[ks]);
+                    for (int nb = 0; nb < NB; ++nb) mma(s[nb], row_frag<T, DP>(kt, lanes, 32 * nb, ks), qf[ks]);
             if constexpr (BIAS) {
                 const int far = w.far(t);
 #pragma unroll
@@ -325,7 +335,8 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 ? 2 : 1) void attention_
                 for (int g = 0; g < 2; ++g) {
                     const Parts<T> p(s[nb], g);
 #pragma unroll
-                    for (int db = 0; db < DB; ++db) p.mma_to(o[db], col_frag<T, DP>(vt, lanes, 32 * nb + 16 * g, db));
+                    for (int db = 0; db < DB; ++db)
+                        if (!beyond<T>(32 * db, a.width)) p.mma_to(o[db], col_frag<T, DP>(vt, lanes, 32 * nb + 16 * g, db));
                 }
         }
         if constexpr (BIAS)
@@ -471,20 +482,22 @@ struct BiasSums {
     }
 };
 
-template <typename T, int DP, bool BIAS>
-__global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 && !(BIAS && DP == 128) ? 2 : 1) void attention_grad_q_kernel(BackwardArgs f) {
+// LDS of a workgroup: the tiles, then the bias's windows and rooms.
+template <typename T, int DP, bool BIAS> constexpr int grad_q_lds() {
+    return 4 * KeyWalk<T, DP>::TILE + (BIAS ? (2 * KeyWalk<T, DP>::WIN + AT_WAVES * BiasSums::ROOM) * 4 : 0);
+}
+
+template <typename T, int DP, bool BIAS> __device__ __forceinline__ void grad_q_block(const BackwardArgs& f, int64_t block, lds_byte_t* buf) {
     typedef KeyWalk<T, DP> W;
     constexpr int NB = W::NB, KS = W::KS, DB = DP / 32;
-    __shared__ __attribute__((aligned(512))) u32x4_t lds[4 * W::TILE / 16];
-    __shared__ float win[BIAS ? 2 * W::WIN + AT_WAVES * BiasSums::ROOM : 1];
     const Common& c = f.c;
     const muon_attention_args& a = c.a;
     int u, head, split;
-    decode(c.unit0 + blockIdx.x, a.heads, c.splits, u, head, split);
-    lds_float_t* wbuf = (lds_float_t*)win;
+    decode(block, a.heads, f.q_splits, u, head, split);
+    lds_float_t* wbuf = (lds_float_t*)(buf + 4 * W::TILE);
     BiasSums sums;
     if constexpr (BIAS) {
-        const int64_t slot = head * f.slots + (static_cast<int64_t>(u) * c.splits + split) * AT_WAVES + wave_id();
+        const int64_t slot = head * f.slots + (static_cast<int64_t>(u) * f.q_splits + split) * AT_WAVES + wave_id();
         sums.start(wbuf + 2 * W::WIN + BiasSums::ROOM * wave_id(), f.bias_part + slot * (2 * a.reach + 1), a.reach);
     }
     Span sp;
@@ -492,11 +505,10 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 && !(BIAS && DP == 128) 
         if constexpr (BIAS) sums.finish();
         return;
     }
-    const W w(c, sp, head, split);
+    const W w(c, sp, head, split, f.q_splits);
     const int lane = threadIdx.x & 63, place = w.wave_at + (lane & 31);
     const int64_t row = sp.start - sp.at + place;
     const Sight sight = w.sight(c, place);
-    lds_byte_t* buf = (lds_byte_t*)lds;
     Lanes<T, DP> lanes;
 
     // a query that sees no key takes no part, whatever its rows hold
@@ -526,7 +538,7 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 && !(BIAS && DP == 128) 
             }
         }
         delta = half_sum(delta);
-        if (place < sp.len && lane < 32 && split == 0) G(f.delta)[row * a.heads + head] = delta;
+        if (f.delta && place < sp.len && lane < 32 && split == 0) G(f.delta)[row * a.heads + head] = delta;
     }
     const float scale = size_of(a.scale), unit = BIAS ? LOG2E : scale * LOG2E;
     const float ref = row_ok ? (BIAS ? lse : lse * LOG2E) : 0.0f;
@@ -580,10 +592,11 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 && !(BIAS && DP == 128) 
                 lanes.fresh();
                 f32x16_t s = {}, dp = {};
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    mma(s, row_frag<T, DP>(kb, lanes, 0, ks), qf[ks]);
-                    mma(dp, row_frag<T, DP>(vb, lanes, 0, ks), df[ks]);
-                }
+                for (int ks = 0; ks < KS; ++ks)
+                    if (!beyond<T>(16 * ks, a.width)) {
+                        mma(s, row_frag<T, DP>(kb, lanes, 0, ks), qf[ks]);
+                        mma(dp, row_frag<T, DP>(vb, lanes, 0, ks), df[ks]);
+                    }
                 if constexpr (BIAS) w.add_bias(s, scale, wbuf + b * W::WIN, far == 0, far < 0 ? far_lo : far_hi, nb);
                 if (seen == SOME) {
                     hide(s, sight, t * W::BN + 32 * nb + 4 * (lane >> 5));
@@ -598,7 +611,8 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 && !(BIAS && DP == 128) 
                 for (int g = 0; g < 2; ++g) {
                     const Parts<T> p(s, g);
 #pragma unroll
-                    for (int db = 0; db < DB; ++db) p.mma_to(o[db], col_frag<T, DP>(kb, lanes, 16 * g, db));
+                    for (int db = 0; db < DB; ++db)
+                        if (!beyond<T>(32 * db, a.width)) p.mma_to(o[db], col_frag<T, DP>(kb, lanes, 16 * g, db));
                 }
                 if constexpr (BIAS) {
                     if (far == 0) {
@@ -618,57 +632,18 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 && !(BIAS && DP == 128) 
     }
     if constexpr (BIAS) sums.finish();
     if (place >= sp.len) return;
-    if (c.splits > 1) {
+    if (f.q_splits > 1) {
         const int64_t at = row * a.heads + head, n = a.queries * a.heads;
-        store_rows<float>(o, 1.0f, f.part + (split * n + at) * a.width, static_cast<float*>(nullptr), a.width, a.width % 4 == 0);
+        store_rows<float>(o, 1.0f, f.q_part + (split * n + at) * a.width, static_cast<float*>(nullptr), a.width, a.width % 4 == 0);
         return;
     }
     store_rows<T>(o, a.scale, static_cast<T*>(f.grad_q) + row * f.ld_dq + static_cast<int64_t>(head) * f.hs_dq, static_cast<T*>(nullptr), a.width, c.vec_out);
 }
 
-// Adds up the slots of one head for 64 distances, then those of a bucket.  The orders are fixed; sums in fp64: they have up to
-// millions of terms of either sign.
-__global__ __launch_bounds__(1024) void attention_bias_slots_kernel(const float* part, int64_t slots, int entries, double* sums) {
-    __shared__ double red[16][64];
-    const int lane = threadIdx.x & 63, wave = wave_id(), head = blockIdx.y;
-    const int d = min(static_cast<int>(blockIdx.x) * 64 + lane, entries - 1);
-    double v = 0.0;
-    const float* p = part + head * slots * entries + d;
-    int64_t s = wave;
-    for (; s + 7 * 16 < slots; s += 8 * 16) {
-        float x[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = G(p)[(s + 16 * k) * entries];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v += x[k];
-    }
-    for (; s < slots; s += 16) v += G(p)[s * entries];
-    red[wave][lane] = v;
-    __syncthreads();
-    if (wave == 0) {
-        for (int k = 1; k < 16; ++k) v += red[k][lane];
-        if (static_cast<int>(blockIdx.x) * 64 + lane < entries) G(sums)[static_cast<int64_t>(head) * entries + d] = v;
-    }
-}
-template <typename T> __global__ __launch_bounds__(64) void attention_bias_kernel(const int32_t* map, const double* sums, int entries, int heads, void* grad) {
-    const int bucket = blockIdx.x, head = blockIdx.y;
-    double v = 0.0;
-    for (int d = threadIdx.x; d < entries; d += 64)
-        if (G(map)[d] == bucket) v += G(sums)[static_cast<int64_t>(head) * entries + d];
-    v = wave_sum(v);
-    if (threadIdx.x == 0) st_el<T>(grad, static_cast<size_t>(bucket) * heads + head, static_cast<float>(v));
-}
-
-// out[row][head][d] = scale * sum over the splits of part[split][row][head][d], for one matrix.
-template <typename T> __global__ __launch_bounds__(256) void attention_sum_kernel(const float* part, int64_t split_pitch, int splits, int64_t rows, int heads,
-                                                                                 int width, float scale, void* out, int64_t ld, int64_t hs, int64_t base) {
-    const int64_t i = base + static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (i >= rows * heads * width) return;
-    float v = 0.0f;
-#pragma unroll 8
-    for (int s = 0; s < splits; ++s) v += G(part)[s * split_pitch + i];
-    const int64_t at = i / width, row = at / heads;
-    st_el<T>(out, row * ld + (at - row * heads) * hs + (i - at * width), v * scale);
+template <typename T, int DP, bool BIAS>
+__global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 && !(BIAS && DP == 128) ? 2 : 1) void attention_grad_q_kernel(BackwardArgs f) {
+    __shared__ __attribute__((aligned(512))) char lds[grad_q_lds<T, DP, BIAS>()];
+    grad_q_block<T, DP, BIAS>(f, f.c.unit0 + blockIdx.x, (lds_byte_t*)lds);
 }
 
 // ---- grad_k and grad_v ------------------------------------------------------------
@@ -681,29 +656,32 @@ template <typename T, int DP> struct KvShape {
     static constexpr int WAVES = sizeof(T) == 2 ? 2 : 1;      // a SIMD
 };
 
-template <typename T, int DP, bool BIAS>
-__global__ __launch_bounds__(AT_THREADS, (KvShape<T, DP>::WAVES)) void attention_grad_kv_kernel(BackwardArgs f) {
+// LDS of a workgroup: the tiles, v, [buffer][lse or delta][query], the bias's windows.
+template <typename T, int DP, bool BIAS> constexpr int grad_kv_lds() {
+    return (4 * KV_ROWS + (KvShape<T, DP>::V_LDS ? AT_ROWS : 0)) * Row<T, DP>::BYTES + 2 * 2 * KV_ROWS * 4 + (BIAS ? 2 * (AT_ROWS + KV_ROWS) * 4 : 0);
+}
+
+// SELF: delta is formed here, tile by tile, for a launch that does not wait for grad_q's: a wave takes 8 of a tile's 32 queries,
+// 8 lanes a query.
+template <typename T, int DP, bool BIAS, bool SELF>
+__device__ __forceinline__ void grad_kv_block(const BackwardArgs& f, int64_t block, lds_byte_t* buf) {
     constexpr int BQ = KV_ROWS;
     constexpr int KS = DP / 16, DB = DP / 32, TILE = BQ * Row<T, DP>::BYTES, WIN = AT_ROWS + BQ;
     constexpr bool V_LDS = KvShape<T, DP>::V_LDS;
     constexpr int VTILE = V_LDS ? AT_ROWS * Row<T, DP>::BYTES : 0;
-    __shared__ __attribute__((aligned(512))) u32x4_t lds[(4 * TILE + VTILE) / 16];
-    __shared__ f32x4_t stat[2 * 2 * BQ / 4];           // [buffer][lse or delta][row]
-    __shared__ float win[BIAS ? 2 * WIN : 1];
     const Common& c = f.c;
     const muon_attention_args& a = c.a;
     int u, kv, split;
-    decode(c.unit0 + blockIdx.x, a.kv_heads, c.splits, u, kv, split);
+    decode(block, a.kv_heads, f.kv_splits, u, kv, split);
     Span sp;
     if (!find_span<AT_ROWS, true>(a.key_offsets, a.offsets, static_cast<int>(a.sequences), static_cast<int>(a.keys), static_cast<int>(a.queries), a.causal, u, sp)) return;
     const int lane = threadIdx.x & 63, wave = wave_id(), h = lane >> 5;
     const int wave_at = sp.at + 32 * wave, place = wave_at + (lane & 31), nq = sp.other_len, off = sp.len - nq;
     const int64_t row = sp.start - sp.at + place;
     const bool in = place < sp.len, key_ok = in && (!a.key_mask || G(a.key_mask)[in ? row : 0] != 0);
-    lds_byte_t* buf = (lds_byte_t*)lds;
     Lanes<T, DP> lanes;
-    lds_float_t* stats = (lds_float_t*)stat;
-    lds_float_t* wbuf = (lds_float_t*)win;
+    lds_float_t* stats = (lds_float_t*)(buf + 4 * TILE + VTILE);
+    lds_float_t* wbuf = stats + 2 * 2 * BQ;
 
     // queries that see this lane's key: places lo .. lo + span - 1
     Sight sight;
@@ -744,7 +722,7 @@ __global__ __launch_bounds__(AT_THREADS, (KvShape<T, DP>::WAVES)) void attention
     }
     const int first = lo / BQ, n = hi > lo ? (hi + BQ - 1) / BQ - first : 0;
     const int64_t steps = static_cast<int64_t>(n) * c.gqa;
-    const int64_t it0 = steps * split / c.splits, it1 = steps * (split + 1) / c.splits;
+    const int64_t it0 = steps * split / f.kv_splits, it1 = steps * (split + 1) / f.kv_splits;
     struct At {
         int head, t;
         int64_t left;             // steps from here on
@@ -763,7 +741,8 @@ __global__ __launch_bounds__(AT_THREADS, (KvShape<T, DP>::WAVES)) void attention
         now.head += g;
         now.t += static_cast<int>(it0 - static_cast<int64_t>(g) * n);
     }
-    // lse of this lane's row of a step (and its delta): -infinity where there is nothing to see
+    Frag<T> own_d[SELF ? DP / 64 : 1], own_o[SELF ? DP / 64 : 1], own_l[SELF ? DP / 64 : 1];
+    // lse of this lane's row of a step (and its delta, or what that is formed of): -infinity where there is nothing to see
     auto ask = [&](const At& w, float& l, float& d) {
         l = NEG_INF;
         d = 0.0f;
@@ -772,7 +751,22 @@ __global__ __launch_bounds__(AT_THREADS, (KvShape<T, DP>::WAVES)) void attention
         if (lane < BQ && i < nq) {
             const int64_t at = static_cast<int64_t>(sp.other + i) * a.heads + w.head;
             l = G(a.lse)[at];
-            d = G(f.delta)[at];
+            if constexpr (!SELF) d = G(f.delta)[at];
+        }
+        if constexpr (SELF) {
+            const int own = 8 * wave + (lane >> 3);
+            const int64_t r = static_cast<int64_t>(sp.other) + w.t * BQ + own, at = r * a.heads + w.head;
+            const bool ok = w.t * BQ + own < nq && G(a.lse)[w.t * BQ + own < nq ? at : 0] != NEG_INF;
+            const T* dr = static_cast<const T*>(f.grad_out) + r * f.ld_do + static_cast<int64_t>(w.head) * f.hs_do;
+            const T* outr = static_cast<const T*>(a.out) + r * a.ld_out + static_cast<int64_t>(w.head) * a.hs_out;
+            const T* low = static_cast<const T*>(a.out_low) + r * a.ld_out_low + static_cast<int64_t>(w.head) * a.hs_out_low;
+#pragma unroll
+            for (int k = 0; k < DP / 64; ++k) {
+                const int e0 = 64 * k + 8 * (lane & 7);
+                own_d[k] = global_frag<T>(dr, e0, a.width, ok, c.vec_in);
+                own_o[k] = global_frag<T>(outr, e0, a.width, ok, c.vec_in);
+                if (a.out_low) own_l[k] = global_frag<T>(low, e0, a.width, ok, c.vec_in);
+            }
         }
     };
     auto load = [&](const At& w, int b, float l, float d) {
@@ -782,7 +776,20 @@ __global__ __launch_bounds__(AT_THREADS, (KvShape<T, DP>::WAVES)) void attention
         load_tile<T, DP, BQ, AT_THREADS>(buf + 2 * TILE * b + TILE, static_cast<const T*>(f.grad_out) + i0 * f.ld_do + static_cast<int64_t>(w.head) * f.hs_do, f.ld_do, a.width, live, c.vec_in);
         if (wave == 0 && lane < BQ) {
             stats[2 * BQ * b + lane] = l == NEG_INF ? 0.0f : BIAS ? l : l * LOG2E;
-            stats[2 * BQ * b + BQ + lane] = l == NEG_INF ? 0.0f : d;
+            if constexpr (!SELF) stats[2 * BQ * b + BQ + lane] = l == NEG_INF ? 0.0f : d;
+        }
+        if constexpr (SELF) {
+            float v = 0.0f;
+#pragma unroll
+            for (int k = 0; k < DP / 64; ++k)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    v = fmaf(frag_get(own_d[k], e), frag_get(own_o[k], e), v);
+                    if (a.out_low) v = fmaf(frag_get(own_d[k], e), frag_get(own_l[k], e), v);
+                }
+#pragma unroll
+            for (int k = 1; k < 8; k <<= 1) v += __shfl_xor(v, k);
+            if ((lane & 7) == 0) stats[2 * BQ * b + BQ + 8 * wave + (lane >> 3)] = v;
         }
     };
     // distance of the window's first entry for tile t: that of this workgroup's first key and the tile's last query
@@ -825,6 +832,7 @@ __global__ __launch_bounds__(AT_THREADS, (KvShape<T, DP>::WAVES)) void attention
             f32x16_t s = {}, dp = {};
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
+                if (beyond<T>(16 * ks, a.width)) continue;
                 mma(s, row_frag<T, DP>(qt, lanes, 0, ks), kf[ks]);
                 if constexpr (V_LDS) mma(dp, row_frag<T, DP>(dt, lanes, 0, ks), row_frag<T, DP>(vt, lanes, 0, ks));
                 else mma(dp, row_frag<T, DP>(dt, lanes, 0, ks), vf[ks]);
@@ -852,6 +860,7 @@ __global__ __launch_bounds__(AT_THREADS, (KvShape<T, DP>::WAVES)) void attention
                 const Parts<T> p(s, g), d(dp, g);
 #pragma unroll
                 for (int db = 0; db < DB; ++db) {
+                    if (beyond<T>(32 * db, a.width)) continue;
                     p.mma_to(dv[db], col_frag<T, DP>(dt, lanes, 16 * g, db));
                     d.mma_to(dk[db], col_frag<T, DP>(qt, lanes, 16 * g, db));
                 }
@@ -861,9 +870,9 @@ __global__ __launch_bounds__(AT_THREADS, (KvShape<T, DP>::WAVES)) void attention
             if (next.left > 0) bw.put(wbuf + (b ^ 1) * WIN);
     }
     if (!in) return;
-    if (c.splits > 1) {
+    if (f.kv_splits > 1) {
         const int64_t at = row * a.kv_heads + kv, total = a.keys * a.kv_heads;
-        float* p = f.part + (2 * split * total + at) * a.width;
+        float* p = f.kv_part + (2 * split * total + at) * a.width;
         store_rows<float>(dk, 1.0f, p, static_cast<float*>(nullptr), a.width, a.width % 4 == 0);
         store_rows<float>(dv, 1.0f, p + total * a.width, static_cast<float*>(nullptr), a.width, a.width % 4 == 0);
         return;
@@ -872,31 +881,161 @@ __global__ __launch_bounds__(AT_THREADS, (KvShape<T, DP>::WAVES)) void attention
     store_rows<T>(dv, 1.0f, static_cast<T*>(f.grad_v) + row * f.ld_dv + static_cast<int64_t>(kv) * f.hs_dv, static_cast<T*>(nullptr), a.width, c.vec_out);
 }
 
+template <typename T, int DP, bool BIAS>
+__global__ __launch_bounds__(AT_THREADS, (KvShape<T, DP>::WAVES)) void attention_grad_kv_kernel(BackwardArgs f) {
+    __shared__ __attribute__((aligned(512))) char lds[grad_kv_lds<T, DP, BIAS>()];
+    grad_kv_block<T, DP, BIAS, false>(f, f.c.unit0 + blockIdx.x, (lds_byte_t*)lds);
+}
+
+// All of a small call at once.
+template <typename T, int DP, bool BIAS> __global__ __launch_bounds__(AT_THREADS, 1) void attention_grad_all_kernel(BackwardArgs f) {
+    constexpr int Q = grad_q_lds<T, DP, BIAS>(), KV = grad_kv_lds<T, DP, BIAS>();
+    __shared__ __attribute__((aligned(512))) char lds[Q > KV ? Q : KV];
+    if (blockIdx.x < f.q_blocks) grad_q_block<T, DP, BIAS>(f, blockIdx.x, (lds_byte_t*)lds);
+    else grad_kv_block<T, DP, BIAS, true>(f, blockIdx.x - f.q_blocks, (lds_byte_t*)lds);
+}
+
+// ---- what splits and slots add up to ----------------------------------------------------
+
+// One matrix's sum over the splits: out[row][head][d] = scale * sum of part[split][row][head][d].
+struct SumJob {
+    const float* part;
+    void* out;
+    int64_t pitch, count, ld, hs;   // count: rows x heads x width, 0: nothing to do
+    int splits, heads;
+    float scale;
+};
+struct FinishArgs {
+    SumJob job[3];
+    int64_t first[4];               // blocks of the jobs: first[k] .. first[k + 1) - 1
+    int64_t block0;
+    const float* bias_part;
+    const double* bias_sums;        // of the distances, or NULL: each bucket adds up its distances' slots
+    const int32_t* bucket_map;
+    void* grad_bias;
+    int64_t slots;
+    int entries, buckets, bias_heads, width;
+};
+
+// Sum over the slots for 64 distances of one head.  The orders are fixed; sums in fp64: they have up to millions of terms of either sign.
+__global__ __launch_bounds__(1024) void attention_bias_slots_kernel(const float* part, int64_t slots, int entries, double* sums) {
+    __shared__ double red[16][64];
+    const int lane = threadIdx.x & 63, wave = wave_id(), head = blockIdx.y;
+    const int d = min(static_cast<int>(blockIdx.x) * 64 + lane, entries - 1);
+    double v = 0.0;
+    const float* p = part + head * slots * entries + d;
+    int64_t s = wave;
+    for (; s + 7 * 16 < slots; s += 8 * 16) {
+        float x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = G(p)[(s + 16 * k) * entries];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v += x[k];
+    }
+    for (; s < slots; s += 16) v += G(p)[s * entries];
+    red[wave][lane] = v;
+    __syncthreads();
+    if (wave == 0) {
+        for (int k = 1; k < 16; ++k) v += red[k][lane];
+        if (static_cast<int>(blockIdx.x) * 64 + lane < entries) G(sums)[static_cast<int64_t>(head) * entries + d] = v;
+    }
+}
+
+// The sums that are left, in one launch: a workgroup for each bucket and head, then 256 values of a matrix each.
+template <typename T> __global__ __launch_bounds__(256) void attention_finish_kernel(FinishArgs f) {
+    __shared__ double red[4];
+    __shared__ int mine[2 * MUON_MAX_REACH + 1];
+    __shared__ int count;
+    const int64_t block = f.block0 + blockIdx.x;
+    if (block < f.first[0]) {
+        const int bucket = static_cast<int>(block / f.bias_heads), head = static_cast<int>(block - static_cast<int64_t>(bucket) * f.bias_heads);
+        const int lane = threadIdx.x & 63, wave = wave_id();
+        double v = 0.0;
+        if (f.bias_sums) {
+            for (int d = threadIdx.x; d < f.entries; d += 256)
+                if (G(f.bucket_map)[d] == bucket) v += G(f.bias_sums)[static_cast<int64_t>(head) * f.entries + d];
+        } else {
+            // the bucket's distances, in order, found by the first wave
+            if (wave == 0) {
+                int n = 0;
+                for (int d0 = 0; d0 < f.entries; d0 += 64) {
+                    const bool in = d0 + lane < f.entries && G(f.bucket_map)[min(d0 + lane, f.entries - 1)] == bucket;
+                    const uint64_t set = __ballot(in);
+                    if (in) mine[n + __popcll(set & ((1ull << lane) - 1))] = d0 + lane;
+                    n += __popcll(set);
+                }
+                if (lane == 0) count = n;
+            }
+            __syncthreads();
+            // a thread a slot and eighth of the distances
+            const int n = count;
+            for (int64_t slot = threadIdx.x >> 3; slot < f.slots; slot += 32) {
+                const float* p = f.bias_part + (head * f.slots + slot) * f.entries;
+#pragma unroll 4
+                for (int i = threadIdx.x & 7; i < n; i += 8) v += G(p)[mine[i]];
+            }
+        }
+        double s[1] = {v};
+        block_sums(s, red);
+        if (threadIdx.x == 0) st_el<T>(f.grad_bias, static_cast<size_t>(bucket) * f.bias_heads + head, static_cast<float>(s[0]));
+        return;
+    }
+    const int k = block >= f.first[2] ? 2 : block >= f.first[1] ? 1 : 0;
+    const SumJob& j = f.job[k];
+    const int64_t i = (block - f.first[k]) * 256 + threadIdx.x;
+    if (i >= j.count) return;
+    float v = 0.0f;
+    int s = 0;
+    for (; s + 7 < j.splits; s += 8) {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = G(j.part)[(s + e) * j.pitch + i];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v += x[e];
+    }
+    for (; s < j.splits; ++s) v += G(j.part)[s * j.pitch + i];
+    const int64_t at = i / f.width, row = at / j.heads;
+    st_el<T>(j.out, row * j.ld + (at - row * j.heads) * j.hs + (i - at * f.width), v * j.scale);
+}
+
 // ---- host -------------------------------------------------------------------------
 
-// Few units of an axis leave CUs idle: their walks are split until about two workgroups a CU have work, while a part keeps two
-// tiles on average.  Walks so long that a part keeps 64 tiles are split until there are eight workgroups a CU, so that the
-// longest under a causal mask do not end alone (16384 tokens, 4 key heads, grad_k and grad_v: 5.8 ms in one part).
-int plan_splits(int64_t rows, int64_t sequences, int heads, int64_t walk, int tile) {
-    const int64_t units = (rows / AT_ROWS + sequences) * heads;
-    const int64_t tiles = std::max<int64_t>(1, walk / sequences / tile);
-    const int64_t n = std::max<int64_t>(1, units);
-    const int64_t want = std::max(std::min(512 / n, tiles / 2), std::min(2048 / n, tiles / 64));
+// Few units of an axis leave CUs idle: their walks are split until the workgroups fill the chip once (`target`: as many as it holds at
+// once; a second round for a few of them costs as much as a full one), while a part keeps two tiles on average.  Walks so long that
+// a part keeps 64 tiles are split until there are eight workgroups a CU, so that the longest under a causal mask do not end alone
+// (16384 tokens, 4 key heads, grad_k and grad_v: 5.8 ms in one part).
+int64_t axis_units(int64_t rows, int64_t sequences, int heads) { return std::max<int64_t>(1, (rows / AT_ROWS + sequences) * heads); }
+int plan_splits(int64_t rows, int64_t sequences, int heads, int64_t walk, int tile, int64_t target) {
+    const int64_t n = axis_units(rows, sequences, heads), tiles = std::max<int64_t>(1, walk / sequences / tile);
+    const int64_t want = std::max(std::min(target / n, tiles / 2), std::min(2048 / n, tiles / 64));
     return static_cast<int>(std::min<int64_t>(std::max<int64_t>(1, want), AT_MAX_SPLITS));
 }
 int tile_rows(int dtype) { return dtype == MUON_BF16 ? walk_rows<uint16_t>() : walk_rows<float>(); }
+// Workgroups at once: two a CU, but one where fp32 takes all registers.
+int64_t at_once(int dtype, int width) { return dtype == MUON_F32 && width > 64 ? AT_CUS : 2 * AT_CUS; }
 
-int forward_splits(const muon_attention_args& a) { return plan_splits(a.queries, a.sequences, a.heads, a.keys, tile_rows(a.dtype)); }
+int forward_splits(const muon_attention_args& a) {
+    return plan_splits(a.queries, a.sequences, a.heads, a.keys, tile_rows(a.dtype), at_once(a.dtype, a.width));
+}
 struct BackwardPlan {
     int q_splits, kv_splits;
+    int64_t q_blocks, kv_blocks;
+    bool all;                                       // one launch for the three gradients
+    bool two_step;                                  // the bias's slots are added up by distance first
     int64_t slots;                                  // of the bias's partial sums, per head
     size_t delta, q_part, kv_part, bias_part, bias_sums, bytes;   // offsets
 };
 BackwardPlan plan_backward(const muon_attention_backward_args& a) {
     BackwardPlan p{};
-    const int tr = tile_rows(a.dtype);
-    p.q_splits = plan_splits(a.queries, a.sequences, a.heads, a.keys, tr);
-    p.kv_splits = plan_splits(a.keys, a.sequences, a.kv_heads, a.queries * (a.heads / a.kv_heads), KV_ROWS);
+    const int64_t qu = axis_units(a.queries, a.sequences, a.heads), ku = axis_units(a.keys, a.sequences, a.kv_heads);
+    // As long as both find room on the chip at once, one launch takes as long as the longer of two: 8 heads of 77 tokens 19 us, 16 and
+    // 12 in two.  Its room goes to them by their products, 3 and 4.
+    p.all = a.queries && a.keys && qu + ku <= AT_CUS;
+    const int64_t kv_walk = a.queries * (a.heads / a.kv_heads);
+    p.q_splits = plan_splits(a.queries, a.sequences, a.heads, a.keys, tile_rows(a.dtype), p.all ? AT_CUS * 3 / 7 : at_once(a.dtype, a.width));
+    p.kv_splits = plan_splits(a.keys, a.sequences, a.kv_heads, kv_walk, KV_ROWS, p.all ? AT_CUS * 4 / 7 : at_once(a.dtype, 128));
+    p.q_blocks = a.queries ? span_units(a.queries, a.sequences, AT_ROWS) * a.heads * p.q_splits : 0;
+    p.kv_blocks = a.keys ? span_units(a.keys, a.sequences, AT_ROWS) * a.kv_heads * p.kv_splits : 0;
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t here = at;
@@ -904,15 +1043,15 @@ BackwardPlan plan_backward(const muon_attention_backward_args& a) {
         return here;
     };
     const size_t q = static_cast<size_t>(a.queries) * a.heads, k = static_cast<size_t>(a.keys) * a.kv_heads;
-    p.delta = take(q * 4);
-    // one after the other: the partial sums of grad_q are added up before those of grad_k and grad_v are written
-    p.q_part = p.kv_part = at;
-    take(std::max(p.q_splits > 1 ? p.q_splits * q * a.width * 4 : 0, p.kv_splits > 1 ? 2 * p.kv_splits * k * a.width * 4 : 0));
+    p.delta = take(p.all ? 0 : q * 4);
+    p.q_part = take(p.q_splits > 1 ? p.q_splits * q * a.width * 4 : 0);
+    p.kv_part = take(p.kv_splits > 1 ? 2 * p.kv_splits * k * a.width * 4 : 0);
     if (a.bias) {
         const size_t entries = 2 * static_cast<size_t>(a.reach) + 1;
-        p.slots = span_units(a.queries, a.sequences, AT_ROWS) * p.q_splits * AT_WAVES;
+        p.slots = a.queries ? span_units(a.queries, a.sequences, AT_ROWS) * p.q_splits * AT_WAVES : 0;
+        p.two_step = p.slots * entries / a.buckets > AT_BUCKET_READS;
         p.bias_part = take(p.slots * a.heads * entries * 4);
-        p.bias_sums = take(a.heads * entries * 8);
+        p.bias_sums = take(p.two_step ? a.heads * entries * 8 : 0);
     }
     p.bytes = at;
     return p;
@@ -956,53 +1095,58 @@ template <typename T, int DP, bool BIAS> hipError_t run_forward(ForwardArgs f, h
     });
 }
 
-template <typename T> hipError_t run_sum(const float* part, int64_t pitch, int splits, int64_t rows, int heads, int width, float scale, void* out, int64_t ld,
-                                         int64_t hs, hipStream_t s) {
-    return in_launches((rows * heads * width + 255) / 256, [&](int64_t base, unsigned n) {
-        hipLaunchKernelGGL((attention_sum_kernel<T>), dim3(n), dim3(256), 0, s, part, pitch, splits, rows, heads, width, scale, out, ld, hs, base * 256);
-        return hipGetLastError();
-    });
-}
-
 template <typename T, int DP, bool BIAS>
 hipError_t run_backward(BackwardArgs f, const BackwardPlan& p, const muon_attention_backward_args& b, char* ws, hipStream_t s) {
     const muon_attention_args& a = f.c.a;
-    hipError_t e;
-    if (a.queries > 0) {
-        f.c.splits = p.q_splits;
-        f.part = reinterpret_cast<float*>(ws + p.q_part);
-        e = in_launches(span_units(a.queries, a.sequences, AT_ROWS) * a.heads * p.q_splits, [&](int64_t base, unsigned n) {
+    hipError_t e = hipSuccess;
+    if (p.all) {
+        hipLaunchKernelGGL((attention_grad_all_kernel<T, DP, BIAS>), dim3(static_cast<unsigned>(p.q_blocks + p.kv_blocks)), dim3(AT_THREADS), 0, s, f);
+        e = hipGetLastError();
+    } else {
+        e = in_launches(p.q_blocks, [&](int64_t base, unsigned n) {
             f.c.unit0 = base;
             hipLaunchKernelGGL((attention_grad_q_kernel<T, DP, BIAS>), dim3(n), dim3(AT_THREADS), 0, s, f);
             return hipGetLastError();
         });
         if (e != hipSuccess) return e;
-        if (p.q_splits > 1) {
-            e = run_sum<T>(f.part, a.queries * a.heads * a.width, p.q_splits, a.queries, a.heads, a.width, a.scale, f.grad_q, f.ld_dq, f.hs_dq, s);
+        e = in_launches(p.kv_blocks, [&](int64_t base, unsigned n) {
+            f.c.unit0 = base;
+            hipLaunchKernelGGL((attention_grad_kv_kernel<T, DP, BIAS>), dim3(n), dim3(AT_THREADS), 0, s, f);
+            return hipGetLastError();
+        });
+    }
+    if (e != hipSuccess) return e;
+    FinishArgs g{};
+    g.width = a.width;
+    if constexpr (BIAS) {
+        g.bias_part = f.bias_part;
+        g.bucket_map = a.bucket_map;
+        g.grad_bias = b.grad_bias;
+        g.slots = p.slots;
+        g.entries = 2 * a.reach + 1;
+        g.buckets = a.buckets;
+        g.bias_heads = a.heads;
+        g.first[0] = static_cast<int64_t>(a.buckets) * a.heads;
+        if (p.two_step) {
+            double* sums = reinterpret_cast<double*>(ws + p.bias_sums);
+            hipLaunchKernelGGL(attention_bias_slots_kernel, dim3((g.entries + 63) / 64, a.heads), dim3(1024), 0, s, f.bias_part, p.slots, g.entries, sums);
+            e = hipGetLastError();
             if (e != hipSuccess) return e;
+            g.bias_sums = sums;
         }
     }
-    if constexpr (BIAS) {
-        const int entries = 2 * a.reach + 1;
-        double* sums = reinterpret_cast<double*>(ws + p.bias_sums);
-        hipLaunchKernelGGL(attention_bias_slots_kernel, dim3((entries + 63) / 64, a.heads), dim3(1024), 0, s, f.bias_part, a.queries > 0 ? p.slots : 0, entries, sums);
-        hipLaunchKernelGGL((attention_bias_kernel<T>), dim3(a.buckets, a.heads), dim3(64), 0, s, a.bucket_map, sums, entries, a.heads, b.grad_bias);
-        e = hipGetLastError();
-        if (e != hipSuccess) return e;
+    const int64_t q = a.queries * a.heads * a.width, k = a.keys * a.kv_heads * a.width;
+    if (p.q_splits > 1) g.job[0] = {f.q_part, f.grad_q, q, q, f.ld_dq, f.hs_dq, p.q_splits, a.heads, a.scale};
+    if (p.kv_splits > 1) {
+        g.job[1] = {f.kv_part, f.grad_k, 2 * k, k, f.ld_dk, f.hs_dk, p.kv_splits, a.kv_heads, a.scale};
+        g.job[2] = {f.kv_part + k, f.grad_v, 2 * k, k, f.ld_dv, f.hs_dv, p.kv_splits, a.kv_heads, 1.0f};
     }
-    if (a.keys == 0) return hipSuccess;
-    f.c.splits = p.kv_splits;
-    f.part = reinterpret_cast<float*>(ws + p.kv_part);
-    e = in_launches(span_units(a.keys, a.sequences, AT_ROWS) * a.kv_heads * p.kv_splits, [&](int64_t base, unsigned n) {
-        f.c.unit0 = base;
-        hipLaunchKernelGGL((attention_grad_kv_kernel<T, DP, BIAS>), dim3(n), dim3(AT_THREADS), 0, s, f);
+    for (int i = 0; i < 3; ++i) g.first[i + 1] = g.first[i] + (g.job[i].count + 255) / 256;
+    return in_launches(g.first[3], [&](int64_t base, unsigned n) {
+        g.block0 = base;
+        hipLaunchKernelGGL((attention_finish_kernel<T>), dim3(n), dim3(256), 0, s, g);
         return hipGetLastError();
     });
-    if (e != hipSuccess || p.kv_splits == 1) return e;
-    const int64_t total = a.keys * a.kv_heads * a.width;
-    e = run_sum<T>(f.part, 2 * total, p.kv_splits, a.keys, a.kv_heads, a.width, a.scale, f.grad_k, f.ld_dk, f.hs_dk, s);
-    if (e != hipSuccess) return e;
-    return run_sum<T>(f.part + total, 2 * total, p.kv_splits, a.keys, a.kv_heads, a.width, 1.0f, f.grad_v, f.ld_dv, f.hs_dv, s);
 }
 
 // Calls f with the tile width and whether there is a bias, as types.
@@ -1065,9 +1209,14 @@ hipError_t launch_attention_backward(const muon_attention_backward_args& b, void
     f.ld_dk = b.ld_grad_k; f.hs_dk = b.hs_grad_k;
     f.ld_dv = b.ld_grad_v; f.hs_dv = b.hs_grad_v;
     char* ws = static_cast<char*>(workspace);
-    f.delta = reinterpret_cast<float*>(ws + p.delta);
+    f.delta = p.all ? nullptr : reinterpret_cast<float*>(ws + p.delta);
     f.bias_part = reinterpret_cast<float*>(ws + p.bias_part);
     f.slots = p.slots;
+    f.q_splits = p.q_splits;
+    f.kv_splits = p.kv_splits;
+    f.q_part = reinterpret_cast<float*>(ws + p.q_part);
+    f.kv_part = reinterpret_cast<float*>(ws + p.kv_part);
+    f.q_blocks = p.q_blocks;
     return dispatch(a.dtype, a.width, a.bias != nullptr, [&](auto t, auto dp, auto bias) {
         return run_backward<decltype(t), decltype(dp)::value, decltype(bias)::value>(f, p, b, ws, s);
     });
