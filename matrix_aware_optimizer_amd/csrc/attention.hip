@@ -23,6 +23,7 @@ using namespace at;
 
 constexpr int AT_THREADS = 256, AT_WAVES = 4, AT_ROWS = 128;   // rows (queries or keys) a workgroup
 constexpr int AT_MAX_SPLITS = 64;
+constexpr int AT_FINISH = 1024;                                 // threads of the sums' workgroups
 constexpr int64_t AT_CUS = 256;
 constexpr int64_t AT_BUCKET_READS = 65536;                      // values of the bias's slots that a workgroup adds up for a bucket
 
@@ -742,6 +743,7 @@ __device__ __forceinline__ void grad_kv_block(const BackwardArgs& f, int64_t blo
         now.t += static_cast<int>(it0 - static_cast<int64_t>(g) * n);
     }
     Frag<T> own_d[SELF ? DP / 64 : 1], own_o[SELF ? DP / 64 : 1], own_l[SELF ? DP / 64 : 1];
+    float own_lse = NEG_INF;
     // lse of this lane's row of a step (and its delta, or what that is formed of): -infinity where there is nothing to see
     auto ask = [&](const At& w, float& l, float& d) {
         l = NEG_INF;
@@ -756,7 +758,9 @@ __device__ __forceinline__ void grad_kv_block(const BackwardArgs& f, int64_t blo
         if constexpr (SELF) {
             const int own = 8 * wave + (lane >> 3);
             const int64_t r = static_cast<int64_t>(sp.other) + w.t * BQ + own, at = r * a.heads + w.head;
-            const bool ok = w.t * BQ + own < nq && G(a.lse)[w.t * BQ + own < nq ? at : 0] != NEG_INF;
+            const bool ok = w.t * BQ + own < nq;
+            own_lse = G(a.lse)[ok ? at : 0];           // looked at where delta is formed: nothing waits for it here
+            if (!ok) own_lse = NEG_INF;
             const T* dr = static_cast<const T*>(f.grad_out) + r * f.ld_do + static_cast<int64_t>(w.head) * f.hs_do;
             const T* outr = static_cast<const T*>(a.out) + r * a.ld_out + static_cast<int64_t>(w.head) * a.hs_out;
             const T* low = static_cast<const T*>(a.out_low) + r * a.ld_out_low + static_cast<int64_t>(w.head) * a.hs_out_low;
@@ -789,7 +793,7 @@ __device__ __forceinline__ void grad_kv_block(const BackwardArgs& f, int64_t blo
                 }
 #pragma unroll
             for (int k = 1; k < 8; k <<= 1) v += __shfl_xor(v, k);
-            if ((lane & 7) == 0) stats[2 * BQ * b + BQ + 8 * wave + (lane >> 3)] = v;
+            if ((lane & 7) == 0) stats[2 * BQ * b + BQ + 8 * wave + (lane >> 3)] = own_lse == NEG_INF ? 0.0f : v;
         }
     };
     // distance of the window's first entry for tile t: that of this workgroup's first key and the tile's last query
@@ -941,9 +945,9 @@ __global__ __launch_bounds__(1024) void attention_bias_slots_kernel(const float*
     }
 }
 
-// The sums that are left, in one launch: a workgroup for each bucket and head, then 256 values of a matrix each.
-template <typename T> __global__ __launch_bounds__(256) void attention_finish_kernel(FinishArgs f) {
-    __shared__ double red[4];
+// The sums that are left, in one launch: a workgroup for each bucket and head, then AT_FINISH values of a matrix each.
+template <typename T> __global__ __launch_bounds__(AT_FINISH) void attention_finish_kernel(FinishArgs f) {
+    __shared__ double red[AT_FINISH / 64];
     __shared__ int mine[2 * MUON_MAX_REACH + 1];
     __shared__ int count;
     const int64_t block = f.block0 + blockIdx.x;
@@ -952,27 +956,33 @@ template <typename T> __global__ __launch_bounds__(256) void attention_finish_ke
         const int lane = threadIdx.x & 63, wave = wave_id();
         double v = 0.0;
         if (f.bias_sums) {
-            for (int d = threadIdx.x; d < f.entries; d += 256)
+            for (int d = threadIdx.x; d < f.entries; d += AT_FINISH)
                 if (G(f.bucket_map)[d] == bucket) v += G(f.bias_sums)[static_cast<int64_t>(head) * f.entries + d];
         } else {
             // the bucket's distances, in order, found by the first wave
             if (wave == 0) {
                 int n = 0;
-                for (int d0 = 0; d0 < f.entries; d0 += 64) {
-                    const bool in = d0 + lane < f.entries && G(f.bucket_map)[min(d0 + lane, f.entries - 1)] == bucket;
-                    const uint64_t set = __ballot(in);
-                    if (in) mine[n + __popcll(set & ((1ull << lane) - 1))] = d0 + lane;
-                    n += __popcll(set);
+                for (int d0 = 0; d0 < f.entries; d0 += 16 * 64) {
+                    int of[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) of[k] = G(f.bucket_map)[min(d0 + 64 * k + lane, f.entries - 1)];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const bool in = d0 + 64 * k + lane < f.entries && of[k] == bucket;
+                        const uint64_t set = __ballot(in);
+                        if (in) mine[n + __popcll(set & ((1ull << lane) - 1))] = d0 + 64 * k + lane;
+                        n += __popcll(set);
+                    }
                 }
                 if (lane == 0) count = n;
             }
             __syncthreads();
-            // a thread a slot and eighth of the distances
+            // 32 slots at once, 32 lanes a slot
             const int n = count;
-            for (int64_t slot = threadIdx.x >> 3; slot < f.slots; slot += 32) {
+            for (int64_t slot = threadIdx.x >> 5; slot < f.slots; slot += AT_FINISH / 32) {
                 const float* p = f.bias_part + (head * f.slots + slot) * f.entries;
 #pragma unroll 4
-                for (int i = threadIdx.x & 7; i < n; i += 8) v += G(p)[mine[i]];
+                for (int i = threadIdx.x & 31; i < n; i += 32) v += G(p)[mine[i]];
             }
         }
         double s[1] = {v};
@@ -982,7 +992,7 @@ template <typename T> __global__ __launch_bounds__(256) void attention_finish_ke
     }
     const int k = block >= f.first[2] ? 2 : block >= f.first[1] ? 1 : 0;
     const SumJob& j = f.job[k];
-    const int64_t i = (block - f.first[k]) * 256 + threadIdx.x;
+    const int64_t i = (block - f.first[k]) * AT_FINISH + threadIdx.x;
     if (i >= j.count) return;
     float v = 0.0f;
     int s = 0;
@@ -1001,13 +1011,13 @@ template <typename T> __global__ __launch_bounds__(256) void attention_finish_ke
 // ---- host -------------------------------------------------------------------------
 
 // Few units of an axis leave CUs idle: their walks are split until the workgroups fill the chip once (`target`: as many as it holds at
-// once; a second round for a few of them costs as much as a full one), while a part keeps two tiles on average.  Walks so long that
+// once; a second round for a few of them costs as much as a full one), while a part keeps two tiles on average, one in fp32.  Walks so long that
 // a part keeps 64 tiles are split until there are eight workgroups a CU, so that the longest under a causal mask do not end alone
 // (16384 tokens, 4 key heads, grad_k and grad_v: 5.8 ms in one part).
 int64_t axis_units(int64_t rows, int64_t sequences, int heads) { return std::max<int64_t>(1, (rows / AT_ROWS + sequences) * heads); }
-int plan_splits(int64_t rows, int64_t sequences, int heads, int64_t walk, int tile, int64_t target) {
+int plan_splits(int64_t rows, int64_t sequences, int heads, int64_t walk, int tile, int dtype, int64_t target) {
     const int64_t n = axis_units(rows, sequences, heads), tiles = std::max<int64_t>(1, walk / sequences / tile);
-    const int64_t want = std::max(std::min(target / n, tiles / 2), std::min(2048 / n, tiles / 64));
+    const int64_t want = std::max(std::min((target + n / 2) / n, dtype == MUON_F32 ? tiles : tiles / 2), std::min(2048 / n, tiles / 64));
     return static_cast<int>(std::min<int64_t>(std::max<int64_t>(1, want), AT_MAX_SPLITS));
 }
 int tile_rows(int dtype) { return dtype == MUON_BF16 ? walk_rows<uint16_t>() : walk_rows<float>(); }
@@ -1015,7 +1025,7 @@ int tile_rows(int dtype) { return dtype == MUON_BF16 ? walk_rows<uint16_t>() : w
 int64_t at_once(int dtype, int width) { return dtype == MUON_F32 && width > 64 ? AT_CUS : 2 * AT_CUS; }
 
 int forward_splits(const muon_attention_args& a) {
-    return plan_splits(a.queries, a.sequences, a.heads, a.keys, tile_rows(a.dtype), at_once(a.dtype, a.width));
+    return plan_splits(a.queries, a.sequences, a.heads, a.keys, tile_rows(a.dtype), a.dtype, at_once(a.dtype, a.width));
 }
 struct BackwardPlan {
     int q_splits, kv_splits;
@@ -1032,8 +1042,8 @@ BackwardPlan plan_backward(const muon_attention_backward_args& a) {
     // 12 in two.  Its room goes to them by their products, 3 and 4.
     p.all = a.queries && a.keys && qu + ku <= AT_CUS;
     const int64_t kv_walk = a.queries * (a.heads / a.kv_heads);
-    p.q_splits = plan_splits(a.queries, a.sequences, a.heads, a.keys, tile_rows(a.dtype), p.all ? AT_CUS * 3 / 7 : at_once(a.dtype, a.width));
-    p.kv_splits = plan_splits(a.keys, a.sequences, a.kv_heads, kv_walk, KV_ROWS, p.all ? AT_CUS * 4 / 7 : at_once(a.dtype, 128));
+    p.q_splits = plan_splits(a.queries, a.sequences, a.heads, a.keys, tile_rows(a.dtype), a.dtype, p.all ? AT_CUS * 3 / 7 : at_once(a.dtype, a.width));
+    p.kv_splits = plan_splits(a.keys, a.sequences, a.kv_heads, kv_walk, KV_ROWS, a.dtype, p.all ? AT_CUS * 4 / 7 : at_once(a.dtype, 128));
     p.q_blocks = a.queries ? span_units(a.queries, a.sequences, AT_ROWS) * a.heads * p.q_splits : 0;
     p.kv_blocks = a.keys ? span_units(a.keys, a.sequences, AT_ROWS) * a.kv_heads * p.kv_splits : 0;
     size_t at = 0;
@@ -1074,7 +1084,7 @@ Common common_args(const muon_attention_args& a, int splits) {
 
 // A launch holds at most 2^32 - 1 threads.
 template <typename F> hipError_t in_launches(int64_t blocks, F launch) {
-    constexpr int64_t MOST = int64_t{1} << 23;
+    constexpr int64_t MOST = int64_t{1} << 21;      // of up to 1024
     for (int64_t b = 0; b < blocks; b += MOST) {
         const hipError_t e = launch(b, static_cast<unsigned>(std::min(MOST, blocks - b)));
         if (e != hipSuccess) return e;
@@ -1141,10 +1151,10 @@ hipError_t run_backward(BackwardArgs f, const BackwardPlan& p, const muon_attent
         g.job[1] = {f.kv_part, f.grad_k, 2 * k, k, f.ld_dk, f.hs_dk, p.kv_splits, a.kv_heads, a.scale};
         g.job[2] = {f.kv_part + k, f.grad_v, 2 * k, k, f.ld_dv, f.hs_dv, p.kv_splits, a.kv_heads, 1.0f};
     }
-    for (int i = 0; i < 3; ++i) g.first[i + 1] = g.first[i] + (g.job[i].count + 255) / 256;
+    for (int i = 0; i < 3; ++i) g.first[i + 1] = g.first[i] + (g.job[i].count + AT_FINISH - 1) / AT_FINISH;
     return in_launches(g.first[3], [&](int64_t base, unsigned n) {
         g.block0 = base;
-        hipLaunchKernelGGL((attention_finish_kernel<T>), dim3(n), dim3(256), 0, s, g);
+        hipLaunchKernelGGL((attention_finish_kernel<T>), dim3(n), dim3(AT_FINISH), 0, s, g);
         return hipGetLastError();
     });
 }
