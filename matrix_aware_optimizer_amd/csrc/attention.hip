@@ -12,6 +12,7 @@
 // Both tiles of a walk are double-buffered in LDS; a step's loads are issued before the step before it is computed, with
 // one barrier a step.  Two workgroups run on a CU.
 #include <algorithm>
+#include <numeric>
 
 #include "attention_tile.h"
 
@@ -38,7 +39,8 @@ constexpr int KV_ROWS = 32;
 struct Common {
     muon_attention_args a;
     int64_t unit0;        // first unit of this launch
-    int64_t units;        // of the whole call: span_units x heads x splits
+    int64_t units;        // of the whole call: units of an axis x heads x splits
+    int64_t q_axis, q_stride, k_axis, k_stride;   // units of the two axes, and the stride through them
     int splits;
     int vec_in, vec_out;  // rows come in whole 16-byte chunks
     int window;           // 0: none
@@ -66,10 +68,12 @@ struct BackwardArgs {
 
 // Which unit of the axis, head and split a workgroup has.  Heads go fastest, and where they allow it in runs that share an XCD
 // (workgroups go to XCDs in turn), so that a key head's rows stay in one L2.
-__device__ __forceinline__ void decode(int64_t id, int heads, int splits, int& u, int& head, int& split) {
+// stride: how to go through the units (unit_stride).
+__device__ __forceinline__ void decode(int64_t id, int heads, int splits, int64_t axis, int64_t stride, int& u, int& head, int& split) {
     const int hs = heads * splits;
-    u = static_cast<int>(id / hs);
-    int k = static_cast<int>(id - static_cast<int64_t>(u) * hs);
+    const int64_t r = id / hs;
+    u = static_cast<int>(stride == 1 ? r : r * stride % axis);
+    int k = static_cast<int>(id - r * hs);
     if (hs % 8 == 0) k = (k % 8) * (hs / 8) + k / 8;
     head = k / splits;
     split = k - head * splits;
@@ -220,7 +224,7 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 ? 2 : 1) void attention_
     const Common& c = f.c;
     const muon_attention_args& a = c.a;
     int u, head, split;
-    decode(c.unit0 + blockIdx.x, a.heads, c.splits, u, head, split);
+    decode(c.unit0 + blockIdx.x, a.heads, c.splits, c.q_axis, c.q_stride, u, head, split);
     Span sp;
     if (!find_span<AT_ROWS, false>(a.offsets, a.key_offsets, static_cast<int>(a.sequences), static_cast<int>(a.queries), static_cast<int>(a.keys), a.causal, u, sp)) return;
     const W w(c, sp, head, split, c.splits);
@@ -494,7 +498,7 @@ template <typename T, int DP, bool BIAS> __device__ __forceinline__ void grad_q_
     const Common& c = f.c;
     const muon_attention_args& a = c.a;
     int u, head, split;
-    decode(block, a.heads, f.q_splits, u, head, split);
+    decode(block, a.heads, f.q_splits, c.q_axis, c.q_stride, u, head, split);
     lds_float_t* wbuf = (lds_float_t*)(buf + 4 * W::TILE);
     BiasSums sums;
     if constexpr (BIAS) {
@@ -673,7 +677,7 @@ __device__ __forceinline__ void grad_kv_block(const BackwardArgs& f, int64_t blo
     const Common& c = f.c;
     const muon_attention_args& a = c.a;
     int u, kv, split;
-    decode(block, a.kv_heads, f.kv_splits, u, kv, split);
+    decode(block, a.kv_heads, f.kv_splits, c.k_axis, c.k_stride, u, kv, split);
     Span sp;
     if (!find_span<AT_ROWS, true>(a.key_offsets, a.offsets, static_cast<int>(a.sequences), static_cast<int>(a.keys), static_cast<int>(a.queries), a.causal, u, sp)) return;
     const int lane = threadIdx.x & 63, wave = wave_id(), h = lane >> 5;
@@ -1011,13 +1015,14 @@ template <typename T> __global__ __launch_bounds__(AT_FINISH) void attention_fin
 // ---- host -------------------------------------------------------------------------
 
 // Few units of an axis leave CUs idle: their walks are split until the workgroups fill the chip once (`target`: as many as it holds at
-// once; a second round for a few of them costs as much as a full one), while a part keeps two tiles on average, one in fp32.  Walks so long that
-// a part keeps 64 tiles are split until there are eight workgroups a CU, so that the longest under a causal mask do not end alone
+// once; a second round for a few of them costs as much as a full one), while a part keeps two tiles on average, one in fp32 if there are
+// more than four (a join costs as much as one).  Under a causal
+// mask walks so long that a part keeps 64 tiles are split until there are eight workgroups a CU, so that the longest do not end alone
 // (16384 tokens, 4 key heads, grad_k and grad_v: 5.8 ms in one part).
 int64_t axis_units(int64_t rows, int64_t sequences, int heads) { return std::max<int64_t>(1, (rows / AT_ROWS + sequences) * heads); }
-int plan_splits(int64_t rows, int64_t sequences, int heads, int64_t walk, int tile, int dtype, int64_t target) {
+int plan_splits(int64_t rows, int64_t sequences, int heads, int64_t walk, int tile, int dtype, bool causal, int64_t target) {
     const int64_t n = axis_units(rows, sequences, heads), tiles = std::max<int64_t>(1, walk / sequences / tile);
-    const int64_t want = std::max(std::min((target + n / 2) / n, dtype == MUON_F32 ? tiles : tiles / 2), std::min(2048 / n, tiles / 64));
+    const int64_t want = std::max(std::min((target + n / 2) / n, dtype == MUON_F32 && tiles > 4 ? tiles : tiles / 2), causal ? std::min(2048 / n, tiles / 64) : 0);
     return static_cast<int>(std::min<int64_t>(std::max<int64_t>(1, want), AT_MAX_SPLITS));
 }
 int tile_rows(int dtype) { return dtype == MUON_BF16 ? walk_rows<uint16_t>() : walk_rows<float>(); }
@@ -1025,7 +1030,7 @@ int tile_rows(int dtype) { return dtype == MUON_BF16 ? walk_rows<uint16_t>() : w
 int64_t at_once(int dtype, int width) { return dtype == MUON_F32 && width > 64 ? AT_CUS : 2 * AT_CUS; }
 
 int forward_splits(const muon_attention_args& a) {
-    return plan_splits(a.queries, a.sequences, a.heads, a.keys, tile_rows(a.dtype), a.dtype, at_once(a.dtype, a.width));
+    return plan_splits(a.queries, a.sequences, a.heads, a.keys, tile_rows(a.dtype), a.dtype, a.causal, at_once(a.dtype, a.width));
 }
 struct BackwardPlan {
     int q_splits, kv_splits;
@@ -1042,8 +1047,8 @@ BackwardPlan plan_backward(const muon_attention_backward_args& a) {
     // 12 in two.  Its room goes to them by their products, 3 and 4.
     p.all = a.queries && a.keys && qu + ku <= AT_CUS;
     const int64_t kv_walk = a.queries * (a.heads / a.kv_heads);
-    p.q_splits = plan_splits(a.queries, a.sequences, a.heads, a.keys, tile_rows(a.dtype), a.dtype, p.all ? AT_CUS * 3 / 7 : at_once(a.dtype, a.width));
-    p.kv_splits = plan_splits(a.keys, a.sequences, a.kv_heads, kv_walk, KV_ROWS, a.dtype, p.all ? AT_CUS * 4 / 7 : at_once(a.dtype, 128));
+    p.q_splits = plan_splits(a.queries, a.sequences, a.heads, a.keys, tile_rows(a.dtype), a.dtype, a.causal, p.all ? AT_CUS * 3 / 7 : at_once(a.dtype, a.width));
+    p.kv_splits = plan_splits(a.keys, a.sequences, a.kv_heads, kv_walk, KV_ROWS, a.dtype, a.causal, p.all ? AT_CUS * 4 / 7 : at_once(a.dtype, 128));
     p.q_blocks = a.queries ? span_units(a.queries, a.sequences, AT_ROWS) * a.heads * p.q_splits : 0;
     p.kv_blocks = a.keys ? span_units(a.keys, a.sequences, AT_ROWS) * a.kv_heads * p.kv_splits : 0;
     size_t at = 0;
@@ -1072,9 +1077,22 @@ bool whole(const void* p, int64_t ld, int64_t hs, int64_t es) {
 }
 int64_t elem(int dtype) { return dtype == MUON_BF16 ? 2 : 4; }
 
+// 1, or for sequences beyond find_span's orders a stride of about 0.618 units that meets every one of them once (units are odd, so that
+// the stride mixes odd and even ones too).
+int64_t unit_stride(int64_t units, int64_t sequences) {
+    if (sequences <= SPAN_SCAN) return 1;
+    int64_t k = units * 309 / 500;
+    while (std::gcd(k, units) != 1) ++k;
+    return k;
+}
+
 Common common_args(const muon_attention_args& a, int splits) {
     Common c{};
     c.a = a;
+    c.q_axis = span_units(a.queries, a.sequences, AT_ROWS);
+    c.k_axis = span_units(a.keys, a.sequences, AT_ROWS);
+    c.q_stride = unit_stride(c.q_axis, a.sequences);
+    c.k_stride = unit_stride(c.k_axis, a.sequences);
     if (!c.a.key_offsets) c.a.key_offsets = c.a.offsets;
     c.splits = splits;
     c.window = static_cast<int>(std::min<int64_t>(a.window, (1 << 30) - 1));

@@ -278,9 +278,13 @@ struct Span {
 // that none of those runs alone at the end (8192 tokens in 6 sequences, 16 heads: grad_k and grad_v 262 -> 240 us, grad_q 189 ->
 // 181; without a mask that order would only part the tiles of a sequence, 166 -> 189 us at 12 sequences): unit (s, r) of sequence s is the one with r units of s behind it (HEAD: before it) in that respect, and all units of a larger r
 // come first.  A wave does that for up to 61 sequences, one a lane: C(r) = sum over s of max(0, units of s - r) units have a rank
-// of r or more.  For more sequences unit u is rows BM j .. of sequence s with bound(s) / BM + s + j = u: distinct for distinct
-// (s, j), since a sequence has at most bound(s + 1) / BM - bound(s) / BM + 1 units; a wave looks at 64 sequences at once.
-__host__ __device__ inline int64_t span_units(int64_t rows, int64_t sequences, int bm) { return rows / bm + sequences + 3; }
+// of r or more.  For more sequences, up to SPAN_SCAN, it adds units up in order, 4 x 63 sequences a trip to memory.  For more still unit u is rows BM j .. of sequence s with bound(s) / BM + s + j = u: distinct for distinct
+// (s, j), since a sequence has at most bound(s + 1) / BM - bound(s) / BM + 1 units; a wave looks at 64 sequences at once.  Units
+// without rows then stand between the others, every second one where sequences have up to BM rows, and XCDs and shader engines, which take
+// workgroups in turn, would leave half the chip without work (200 sequences of 128 rows: 188 us, 95 in order): the caller
+// goes through the units by a stride that mixes them.
+constexpr int SPAN_LANES = 61, SPAN_SCAN = 512;   // sequences that find_span handles a lane each, and in order
+__host__ __device__ inline int64_t span_units(int64_t rows, int64_t sequences, int bm) { return (rows / bm + sequences + 3) | 1; }
 __device__ __forceinline__ int bound(const int64_t* offsets, int sequences, int rows, int s) {
     if (s <= 0) return 0;
     if (s > sequences + 1) return rows;
@@ -293,7 +297,7 @@ template <int BM, bool HEAD>
 __device__ __forceinline__ bool find_span(const int64_t* offsets, const int64_t* others, int sequences, int rows, int other_rows, bool causal, int u, Span& sp) {
     const int lane = threadIdx.x & 63;
     int s, b0, o0, o1, j;
-    if (sequences <= 61) {
+    if (sequences <= SPAN_LANES) {
         // every bound of both axes at once, one trip to memory
         const int mine = bound(offsets, sequences, rows, lane), other = bound(others, sequences, other_rows, lane);
         const int len = __shfl(mine, lane + 1) - mine, units = lane <= sequences + 1 && len > 0 ? (len + BM - 1) / BM : 0;
@@ -329,8 +333,41 @@ __device__ __forceinline__ bool find_span(const int64_t* offsets, const int64_t*
         sp.len = __builtin_amdgcn_readlane(len, s);
         o0 = __builtin_amdgcn_readlane(other, s);
         o1 = __builtin_amdgcn_readlane(other, s + 1);
+    } else if (sequences <= SPAN_SCAN) {
+        int c = 0, base = 0;
+        bool found = false;
+        s = j = b0 = 0;
+        while (!found && c < sequences + 2) {
+            int mine[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mine[k] = bound(offsets, sequences, rows, c + 63 * k + lane);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int at = c + 63 * k + lane, len = __shfl(mine[k], lane + 1) - mine[k];
+                const int units = lane < 63 && at <= sequences + 1 && len > 0 ? (len + BM - 1) / BM : 0;
+                const int total = static_cast<int>(wave_sum(static_cast<float>(units)));
+                if (!found && u < base + total) {
+                    found = true;
+                    int upto = units;
+#pragma unroll
+                    for (int d = 1; d < 64; d <<= 1) {
+                        const int v = __shfl_up(upto, d);
+                        upto += lane >= d ? v : 0;
+                    }
+                    const int l = __popcll(__ballot(base + upto <= u));
+                    s = c + 63 * k + l;
+                    j = u - base - __builtin_amdgcn_readlane(upto - units, l);
+                    b0 = __builtin_amdgcn_readlane(mine[k], l);
+                    sp.len = __builtin_amdgcn_readlane(len, l);
+                }
+                base += found ? 0 : total;
+            }
+            c += 4 * 63;
+        }
+        if (!found) return false;
+        o0 = bound(others, sequences, other_rows, s);
+        o1 = bound(others, sequences, other_rows, s + 1);
     } else {
-        if constexpr (!HEAD) u = static_cast<int>(span_units(rows, sequences, BM)) - 1 - u;
         int lo = 0, hi = sequences + 1;
         while (hi > lo) {
             const int step = (hi - lo + 63) / 64;
