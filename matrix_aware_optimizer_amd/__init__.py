@@ -926,44 +926,58 @@ def muon_policy_loss(logp, old_logp, advantages, offsets, loss, grad_logp=None, 
 
 def _heads(t, what, shape, dtype):
     """Pitches (token, head) in elements of a tokens x heads x width tensor of this shape and dtype, unit stride along width."""
-    if t.shape != shape or t.dtype != dtype:
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{what} must be {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    if shape[0] == 0:
-        return shape[1] * shape[2], shape[2]
+    tokens, heads, width = shape
+    if tokens == 0:
+        return heads * width, width
     ld, hs, step = t.stride()
-    if step != 1 and shape[2] > 1:
+    if step != 1 and width > 1:
         raise ValueError(f"{what} must have unit stride along the head width")
     # the stride of a dimension of one is nobody's
-    hs = shape[2] if shape[1] <= 1 else hs
-    return (shape[1] * hs if shape[0] <= 1 else ld), hs
+    if heads <= 1:
+        hs = width
+    return (heads * hs if tokens == 1 else ld), hs
+
+
+def _check_offsets(t, what):
+    """The number of spans of an int64 vector of their bounds."""
+    import torch
+    shape = t.shape
+    if len(shape) != 1 or shape[0] < 2 or t.dtype is not torch.int64 or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous int64 vector of at least two")
+    return shape[0] - 1
 
 
 def _attention_shape(q, k, v, offsets, key_offsets, key_mask, bias, bucket_map):
     """(queries, keys, sequences, heads, kv_heads, width, buckets, reach, dtype code)."""
     import torch
-    if q.dim() != 3 or k.dim() != 3 or q.shape[2] != k.shape[2] or (v is not None and v.shape != k.shape):
-        raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)} and v must be tokens x heads x width, k and v of one shape")
-    (queries, heads, width), (keys, kv_heads) = q.shape, k.shape[:2]
-    sequences = 1
-    for t, what in ((offsets, "offsets"), (key_offsets, "key_offsets")):
-        if t is not None:
-            if t.dim() != 1 or t.shape[0] < 2 or t.dtype != torch.int64 or not t.is_contiguous():
-                raise ValueError(f"{what} must be a contiguous int64 vector of sequences + 1")
-            if what == "key_offsets" and (offsets is None or t.shape != offsets.shape):
-                raise ValueError("key_offsets must have the length of offsets")
-            sequences = t.shape[0] - 1
+    qs, ks = q.shape, k.shape
+    if len(qs) != 3 or len(ks) != 3 or qs[2] != ks[2] or (v is not None and v.shape != ks):
+        raise ValueError(f"q {tuple(qs)}, k {tuple(ks)} and v must be tokens x heads x width, k and v of one shape")
+    queries, heads, width = qs
+    keys, kv_heads, _ = ks
+    sequences, buckets, reach = 1, 0, 0
+    if offsets is not None:
+        sequences = _check_offsets(offsets, "offsets")
+        if key_offsets is None:
+            if queries != keys and v is not None:
+                raise ValueError("queries and keys differ: key_offsets is needed")
+        elif _check_offsets(key_offsets, "key_offsets") != sequences:
+            raise ValueError("key_offsets must have the length of offsets")
+    elif key_offsets is not None:
+        raise ValueError("key_offsets needs offsets")
     if key_mask is not None:
         _check_vector(key_mask, "key_mask", keys, torch.uint8, torch.bool)
-    buckets = reach = 0
-    if (bias is None) != (bucket_map is None):
-        raise ValueError("bias and bucket_map go together")
-    if bias is not None:
+    if bias is not None or bucket_map is not None:
+        if bias is None or bucket_map is None:
+            raise ValueError("bias and bucket_map go together")
         if bias.dim() != 2 or bias.shape[1] != heads or bias.dtype != q.dtype or not bias.is_contiguous():
             raise ValueError(f"bias must be contiguous {q.dtype} of buckets x {heads} heads, got {bias.dtype} {tuple(bias.shape)}")
         if bucket_map.dim() != 1 or bucket_map.shape[0] % 2 != 1 or bucket_map.dtype != torch.int32 or not bucket_map.is_contiguous():
             raise ValueError("bucket_map must be a contiguous int32 vector of 2 reach + 1")
         buckets, reach = bias.shape[0], bucket_map.shape[0] // 2
-    return queries, keys, sequences, heads, kv_heads, width, buckets, reach, _dtype_code(q)
+    return queries, keys, sequences, heads, kv_heads, width, buckets, reach, _dtype_code(q.dtype)
 
 
 def _attention_scale(scale, width):
@@ -998,10 +1012,8 @@ def muon_attention(q, k, v, out, lse, *, offsets=None, key_offsets=None, key_mas
     n, m, sequences, heads, kv_heads, width, buckets, reach, code = _attention_shape(
         q, k, v, offsets, key_offsets, key_mask, bias, bucket_map)
     shape, dtype = q.shape, q.dtype
-    if offsets is not None and key_offsets is None and n != m:
-        raise ValueError("queries and keys differ: key_offsets is needed")
-    if lse.dtype != torch.float32 or lse.shape != shape[:2] or not lse.is_contiguous():
-        raise ValueError(f"lse must be contiguous float32 of shape {tuple(shape[:2])}")
+    if lse.dtype is not torch.float32 or lse.shape != (n, heads) or not lse.is_contiguous():
+        raise ValueError(f"lse must be contiguous float32 of shape {(n, heads)}")
     packed = _pack_attention(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(offsets), _ptr(key_offsets), _ptr(key_mask), _ptr(bias),
         _ptr(bucket_map), out.data_ptr(), lse.data_ptr(), _ptr(out_low), n, m, sequences, *_heads(q, "q", shape, dtype),
@@ -1037,10 +1049,8 @@ def muon_attention_backward(q, k, v, out, lse, grad_out, grad_q, grad_k, grad_v,
     n, m, sequences, heads, kv_heads, width, buckets, reach, code = _attention_shape(
         q, k, v, offsets, key_offsets, key_mask, bias, bucket_map)
     shape, dtype = q.shape, q.dtype
-    if offsets is not None and key_offsets is None and n != m:
-        raise ValueError("queries and keys differ: key_offsets is needed")
-    if lse.dtype != torch.float32 or lse.shape != shape[:2] or not lse.is_contiguous():
-        raise ValueError(f"lse must be contiguous float32 of shape {tuple(shape[:2])}")
+    if lse.dtype is not torch.float32 or lse.shape != (n, heads) or not lse.is_contiguous():
+        raise ValueError(f"lse must be contiguous float32 of shape {(n, heads)}")
     if (bias is None) != (grad_bias is None):
         raise ValueError("bias and its gradient go together")
     if bias is not None and (grad_bias.shape != bias.shape or grad_bias.dtype != dtype or not grad_bias.is_contiguous()):
@@ -1063,15 +1073,17 @@ def muon_attention_backward(q, k, v, out, lse, grad_out, grad_q, grad_k, grad_v,
 
 def _choices(t, what, tokens, dtype):
     """The number of choices a token of a contiguous tokens x chosen tensor."""
-    if t.dim() != 2 or t.shape[0] != tokens or t.dtype != dtype or not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous {dtype} of {tokens} tokens x choices, got {t.dtype} {tuple(t.shape)}")
-    return t.shape[1]
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != tokens or t.dtype is not dtype or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous {dtype} of {tokens} tokens x choices, got {t.dtype} {tuple(shape)}")
+    return shape[1]
 
 
 def _matrix_shape(t, what):
-    if t.dim() != 2:
-        raise ValueError(f"{what} must be 2-D, got shape {tuple(t.shape)}")
-    return t.shape
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{what} must be 2-D, got shape {tuple(shape)}")
+    return shape
 
 
 def muon_expert_sort_workspace_bytes(x, experts, num_experts) -> int:
@@ -1097,11 +1109,10 @@ def muon_expert_sort(x, experts, sorted_x, slots, offsets, *, workspace=None, st
     chosen = _choices(experts, "experts", tokens, torch.int64)
     if _choices(slots, "slots", tokens, torch.int32) != chosen:
         raise ValueError("slots must have the shape of experts")
-    if offsets.dim() != 1 or offsets.shape[0] < 2 or offsets.dtype != torch.int64 or not offsets.is_contiguous():
-        raise ValueError("offsets must be a contiguous int64 vector of experts + 1")
+    num_experts = _check_offsets(offsets, "offsets")
     packed = _pack_sort(x.data_ptr(), experts.data_ptr(), sorted_x.data_ptr(), slots.data_ptr(), offsets.data_ptr(), tokens,
                         cols, _pitch(x, "x", x.shape, x.dtype), _pitch(sorted_x, "sorted_x", (tokens * chosen, cols), x.dtype),
-                        chosen, offsets.shape[0] - 1, _dtype_code(x))
+                        chosen, num_experts, _dtype_code(x.dtype))
     raw = _raw_stream(stream, x, experts, sorted_x, slots, offsets, workspace)
     lib = load()
     return _call(lib.muon_expert_sort, lib.muon_expert_sort_workspace_bytes, packed, workspace, x.device, stream, raw)
@@ -1149,13 +1160,12 @@ def muon_expert_combine_backward(grad_out, y, slots, weights, offsets, grad_y, g
     for t, what in ((weights, "weights"), (grad_weights, "grad_weights")):
         if _choices(t, what, tokens, torch.float32) != chosen:
             raise ValueError(f"{what} must have the shape of slots")
-    if offsets.dim() != 1 or offsets.shape[0] < 2 or offsets.dtype != torch.int64 or not offsets.is_contiguous():
-        raise ValueError("offsets must be a contiguous int64 vector of experts + 1")
+    num_experts = _check_offsets(offsets, "offsets")
     rows, dtype = (tokens * chosen, cols), grad_out.dtype
     packed = _pack_combine_backward(
         grad_out.data_ptr(), y.data_ptr(), slots.data_ptr(), weights.data_ptr(), offsets.data_ptr(), grad_y.data_ptr(),
         grad_weights.data_ptr(), tokens, cols, _pitch(grad_out, "grad_out", grad_out.shape, dtype), _pitch(y, "y", rows, dtype),
-        _pitch(grad_y, "grad_y", rows, dtype), chosen, offsets.shape[0] - 1, _dtype_code(grad_out))
+        _pitch(grad_y, "grad_y", rows, dtype), chosen, num_experts, _dtype_code(dtype))
     raw = _raw_stream(stream, grad_out, y, slots, weights, offsets, grad_y, grad_weights)
     _check(load().muon_expert_combine_backward(packed, raw))
 
