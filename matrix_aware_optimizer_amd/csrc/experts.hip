@@ -97,10 +97,25 @@ template <typename T> __global__ __launch_bounds__(EX_THREADS) void expert_place
     if (block != 0 && chunk * EX_CHUNK + share * span >= n) return;
     int* hist = lds;                         // [wave][E + 1], then the choices of the waves before
     int* first = hist + EX_WAVES * (E + 1);  // E + 1: where the expert's choices of this chunk begin
-    int* place = first + E + 1;              // EX_CHUNK
+    int* totals = first + E + 1;             // E + 1
+    int* place = totals + E + 1;             // EX_CHUNK
     int* red = place + EX_CHUNK;             // EX_WAVES
-    for (int i = threadIdx.x; i < EX_WAVES * (E + 1); i += EX_THREADS) hist[i] = 0;
+    for (int i = threadIdx.x; i < (EX_WAVES + 2) * (E + 1); i += EX_THREADS) hist[i] = 0;
     __syncthreads();
+
+    // totals of all experts, and what the chunks before this one hold: chunks in turn to the waves
+    if (s.chunks > 1 && !s.scanned)
+        for (int e = lane; e < E; e += 64) {
+            int before = 0, total = 0;
+#pragma unroll 8
+            for (int c = wave; c < s.chunks; c += EX_WAVES) {
+                const int v = G(s.counts)[static_cast<int64_t>(c) * E + e];
+                before += c < chunk ? v : 0;
+                total += v;
+            }
+            atomicAdd(&first[e], before);
+            atomicAdd(&totals[e], total);
+        }
 
     // each wave ranks its own choices, in order
     int expert[EX_PER], rank[EX_PER];
@@ -122,29 +137,19 @@ template <typename T> __global__ __launch_bounds__(EX_THREADS) void expert_place
         __syncthreads();
     }
 
-    // totals of all experts, their running sum, and what chunks before this one hold
+    // the running sum of the totals
     const int per = (E + EX_THREADS - 1) / EX_THREADS, e0 = threadIdx.x * per;
     int sum = 0;
     for (int e = e0; e < min(e0 + per, E); ++e) {
-        int own = 0, before = 0, total = 0;
+        int own = 0;
 #pragma unroll
         for (int w = 0; w < EX_WAVES; ++w) {
             const int v = hist[w * (E + 1) + e];
             hist[w * (E + 1) + e] = own;
             own += v;
         }
-        if (s.chunks == 1) {
-            total = own;
-        } else if (s.scanned) {
-            before = G(s.counts)[chunk * E + e];
-            total = G(s.totals)[e];
-        } else {
-            for (int c = 0; c < s.chunks; ++c) {
-                const int v = G(s.counts)[static_cast<int64_t>(c) * E + e];
-                before += c < chunk ? v : 0;
-                total += v;
-            }
-        }
+        const int before = s.scanned ? G(s.counts)[chunk * E + e] : first[e];
+        const int total = s.chunks == 1 ? own : s.scanned ? G(s.totals)[e] : totals[e];
         first[e] = sum + before;
         sum += total;
     }
@@ -359,7 +364,7 @@ hipError_t launch_expert_sort(const muon_expert_sort_args& a, void* workspace, h
     }
     int shares = 4;
     while (shares < EX_MOST_SHARES && shares * g.chunks < EX_WORKGROUPS) shares *= 2;
-    const size_t lds = ((EX_WAVES + 1) * (a.num_experts + 1) + EX_CHUNK + EX_WAVES) * sizeof(int);
+    const size_t lds = ((EX_WAVES + 2) * (a.num_experts + 1) + EX_CHUNK + EX_WAVES) * sizeof(int);
     return in_launches(static_cast<int64_t>(g.chunks) * shares, [&](int64_t b, unsigned blocks) {
         g.block0 = b;
         if (a.dtype == MUON_BF16) hipLaunchKernelGGL((expert_place_kernel<uint16_t>), dim3(blocks), dim3(EX_THREADS), lds, s, g, shares);
