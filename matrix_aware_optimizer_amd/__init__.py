@@ -980,19 +980,29 @@ def _attention_shape(q, k, v, offsets, key_offsets, key_mask, bias, bucket_map):
     return queries, keys, sequences, heads, kv_heads, width, buckets, reach, _dtype_code(q.dtype)
 
 
+def _attention_stand_ins(q, k, n):
+    """Stand-in addresses for calls that ask for sizes, never dereferenced; q's and k's aligned as they are, the others like k."""
+    odd = k.data_ptr() % 16
+    return [(1 << 44) + q.data_ptr() % 16] + [(j << 44) + odd for j in range(2, n + 1)]
+
+
 def _attention_scale(scale, width):
     return width ** -0.5 if scale is None else scale
 
 
 def muon_attention_workspace_bytes(q, k, *, sequences=1) -> int:
-    """Workspace of :func:`muon_attention` for these shapes."""
+    """Workspace of :func:`muon_attention` for these shapes, v laid out like k.
+
+    Inputs of odd widths, pitches or starts take more (they are copied first); the call itself says how much if it is
+    given too little.
+    """
     n, m, _, heads, kv_heads, width, _, _, code = _attention_shape(q, k, None, None, None, None, None, None)
-    # sizes only: distinct stand-in addresses, never dereferenced
-    at = [j << 44 for j in range(1, 8)]
-    lq, lk = heads * width, kv_heads * width
-    return _size(load().muon_attention_workspace_bytes,
-                 _pack_attention(at[0], at[1], at[2], at[3], 0, 0, 0, 0, at[4], at[5], 0, n, m, sequences, lq, width, lk,
-                                 width, lk, width, lq, width, 0, 0, 0, 1.0, heads, kv_heads, width, 0, 0, 0, code))
+    at, lq, lk = _attention_stand_ins(q, k, 3), _heads(q, "q", q.shape, q.dtype), _heads(k, "k", k.shape, q.dtype)
+    size = load().muon_attention_workspace_bytes
+    # the longest walks are split under a causal mask, others where there are few: as much as either takes
+    return max(_size(size, _pack_attention(*at, 4 << 44, 0, 0, 0, 0, 5 << 44, 6 << 44, 0, n, m, sequences, *lq, *lk, *lk,
+                                           heads * width, width, 0, 0, 0, 1.0, heads, kv_heads, width, 0, 0, causal, code))
+               for causal in (0, 1))
 
 
 def muon_attention(q, k, v, out, lse, *, offsets=None, key_offsets=None, key_mask=None, bias=None, bucket_map=None,
@@ -1026,14 +1036,18 @@ def muon_attention(q, k, v, out, lse, *, offsets=None, key_offsets=None, key_mas
 
 
 def muon_attention_backward_workspace_bytes(q, k, *, sequences=1, bias=None, bucket_map=None) -> int:
-    """Workspace of :func:`muon_attention_backward` for these shapes."""
+    """Workspace of :func:`muon_attention_backward` for these shapes, v laid out like k, out, out_low and grad_out like q
+    (see :func:`muon_attention_workspace_bytes`)."""
     n, m, _, heads, kv_heads, width, buckets, reach, code = _attention_shape(q, k, None, None, None, None, bias, bucket_map)
-    at = [j << 44 for j in range(1, 16)]
-    lq, lk, b = heads * width, kv_heads * width, bias is not None
-    return _size(load().muon_attention_backward_workspace_bytes, _pack_attention_backward(
-        at[0], at[1], at[2], at[3], 0, 0, at[4] if b else 0, at[5] if b else 0, at[6], at[7], 0, at[8], at[9], at[10],
-        at[11], at[12] if b else 0, n, m, sequences, lq, width, lk, width, lk, width, lq, width, 0, 0, lq, width, lq, width,
-        lk, width, lk, width, 0, 1.0, heads, kv_heads, width, buckets, reach, 0, code))
+    odd, b = q.data_ptr() % 16, bias is not None
+    at, lq, lk = _attention_stand_ins(q, k, 3), _heads(q, "q", q.shape, q.dtype), _heads(k, "k", k.shape, q.dtype)
+    far = [j << 44 for j in range(4, 16)]
+    size = load().muon_attention_backward_workspace_bytes
+    return max(_size(size, _pack_attention_backward(
+        *at, far[0], 0, 0, far[1] if b else 0, far[2] if b else 0, far[3] + odd, far[4], far[5] + odd, far[6] + odd,
+        far[7], far[8], far[9], far[10] if b else 0, n, m, sequences, *lq, *lk, *lk, *lq, *lq, *lq, heads * width, width,
+        kv_heads * width, width, kv_heads * width, width, 0, 1.0, heads, kv_heads, width, buckets, reach, causal, code))
+        for causal in (0, 1))
 
 
 def muon_attention_backward(q, k, v, out, lse, grad_out, grad_q, grad_k, grad_v, *, offsets=None, key_offsets=None,

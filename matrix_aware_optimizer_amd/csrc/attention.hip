@@ -42,7 +42,7 @@ struct Common {
     int64_t units;        // of the whole call: units of an axis x heads x splits
     int64_t q_axis, q_stride, k_axis, k_stride;   // units of the two axes, and the stride through them
     int splits;
-    int vec_in, vec_out;  // rows come in whole 16-byte chunks
+    int vec_out;          // the outputs' rows come in whole 16-byte chunks; the inputs' always do (packed first where they do not)
     int window;           // 0: none
     int gqa;              // heads / kv_heads
 };
@@ -169,10 +169,10 @@ template <typename T, int DP> struct KeyWalk {
         const bool in = j < sp.other_len && static_cast<int>(threadIdx.x & 63) < BN;
         return in ? (a.key_mask ? G(a.key_mask)[sp.other + j] : 1u) : 0u;
     }
-    __device__ __forceinline__ void load(int t, lds_byte_t* k, lds_byte_t* v, uint64_t live, bool vec) const {
+    __device__ __forceinline__ void load(int t, lds_byte_t* k, lds_byte_t* v, uint64_t live) const {
         const int64_t j = static_cast<int64_t>(t) * BN;
-        load_tile<T, DP, BN, AT_THREADS>(k, kbase + j * a.ld_k, a.ld_k, a.width, live, vec);
-        load_tile<T, DP, BN, AT_THREADS>(v, vbase + j * a.ld_v, a.ld_v, a.width, live, vec);
+        load_tile<T, DP, BN, AT_THREADS>(k, kbase + j * a.ld_k, a.ld_k, a.width, live);
+        load_tile<T, DP, BN, AT_THREADS>(v, vbase + j * a.ld_v, a.ld_v, a.width, live);
     }
     __device__ __forceinline__ Sight sight(const Common& c, int at) const {      // of the query at place `at`
         const int p = at + off;
@@ -241,7 +241,7 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 ? 2 : 1) void attention_
         const T* q = static_cast<const T*>(a.q) + row * a.ld_q + static_cast<int64_t>(head) * a.hs_q;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-            qf[ks] = global_frag<T>(q, 16 * ks + 8 * (lane >> 5), a.width, row_ok && a.scale != 0.0f, c.vec_in);
+            qf[ks] = global_frag<T>(q, 16 * ks + 8 * (lane >> 5), a.width, row_ok && a.scale != 0.0f);
             if (a.scale < 0.0f) negate<T>(qf[ks]);
         }
     }
@@ -271,7 +271,7 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 ? 2 : 1) void attention_
             far_hi = bias_value<T>(a, hi_bucket, head);
             bw.ask(a, w.window_first(w.first + 1));
         }
-        w.load(w.first, buf, buf + W::TILE, next, c.vec_in);
+        w.load(w.first, buf, buf + W::TILE, next);
         if constexpr (BIAS) bw.put(wbuf);
     }
     for (int t = w.first; t < w.last; ++t) {
@@ -280,7 +280,7 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 ? 2 : 1) void attention_
         live = next;
         if (t + 1 < w.last) {
             next = __ballot(byte != 0);
-            w.load(t + 1, buf + 2 * W::TILE * (b ^ 1), buf + 2 * W::TILE * (b ^ 1) + W::TILE, next, c.vec_in);
+            w.load(t + 1, buf + 2 * W::TILE * (b ^ 1), buf + 2 * W::TILE * (b ^ 1) + W::TILE, next);
             byte = w.key_byte(t + 2);
             if constexpr (BIAS) {
                 bw.fetch(a, head);
@@ -530,14 +530,14 @@ template <typename T, int DP, bool BIAS> __device__ __forceinline__ void grad_q_
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
             const int e0 = 16 * ks + 8 * h;
-            qf[ks] = global_frag<T>(q, e0, a.width, row_ok && a.scale != 0.0f, c.vec_in);
+            qf[ks] = global_frag<T>(q, e0, a.width, row_ok && a.scale != 0.0f);
             if (a.scale < 0.0f) negate<T>(qf[ks]);
-            df[ks] = global_frag<T>(d, e0, a.width, row_ok, c.vec_in);
-            const Frag<T> of = global_frag<T>(out, e0, a.width, row_ok, c.vec_in);
+            df[ks] = global_frag<T>(d, e0, a.width, row_ok);
+            const Frag<T> of = global_frag<T>(out, e0, a.width, row_ok);
 #pragma unroll
             for (int e = 0; e < 8; ++e) delta = fmaf(frag_get(df[ks], e), frag_get(of, e), delta);
             if (a.out_low) {
-                const Frag<T> lf = global_frag<T>(low, e0, a.width, row_ok, c.vec_in);
+                const Frag<T> lf = global_frag<T>(low, e0, a.width, row_ok);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) delta = fmaf(frag_get(df[ks], e), frag_get(lf, e), delta);
             }
@@ -570,7 +570,7 @@ template <typename T, int DP, bool BIAS> __device__ __forceinline__ void grad_q_
             far_hi = bias_value<T>(a, hi_bucket, head);
             bw.ask(a, w.window_first(w.first + 1));
         }
-        w.load(w.first, buf, buf + W::TILE, next, c.vec_in);
+        w.load(w.first, buf, buf + W::TILE, next);
         if constexpr (BIAS) bw.put(wbuf);
     }
     for (int t = w.first; t < w.last; ++t) {
@@ -579,7 +579,7 @@ template <typename T, int DP, bool BIAS> __device__ __forceinline__ void grad_q_
         live = next;
         if (t + 1 < w.last) {
             next = __ballot(byte != 0);
-            w.load(t + 1, buf + 2 * W::TILE * (b ^ 1), buf + 2 * W::TILE * (b ^ 1) + W::TILE, next, c.vec_in);
+            w.load(t + 1, buf + 2 * W::TILE * (b ^ 1), buf + 2 * W::TILE * (b ^ 1) + W::TILE, next);
             byte = w.key_byte(t + 2);
             if constexpr (BIAS) {
                 bw.fetch(a, head);
@@ -705,7 +705,7 @@ __device__ __forceinline__ void grad_kv_block(const BackwardArgs& f, int64_t blo
             const int64_t first = sp.start + b;
             const uint64_t live = __ballot(j < sp.len && (!a.key_mask || G(a.key_mask)[j < sp.len ? first + lane : 0] != 0));
             load_tile<T, DP, 64, AT_THREADS>(buf + 4 * TILE + b * Row<T, DP>::BYTES,
-                                          static_cast<const T*>(a.v) + first * a.ld_v + static_cast<int64_t>(kv) * a.hs_v, a.ld_v, a.width, live, c.vec_in);
+                                          static_cast<const T*>(a.v) + first * a.ld_v + static_cast<int64_t>(kv) * a.hs_v, a.ld_v, a.width, live);
         }
     }
     {
@@ -713,9 +713,9 @@ __device__ __forceinline__ void grad_kv_block(const BackwardArgs& f, int64_t blo
         const T* v = static_cast<const T*>(a.v) + row * a.ld_v + static_cast<int64_t>(kv) * a.hs_v;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-            kf[ks] = global_frag<T>(k, 16 * ks + 8 * h, a.width, key_ok && a.scale != 0.0f, c.vec_in);
+            kf[ks] = global_frag<T>(k, 16 * ks + 8 * h, a.width, key_ok && a.scale != 0.0f);
             if (a.scale < 0.0f) negate<T>(kf[ks]);
-            if constexpr (!V_LDS) vf[ks] = global_frag<T>(v, 16 * ks + 8 * h, a.width, key_ok, c.vec_in);
+            if constexpr (!V_LDS) vf[ks] = global_frag<T>(v, 16 * ks + 8 * h, a.width, key_ok);
         }
     }
     // the walk: tiles first .. first + n - 1 of the queries, for every head that shares this key head
@@ -771,17 +771,17 @@ __device__ __forceinline__ void grad_kv_block(const BackwardArgs& f, int64_t blo
 #pragma unroll
             for (int k = 0; k < DP / 64; ++k) {
                 const int e0 = 64 * k + 8 * (lane & 7);
-                own_d[k] = global_frag<T>(dr, e0, a.width, ok, c.vec_in);
-                own_o[k] = global_frag<T>(outr, e0, a.width, ok, c.vec_in);
-                if (a.out_low) own_l[k] = global_frag<T>(low, e0, a.width, ok, c.vec_in);
+                own_d[k] = global_frag<T>(dr, e0, a.width, ok);
+                own_o[k] = global_frag<T>(outr, e0, a.width, ok);
+                if (a.out_low) own_l[k] = global_frag<T>(low, e0, a.width, ok);
             }
         }
     };
     auto load = [&](const At& w, int b, float l, float d) {
         const uint64_t live = __ballot(l != NEG_INF);
         const int64_t i0 = static_cast<int64_t>(sp.other) + static_cast<int64_t>(w.t) * BQ;
-        load_tile<T, DP, BQ, AT_THREADS>(buf + 2 * TILE * b, static_cast<const T*>(a.q) + i0 * a.ld_q + static_cast<int64_t>(w.head) * a.hs_q, a.ld_q, a.width, live, c.vec_in);
-        load_tile<T, DP, BQ, AT_THREADS>(buf + 2 * TILE * b + TILE, static_cast<const T*>(f.grad_out) + i0 * f.ld_do + static_cast<int64_t>(w.head) * f.hs_do, f.ld_do, a.width, live, c.vec_in);
+        load_tile<T, DP, BQ, AT_THREADS>(buf + 2 * TILE * b, static_cast<const T*>(a.q) + i0 * a.ld_q + static_cast<int64_t>(w.head) * a.hs_q, a.ld_q, a.width, live);
+        load_tile<T, DP, BQ, AT_THREADS>(buf + 2 * TILE * b + TILE, static_cast<const T*>(f.grad_out) + i0 * f.ld_do + static_cast<int64_t>(w.head) * f.hs_do, f.ld_do, a.width, live);
         if (wave == 0 && lane < BQ) {
             stats[2 * BQ * b + lane] = l == NEG_INF ? 0.0f : BIAS ? l : l * LOG2E;
             if constexpr (!SELF) stats[2 * BQ * b + BQ + lane] = l == NEG_INF ? 0.0f : d;
@@ -1012,6 +1012,33 @@ template <typename T> __global__ __launch_bounds__(AT_FINISH) void attention_fin
     st_el<T>(j.out, row * j.ld + (at - row * j.heads) * j.hs + (i - at * f.width), v * j.scale);
 }
 
+// ---- rows to whole chunks -----------------------------------------------------------------
+
+struct PackJob {
+    const void* src;
+    void* dst;
+    int64_t ld, hs, count, heads;   // count: rows x heads
+    int64_t first;                  // chunk of the whole launch
+};
+struct PackArgs {
+    PackJob job[6];
+    int64_t total;                  // chunks
+    int64_t base;
+    int jobs, width, chunks;        // chunks a row
+};
+template <typename T> __global__ __launch_bounds__(256) void attention_pack_kernel(PackArgs p) {
+    const int64_t i = p.base + static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= p.total) return;
+    int k = 0;
+#pragma unroll
+    for (int n = 1; n < 6; ++n) k = n < p.jobs && i >= p.job[n].first ? n : k;
+    const PackJob& j = p.job[k];
+    const int64_t c = i - j.first, row = c / p.chunks, t = row / j.heads;
+    const int e0 = static_cast<int>(c - row * p.chunks) * (16 / static_cast<int>(sizeof(T)));
+    const T* src = static_cast<const T*>(j.src) + t * j.ld + (row - t * j.heads) * j.hs;
+    G(static_cast<u32x4_t*>(j.dst))[c] = ld_part<T>(src + e0, p.width - e0);
+}
+
 // ---- host -------------------------------------------------------------------------
 
 // Few units of an axis leave CUs idle: their walks are split until the workgroups fill the chip once (`target`: as many as it holds at
@@ -1072,10 +1099,36 @@ BackwardPlan plan_backward(const muon_attention_backward_args& a) {
     return p;
 }
 
+int64_t elem(int dtype) { return dtype == MUON_BF16 ? 2 : 4; }
 bool whole(const void* p, int64_t ld, int64_t hs, int64_t es) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * es % 16 == 0 && hs * es % 16 == 0;
 }
-int64_t elem(int dtype) { return dtype == MUON_BF16 ? 2 : 4; }
+
+// Inputs whose rows do not come in whole 16-byte chunks (odd widths, pitches or starts) are copied into the workspace first, one
+// launch for all, rows of the next whole width with zeros behind: the walks read every row many times, and loads that go through
+// registers wait for each other (2048 tokens, 8 heads of 101, both passes: 322 us without the copy, 126 at 104).
+struct Packer {
+    PackArgs args{};
+    int64_t es;
+    int width, padded;
+    size_t at = 0;            // bytes of the workspace taken so far
+    char* ws;
+    Packer(int dtype, int w, void* workspace) : es(elem(dtype)), width(w), padded(static_cast<int>((w * es + 15) / 16 * 16 / es)), ws(static_cast<char*>(workspace)) {
+        args.width = width;
+        args.chunks = static_cast<int>(padded * es / 16);
+    }
+    // Puts the copy in place of a tensor that needs one.
+    void operator()(const void*& p, int64_t& ld, int64_t& hs, int64_t rows, int64_t heads) {
+        if (!p || rows == 0 || (width == padded && whole(p, ld, hs, es))) return;
+        PackJob& j = args.job[args.jobs++];
+        j = {p, ws + at, ld, hs, rows * heads, heads, args.total};
+        args.total += j.count * args.chunks;
+        p = ws + at;
+        at += (static_cast<size_t>(j.count) * padded * es + 255) / 256 * 256;
+        ld = heads * padded;
+        hs = padded;
+    }
+};
 
 // 1, or for sequences beyond find_span's orders a stride of about 0.618 units that meets every one of them once (units are odd, so that
 // the stride mixes odd and even ones too).
@@ -1188,29 +1241,73 @@ template <typename F> hipError_t dispatch(int dtype, int width, bool bias, F f) 
 
 }  // namespace
 
-size_t attention_bytes(const muon_attention_args& a) {
-    const int s = forward_splits(a);
-    return s > 1 ? static_cast<size_t>(s) * a.queries * a.heads * (a.width + 2) * sizeof(float) : 0;
+namespace {
+
+template <typename T> hipError_t run_pack_as(PackArgs p, hipStream_t s) {
+    return in_launches((p.total + 255) / 256, [&](int64_t base, unsigned n) {
+        p.base = base * 256;
+        hipLaunchKernelGGL((attention_pack_kernel<T>), dim3(n), dim3(256), 0, s, p);
+        return hipGetLastError();
+    });
+}
+hipError_t run_pack(const Packer& p, int dtype, hipStream_t s) {
+    return dtype == MUON_BF16 ? run_pack_as<uint16_t>(p.args, s) : run_pack_as<float>(p.args, s);
 }
 
-hipError_t launch_attention(const muon_attention_args& a, void* workspace, hipStream_t s) {
-    if (a.queries == 0) return hipSuccess;
+// The forward call with its packed inputs; the workspace: copies, then the splits' sums.
+Packer pack_forward(muon_attention_args& a, void* workspace) {
+    Packer p(a.dtype, a.width, workspace);
+    p(a.q, a.ld_q, a.hs_q, a.queries, a.heads);
+    p(a.k, a.ld_k, a.hs_k, a.keys, a.kv_heads);
+    p(a.v, a.ld_v, a.hs_v, a.keys, a.kv_heads);
+    return p;
+}
+Packer pack_backward(muon_attention_backward_args& b, void* workspace) {
+    Packer p(b.dtype, b.width, workspace);
+    p(b.q, b.ld_q, b.hs_q, b.queries, b.heads);
+    p(b.k, b.ld_k, b.hs_k, b.keys, b.kv_heads);
+    p(b.v, b.ld_v, b.hs_v, b.keys, b.kv_heads);
+    p(b.grad_out, b.ld_grad_out, b.hs_grad_out, b.queries, b.heads);
+    p(b.out, b.ld_out, b.hs_out, b.queries, b.heads);
+    p(b.out_low, b.ld_out_low, b.hs_out_low, b.queries, b.heads);
+    return p;
+}
+
+}  // namespace
+
+size_t attention_bytes(const muon_attention_args& args) {
+    muon_attention_args a = args;
+    const int s = forward_splits(a);
+    return pack_forward(a, nullptr).at + (s > 1 ? static_cast<size_t>(s) * a.queries * a.heads * (a.width + 2) * sizeof(float) : 0);
+}
+
+hipError_t launch_attention(const muon_attention_args& args, void* workspace, hipStream_t s) {
+    if (args.queries == 0) return hipSuccess;
+    muon_attention_args a = args;
+    const Packer pack = pack_forward(a, workspace);
+    const hipError_t e = run_pack(pack, a.dtype, s);
+    if (e != hipSuccess) return e;
     ForwardArgs f{};
     f.c = common_args(a, forward_splits(a));
-    f.c.units = at::span_units(a.queries, a.sequences, AT_ROWS) * a.heads * f.c.splits;
+    f.c.units = f.c.q_axis * a.heads * f.c.splits;
     const int64_t es = elem(a.dtype);
-    const bool w = a.width * es % 16 == 0;
-    f.c.vec_in = w && whole(a.q, a.ld_q, a.hs_q, es) && whole(a.k, a.ld_k, a.hs_k, es) && whole(a.v, a.ld_v, a.hs_v, es);
-    f.c.vec_out = w && whole(a.out, a.ld_out, a.hs_out, es) && (!a.out_low || whole(a.out_low, a.ld_out_low, a.hs_out_low, es));
-    f.part = static_cast<float*>(workspace);
+    f.c.vec_out = a.width * es % 16 == 0 && whole(a.out, a.ld_out, a.hs_out, es) && (!a.out_low || whole(a.out_low, a.ld_out_low, a.hs_out_low, es));
+    f.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + pack.at);
     return dispatch(a.dtype, a.width, a.bias != nullptr, [&](auto t, auto dp, auto bias) {
         return run_forward<decltype(t), decltype(dp)::value, decltype(bias)::value>(f, s);
     });
 }
 
-size_t attention_backward_bytes(const muon_attention_backward_args& a) { return plan_backward(a).bytes; }
+size_t attention_backward_bytes(const muon_attention_backward_args& args) {
+    muon_attention_backward_args b = args;
+    return pack_backward(b, nullptr).at + plan_backward(b).bytes;
+}
 
-hipError_t launch_attention_backward(const muon_attention_backward_args& b, void* workspace, hipStream_t s) {
+hipError_t launch_attention_backward(const muon_attention_backward_args& args, void* workspace, hipStream_t s) {
+    muon_attention_backward_args b = args;
+    const Packer pack = pack_backward(b, workspace);
+    hipError_t e = run_pack(pack, b.dtype, s);
+    if (e != hipSuccess) return e;
     const BackwardPlan p = plan_backward(b);
     muon_attention_args a{};
     a.q = b.q; a.k = b.k; a.v = b.v;
@@ -1226,17 +1323,15 @@ hipError_t launch_attention_backward(const muon_attention_backward_args& b, void
     BackwardArgs f{};
     f.c = common_args(a, 1);
     const int64_t es = elem(a.dtype);
-    const bool w = a.width * es % 16 == 0;
-    f.c.vec_in = w && whole(a.q, a.ld_q, a.hs_q, es) && whole(a.k, a.ld_k, a.hs_k, es) && whole(a.v, a.ld_v, a.hs_v, es) && whole(b.grad_out, b.ld_grad_out, b.hs_grad_out, es) &&
-                 whole(b.out, b.ld_out, b.hs_out, es) && (!b.out_low || whole(b.out_low, b.ld_out_low, b.hs_out_low, es));
-    f.c.vec_out = w && whole(b.grad_q, b.ld_grad_q, b.hs_grad_q, es) && whole(b.grad_k, b.ld_grad_k, b.hs_grad_k, es) && whole(b.grad_v, b.ld_grad_v, b.hs_grad_v, es);
+    f.c.vec_out = a.width * es % 16 == 0 && whole(b.grad_q, b.ld_grad_q, b.hs_grad_q, es) && whole(b.grad_k, b.ld_grad_k, b.hs_grad_k, es) &&
+                  whole(b.grad_v, b.ld_grad_v, b.hs_grad_v, es);
     f.grad_out = b.grad_out;
     f.grad_q = b.grad_q; f.grad_k = b.grad_k; f.grad_v = b.grad_v;
     f.ld_do = b.ld_grad_out; f.hs_do = b.hs_grad_out;
     f.ld_dq = b.ld_grad_q; f.hs_dq = b.hs_grad_q;
     f.ld_dk = b.ld_grad_k; f.hs_dk = b.hs_grad_k;
     f.ld_dv = b.ld_grad_v; f.hs_dv = b.hs_grad_v;
-    char* ws = static_cast<char*>(workspace);
+    char* ws = static_cast<char*>(workspace) + pack.at;
     f.delta = p.all ? nullptr : reinterpret_cast<float*>(ws + p.delta);
     f.bias_part = reinterpret_cast<float*>(ws + p.bias_part);
     f.slots = p.slots;

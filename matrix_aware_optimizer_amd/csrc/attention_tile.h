@@ -178,18 +178,16 @@ template <typename T> __device__ __forceinline__ u32x4_t ld_part(const T* p, int
     return w;
 }
 
-// B operand straight from global memory: values e0 .. e0 + 7 of a row of `width`, zeros behind it.  vec (the same for the whole
-// wave): the row comes in whole 16-byte chunks; a load is then one unconditional access, and a row's loads are all in
-// flight at once, where two ways for a lane to get its register would make each wait for the one before.
-template <typename T> __device__ __forceinline__ Frag<T> global_frag(const T* row, int e0, int width, bool ok, bool vec) {
+// B operand straight from global memory: values e0 .. e0 + 7 of a row of `width`, zeros behind it; rows come in whole 16-byte
+// chunks.  A load is one unconditional access, so a row's loads are all in flight at once.
+template <typename T> __device__ __forceinline__ Frag<T> global_frag(const T* row, int e0, int width, bool ok) {
     Frag<T> f;
     constexpr int N = sizeof(T) / 2, PER = 16 / sizeof(T);
     u32x4_t w[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) {
         const int e = e0 + PER * k;
-        if (vec) w[k] = *(const MUON_GLOBAL u32x4_t*)G(ok && e < width ? static_cast<const void*>(row + e) : static_cast<const void*>(&zero_chunk));
-        else w[k] = ld_part<T>(row + e, ok ? width - e : 0);
+        w[k] = *(const MUON_GLOBAL u32x4_t*)G(ok && e < width ? static_cast<const void*>(row + e) : static_cast<const void*>(&zero_chunk));
     }
     if constexpr (sizeof(T) == 2) f.w = w[0];
     else
@@ -202,30 +200,20 @@ __device__ __forceinline__ float frag_get(const Frag<uint16_t>& f, int e) {
 }
 __device__ __forceinline__ float frag_get(const Frag<float>& f, int e) { return f.w[e >> 2][e & 3]; }
 
-// Loads rows 0 .. ROWS - 1 at `base` (pitch ld) into a tile: rows whose bit of `live` is 0 and columns from `width` on as
-// zeros.  vec: base, ld and width come in whole 16-byte chunks; then the loads go straight into LDS and are under way when
-// this returns (vmcnt), otherwise they pass through registers.
+// Loads rows 0 .. ROWS - 1 at `base` (pitch ld), in whole 16-byte chunks, into a tile: rows whose bit of `live` is 0 and columns
+// from `width` on as zeros.  The loads go straight into LDS and are under way when this returns (vmcnt).
 template <typename T, int DP, int ROWS, int THREADS>
-__device__ __forceinline__ void load_tile(lds_byte_t* tile, const T* base, int64_t ld, int width, uint64_t live, bool vec) {
+__device__ __forceinline__ void load_tile(lds_byte_t* tile, const T* base, int64_t ld, int width, uint64_t live) {
     typedef Row<T, DP> R;
     constexpr int N = ROWS * R::CH / THREADS;
     static_assert(N * THREADS == ROWS * R::CH && THREADS % R::CH == 0, "whole passes of whole rows");
     const int tid = threadIdx.x, wave = wave_id();
-    if (vec) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int row = (i * THREADS + tid) / R::CH, e0 = ((tid % R::CH) ^ R::swizzle(row)) * R::PER;
-            const bool ok = ((live >> row) & 1) && e0 < width;
-            const void* src = ok ? static_cast<const void*>(base + row * ld + e0) : static_cast<const void*>(&zero_chunk);
-            __builtin_amdgcn_global_load_lds(src, (lds_ptr_t)(tile + (i * THREADS + wave * 64) * 16), 16, 0, 0);
-        }
-    } else {
-#pragma unroll 2
-        for (int i = 0; i < N; ++i) {
-            const int row = (i * THREADS + tid) / R::CH, e0 = ((tid % R::CH) ^ R::swizzle(row)) * R::PER;
-            const u32x4_t w = ld_part<T>(base + row * ld + e0, ((live >> row) & 1) ? width - e0 : 0);
-            *(lds_u32x4_t*)(tile + (i * THREADS + tid) * 16) = w;
-        }
+    for (int i = 0; i < N; ++i) {
+        const int row = (i * THREADS + tid) / R::CH, e0 = ((tid % R::CH) ^ R::swizzle(row)) * R::PER;
+        const bool ok = ((live >> row) & 1) && e0 < width;
+        const void* src = ok ? static_cast<const void*>(base + row * ld + e0) : static_cast<const void*>(&zero_chunk);
+        __builtin_amdgcn_global_load_lds(src, (lds_ptr_t)(tile + (i * THREADS + wave * 64) * 16), 16, 0, 0);
     }
 }
 
