@@ -42,7 +42,6 @@ struct Common {
     int64_t units;        // of the whole call: units of an axis x heads x splits
     int64_t q_axis, q_stride, k_axis, k_stride;   // units of the two axes, and the stride through them
     int splits;
-    int vec_out;          // the outputs' rows come in whole 16-byte chunks; the inputs' always do (packed first where they do not)
     int window;           // 0: none
     int gqa;              // heads / kv_heads
 };
@@ -353,7 +352,7 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 ? 2 : 1) void attention_
         const int64_t at = row * a.heads + head, n = a.queries * a.heads;
         float* o_part = f.part + (split * n + at) * a.width;
         float* ml = f.part + c.splits * n * a.width + (split * n + at) * 2;
-        store_rows<float>(o, 1.0f, o_part, static_cast<float*>(nullptr), a.width, a.width % 4 == 0);
+        store_rows<float>(o, 1.0f, o_part, static_cast<float*>(nullptr), a.width);
         if (lane < 32) {
             G(ml)[0] = m;
             G(ml)[1] = l;
@@ -362,7 +361,7 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 ? 2 : 1) void attention_
     }
     T* out = static_cast<T*>(a.out) + row * a.ld_out + static_cast<int64_t>(head) * a.hs_out;
     T* low = a.out_low ? static_cast<T*>(a.out_low) + row * a.ld_out_low + static_cast<int64_t>(head) * a.hs_out_low : nullptr;
-    store_rows<T>(o, l == 0.0f ? 0.0f : 1.0f / l, out, low, a.width, c.vec_out);
+    store_rows<T>(o, l == 0.0f ? 0.0f : 1.0f / l, out, low, a.width);
     if (lane < 32) G(a.lse)[row * a.heads + head] = l == 0.0f ? NEG_INF : (BIAS ? m : m * LN2) + __logf(l);
 }
 
@@ -639,10 +638,10 @@ template <typename T, int DP, bool BIAS> __device__ __forceinline__ void grad_q_
     if (place >= sp.len) return;
     if (f.q_splits > 1) {
         const int64_t at = row * a.heads + head, n = a.queries * a.heads;
-        store_rows<float>(o, 1.0f, f.q_part + (split * n + at) * a.width, static_cast<float*>(nullptr), a.width, a.width % 4 == 0);
+        store_rows<float>(o, 1.0f, f.q_part + (split * n + at) * a.width, static_cast<float*>(nullptr), a.width);
         return;
     }
-    store_rows<T>(o, a.scale, static_cast<T*>(f.grad_q) + row * f.ld_dq + static_cast<int64_t>(head) * f.hs_dq, static_cast<T*>(nullptr), a.width, c.vec_out);
+    store_rows<T>(o, a.scale, static_cast<T*>(f.grad_q) + row * f.ld_dq + static_cast<int64_t>(head) * f.hs_dq, static_cast<T*>(nullptr), a.width);
 }
 
 template <typename T, int DP, bool BIAS>
@@ -881,12 +880,12 @@ __device__ __forceinline__ void grad_kv_block(const BackwardArgs& f, int64_t blo
     if (f.kv_splits > 1) {
         const int64_t at = row * a.kv_heads + kv, total = a.keys * a.kv_heads;
         float* p = f.kv_part + (2 * split * total + at) * a.width;
-        store_rows<float>(dk, 1.0f, p, static_cast<float*>(nullptr), a.width, a.width % 4 == 0);
-        store_rows<float>(dv, 1.0f, p + total * a.width, static_cast<float*>(nullptr), a.width, a.width % 4 == 0);
+        store_rows<float>(dk, 1.0f, p, static_cast<float*>(nullptr), a.width);
+        store_rows<float>(dv, 1.0f, p + total * a.width, static_cast<float*>(nullptr), a.width);
         return;
     }
-    store_rows<T>(dk, a.scale, static_cast<T*>(f.grad_k) + row * f.ld_dk + static_cast<int64_t>(kv) * f.hs_dk, static_cast<T*>(nullptr), a.width, c.vec_out);
-    store_rows<T>(dv, 1.0f, static_cast<T*>(f.grad_v) + row * f.ld_dv + static_cast<int64_t>(kv) * f.hs_dv, static_cast<T*>(nullptr), a.width, c.vec_out);
+    store_rows<T>(dk, a.scale, static_cast<T*>(f.grad_k) + row * f.ld_dk + static_cast<int64_t>(kv) * f.hs_dk, static_cast<T*>(nullptr), a.width);
+    store_rows<T>(dv, 1.0f, static_cast<T*>(f.grad_v) + row * f.ld_dv + static_cast<int64_t>(kv) * f.hs_dv, static_cast<T*>(nullptr), a.width);
 }
 
 template <typename T, int DP, bool BIAS>
@@ -1290,8 +1289,6 @@ hipError_t launch_attention(const muon_attention_args& args, void* workspace, hi
     ForwardArgs f{};
     f.c = common_args(a, forward_splits(a));
     f.c.units = f.c.q_axis * a.heads * f.c.splits;
-    const int64_t es = elem(a.dtype);
-    f.c.vec_out = a.width * es % 16 == 0 && whole(a.out, a.ld_out, a.hs_out, es) && (!a.out_low || whole(a.out_low, a.ld_out_low, a.hs_out_low, es));
     f.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + pack.at);
     return dispatch(a.dtype, a.width, a.bias != nullptr, [&](auto t, auto dp, auto bias) {
         return run_forward<decltype(t), decltype(dp)::value, decltype(bias)::value>(f, s);
@@ -1322,9 +1319,6 @@ hipError_t launch_attention_backward(const muon_attention_backward_args& args, v
     a.buckets = b.buckets; a.reach = b.reach; a.causal = b.causal; a.dtype = b.dtype;
     BackwardArgs f{};
     f.c = common_args(a, 1);
-    const int64_t es = elem(a.dtype);
-    f.c.vec_out = a.width * es % 16 == 0 && whole(b.grad_q, b.ld_grad_q, b.hs_grad_q, es) && whole(b.grad_k, b.ld_grad_k, b.hs_grad_k, es) &&
-                  whole(b.grad_v, b.ld_grad_v, b.hs_grad_v, es);
     f.grad_out = b.grad_out;
     f.grad_q = b.grad_q; f.grad_k = b.grad_k; f.grad_v = b.grad_v;
     f.ld_do = b.ld_grad_out; f.hs_do = b.hs_grad_out;

@@ -221,8 +221,9 @@ __device__ __forceinline__ void load_tile(lds_byte_t* tile, const T* base, int64
 __device__ __forceinline__ void tile_barrier() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 // C (rows: width, column: this lane's row of the output) times f, to row pointer `out` of type T and, where wanted, what
-// rounding took to `low`.
-template <typename T, int NB> __device__ __forceinline__ void store_rows(const f32x16_t (&c)[NB], float f, T* out, T* low, int width, bool vec) {
+// rounding took to `low`.  Four values at once at any alignment, the last ones of an odd width one by one.
+typedef u32x2_t u32x2_el2 __attribute__((aligned(2)));
+template <typename T, int NB> __device__ __forceinline__ void store_rows(const f32x16_t (&c)[NB], float f, T* out, T* low, int width) {
     const int h = (threadIdx.x & 63) >> 5;
 #pragma unroll
     for (int b = 0; b < NB; ++b)
@@ -230,23 +231,22 @@ template <typename T, int NB> __device__ __forceinline__ void store_rows(const f
         for (int q = 0; q < 4; ++q) {
             const int d = 32 * b + 8 * q + 4 * h;
             const float v[4] = {c[b][4 * q] * f, c[b][4 * q + 1] * f, c[b][4 * q + 2] * f, c[b][4 * q + 3] * f};
-            if (vec) {
-                if (d >= width) continue;
+            if (d + 4 <= width) {
                 if constexpr (sizeof(T) == 2) {
                     const u32x2_t w = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-                    *(MUON_GLOBAL u32x2_t*)G(out + d) = w;
+                    *(MUON_GLOBAL u32x2_el2*)G(out + d) = w;
                     if (low) {
                         const u32x2_t l = {pack_bf16x2(v[0] - __uint_as_float(w.x << 16), v[1] - __uint_as_float(w.x & 0xffff0000u)),
                                            pack_bf16x2(v[2] - __uint_as_float(w.y << 16), v[3] - __uint_as_float(w.y & 0xffff0000u))};
-                        *(MUON_GLOBAL u32x2_t*)G(low + d) = l;
+                        *(MUON_GLOBAL u32x2_el2*)G(low + d) = l;
                     }
                 } else {
-                    *(MUON_GLOBAL f32x4_t*)G(out + d) = f32x4_t{v[0], v[1], v[2], v[3]};
-                    if (low) *(MUON_GLOBAL f32x4_t*)G(low + d) = f32x4_t{};
+                    *(MUON_GLOBAL f32x4_el4*)G(out + d) = f32x4_t{v[0], v[1], v[2], v[3]};
+                    if (low) *(MUON_GLOBAL f32x4_el4*)G(low + d) = f32x4_t{};
                 }
             } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
+                for (int e = 0; e < 3; ++e)
                     if (d + e < width) {
                         st_el<T>(out, d + e, v[e]);
                         if (low) st_el<T>(low, d + e, sizeof(T) == 2 ? v[e] - bf16_to_f32(f32_to_bf16(v[e])) : 0.0f);
