@@ -22,7 +22,7 @@ namespace {
 
 using namespace at;
 
-constexpr int AT_THREADS = 256, AT_WAVES = 4, AT_ROWS = 128;   // rows (queries or keys) a workgroup
+constexpr int AT_THREADS = 256, AT_WAVES = 4, AT_SHIFT = 7, AT_ROWS = 1 << AT_SHIFT;   // rows (queries or keys) a workgroup
 constexpr int AT_MAX_SPLITS = 64;
 constexpr int AT_FINISH = 1024;                                 // threads of the sums' workgroups
 constexpr int64_t AT_CUS = 256;
@@ -44,6 +44,7 @@ struct Common {
     int splits;
     int window;           // 0: none
     int gqa;              // heads / kv_heads
+    int pack;             // the heads of a workgroup's rows: 2^pack heads that share a key head, row by row for each query (forward)
 };
 struct ForwardArgs {
     Common c;
@@ -141,17 +142,17 @@ template <typename T, int DP> struct KeyWalk {
     static constexpr int WIN = AT_ROWS + BN;          // distances between 128 queries and a tile of keys (one to spare)
     const muon_attention_args& a;
     Span sp;
-    int head, wave_at;                                // this wave's first query in its sequence
+    int head, pack, wave_at;                          // (first) head, this wave's first query in its sequence
     int off;                                          // key position of query 0
     int first, last;                                  // tiles
     const T* kbase;
     const T* vbase;
     uint64_t pending;
 
-    __device__ __forceinline__ KeyWalk(const Common& c, const Span& s, int h, int split, int splits) : a(c.a), sp(s), head(h) {
-        wave_at = sp.at + 32 * wave_id();
+    __device__ __forceinline__ KeyWalk(const Common& c, const Span& s, int h, int split, int splits, int p) : a(c.a), sp(s), head(h), pack(p) {
+        wave_at = sp.at + (32 * wave_id() >> pack);
         off = sp.other_len - sp.len;
-        const int a0 = sp.at + off, a1 = sp.at + min(sp.rows, AT_ROWS) - 1 + off;
+        const int a0 = sp.at + off, a1 = sp.at + min(sp.rows, AT_ROWS >> pack) - 1 + off;
         int lo = 0, hi = sp.other_len;
         if (a.causal) hi = min(hi, a1 + 1);
         if (c.window) { lo = max(lo, a0 - c.window + 1); hi = min(hi, a1 + c.window); }
@@ -184,7 +185,7 @@ template <typename T, int DP> struct KeyWalk {
     }
     // Scores of tile t (raw products) with what the wave sees of it; false if nothing.
     __device__ __forceinline__ int seen(const Common& c, int t, uint64_t live) const {
-        const int j0 = t * BN, a0 = wave_at + off, a1 = a0 + 31;
+        const int j0 = t * BN, a0 = wave_at + off, a1 = a0 + (31 >> pack);
         constexpr uint64_t full = BN == 64 ? ~0ull : (1ull << (BN & 63)) - 1;
         const int s = wave_at >= sp.len ? NOTHING : tile_sight(a0, a1, j0, j0 + BN - 1, a.causal, c.window);
         return s == ALL && live != full ? SOME : s;
@@ -223,11 +224,12 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 ? 2 : 1) void attention_
     const Common& c = f.c;
     const muon_attention_args& a = c.a;
     int u, head, split;
-    decode(c.unit0 + blockIdx.x, a.heads, c.splits, c.q_axis, c.q_stride, u, head, split);
+    decode(c.unit0 + blockIdx.x, a.heads >> c.pack, c.splits, c.q_axis, c.q_stride, u, head, split);
+    head <<= c.pack;
     Span sp;
-    if (!find_span<AT_ROWS, false>(a.offsets, a.key_offsets, static_cast<int>(a.sequences), static_cast<int>(a.queries), static_cast<int>(a.keys), a.causal, u, sp)) return;
-    const W w(c, sp, head, split, c.splits);
-    const int lane = threadIdx.x & 63, place = w.wave_at + (lane & 31);
+    if (!find_span<false>(AT_SHIFT - c.pack, a.offsets, a.key_offsets, static_cast<int>(a.sequences), static_cast<int>(a.queries), static_cast<int>(a.keys), a.causal, u, sp)) return;
+    const W w(c, sp, head, split, c.splits, c.pack);
+    const int lane = threadIdx.x & 63, place = w.wave_at + ((lane & 31) >> c.pack), own = head + (lane & ((1 << c.pack) - 1));   // this lane's query and head
     const bool row_ok = place < sp.len;
     const int64_t row = sp.start - sp.at + place;
     const Sight sight = w.sight(c, place);
@@ -237,7 +239,7 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 ? 2 : 1) void attention_
 
     Frag<T> qf[KS];
     {
-        const T* q = static_cast<const T*>(a.q) + row * a.ld_q + static_cast<int64_t>(head) * a.hs_q;
+        const T* q = static_cast<const T*>(a.q) + row * a.ld_q + static_cast<int64_t>(own) * a.hs_q;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
             qf[ks] = global_frag<T>(q, 16 * ks + 8 * (lane >> 5), a.width, row_ok && a.scale != 0.0f);
@@ -349,7 +351,7 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 ? 2 : 1) void attention_
     l = half_sum(l);
     if (!row_ok) return;
     if (c.splits > 1) {
-        const int64_t at = row * a.heads + head, n = a.queries * a.heads;
+        const int64_t at = row * a.heads + own, n = a.queries * a.heads;
         float* o_part = f.part + (split * n + at) * a.width;
         float* ml = f.part + c.splits * n * a.width + (split * n + at) * 2;
         store_rows<float>(o, 1.0f, o_part, static_cast<float*>(nullptr), a.width);
@@ -359,10 +361,10 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 ? 2 : 1) void attention_
         }
         return;
     }
-    T* out = static_cast<T*>(a.out) + row * a.ld_out + static_cast<int64_t>(head) * a.hs_out;
-    T* low = a.out_low ? static_cast<T*>(a.out_low) + row * a.ld_out_low + static_cast<int64_t>(head) * a.hs_out_low : nullptr;
+    T* out = static_cast<T*>(a.out) + row * a.ld_out + static_cast<int64_t>(own) * a.hs_out;
+    T* low = a.out_low ? static_cast<T*>(a.out_low) + row * a.ld_out_low + static_cast<int64_t>(own) * a.hs_out_low : nullptr;
     store_rows<T>(o, l == 0.0f ? 0.0f : 1.0f / l, out, low, a.width);
-    if (lane < 32) G(a.lse)[row * a.heads + head] = l == 0.0f ? NEG_INF : (BIAS ? m : m * LN2) + __logf(l);
+    if (lane < 32) G(a.lse)[row * a.heads + own] = l == 0.0f ? NEG_INF : (BIAS ? m : m * LN2) + __logf(l);
 }
 
 // Joins the splits of a row: a wave each.
@@ -505,11 +507,11 @@ template <typename T, int DP, bool BIAS> __device__ __forceinline__ void grad_q_
         sums.start(wbuf + 2 * W::WIN + BiasSums::ROOM * wave_id(), f.bias_part + slot * (2 * a.reach + 1), a.reach);
     }
     Span sp;
-    if (!find_span<AT_ROWS, false>(a.offsets, a.key_offsets, static_cast<int>(a.sequences), static_cast<int>(a.queries), static_cast<int>(a.keys), a.causal, u, sp)) {
+    if (!find_span<false>(AT_SHIFT, a.offsets, a.key_offsets, static_cast<int>(a.sequences), static_cast<int>(a.queries), static_cast<int>(a.keys), a.causal, u, sp)) {
         if constexpr (BIAS) sums.finish();
         return;
     }
-    const W w(c, sp, head, split, f.q_splits);
+    const W w(c, sp, head, split, f.q_splits, 0);
     const int lane = threadIdx.x & 63, place = w.wave_at + (lane & 31);
     const int64_t row = sp.start - sp.at + place;
     const Sight sight = w.sight(c, place);
@@ -678,7 +680,7 @@ __device__ __forceinline__ void grad_kv_block(const BackwardArgs& f, int64_t blo
     int u, kv, split;
     decode(block, a.kv_heads, f.kv_splits, c.k_axis, c.k_stride, u, kv, split);
     Span sp;
-    if (!find_span<AT_ROWS, true>(a.key_offsets, a.offsets, static_cast<int>(a.sequences), static_cast<int>(a.keys), static_cast<int>(a.queries), a.causal, u, sp)) return;
+    if (!find_span<true>(AT_SHIFT, a.key_offsets, a.offsets, static_cast<int>(a.sequences), static_cast<int>(a.keys), static_cast<int>(a.queries), a.causal, u, sp)) return;
     const int lane = threadIdx.x & 63, wave = wave_id(), h = lane >> 5;
     const int wave_at = sp.at + 32 * wave, place = wave_at + (lane & 31), nq = sp.other_len, off = sp.len - nq;
     const int64_t row = sp.start - sp.at + place;
@@ -1045,9 +1047,11 @@ template <typename T> __global__ __launch_bounds__(256) void attention_pack_kern
 // more than four (a join costs as much as one).  Under a causal
 // mask walks so long that a part keeps 64 tiles are split until there are eight workgroups a CU, so that the longest do not end alone
 // (16384 tokens, 4 key heads, grad_k and grad_v: 5.8 ms in one part).
-int64_t axis_units(int64_t rows, int64_t sequences, int heads) { return std::max<int64_t>(1, (rows / AT_ROWS + sequences) * heads); }
-int plan_splits(int64_t rows, int64_t sequences, int heads, int64_t walk, int tile, int dtype, bool causal, int64_t target) {
-    const int64_t n = axis_units(rows, sequences, heads), tiles = std::max<int64_t>(1, walk / sequences / tile);
+int64_t axis_units(int64_t rows, int64_t sequences, int heads, int pack = 0) {
+    return std::max<int64_t>(1, ((rows >> (AT_SHIFT - pack)) + sequences) * (heads >> pack));
+}
+int plan_splits(int64_t rows, int64_t sequences, int heads, int64_t walk, int tile, int dtype, bool causal, int64_t target, int pack = 0) {
+    const int64_t n = axis_units(rows, sequences, heads, pack), tiles = std::max<int64_t>(1, walk / sequences / tile);
     const int64_t want = std::max(std::min((target + n / 2) / n, dtype == MUON_F32 && tiles > 4 ? tiles : tiles / 2), causal ? std::min(2048 / n, tiles / 64) : 0);
     return static_cast<int>(std::min<int64_t>(std::max<int64_t>(1, want), AT_MAX_SPLITS));
 }
@@ -1055,8 +1059,16 @@ int tile_rows(int dtype) { return dtype == MUON_BF16 ? walk_rows<uint16_t>() : w
 // Workgroups at once: two a CU, but one where fp32 takes all registers.
 int64_t at_once(int dtype, int width) { return dtype == MUON_F32 && width > 64 ? AT_CUS : 2 * AT_CUS; }
 
+// Sequences of fewer queries than a workgroup has rows: heads that share a key head fill them (a bias is one head's), so that
+// keys are read once for all of them (one query over 4096 keys, 4 heads each of 4 key heads: 14.2 us with a workgroup a head).
+int forward_pack(const muon_attention_args& a) {
+    int pack = 0;
+    if (!a.bias && a.queries / a.sequences < AT_ROWS)
+        while (pack < 5 && (a.heads / a.kv_heads) % (2 << pack) == 0) ++pack;
+    return pack;
+}
 int forward_splits(const muon_attention_args& a) {
-    return plan_splits(a.queries, a.sequences, a.heads, a.keys, tile_rows(a.dtype), a.dtype, a.causal, at_once(a.dtype, a.width));
+    return plan_splits(a.queries, a.sequences, a.heads, a.keys, tile_rows(a.dtype), a.dtype, a.causal, at_once(a.dtype, a.width), forward_pack(a));
 }
 struct BackwardPlan {
     int q_splits, kv_splits;
@@ -1138,10 +1150,11 @@ int64_t unit_stride(int64_t units, int64_t sequences) {
     return k;
 }
 
-Common common_args(const muon_attention_args& a, int splits) {
+Common common_args(const muon_attention_args& a, int splits, int pack) {
     Common c{};
     c.a = a;
-    c.q_axis = span_units(a.queries, a.sequences, AT_ROWS);
+    c.pack = pack;
+    c.q_axis = span_units(a.queries, a.sequences, AT_ROWS >> pack);
     c.k_axis = span_units(a.keys, a.sequences, AT_ROWS);
     c.q_stride = unit_stride(c.q_axis, a.sequences);
     c.k_stride = unit_stride(c.k_axis, a.sequences);
@@ -1287,8 +1300,8 @@ hipError_t launch_attention(const muon_attention_args& args, void* workspace, hi
     const hipError_t e = run_pack(pack, a.dtype, s);
     if (e != hipSuccess) return e;
     ForwardArgs f{};
-    f.c = common_args(a, forward_splits(a));
-    f.c.units = f.c.q_axis * a.heads * f.c.splits;
+    f.c = common_args(a, forward_splits(a), forward_pack(a));
+    f.c.units = f.c.q_axis * (a.heads >> f.c.pack) * f.c.splits;
     f.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + pack.at);
     return dispatch(a.dtype, a.width, a.bias != nullptr, [&](auto t, auto dp, auto bias) {
         return run_forward<decltype(t), decltype(dp)::value, decltype(bias)::value>(f, s);
@@ -1318,7 +1331,7 @@ hipError_t launch_attention_backward(const muon_attention_backward_args& args, v
     a.heads = b.heads; a.kv_heads = b.kv_heads; a.width = b.width;
     a.buckets = b.buckets; a.reach = b.reach; a.causal = b.causal; a.dtype = b.dtype;
     BackwardArgs f{};
-    f.c = common_args(a, 1);
+    f.c = common_args(a, 1, 0);
     f.grad_out = b.grad_out;
     f.grad_q = b.grad_q; f.grad_k = b.grad_k; f.grad_v = b.grad_v;
     f.ld_do = b.ld_grad_out; f.hs_do = b.hs_grad_out;

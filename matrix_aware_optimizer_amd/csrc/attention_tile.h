@@ -280,15 +280,15 @@ __device__ __forceinline__ int bound(const int64_t* offsets, int sequences, int 
     const int64_t v = G(offsets)[s - 1];
     return static_cast<int>(v < 0 ? 0 : v > rows ? rows : v);
 }
-// HEAD: the first rows of a sequence walk the longest (keys), else the last (queries).
-template <int BM, bool HEAD>
-__device__ __forceinline__ bool find_span(const int64_t* offsets, const int64_t* others, int sequences, int rows, int other_rows, bool causal, int u, Span& sp) {
+// HEAD: the first rows of a sequence walk the longest (keys), else the last (queries).  BM = 2^shift.
+template <bool HEAD>
+__device__ __forceinline__ bool find_span(int shift, const int64_t* offsets, const int64_t* others, int sequences, int rows, int other_rows, bool causal, int u, Span& sp) {
     const int lane = threadIdx.x & 63;
     int s, b0, o0, o1, j;
     if (sequences <= SPAN_LANES) {
         // every bound of both axes at once, one trip to memory
         const int mine = bound(offsets, sequences, rows, lane), other = bound(others, sequences, other_rows, lane);
-        const int len = __shfl(mine, lane + 1) - mine, units = lane <= sequences + 1 && len > 0 ? (len + BM - 1) / BM : 0;
+        const int len = __shfl(mine, lane + 1) - mine, units = lane <= sequences + 1 && len > 0 ? ((len - 1) >> shift) + 1 : 0;
         auto ranked = [&](int r) { return static_cast<int>(wave_sum(static_cast<float>(units > r ? units - r : 0))); };     // below 2^24
         if (u >= ranked(0)) return false;
         if (causal) {
@@ -332,7 +332,7 @@ __device__ __forceinline__ bool find_span(const int64_t* offsets, const int64_t*
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int at = c + 63 * k + lane, len = __shfl(mine[k], lane + 1) - mine[k];
-                const int units = lane < 63 && at <= sequences + 1 && len > 0 ? (len + BM - 1) / BM : 0;
+                const int units = lane < 63 && at <= sequences + 1 && len > 0 ? ((len - 1) >> shift) + 1 : 0;
                 const int total = static_cast<int>(wave_sum(static_cast<float>(units)));
                 if (!found && u < base + total) {
                     found = true;
@@ -360,7 +360,7 @@ __device__ __forceinline__ bool find_span(const int64_t* offsets, const int64_t*
         while (hi > lo) {
             const int step = (hi - lo + 63) / 64;
             const int64_t at = lo + static_cast<int64_t>(lane + 1) * step;
-            const bool below = at <= hi && bound(offsets, sequences, rows, static_cast<int>(at)) / BM + at <= u;
+            const bool below = at <= hi && (bound(offsets, sequences, rows, static_cast<int>(at)) >> shift) + at <= u;
             const int n = __popcll(__ballot(below));
             lo += n * step;
             hi = hi < lo + step - 1 ? hi : lo + step - 1;
@@ -370,10 +370,10 @@ __device__ __forceinline__ bool find_span(const int64_t* offsets, const int64_t*
         sp.len = bound(offsets, sequences, rows, s + 1) - b0;
         o0 = bound(others, sequences, other_rows, s);
         o1 = bound(others, sequences, other_rows, s + 1);
-        j = u - (b0 / BM + s);
-        if (j < 0 || sp.len <= 0 || static_cast<int64_t>(j) * BM >= sp.len) return false;
+        j = u - ((b0 >> shift) + s);
+        if (j < 0 || sp.len <= 0 || (static_cast<int64_t>(j) << shift) >= sp.len) return false;
     }
-    sp.at = j * BM;
+    sp.at = j << shift;
     sp.start = b0 + sp.at;
     sp.rows = sp.len - sp.at;
     sp.other = 0;
