@@ -188,6 +188,44 @@ def test_attention(gpu_lib, shape, dtype):
     _check(c, _run(gpu_lib, c, t), val)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", [
+    dict(nq=[1], nk=[900], heads=8, kv=2, causal=True), dict(nq=[3, 1, 0, 5], nk=[40, 1, 7, 300], heads=32, kv=1, width=40, causal=True),
+    dict(nq=[7], nk=[200], heads=64, kv=1, width=16, window=30), dict(nq=[100, 20], heads=12, kv=3, masked=0.3), dict(nq=[9], nk=[4], heads=8, kv=4, causal=True),
+    dict(nq=[70, 5], nk=[90, 66], heads=4, kv=1, width=101, causal=True, scale=-0.1),
+], ids=lambda s: f"{s['heads']}of{s['kv']}")
+def test_heads_that_share_a_workgroups_rows(gpu_lib, shape, dtype):
+    c = _case(dtype=dtype, **shape)
+    t, val = _make(c)
+    _check(c, _run(gpu_lib, c, t), val)
+
+
+@pytest.mark.parametrize("count", [61, 62, 300, 512, 513, 2000])
+def test_many_sequences(gpu_lib, count):
+    # by lane up to 61, in order up to 512, by a stride beyond; lengths from nothing to more than a workgroup's rows
+    r = np.random.default_rng(count)
+    nq = [int(v) for v in r.integers(0, 5, count)]
+    nq[count // 3], nq[count // 2], nq[-1] = 150, 300, 129
+    nk = [n + int(v) for n, v in zip(nq, r.integers(0, 4, count))]
+    c = _case(nq=nq, nk=nk, heads=1, kv=1, width=16, dtype="f32", causal=bool(count % 2), before=2, after=140)
+    t, val = _make(c)
+    _check(c, _run(gpu_lib, c, t), val)
+
+
+def test_a_workspace_for_other_layouts_is_refused(gpu_lib):
+    import torch
+    c = _case(nq=[200], causal=True)
+    t, _ = _make(c)
+    ws = torch.empty(gpu_lib.muon_attention_workspace_bytes(t["q"], t["k"]), dtype=torch.uint8, device="cuda")
+    odd = torch.zeros(200 * 128 + 1, dtype=torch.bfloat16, device="cuda")[1:].view(200, 2, 64)
+    out, lse = torch.empty_like(t["q"]), torch.empty(200, 2, device="cuda")
+    with pytest.raises(gpu_lib.MuonError, match="needed"):
+        gpu_lib.muon_attention(t["q"], t["k"], odd, out, lse, workspace=ws)
+    gpu_lib.muon_attention(t["q"], t["k"], odd, out, lse)
+    assert gpu_lib.muon_attention_workspace_bytes(odd, odd) >= 3 * 200 * 128 * 2           # a copy of each of q, k and v
+    torch.cuda.synchronize()
+
+
 def test_one_sequence_without_offsets(gpu_lib):
     for c in (_case(nq=[90], causal=True), _case(nq=[20], nk=[90], causal=True, dtype="f32")):
         t, val = _make(c)
