@@ -317,10 +317,10 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 ? 2 : 1) void attention_
                 for (int i = 0; i < 16; ++i) top = fmaxf(top, s[nb][i]);
             top = half_max(top);
             if constexpr (!BIAS) top *= unit;
-            // The reference follows the maximum only when it has grown by more than 2^8: the terms stay below 2^8, and
-            // most tiles need no rescale.
-            if (__any(top > m + slack)) {
-                const float r = top > m + slack ? top : m;
+            // The reference goes 2^8 above the maximum and moves only when that passes it: the terms stay at or below 1, and most
+            // tiles need no rescale.
+            if (__any(top > m)) {
+                const float r = top > m ? top + slack : m;
                 const float f2 = r == m ? 1.0f : exp2_((m - r) * (BIAS ? LOG2E : 1.0f));
                 m = r;
                 l *= f2;
@@ -462,9 +462,12 @@ struct BiasSums {
         lds_float_t* p = room + 64 * q + 31 - q + 4 * (lane >> 5);
 #pragma unroll
         for (int i = 0; i < 16; ++i) p[8 * (i >> 2) + (i & 3)] = dz[i];
+        // a wave's LDS accesses come in order; the compiler has to leave them so, since lanes read what others wrote
+        asm volatile("" ::: "memory");
         float v[4] = {};
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i & 3] += room[64 * i + lane];
+        asm volatile("" ::: "memory");
         const float sum = (v[0] + v[1]) + (v[2] + v[3]) + carry;
         flush(sum);
         const float up = __shfl_xor(sum, 32);

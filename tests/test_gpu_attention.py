@@ -212,6 +212,22 @@ def test_many_sequences(gpu_lib, count):
     _check(c, _run(gpu_lib, c, t), val)
 
 
+def test_more_units_than_a_launch_holds(gpu_lib):
+    # 2.2 million sequences, nearly all empty: more workgroups than the 2^21 of one launch
+    import torch
+    c = _case(nq=[90, 40], heads=1, kv=1, width=16, dtype="f32", causal=True)
+    t, val = _make(c)
+    want = _run(gpu_lib, c, t)
+    off = torch.full((2_200_001,), 130, dtype=torch.int64, device="cuda")
+    off[:5] = 0
+    off[5:2_199_000] = 90
+    got = _run(gpu_lib, c, {**t, "off": off, "koff": off})
+    # the walks are the same; the split of few units is not, so the sums may be taken in another order
+    ref = _reference(c, val)
+    _check(c, got, val, ref)
+    _check(c, want, val, ref)
+
+
 def test_a_workspace_for_other_layouts_is_refused(gpu_lib):
     import torch
     c = _case(nq=[200], causal=True)

@@ -177,3 +177,33 @@ def test_another_stream_and_a_graph(gpu_lib, shape):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(want[k], got[k]) for k in want)
+
+
+def test_more_choices_than_a_launch_has_waves(gpu_lib):
+    import torch
+    tokens, chosen, experts = 8_500_000, 2, 300
+    ids = torch.randint(-1, experts, (tokens, chosen), device="cuda", generator=torch.Generator("cuda").manual_seed(3))
+    x = torch.arange(tokens, device="cuda").float()[:, None] % 1021
+    n = tokens * chosen
+    y = torch.arange(n, device="cuda").float()[:, None] % 509
+    s, gy, slots = torch.full_like(y, NAN), torch.full_like(y, NAN), torch.zeros((tokens, chosen), dtype=torch.int32, device="cuda")
+    off, w = torch.zeros(experts + 1, dtype=torch.int64, device="cuda"), torch.rand((tokens, chosen), device="cuda")
+    gw, out, gx = torch.full_like(w, NAN), torch.full_like(x, NAN), torch.full_like(x, NAN)
+    gpu_lib.muon_expert_sort(x, ids, s, slots, off)
+    gpu_lib.muon_expert_combine(y, slots, w, out)
+    gpu_lib.muon_expert_combine_backward(x, y, slots, w, off, gy, gw)
+    gpu_lib.muon_expert_sort_backward(y, slots, gx)
+    key = torch.where(ids < 0, experts, ids).reshape(-1)
+    order = torch.sort(key, stable=True).indices
+    count = int((key < experts).sum())
+    assert off.tolist() == torch.searchsorted(key[order], torch.arange(experts + 1, device="cuda")).tolist()
+    place = torch.empty_like(order)
+    place[order] = torch.arange(n, device="cuda")
+    assert torch.equal(slots.reshape(-1).long(), torch.where(key < experts, place, -1))
+    assert torch.equal(s[:count], x[order[:count] // chosen]) and not s[count:].any()
+    live = (slots >= 0)
+    picked = torch.where(live, y[slots.clamp(min=0).long(), 0], 0.0)
+    assert torch.equal(gw, torch.where(live, x * picked, 0.0))             # one product each
+    assert torch.equal(gy[:count, 0], (w * x).reshape(-1)[order[:count]]) and not gy[count:].any()
+    assert torch.equal(gx, picked.sum(1, keepdim=True))                    # whole numbers
+    assert ((out[:, 0] - (picked.double() * w).sum(1)).abs() <= 3 * U * (picked.double() * w).sum(1) + 1e-30).all()
