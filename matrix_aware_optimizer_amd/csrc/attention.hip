@@ -1084,9 +1084,11 @@ struct BackwardPlan {
 BackwardPlan plan_backward(const muon_attention_backward_args& a) {
     BackwardPlan p{};
     const int64_t qu = axis_units(a.queries, a.sequences, a.heads), ku = axis_units(a.keys, a.sequences, a.kv_heads);
-    // As long as both find room on the chip at once, one launch takes as long as the longer of two: 8 heads of 77 tokens 19 us, 16 and
-    // 12 in two.  Its room goes to them by their products, 3 and 4.
-    p.all = a.queries && a.keys && qu + ku <= AT_CUS;
+    // As long as both find room on the chip at once, and walk over about 1024 keys at most, one launch takes as long as the longer of two
+    // (3 sequences of 167 tokens, 16 heads of 64: 34 us the forward and backward pass, 43 in two launches; one of 1024 tokens, 2 heads: 39 and
+    // 46).  Beyond that the registers of both parts together cost more, one workgroup a CU (4096 tokens, 4 heads of 128 over one key head: 282
+    // and 224; 3 sequences of 683, 8 heads of 64: 104 and 90).  Its room goes to them by their products, 3 and 4.
+    p.all = a.queries && a.keys && qu + ku <= AT_CUS && a.keys / a.sequences <= 1024;
     const int64_t kv_walk = a.queries * (a.heads / a.kv_heads);
     p.q_splits = plan_splits(a.queries, a.sequences, a.heads, a.keys, tile_rows(a.dtype), a.dtype, a.causal, p.all ? AT_CUS * 3 / 7 : at_once(a.dtype, a.width));
     p.kv_splits = plan_splits(a.keys, a.sequences, a.kv_heads, kv_walk, KV_ROWS, a.dtype, a.causal, p.all ? AT_CUS * 4 / 7 : at_once(a.dtype, 128));
@@ -1120,7 +1122,7 @@ bool whole(const void* p, int64_t ld, int64_t hs, int64_t es) {
 
 // Inputs whose rows do not come in whole 16-byte chunks (odd widths, pitches or starts) are copied into the workspace first, one
 // launch for all, rows of the next whole width with zeros behind: the walks read every row many times, and loads that go through
-// registers wait for each other (2048 tokens, 8 heads of 101, both passes: 322 us without the copy, 126 at 104).
+// registers wait for each other (2048 tokens, 8 heads of 101, both passes: 322 us without the copy, 142 with it, 120 at 104).
 struct Packer {
     PackArgs args{};
     int64_t es;
