@@ -5,6 +5,10 @@
 // with the same expert bit by bit, by ballots) and copies the rows.  Several workgroups share a chunk: each ranks all of it and
 // copies its part, which costs less than a launch in between.  A call of one chunk needs no count.
 // The rows' runs of 8 values go at any alignment (Run, st_run).
+//
+// Measured (8192 x 2048 bf16 to 6 of 64 experts; a copy moves 5.05 TB/s): sort 4.6 + 46 us (5.1 TB/s), its gradient and the weighted
+// sum 60 - 65 us each (3.6 - 3.9 TB/s, the rate of a reading kernel), the weighted sum's gradient 73 us (6.0 TB/s, some of it from the
+// 256 MB cache).
 #include <algorithm>
 
 #include "train_internal.h"
