@@ -7,7 +7,7 @@
 // The rows' runs of 8 values go at any alignment (Run, st_run).
 //
 // Measured (8192 x 2048 bf16 to 6 of 64 experts; a copy moves 5.05 TB/s): sort 4.6 + 46 us (5.1 TB/s), its gradient and the weighted
-// sum 60 - 66 us each (3.6 - 3.9 TB/s; a library's sum over 1 GiB reads 3.95), the weighted sum's gradient 74 us (5.9 TB/s).
+// sum 60 - 66 us each (3.6 - 3.9 TB/s; a library's sum over 1 GiB reads 3.95; 35 us, 6.7 TB/s, where the rows are in cache), the weighted sum's gradient 74 us (5.9 TB/s).
 #include <algorithm>
 
 #include "train_internal.h"
@@ -19,7 +19,11 @@ namespace {
 constexpr int EX_THREADS = 256, EX_WAVES = 4;
 constexpr int EX_CHUNK = 512, EX_PER = EX_CHUNK / EX_THREADS;   // choices a chunk, a lane
 constexpr int EX_MOST_SHARES = EX_CHUNK / EX_WAVES, EX_WORKGROUPS = 1024;   // workgroups a chunk; as many in all, where they have rows
-constexpr int EX_DIRECT = 128;                                  // chunks whose counts every workgroup adds up by itself
+// (8192 x 2048 to 6 of 64: 45 us; with 256 and 4096 51 and 50; 2048 tokens 18, 21 and 22)
+// Up to so many chunks and experts every workgroup adds up the chunks' counts by itself; for more a launch in between does it once.  64 wide,
+// bf16, direct and scanned: 64 experts 8.5 and 10.0 us (4 chunks), 68 and 72 (256); 128 experts 9.1 and 10.4, 71 and 73, 408 and 308 (1536
+// chunks); 256 experts 10.2 and 10.8 (4), 15.8 and 14.1 (16), 78 and 73 (256); 1024 experts 35 and 16.5 (16).
+constexpr int EX_DIRECT_CHUNKS = 256, EX_DIRECT_EXPERTS = 128;
 
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6)); }
 
@@ -227,7 +231,7 @@ struct GatherArgs {
 };
 
 // out[t] = sum over c of weights[t][c] rows[slots[t][c]], in fp32 in the order of c, rounded once.  EX_AHEAD rows' runs are
-// loaded before the first is added.
+// loaded before the first is added (2: 2 % faster at 6 rows a token in cache; 8: 5 to 20 % slower).
 constexpr int EX_AHEAD = 4;
 template <typename T> __global__ __launch_bounds__(EX_THREADS) void expert_gather_kernel(GatherArgs g) {
     const int per = EX_THREADS / g.lanes;
@@ -349,7 +353,7 @@ hipError_t launch_expert_sort(const muon_expert_sort_args& a, void* workspace, h
     SortArgs g{};
     g.a = a;
     g.chunks = static_cast<int>(sort_chunks(n));
-    g.scanned = g.chunks > EX_DIRECT;
+    g.scanned = g.chunks > 1 && (g.chunks > EX_DIRECT_CHUNKS || a.num_experts > EX_DIRECT_EXPERTS);
     g.counts = static_cast<int32_t*>(workspace);
     g.totals = g.counts + static_cast<size_t>(g.chunks) * a.num_experts;
     hipError_t e;

@@ -90,6 +90,16 @@ def test_experts(gpu_lib, shape, dtype):
     _check(t, o, shape[2], dtype)
 
 
+@pytest.mark.parametrize("shape", [(1024, 4, 128, 1), (1024, 4, 129, 1), (131072, 1, 128, 1), (131073, 1, 128, 1), (131073, 1, 7, 1), (2000, 3, 2048, 2)], ids=str)
+def test_both_ways_to_add_up_the_chunks_counts(gpu_lib, shape):
+    import torch
+    t = _make(*shape, "f32")
+    o = _buffers(t, shape[2])
+    _calls(gpu_lib, t, o)
+    torch.cuda.synchronize()
+    _check(t, o, shape[2], "f32")
+
+
 @pytest.mark.parametrize("pick", ["one", "none", "same_twice", "reversed"])
 def test_uneven_choices(gpu_lib, pick):
     import torch
