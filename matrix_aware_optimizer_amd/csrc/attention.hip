@@ -31,7 +31,11 @@ constexpr int AT_THREADS = 256, AT_WAVES = 4, AT_SHIFT = 7, AT_ROWS = 1 << AT_SH
 constexpr int AT_MAX_SPLITS = 64;
 constexpr int AT_FINISH = 1024;                                 // threads of the sums' workgroups
 constexpr int64_t AT_CUS = 256;
-constexpr int64_t AT_BUCKET_READS = 65536;                      // values of the bias's slots that a workgroup adds up for a bucket
+// The bias's slots are added up a distance at a time in a launch of its own, and buckets from those sums, where there are more slots or more
+// distances a bucket; else by bucket at once.  Both passes, bf16, at once and in two: 8192 tokens, 16 heads of 64, 304 slots 349 and 346 us, reach 1024
+// 398 and 382; 2 sequences, 8 heads, reach 4096 960 and 912; 77 tokens, 8 heads 29.0 and 29.8, 512 tokens 47.6 and 50.4, 4 x 512
+// tokens 104.1 and 105.1.  With 75 distances a bucket (300 queries over 900 keys) 51.9 and 50.1, with 32 (2 x 512 tokens) 80.2 and 82.0.
+constexpr int64_t AT_FEW_SLOTS = 256, AT_FEW_DISTANCES = 64;
 
 // fp32 products take 16 times as long as bf16's: steps and blocks of columns that a narrow head does not have are left out (72 of
 // 128: 4 of 11 of a tile's products).
@@ -664,7 +668,7 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 && !(BIAS && DP == 128) 
 
 // Two waves a SIMD, of workgroups that share no barrier, fill each other's waits.  In bf16 with DP 128 that takes v's fragments out of
 // LDS (both accumulators, k's fragments and a block's scores fill 256 registers), and tiles of 32 queries, so that two
-// workgroups fit a CU's LDS.
+// workgroups fit a CU's LDS (8192 tokens, 16 heads of 128: 265 us; one workgroup of 8 waves and tiles of 64 queries 285).
 template <typename T, int DP> struct KvShape {
     static constexpr bool V_LDS = sizeof(T) == 2 && DP == 128;
     static constexpr int WAVES = sizeof(T) == 2 ? 2 : 1;      // a SIMD
@@ -1068,7 +1072,7 @@ int tile_rows(int dtype) { return dtype == MUON_BF16 ? walk_rows<uint16_t>() : w
 int64_t at_once(int dtype, int width) { return dtype == MUON_F32 && width > 64 ? AT_CUS : 2 * AT_CUS; }
 
 // Sequences of fewer queries than a workgroup has rows: heads that share a key head fill them (a bias is one head's), so that
-// keys are read once for all of them (one query over 4096 keys, 4 heads each of 4 key heads: 14.2 us with a workgroup a head).
+// keys are read once for all of them (one query over 4096 keys, 4 heads each of 4 key heads: 10.0 us, 14.2 with a workgroup a head).
 int forward_pack(const muon_attention_args& a) {
     int pack = 0;
     if (!a.bias && a.queries / a.sequences < AT_ROWS)
@@ -1112,7 +1116,7 @@ BackwardPlan plan_backward(const muon_attention_backward_args& a) {
     if (a.bias) {
         const size_t entries = 2 * static_cast<size_t>(a.reach) + 1;
         p.slots = a.queries ? span_units(a.queries, a.sequences, AT_ROWS) * p.q_splits * AT_WAVES : 0;
-        p.two_step = p.slots * entries / a.buckets > AT_BUCKET_READS;
+        p.two_step = p.slots > AT_FEW_SLOTS || static_cast<int64_t>(entries) > AT_FEW_DISTANCES * a.buckets;
         p.bias_part = take(p.slots * a.heads * entries * 4);
         p.bias_sums = take(p.two_step ? a.heads * entries * 8 : 0);
     }

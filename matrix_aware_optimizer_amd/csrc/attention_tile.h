@@ -271,6 +271,7 @@ struct Span {
 // without rows then stand between the others, every second one where sequences have up to BM rows, and XCDs and shader engines, which take
 // workgroups in turn, would leave half the chip without work (200 sequences of 128 rows: 188 us, 95 in order): the caller
 // goes through the units by a stride that mixes them.
+// (4000 sequences of 40 tokens, forward: 119 us in order, 36 by the stride; 240 of 128: 95 in order.)
 constexpr int SPAN_LANES = 61, SPAN_SCAN = 512;   // sequences that find_span handles a lane each, and in order
 __host__ __device__ inline int64_t span_units(int64_t rows, int64_t sequences, int bm) { return (rows / bm + sequences + 3) | 1; }
 __device__ __forceinline__ int bound(const int64_t* offsets, int sequences, int rows, int s) {

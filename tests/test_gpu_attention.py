@@ -400,6 +400,24 @@ def test_offsets_outside_the_rows_are_clamped(gpu_lib, dtype):
         assert torch.equal(want[k], got[k])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", [dict(nq=[90], buckets=3, reach=95), dict(nq=[90], buckets=3, reach=96), dict(nq=[2] * 40, nk=[3] * 40, buckets=4, reach=9),
+                                   dict(nq=[2] * 70, nk=[3] * 70, buckets=4, reach=9), dict(nq=[300], nk=[900], buckets=1, reach=300)],
+                         ids=lambda s: f"{len(s['nq'])}x{s['nq'][0]}-{s['buckets']}-{s['reach']}")
+def test_both_ways_to_add_up_the_biass_slots(gpu_lib, shape, dtype):
+    c = _case(dtype=dtype, **shape)
+    t, val = _make(c)
+    _check(c, _run(gpu_lib, c, t), val)
+
+
+@pytest.mark.parametrize("reach", [2, 400])
+def test_a_bias_of_no_queries(gpu_lib, reach):
+    c = _case(nq=[0], nk=[9], buckets=3, reach=reach)
+    t, val = _make(c)
+    o = _run(gpu_lib, c, t)
+    assert not o["k"].any() and not o["v"].any() and not o["bias"].any()
+
+
 def test_no_queries_and_no_keys(gpu_lib):
     import torch
     c = _case(nq=[0], nk=[9], buckets=3, reach=2)
