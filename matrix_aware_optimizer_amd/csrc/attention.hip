@@ -156,7 +156,6 @@ template <typename T, int DP> struct KeyWalk {
     int first, last;                                  // tiles
     const T* kbase;
     const T* vbase;
-    uint64_t pending;
 
     __device__ __forceinline__ KeyWalk(const Common& c, const Span& s, int h, int split, int splits, int p) : a(c.a), sp(s), head(h), pack(p) {
         wave_at = sp.at + (32 * wave_id() >> pack);
