@@ -558,7 +558,10 @@ template <typename T, int DP, bool BIAS> __device__ __forceinline__ void grad_q_
         if (f.delta && place < sp.len && lane < 32 && split == 0) G(f.delta)[row * a.heads + head] = delta;
     }
     const float scale = size_of(a.scale), unit = BIAS ? LOG2E : scale * LOG2E;
-    const float ref = row_ok ? (BIAS ? lse : lse * LOG2E) : 0.0f;
+    // +infinity: p is 0 where nothing is seen (a bias alone, from 89 on, would be an infinite one, and 0 times that is in the bias's sums)
+    const float ref = row_ok ? (BIAS ? lse : lse * LOG2E) : -NEG_INF;
+    // a bias may be anything at distances that only places behind the last query have
+    const bool partly = BIAS && w.wave_at + 31 >= sp.len;
 
     f32x16_t o[DB] = {};
     BiasWindow<T, W::WIN> bw;
@@ -598,8 +601,9 @@ template <typename T, int DP, bool BIAS> __device__ __forceinline__ void grad_q_
                 bw.ask(a, w.window_first(t + 2));
             }
         }
-        const int seen = w.seen(c, t, live);
+        int seen = w.seen(c, t, live);
         if (seen != NOTHING) {
+            if (partly) seen = SOME;
             const unsigned kt = lds_at(buf) + 2 * W::TILE * b;
             const int far = BIAS ? w.far(t) : 0;
             // a block of 32 keys at a time: all of a tile at once does not fit the registers of two waves a SIMD
@@ -795,7 +799,7 @@ __device__ __forceinline__ void grad_kv_block(const BackwardArgs& f, int64_t blo
         load_tile<T, DP, BQ, AT_THREADS>(buf + 2 * TILE * b, static_cast<const T*>(a.q) + i0 * a.ld_q + static_cast<int64_t>(w.head) * a.hs_q, a.ld_q, a.width, live);
         load_tile<T, DP, BQ, AT_THREADS>(buf + 2 * TILE * b + TILE, static_cast<const T*>(f.grad_out) + i0 * f.ld_do + static_cast<int64_t>(w.head) * f.hs_do, f.ld_do, a.width, live);
         if (wave == 0 && lane < BQ) {
-            stats[2 * BQ * b + lane] = l == NEG_INF ? 0.0f : BIAS ? l : l * LOG2E;
+            stats[2 * BQ * b + lane] = l == NEG_INF ? -NEG_INF : BIAS ? l : l * LOG2E;       // p is 0 where nothing is seen
             if constexpr (!SELF) stats[2 * BQ * b + BQ + lane] = l == NEG_INF ? 0.0f : d;
         }
         if constexpr (SELF) {
