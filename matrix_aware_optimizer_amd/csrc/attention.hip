@@ -124,12 +124,13 @@ struct Sight {
     __device__ __forceinline__ void set(int l, int h) { lo = l; span = h > l ? h - l : 0; }
 };
 enum { NOTHING = 0, SOME = 1, ALL = 2 };
-// Queries at key positions a0 .. a1, keys j0 .. j1, all of them within the sequence.
+// Queries at key positions a0 .. a1, keys j0 .. j1, all of them within the sequence or less than a tile behind it.  Positions and window
+// reach 2^30: their differences stay within 32 bits, a sum of the two does not.
 __device__ __forceinline__ int tile_sight(int a0, int a1, int j0, int j1, bool causal, int window) {
     if (causal && j0 > a1) return NOTHING;
-    if (window && (j1 <= a0 - window || j0 >= a1 + window)) return NOTHING;
+    if (window && (j1 - a0 <= -window || j0 - a1 >= window)) return NOTHING;
     if (causal && j1 > a0) return SOME;
-    if (window && (j0 <= a1 - window || j1 >= a0 + window)) return SOME;
+    if (window && (j0 - a1 <= -window || j1 - a0 >= window)) return SOME;
     return ALL;
 }
 // Scores outside a lane's sight to -infinity: register i stands for place at + 8 (i / 4) + i % 4 (4 h is in `at`); bits: the
@@ -183,7 +184,7 @@ template <typename T, int DP> struct KeyWalk {
         load_tile<T, DP, BN, AT_THREADS>(v, vbase + j * a.ld_v, a.ld_v, a.width, live);
     }
     __device__ __forceinline__ Sight sight(const Common& c, int at) const {      // of the query at place `at`
-        const int p = at + off;
+        const int p = min(at, sp.len - 1) + off;
         int lo = 0, hi = sp.other_len;
         if (a.causal) hi = min(hi, p + 1);
         if (c.window) { lo = max(lo, p - c.window + 1); hi = min(hi, p + c.window); }
@@ -558,8 +559,8 @@ template <typename T, int DP, bool BIAS> __device__ __forceinline__ void grad_q_
         if (f.delta && place < sp.len && lane < 32 && split == 0) G(f.delta)[row * a.heads + head] = delta;
     }
     const float scale = size_of(a.scale), unit = BIAS ? LOG2E : scale * LOG2E;
-    // +infinity: p is 0 where nothing is seen (a bias alone, from 89 on, would be an infinite one, and 0 times that is in the bias's sums)
-    const float ref = row_ok ? (BIAS ? lse : lse * LOG2E) : -NEG_INF;
+    // With a bias +infinity, so that p is 0, where nothing is seen (a bias alone, from 89 on, would be an infinite one, and 0 times that is in the bias's sums)
+    const float ref = BIAS ? (row_ok ? lse : -NEG_INF) : row_ok ? lse * LOG2E : 0.0f;
     // a bias may be anything at distances that only places behind the last query have
     const bool partly = BIAS && w.wave_at + 31 >= sp.len;
 
@@ -708,8 +709,9 @@ __device__ __forceinline__ void grad_kv_block(const BackwardArgs& f, int64_t blo
     Sight sight;
     {
         int lo = 0, hi = nq;
-        if (a.causal) lo = max(lo, place - off);
-        if (c.window) { lo = max(lo, place - c.window + 1 - off); hi = min(hi, place + c.window - off); }
+        const int p = min(place, sp.len - 1) - off;
+        if (a.causal) lo = max(lo, p);
+        if (c.window) { lo = max(lo, p - c.window + 1); hi = min(hi, p + c.window); }
         sight.set(lo, key_ok ? hi : lo);
     }
     const bool keys_all = __all(key_ok);
@@ -739,7 +741,7 @@ __device__ __forceinline__ void grad_kv_block(const BackwardArgs& f, int64_t blo
     {
         const int j1 = sp.at + min(sp.rows, AT_ROWS) - 1;
         if (a.causal) lo = max(lo, sp.at - off);
-        if (c.window) { lo = max(lo, sp.at - c.window + 1 - off); hi = min(hi, j1 + c.window - off); }
+        if (c.window) { lo = max(lo, sp.at - off - c.window + 1); hi = min(hi, j1 - off + c.window); }
     }
     const int first = lo / BQ, n = hi > lo ? (hi + BQ - 1) / BQ - first : 0;
     const int64_t steps = static_cast<int64_t>(n) * c.gqa;
@@ -799,7 +801,7 @@ __device__ __forceinline__ void grad_kv_block(const BackwardArgs& f, int64_t blo
         load_tile<T, DP, BQ, AT_THREADS>(buf + 2 * TILE * b, static_cast<const T*>(a.q) + i0 * a.ld_q + static_cast<int64_t>(w.head) * a.hs_q, a.ld_q, a.width, live);
         load_tile<T, DP, BQ, AT_THREADS>(buf + 2 * TILE * b + TILE, static_cast<const T*>(f.grad_out) + i0 * f.ld_do + static_cast<int64_t>(w.head) * f.hs_do, f.ld_do, a.width, live);
         if (wave == 0 && lane < BQ) {
-            stats[2 * BQ * b + lane] = l == NEG_INF ? -NEG_INF : BIAS ? l : l * LOG2E;       // p is 0 where nothing is seen
+            stats[2 * BQ * b + lane] = BIAS ? (l == NEG_INF ? -NEG_INF : l) : l == NEG_INF ? 0.0f : l * LOG2E;       // as in grad_q_block
             if constexpr (!SELF) stats[2 * BQ * b + BQ + lane] = l == NEG_INF ? 0.0f : d;
         }
         if constexpr (SELF) {

@@ -55,3 +55,44 @@ def test_buckets_of_distances_that_no_pair_has_reach_nothing(gpu_lib, value, dty
     got = _run(gpu_lib, c, clean)
     for k in ("out", "lse", "q", "k", "v", "bias"):
         assert torch.equal(want[k], got[k]), k
+
+
+@pytest.mark.parametrize("causal", [False, True])
+def test_a_window_over_as_many_keys_as_there_may_be(gpu_lib, causal):
+    # one query behind 2^30 - 1 keys, all of them one broadcast row: key positions and windows that sum to more than 2^31
+    import torch
+    n, width = 1 << 30, 8
+    if torch.cuda.mem_get_info()[0] < 3 * n * width * 2:
+        pytest.skip("needs 52 GB")
+    r = np.random.default_rng(3)
+    put = lambda *s: torch.from_numpy(r.standard_normal(s).astype(np.float32)).bfloat16().cuda()
+    q, k, v, do = put(1, 1, width), put(1, 1, width), put(1, 1, width), put(1, 1, width)
+    keys, values = k.expand(n, 1, width), v.expand(n, 1, width)
+    gk, gv = (torch.full((n, 1, width), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    out, lse, gq = torch.full_like(q, float("nan")), torch.full((1, 1), float("nan"), device="cuda"), torch.full_like(q, float("nan"))
+    form = dict(causal=causal, window=n - 1, scale=0.25)
+    gpu_lib.muon_attention(q, keys, values, out, lse, **form)
+    gpu_lib.muon_attention_backward(q, keys, values, out, lse, do, gq, gk, gv, **form)
+    torch.cuda.synchronize()
+    # It sees n - 1 keys alike.  A part of the walk (64 at most) takes 2^18 tiles: 2^18 x 4 steps x 2 parts = 2^21 additions to an element of
+    # out, each within 2 u of a running sum that grows evenly, so half of 2^22 u = 2^-3 in all; a lane adds 2^23 probabilities, each
+    # addition within u, half of 2^23 u = 2^-2.
+    assert (np.abs(_np(out) - _np(v)) <= (2.0 ** -3 + 2.0 ** -2) * np.abs(_np(v))).all() and out.any()
+    z, low, high = 0.25 * float((_np(q) * _np(k)).sum()), np.log(0.75), np.log(1.25)
+    assert low - 1e-4 <= float(lse) - (z + np.log(n - 1)) <= high + 1e-4
+    # grad_v = p grad_out with p from lse, the same for every key that is seen
+    p = np.exp(z - float(lse))
+    want = _np(do)[0, 0] * p
+    assert not gv[0].any() and not gk[0].any()
+    for part in gv[1:].split(1 << 27):
+        lo, hi = part.amin((0, 1)), part.amax((0, 1))
+        # p: the score and lse in fp32, an exponential, 2^-16 in all for |lse| up to 64; then bf16
+        assert (lo == hi).all() and (np.abs(_np(lo) - want) <= (2.0 ** -8 + 2.0 ** -15) * np.abs(want)).all()
+    # dz = p (do.v - do.out), the same for every key: what out is off by
+    dz = float((_np(do) * (_np(v) - _np(out))).sum())
+    size = float((np.abs(_np(do)) * np.abs(_np(v))).sum())
+    bound = 0.25 * p * (2.0 ** -7 * abs(dz) + 2.0 ** -18 * size)
+    for part in gk[1:].split(1 << 27):
+        lo, hi = part.amin((0, 1)), part.amax((0, 1))
+        assert (lo == hi).all() and (np.abs(_np(lo) - 0.25 * p * dz * _np(q)[0, 0]) <= bound * np.abs(_np(q)[0, 0])).all()
+    assert (np.abs(_np(gq)) <= 0.25 * 1.5 * (abs(dz) + 2.0 ** -18 * size) * np.abs(_np(k))).all()
