@@ -70,7 +70,7 @@ class Block:
         t, n = tokens, tokens * chosen
         self.qkv, self.gqkv = empty(t, rows), empty(t, rows)
         self.att, self.low, self.gatt = (empty(t, heads, self.head_width) for _ in range(3))
-        self.lse_att = empty(t, heads, like=f32)
+        self.lse_att, self.lse_att_low = empty(t, heads, like=f32), empty(t, heads, like=f32)
         self.o, self.m, self.r1, self.n1, self.r2, self.n2 = (empty(t, width) for _ in range(6))
         self.gn2, self.gm, self.gr1, self.gn1, self.go, self.gx = (empty(t, width) for _ in range(6))
         self.rstd = [empty(2, t, like=f32) for _ in range(2)]
@@ -93,7 +93,8 @@ class Block:
         return {f"grad_{k}_weight" if k != "gate" else "grad_gate": self.grads[f"{k}{i}"] for k in ("post", "gate", "pre")}
 
     def attention_form(self, offsets):
-        return dict(offsets=offsets, bias=self.small["bias"], bucket_map=self.map, causal=True, out_low=self.low)
+        return dict(offsets=offsets, bias=self.small["bias"], bucket_map=self.map, causal=True, out_low=self.low,
+                    lse_low=self.lse_att_low)
 
     def forward(self, x, offsets, targets):
         """logp of the targets (< 0: not scored) for sequences packed one after the other."""

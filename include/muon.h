@@ -468,7 +468,13 @@ muon_status muon_policy_loss(const muon_policy_args* args, void* workspace, size
  * calls take the probabilities (and dz below) into their products as two bf16
  * parts, 16 bits.  `out_low` is what rounding took from `out`: with it the
  * backward pass has out in 16 bits, which it needs where a row sees almost
- * only one key. */
+ * only one key.  Scores are held in fp32, and so is lse: what rounding takes from
+ * it muon_attention_two_part keeps.  Scores are off by some 2^-23 of their size, so
+ * that from about 2^20 on a row's probabilities are no longer those of its inputs;
+ * without a bias scores from 2^30 on may come out as NaN.
+ *
+ * A key that `causal` or `window` hides from a query but that another one of the same
+ * sequence sees reaches the first one too if it holds infinities or NaN. */
 #define MUON_MAX_HEAD_WIDTH 128
 #define MUON_MAX_HEADS      4096
 #define MUON_MAX_REACH      4096
@@ -499,6 +505,11 @@ typedef struct {
 
 size_t muon_attention_workspace_bytes(const muon_attention_args* args);
 muon_status muon_attention(const muon_attention_args* args, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The same with lse in two parts: lse_low (queries x heads, contiguous, fp32) is
+ * what rounding took from lse; NULL: muon_attention.  The workspace is the same. */
+muon_status muon_attention_two_part(const muon_attention_args* args, float* lse_low, void* workspace, size_t workspace_bytes,
+                                    void* stream);
 
 /* Its gradients, from grad_out; the probabilities are formed again.  out, lse and
  * out_low (which may be NULL) are the forward call's.  With p_ij = exp(z_ij - lse_i):
@@ -534,6 +545,14 @@ typedef struct {
 size_t muon_attention_backward_workspace_bytes(const muon_attention_backward_args* args);
 muon_status muon_attention_backward(const muon_attention_backward_args* args, void* workspace, size_t workspace_bytes,
                                     void* stream);
+
+/* The same with lse_low as muon_attention_two_part wrote it; NULL: muon_attention_backward.
+ * Without it p_ij comes from lse alone, so a row's probabilities are all off by a
+ * factor within exp(|lse| 2^-24): 2^-20 of them at |lse| = 16, and wholly where a row
+ * sees nothing but a bias so low (below about -1e5) that lse no longer holds the
+ * logarithm of its sum; there its keys count as 1 each instead of 1 in all. */
+muon_status muon_attention_backward_two_part(const muon_attention_backward_args* args, const float* lse_low, void* workspace,
+                                             size_t workspace_bytes, void* stream);
 
 /* --- Tokens sorted by expert, and back --------------------------------------
  * experts[t][c] is the c-th expert that token t goes to; a value outside

@@ -16,7 +16,8 @@ The names mirror the C entry points:
 ``muon_token_logp_backward_workspace_bytes``, ``muon_preference_loss``,
 ``muon_preference_loss_workspace_bytes``, ``muon_policy_loss``,
 ``muon_policy_loss_workspace_bytes``, ``muon_attention``,
-``muon_attention_workspace_bytes``, ``muon_attention_backward``,
+``muon_attention_workspace_bytes``, ``muon_attention_backward`` (C:
+``muon_attention_two_part`` and ``muon_attention_backward_two_part`` too),
 ``muon_attention_backward_workspace_bytes``, ``muon_expert_sort``,
 ``muon_expert_sort_workspace_bytes``, ``muon_expert_sort_backward``,
 ``muon_expert_combine``, ``muon_expert_combine_backward``,
@@ -207,6 +208,8 @@ SIGNATURES = {
     **{f"muon_{op}_workspace_bytes": (ctypes.c_size_t, [ctypes.c_void_p]) for op in _WORKSPACE_OPS},
     **{f"muon_{op}": (ctypes.c_int32, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p])
        for op in _WORKSPACE_OPS},
+    **{f"muon_{op}_two_part": (ctypes.c_int32, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p])
+       for op in ("attention", "attention_backward")},
     "muon_token_logp_saved_bytes": (ctypes.c_size_t, [ctypes.c_void_p]),
     "muon_status_string": (ctypes.c_char_p, [ctypes.c_int32]),
     "muon_last_error_message": (ctypes.c_char_p, []),
@@ -624,13 +627,13 @@ def _size(size_fn, packed) -> int:
     return int(need)
 
 
-def _call(fn, size_fn, packed, workspace, device, stream, raw):
-    """Runs one operator with the caller's workspace or one of its own; returns the workspace."""
+def _call(fn, size_fn, packed, workspace, device, stream, raw, *more):
+    """Runs one operator with the caller's workspace or one of its own; returns the workspace.  `more`: arguments behind the struct."""
     if workspace is None:
         workspace = _workspace_for(_size(size_fn, packed), None, device, stream)
     elif stream is not None:
         workspace = _workspace_for(0, workspace, device, stream)
-    _check(fn(packed, workspace.data_ptr(), workspace.numel() * workspace.element_size(), raw))
+    _check(fn(packed, *more, workspace.data_ptr(), workspace.numel() * workspace.element_size(), raw))
     return workspace
 
 
@@ -986,6 +989,12 @@ def _attention_stand_ins(q, k, n):
     return [(1 << 44) + q.data_ptr() % 16] + [(j << 44) + odd for j in range(2, n + 1)]
 
 
+def _check_lse(t, what, queries, heads):
+    import torch
+    if t.dtype is not torch.float32 or t.shape != (queries, heads) or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous float32 of shape {(queries, heads)}")
+
+
 def _attention_scale(scale, width):
     return width ** -0.5 if scale is None else scale
 
@@ -1006,7 +1015,7 @@ def muon_attention_workspace_bytes(q, k, *, sequences=1) -> int:
 
 
 def muon_attention(q, k, v, out, lse, *, offsets=None, key_offsets=None, key_mask=None, bias=None, bucket_map=None,
-                   scale=None, causal=False, window=0, out_low=None, workspace=None, stream=None):
+                   scale=None, causal=False, window=0, out_low=None, lse_low=None, workspace=None, stream=None):
     """Softmax attention over packed sequences, with a learned relative position bias where one is given.
 
     ``q`` and ``out`` are queries x heads x width, ``k`` and ``v`` keys x kv_heads x width (heads a multiple of
@@ -1016,23 +1025,24 @@ def muon_attention(q, k, v, out, lse, *, offsets=None, key_offsets=None, key_mas
     ``causal`` hides the keys behind a query, ``window`` those at that distance or farther, ``key_mask`` 0 a key.
     ``scale`` defaults to ``width ** -0.5``.  ``bias[b, h]`` (buckets x heads, like q) is added at the distances whose
     entry of ``bucket_map`` (int32, for the distances key - query from -reach to reach, farther ones as those) is b.
-    ``out_low`` (like out) keeps what rounding took from ``out`` for :func:`muon_attention_backward`.
+    ``out_low`` (like out) and ``lse_low`` (like lse) keep what rounding took from ``out`` and ``lse`` for
+    :func:`muon_attention_backward`.
     """
-    import torch
     n, m, sequences, heads, kv_heads, width, buckets, reach, code = _attention_shape(
         q, k, v, offsets, key_offsets, key_mask, bias, bucket_map)
     shape, dtype = q.shape, q.dtype
-    if lse.dtype is not torch.float32 or lse.shape != (n, heads) or not lse.is_contiguous():
-        raise ValueError(f"lse must be contiguous float32 of shape {(n, heads)}")
+    _check_lse(lse, "lse", n, heads)
+    if lse_low is not None:
+        _check_lse(lse_low, "lse_low", n, heads)
     packed = _pack_attention(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(offsets), _ptr(key_offsets), _ptr(key_mask), _ptr(bias),
         _ptr(bucket_map), out.data_ptr(), lse.data_ptr(), _ptr(out_low), n, m, sequences, *_heads(q, "q", shape, dtype),
         *_heads(k, "k", k.shape, dtype), *_heads(v, "v", k.shape, dtype), *_heads(out, "out", shape, dtype),
         *((0, 0) if out_low is None else _heads(out_low, "out_low", shape, dtype)), window,
         _attention_scale(scale, width), heads, kv_heads, width, buckets, reach, 1 if causal else 0, code)
-    raw = _raw_stream(stream, q, k, v, offsets, key_offsets, key_mask, bias, bucket_map, out, lse, out_low, workspace)
+    raw = _raw_stream(stream, q, k, v, offsets, key_offsets, key_mask, bias, bucket_map, out, lse, out_low, lse_low, workspace)
     lib = load()
-    return _call(lib.muon_attention, lib.muon_attention_workspace_bytes, packed, workspace, q.device, stream, raw)
+    return _call(lib.muon_attention_two_part, lib.muon_attention_workspace_bytes, packed, workspace, q.device, stream, raw, _ptr(lse_low))
 
 
 def muon_attention_backward_workspace_bytes(q, k, *, sequences=1, bias=None, bucket_map=None) -> int:
@@ -1052,19 +1062,20 @@ def muon_attention_backward_workspace_bytes(q, k, *, sequences=1, bias=None, buc
 
 def muon_attention_backward(q, k, v, out, lse, grad_out, grad_q, grad_k, grad_v, *, offsets=None, key_offsets=None,
                             key_mask=None, bias=None, bucket_map=None, grad_bias=None, scale=None, causal=False, window=0,
-                            out_low=None, workspace=None, stream=None):
+                            out_low=None, lse_low=None, workspace=None, stream=None):
     """Gradients of :func:`muon_attention` for the gradient ``grad_out`` of its ``out``.
 
-    The arguments that it shares with the forward call are that call's, ``out``, ``lse`` and ``out_low`` (which may be
-    None) what it wrote.  ``grad_k`` and ``grad_v`` are summed over the heads that share a key head, ``grad_bias`` over
+    The arguments that it shares with the forward call are that call's, ``out``, ``lse``, ``out_low`` and ``lse_low`` what
+    it wrote.  The last two may be None; without ``lse_low`` a row's probabilities are off by up to ``abs(lse) * 2 ** -24``
+    of them, so that a bias of -1e5 and below, where a row has nothing else, needs it.  ``grad_k`` and ``grad_v`` are summed over the heads that share a key head, ``grad_bias`` over
     all pairs of a bucket.
     """
-    import torch
     n, m, sequences, heads, kv_heads, width, buckets, reach, code = _attention_shape(
         q, k, v, offsets, key_offsets, key_mask, bias, bucket_map)
     shape, dtype = q.shape, q.dtype
-    if lse.dtype is not torch.float32 or lse.shape != (n, heads) or not lse.is_contiguous():
-        raise ValueError(f"lse must be contiguous float32 of shape {(n, heads)}")
+    _check_lse(lse, "lse", n, heads)
+    if lse_low is not None:
+        _check_lse(lse_low, "lse_low", n, heads)
     if (bias is None) != (grad_bias is None):
         raise ValueError("bias and its gradient go together")
     if bias is not None and (grad_bias.shape != bias.shape or grad_bias.dtype != dtype or not grad_bias.is_contiguous()):
@@ -1079,10 +1090,10 @@ def muon_attention_backward(q, k, v, out, lse, grad_out, grad_q, grad_k, grad_v,
         *_heads(grad_k, "grad_k", k.shape, dtype), *_heads(grad_v, "grad_v", k.shape, dtype), window,
         _attention_scale(scale, width), heads, kv_heads, width, buckets, reach, 1 if causal else 0, code)
     raw = _raw_stream(stream, q, k, v, offsets, key_offsets, key_mask, bias, bucket_map, out, lse, out_low, grad_out, grad_q,
-                      grad_k, grad_v, grad_bias, workspace)
+                      grad_k, grad_v, grad_bias, lse_low, workspace)
     lib = load()
-    return _call(lib.muon_attention_backward, lib.muon_attention_backward_workspace_bytes, packed, workspace, q.device,
-                 stream, raw)
+    return _call(lib.muon_attention_backward_two_part, lib.muon_attention_backward_workspace_bytes, packed, workspace, q.device,
+                 stream, raw, _ptr(lse_low))
 
 
 def _choices(t, what, tokens, dtype):

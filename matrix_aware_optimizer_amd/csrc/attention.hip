@@ -47,6 +47,7 @@ constexpr int KV_ROWS = 32;
 
 struct Common {
     muon_attention_args a;
+    float* lse_low;       // queries x heads, or NULL
     int64_t unit0;        // first unit of this launch
     int64_t units;        // of the whole call: units of an axis x heads x splits
     int64_t q_axis, q_stride, k_axis, k_stride;   // units of the two axes, and the stride through them
@@ -95,6 +96,35 @@ template <typename T> __device__ __forceinline__ void negate(Frag<T>& f) {
     else { f.w[0] = -f.w[0]; f.w[1] = -f.w[1]; }
 }
 __device__ __forceinline__ float size_of(float scale) { return scale == 0.0f ? 1.0f : fabsf(scale); }
+
+// A row's lse in two parts, L = hi + low, from its reference m (natural units with a bias, else powers of two) and the sum l of its terms.
+// Whole powers of two of l are added as they are, so that the logarithm is one between sqrt(1/2) and sqrt(2), within 2^-24.
+template <bool BIAS> __device__ __forceinline__ void store_lse(const Common& c, int64_t at, float m, float l) {
+    float hi = NEG_INF, low = 0.0f;
+    if (l != 0.0f) {
+        float x = __builtin_amdgcn_frexp_mantf(l);
+        int e = __builtin_amdgcn_frexp_expf(l);
+        if (x < 0.70710678f) {
+            x *= 2.0f;
+            --e;
+        }
+        const double n = LN2_64 * (static_cast<double>(e) + static_cast<double>(__builtin_amdgcn_logf(x))), at_m = BIAS ? m : LN2_64 * m;
+        hi = static_cast<float>(at_m + n);
+        low = fabsf(hi) < -NEG_INF ? static_cast<float>((at_m - hi) + n) : 0.0f;      // a low m takes all of n out of their sum
+    }
+    G(c.a.lse)[at] = hi;
+    if (c.lse_low) G(c.lse_low)[at] = low;
+}
+// What a row's probabilities are formed again with: p = 2^low2 exp(score - ref), the score times log2 e in `ref`'s place and a power of two
+// where there is no bias.  low2 is what lse and its product with log2 e lose in 32 bits: without it a row's probabilities would all be
+// off by up to |lse| 2^-23, and with a bias so low that the logarithm of the sum is lost in lse by a factor of the keys' number.
+struct RowRef {
+    float ref, low2;
+    template <bool BIAS> __device__ __forceinline__ void set(float lse, float low) {
+        ref = BIAS ? lse : lse * LOG2E;
+        low2 = -LOG2E * low - (BIAS ? 0.0f : fmaf(lse, LOG2E, -ref) + lse * LOG2E_LOW);
+    }
+};
 
 // Bias of a head at distance j - a.
 template <typename T> __device__ __forceinline__ int bucket_at(const muon_attention_args& a, int dist) {
@@ -373,7 +403,7 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 ? 2 : 1) void attention_
     T* out = static_cast<T*>(a.out) + row * a.ld_out + static_cast<int64_t>(own) * a.hs_out;
     T* low = a.out_low ? static_cast<T*>(a.out_low) + row * a.ld_out_low + static_cast<int64_t>(own) * a.hs_out_low : nullptr;
     store_rows<T>(o, l == 0.0f ? 0.0f : 1.0f / l, out, low, a.width);
-    if (lane < 32) G(a.lse)[row * a.heads + own] = l == 0.0f ? NEG_INF : (BIAS ? m : m * LN2) + __logf(l);
+    if (lane < 32) store_lse<BIAS>(c, row * a.heads + own, m, l);
 }
 
 // Joins the splits of a row: a wave each.
@@ -425,7 +455,7 @@ template <typename T, bool BIAS> __global__ __launch_bounds__(256) void attentio
                 st_el<T>(a.out_low, row * a.ld_out_low + static_cast<int64_t>(head) * a.hs_out_low + lane + 64 * k,
                          sizeof(T) == 2 ? x - bf16_to_f32(f32_to_bf16(x)) : 0.0f);
         }
-    if (lane == 0) G(a.lse)[at] = sum == 0.0f ? NEG_INF : (BIAS ? top : top * LN2) + __logf(sum);
+    if (lane == 0) store_lse<BIAS>(c, at, top, sum);
 }
 
 // ---- grad_q, and the bias's gradient --------------------------------------------
@@ -532,6 +562,7 @@ template <typename T, int DP, bool BIAS> __device__ __forceinline__ void grad_q_
     // a query that sees no key takes no part, whatever its rows hold
     const float lse = place < sp.len ? G(a.lse)[row * a.heads + head] : NEG_INF;
     const bool row_ok = lse != NEG_INF;
+    const float lse_low = c.lse_low && row_ok ? G(c.lse_low)[row * a.heads + head] : 0.0f;
     Frag<T> qf[KS], df[KS];
     float delta = 0.0f;
     {
@@ -560,7 +591,9 @@ template <typename T, int DP, bool BIAS> __device__ __forceinline__ void grad_q_
     }
     const float scale = size_of(a.scale), unit = BIAS ? LOG2E : scale * LOG2E;
     // With a bias +infinity, so that p is 0, where nothing is seen (a bias alone, from 89 on, would be an infinite one, and 0 times that is in the bias's sums)
-    const float ref = BIAS ? (row_ok ? lse : -NEG_INF) : row_ok ? lse * LOG2E : 0.0f;
+    RowRef r{BIAS ? -NEG_INF : 0.0f, 0.0f};
+    if (row_ok) r.set<BIAS>(lse, lse_low);
+    const float ref = r.ref, norm = exp2_(r.low2), delta_norm = delta * norm;
     // a bias may be anything at distances that only places behind the last query have
     const bool partly = BIAS && w.wave_at + 31 >= sp.len;
 
@@ -627,7 +660,7 @@ template <typename T, int DP, bool BIAS> __device__ __forceinline__ void grad_q_
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const float p = BIAS ? exp2_((s[i] - ref) * unit) : exp2_(fmaf(s[i], unit, -ref));
-                    s[i] = p * (dp[i] - delta);
+                    s[i] = p * fmaf(dp[i], norm, -delta_norm);
                 }
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
@@ -678,9 +711,9 @@ template <typename T, int DP> struct KvShape {
     static constexpr int WAVES = sizeof(T) == 2 ? 2 : 1;      // a SIMD
 };
 
-// LDS of a workgroup: the tiles, v, [buffer][lse or delta][query], the bias's windows.
+// LDS of a workgroup: the tiles, v, [buffer][ref; low2 (fp32: 2^low2); delta][query], a zero for each query, the bias's windows.
 template <typename T, int DP, bool BIAS> constexpr int grad_kv_lds() {
-    return (4 * KV_ROWS + (KvShape<T, DP>::V_LDS ? AT_ROWS : 0)) * Row<T, DP>::BYTES + 2 * 2 * KV_ROWS * 4 + (BIAS ? 2 * (AT_ROWS + KV_ROWS) * 4 : 0);
+    return (4 * KV_ROWS + (KvShape<T, DP>::V_LDS ? AT_ROWS : 0)) * Row<T, DP>::BYTES + 7 * KV_ROWS * 4 + (BIAS ? 2 * (AT_ROWS + KV_ROWS) * 4 : 0);
 }
 
 // SELF: delta is formed here, tile by tile, for a launch that does not wait for grad_q's: a wave takes 8 of a tile's 32 queries,
@@ -703,7 +736,8 @@ __device__ __forceinline__ void grad_kv_block(const BackwardArgs& f, int64_t blo
     const bool in = place < sp.len, key_ok = in && (!a.key_mask || G(a.key_mask)[in ? row : 0] != 0);
     Lanes<T, DP> lanes;
     lds_float_t* stats = (lds_float_t*)(buf + 4 * TILE + VTILE);
-    lds_float_t* wbuf = stats + 2 * 2 * BQ;
+    lds_float_t* zeros = stats + 6 * BQ;
+    lds_float_t* wbuf = stats + 7 * BQ;
 
     // queries that see this lane's key: places lo .. lo + span - 1
     Sight sight;
@@ -767,14 +801,15 @@ __device__ __forceinline__ void grad_kv_block(const BackwardArgs& f, int64_t blo
     Frag<T> own_d[SELF ? DP / 64 : 1], own_o[SELF ? DP / 64 : 1], own_l[SELF ? DP / 64 : 1];
     float own_lse = NEG_INF;
     // lse of this lane's row of a step (and its delta, or what that is formed of): -infinity where there is nothing to see
-    auto ask = [&](const At& w, float& l, float& d) {
+    auto ask = [&](const At& w, float& l, float& low, float& d) {
         l = NEG_INF;
-        d = 0.0f;
+        low = d = 0.0f;
         if (w.left <= 0) return;
         const int i = w.t * BQ + lane;
         if (lane < BQ && i < nq) {
             const int64_t at = static_cast<int64_t>(sp.other + i) * a.heads + w.head;
             l = G(a.lse)[at];
+            if (c.lse_low) low = G(c.lse_low)[at];
             if constexpr (!SELF) d = G(f.delta)[at];
         }
         if constexpr (SELF) {
@@ -795,14 +830,20 @@ __device__ __forceinline__ void grad_kv_block(const BackwardArgs& f, int64_t blo
             }
         }
     };
-    auto load = [&](const At& w, int b, float l, float d) {
+    // Loads a step's tiles; returns whether its probabilities take low2.  fp32: a factor for each.  In bf16 it is left out up to an lse of 2^10,
+    // where it is below 2^-13; a factor for each, as in fp32, costs 16 products a block and registers that 128 wide does not have (8192
+    // tokens, 16 heads: 426 -> 467 us both passes).
+    auto load = [&](const At& w, int b, float l, float low, float d) {
         const uint64_t live = __ballot(l != NEG_INF);
         const int64_t i0 = static_cast<int64_t>(sp.other) + static_cast<int64_t>(w.t) * BQ;
         load_tile<T, DP, BQ, AT_THREADS>(buf + 2 * TILE * b, static_cast<const T*>(a.q) + i0 * a.ld_q + static_cast<int64_t>(w.head) * a.hs_q, a.ld_q, a.width, live);
         load_tile<T, DP, BQ, AT_THREADS>(buf + 2 * TILE * b + TILE, static_cast<const T*>(f.grad_out) + i0 * f.ld_do + static_cast<int64_t>(w.head) * f.hs_do, f.ld_do, a.width, live);
         if (wave == 0 && lane < BQ) {
-            stats[2 * BQ * b + lane] = BIAS ? (l == NEG_INF ? -NEG_INF : l) : l == NEG_INF ? 0.0f : l * LOG2E;       // as in grad_q_block
-            if constexpr (!SELF) stats[2 * BQ * b + BQ + lane] = l == NEG_INF ? 0.0f : d;
+            RowRef r{BIAS ? -NEG_INF : 0.0f, 0.0f};       // as in grad_q_block
+            if (l != NEG_INF) r.set<BIAS>(l, low);
+            stats[3 * BQ * b + lane] = r.ref;
+            stats[3 * BQ * b + BQ + lane] = sizeof(T) == 2 ? r.low2 : exp2_(r.low2);
+            if constexpr (!SELF) stats[3 * BQ * b + 2 * BQ + lane] = l == NEG_INF ? 0.0f : d;
         }
         if constexpr (SELF) {
             float v = 0.0f;
@@ -815,8 +856,10 @@ __device__ __forceinline__ void grad_kv_block(const BackwardArgs& f, int64_t blo
                 }
 #pragma unroll
             for (int k = 1; k < 8; k <<= 1) v += __shfl_xor(v, k);
-            if ((lane & 7) == 0) stats[2 * BQ * b + BQ + 8 * wave + (lane >> 3)] = own_lse == NEG_INF ? 0.0f : v;
+            if ((lane & 7) == 0) stats[3 * BQ * b + 2 * BQ + 8 * wave + (lane >> 3)] = own_lse == NEG_INF ? 0.0f : v;
         }
+        if (BIAS && !c.lse_low) return false;
+        return (sizeof(T) == 4 ? __any(l != NEG_INF) : __any(l >= 1024.0f || (l <= -1024.0f && l != NEG_INF))) != 0;
     };
     // distance of the window's first entry for tile t: that of this workgroup's first key and the tile's last query
     auto window_first = [&](int t) { return sp.at - (t * BQ + BQ - 1 + off); };
@@ -824,11 +867,13 @@ __device__ __forceinline__ void grad_kv_block(const BackwardArgs& f, int64_t blo
     const float scale = size_of(a.scale), unit = BIAS ? LOG2E : scale * LOG2E;
     f32x16_t dk[DB] = {}, dv[DB] = {};
     BiasWindow<T, WIN> bw;
-    float lse = 0.0f, delta = 0.0f;
+    float lse = 0.0f, lse_low = 0.0f, delta = 0.0f;
+    bool take_low = false, take_low_next = false;
+    if (wave == 0 && lane < BQ) zeros[lane] = 0.0f;
     if (now.left > 0) {
-        ask(now, lse, delta);
-        load(now, 0, lse, delta);
-        ask(after(now), lse, delta);
+        ask(now, lse, lse_low, delta);
+        take_low_next = load(now, 0, lse, lse_low, delta);
+        ask(after(now), lse, lse_low, delta);
         if constexpr (BIAS) {
             bw.ask(a, window_first(now.t));
             bw.fetch(a, now.head);
@@ -840,9 +885,10 @@ __device__ __forceinline__ void grad_kv_block(const BackwardArgs& f, int64_t blo
     for (; now.left > 0; now = after(now), b ^= 1) {
         const At next = after(now);
         tile_barrier();
+        take_low = take_low_next;
         if (next.left > 0) {
-            load(next, b ^ 1, lse, delta);
-            ask(after(next), lse, delta);
+            take_low_next = load(next, b ^ 1, lse, lse_low, delta);
+            ask(after(next), lse, lse_low, delta);
             if constexpr (BIAS) {
                 bw.fetch(a, next.head);
                 bw.ask(a, window_first(after(next).t));
@@ -850,7 +896,7 @@ __device__ __forceinline__ void grad_kv_block(const BackwardArgs& f, int64_t blo
         }
         const unsigned qt = lds_at(buf) + 2 * TILE * b, dt = qt + TILE;
         lanes.fresh();
-        const lds_float_t* st = stats + 2 * BQ * b;
+        const lds_float_t* st = stats + 3 * BQ * b;
         const int i0 = now.t * BQ;
         int seen = wave_at >= sp.len ? NOTHING : tile_sight(i0 + off, i0 + off + 31, wave_at, wave_at + 31, a.causal, c.window);
         if (seen != NOTHING) {
@@ -869,17 +915,47 @@ __device__ __forceinline__ void grad_kv_block(const BackwardArgs& f, int64_t blo
 #pragma unroll
                 for (int i = 0; i < 16; ++i) s[i] = fmaf(s[i], scale, p[-(8 * (i >> 2) + (i & 3))]);
             }
-            if (seen == SOME) hide(s, sight, i0 + 4 * h);
+            const lds_float_t* refs = st;
+            float factor = unit;
+            if (sizeof(T) == 4 ? seen == SOME : __builtin_expect(seen == SOME || take_low, 0)) {
+                if (seen == SOME) hide(s, sight, i0 + 4 * h);
+                if (sizeof(T) == 2 && take_low) {
+                    // the whole exponent, so that what follows has nothing to take from it
+                    refs = zeros;
+                    factor = 1.0f;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const f32x4_t ref = *(const lds_f32x4_t*)(st + 8 * q + 4 * h), low = *(const lds_f32x4_t*)(st + BQ + 8 * q + 4 * h);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float z = s[4 * q + e];
+                            s[4 * q + e] = (BIAS ? (z - ref[e]) * unit : fmaf(z, unit, -ref[e])) + low[e];
+                        }
+                    }
+                }
+            }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const f32x4_t ref = *(const lds_f32x4_t*)(st + 8 * q + 4 * h), dl = *(const lds_f32x4_t*)(st + BQ + 8 * q + 4 * h);
+                const f32x4_t ref = *(const lds_f32x4_t*)(refs + 8 * q + 4 * h);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float z = s[4 * q + e];
-                    const float p = BIAS ? exp2_((z - ref[e]) * unit) : exp2_(fmaf(z, unit, -ref[e]));
-                    s[4 * q + e] = p;
-                    dp[4 * q + e] = p * (dp[4 * q + e] - dl[e]);
+                    s[4 * q + e] = BIAS ? exp2_((z - ref[e]) * factor) : exp2_(fmaf(z, factor, -ref[e]));
                 }
+            }
+            if (sizeof(T) == 4 && take_low) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const f32x4_t norm = *(const lds_f32x4_t*)(st + BQ + 8 * q + 4 * h);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[4 * q + e] *= norm[e];
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const f32x4_t dl = *(const lds_f32x4_t*)(st + 2 * BQ + 8 * q + 4 * h);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dp[4 * q + e] = s[4 * q + e] * (dp[4 * q + e] - dl[e]);
             }
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
@@ -1312,7 +1388,7 @@ size_t attention_bytes(const muon_attention_args& args) {
     return pack_forward(a, nullptr).at + (s > 1 ? static_cast<size_t>(s) * a.queries * a.heads * (a.width + 2) * sizeof(float) : 0);
 }
 
-hipError_t launch_attention(const muon_attention_args& args, void* workspace, hipStream_t s) {
+hipError_t launch_attention(const muon_attention_args& args, float* lse_low, void* workspace, hipStream_t s) {
     if (args.queries == 0) return hipSuccess;
     muon_attention_args a = args;
     const Packer pack = pack_forward(a, workspace);
@@ -1321,6 +1397,7 @@ hipError_t launch_attention(const muon_attention_args& args, void* workspace, hi
     ForwardArgs f{};
     f.c = common_args(a, forward_splits(a), forward_pack(a));
     f.c.units = f.c.q_axis * (a.heads >> f.c.pack) * f.c.splits;
+    f.c.lse_low = lse_low;
     f.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + pack.at);
     return dispatch(a.dtype, a.width, a.bias != nullptr, [&](auto t, auto dp, auto bias) {
         return run_forward<decltype(t), decltype(dp)::value, decltype(bias)::value>(f, s);
@@ -1332,7 +1409,7 @@ size_t attention_backward_bytes(const muon_attention_backward_args& args) {
     return pack_backward(b, nullptr).at + plan_backward(b).bytes;
 }
 
-hipError_t launch_attention_backward(const muon_attention_backward_args& args, void* workspace, hipStream_t s) {
+hipError_t launch_attention_backward(const muon_attention_backward_args& args, const float* lse_low, void* workspace, hipStream_t s) {
     muon_attention_backward_args b = args;
     const Packer pack = pack_backward(b, workspace);
     hipError_t e = run_pack(pack, b.dtype, s);
@@ -1351,6 +1428,7 @@ hipError_t launch_attention_backward(const muon_attention_backward_args& args, v
     a.buckets = b.buckets; a.reach = b.reach; a.causal = b.causal; a.dtype = b.dtype;
     BackwardArgs f{};
     f.c = common_args(a, 1, 0);
+    f.c.lse_low = const_cast<float*>(lse_low);
     f.grad_out = b.grad_out;
     f.grad_q = b.grad_q; f.grad_k = b.grad_k; f.grad_v = b.grad_v;
     f.ld_do = b.ld_grad_out; f.hs_do = b.hs_grad_out;

@@ -30,7 +30,8 @@ typedef __attribute__((address_space(3))) f32x4_t lds_f32x4_t;
 typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
 typedef __attribute__((address_space(3))) float lds_float_t;
 
-constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.69314718055994530942f;
+constexpr double LOG2E_64 = 1.44269504088896340736, LN2_64 = 0.69314718055994530942;
+constexpr float LOG2E = static_cast<float>(LOG2E_64), LOG2E_LOW = static_cast<float>(LOG2E_64 - static_cast<double>(LOG2E));
 constexpr float NEG_INF = -__builtin_inff();
 
 static __device__ const u32x4_t zero_chunk = {};   // what a load reads in place of a row or column that is not there

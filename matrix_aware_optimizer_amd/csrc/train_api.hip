@@ -354,7 +354,7 @@ template <typename A> void attention_inputs(const A* a, Buffers& buf) {
     }
 }
 
-muon_status check_attention(const muon_attention_args* a, Buffers& buf) {
+muon_status check_attention(const muon_attention_args* a, Buffers& buf, const float* lse_low = nullptr) {
     if (!a) return fail(MUON_ERR_INVALID_ARG, "args is NULL");
     MUON_TRY(check_attention_shape(a));
     const size_t es = elem_size(a->dtype);
@@ -362,10 +362,11 @@ muon_status check_attention(const muon_attention_args* a, Buffers& buf) {
     buf.heads("out", a->out, a->queries, a->heads, a->width, a->ld_out, a->hs_out, es, true);
     buf.add("lse", a->lse, static_cast<size_t>(a->queries) * a->heads * 4, 4, true);
     buf.heads("out_low", a->out_low, a->queries, a->heads, a->width, a->ld_out_low, a->hs_out_low, es, true, true);
+    buf.add("lse_low", lse_low, static_cast<size_t>(a->queries) * a->heads * 4, 4, true, true);
     return buf.check();
 }
 
-muon_status check_attention_backward(const muon_attention_backward_args* a, Buffers& buf) {
+muon_status check_attention_backward(const muon_attention_backward_args* a, Buffers& buf, const float* lse_low = nullptr) {
     if (!a) return fail(MUON_ERR_INVALID_ARG, "args is NULL");
     MUON_TRY(check_attention_shape(a));
     if ((a->bias != nullptr) != (a->grad_bias != nullptr)) return fail(MUON_ERR_INVALID_ARG, "bias and its gradient go together");
@@ -373,6 +374,7 @@ muon_status check_attention_backward(const muon_attention_backward_args* a, Buff
     attention_inputs(a, buf);
     buf.heads("out", a->out, a->queries, a->heads, a->width, a->ld_out, a->hs_out, es, false);
     buf.add("lse", a->lse, static_cast<size_t>(a->queries) * a->heads * 4, 4, false);
+    buf.add("lse_low", lse_low, static_cast<size_t>(a->queries) * a->heads * 4, 4, false, true);
     buf.heads("out_low", a->out_low, a->queries, a->heads, a->width, a->ld_out_low, a->hs_out_low, es, false, true);
     buf.heads("grad_out", a->grad_out, a->queries, a->heads, a->width, a->ld_grad_out, a->hs_grad_out, es, false);
     buf.heads("grad_q", a->grad_q, a->queries, a->heads, a->width, a->ld_grad_q, a->hs_grad_q, es, true);
@@ -562,13 +564,17 @@ size_t muon_attention_workspace_bytes(const muon_attention_args* a) {
     return check_attention(a, buf) == MUON_OK ? at_least_one(attention_bytes(*a)) : 0;
 }
 
-muon_status muon_attention(const muon_attention_args* a, void* ws, size_t ws_bytes, void* stream) {
+muon_status muon_attention_two_part(const muon_attention_args* a, float* lse_low, void* ws, size_t ws_bytes, void* stream) {
     Buffers buf;
-    MUON_TRY(check_attention(a, buf));
+    MUON_TRY(check_attention(a, buf, lse_low));
     const hipStream_t s = static_cast<hipStream_t>(stream);
     return run_op(buf, attention_bytes(*a), ws, ws_bytes, [&] {
-        return timed_launch(13, s, "attention kernels", [&] { return launch_attention(*a, ws, s); });
+        return timed_launch(13, s, "attention kernels", [&] { return launch_attention(*a, lse_low, ws, s); });
     });
+}
+
+muon_status muon_attention(const muon_attention_args* a, void* ws, size_t ws_bytes, void* stream) {
+    return muon_attention_two_part(a, nullptr, ws, ws_bytes, stream);
 }
 
 size_t muon_attention_backward_workspace_bytes(const muon_attention_backward_args* a) {
@@ -576,13 +582,18 @@ size_t muon_attention_backward_workspace_bytes(const muon_attention_backward_arg
     return check_attention_backward(a, buf) == MUON_OK ? at_least_one(attention_backward_bytes(*a)) : 0;
 }
 
-muon_status muon_attention_backward(const muon_attention_backward_args* a, void* ws, size_t ws_bytes, void* stream) {
+muon_status muon_attention_backward_two_part(const muon_attention_backward_args* a, const float* lse_low, void* ws, size_t ws_bytes,
+                                             void* stream) {
     Buffers buf;
-    MUON_TRY(check_attention_backward(a, buf));
+    MUON_TRY(check_attention_backward(a, buf, lse_low));
     const hipStream_t s = static_cast<hipStream_t>(stream);
     return run_op(buf, attention_backward_bytes(*a), ws, ws_bytes, [&] {
-        return timed_launch(13, s, "attention backward kernels", [&] { return launch_attention_backward(*a, ws, s); });
+        return timed_launch(13, s, "attention backward kernels", [&] { return launch_attention_backward(*a, lse_low, ws, s); });
     });
+}
+
+muon_status muon_attention_backward(const muon_attention_backward_args* a, void* ws, size_t ws_bytes, void* stream) {
+    return muon_attention_backward_two_part(a, nullptr, ws, ws_bytes, stream);
 }
 
 size_t muon_expert_sort_workspace_bytes(const muon_expert_sort_args* a) {

@@ -142,9 +142,9 @@ size_t policy_bytes(const muon_policy_args& a);
 hipError_t launch_policy(const muon_policy_args& a, void* workspace, hipStream_t s);
 
 size_t attention_bytes(const muon_attention_args& a);
-hipError_t launch_attention(const muon_attention_args& a, void* workspace, hipStream_t s);
+hipError_t launch_attention(const muon_attention_args& a, float* lse_low, void* workspace, hipStream_t s);
 size_t attention_backward_bytes(const muon_attention_backward_args& a);
-hipError_t launch_attention_backward(const muon_attention_backward_args& a, void* workspace, hipStream_t s);
+hipError_t launch_attention_backward(const muon_attention_backward_args& a, const float* lse_low, void* workspace, hipStream_t s);
 
 size_t expert_sort_bytes(const muon_expert_sort_args& a);
 hipError_t launch_expert_sort(const muon_expert_sort_args& a, void* workspace, hipStream_t s);

@@ -178,3 +178,22 @@ def test_binding_refuses_wrong_tensors():
             (mao.muon_expert_combine_backward, (x, s, slots, w, eo.int(), s, w), "offsets")):
         with pytest.raises(ValueError, match=match):
             fn(*args)
+
+
+def test_lse_low_is_checked():
+    lib = mao.load()
+    for make, fn, other in ((_attention, lib.muon_attention_two_part, AT[8]), (_backward, lib.muon_attention_backward_two_part, AT[13])):
+        call = lambda low, ws=WS: fn(ctypes.byref(make()), ctypes.c_void_p(low), ctypes.c_void_p(ws), WS_BYTES, None)
+        assert call(AT[17] + 2) == mao.MUON_ERR_INVALID_ARG and "lse_low" in mao.muon_last_error_message()
+        assert call(other) == mao.MUON_ERR_INVALID_ARG and "overlap" in mao.muon_last_error_message()
+        if make is _backward:                                                   # this forward call takes no workspace
+            assert call(AT[17], AT[17] & ~255) == mao.MUON_ERR_INVALID_ARG
+        assert call(None) != mao.MUON_ERR_INVALID_ARG and call(AT[17]) != mao.MUON_ERR_INVALID_ARG
+        assert fn(None, None, ctypes.c_void_p(WS), WS_BYTES, None) == mao.MUON_ERR_INVALID_ARG
+    q, k = torch.zeros(5, 4, 8), torch.zeros(5, 2, 8)
+    lse = torch.zeros(5, 4)
+    for low in (lse.double(), lse[:4], torch.zeros(4, 5).t()):
+        with pytest.raises(ValueError, match="lse_low"):
+            mao.muon_attention(q, k, k, q.clone(), lse, lse_low=low)
+        with pytest.raises(ValueError, match="lse_low"):
+            mao.muon_attention_backward(q, k, k, q, lse, q, q.clone(), k.clone(), k.clone(), lse_low=low)

@@ -6,7 +6,7 @@ ordinary one.
 import numpy as np
 import pytest
 
-from test_gpu_attention import _case, _check, _make, _np, _run
+from test_gpu_attention import U, _bounds, _case, _check, _make, _near, _np, _reference, _run
 
 pytestmark = pytest.mark.gpu
 
@@ -96,3 +96,91 @@ def test_a_window_over_as_many_keys_as_there_may_be(gpu_lib, causal):
         lo, hi = part.amin((0, 1)), part.amax((0, 1))
         assert (lo == hi).all() and (np.abs(_np(lo) - 0.25 * p * dz * _np(q)[0, 0]) <= bound * np.abs(_np(q)[0, 0])).all()
     assert (np.abs(_np(gq)) <= 0.25 * 1.5 * (abs(dz) + 2.0 ** -18 * size) * np.abs(_np(k))).all()
+
+
+def _two_part(mao, c, t):
+    import torch
+    low = torch.full(t["q"].shape[:2], float("nan"), device="cuda")
+    return {**_run(mao, c, t, lse_low=low), "lse_low": low}
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", [dict(nq=[77]), dict(nq=[3, 0, 200], nk=[40, 9, 300], causal=True, width=128, heads=4, kv=2), dict(nq=[1], nk=[5000], heads=8, kv=2),
+                                   dict(nq=[60], nk=[20], causal=True), dict(nq=[130], nk=[260], buckets=8, reach=20, window=33),
+                                   dict(nq=[1, 2], nk=[1700, 900], buckets=7, reach=500, causal=True), dict(nq=[1150], heads=1, kv=1, causal=True, masked=0.1)],
+                         ids=lambda s: "-".join(f"{k}{v}" for k, v in s.items()).replace(" ", ""))
+def test_lse_in_two_parts(gpu_lib, shape, dtype):
+    import torch
+    c = _case(dtype=dtype, **shape)
+    t, val = _make(c)
+    o, alone, ref = _two_part(gpu_lib, c, t), _run(gpu_lib, c, t), _reference(c, val)
+    _check(c, o, val, ref)
+    assert torch.equal(o["lse"], alone["lse"]) and torch.equal(o["out"], alone["out"])
+    hi, low = _np(o["lse"]), _np(o["lse_low"])
+    blind = np.isinf(hi)
+    assert (hi[blind] == -np.inf).all() and not low[blind].any() and (blind == np.isinf(ref["lse"])).all()
+    # half a step of lse, and the sum of both within the bound of test_gpu_attention's lse without its own rounding
+    assert (np.abs(low) <= 2.0 ** -24 * np.where(blind, 0.0, np.abs(hi))).all()
+    bound = _bounds(c, ref, val["q"], val["k"], val["v"], None, val["bias"], None)["lse"] - U * np.where(blind, 0.0, np.abs(ref["lse"]))
+    with np.errstate(invalid="ignore"):
+        off = np.where(blind, 0.0, np.abs(hi + low - ref["lse"]))
+    assert (off <= bound).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("level", [1000.0, -16000.0])
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_a_rows_probabilities_add_up_to_one_in_the_backward_pass(gpu_lib, with_bias, level, dtype):
+    # One query a head; grad_out is 1 in one column, so a key's grad_v there is its probability.  lse alone is off by up to 3.1e-5 at 1000
+    # and 4.9e-4 at 16000.  In two parts what is left are the sum's chain (32 or 288 additions of u each: 1.7e-5), the exponents'
+    # roundings (30 u) and exponentials (2^-22) of both passes, 4e-6, and in bf16 the outputs' own: within 2^-8 of each and of either
+    # sign, so that their sum passes 6 x 2^-8 sqrt(sum p^2) with a probability below 2 exp(-18) (Hoeffding's bound).
+    import torch
+    n = 64 if level > 0 else 1150
+    c = _case(nq=[1], nk=[n], heads=4, kv=4, dtype=dtype, scale=1.0, logits=0.25, **(dict(buckets=1, reach=3) if with_bias else {}))
+    t, val = _make(c, seed=7)
+    if with_bias:
+        t["bias"].fill_(level)
+    else:
+        # the scores' common part by one column of q and k
+        t["q"][:, :, 0], t["k"][:, :, 0] = 32.0, level / 32
+    t["do"].zero_()
+    t["do"][:, :, 0] = 1.0
+    o = _two_part(gpu_lib, c, t)
+    p = _np(o["v"])[:, :, 0]
+    bound = (2.0 ** -14 if level < 0 else 2.0 ** -17) + (6 * 2.0 ** -8 * np.sqrt((p * p).sum(0)) if dtype == "bf16" else 0.0)
+    assert (np.abs(p.sum(0) - 1) <= bound).all(), p.sum(0) - 1
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("value", [None, -1e9, -1e6])
+@pytest.mark.parametrize("shape", [dict(nq=[150], window=30), dict(nq=[70, 1, 40], nk=[90, 5, 60], causal=True, heads=4, kv=2, width=40), dict(nq=[1], nk=[900], width=128),
+                                   dict(nq=[1101], heads=1, kv=1, width=24, causal=True), dict(nq=[200], nk=[1101], heads=1, kv=1, width=128, masked=0.3)],
+                         ids=lambda s: "-".join(f"{k}{v}" for k, v in s.items()).replace(" ", ""))
+def test_gradients_where_a_row_sees_nothing_but_a_very_low_bias(gpu_lib, shape, value, dtype):
+    # Keys count alike, also in the gradients.  At the lowest value (None) a score is the bias, whatever the product; else q is 0.
+    import torch
+    c = _case(dtype=dtype, buckets=3, reach=17, **shape)
+    t, val = _make(c)
+    t["bias"].fill_(float(torch.finfo(t["q"].dtype).min) if value is None else value)
+    if value is not None:
+        t["q"].zero_()
+    val = {**val, "q": _np(t["q"]), "bias": _np(t["bias"])}
+    o, ref = _two_part(gpu_lib, c, t), _reference(c, val)
+    count = np.full(ref["lse"].shape, 0.0)
+    for s in ref["parts"]:
+        assert np.ptp(s["z"][s["seen"]]) == 0
+        s["z"] = np.zeros_like(s["z"])
+        count[s["rows"], s["head"]] = s["seen"].sum(1)
+    seen = count > 0
+    want = np.log(np.maximum(count, 1))
+    over = _np(o["lse"])[seen] - val["bias"][0, 0]                  # exact: equal, or within a factor of two
+    off = np.zeros_like(want)
+    off[seen] = np.abs(over + _np(o["lse_low"])[seen] - want[seen])
+    off -= (2.0 ** -20 + 2.0 ** -22 * want + count * U)
+    assert off.max() <= 0, off.max()
+    # the bounds for scores of 0 (no rounding in them), against the probabilities 1 / n
+    flat = {**ref, "lse": np.where(seen, want, -np.inf)}
+    b = _bounds(c, flat, val["q"], val["k"], val["v"], val["do"], np.zeros((3, c["heads"])), o["low"])
+    for name in ("out", "q", "k", "v", "bias"):
+        _near(o[name], ref[name], b[name], name)
