@@ -516,7 +516,13 @@ muon_status muon_attention_two_part(const muon_attention_args* args, float* lse_
  *   delta_i = grad_out_i.out_i,   dz_ij = p_ij (grad_out_i.v_j - delta_i)
  *   grad_q = scale dz k,  grad_k = scale dz^T q,  grad_v = p^T grad_out  (k, v: over the heads that share one)
  *   grad_bias[b][h] = sum of dz over the pairs of bucket b
- * Rows of no sequence and masked keys get 0. */
+ * Rows of no sequence and masked keys get 0.
+ *
+ * The workspace holds copies of inputs whose rows do not come in whole 16-byte
+ * chunks, 4 bytes a query and head, the parts of walks that are split where there are
+ * few rows, and partial sums of a bias: 4 (2 reach + 1) bytes for each head and 32
+ * queries of a sequence, half a gigabyte at most (one sequence's 128 queries if
+ * those take more). */
 typedef struct {
     const void*    q;
     const void*    k;

@@ -36,6 +36,10 @@ constexpr int64_t AT_CUS = 256;
 // 398 and 382; 2 sequences, 8 heads, reach 4096 960 and 912; 77 tokens, 8 heads 29.0 and 29.8, 512 tokens 47.6 and 50.4, 4 x 512
 // tokens 104.1 and 105.1.  With 75 distances a bucket (300 queries over 900 keys) 51.9 and 50.1, with 32 (2 x 512 tokens) 80.2 and 82.0.
 constexpr int64_t AT_FEW_SLOTS = 256, AT_FEW_DISTANCES = 64;
+// Slots take 4 (2 reach + 1) bytes a wave and head.  Where those of all units pass this many bytes (4000 sequences of 40 tokens, 16 heads, reach
+// 1024: 2.8 GB, both passes 5.25 ms in one go and 5.38 so), grad_q goes over the units in batches, and each batch's slots are added to the
+// distances' sums before the next.
+constexpr int64_t AT_SLOT_BYTES = int64_t{1} << 29;
 
 // fp32 products take 16 times as long as bf16's: steps and blocks of columns that a narrow head does not have are left out (72 of
 // 128: 4 of 11 of a tile's products).
@@ -71,15 +75,16 @@ struct BackwardArgs {
     int q_splits, kv_splits;
     float* q_part;        // splits > 1: sums of each split
     float* kv_part;
-    float* bias_part;     // [head][slot][2 reach + 1], a slot per wave
+    float* bias_part;     // [head][slot][2 reach + 1], a slot per wave of a batch of units
     int64_t slots;
+    int64_t first_unit;   // of the batch
     int64_t q_blocks;     // one launch for all: its first blocks make grad_q
 };
 
 // Which unit of the axis, head and split a workgroup has.  Heads go fastest, and where they allow it in runs that share an XCD
 // (workgroups go to XCDs in turn), so that a key head's rows stay in one L2.
-// stride: how to go through the units (unit_stride).
-__device__ __forceinline__ void decode(int64_t id, int heads, int splits, int64_t axis, int64_t stride, int& u, int& head, int& split) {
+// stride: how to go through the units (unit_stride).  Returns the unit's turn on that way.
+__device__ __forceinline__ int64_t decode(int64_t id, int heads, int splits, int64_t axis, int64_t stride, int& u, int& head, int& split) {
     const int hs = heads * splits;
     const int64_t r = id / hs;
     u = static_cast<int>(stride == 1 ? r : r * stride % axis);
@@ -87,6 +92,7 @@ __device__ __forceinline__ void decode(int64_t id, int heads, int splits, int64_
     if (hs % 8 == 0) k = (k % 8) * (hs / 8) + k / 8;
     head = k / splits;
     split = k - head * splits;
+    return r;
 }
 
 // A negative scale goes into the sign of one factor of the scores and a scale of 0 into its values: then a score that is hidden, at
@@ -144,6 +150,10 @@ template <typename T, int N> struct BiasWindow {
     float value = 0.0f;
     __device__ __forceinline__ void ask(const muon_attention_args& a, int first) { if (static_cast<int>(threadIdx.x) < N) bucket = bucket_at<T>(a, first + static_cast<int>(threadIdx.x)); }
     __device__ __forceinline__ void fetch(const muon_attention_args& a, int head) { if (static_cast<int>(threadIdx.x) < N) value = bias_value<T>(a, bucket, head); }
+    // distances below `lowest` count as of no bucket, so 0, whatever the table holds for them (first: as asked)
+    __device__ __forceinline__ void fetch(const muon_attention_args& a, int head, int first, int lowest) {
+        if (static_cast<int>(threadIdx.x) < N) value = bias_value<T>(a, first + static_cast<int>(threadIdx.x) < lowest ? -1 : bucket, head);
+    }
     __device__ __forceinline__ void put(lds_float_t* buf) const { if (static_cast<int>(threadIdx.x) < N) buf[threadIdx.x] = value; }
 };
 
@@ -541,11 +551,11 @@ template <typename T, int DP, bool BIAS> __device__ __forceinline__ void grad_q_
     const Common& c = f.c;
     const muon_attention_args& a = c.a;
     int u, head, split;
-    decode(block, a.heads, f.q_splits, c.q_axis, c.q_stride, u, head, split);
+    const int64_t turn = decode(block, a.heads, f.q_splits, c.q_axis, c.q_stride, u, head, split);
     lds_float_t* wbuf = (lds_float_t*)(buf + 4 * W::TILE);
     BiasSums sums;
     if constexpr (BIAS) {
-        const int64_t slot = head * f.slots + (static_cast<int64_t>(u) * f.q_splits + split) * AT_WAVES + wave_id();
+        const int64_t slot = head * f.slots + ((turn - f.first_unit) * f.q_splits + split) * AT_WAVES + wave_id();
         sums.start(wbuf + 2 * W::WIN + BiasSums::ROOM * wave_id(), f.bias_part + slot * (2 * a.reach + 1), a.reach);
     }
     Span sp;
@@ -594,8 +604,8 @@ template <typename T, int DP, bool BIAS> __device__ __forceinline__ void grad_q_
     RowRef r{BIAS ? -NEG_INF : 0.0f, 0.0f};
     if (row_ok) r.set<BIAS>(lse, lse_low);
     const float ref = r.ref, norm = exp2_(r.low2), delta_norm = delta * norm;
-    // a bias may be anything at distances that only places behind the last query have
-    const bool partly = BIAS && w.wave_at + 31 >= sp.len;
+    // no pair is further apart than the sequence's last query and first key, but the places behind that query are
+    const int lowest = 1 - sp.other_len;
 
     f32x16_t o[DB] = {};
     BiasWindow<T, W::WIN> bw;
@@ -614,7 +624,7 @@ template <typename T, int DP, bool BIAS> __device__ __forceinline__ void grad_q_
         }
         next = __ballot(first_byte != 0);
         if constexpr (BIAS) {
-            bw.fetch(a, head);
+            bw.fetch(a, head, w.window_first(w.first), lowest);
             far_lo = bias_value<T>(a, lo_bucket, head);
             far_hi = bias_value<T>(a, hi_bucket, head);
             bw.ask(a, w.window_first(w.first + 1));
@@ -631,13 +641,12 @@ template <typename T, int DP, bool BIAS> __device__ __forceinline__ void grad_q_
             w.load(t + 1, buf + 2 * W::TILE * (b ^ 1), buf + 2 * W::TILE * (b ^ 1) + W::TILE, next);
             byte = w.key_byte(t + 2);
             if constexpr (BIAS) {
-                bw.fetch(a, head);
+                bw.fetch(a, head, w.window_first(t + 1), lowest);
                 bw.ask(a, w.window_first(t + 2));
             }
         }
-        int seen = w.seen(c, t, live);
+        const int seen = w.seen(c, t, live);
         if (seen != NOTHING) {
-            if (partly) seen = SOME;
             const unsigned kt = lds_at(buf) + 2 * W::TILE * b;
             const int far = BIAS ? w.far(t) : 0;
             // a block of 32 keys at a time: all of a tile at once does not fit the registers of two waves a SIMD
@@ -936,11 +945,12 @@ __device__ __forceinline__ void grad_kv_block(const BackwardArgs& f, int64_t blo
             }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const f32x4_t ref = *(const lds_f32x4_t*)(refs + 8 * q + 4 * h);
+                const f32x4_t ref = *(const lds_f32x4_t*)(refs + 8 * q + 4 * h), dl = *(const lds_f32x4_t*)(st + 2 * BQ + 8 * q + 4 * h);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float z = s[4 * q + e];
                     s[4 * q + e] = BIAS ? exp2_((z - ref[e]) * factor) : exp2_(fmaf(z, factor, -ref[e]));
+                    if (sizeof(T) == 2) dp[4 * q + e] = s[4 * q + e] * (dp[4 * q + e] - dl[e]);
                 }
             }
             if (sizeof(T) == 4 && take_low) {
@@ -951,6 +961,7 @@ __device__ __forceinline__ void grad_kv_block(const BackwardArgs& f, int64_t blo
                     for (int e = 0; e < 4; ++e) s[4 * q + e] *= norm[e];
                 }
             }
+            if (sizeof(T) == 4)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const f32x4_t dl = *(const lds_f32x4_t*)(st + 2 * BQ + 8 * q + 4 * h);
@@ -1019,27 +1030,30 @@ struct FinishArgs {
     int entries, buckets, bias_heads, width;
 };
 
-// Sum over the slots for 64 distances of one head.  The orders are fixed; sums in fp64: they have up to millions of terms of either sign.
-__global__ __launch_bounds__(1024) void attention_bias_slots_kernel(const float* part, int64_t slots, int entries, double* sums) {
+// Sum over `count` slots for 64 distances of one head, added to what the batches before left (`more`).  The orders are fixed; sums in fp64:
+// they have up to millions of terms of either sign.
+__global__ __launch_bounds__(1024) void attention_bias_slots_kernel(const float* part, int64_t slots, int64_t count, int entries, double* sums, int more) {
     __shared__ double red[16][64];
     const int lane = threadIdx.x & 63, wave = wave_id(), head = blockIdx.y;
     const int d = min(static_cast<int>(blockIdx.x) * 64 + lane, entries - 1);
     double v = 0.0;
     const float* p = part + head * slots * entries + d;
     int64_t s = wave;
-    for (; s + 7 * 16 < slots; s += 8 * 16) {
+    for (; s + 7 * 16 < count; s += 8 * 16) {
         float x[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) x[k] = G(p)[(s + 16 * k) * entries];
 #pragma unroll
         for (int k = 0; k < 8; ++k) v += x[k];
     }
-    for (; s < slots; s += 16) v += G(p)[s * entries];
+    for (; s < count; s += 16) v += G(p)[s * entries];
     red[wave][lane] = v;
     __syncthreads();
     if (wave == 0) {
         for (int k = 1; k < 16; ++k) v += red[k][lane];
-        if (static_cast<int>(blockIdx.x) * 64 + lane < entries) G(sums)[static_cast<int64_t>(head) * entries + d] = v;
+        MUON_GLOBAL double* sum = G(sums) + static_cast<int64_t>(head) * entries + d;
+        if (more) v += *sum;
+        if (static_cast<int>(blockIdx.x) * 64 + lane < entries) *sum = v;
     }
 }
 
@@ -1168,7 +1182,7 @@ struct BackwardPlan {
     int64_t q_blocks, kv_blocks;
     bool all;                                       // one launch for the three gradients
     bool two_step;                                  // the bias's slots are added up by distance first
-    int64_t slots;                                  // of the bias's partial sums, per head
+    int64_t slots, batch;                           // of the bias's partial sums, per head, for a batch of so many units
     size_t delta, q_part, kv_part, bias_part, bias_sums, bytes;   // offsets
 };
 BackwardPlan plan_backward(const muon_attention_backward_args& a) {
@@ -1196,8 +1210,11 @@ BackwardPlan plan_backward(const muon_attention_backward_args& a) {
     p.kv_part = take(p.kv_splits > 1 ? 2 * p.kv_splits * k * a.width * 4 : 0);
     if (a.bias) {
         const size_t entries = 2 * static_cast<size_t>(a.reach) + 1;
-        p.slots = a.queries ? span_units(a.queries, a.sequences, AT_ROWS) * p.q_splits * AT_WAVES : 0;
-        p.two_step = p.slots > AT_FEW_SLOTS || static_cast<int64_t>(entries) > AT_FEW_DISTANCES * a.buckets;
+        const int64_t units = a.queries ? span_units(a.queries, a.sequences, AT_ROWS) : 0, of_unit = static_cast<int64_t>(p.q_splits) * AT_WAVES;
+        const int64_t fit = std::max<int64_t>(1, AT_SLOT_BYTES / static_cast<int64_t>(of_unit * a.heads * entries * 4)), batches = (units + fit - 1) / fit;
+        p.batch = p.all || batches <= 1 ? units : (units + batches - 1) / batches;
+        p.slots = p.batch * of_unit;
+        p.two_step = p.batch < units || p.slots > AT_FEW_SLOTS || static_cast<int64_t>(entries) > AT_FEW_DISTANCES * a.buckets;
         p.bias_part = take(p.slots * a.heads * entries * 4);
         p.bias_sums = take(p.two_step ? a.heads * entries * 8 : 0);
     }
@@ -1287,15 +1304,30 @@ template <typename T, int DP, bool BIAS>
 hipError_t run_backward(BackwardArgs f, const BackwardPlan& p, const muon_attention_backward_args& b, char* ws, hipStream_t s) {
     const muon_attention_args& a = f.c.a;
     hipError_t e = hipSuccess;
+    auto add_slots = [&](int64_t units, bool more) {
+        const int entries = 2 * a.reach + 1;
+        hipLaunchKernelGGL(attention_bias_slots_kernel, dim3((entries + 63) / 64, a.heads), dim3(1024), 0, s, f.bias_part, p.slots,
+                           units * p.q_splits * AT_WAVES, entries, reinterpret_cast<double*>(ws + p.bias_sums), more ? 1 : 0);
+        return hipGetLastError();
+    };
     if (p.all) {
         hipLaunchKernelGGL((attention_grad_all_kernel<T, DP, BIAS>), dim3(static_cast<unsigned>(p.q_blocks + p.kv_blocks)), dim3(AT_THREADS), 0, s, f);
         e = hipGetLastError();
+        if (e == hipSuccess && BIAS && p.two_step) e = add_slots(p.batch, false);
     } else {
-        e = in_launches(p.q_blocks, [&](int64_t base, unsigned n) {
-            f.c.unit0 = base;
-            hipLaunchKernelGGL((attention_grad_q_kernel<T, DP, BIAS>), dim3(n), dim3(AT_THREADS), 0, s, f);
-            return hipGetLastError();
-        });
+        const int64_t of_unit = static_cast<int64_t>(a.heads) * p.q_splits, units = p.q_blocks / of_unit, batch = BIAS && units ? p.batch : units;
+        for (int64_t u = 0; u < units; u += batch) {
+            const int64_t n_units = std::min(batch, units - u);
+            f.first_unit = u;
+            e = in_launches(n_units * of_unit, [&](int64_t base, unsigned n) {
+                f.c.unit0 = u * of_unit + base;
+                hipLaunchKernelGGL((attention_grad_q_kernel<T, DP, BIAS>), dim3(n), dim3(AT_THREADS), 0, s, f);
+                return hipGetLastError();
+            });
+            if (e == hipSuccess && BIAS && p.two_step) e = add_slots(n_units, u > 0);
+            if (e != hipSuccess) return e;
+        }
+        if (BIAS && p.two_step && units == 0) e = add_slots(0, false);
         if (e != hipSuccess) return e;
         e = in_launches(p.kv_blocks, [&](int64_t base, unsigned n) {
             f.c.unit0 = base;
@@ -1315,13 +1347,7 @@ hipError_t run_backward(BackwardArgs f, const BackwardPlan& p, const muon_attent
         g.buckets = a.buckets;
         g.bias_heads = a.heads;
         g.first[0] = static_cast<int64_t>(a.buckets) * a.heads;
-        if (p.two_step) {
-            double* sums = reinterpret_cast<double*>(ws + p.bias_sums);
-            hipLaunchKernelGGL(attention_bias_slots_kernel, dim3((g.entries + 63) / 64, a.heads), dim3(1024), 0, s, f.bias_part, p.slots, g.entries, sums);
-            e = hipGetLastError();
-            if (e != hipSuccess) return e;
-            g.bias_sums = sums;
-        }
+        if (p.two_step) g.bias_sums = reinterpret_cast<const double*>(ws + p.bias_sums);
     }
     const int64_t q = a.queries * a.heads * a.width, k = a.keys * a.kv_heads * a.width;
     if (p.q_splits > 1) g.job[0] = {f.q_part, f.grad_q, q, q, f.ld_dq, f.hs_dq, p.q_splits, a.heads, a.scale};
