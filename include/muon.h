@@ -473,8 +473,8 @@ muon_status muon_policy_loss(const muon_policy_args* args, void* workspace, size
  * that from about 2^20 on a row's probabilities are no longer those of its inputs;
  * without a bias scores from 2^30 on may come out as NaN.
  *
- * A key that `causal` or `window` hides from a query but that another one of the same
- * sequence sees reaches the first one too if it holds infinities or NaN. */
+ * A key that only `causal` or `window` hides from a query may reach it all the same
+ * if it holds infinities or NaN; one that key_mask hides does not. */
 #define MUON_MAX_HEAD_WIDTH 128
 #define MUON_MAX_HEADS      4096
 #define MUON_MAX_REACH      4096
@@ -554,9 +554,9 @@ muon_status muon_attention_backward(const muon_attention_backward_args* args, vo
 
 /* The same with lse_low as muon_attention_two_part wrote it; NULL: muon_attention_backward.
  * Without it p_ij comes from lse alone, so a row's probabilities are all off by a
- * factor within exp(|lse| 2^-24): 2^-20 of them at |lse| = 16, and wholly where a row
- * sees nothing but a bias so low (below about -1e5) that lse no longer holds the
- * logarithm of its sum; there its keys count as 1 each instead of 1 in all. */
+ * factor within exp(|lse| 2^-24): 2^-20 of them at |lse| = 16, 0.6 % where a row sees
+ * nothing but a bias of -1e5, and from about -1e8 on lse no longer holds the logarithm
+ * of the sum, so that the keys of such a row count as 1 each instead of 1 in all. */
 muon_status muon_attention_backward_two_part(const muon_attention_backward_args* args, const float* lse_low, void* workspace,
                                              size_t workspace_bytes, void* stream);
 

@@ -10,11 +10,12 @@
 // same bits on every run, and shared key heads add up in registers.
 //
 // Both tiles of a walk are double-buffered in LDS; a step's loads are issued before the step before it is computed, with
-// one barrier a step.  Two workgroups run on a CU.
+// one barrier a step.  Two workgroups run on a CU in bf16, but one of grad_q where a bias meets heads wider than 64 (LDS) and one of what makes
+// all gradients at once; in fp32 one, two of the forward and grad_q kernels up to 64 wide.
 //
-// Measured (16384 tokens, causal, 16 heads of 128 over 4, bf16): forward 1.5 ms, 730 TFLOP/s by the operator's own count; grad_q 2.1 ms
-// and grad_k with grad_v 3.4 ms, 770 and 650 by the three and four products that they form, second parts not counted.  The matrix cores are busy 60, 59 and 53 % of the time, half
-// of it or a third with the second parts of probabilities and dz, and the vector units 58, 50 and 43 %: a lane's exponentials, maxima and
+// Measured (16384 tokens, causal, 16 heads of 128 over 4, bf16): forward 1.45 to 1.54 ms, 710 to 760 TFLOP/s by the operator's own count; grad_q 2.0
+// to 2.1 ms and grad_k with grad_v 3.1 to 3.4 ms, 770 to 830 and 650 to 710 by the three and four products that they form, second parts not counted.  The matrix cores are busy 60, 59 and 53 % of the time, half
+// of it or a third with the second parts of probabilities and dz, and the vector units 58, 50 and 44 %: a lane's exponentials, maxima and
 // roundings take about as long as its products, and of two waves a SIMD the one's products cover only part of the other's.
 #include <algorithm>
 #include <numeric>
@@ -713,7 +714,7 @@ __global__ __launch_bounds__(AT_THREADS, sizeof(T) == 2 && !(BIAS && DP == 128) 
 // ---- grad_k and grad_v ------------------------------------------------------------
 
 // Two waves a SIMD, of workgroups that share no barrier, fill each other's waits.  In bf16 with DP 128 that takes v's fragments out of
-// LDS (both accumulators, k's fragments and a block's scores fill 256 registers), and tiles of 32 queries, so that two
+// LDS (both accumulators, k's fragments and a block's scores fill 256 registers; 1 is spilled, with a bias 16), and tiles of 32 queries, so that two
 // workgroups fit a CU's LDS (8192 tokens, 16 heads of 128: 265 us; one workgroup of 8 waves and tiles of 64 queries 285).
 template <typename T, int DP> struct KvShape {
     static constexpr bool V_LDS = sizeof(T) == 2 && DP == 128;
@@ -1163,7 +1164,8 @@ int plan_splits(int64_t rows, int64_t sequences, int heads, int64_t walk, int ti
     return static_cast<int>(std::min<int64_t>(std::max<int64_t>(1, want), AT_MAX_SPLITS));
 }
 int tile_rows(int dtype) { return dtype == MUON_BF16 ? walk_rows<uint16_t>() : walk_rows<float>(); }
-// Workgroups at once: two a CU, but one where fp32 takes all registers.
+// Workgroups at once: two a CU, but one where fp32 takes all registers.  grad_q of a bias runs one a CU beyond 64 wide and is split as if two ran: split
+// for one, 4096 causal tokens in 2 sequences, 4 heads, take 250 us for 237 (both passes), 2048 tokens, 8 heads 208 for 202, 1100 tokens, 4 heads 99 for 102.
 int64_t at_once(int dtype, int width) { return dtype == MUON_F32 && width > 64 ? AT_CUS : 2 * AT_CUS; }
 
 // Sequences of fewer queries than a workgroup has rows: heads that share a key head fill them (a bias is one head's), so that

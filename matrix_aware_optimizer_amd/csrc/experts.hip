@@ -1,4 +1,4 @@
-// Tokens sorted by expert and back (formulas: muon.h).  All four calls move rows and are bound by HBM.
+// Tokens sorted by expert and back (formulas: muon.h).  All four calls move rows; wide ones come near a copy's rate, or past it.
 //
 // Sort: a counting sort of tokens x chosen choices, stable, without atomics on what it returns.  The choices are cut
 // into chunks; one launch counts each chunk's experts, the next ranks every choice within its chunk (a wave finds the lanes
@@ -7,7 +7,9 @@
 // The rows' runs of 8 values go at any alignment (Run, st_run).
 //
 // Measured (8192 x 2048 bf16 to 6 of 64 experts; a copy moves 5.05 TB/s): sort 4.6 + 46 us (5.1 TB/s), its gradient and the weighted
-// sum 60 - 66 us each (3.6 - 3.9 TB/s; a library's sum over 1 GiB reads 3.95; 35 us, 6.7 TB/s, where the rows are in cache), the weighted sum's gradient 74 us (5.9 TB/s).
+// sum 60 - 66 us each (3.6 - 3.9 TB/s, what holds them there was not found; 35 us, 6.7 TB/s, where the rows are in cache), the weighted sum's gradient 74 us (5.9 TB/s).
+// Narrow rows are far from it: the sort and the weighted sum's gradient give a row to a whole wave, one after the other (65536 x 64 to 2 of 64: 69 and
+// 70 us for 25 and 42 MB; the sums, which take as many lanes a row as it fills, 6).
 #include <algorithm>
 
 #include "train_internal.h"

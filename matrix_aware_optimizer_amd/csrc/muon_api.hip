@@ -1078,6 +1078,6 @@ muon_status muon_profile_read_classes(int32_t classes, double* ms, int64_t* laun
     return st;
 }
 
-int32_t muon_version(void) { return 300; }
+int32_t muon_version(void) { return 310; }
 
 }  // extern "C"
