@@ -96,6 +96,8 @@ def test_a_window_over_as_many_keys_as_there_may_be(gpu_lib, causal):
         lo, hi = part.amin((0, 1)), part.amax((0, 1))
         assert (lo == hi).all() and (np.abs(_np(lo) - 0.25 * p * dz * _np(q)[0, 0]) <= bound * np.abs(_np(q)[0, 0])).all()
     assert (np.abs(_np(gq)) <= 0.25 * 1.5 * (abs(dz) + 2.0 ** -18 * size) * np.abs(_np(k))).all()
+    del gk, gv, part
+    torch.cuda.empty_cache()
 
 
 def _two_part(mao, c, t):
