@@ -151,10 +151,6 @@ template <typename T, int N> struct BiasWindow {
     float value = 0.0f;
     __device__ __forceinline__ void ask(const muon_attention_args& a, int first) { if (static_cast<int>(threadIdx.x) < N) bucket = bucket_at<T>(a, first + static_cast<int>(threadIdx.x)); }
     __device__ __forceinline__ void fetch(const muon_attention_args& a, int head) { if (static_cast<int>(threadIdx.x) < N) value = bias_value<T>(a, bucket, head); }
-    // distances below `lowest` count as of no bucket, so 0, whatever the table holds for them (first: as asked)
-    __device__ __forceinline__ void fetch(const muon_attention_args& a, int head, int first, int lowest) {
-        if (static_cast<int>(threadIdx.x) < N) value = bias_value<T>(a, first + static_cast<int>(threadIdx.x) < lowest ? -1 : bucket, head);
-    }
     __device__ __forceinline__ void put(lds_float_t* buf) const { if (static_cast<int>(threadIdx.x) < N) buf[threadIdx.x] = value; }
 };
 
@@ -477,8 +473,9 @@ template <typename T, bool BIAS> __global__ __launch_bounds__(256) void attentio
 // beyond the reach have one bucket a side and add up in registers.  The order of the additions is fixed.  (Adding to LDS
 // by its float atomics: 363 us for grad_q at 8192 x 16 x 64, 135 so.)
 struct BiasSums {
-    static constexpr int ROOM = 32 * 64;   // floats a wave
-    lds_float_t* room;       // [query][64]
+    static constexpr int ROWS = 32 * 64, ROOM = ROWS + 32;   // floats a wave
+    lds_float_t* room;       // [query][64], and a place that is never read
+    lds_float_t* mine;       // where this lane's part of a block goes
     float* slot;             // 2 reach + 1
     int reach, begin, next;  // distances written to the slot: begin .. next - 1
     bool any;
@@ -492,6 +489,11 @@ struct BiasSums {
         carry = below = above = 0.0f;
         for (int i = 0; i < 32; ++i) room[64 * i + (threadIdx.x & 63)] = 0.0f;
     }
+    // A query that sees nothing, or a place behind the last one, stays out of the sums: its part of a block may hold anything (a bias of no pair).
+    __device__ __forceinline__ void set_row(bool ok) {
+        const int lane = threadIdx.x & 63, q = lane & 31;
+        mine = room + (ok ? 64 * q + 31 - q + 4 * (lane >> 5) : ROWS);
+    }
     // lanes 0 .. 31 hold the sums of distances next ..
     __device__ __forceinline__ void flush(float v) {
         const int lane = threadIdx.x & 63, dist = next + lane;
@@ -504,14 +506,13 @@ struct BiasSums {
     }
     // one block of dz; dist: the distance of its first key from its last query
     __device__ __forceinline__ void add(const f32x16_t& dz, int dist) {
-        const int lane = threadIdx.x & 63, q = lane & 31;
+        const int lane = threadIdx.x & 63;
         if (!any) {
             any = true;
             begin = next = dist;
         }
-        lds_float_t* p = room + 64 * q + 31 - q + 4 * (lane >> 5);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) p[8 * (i >> 2) + (i & 3)] = dz[i];
+        for (int i = 0; i < 16; ++i) mine[8 * (i >> 2) + (i & 3)] = dz[i];
         // a wave's LDS accesses come in order; the compiler has to leave them so, since lanes read what others wrote
         asm volatile("" ::: "memory");
         float v[4] = {};
@@ -571,9 +572,13 @@ template <typename T, int DP, bool BIAS> __device__ __forceinline__ void grad_q_
     Lanes<T, DP> lanes;
 
     // a query that sees no key takes no part, whatever its rows hold
-    const float lse = place < sp.len ? G(a.lse)[row * a.heads + head] : NEG_INF;
+    const bool in = place < sp.len;
+    const int64_t stat = in ? row * a.heads + head : 0;
+    const float lse_there = G(a.lse)[stat], low_there = G(c.lse_low ? c.lse_low : a.lse)[stat];      // both at once, with no branch between
+    const float lse = in ? lse_there : NEG_INF;
     const bool row_ok = lse != NEG_INF;
-    const float lse_low = c.lse_low && row_ok ? G(c.lse_low)[row * a.heads + head] : 0.0f;
+    if constexpr (BIAS) sums.set_row(row_ok);
+    const float lse_low = c.lse_low && row_ok ? low_there : 0.0f;
     Frag<T> qf[KS], df[KS];
     float delta = 0.0f;
     {
@@ -601,12 +606,10 @@ template <typename T, int DP, bool BIAS> __device__ __forceinline__ void grad_q_
         if (f.delta && place < sp.len && lane < 32 && split == 0) G(f.delta)[row * a.heads + head] = delta;
     }
     const float scale = size_of(a.scale), unit = BIAS ? LOG2E : scale * LOG2E;
-    // With a bias +infinity, so that p is 0, where nothing is seen (a bias alone, from 89 on, would be an infinite one, and 0 times that is in the bias's sums)
+    // With a bias +infinity, so that p is 0, where nothing is seen: from 89 on a bias alone would make an infinite one.
     RowRef r{BIAS ? -NEG_INF : 0.0f, 0.0f};
     if (row_ok) r.set<BIAS>(lse, lse_low);
     const float ref = r.ref, norm = exp2_(r.low2), delta_norm = delta * norm;
-    // no pair is further apart than the sequence's last query and first key, but the places behind that query are
-    const int lowest = 1 - sp.other_len;
 
     f32x16_t o[DB] = {};
     BiasWindow<T, W::WIN> bw;
@@ -625,7 +628,7 @@ template <typename T, int DP, bool BIAS> __device__ __forceinline__ void grad_q_
         }
         next = __ballot(first_byte != 0);
         if constexpr (BIAS) {
-            bw.fetch(a, head, w.window_first(w.first), lowest);
+            bw.fetch(a, head);
             far_lo = bias_value<T>(a, lo_bucket, head);
             far_hi = bias_value<T>(a, hi_bucket, head);
             bw.ask(a, w.window_first(w.first + 1));
@@ -642,7 +645,7 @@ template <typename T, int DP, bool BIAS> __device__ __forceinline__ void grad_q_
             w.load(t + 1, buf + 2 * W::TILE * (b ^ 1), buf + 2 * W::TILE * (b ^ 1) + W::TILE, next);
             byte = w.key_byte(t + 2);
             if constexpr (BIAS) {
-                bw.fetch(a, head, w.window_first(t + 1), lowest);
+                bw.fetch(a, head);
                 bw.ask(a, w.window_first(t + 2));
             }
         }
@@ -686,6 +689,7 @@ template <typename T, int DP, bool BIAS> __device__ __forceinline__ void grad_q_
                         float v = 0.0f;
 #pragma unroll
                         for (int i = 0; i < 16; ++i) v += s[i];
+                        v = row_ok ? v : 0.0f;
                         if (far < 0) sums.below += v;
                         else sums.above += v;
                     }

@@ -57,6 +57,28 @@ def test_buckets_of_distances_that_no_pair_has_reach_nothing(gpu_lib, value, dty
         assert torch.equal(want[k], got[k]), k
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), 100.0])
+@pytest.mark.parametrize("reach", [135, 70])
+def test_buckets_of_distances_that_only_masked_keys_have_reach_nothing(gpu_lib, reach, value, dtype):
+    # the first 64 of 128 keys are padding: 40 queries see distances -63 .. 39, places behind the last one would have some to -87
+    import torch
+    c = _case(dtype=dtype, nq=[40], nk=[128], buckets=3, reach=reach)
+    t, val = _make(c)
+    t["mask"] = torch.arange(128, device="cuda") >= 64
+    got = []
+    for v in (0.125, value):
+        p, v2 = _with_bias(c, dict(t), val, [0.25, -0.5, v])
+        p["map"] = torch.zeros(2 * reach + 1, dtype=torch.int32, device="cuda")
+        p["map"][reach - 63:reach] = 1
+        p["map"][:reach - 63] = 2
+        got.append(_run(gpu_lib, c, p))
+        if v == 0.125:
+            _check(c, got[0], {**v2, "map": p["map"].cpu().numpy(), "mask": t["mask"].cpu().numpy()})
+    for k in ("out", "lse", "q", "k", "v", "bias"):
+        assert torch.equal(got[0][k], got[1][k]), k
+
+
 @pytest.mark.parametrize("causal", [False, True])
 def test_a_window_over_as_many_keys_as_there_may_be(gpu_lib, causal):
     # one query behind 2^30 - 1 keys, all of them one broadcast row: key positions and windows that sum to more than 2^31
